@@ -364,6 +364,199 @@ HLA_API int hla_backward(const hla_params* params, const void* q, const void* k,
                          float* dconv_wq, float* dconv_wk, float* dconv_wv, void* ws, size_t ws_bytes,
                          void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The full softmax layers beside the hybrid ones: a linearised backbone keeps
+ * some of its layers (and its teacher all of them) as plain causal attention.
+ * Rotary positions, attention over packed prompts with its gradient, a paged
+ * key / value cache kept in 8 bits, and the decode step over that cache.
+ * ------------------------------------------------------------------------- */
+
+/* element type of a cache (hla_cache_params.cache_dtype): 8-bit floats (4
+ * exponent, 3 mantissa bits, largest 448) with one power of two per row */
+#define HLA_DTYPE_E4M3 2
+
+/* which elements of a head form a rotated pair (r = rot_dim) */
+#define HLA_ROPE_HALF 0        /* (i, i + r/2) */
+#define HLA_ROPE_INTERLEAVED 1 /* (2i, 2i + 1) */
+
+/* how the angle per position w_i = base^(-2i/r) is scaled for long contexts */
+#define HLA_ROPE_SCALE_NONE 0
+#define HLA_ROPE_SCALE_LINEAR 1 /* w_i / factor */
+#define HLA_ROPE_SCALE_BANDS 2  /* by t_i = original_len w_i / (2 pi), the turns of the original context: t_i <= low
+                                   gives w_i / factor, t_i >= high gives w_i, linear in t_i between */
+#define HLA_ROPE_SCALE_YARN 3   /* by index: with x(t) = r ln(original_len / (2 pi t)) / (2 ln base), pairs below
+                                   floor(x(high)) keep w_i, above ceil(x(low)) get w_i / factor, linear in i between
+                                   (both ends clamped to [0, r - 1]); rotated values times 0.1 ln(factor) + 1 */
+
+/* Rotary positions of q and k.  head_dim: even, 2 to 256.  rot_dim: even, 2 to
+ * head_dim; the elements past it are copied.  n_q_heads or n_kv_heads may be 0
+ * when that tensor is absent.  low, high: the band edges in turns (read with
+ * BANDS and YARN; 0 for both = 1 and 4 for BANDS, 1 and 32 for YARN).
+ * q_stride, k_stride: elements from a token to the next in q and k (0: dense;
+ * otherwise at least heads * head_dim: the slices of a fused projection).  The
+ * outputs are dense; or, given the address of the input, take its stride. */
+typedef struct hla_rope_params {
+    int n_q_heads;
+    int n_kv_heads;
+    int head_dim;
+    int rot_dim;
+    int layout;
+    int scaling;
+    int dtype;
+    int original_len;
+    double base;
+    double factor;
+    double low;
+    double high;
+    int64_t q_stride;
+    int64_t k_stride;
+} hla_rope_params;
+
+/* Host only: the scaled angle per position of every pair (w, rot_dim / 2
+ * doubles) and the factor on the rotated values. */
+HLA_API int hla_rope_frequencies(const hla_rope_params* params, double* w, double* gain);
+
+/* Rotates q [total, Hq, d] and k [total, Hkv, d] (params->dtype; either may be
+ * NULL, with its output) to the positions given per token (int64, device, any
+ * value): a pair (a, b) at angle t becomes gain (a cos t - b sin t, b cos t +
+ * a sin t).  In place where an output is its input's address.  Angles are
+ * formed as 64-bit fractions of a turn, so far positions lose nothing.  The
+ * outputs must not overlap the inputs in any other way.  Asynchronous. */
+HLA_API int hla_rope(const hla_rope_params* params, const void* q, const void* k, const int64_t* positions,
+                     int64_t total_tokens, void* q_out, void* k_out, void* stream);
+
+/* Its gradient: rotates back, times gain (dq_out, dk_out are the gradients of
+ * hla_rope's outputs, with q_stride and k_stride; dq, dk those of its inputs). */
+HLA_API int hla_rope_backward(const hla_rope_params* params, const void* dq_out, const void* dk_out,
+                              const int64_t* positions, int64_t total_tokens, void* dq, void* dk, void* stream);
+
+/* Softmax attention.  n_q_heads a multiple of n_kv_heads; head_dim 64 or 128;
+ * dtype of q, k, v, out and the gradients; scale: on the scores (0: 1 /
+ * sqrt(head_dim)).  q_stride, k_stride, v_stride: elements from a token to the
+ * next (0: dense; otherwise at least heads * head_dim and a multiple of 16
+ * bytes).  out, dout and the gradients are dense. */
+typedef struct hla_attn_params {
+    int n_q_heads;
+    int n_kv_heads;
+    int head_dim;
+    int dtype;
+    float scale;
+    int reserved; /* 0 */
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+} hla_attn_params;
+
+/* Workspace bytes of hla_attention, or (backward != 0) of
+ * hla_attention_backward; a workspace serves any call it is large enough for.
+ * Its first 16 bytes are the error word: zero them before the first use; calls
+ * only ever set it, hla_check_workspace_error reads and clears it.  Two calls
+ * that may run at the same time need a workspace each. */
+HLA_API int hla_attention_workspace_bytes(const hla_attn_params* params, int64_t total_q, int64_t total_k,
+                                          int n_seqs, int backward, size_t* bytes);
+
+/* Causal attention over n_seqs packed sequences.
+ *   q [total_q, Hq, d], k, v [total_k, Hkv, d]
+ *   cu_seqlens_q, cu_seqlens_k int32 [n_seqs + 1] (device): offsets of each
+ *       sequence's query and key rows, 0 = c_0 <= ... <= c_n <= total;
+ *       cu_seqlens_k NULL: the same as cu_seqlens_q (total_k = total_q).  Row
+ *       i of a sequence with Lq queries and Lk keys sees keys j <= i + Lk - Lq
+ *       (whole prompts: Lk = Lq; a prompt's next chunk behind its earlier
+ *       keys: Lk > Lq).
+ *   out [total_q, Hq, d], lse fp32 [total_q, Hq]: the natural log of the sum
+ *       of exponentials (what hla_attention_backward needs)
+ * A row that sees no key has out 0 and lse -infinity.  Rows at and past c_n
+ * are left as they were.  A malformed table is clamped on the device (no
+ * access out of range) and flagged in the workspace's error word.  bf16 layers
+ * run on the tensor cores: fp32 scores and sums, probabilities rounded to bf16
+ * for their product with v.  Asynchronous; deterministic. */
+HLA_API int hla_attention(const hla_attn_params* params, const void* q, const void* k, const void* v,
+                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int n_seqs, int64_t total_q,
+                          int64_t total_k, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of sum(dout . out) from hla_attention's inputs, out and lse:
+ * dq [total_q, Hq, d], dk, dv [total_k, Hkv, d] (a kv head's sums over the
+ * query heads that read it), in params->dtype from fp32 sums.  Keys that no
+ * row sees have gradients 0; rows at and past c_n are left as they were.
+ * Asynchronous; deterministic (fixed order of sums, no atomics). */
+HLA_API int hla_attention_backward(const hla_attn_params* params, const void* q, const void* k, const void* v,
+                                   const void* out, const float* lse, const void* dout,
+                                   const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int n_seqs,
+                                   int64_t total_q, int64_t total_k, void* dq, void* dk, void* dv, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* A paged key / value cache.  dtype: of the rows written and read (F32 or
+ * BF16); cache_dtype: HLA_DTYPE_E4M3, or dtype itself (kept as it is).
+ * page_size: tokens per page, a multiple of 16; n_pages: pages in the pool;
+ * max_pages: entries per sequence in the page table. */
+typedef struct hla_cache_params {
+    int n_kv_heads;
+    int head_dim;
+    int dtype;
+    int cache_dtype;
+    int page_size;
+    int n_pages;
+    int max_pages;
+    int reserved; /* 0 */
+} hla_cache_params;
+
+/* Caller-owned device buffers (every pointer 16-byte aligned):
+ *   k, v          cache_dtype [n_pages, Hkv, page_size, d]
+ *   k_exp, v_exp  uint8 [n_pages, Hkv, page_size] (E4M3 only, else NULL): the
+ *                 row's value is its 8-bit floats times 2^(byte - 127)
+ *   page_table    int32 [n_seqs, max_pages]: position p of a sequence is row
+ *                 p % page_size of page page_table[n][p / page_size]
+ *   err           int32 [4], the error word: zero it before the first use; set
+ *                 by a position or page number out of range (HLA_ERR_STATE) */
+typedef struct hla_cache {
+    void* k;
+    void* v;
+    uint8_t* k_exp;
+    uint8_t* v_exp;
+    const int32_t* page_table;
+    int32_t* err;
+} hla_cache;
+
+/* Bytes of k (and of v), and of k_exp (and of v_exp; 0 if not E4M3). */
+HLA_API int hla_cache_bytes(const hla_cache_params* params, size_t* rows, size_t* exponents);
+
+/* Writes k, v [total, Hkv, d] (packed sequences, cu_seqlens as for
+ * hla_attention) into the cache: row i of sequence n at position start[n] + i
+ * (start: int64, device).  E4M3: the row's power of two is the smallest 2^e
+ * with max |x| <= 448 2^e (e >= -127; over the row's finite values), and each
+ * value is rounded once, to the nearest 8-bit float of x 2^-e (infinities to
+ * the largest, NaN stays NaN).  A row whose position or page is out of range
+ * is skipped and flagged.  No two rows may be the same place.  Asynchronous. */
+HLA_API int hla_cache_write(const hla_cache_params* params, const hla_cache* cache, const void* k, const void* v,
+                            const int32_t* cu_seqlens, const int64_t* start, int n_seqs, int64_t total_tokens,
+                            void* stream);
+
+/* Reads rows back in params->dtype: the positions start[n] + i into k, v
+ * [total, Hkv, d], as hla_cache_write takes them (exact but for values below
+ * the type's smallest normal).  A row out of range reads as zeros and is
+ * flagged; rows at and past cu_seqlens[n_seqs] are left as they were. */
+HLA_API int hla_cache_read(const hla_cache_params* params, const hla_cache* cache, const int32_t* cu_seqlens,
+                           const int64_t* start, int n_seqs, int64_t total_tokens, void* k, void* v, void* stream);
+
+/* Workspace bytes of hla_attention_decode (no error word: flags go to the
+ * cache's).  Two calls that may run at the same time need one each. */
+HLA_API int hla_attention_decode_workspace_bytes(const hla_attn_params* params, const hla_cache_params* cache_params,
+                                                 size_t* bytes);
+
+/* One query token per sequence over the cache: q [n_seqs, Hq, d] (q_stride
+ * applies) attends to positions 0 .. lens[n] - 1 (int64, device; the token's
+ * own key and value written before), into out [n_seqs, Hq, d].  A sequence
+ * with no keys has out 0.  Keys whose page is out of range, and positions past
+ * max_pages * page_size, are left out and flagged; a negative length counts as
+ * 0 and is flagged.  The heads, head_dim and dtype of both parameter sets must
+ * agree.  Asynchronous; deterministic. */
+HLA_API int hla_attention_decode(const hla_attn_params* params, const hla_cache_params* cache_params,
+                                 const hla_cache* cache, const void* q, const int64_t* lens, int n_seqs, void* out,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* As hla_check_device_error, for a cache's error word. */
+HLA_API int hla_check_cache_error(const hla_cache* cache, void* stream, int32_t* code);
+
 /* Synchronises `stream`, reads the state's device error word into *code
  * (may be NULL), clears it, and returns HLA_OK if it was zero, else the
  * matching HLA_ERR_* status. */

@@ -7,6 +7,7 @@ calling into the library without a built ``libhla.so`` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -26,6 +27,13 @@ HLA_ERR_WORKSPACE = 6
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPE_E4M3 = 2  # caches only
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+ROPE_SCALE_NONE = 0
+ROPE_SCALE_LINEAR = 1
+ROPE_SCALE_BANDS = 2
+ROPE_SCALE_YARN = 3
 FLAG_L2NORM_Q = 0x1
 FLAG_SOFTMAX_OFF = 0x2
 FLAG_LINEAR_OFF = 0x4
@@ -57,6 +65,30 @@ class CState(ctypes.Structure):
 
 class CStateSizes(ctypes.Structure):
     _fields_ = [(name, ctypes.c_size_t) for name in STATE_FIELDS]
+
+
+class CRopeParams(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("original_len", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64)]
+
+
+class CAttnParams(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("reserved", ctypes.c_int),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class CCacheParams(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("cache_dtype", ctypes.c_int), ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class CCache(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("k", "v", "k_exp", "v_exp", "page_table", "err")]
 
 
 _vp = ctypes.c_void_p
@@ -104,6 +136,24 @@ def load():
         lib.hla_backward.restype = ctypes.c_int
         lib.hla_prefill_noalloc_check_error.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32)]
         lib.hla_prefill_noalloc_check_error.restype = ctypes.c_int
+        RP, AP, CP = (ctypes.POINTER(t) for t in (CRopeParams, CAttnParams, CCacheParams))
+        C, i64, size_p = ctypes.POINTER(CCache), ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)
+        for name, args in {
+                "hla_rope_frequencies": [RP, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)],
+                "hla_rope": [RP, _vp, _vp, _vp, i64, _vp, _vp, _vp],
+                "hla_rope_backward": [RP, _vp, _vp, _vp, i64, _vp, _vp, _vp],
+                "hla_attention_workspace_bytes": [AP, i64, i64, ctypes.c_int, ctypes.c_int, size_p],
+                "hla_attention": [AP] + [_vp] * 5 + [ctypes.c_int, i64, i64, _vp, _vp, _vp, ctypes.c_size_t, _vp],
+                "hla_attention_backward": [AP] + [_vp] * 8 + [ctypes.c_int, i64, i64] + [_vp] * 4 +
+                                          [ctypes.c_size_t, _vp],
+                "hla_cache_bytes": [CP, size_p, size_p],
+                "hla_cache_write": [CP, C, _vp, _vp, _vp, _vp, ctypes.c_int, i64, _vp],
+                "hla_cache_read": [CP, C, _vp, _vp, ctypes.c_int, i64, _vp, _vp, _vp],
+                "hla_attention_decode_workspace_bytes": [AP, CP, size_p],
+                "hla_attention_decode": [AP, CP, C, _vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp],
+                "hla_check_cache_error": [C, _vp, ctypes.POINTER(ctypes.c_int32)]}.items():
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ctypes.c_int
         for fn in ("hla_state_bytes", "hla_prefill_workspace_bytes", "hla_state_init", "hla_prefill",
                    "hla_decode_step", "hla_check_device_error", "hla_check_workspace_error",
                    "hla_prefill_stage_events", "hla_prefill_launch_count"):
@@ -352,3 +402,355 @@ def prefill_noalloc_check_error(stream=None) -> int:
     if rc not in (HLA_OK, HLA_ERR_STATE, HLA_ERR_TIMEOUT):
         _check(rc, "hla_prefill_noalloc_check_error")
     return code.value
+
+
+# ---- full softmax layers: rotary positions, packed attention, paged cache, decode ----------------------
+#
+# These calls check their tensors (type, shape, device, strides) and raise HlaError with
+# HLA_ERR_INVALID_ARG before anything is launched; they run on the tensors' device, on `stream` or that
+# device's current stream.
+
+_TORCH = {DTYPE_F32: torch.float32, DTYPE_BF16: torch.bfloat16, DTYPE_E4M3: torch.uint8}
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise HlaError(HLA_ERR_INVALID_ARG, what)
+
+
+def _check_tensor(t, what: str, dtype, shape, device, strided: bool = False) -> int:
+    """The token stride of t in elements; t must have the type, shape and device given and be dense, or
+    (strided) have dense rows at any token stride."""
+    _need(isinstance(t, torch.Tensor) and t.dtype == dtype, f"{what}: expected a {dtype} tensor")
+    _need(tuple(t.shape) == tuple(shape), f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    _need(t.device == device, f"{what}: expected on {device}, got {t.device}")
+    if t.is_contiguous() or t.numel() == 0:
+        return t.shape[1] * t.shape[2] if t.dim() == 3 else 0
+    _need(strided and t.dim() == 3 and t.stride(2) == 1 and t.stride(1) == t.shape[2] and
+          t.stride(0) >= t.shape[1] * t.shape[2], f"{what}: expected dense {'rows' if strided else 'storage'}")
+    return t.stride(0)
+
+
+_HERE_CTX = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """(context for the call's allocations and launches, stream argument): `device` current, and `stream`
+    too if one is given, so that buffers allocated here belong to the stream that uses them."""
+    _need(device.type == "cuda", f"expected CUDA tensors, got {device}")
+    if stream is not None:
+        _need(stream.device == device, f"expected a stream of {device}, got one of {stream.device}")
+        return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
+    stream = torch.cuda.current_stream(device)
+    here = device.index == torch.cuda.current_device()
+    return _HERE_CTX if here else torch.cuda.device(device), ctypes.c_void_p(stream.cuda_stream)
+
+
+@dataclass
+class RopeParams:
+    n_q_heads: int
+    n_kv_heads: int
+    head_dim: int
+    rot_dim: int = 0            # 0: the whole head
+    layout: int = ROPE_HALF
+    scaling: int = ROPE_SCALE_NONE
+    dtype: int = DTYPE_BF16
+    base: float = 500000.0
+    factor: float = 1.0
+    original_len: int = 8192
+    low: float = 0.0            # band edges in turns; 0, 0: the scaling's own
+    high: float = 0.0
+
+    def c(self, q_stride: int = 0, k_stride: int = 0) -> CRopeParams:
+        return CRopeParams(self.n_q_heads, self.n_kv_heads, self.head_dim, self.rot_dim or self.head_dim, self.layout,
+                           self.scaling, self.dtype, self.original_len, self.base, self.factor, self.low, self.high,
+                           q_stride, k_stride)
+
+
+def rope_frequencies(params: RopeParams):
+    """hla_rope_frequencies: (scaled angle per position of every pair, as a list; factor on rotated values)."""
+    c = params.c()
+    w, gain = (ctypes.c_double * max(1, c.rot_dim // 2))(), ctypes.c_double()
+    _check(load().hla_rope_frequencies(ctypes.byref(c), w, ctypes.byref(gain)), "hla_rope_frequencies")
+    return list(w), gain.value
+
+
+def _rope(fn, params, q, k, positions, q_out, k_out, stream):
+    dt = _TORCH.get(params.dtype)
+    _need(dt is not None and dt != torch.uint8, f"{fn}: dtype")
+    _need(isinstance(positions, torch.Tensor) and positions.dim() == 1, f"{fn}: positions must be a vector")
+    n, dev, strides, outs = positions.numel(), positions.device, [0, 0], [q_out, k_out]
+    _check_tensor(positions, f"{fn}: positions", torch.int64, (n,), dev)
+    for i, (x, o, heads, name) in enumerate(((q, q_out, params.n_q_heads, "q"), (k, k_out, params.n_kv_heads, "k"))):
+        if x is None:
+            _need(o is None, f"{fn}: {name}_out without {name}")
+            continue
+        shape = (n, heads, params.head_dim)
+        strides[i] = _check_tensor(x, f"{fn}: {name}", dt, shape, dev, strided=True)
+        if o is None:
+            pass
+        elif o.data_ptr() == x.data_ptr():
+            _need(o.shape == x.shape and o.dtype == x.dtype and o.stride() == x.stride(), f"{fn}: {name}_out in place")
+        else:
+            _check_tensor(o, f"{fn}: {name}_out", dt, shape, dev)
+    c = params.c(*strides)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        for i, x in enumerate((q, k)):
+            if x is not None and outs[i] is None:
+                outs[i] = torch.empty(x.shape, dtype=dt, device=dev)
+        _check(getattr(load(), fn)(ctypes.byref(c), _ptr(q), _ptr(k), _ptr(positions), n, _ptr(outs[0]),
+                                   _ptr(outs[1]), st), fn)
+    return outs[0], outs[1]
+
+
+def rope(params: RopeParams, q, k, positions, q_out=None, k_out=None, stream=None):
+    """hla_rope: (q_out, k_out), q [T, Hq, d] and k [T, Hkv, d] (either may be None) rotated to positions
+    [T] int64.  Rows may be slices of a wider tensor; q_out=q / k_out=k rotate in place."""
+    return _rope("hla_rope", params, q, k, positions, q_out, k_out, stream)
+
+
+def rope_backward(params: RopeParams, dq_out, dk_out, positions, dq=None, dk=None, stream=None):
+    """hla_rope_backward: the gradients of rope's inputs from those of its outputs."""
+    return _rope("hla_rope_backward", params, dq_out, dk_out, positions, dq, dk, stream)
+
+
+@dataclass
+class AttnParams:
+    n_q_heads: int
+    n_kv_heads: int
+    head_dim: int
+    dtype: int = DTYPE_BF16
+    scale: float = 0.0          # 0: 1 / sqrt(head_dim)
+
+    def c(self, q_stride: int = 0, k_stride: int = 0, v_stride: int = 0) -> CAttnParams:
+        return CAttnParams(self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype, self.scale, 0, q_stride,
+                           k_stride, v_stride)
+
+
+def _zeroed(n: int, device):
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()  # the error word
+    return ws
+
+
+def attention_workspace_bytes(params: AttnParams, total_q: int, total_k: int, n_seqs: int,
+                              backward: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(load().hla_attention_workspace_bytes(ctypes.byref(params.c()), total_q, total_k, n_seqs, int(backward),
+                                                ctypes.byref(n)), "hla_attention_workspace_bytes")
+    return n.value
+
+
+def alloc_attention_workspace(params: AttnParams, total_q: int, total_k: int, n_seqs: int, backward: bool = False,
+                              device="cuda"):
+    """A workspace for attention (and, backward=True, attention_backward) with its error word zeroed;
+    check_workspace_error reads it."""
+    n = attention_workspace_bytes(params, total_q, total_k, n_seqs)
+    if backward:
+        n = max(n, attention_workspace_bytes(params, total_q, total_k, n_seqs, True))
+    return _zeroed(n, device)
+
+
+def _check_packed(fn, params, q, k, v, cu_q, cu_k, ws):
+    """Checks the inputs shared by attention and its gradient; returns (strides, total_q, total_k, n_seqs)."""
+    dt = _TORCH.get(params.dtype)
+    _need(dt is not None and dt != torch.uint8, f"{fn}: dtype")
+    _need(all(isinstance(x, torch.Tensor) and x.dim() == 3 for x in (q, k, v)), f"{fn}: q, k, v must be [T, H, d]")
+    _need(isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 and cu_q.numel() >= 2, f"{fn}: cu_seqlens_q")
+    dev, d, n = q.device, params.head_dim, cu_q.numel() - 1
+    strides = (_check_tensor(q, f"{fn}: q", dt, (q.shape[0], params.n_q_heads, d), dev, strided=True),
+               _check_tensor(k, f"{fn}: k", dt, (k.shape[0], params.n_kv_heads, d), dev, strided=True),
+               _check_tensor(v, f"{fn}: v", dt, (k.shape[0], params.n_kv_heads, d), dev, strided=True))
+    _check_tensor(cu_q, f"{fn}: cu_seqlens_q", torch.int32, (n + 1,), dev)
+    if cu_k is not None:
+        _check_tensor(cu_k, f"{fn}: cu_seqlens_k", torch.int32, (n + 1,), dev)
+    _check_workspace(fn, ws, dev)
+    return strides, q.shape[0], k.shape[0], n
+
+
+def _check_workspace(fn, ws, dev):
+    if ws is not None:
+        _need(isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev,
+              f"{fn}: ws must be a dense uint8 tensor on {dev}")
+
+
+def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, ws=None, stream=None):
+    """hla_attention: (out [Tq, Hq, d], lse [Tq, Hq] fp32) of causal attention over packed sequences.  q, k, v
+    may be slices of one fused projection.  cu_seqlens_k: the key rows' offsets where they differ from the
+    query rows' (chunks of prompts behind earlier keys)."""
+    strides, tq, tk, n = _check_packed("hla_attention", params, q, k, v, cu_seqlens_q, cu_seqlens_k, ws)
+    dev, shape = q.device, (tq, params.n_q_heads, params.head_dim)
+    if out is not None:
+        _check_tensor(out, "hla_attention: out", q.dtype, shape, dev)
+    if lse is not None:
+        _check_tensor(lse, "hla_attention: lse", torch.float32, shape[:2], dev)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = alloc_attention_workspace(params, tq, tk, n, device=dev)
+        _check(load().hla_attention(ctypes.byref(params.c(*strides)), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
+                                    _ptr(cu_seqlens_k), n, tq, tk, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), st),
+               "hla_attention")
+    return out, lse
+
+
+def attention_backward(params: AttnParams, q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k=None, grads=None,
+                       ws=None, stream=None):
+    """hla_attention_backward: {"q", "k", "v"} gradients of sum(dout * out), dense, in the layer's type, from
+    attention's inputs and results.  `grads` (same dict) and `ws` may be passed in to be reused."""
+    fn = "hla_attention_backward"
+    strides, tq, tk, n = _check_packed(fn, params, q, k, v, cu_seqlens_q, cu_seqlens_k, ws)
+    dev = q.device
+    for x, name in ((out, "out"), (dout, "dout")):
+        _check_tensor(x, f"{fn}: {name}", q.dtype, tuple(q.shape), dev)
+    _check_tensor(lse, f"{fn}: lse", torch.float32, tuple(q.shape[:2]), dev)
+    if grads is not None:
+        for name, x in zip("qkv", (q, k, v)):
+            _check_tensor(grads.get(name), f"{fn}: grads[{name!r}]", x.dtype, tuple(x.shape), dev)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        if grads is None:
+            grads = {name: torch.empty(x.shape, dtype=x.dtype, device=dev) for name, x in zip("qkv", (q, k, v))}
+        if ws is None:
+            ws = alloc_attention_workspace(params, tq, tk, n, backward=True, device=dev)
+        _check(load().hla_attention_backward(ctypes.byref(params.c(*strides)), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                             _ptr(lse), _ptr(dout), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), n, tq, tk,
+                                             _ptr(grads["q"]), _ptr(grads["k"]), _ptr(grads["v"]), _ptr(ws),
+                                             ws.numel(), st), fn)
+    return grads
+
+
+@dataclass
+class CacheParams:
+    n_kv_heads: int
+    head_dim: int
+    page_size: int
+    n_pages: int
+    max_pages: int
+    dtype: int = DTYPE_BF16         # of the rows written and read
+    cache_dtype: int = DTYPE_E4M3   # E4M3, or dtype
+
+    def c(self) -> CCacheParams:
+        return CCacheParams(self.n_kv_heads, self.head_dim, self.dtype, self.cache_dtype, self.page_size, self.n_pages,
+                            self.max_pages, 0)
+
+
+class Cache:
+    """A paged key / value cache: page_table int32 [n_seqs, max_pages] (kept, not copied: the caller updates it
+    as sequences grow); k, v [n_pages, Hkv, page_size, d] and k_exp, v_exp uint8 [n_pages, Hkv, page_size] are
+    allocated unless given."""
+
+    def __init__(self, params: CacheParams, page_table, k=None, v=None, k_exp=None, v_exp=None):
+        rows, exps = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(load().hla_cache_bytes(ctypes.byref(params.c()), ctypes.byref(rows), ctypes.byref(exps)),
+               "hla_cache_bytes")
+        _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2 and page_table.is_cuda,
+              "Cache: page_table must be [n_seqs, max_pages] on the GPU")
+        self.params, self.n_seqs, self.device = params, page_table.shape[0], page_table.device
+        _check_tensor(page_table, "Cache: page_table", torch.int32, (self.n_seqs, params.max_pages), self.device)
+        self.page_table = page_table
+        shape = (params.n_pages, params.n_kv_heads, params.page_size, params.head_dim)
+        kind = _TORCH[params.cache_dtype]
+        self.k, self.v = (self._buffer(t, n, kind, shape) for t, n in ((k, "k"), (v, "v")))
+        if exps.value or params.cache_dtype == DTYPE_E4M3:
+            self.k_exp, self.v_exp = (self._buffer(t, n, torch.uint8, shape[:3])
+                                      for t, n in ((k_exp, "k_exp"), (v_exp, "v_exp")))
+        else:
+            _need(k_exp is None and v_exp is None, "Cache: exponents go with an E4M3 cache")
+            self.k_exp = self.v_exp = None
+        self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self.c = CCache(*[None if t is None else t.data_ptr() for t in
+                          (self.k, self.v, self.k_exp, self.v_exp, self.page_table, self.err)])
+        self.cp = params.c()
+
+    def _buffer(self, t, name, dtype, shape):
+        if t is None:
+            return torch.zeros(shape, dtype=dtype, device=self.device)
+        _check_tensor(t, f"Cache: {name}", dtype, shape, self.device)
+        return t
+
+    def check_error(self, stream=None) -> int:
+        """Synchronises, reads and clears the cache's error word; returns it (0 = fine)."""
+        code = ctypes.c_int32()
+        ctx, st = _on(self.device, stream)
+        with ctx:
+            rc = load().hla_check_cache_error(ctypes.byref(self.c), st, ctypes.byref(code))
+        if rc not in (HLA_OK, HLA_ERR_STATE, HLA_ERR_TIMEOUT):
+            _check(rc, "cache error word")
+        return code.value
+
+
+def _check_rows(fn, cache, cu_seqlens, start):
+    dev = cache.device
+    _check_tensor(cu_seqlens, f"{fn}: cu_seqlens", torch.int32, (cache.n_seqs + 1,), dev)
+    _check_tensor(start, f"{fn}: start", torch.int64, (cache.n_seqs,), dev)
+
+
+def cache_write(cache: Cache, k, v, cu_seqlens, start, stream=None):
+    """hla_cache_write: packed rows k, v [T, Hkv, d] of cache.n_seqs sequences to positions start[n] + i."""
+    fn, p = "hla_cache_write", cache.params
+    _check_rows(fn, cache, cu_seqlens, start)
+    _need(isinstance(k, torch.Tensor) and k.dim() == 3, f"{fn}: k must be [T, Hkv, d]")
+    shape = (k.shape[0], p.n_kv_heads, p.head_dim)
+    for t, name in ((k, "k"), (v, "v")):
+        _check_tensor(t, f"{fn}: {name}", _TORCH[p.dtype], shape, cache.device)
+    ctx, st = _on(cache.device, stream)
+    with ctx:
+        _check(load().hla_cache_write(ctypes.byref(cache.cp), ctypes.byref(cache.c), _ptr(k), _ptr(v),
+                                      _ptr(cu_seqlens), _ptr(start), cache.n_seqs, shape[0], st), fn)
+
+
+def cache_read(cache: Cache, cu_seqlens, start, total_tokens: int, k=None, v=None, stream=None):
+    """hla_cache_read: (k, v) [total_tokens, Hkv, d] in the layer's type, the rows at positions start[n] + i."""
+    fn, p = "hla_cache_read", cache.params
+    _check_rows(fn, cache, cu_seqlens, start)
+    shape, dt = (total_tokens, p.n_kv_heads, p.head_dim), _TORCH[p.dtype]
+    _need(total_tokens >= 0, f"{fn}: total_tokens")
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            _check_tensor(t, f"{fn}: {name}", dt, shape, cache.device)
+    ctx, st = _on(cache.device, stream)
+    with ctx:
+        out = [torch.empty(shape, dtype=dt, device=cache.device) if t is None else t for t in (k, v)]
+        _check(load().hla_cache_read(ctypes.byref(cache.cp), ctypes.byref(cache.c), _ptr(cu_seqlens), _ptr(start),
+                                     cache.n_seqs, total_tokens, _ptr(out[0]), _ptr(out[1]), st), fn)
+    return out[0], out[1]
+
+
+def decode_workspace_bytes(params: AttnParams, cache_params: CacheParams) -> int:
+    n = ctypes.c_size_t()
+    _check(load().hla_attention_decode_workspace_bytes(ctypes.byref(params.c()), ctypes.byref(cache_params.c()),
+                                                       ctypes.byref(n)), "hla_attention_decode_workspace_bytes")
+    return n.value
+
+
+def alloc_decode_workspace(params: AttnParams, cache: Cache):
+    return torch.empty(decode_workspace_bytes(params, cache.params), dtype=torch.uint8, device=cache.device)
+
+
+def attention_decode(params: AttnParams, cache: Cache, q, lens, out=None, ws=None, stream=None):
+    """hla_attention_decode: out [N, Hq, d] of one query token per sequence, q [N, Hq, d] (rows may be slices of
+    a wider tensor), over positions 0 .. lens[n] - 1 of the cache."""
+    fn = "hla_attention_decode"
+    _need(params.dtype == cache.params.dtype, f"{fn}: the layer's and the cache's row types differ")
+    dt, dev, shape = _TORCH[params.dtype], cache.device, (cache.n_seqs, params.n_q_heads, params.head_dim)
+    stride = _check_tensor(q, f"{fn}: q", dt, shape, dev, strided=True)
+    _check_tensor(lens, f"{fn}: lens", torch.int64, (cache.n_seqs,), dev)
+    if out is not None:
+        _check_tensor(out, f"{fn}: out", dt, shape, dev)
+    _check_workspace(fn, ws, dev)
+    ctx, st = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=dev)
+        if ws is None:
+            ws = alloc_decode_workspace(params, cache)
+        _check(load().hla_attention_decode(ctypes.byref(params.c(stride)), ctypes.byref(cache.cp),
+                                           ctypes.byref(cache.c), _ptr(q), _ptr(lens), cache.n_seqs, _ptr(out),
+                                           _ptr(ws), ws.numel(), st), fn)
+    return out

@@ -1,0 +1,259 @@
+"""GPU packed causal attention and its gradient against a 64-bit form: types, head groups, lengths from none to
+several blocks, chunks behind earlier keys, rows that see nothing, padding, strides, streams and graphs.
+
+Tolerances, per element (u = eps / 2 of the stored type, u32 = 2^-24; mag = the sums with every product replaced
+by its magnitude):
+  scores: d fp32 products and sums, off by at most d u32 sum |q k| scale, which is the relative error of exp;
+  a sum over L keys adds at most L u32.  fp32 layers: out and dv (2 d S + L + 32) u32 mag, with S the largest
+  sum |q k| scale; dq and dk the same with twice the score error (p and dp) and their own sums.
+  bf16 layers add one rounding of p (and of dp's factor ds) to bf16, one of the stored out that D is formed
+  from, and the result's own: out, dv: u mag + u |x|; dq, dk: 3 u mag + u |x| (a rounding of ds, and D off by u |do| |o|).
+"""
+import math
+
+import pytest
+import torch
+
+import attention_cases as ac
+from linearized_attention_rope_gb300 import hla
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+TYPE = {"f32": (hla.DTYPE_F32, torch.float32), "bf16": (hla.DTYPE_BF16, torch.bfloat16)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    assert torch.cuda.is_available(), "the gpu-marked tests need a CUDA device"
+    from linearized_attention_rope_gb300 import build
+
+    build.build()
+
+
+def make(dtype, d, hq, hkv, q_lens, k_lens, pad_q=0, pad_k=0, seed=0):
+    t = TYPE[dtype][1]
+    tq, tk = sum(q_lens) + pad_q, sum(k_lens) + pad_k
+    x = {"q": ac.randn(seed + 1, tq, hq, d), "k": ac.randn(seed + 2, tk, hkv, d), "v": ac.randn(seed + 3, tk, hkv, d),
+         "dout": ac.randn(seed + 4, tq, hq, d)}
+    return {n: v.to(t) for n, v in x.items()}
+
+
+def params(dtype, d, hq, hkv, scale=0.0):
+    return hla.AttnParams(hq, hkv, d, dtype=TYPE[dtype][0], scale=scale)
+
+
+def run(prm, x, q_lens, k_lens, backward=True, same=False):
+    g = {n: t.cuda() for n, t in x.items()}
+    cq, ck = ac.cu(q_lens), None if same else ac.cu(k_lens)
+    ws = hla.alloc_attention_workspace(prm, g["q"].shape[0], g["k"].shape[0], len(q_lens), backward=True)
+    out, lse = hla.attention(prm, g["q"], g["k"], g["v"], cq, ck, ws=ws)
+    grads = hla.attention_backward(prm, g["q"], g["k"], g["v"], out, lse, g["dout"], cq, ck, ws=ws) if backward else {}
+    torch.cuda.synchronize()
+    assert hla.check_workspace_error(ws) == 0
+    return out, lse, grads
+
+
+def check(dtype, d, x, ref, out, lse, grads, q_lens, k_lens, scale=None):
+    r_out, r_lse, r_grads, mag = ref
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    nq, nk = sum(q_lens), sum(k_lens)
+    qm = x["q"][:nq].double().abs()
+    km = x["k"][:nk].double().abs()
+    S = float(scale * qm.norm(dim=-1).max() * km.norm(dim=-1).max()) if nq and nk else 0.0
+    L = max([1] + k_lens + [n * (x["q"].shape[1] // x["k"].shape[1]) for n in q_lens])
+    fp = (2 * d * S + L + 32) * U32
+    u = ac.EPS[TYPE[dtype][1]] / 2
+    half = 0.0 if dtype == "f32" else u
+    off = (lse.cpu().double()[:nq] - r_lse).abs()
+    seen = torch.isfinite(r_lse)
+    assert torch.equal(torch.isneginf(lse.cpu()[:nq]), ~seen)
+    assert (off[seen] <= fp + 4 * U32 * r_lse[seen].abs()).all()
+    got = {"out": out[:nq], **{n: g[: nq if n == "q" else nk] for n, g in grads.items()}}
+    want = {"out": r_out, **r_grads}
+    for name, g in got.items():
+        n = 3 if name in ("q", "k") else 1
+        tol = (n * half + 3 * fp) * mag[name] + 1.01 * u * want[name].abs()
+        diff = (g.cpu().double() - want[name]).abs()
+        assert (diff <= tol).all(), f"{name}: {float((diff - tol).max())} over, of {float(want[name].abs().max())}"
+        # on the whole (independent roundings): far below the bound per element.  Not where the exact result
+        # cancels: a row with one key has p = 1 and dp = D, so dq = 0 exactly, while dp and D, two sums of d
+        # products, each keep up to d u32 of their magnitude (for that the bound per element stands)
+        lim = 1e-4 if dtype == "f32" else 4 * u / math.sqrt(3)
+        if float(want[name].norm()) > 1e-2 * float(mag[name].norm()):
+            assert ac.rel(g, want[name]) <= lim, f"{name}: {ac.rel(g, want[name])}"
+
+
+def full_check(dtype, d, hq, hkv, q_lens, k_lens=None, scale=None, seed=0):
+    same = k_lens is None
+    k_lens = q_lens if same else k_lens
+    x = make(dtype, d, hq, hkv, q_lens, k_lens, seed=seed)
+    out, lse, grads = run(params(dtype, d, hq, hkv, scale or 0.0), x, q_lens, k_lens, same=same)
+    ref = ac.attention(x["q"], x["k"], x["v"], q_lens, k_lens, scale, dout=x["dout"])
+    check(dtype, d, x, ref, out, lse, grads, q_lens, k_lens, scale)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (2, 2), (6, 2), (8, 1), (12, 2)])
+def test_packed_prompts(dtype, d, hq, hkv):
+    full_check(dtype, d, hq, hkv, [1, 33, 0, 200, 64, 5])
+
+
+@pytest.mark.parametrize("dtype,d,lens", [("bf16", 128, [1]), ("bf16", 64, [1]), ("bf16", 128, [128]),
+                                          ("bf16", 128, [129]), ("bf16", 128, [255, 257]), ("bf16", 64, [700]),
+                                          ("bf16", 128, [900, 31]), ("f32", 64, [1]), ("f32", 128, [65, 190])])
+def test_lengths_around_the_tiles(dtype, d, lens):
+    full_check(dtype, d, 4, 2, lens)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunks_behind_earlier_keys(dtype, d):
+    full_check(dtype, d, 4, 2, [1, 40, 130, 3], [300, 41, 390, 3])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_see_no_key(dtype, d):
+    # fewer keys than queries: the first rows see nothing; a sequence without keys; one without queries
+    full_check(dtype, d, 4, 2, [60, 200, 10, 0], [20, 3, 0, 70])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_sequences(dtype):
+    lens = [(7 * i) % 23 for i in range(75)]
+    full_check(dtype, 64, 2, 1, lens)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scale_and_large_scores(dtype):
+    # scores of +-60: one key takes almost everything in many rows
+    full_check(dtype, 64, 2, 1, [150], scale=2.0, seed=5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_padding_is_left_alone_and_kept_out(dtype, d):
+    # rows behind the last sequence hold NaN: nothing of them is read into results, none of them is written
+    q_lens, k_lens = [50, 77], [50, 140]
+    x = make(dtype, d, 4, 2, q_lens, k_lens, pad_q=30, pad_k=41)
+    nq, nk = sum(q_lens), sum(k_lens)
+    for n in ("q", "dout"):
+        x[n][nq:] = math.nan
+    for n in ("k", "v"):
+        x[n][nk:] = math.nan
+    prm = params(dtype, d, 4, 2)
+    g = {n: t.cuda() for n, t in x.items()}
+    cq, ck = ac.cu(q_lens), ac.cu(k_lens)
+    ws = hla.alloc_attention_workspace(prm, nq + 30, nk + 41, 2, backward=True)
+    out, lse = torch.full_like(g["q"], 7.0), torch.full(g["q"].shape[:2], 7.0, device="cuda")
+    grads = {n: torch.full_like(g[n], 7.0) for n in "qkv"}
+    hla.attention(prm, g["q"], g["k"], g["v"], cq, ck, out=out, lse=lse, ws=ws)
+    hla.attention_backward(prm, g["q"], g["k"], g["v"], out, lse, g["dout"], cq, ck, grads=grads, ws=ws)
+    assert hla.check_workspace_error(ws) == 0
+    for t, n in ((out, nq), (lse, nq), (grads["q"], nq), (grads["k"], nk), (grads["v"], nk)):
+        assert (t[n:] == 7.0).all()
+    ref = ac.attention(x["q"][:nq], x["k"][:nk], x["v"][:nk], q_lens, k_lens, dout=x["dout"][:nq])
+    check(dtype, d, x, ref, out, lse, grads, q_lens, k_lens)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_other_sequences_stay_out(dtype, d):
+    # a sequence of NaN and infinities between two others changes nothing of them
+    lens = [70, 90, 41]
+    x = make(dtype, d, 2, 1, lens, lens)
+    x["q"][70:160], x["k"][70:160], x["v"][70:160], x["dout"][70:160] = math.nan, math.inf, -math.inf, math.nan
+    out, lse, grads = run(params(dtype, d, 2, 1), x, lens, lens)
+    for a, b in ((0, 70), (160, 201)):
+        y = {n: t[a:b] for n, t in x.items()}
+        ref = ac.attention(y["q"], y["k"], y["v"], [b - a], [b - a], dout=y["dout"])
+        check(dtype, d, y, ref, out[a:b], lse[a:b], {n: t[a:b] for n, t in grads.items()}, [b - a], [b - a])
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+def test_slices_of_a_fused_projection(dtype, d):
+    hq, hkv, lens = 4, 2, [100, 45]
+    x = make(dtype, d, hq, hkv, lens, lens)
+    ref = run(params(dtype, d, hq, hkv), x, lens, lens)
+    wide = torch.cat([x[n].flatten(1) for n in "qkv"], 1).cuda()
+    parts = wide.split([hq * d, hkv * d, hkv * d], 1)
+    q, k, v = (p.unflatten(1, (-1, d)) for p in parts)
+    prm, c = params(dtype, d, hq, hkv), ac.cu(lens)
+    out, lse = hla.attention(prm, q, k, v, c)
+    grads = hla.attention_backward(prm, q, k, v, out, lse, x["dout"].cuda(), c)
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    for n in "qkv":
+        assert torch.equal(grads[n], ref[2][n])
+
+
+def test_gradient_against_differences():
+    # (f(x + e r) - f(x - e r)) / 2e of sum(dout out), summed in float64 from the fp32 layer's outputs, against
+    # the gradient's product with r.  Outputs are off by about 50 u32 of their size each, so the quotient by
+    # sqrt(n) 50 u32 / e; the third derivative adds about e^2.
+    lens, d, hq, hkv = [40, 25], 64, 2, 1
+    x = make("f32", d, hq, hkv, lens, lens, seed=20)
+    prm, c = params("f32", d, hq, hkv), ac.cu(lens)
+    _, _, grads = run(prm, x, lens, lens)
+    e = 2.0 ** -6
+    for i, n in enumerate("qkv"):
+        r = ac.randn(40 + i, *x[n].shape, dtype=torch.float32)
+        f = []
+        for sign in (1, -1):
+            y = {m: (t + sign * e * r if m == n else t).cuda() for m, t in x.items()}
+            out, _ = hla.attention(prm, y["q"], y["k"], y["v"], c)
+            f.append(float((out.double() * y["dout"].double()).sum()))
+        step = float(((x[n] + e * r).double() - (x[n] - e * r).double()).flatten() @ grads[n].cpu().double().flatten()) / (2 * e)
+        size = float(grads[n].double().norm()) * float(r.double().norm()) / math.sqrt(r.numel())
+        assert abs((f[0] - f[1]) / (2 * e) - step) <= 20 * e * e * size + 1e-3 * size
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+def test_runs_agree_bit_for_bit_on_any_stream_and_in_a_graph(dtype, d):
+    lens = [300, 1, 170]
+    x = make(dtype, d, 4, 2, lens, lens)
+    prm, c = params(dtype, d, 4, 2), ac.cu(lens)
+    g = {n: t.cuda() for n, t in x.items()}
+    ref = run(prm, x, lens, lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = hla.attention(prm, g["q"], g["k"], g["v"], c, stream=side)
+    grads = hla.attention_backward(prm, g["q"], g["k"], g["v"], out, lse, g["dout"], c, stream=side)
+    side.synchronize()
+    assert torch.equal(out, ref[0]) and all(torch.equal(grads[n], ref[2][n]) for n in "qkv")
+    ws = hla.alloc_attention_workspace(prm, sum(lens), sum(lens), 3, backward=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, l2 = hla.attention(prm, g["q"], g["k"], g["v"], c, ws=ws)
+        g2 = hla.attention_backward(prm, g["q"], g["k"], g["v"], o2, l2, g["dout"], c, ws=ws)
+    for _ in range(2):
+        o2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, ref[0]) and all(torch.equal(g2[n], ref[2][n]) for n in "qkv")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("table", [[0, 50, 40, 100], [5, 50, 60, 100], [0, 50, 60, 300], [0, -7, 1 << 30, 20]])
+def test_malformed_tables_are_flagged(dtype, table):
+    x = make(dtype, 64, 2, 1, [100], [100])
+    prm, g = params(dtype, 64, 2, 1), {n: t.cuda() for n, t in x.items()}
+    c = torch.tensor(table, dtype=torch.int32, device="cuda")
+    ws = hla.alloc_attention_workspace(prm, 100, 100, 3, backward=True)
+    out, lse = hla.attention(prm, g["q"], g["k"], g["v"], c, ws=ws)
+    assert hla.check_workspace_error(ws) != 0 and hla.check_workspace_error(ws) == 0
+    hla.attention_backward(prm, g["q"], g["k"], g["v"], out, lse, g["dout"], c, ws=ws)
+    assert hla.check_workspace_error(ws) != 0
+
+
+def test_longer_prompt_against_64_bit_on_the_gpu():
+    # several rounds of the key ring and every query block of a 2300-token prompt with eight heads per kv head
+    lens = [2300]
+    x = make("bf16", 128, 8, 1, lens, lens, seed=9)
+    out, lse, grads = run(params("bf16", 128, 8, 1), x, lens, lens)
+    y = {n: t.cuda() for n, t in x.items()}
+    ref = ac.attention(y["q"], y["k"], y["v"], lens, lens, dout=y["dout"])
+    ref = tuple({n: t.cpu() for n, t in r.items()} if isinstance(r, dict) else r.cpu() for r in ref)
+    check("bf16", 128, x, ref, out, lse, grads, lens, lens)
