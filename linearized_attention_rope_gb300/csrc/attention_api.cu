@@ -4,7 +4,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "attention.cuh"
+#include "attention_tc.cuh"
 
 using namespace hla;
 
@@ -241,9 +241,10 @@ HLA_API int hla_attention(const hla_attn_params* p, const void* q, const void* k
         return status(launch_attention_simt(A, static_cast<const float*>(q), static_cast<const float*>(k),
                                             static_cast<const float*>(v), cu_q, cu_k, static_cast<float*>(out), lse,
                                             err, st));
-    return status(launch_attention_simt(A, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-                                        static_cast<const __nv_bfloat16*>(v), cu_q, cu_k,
-                                        static_cast<__nv_bfloat16*>(out), lse, err, st));
+    const auto launch = attention_tc_supported(A) ? launch_attention_tc : launch_attention_simt<__nv_bfloat16>;
+    return status(launch(A, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+                         static_cast<const __nv_bfloat16*>(v), cu_q, cu_k, static_cast<__nv_bfloat16*>(out), lse, err,
+                         st));
 }
 
 HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, const void* k, const void* v,

@@ -22,6 +22,9 @@ namespace tma {
 // if the driver rejects it.
 bool make_map_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t n0, uint64_t n1, uint64_t n2, uint32_t b0,
                  uint32_t b1, uint32_t b2);
+// The same with the byte stride between the outermost rows (a multiple of 16) given.
+bool make_map_3d_strided(CUtensorMap* map, const void* base, bool bf16, uint64_t n0, uint64_t n1, uint64_t n2,
+                         uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2);
 // The (64, 1, 64) fp16 box used for chunks of 64 token rows.
 inline bool make_map_f16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2) {
     return make_map_3d(map, base, false, n0, n1, n2, 64, 1, 64);
