@@ -137,7 +137,7 @@ constexpr size_t kWsHead = 256;  // the error word
 
 size_t attn_ws_bytes(const hla_attn_params* p, int64_t total_q, int64_t, int, bool backward) {
     size_t n = kWsHead;
-    if (backward) n += ((size_t)total_q * p->n_q_heads * sizeof(float) + 255) / 256 * 256;  // dout . out per row
+    if (backward) n += ((size_t)total_q * p->n_q_heads * sizeof(float2) + 255) / 256 * 256;  // per row and head
     return n;
 }
 
@@ -266,16 +266,22 @@ HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, cons
     if (!cu_k) cu_k = cu_q;
     const AttnDims A = attn_dims(p, n_seqs, total_q, total_k);
     int32_t* err = static_cast<int32_t*>(ws);
-    float* delta = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHead);
+    void* rows_ws = static_cast<char*>(ws) + kWsHead;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    using bf = __nv_bfloat16;
+    if (p->dtype == HLA_DTYPE_BF16 && attention_tc_supported(A))
+        return status(launch_attention_backward_tc(
+            A, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
+            static_cast<const bf*>(out), lse, static_cast<const bf*>(dout), cu_q, cu_k, static_cast<bf*>(dq),
+            static_cast<bf*>(dk), static_cast<bf*>(dv), static_cast<float2*>(rows_ws), err, st));
     auto run = [&](auto t) {
         using T = decltype(t);
         return status(launch_attention_backward_simt(
             A, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), static_cast<const T*>(out),
             lse, static_cast<const T*>(dout), cu_q, cu_k, static_cast<T*>(dq), static_cast<T*>(dk),
-            static_cast<T*>(dv), delta, err, st));
+            static_cast<T*>(dv), static_cast<float*>(rows_ws), err, st));
     };
-    return p->dtype == HLA_DTYPE_F32 ? run(float()) : run(__nv_bfloat16());
+    return p->dtype == HLA_DTYPE_F32 ? run(float()) : run(bf());
 }
 
 HLA_API int hla_cache_bytes(const hla_cache_params* p, size_t* rows, size_t* exponents) {

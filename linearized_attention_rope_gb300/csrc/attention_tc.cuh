@@ -95,7 +95,7 @@ cudaError_t launch_attention_tc(const AttnDims& A, const __nv_bfloat16* q, const
 cudaError_t launch_attention_backward_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                          const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
                                          const __nv_bfloat16* dout, const int32_t* cu_q, const int32_t* cu_k,
-                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, float* delta,
+                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, float2* stats,
                                          int32_t* err, cudaStream_t st);
 
 }  // namespace hla

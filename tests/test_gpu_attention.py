@@ -248,12 +248,13 @@ def test_malformed_tables_are_flagged(dtype, table):
     assert hla.check_workspace_error(ws) != 0
 
 
-def test_longer_prompt_against_64_bit_on_the_gpu():
-    # several rounds of the key ring and every query block of a 2300-token prompt with eight heads per kv head
-    lens = [2300]
-    x = make("bf16", 128, 8, 1, lens, lens, seed=9)
-    out, lse, grads = run(params("bf16", 128, 8, 1), x, lens, lens)
+@pytest.mark.parametrize("d,hq,hkv,q_lens,k_lens", [(128, 8, 1, [2300], [2300]), (64, 8, 1, [2300], [2300]),
+                                                    (128, 3, 1, [1500, 900], [1500, 1900]), (64, 6, 1, [1011, 700], [1011, 3000])])
+def test_longer_prompts_against_64_bit_on_the_gpu(d, hq, hkv, q_lens, k_lens):
+    # many rounds of the rings of tiles, with a ragged last tile in every group of heads
+    x = make("bf16", d, hq, hkv, q_lens, k_lens, seed=9)
+    out, lse, grads = run(params("bf16", d, hq, hkv), x, q_lens, k_lens)
     y = {n: t.cuda() for n, t in x.items()}
-    ref = ac.attention(y["q"], y["k"], y["v"], lens, lens, dout=y["dout"])
+    ref = ac.attention(y["q"], y["k"], y["v"], q_lens, k_lens, dout=y["dout"])
     ref = tuple({n: t.cpu() for n, t in r.items()} if isinstance(r, dict) else r.cpu() for r in ref)
-    check("bf16", 128, x, ref, out, lse, grads, lens, lens)
+    check("bf16", d, x, ref, out, lse, grads, q_lens, k_lens)
