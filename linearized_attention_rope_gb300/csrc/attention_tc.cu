@@ -30,6 +30,7 @@ namespace {
 using namespace attn_tc;
 
 constexpr float kLazy = 8.0f;
+constexpr int kBarS = 1, kBarP = 3;  // hardware barriers: scores ready, probabilities ready (+ tile)
 
 template <int D> struct Cfg {
     static constexpr uint32_t kTile = kRows * D * 2;  // bytes of a tile
@@ -49,7 +50,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     using C = Cfg<D>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int pack = 1 << lpack, qb = kRows >> lpack, n_hg = A.Hq >> lpack;
     if (blockIdx.x == 0) {
         attn_check_table(cu_q, A.n_seqs, A.total_q, err);
@@ -65,17 +66,17 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         return p0 < B.lq ? max(0, min(B.lk, min(p0 + qb, B.lq) + off)) : 0;
     };
     const int end0 = key_end(0), end1 = key_end(1), end = max(end0, end1);
-    const int n0 = (end0 + kRows - 1) / kRows, n1 = (end1 + kRows - 1) / kRows, n = max(n0, n1);
+    const int n0 = __shfl_sync(0xffffffffu, (end0 + kRows - 1) / kRows, 0);
+    const int n1 = __shfl_sync(0xffffffffu, (end1 + kRows - 1) / kRows, 0), n = max(n0, n1);
 
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
     const uint32_t bar_q = bars, bar_full = bars + 16, bar_empty = bar_full + 8 * C::kSlots;
-    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_fix = bar_o + 16;
+    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_o = bar_s + 16, bar_fix = bar_o + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 248);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             umma::mbar_init(bar_q + 8 * i, 1);
             umma::mbar_init(bar_s + 8 * i, 1);
-            umma::mbar_init(bar_p + 8 * i, kRows);
             umma::mbar_init(bar_o + 8 * i, 1);
         }
         for (int i = 0; i < C::kSlots; ++i) {
@@ -89,7 +90,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp >= 8) {
     give_registers();
@@ -131,56 +132,72 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             for (int i = max(0, issued - C::kSlots); i < issued; ++i)
                 wait_or_flag(bar_full + 8 * (i % C::kSlots), (i / C::kSlots) & 1, err);
     } else if (warp == 9) {
-        // ---- products
-        if (lane == 0 && n > 0) {
-            const uint32_t id_s = umma::idesc_bf16(kRows, kRows, false, false);
-            const uint32_t id_o = umma::idesc_bf16(kRows, D, false, true);
-            auto full = [&](int u) { return wait_or_flag(bar_full + 8 * (u % C::kSlots), (u / C::kSlots) & 1, err); };
-            auto scores = [&](int t, int j) {
-                const uint32_t kb = base + C::kRing + ((2 * j) % C::kSlots) * C::kTile;
-                const uint64_t a = umma::kmajor(base + C::kQ + t * C::kTile, kRows, 0), b = umma::kmajor(kb, kRows, 0);
+        // ---- products: one lane issues, the warp stays together
+        const uint32_t lead = umma::elect_one();
+        const uint32_t id_s = umma::idesc_bf16(kRows, kRows, false, false);
+        const uint32_t id_o = umma::idesc_bf16(kRows, D, false, true);
+        bool ok = true;
+        auto full = [&](int u) {
+            ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar_full + 8 * (u % C::kSlots), (u / C::kSlots) & 1, err));
+        };
+        auto scores = [&](int t, int j) {
+            if (!ok) return;
+            const uint32_t kb = base + C::kRing + ((2 * j) % C::kSlots) * C::kTile;
+            const uint64_t a = umma::kmajor(base + C::kQ + t * C::kTile, kRows, 0), b = umma::kmajor(kb, kRows, 0);
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
-                    umma::mma(tmem + C::kS + t * kRows, a + ks, b + ks, id_s, s > 0);
-                }
-                umma::commit(bar_s + 8 * t);
-            };
-            auto values = [&](int t, int j) {
-                const uint32_t vb = base + C::kRing + ((2 * j + 1) % C::kSlots) * C::kTile;
-                const uint64_t b = umma::mnmajor(vb, kRows * 128, 0);
+            for (int s = 0; s < D / 16; ++s) {
+                const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
+                umma::mma_lead(tmem + C::kS + t * kRows, a + ks, b + ks, id_s, s > 0, lead);
+            }
+            if (lead) umma::commit(bar_s + 8 * t);
+        };
+        auto values = [&](int t, int j) {
+            if (!ok) return;
+            const uint32_t vb = base + C::kRing + ((2 * j + 1) % C::kSlots) * C::kTile;
+            const uint64_t b = umma::mnmajor(vb, kRows * 128, 0);
 #pragma unroll
-                for (int s = 0; s < kRows / 16; ++s)
-                    umma::mma_ts(tmem + C::kO + t * D, tmem + C::kS + t * kRows + 8 * s, b + (uint64_t)(s * 128), id_o,
-                                 j > 0 || s > 0);
-            };
-            bool ok = full(0);
-            for (int t = 0; t < 2 && ok; ++t) {
-                if ((t ? n1 : n0) == 0) continue;
-                if (!(ok = wait_or_flag(bar_q + 8 * t, 0, err))) break;
-                umma::fence_after_sync();
-                scores(t, 0);
-            }
-            if (ok) umma::commit(bar_empty + 0);
-            for (int j = 0; j < n && ok; ++j) {
-                const bool more = j + 1 < n;
-                if (!(ok = full(2 * j + 1) && (!more || full(2 * j + 2)))) break;
-                if (!more && !(ok = wait_or_flag(bar_fix, 0, err))) break;
-                for (int t = 0; t < 2; ++t) {
-                    const int nt = t ? n1 : n0;
-                    if (j >= nt) continue;
-                    if (!(ok = wait_or_flag(bar_p + 8 * t, j & 1, err))) break;
-                    umma::fence_after_sync();
-                    values(t, j);
-                    if (j + 1 < nt) scores(t, j + 1);
-                    else umma::commit(bar_o + 8 * t);
-                }
-                if (!ok) break;
-                umma::commit(bar_empty + 8 * ((2 * j + 1) % C::kSlots));
-                if (more) umma::commit(bar_empty + 8 * ((2 * j + 2) % C::kSlots));
-            }
+            for (int s = 0; s < kRows / 16; ++s)
+                umma::mma_ts_lead(tmem + C::kO + t * D, tmem + C::kS + t * kRows + 8 * s, b + (uint64_t)(s * 128),
+                                  id_o, j > 0 || s > 0, lead);
+        };
+        auto done = [&](uint32_t bar) {
+            if (ok && lead) umma::commit(bar);
+        };
+        if (n > 0) full(0);
+        for (int t = 0; t < 2; ++t) {
+            if ((t ? n1 : n0) == 0) continue;
+            ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar_q + 8 * t, 0, err));
+            umma::fence_after_sync();
+            scores(t, 0);
         }
-        __syncwarp();
+        if (n > 0) done(bar_empty);
+        for (int j = 0; j < n; ++j) {
+            const bool more = j + 1 < n;
+            full(2 * j + 1);
+            if (more) full(2 * j + 2);
+            else ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar_fix, 0, err));
+            for (int t = 0; t < 2; ++t) {
+                const int nt = t ? n1 : n0;
+                if (j >= nt) continue;
+                named_sync(kBarP + t, 160);
+                umma::fence_after_sync();
+                values(t, j);
+                if (j + 1 < nt) scores(t, j + 1);
+                else done(bar_o + 8 * t);
+            }
+            done(bar_empty + 8 * ((2 * j + 1) % C::kSlots));
+            if (more) done(bar_empty + 8 * ((2 * j + 2) % C::kSlots));
+        }
+    } else {
+        // ---- warps 10, 11: pass "scores ready" of tile 0, 1 on to its softmax warps
+        const int t = warp - 10, nt = t ? n1 : n0;
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            ok = ok && wait_or_flag(bar_s + 8 * t, j & 1, err);
+            umma::fence_after_sync();
+            umma::fence_before_sync();
+            named_arrive(kBarS + t, 160);
+        }
     }
     } else {
         take_registers();
@@ -194,9 +211,8 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         const float cs = A.scale * kLog2e;
         float m = -INFINITY;
         float2 l = make_float2(0.f, 0.f);
-        bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            if (!(ok = wait_or_flag(bar_s + 8 * t, j & 1, err))) break;
+            named_sync(kBarS + t, 160);
             umma::fence_after_sync();
             float x[128];
             {
@@ -257,14 +273,14 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             }
             umma::tmem_wait_st();
             umma::fence_before_sync();
-            umma::mbar_arrive(bar_p + 8 * t);
+            named_arrive(kBarP + t, 160);
         }
         // ---- the row's output
         const float sum = l.x + l.y;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t at = (B.q0 + pos) * A.Hq + h;
         if (on) lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
-        if (ok && nt > 0) ok = wait_or_flag(bar_o + 8 * t, 0, err);
+        if (nt > 0) wait_or_flag(bar_o + 8 * t, 0, err);
         umma::fence_after_sync();
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {

@@ -77,6 +77,18 @@ __device__ __forceinline__ bool wait_or_flag(uint32_t mbar, uint32_t parity, int
     return false;
 }
 
+// Hardware barriers 1 .. 15 among some of the block's warps: `sync` waits,
+// `arrive` does not.  A warp that waits this way takes no issue slots, where
+// one that polls an mbarrier slows the warps beside it.  They cannot time out,
+// so whoever arrives does so in every round, whatever has happened; only
+// mbarrier waits, which are bounded, can fail.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // Rows [first, 128) of a 128 x D 16-bit tile (128-byte-swizzled 64-column blocks) set to zero by one warp.
 template <int D>
 __device__ __forceinline__ void zero_rows(unsigned char* tile, int first) {

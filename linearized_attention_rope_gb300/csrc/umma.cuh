@@ -75,12 +75,32 @@ __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uin
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
 }
 
-// The same with A in tensor memory: row m of A in lane m, 16-bit elements two to a column.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate) {
+// One lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p;
+}
+
+// For a converged warp: the lane with `lead` issues.  The operands are then
+// warp-uniform values; the same instruction inside a branch taken by one lane
+// cost about 90 cycles to issue (its operands moved to uniform registers one
+// by one), more than the 64 cycles of a 128 x 128 x 16 product.
+__device__ __forceinline__ void mma_lead(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate,
+                                         uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+        : "memory");
+}
+// The same with A in tensor memory: row m of A in lane m, 16-bit elements two to a column.
+__device__ __forceinline__ void mma_ts_lead(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            bool accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
         : "memory");
 }
 
