@@ -68,6 +68,10 @@ attn_stats_kernel(int64_t rows, const __nv_bfloat16* __restrict__ out, const __n
     }
 }
 
+// Hardware barriers between the elementwise warps (256 threads) and the warp that issues or passes on (32):
+// scores, probabilities, score gradients dP and dS ready.
+constexpr int kBarS = 1, kBarP = 2, kBarDp = 3, kBarDs = 4;
+
 template <int D> struct Cfg {
     static constexpr uint32_t kTile = kRows * D * 2;
     static constexpr int kSlots = D == 128 ? 5 : 8;
@@ -108,7 +112,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, int32_t* __restrict__ err) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char sm[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int qb = kRows >> lpack;
     if (blockIdx.x == 0) {
         attn_check_table(cu_q, A.n_seqs, A.total_q, err);
@@ -118,13 +122,13 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     if (!B.found) return;  // the whole block
     const int kv = blockIdx.x % A.Hkv, off = B.lk - B.lq;
     // query tiles: of each packed head group, those from the first that sees the block's first key
-    const int i0 = max(0, B.first - off) / qb, per = max(0, (B.lq + qb - 1) / qb - i0), n = per * (A.G >> lpack);
+    const int i0 = max(0, B.first - off) / qb, per = max(0, (B.lq + qb - 1) / qb - i0);
+    const int n = __shfl_sync(0xffffffffu, per * (A.G >> lpack), 0);
     const int tail = B.lq % qb ? (B.lq % qb) << lpack : kRows;  // rows of a group's last tile
 
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
     const uint32_t bar_kv = bars, bar_full = bars + 8, bar_empty = bar_full + 8 * C::kSlots;
-    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_p = bar_s + 8, bar_dp = bar_p + 8, bar_ds = bar_dp + 8;
-    const uint32_t bar_sf = bar_ds + 8, bar_se = bar_sf + 16, bar_fix = bar_se + 16, bar_done = bar_fix + 32;
+    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_dp = bar_s + 8, bar_fix = bar_dp + 8, bar_done = bar_fix + 32;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 248);
     if (tid == 0) {
         umma::mbar_init(bar_kv, 1);
@@ -133,13 +137,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             umma::mbar_init(bar_empty + 8 * i, 1);
         }
         umma::mbar_init(bar_s, 1);
-        umma::mbar_init(bar_p, 8);
         umma::mbar_init(bar_dp, 1);
-        umma::mbar_init(bar_ds, 8);
-        for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(bar_sf + 8 * i, 1);
-            umma::mbar_init(bar_se + 8 * i, 8);
-        }
         for (int i = 0; i < 4; ++i) umma::mbar_init(bar_fix + 8 * i, 1);
         umma::mbar_init(bar_done, 1);
         umma::fence_mbar_init();
@@ -148,7 +146,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t cS = tmem, cP = tmem + 128, cV = tmem + 256, cK = cV + D;  // S / P, dP / dS, dV, dK
     auto slot_of = [&](int use) { return use % C::kSlots; };
     auto par_of = [&](int use) { return (uint32_t)(use / C::kSlots) & 1u; };
@@ -200,85 +198,102 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 wait_or_flag(bar_kv, 0, err);
                 for (int i = max(0, u - C::kSlots); i < u; ++i) wait_or_flag(bar_full + 8 * slot_of(i), par_of(i), err);
             }
-        } else if (warp == 9 && lane == 0 && n > 0) {
-            // ---- products
+        } else if (warp == 9 && n > 0) {
+            // ---- products: one lane issues, the warp stays together
+            const uint32_t lead = umma::elect_one();
             const uint32_t id_s = umma::idesc_bf16(kRows, kRows, false, false);
             const uint32_t id_d = umma::idesc_bf16(kRows, D, false, true);
             int fixed = 0;
-            auto full = [&](int u) { return wait_or_flag(bar_full + 8 * slot_of(u), par_of(u), err); };
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar, parity, err));
+            };
             auto ring = [&](int u) { return base + C::kRing + slot_of(u) * C::kTile; };
             auto ready = [&](int i) {  // Q and dO of tile i, cleared behind the last row
-                bool r = full(2 * i) && full(2 * i + 1);
-                if (r && has_tail(i)) {
-                    r = wait_or_flag(bar_fix + 8 * (fixed & 3), (fixed >> 2) & 1, err);
+                wait(bar_full + 8 * slot_of(2 * i), par_of(2 * i));
+                wait(bar_full + 8 * slot_of(2 * i + 1), par_of(2 * i + 1));
+                if (has_tail(i)) {
+                    wait(bar_fix + 8 * (fixed & 3), (fixed >> 2) & 1);
                     ++fixed;
                 }
-                return r;
+                umma::fence_after_sync();
             };
             auto outer = [&](uint32_t d, uint32_t a_tile, uint32_t b_tile) {  // d = a b^T over d
+                if (!ok) return;
                 const uint64_t a = umma::kmajor(a_tile, kRows, 0), b = umma::kmajor(b_tile, kRows, 0);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
                     const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
-                    umma::mma(d, a + ks, b + ks, id_s, s > 0);
+                    umma::mma_lead(d, a + ks, b + ks, id_s, s > 0, lead);
                 }
             };
             auto inner = [&](uint32_t d, uint32_t a_cols, uint32_t b_tile, bool add) {  // d += a b over the rows
+                if (!ok) return;
                 const uint64_t b = umma::mnmajor(b_tile, kRows * 128, 0);
 #pragma unroll
                 for (int s = 0; s < kRows / 16; ++s)
-                    umma::mma_ts(d, half_step(a_cols, s), b + (uint64_t)(s * 128), id_d, add || s > 0);
+                    umma::mma_ts_lead(d, half_step(a_cols, s), b + (uint64_t)(s * 128), id_d, add || s > 0, lead);
             };
-            ok = wait_or_flag(bar_kv, 0, err) && ready(0);
-            if (ok) {
-                umma::fence_after_sync();
-                outer(cS, base + C::kFix, ring(0));
-                umma::commit(bar_s);
-                outer(cP, base + C::kFix + C::kTile, ring(1));
-                umma::commit(bar_dp);
-            }
-            for (int i = 0; i < n && ok; ++i) {
+            auto done = [&](uint32_t bar) {
+                if (ok && lead) umma::commit(bar);
+            };
+            wait(bar_kv, 0);
+            ready(0);
+            outer(cS, base + C::kFix, ring(0));
+            done(bar_s);
+            outer(cP, base + C::kFix + C::kTile, ring(1));
+            done(bar_dp);
+            for (int i = 0; i < n; ++i) {
                 const bool more = i + 1 < n;
-                if (!(ok = wait_or_flag(bar_p, i & 1, err))) break;
+                named_sync(kBarP, 288);
                 umma::fence_after_sync();
                 inner(cV, cS, ring(2 * i + 1), i > 0);
-                umma::commit(bar_empty + 8 * slot_of(2 * i + 1));
+                done(bar_empty + 8 * slot_of(2 * i + 1));
                 if (more) {
-                    if (!(ok = ready(i + 1))) break;
-                    umma::fence_after_sync();
+                    ready(i + 1);
                     outer(cS, base + C::kFix, ring(2 * i + 2));
-                    umma::commit(bar_s);
+                    done(bar_s);
                 }
-                if (!(ok = wait_or_flag(bar_ds, i & 1, err))) break;
+                named_sync(kBarDs, 288);
                 umma::fence_after_sync();
                 inner(cK, cP, ring(2 * i), i > 0);
-                umma::commit(bar_empty + 8 * slot_of(2 * i));
+                done(bar_empty + 8 * slot_of(2 * i));
                 if (more) {
                     outer(cP, base + C::kFix + C::kTile, ring(2 * i + 3));
-                    umma::commit(bar_dp);
+                    done(bar_dp);
                 }
             }
-            if (ok) umma::commit(bar_done);
+            done(bar_done);
         } else if (warp == 10) {
-            // ---- row stats of each tile, two stages; rows behind the sequence: probability 0
-            for (int i = 0; i < n && ok; ++i) {
+            // ---- row stats of each tile (rows behind the sequence: probability 0) in two stages, and "scores ready",
+            //      "score gradients ready" passed on to the elementwise warps.  dP of tile i + 1 is formed after dS of
+            //      tile i is complete, so by then the stage of tile i has been read.
+            auto load = [&](int i, float2 (&x)[4]) {
                 const int r0 = first_row(i), hg = h0 + ((i / per) << lpack);
-                float2 x[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const int r = lane + 32 * y, p = r0 + (r >> lpack);
                     x[y] = p < B.lq ? __ldg(stats + (B.q0 + p) * A.Hq + hg + (r & ((1 << lpack) - 1)))
                                     : make_float2(-INFINITY, 0.f);
                 }
-                if (i >= 2) ok = wait_or_flag(bar_se + 8 * (i & 1), ((i >> 1) - 1) & 1, err);
+            };
+            float2 x[4];
+            if (n > 0) load(0, x);
+            for (int i = 0; i < n; ++i) {
                 float* st = reinterpret_cast<float*>(sm + C::kStat + (i & 1) * 1024);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     st[lane + 32 * y] = x[y].x;
                     st[128 + lane + 32 * y] = x[y].y;
                 }
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive(bar_sf + 8 * (i & 1));
+                if (i + 1 < n) load(i + 1, x);
+                ok = ok && wait_or_flag(bar_s, i & 1, err);
+                umma::fence_after_sync();
+                umma::fence_before_sync();
+                named_arrive(kBarS, 288);
+                ok = ok && wait_or_flag(bar_dp, i & 1, err);
+                umma::fence_after_sync();
+                umma::fence_before_sync();
+                named_arrive(kBarDp, 288);
             }
         }
         __syncwarp();
@@ -289,12 +304,11 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         const uint32_t lanes = (uint32_t)((warp & 3) << 5) << 16;
         const uint32_t tS = cS + lanes + half * 64, tP = cP + lanes + half * 64;
         const float2 c2 = make_float2(A.scale * kLog2e, A.scale * kLog2e);
-        bool ok = true;
         for (int i = 0; i < n; ++i) {
             const float* st = reinterpret_cast<const float*>(sm + C::kStat + (i & 1) * 1024) + half * 64;
             // rows from column `from` on see the key: row position >= key - off
             const int from = max(-kRows, min(kRows, key - off - first_row(i))) * (1 << lpack) - half * 64;
-            if (!(ok = wait_or_flag(bar_sf + 8 * (i & 1), (i >> 1) & 1, err) && wait_or_flag(bar_s, i & 1, err))) break;
+            named_sync(kBarS, 288);
             umma::fence_after_sync();
             float2 p[32];
             load64(tS, p);
@@ -318,9 +332,8 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             umma::tmem_st32_async(tS, w);
             umma::tmem_wait_st();
             umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(bar_p);
-            if (!(ok = wait_or_flag(bar_dp, i & 1, err))) break;
+            named_arrive(kBarP, 288);
+            named_sync(kBarDp, 288);
             umma::fence_after_sync();
             float2 d[32];
             load64(tP, d);
@@ -335,14 +348,10 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             umma::tmem_st32_async(tP, w);
             umma::tmem_wait_st();
             umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                umma::mbar_arrive(bar_ds);
-                umma::mbar_arrive(bar_se + 8 * (i & 1));
-            }
+            named_arrive(kBarDs, 288);
         }
         // ---- results: dv by the first warpgroup, dk by the second
-        if (n > 0 && ok) ok = wait_or_flag(bar_done, 0, err);
+        if (n > 0) wait_or_flag(bar_done, 0, err);
         umma::fence_after_sync();
         const float mul = half ? A.scale : 1.f;
         __nv_bfloat16* dst = (half ? dk : dv) + ((B.k0 + key) * A.Hkv + kv) * D;
@@ -380,17 +389,18 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                   __nv_bfloat16* __restrict__ dq, int32_t* __restrict__ err) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char sm[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int qb = kRows >> lpack, n_hg = A.Hq >> lpack;
     const AttnBlock B = attn_find_block(A, cu_q, cu_k, qb, blockIdx.x / n_hg, false);
     if (!B.found) return;  // the whole block
     const int h0 = (int)(blockIdx.x % n_hg) << lpack, kv = h0 / A.G, off = B.lk - B.lq;
-    const int end = max(0, min(B.lk, min(B.first + qb, B.lq) + off)), n = (end + kRows - 1) / kRows;
+    const int end = max(0, min(B.lk, min(B.first + qb, B.lq) + off));
+    const int n = __shfl_sync(0xffffffffu, (end + kRows - 1) / kRows, 0);
 
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
     const uint32_t bar_q = bars, bar_full = bars + 8, bar_empty = bar_full + 8 * C::kSlots;
-    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_se = bar_s + 16, bar_dp = bar_se + 16, bar_ds = bar_dp + 8;
-    const uint32_t bar_fix = bar_ds + 8, bar_done = bar_fix + 8;
+    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_se = bar_s + 16, bar_dp = bar_se + 16, bar_fix = bar_dp + 8;
+    const uint32_t bar_done = bar_fix + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 248);
     if (tid == 0) {
         umma::mbar_init(bar_q, 1);
@@ -403,7 +413,6 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             umma::mbar_init(bar_se + 8 * i, 8);
         }
         umma::mbar_init(bar_dp, 1);
-        umma::mbar_init(bar_ds, 8);
         umma::mbar_init(bar_fix, 1);
         umma::mbar_init(bar_done, 1);
         umma::fence_mbar_init();
@@ -412,7 +421,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t cS = tmem, cP = tmem + 256, cQ = tmem + 384;  // S (two buffers), dP / dS, dQ
     auto slot_of = [&](int use) { return use % C::kSlots; };
     auto par_of = [&](int use) { return (uint32_t)(use / C::kSlots) & 1u; };
@@ -455,50 +464,72 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 wait_or_flag(bar_q, 0, err);
                 for (int i = max(0, u - C::kSlots); i < u; ++i) wait_or_flag(bar_full + 8 * slot_of(i), par_of(i), err);
             }
-        } else if (warp == 9 && lane == 0 && n > 0) {
-            // ---- products
+        } else if (warp == 9 && n > 0) {
+            // ---- products: one lane issues, the warp stays together
+            const uint32_t lead = umma::elect_one();
             const uint32_t id_s = umma::idesc_bf16(kRows, kRows, false, false);
             const uint32_t id_d = umma::idesc_bf16(kRows, D, false, true);
-            auto full = [&](int u) { return wait_or_flag(bar_full + 8 * slot_of(u), par_of(u), err); };
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar, parity, err));
+            };
             auto ring = [&](int u) { return base + C::kRing + slot_of(u) * C::kTile; };
             auto outer = [&](uint32_t d, uint32_t a_tile, uint32_t b_tile) {
+                if (!ok) return;
                 const uint64_t a = umma::kmajor(a_tile, kRows, 0), b = umma::kmajor(b_tile, kRows, 0);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
                     const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
-                    umma::mma(d, a + ks, b + ks, id_s, s > 0);
+                    umma::mma_lead(d, a + ks, b + ks, id_s, s > 0, lead);
                 }
             };
+            auto done = [&](uint32_t bar) {
+                if (ok && lead) umma::commit(bar);
+            };
             auto score = [&](int i) {  // S of tile i into its buffer, free once tile i - 2 has been read
-                if (i >= 2 && !wait_or_flag(bar_se + 8 * (i & 1), ((i >> 1) - 1) & 1, err)) return false;
-                if (!full(2 * i)) return false;
-                if (i == n - 1 && !wait_or_flag(bar_fix, 0, err)) return false;
+                if (i >= 2) wait(bar_se + 8 * (i & 1), ((i >> 1) - 1) & 1);
+                wait(bar_full + 8 * slot_of(2 * i), par_of(2 * i));
+                if (i == n - 1) wait(bar_fix, 0);
                 umma::fence_after_sync();
                 outer(cS + (i & 1) * 128, base + C::kFix, ring(2 * i));
-                umma::commit(bar_s + 8 * (i & 1));
-                return true;
+                done(bar_s + 8 * (i & 1));
             };
             auto grad = [&](int i) {  // dP of tile i
-                if (!full(2 * i + 1)) return false;
+                wait(bar_full + 8 * slot_of(2 * i + 1), par_of(2 * i + 1));
                 umma::fence_after_sync();
                 outer(cP, base + C::kFix + C::kTile, ring(2 * i + 1));
-                umma::commit(bar_dp);
-                umma::commit(bar_empty + 8 * slot_of(2 * i + 1));
-                return true;
+                done(bar_dp);
+                done(bar_empty + 8 * slot_of(2 * i + 1));
             };
-            ok = wait_or_flag(bar_q, 0, err) && score(0) && grad(0) && (n < 2 || score(1));
-            for (int i = 0; i < n && ok; ++i) {
-                if (!(ok = wait_or_flag(bar_ds, i & 1, err))) break;
+            wait(bar_q, 0);
+            score(0);
+            grad(0);
+            if (n > 1) score(1);
+            for (int i = 0; i < n; ++i) {
+                named_sync(kBarDs, 288);
                 umma::fence_after_sync();
-                const uint64_t b = umma::mnmajor(ring(2 * i), kRows * 128, 0);
+                if (ok) {
+                    const uint64_t b = umma::mnmajor(ring(2 * i), kRows * 128, 0);
 #pragma unroll
-                for (int s = 0; s < kRows / 16; ++s)
-                    umma::mma_ts(cQ, half_step(cP, s), b + (uint64_t)(s * 128), id_d, i > 0 || s > 0);
-                umma::commit(bar_empty + 8 * slot_of(2 * i));
-                if (i + 1 < n) ok = grad(i + 1);
-                if (ok && i + 2 < n) ok = score(i + 2);
+                    for (int s = 0; s < kRows / 16; ++s)
+                        umma::mma_ts_lead(cQ, half_step(cP, s), b + (uint64_t)(s * 128), id_d, i > 0 || s > 0, lead);
+                }
+                done(bar_empty + 8 * slot_of(2 * i));
+                if (i + 1 < n) grad(i + 1);
+                if (i + 2 < n) score(i + 2);
             }
-            if (ok) umma::commit(bar_done);
+            done(bar_done);
+        } else if (warp == 10) {
+            // ---- "scores ready", "score gradients ready" passed on to the elementwise warps
+            for (int i = 0; i < n; ++i) {
+                ok = ok && wait_or_flag(bar_s + 8 * (i & 1), (i >> 1) & 1, err);
+                umma::fence_after_sync();
+                umma::fence_before_sync();
+                named_arrive(kBarS, 288);
+                ok = ok && wait_or_flag(bar_dp, i & 1, err);
+                umma::fence_after_sync();
+                umma::fence_before_sync();
+                named_arrive(kBarDp, 288);
+            }
         }
         __syncwarp();
     } else {
@@ -513,11 +544,10 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
         const float2 st = on ? __ldg(stats + at) : make_float2(-INFINITY, 0.f);
         const float2 c2 = make_float2(A.scale * kLog2e, A.scale * kLog2e);
         const float2 nl = make_float2(st.x, st.x), nd = make_float2(st.y, st.y);
-        bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int seen = limit - i * kRows - half * 64;
             const bool edge = __any_sync(0xffffffffu, seen < 64);
-            if (!(ok = wait_or_flag(bar_s + 8 * (i & 1), (i >> 1) & 1, err))) break;
+            named_sync(kBarS, 288);
             umma::fence_after_sync();
             float2 p[32];
             load64(cS + (i & 1) * 128 + lanes + half * 64, p);
@@ -529,7 +559,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 const float2 a = ffma2(p[x], c2, nl);
                 p[x] = make_float2(ex2(a.x), ex2(a.y));
             }
-            if (!(ok = wait_or_flag(bar_dp, i & 1, err))) break;
+            named_sync(kBarDp, 288);
             umma::fence_after_sync();
             float2 d[32];
             load64(tP, d);
@@ -546,10 +576,9 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             umma::tmem_st32_async(tP, w);
             umma::tmem_wait_st();
             umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(bar_ds);
+            named_arrive(kBarDs, 288);
         }
-        if (n > 0 && ok) ok = wait_or_flag(bar_done, 0, err);
+        if (n > 0) wait_or_flag(bar_done, 0, err);
         umma::fence_after_sync();
         // ---- results: half of the columns each
         __nv_bfloat16* dst = dq + at * D + half * (D / 2);
