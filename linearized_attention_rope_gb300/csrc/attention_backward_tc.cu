@@ -69,7 +69,7 @@ attn_stats_kernel(int64_t rows, const __nv_bfloat16* __restrict__ out, const __n
 }
 
 // Hardware barriers between the elementwise warps (256 threads) and the warp that issues or passes on (32):
-// scores, probabilities, score gradients dP and dS ready.
+// scores, probabilities (dkdv; dq: scores of odd tiles), score gradients dP and dS ready.
 constexpr int kBarS = 1, kBarP = 2, kBarDp = 3, kBarDs = 4;
 
 template <int D> struct Cfg {
@@ -519,12 +519,14 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             }
             done(bar_done);
         } else if (warp == 10) {
-            // ---- "scores ready", "score gradients ready" passed on to the elementwise warps
+            // ---- "scores ready", "score gradients ready" passed on to the elementwise warps.  Scores run one tile
+            //      ahead: two barriers, so that a slow warp never meets the signal of the tile after its own (the one
+            //      after that waits until every warp has read this tile's scores)
             for (int i = 0; i < n; ++i) {
                 ok = ok && wait_or_flag(bar_s + 8 * (i & 1), (i >> 1) & 1, err);
                 umma::fence_after_sync();
                 umma::fence_before_sync();
-                named_arrive(kBarS, 288);
+                named_arrive(kBarS + (i & 1), 288);
                 ok = ok && wait_or_flag(bar_dp, i & 1, err);
                 umma::fence_after_sync();
                 umma::fence_before_sync();
@@ -547,7 +549,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
         for (int i = 0; i < n; ++i) {
             const int seen = limit - i * kRows - half * 64;
             const bool edge = __any_sync(0xffffffffu, seen < 64);
-            named_sync(kBarS, 288);
+            named_sync(kBarS + (i & 1), 288);
             umma::fence_after_sync();
             float2 p[32];
             load64(cS + (i & 1) * 128 + lanes + half * 64, p);

@@ -126,6 +126,31 @@ def test_many_sequences(dtype):
     full_check(dtype, 64, 2, 1, lens)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("length,hq,hkv", [(64, 32, 8), (130, 4, 1), (512, 32, 8), (33, 6, 2)])
+def test_many_short_items_again_and_again(d, length, hq, hkv):
+    # thousands of items of a few tiles each, many calls back to back: every hand-over between the warps of a block
+    # in every order that timing allows; all results equal, no wait runs out
+    lens = [length] * (16384 // length)
+    prm, c, n = hla.AttnParams(hq, hkv, d), ac.cu(lens), sum(lens)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    q, k, v, do = (torch.randn(n, h, d, generator=g, device="cuda").bfloat16() for h in (hq, hkv, hkv, hq))
+    ws = hla.alloc_attention_workspace(prm, n, n, len(lens), backward=True)
+    out, lse = hla.attention(prm, q, k, v, c, ws=ws)
+    grads = hla.attention_backward(prm, q, k, v, out, lse, do, c, ws=ws)
+    o2, l2, g2 = torch.empty_like(out), torch.empty_like(lse), {m: torch.empty_like(t) for m, t in grads.items()}
+    for _ in range(100):
+        hla.attention(prm, q, k, v, c, out=o2, lse=l2, ws=ws)
+        hla.attention_backward(prm, q, k, v, o2, l2, do, c, grads=g2, ws=ws)
+    assert hla.check_workspace_error(ws) == 0
+    assert torch.equal(out, o2) and torch.equal(lse, l2) and all(torch.equal(grads[m], g2[m]) for m in grads)
+    a, b = 2 * length, 3 * length  # one of them against the 64-bit form
+    x = {m: t[a:b].cpu() for m, t in (("q", q), ("k", k), ("v", v), ("dout", do))}
+    ref = ac.attention(x["q"], x["k"], x["v"], [length], [length], dout=x["dout"])
+    check("bf16", d, x, ref, out[a:b], lse[a:b], {m: t[a:b] for m, t in grads.items()}, [length], [length])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_scale_and_large_scores(dtype):
     # scores of +-60: one key takes almost everything in many rows
