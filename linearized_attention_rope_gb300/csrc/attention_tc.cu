@@ -36,7 +36,7 @@ template <int D> struct Cfg {
     static constexpr uint32_t kTile = kRows * D * 2;  // bytes of a tile
     static constexpr int kSlots = D == 128 ? 5 : 8;
     static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBar = kRing + kSlots * kTile;
-    static constexpr uint32_t kSmem = kBar + 256 + 1024;
+    static constexpr uint32_t kSmem = kBar + 320 + sizeof(ItemRing) + 1024;
     // TMEM columns
     static constexpr uint32_t kS = 0, kO = 256, kCols = 512;
 };
@@ -56,34 +56,31 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         attn_check_table(cu_q, A.n_seqs, A.total_q, err);
         attn_check_table(cu_k, A.n_seqs, A.total_k, err);
     }
-    const AttnBlock B = attn_find_block(A, cu_q, cu_k, 2 * qb, blockIdx.x / n_hg, false);
-    if (!B.found) return;  // the whole block
-    const int hg = blockIdx.x % n_hg, h0 = hg << lpack, kv = h0 / A.G;
-    const int off = B.lk - B.lq;
-    // positions of tile t: [first + t qb, ...); keys it sees: [0, end(t))
-    auto key_end = [&](int t) {
-        const int p0 = B.first + t * qb;
-        return p0 < B.lq ? max(0, min(B.lk, min(p0 + qb, B.lq) + off)) : 0;
-    };
-    const int end0 = key_end(0), end1 = key_end(1), end = max(end0, end1);
-    const int n0 = __shfl_sync(0xffffffffu, (end0 + kRows - 1) / kRows, 0);
-    const int n1 = __shfl_sync(0xffffffffu, (end1 + kRows - 1) / kRows, 0), n = max(n0, n1);
-
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
-    const uint32_t bar_q = bars, bar_full = bars + 16, bar_empty = bar_full + 8 * C::kSlots;
-    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_o = bar_s + 16, bar_fix = bar_o + 16;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 248);
+    const uint32_t bar_q = bars, bar_qe = bar_q + 16, bar_full = bar_qe + 16, bar_empty = bar_full + 8 * C::kSlots;
+    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_o = bar_s + 16, bar_oe = bar_o + 16, bar_fix = bar_oe + 16;
+    const uint32_t bar_it = bar_fix + 32, bar_ie = bar_it + 8 * kItems, bar_ask = bar_ie + 8 * kItems, bar_want = bar_ask + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 316);
+    ItemRing* items = reinterpret_cast<ItemRing*>(sm + C::kBar + 320);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             umma::mbar_init(bar_q + 8 * i, 1);
+            umma::mbar_init(bar_qe + 8 * i, 1);
             umma::mbar_init(bar_s + 8 * i, 1);
             umma::mbar_init(bar_o + 8 * i, 1);
+            umma::mbar_init(bar_oe + 8 * i, 4);
         }
         for (int i = 0; i < C::kSlots; ++i) {
             umma::mbar_init(bar_full + 8 * i, 1);
             umma::mbar_init(bar_empty + 8 * i, 1);
         }
-        umma::mbar_init(bar_fix, 1);
+        for (int i = 0; i < 4; ++i) umma::mbar_init(bar_fix + 8 * i, 1);
+        umma::mbar_init(bar_ask, 1);
+        umma::mbar_init(bar_want, 1);
+        for (int i = 0; i < kItems; ++i) {
+            umma::mbar_init(bar_it + 8 * i, 1);
+            umma::mbar_init(bar_ie + 8 * i, kItemWarps);
+        }
         umma::fence_mbar_init();
     }
     if (warp == 9) umma::tmem_alloc(tmem_slot, C::kCols);
@@ -92,212 +89,286 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     umma::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
+    // what an item's two tiles see: keys [0, end), tile t in nt = n[t] key tiles
+    struct Span { int end, n0, n1, n; };
+    auto span = [&](const Item& it) {
+        const int off = it.lk - it.lq;
+        auto key_end = [&](int t) {
+            const int p0 = it.first + t * qb;
+            return p0 < it.lq ? max(0, min(it.lk, min(p0 + qb, it.lq) + off)) : 0;
+        };
+        const int e0 = key_end(0), e1 = key_end(1);
+        const int n0 = __shfl_sync(0xffffffffu, (e0 + kRows - 1) / kRows, 0);
+        const int n1 = __shfl_sync(0xffffffffu, (e1 + kRows - 1) / kRows, 0);
+        return Span{max(e0, e1), n0, n1, max(n0, n1)};
+    };
+    auto slot_of = [&](int use) { return use % C::kSlots; };
+    auto par_of = [&](int use) { return (uint32_t)(use / C::kSlots) & 1u; };
+
     if (warp >= 8) {
-    give_registers();
-    if (warp == 8) {
-        // ---- loads: use u of the ring is K tile u / 2 (even) or V tile u / 2 (odd)
+        give_registers();
         bool ok = true;
-        int issued = 0;
-        const int uses = 2 * n;
-        if (lane == 0 && n > 0) {
-            for (int t = 0; t < 2; ++t) {
-                const int p0 = B.first + t * qb;
-                if ((t ? n1 : n0) == 0) continue;
-                tma::expect_tx(bar_q + 8 * t, C::kTile);
-                for (int b = 0; b < D / 64; ++b)
-                    tma::tensor_load_3d(base + C::kQ + t * C::kTile + b * (kRows * 128), &map_q, 64 * b, h0,
-                                        (int)(B.q0 + p0), bar_q + 8 * t);
+        if (warp == 8) {
+            // ---- loads: of an item, use 2 j of the ring is K tile j, use 2 j + 1 V tile j
+            int use = 0, items_q[2] = {0, 0}, n_fix = 0;
+            for (int i = 0;; ++i) {
+                const Item it = next_item(items, i, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                const Span sp = span(it);
+                const int kv = it.head / A.G, ask_at = max(0, 2 * sp.n - 3);
+                if (sp.n == 0 && lane == 0) umma::mbar_arrive(bar_want);
+                for (int u = 0; u < 2 * sp.n; ++u) {
+                    if (u == ask_at && lane == 0) umma::mbar_arrive(bar_want);  // time to look for the next item
+                    if (!ok) continue;
+                    const int slot = slot_of(use + u);
+                    if (use + u >= C::kSlots)
+                        ok = wait_or_flag(bar_empty + 8 * slot, par_of(use + u - C::kSlots), err);
+                    if (!ok) continue;
+                    if (lane == 0) {
+                        tma::expect_tx(bar_full + 8 * slot, C::kTile);
+                        for (int b = 0; b < D / 64; ++b)
+                            tma::tensor_load_3d(base + C::kRing + slot * C::kTile + b * (kRows * 128),
+                                                u & 1 ? &map_v : &map_k, 64 * b, kv, it.k0 + (u >> 1) * kRows,
+                                                bar_full + 8 * slot);
+                    }
+                    if (u > 0) continue;
+                    for (int t = 0; t < 2 && ok; ++t) {  // the query tiles, once the last item's scores are formed
+                        if ((t ? sp.n1 : sp.n0) == 0) continue;
+                        if (items_q[t] > 0) ok = wait_or_flag(bar_qe + 8 * t, (items_q[t] - 1) & 1, err);
+                        ++items_q[t];
+                        if (ok && lane == 0) {
+                            tma::expect_tx(bar_q + 8 * t, C::kTile);
+                            for (int b = 0; b < D / 64; ++b)
+                                tma::tensor_load_3d(base + C::kQ + t * C::kTile + b * (kRows * 128), &map_q, 64 * b,
+                                                    it.head, it.q0 + it.first + t * qb, bar_q + 8 * t);
+                        }
+                    }
+                }
+                if (sp.n > 0 && ok) {
+                    // the last V tile: rows behind the last visible key weigh 0; clear them, whatever they hold.  (The
+                    // ring holds the tiles of at most four items, so four barriers keep an item's signal until the
+                    // products have seen it.)
+                    static_assert(C::kSlots <= 8, "items in the ring");
+                    const int u = use + 2 * sp.n - 1;
+                    ok = wait_or_flag(bar_full + 8 * slot_of(u), par_of(u), err);
+                    if (ok) zero_rows<D>(sm + C::kRing + slot_of(u) * C::kTile, sp.end - (sp.n - 1) * kRows);
+                    umma::fence_async_smem();
+                    __syncwarp();
+                    if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (n_fix & 3));
+                    ++n_fix;
+                }
+                use += 2 * sp.n;
             }
-            for (; issued < uses && ok; ++issued) {
-                const int slot = issued % C::kSlots, round = issued / C::kSlots;
-                if (round > 0 && !(ok = wait_or_flag(bar_empty + 8 * slot, (round - 1) & 1, err))) break;
-                tma::expect_tx(bar_full + 8 * slot, C::kTile);
-                const int tk = (int)B.k0 + (issued >> 1) * kRows;
-                for (int b = 0; b < D / 64; ++b)
-                    tma::tensor_load_3d(base + C::kRing + slot * C::kTile + b * (kRows * 128),
-                                        issued & 1 ? &map_v : &map_k, 64 * b, kv, tk, bar_full + 8 * slot);
-            }
-        }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-        if (n > 0 && ok) {
-            // the last V tile: rows behind the last visible key weigh 0; clear them, whatever they hold
-            const int u = uses - 1, slot = u % C::kSlots;
-            ok = wait_or_flag(bar_full + 8 * slot, (u / C::kSlots) & 1, err);
-            zero_rows<D>(sm + C::kRing + slot * C::kTile, end - (n - 1) * kRows);
-            umma::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(bar_fix);
-        }
-        if (!ok && lane == 0)  // copies in flight land before the block ends
-            for (int i = max(0, issued - C::kSlots); i < issued; ++i)
-                wait_or_flag(bar_full + 8 * (i % C::kSlots), (i / C::kSlots) & 1, err);
-    } else if (warp == 9) {
-        // ---- products: one lane issues, the warp stays together
-        const uint32_t lead = umma::elect_one();
-        const uint32_t id_s = umma::idesc_bf16(kRows, kRows, false, false);
-        const uint32_t id_o = umma::idesc_bf16(kRows, D, false, true);
-        bool ok = true;
-        auto full = [&](int u) {
-            ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar_full + 8 * (u % C::kSlots), (u / C::kSlots) & 1, err));
-        };
-        auto scores = [&](int t, int j) {
-            if (!ok) return;
-            const uint32_t kb = base + C::kRing + ((2 * j) % C::kSlots) * C::kTile;
-            const uint64_t a = umma::kmajor(base + C::kQ + t * C::kTile, kRows, 0), b = umma::kmajor(kb, kRows, 0);
+            // after a failed wait, copies may be in flight: let them land (a failed wait has taken two seconds,
+            // a copy takes microseconds)
+        } else if (warp == 9) {
+            // ---- products: one lane issues, the warp stays together
+            const uint32_t lead = umma::elect_one();
+            const uint32_t id_s = umma::idesc_bf16(kRows, kRows, false, false);
+            const uint32_t id_o = umma::idesc_bf16(kRows, D, false, true);
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar, parity, err));
+            };
+            auto done = [&](uint32_t bar) {
+                if (ok && lead) umma::commit(bar);
+            };
+            int use = 0, count[2] = {0, 0}, n_fix = 0;  // ring uses, items with tile t, items
+            for (int i = 0;; ++i) {
+                const Item it = next_item(items, i, bar_it, bar_ie, err);
+                if (__shfl_sync(0xffffffffu, it.head, 0) < 0) break;
+                const Span sp = span(it);
+                const int n = sp.n;
+                if (n == 0) continue;
+                auto k_tile = [&](int j) { return umma::kmajor(base + C::kRing + slot_of(use + 2 * j) * C::kTile, kRows, 0); };
+                auto v_tile = [&](int j) {
+                    return umma::mnmajor(base + C::kRing + slot_of(use + 2 * j + 1) * C::kTile, kRows * 128, 0);
+                };
+                auto scores = [&](int t, int j, uint64_t b) {
+                    if (ok) {
+                        const uint64_t a = umma::kmajor(base + C::kQ + t * C::kTile, kRows, 0);
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
-                umma::mma_lead(tmem + C::kS + t * kRows, a + ks, b + ks, id_s, s > 0, lead);
-            }
-            if (lead) umma::commit(bar_s + 8 * t);
-        };
-        auto values = [&](int t, int j) {
-            if (!ok) return;
-            const uint32_t vb = base + C::kRing + ((2 * j + 1) % C::kSlots) * C::kTile;
-            const uint64_t b = umma::mnmajor(vb, kRows * 128, 0);
+                        for (int s = 0; s < D / 16; ++s) {
+                            const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
+                            umma::mma_lead(tmem + C::kS + t * kRows, a + ks, b + ks, id_s, s > 0, lead);
+                        }
+                    }
+                    done(bar_s + 8 * t);
+                    if (j + 1 == (t ? sp.n1 : sp.n0)) done(bar_qe + 8 * t);
+                };
+                auto values = [&](int t, int j, uint64_t b) {
+                    if (!ok) return;
 #pragma unroll
-            for (int s = 0; s < kRows / 16; ++s)
-                umma::mma_ts_lead(tmem + C::kO + t * D, tmem + C::kS + t * kRows + 8 * s, b + (uint64_t)(s * 128),
-                                  id_o, j > 0 || s > 0, lead);
-        };
-        auto done = [&](uint32_t bar) {
-            if (ok && lead) umma::commit(bar);
-        };
-        if (n > 0) full(0);
-        for (int t = 0; t < 2; ++t) {
-            if ((t ? n1 : n0) == 0) continue;
-            ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar_q + 8 * t, 0, err));
-            umma::fence_after_sync();
-            scores(t, 0);
-        }
-        if (n > 0) done(bar_empty);
-        for (int j = 0; j < n; ++j) {
-            const bool more = j + 1 < n;
-            full(2 * j + 1);
-            if (more) full(2 * j + 2);
-            else ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar_fix, 0, err));
-            for (int t = 0; t < 2; ++t) {
-                const int nt = t ? n1 : n0;
-                if (j >= nt) continue;
-                named_sync(kBarP + t, 160);
-                umma::fence_after_sync();
-                values(t, j);
-                if (j + 1 < nt) scores(t, j + 1);
-                else done(bar_o + 8 * t);
+                    for (int s = 0; s < kRows / 16; ++s)
+                        umma::mma_ts_lead(tmem + C::kO + t * D, tmem + C::kS + t * kRows + 8 * s,
+                                          b + (uint64_t)(s * 128), id_o, j > 0 || s > 0, lead);
+                };
+                wait(bar_full + 8 * slot_of(use), par_of(use));
+                for (int t = 0; t < 2; ++t) {
+                    if ((t ? sp.n1 : sp.n0) == 0) continue;
+                    wait(bar_q + 8 * t, count[t] & 1);
+                    umma::fence_after_sync();
+                    scores(t, 0, k_tile(0));
+                }
+                done(bar_empty + 8 * slot_of(use));
+                for (int j = 0; j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    wait(bar_full + 8 * slot_of(use + 2 * j + 1), par_of(use + 2 * j + 1));
+                    if (more) wait(bar_full + 8 * slot_of(use + 2 * j + 2), par_of(use + 2 * j + 2));
+                    else wait(bar_fix + 8 * (n_fix & 3), (n_fix >> 2) & 1);
+                    const uint64_t vt = v_tile(j), kt = k_tile(j + 1);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int nt = t ? sp.n1 : sp.n0;
+                        if (j >= nt) continue;
+                        named_sync(kBarP + t, 160);
+                        if (j == 0 && count[t] > 0) wait(bar_oe + 8 * t, (count[t] - 1) & 1);  // O has been read
+                        umma::fence_after_sync();
+                        values(t, j, vt);
+                        if (j + 1 < nt) scores(t, j + 1, kt);
+                        else done(bar_o + 8 * t);
+                    }
+                    done(bar_empty + 8 * slot_of(use + 2 * j + 1));
+                    if (more) done(bar_empty + 8 * slot_of(use + 2 * j + 2));
+                }
+                use += 2 * n;
+                count[0] += sp.n0 > 0;
+                count[1] += sp.n1 > 0;
+                ++n_fix;
             }
-            done(bar_empty + 8 * ((2 * j + 1) % C::kSlots));
-            if (more) done(bar_empty + 8 * ((2 * j + 2) % C::kSlots));
+        } else if (warp == 10) {
+            // ---- "scores ready" passed on to the softmax warps, in the order the products are issued
+            int seen[2] = {0, 0};
+            for (int i = 0;; ++i) {
+                const Item it = next_item(items, i, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                const Span sp = span(it);
+                for (int j = 0; j < sp.n; ++j)
+                    for (int t = 0; t < 2; ++t) {
+                        if (j >= (t ? sp.n1 : sp.n0)) continue;
+                        ok = ok && wait_or_flag(bar_s + 8 * t, seen[t] & 1, err);
+                        ++seen[t];
+                        umma::fence_after_sync();
+                        umma::fence_before_sync();
+                        named_arrive(kBarS + t, 160);
+                    }
+            }
+        } else {
+            schedule_items(A, cu_q, cu_k, 2 * qb, n_hg, false, items, bar_it, bar_ie, bar_ask, bar_want, err,
+                           [&](int hg) { return hg << lpack; });
         }
-    } else {
-        // ---- warps 10, 11: pass "scores ready" of tile 0, 1 on to its softmax warps
-        const int t = warp - 10, nt = t ? n1 : n0;
-        bool ok = true;
-        for (int j = 0; j < nt; ++j) {
-            ok = ok && wait_or_flag(bar_s + 8 * t, j & 1, err);
-            umma::fence_after_sync();
-            umma::fence_before_sync();
-            named_arrive(kBarS + t, 160);
-        }
-    }
     } else {
         take_registers();
         // ---- softmax, one row per thread
-        const int t = warp >> 2, row = tid & 127, pos = B.first + t * qb + (row >> lpack), h = h0 + (row & (pack - 1));
-        const int nt = t ? n1 : n0;
-        const bool on = pos < B.lq;
-        const int limit = on ? min(B.lk, pos + off + 1) : 0;  // keys the row sees: [0, limit)
+        const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) << 5) << 16;
         const uint32_t ts = tmem + lanes + C::kS + t * kRows, to = tmem + lanes + C::kO + t * D;
         const float cs = A.scale * kLog2e;
-        float m = -INFINITY;
-        float2 l = make_float2(0.f, 0.f);
-        for (int j = 0; j < nt; ++j) {
-            named_sync(kBarS + t, 160);
-            umma::fence_after_sync();
-            float x[128];
-            {
-                uint32_t r[4][32];
+        int count = 0;  // items with this tile
+        bool ok = true;
+        for (int i = 0;; ++i) {
+            const Item it = next_item(items, i, bar_it, bar_ie, err);
+            if (it.head < 0) break;
+            const Span sp = span(it);
+            const int pos = it.first + t * qb + (row >> lpack), h = it.head + (row & (pack - 1));
+            const int nt = t ? sp.n1 : sp.n0;
+            const bool on = pos < it.lq;
+            const int limit = on ? min(it.lk, pos + it.lk - it.lq + 1) : 0;  // keys the row sees: [0, limit)
+            float m = -INFINITY;
+            float2 l = make_float2(0.f, 0.f);
+            for (int j = 0; j < nt; ++j) {
+                named_sync(kBarS + t, 160);
+                umma::fence_after_sync();
+                float x[128];
+                {
+                    uint32_t r[4][32];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) umma::tmem_ld32_async(ts + 32 * b, r[b]);
-                umma::tmem_wait_ld();
+                    for (int b = 0; b < 4; ++b) umma::tmem_ld32_async(ts + 32 * b, r[b]);
+                    umma::tmem_wait_ld();
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    umma::reg_fence32(r[b]);
+                    for (int b = 0; b < 4; ++b) {
+                        umma::reg_fence32(r[b]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[32 * b + i] = __uint_as_float(r[b][i]);
-                }
-            }
-            const int seen = limit - j * kRows;
-            if (__any_sync(0xffffffffu, seen < kRows)) {
-#pragma unroll
-                for (int i = 0; i < 128; ++i) x[i] = i < seen ? x[i] : -INFINITY;
-            }
-            float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int i = 4; i < 128; i += 8)
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (i + b + 4 < 128) top[b] = fmaxf(top[b], fmaxf(x[i + b], x[i + b + 4]));
-                    else top[b] = fmaxf(top[b], x[i + b]);
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cs;
-            const bool grow = mx > m + kLazy;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
-                if (grow) m = mx;
-                l.x *= corr;
-                l.y *= corr;
-                if (j > 0) {
-#pragma unroll
-                    for (int b = 0; b < D / 32; ++b) {
-                        float o[32];
-                        umma::tmem_ld32(to + 32 * b, o);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= corr;
-                        umma::tmem_st32(to + 32 * b, o);
+                        for (int e = 0; e < 32; ++e) x[32 * b + e] = __uint_as_float(r[b][e]);
                     }
                 }
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
-            const float2 c2 = make_float2(cs, cs), m2 = make_float2(-ref, -ref);
+                const int seen = limit - j * kRows;
+                if (__any_sync(0xffffffffu, seen < kRows)) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float2 y = ffma2(make_float2(x[64 * b + 2 * i], x[64 * b + 2 * i + 1]), c2, m2);
-                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                    l = fadd2(l, e);
-                    p[i] = pack_bf2(e.x, e.y);
+                    for (int e = 0; e < 128; ++e) x[e] = e < seen ? x[e] : -INFINITY;
                 }
-                umma::tmem_st32_async(ts + 32 * b, p);
+                float top[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) top[b] = fmaxf(x[b], x[b + 4]);
+#pragma unroll
+                for (int e = 8; e < 128; e += 8)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) top[b] = fmaxf(top[b], fmaxf(x[e + b], x[e + b + 4]));
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cs;
+                const bool grow = mx > m + kLazy;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
+                    if (grow) m = mx;
+                    l.x *= corr;
+                    l.y *= corr;
+                    if (j > 0) {
+#pragma unroll
+                        for (int b = 0; b < D / 32; ++b) {
+                            float o[32];
+                            umma::tmem_ld32(to + 32 * b, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= corr;
+                            umma::tmem_st32(to + 32 * b, o);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                const float2 c2 = make_float2(cs, cs), m2 = make_float2(-ref, -ref);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 y = ffma2(make_float2(x[64 * b + 2 * e], x[64 * b + 2 * e + 1]), c2, m2);
+                        const float2 w = make_float2(ex2(y.x), ex2(y.y));
+                        l = fadd2(l, w);
+                        p[e] = pack_bf2(w.x, w.y);
+                    }
+                    umma::tmem_st32_async(ts + 32 * b, p);
+                }
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                named_arrive(kBarP + t, 160);
             }
-            umma::tmem_wait_st();
-            umma::fence_before_sync();
-            named_arrive(kBarP + t, 160);
-        }
-        // ---- the row's output
-        const float sum = l.x + l.y;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t at = (B.q0 + pos) * A.Hq + h;
-        if (on) lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
-        if (nt > 0) wait_or_flag(bar_o + 8 * t, 0, err);
-        umma::fence_after_sync();
+            // ---- the row's output
+            const float sum = l.x + l.y;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t at = ((int64_t)it.q0 + pos) * A.Hq + h;
+            if (on) lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+            if (nt > 0) ok = ok && wait_or_flag(bar_o + 8 * t, count & 1, err);
+            umma::fence_after_sync();
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) {
-            float o[32];
-            if (nt > 0) {
-                umma::tmem_ld32(to + 32 * b, o);
-            } else {
+            for (int b = 0; b < D / 32; ++b) {
+                float o[32];
+                if (nt > 0) {
+                    umma::tmem_ld32(to + 32 * b, o);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
-            if (on) {
-                __nv_bfloat16* dst = out + at * D + 32 * b;
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (b == D / 32 - 1 && nt > 0) {  // O may be overwritten
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(bar_oe + 8 * t);
+                    ++count;
+                }
+                if (on) {
+                    __nv_bfloat16* dst = out + at * D + 32 * b;
 #pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                    *reinterpret_cast<uint4*>(dst + i) =
-                        make_uint4(pack_bf2(o[i] * inv, o[i + 1] * inv), pack_bf2(o[i + 2] * inv, o[i + 3] * inv),
-                                   pack_bf2(o[i + 4] * inv, o[i + 5] * inv), pack_bf2(o[i + 6] * inv, o[i + 7] * inv));
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(dst + e) = make_uint4(
+                            pack_bf2(o[e] * inv, o[e + 1] * inv), pack_bf2(o[e + 2] * inv, o[e + 3] * inv),
+                            pack_bf2(o[e + 4] * inv, o[e + 5] * inv), pack_bf2(o[e + 6] * inv, o[e + 7] * inv));
+                }
             }
         }
     }
@@ -327,7 +398,6 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
                                   kRows))
         return cudaErrorInvalidValue;
     const int64_t blocks = (A.total_q / (2 * qb) + A.n_seqs) * (A.Hq / pack);
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     attention_tc_kernel<D><<<(unsigned)blocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mk, mv, cu_q, cu_k, lpack, out,
                                                                              lse, err);
     return cudaGetLastError();

@@ -18,7 +18,7 @@ namespace hla {
 namespace attn_tc {
 
 constexpr int kRows = 128;  // rows of a query tile, keys of a key tile
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kWaitLimit = 1u << 22, kItemSeconds = 60;  // polls per second allowed
 
 // Registers of a block of three warpgroups: 168 a thread at launch; the third
 // (loads and products) gives 96 a thread up, the softmax warpgroups take 48
@@ -65,13 +65,14 @@ __device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
 
 // Waits with a bound (polls, and two seconds); a wait that runs out is recorded and ends the caller's role.
 // Inlined: a function call would not leave its caller the registers of setmaxnreg.
-__device__ __forceinline__ bool wait_or_flag(uint32_t mbar, uint32_t parity, int32_t* err) {
+// The waits for the next item, which last as long as the items before it, get a minute.
+__device__ __forceinline__ bool wait_or_flag(uint32_t mbar, uint32_t parity, int32_t* err, uint32_t seconds = 2) {
     if (umma::mbar_try_wait(mbar, parity)) return true;
     const uint64_t t0 = umma::global_ns();
 #pragma unroll 1
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    for (uint32_t i = 0; i < kWaitLimit * seconds; ++i) {
         if (umma::mbar_try_wait(mbar, parity)) return true;
-        if (umma::global_ns() - t0 > 2000000000ull) break;
+        if (umma::global_ns() - t0 > 1000000000ull * seconds) break;
     }
     atomicExch(err, kErrTimeout);
     return false;
@@ -87,6 +88,99 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 }
 __device__ __forceinline__ void named_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ---- persistent blocks ------------------------------------------------------
+//
+// The grid has a block per item (a tile or two of one head group), longest
+// first; a block that runs takes over items of blocks that have not started
+// (cluster launch control), so one block per SM does them all and the next
+// free SM always takes the longest that is left.  A warp of its own asks for
+// the next item, finds what it is, and hands it to the others through a short
+// ring, so that every role runs ahead into the next item on its own: its loads
+// start while the last products and results of this one are under way.
+// The next item is asked for when the loads of this one come to an end, not
+// before: items claimed early would be kept from blocks that are free sooner.
+
+struct Item {
+    int q0, k0;  // first query and key row of the sequence
+    int lq, lk;  // its lengths
+    int first;   // first position of the tile(s)
+    int head;    // first query head, or the kv head; -1: no more items
+};
+constexpr int kItems = 2;       // entries of the ring
+constexpr int kItemWarps = 11;  // warps that read them
+struct ItemRing {
+    int4 word[kItems][2];
+    uint4 answer;  // of a request for the next item
+};
+
+// Asks for an item of a block that has not started; the answer arrives on mbar.  (One lane.)
+__device__ __forceinline__ void ask_item(uint32_t answer, uint32_t mbar) {
+    tma::expect_tx(mbar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     answer),
+                 "r"(mbar)
+                 : "memory");
+}
+// The block whose item was taken over; -1: there is none left.
+__device__ __forceinline__ int64_t taken_item(uint32_t answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n .reg .b128 a;\n .reg .pred p;\n ld.shared.b128 a, [%2];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n}\n"
+        : "=r"(got), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return got ? (int64_t)x : -1;
+}
+
+// The scheduling warp: `heads` head groups, `rows` positions per item.
+template <class HeadOf>
+__device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t* cu_q, const int32_t* cu_k, int rows,
+                                               int heads, bool by_key, ItemRing* ring, uint32_t bar_full,
+                                               uint32_t bar_empty, uint32_t bar_ask, uint32_t bar_want, int32_t* err,
+                                               HeadOf head_of) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t answer = umma::smem_addr(&ring->answer);
+    int64_t x = blockIdx.x;
+    bool more = true;
+    for (int i = 0; more; ++i) {
+        AttnBlock B = {};
+        if (x >= 0) B = attn_find_block(A, cu_q, cu_k, rows, x / heads, by_key);
+        const int s = i % kItems;
+        more = B.found;
+        if (i >= kItems && !wait_or_flag(bar_empty + 8 * s, ((i / kItems) - 1) & 1, err, kItemSeconds)) more = false;
+        if (lane == 0) {
+            ring->word[s][0] = make_int4((int)B.q0, (int)B.k0, B.lq, B.lk);
+            ring->word[s][1] = make_int4(B.first, more ? head_of((int)(x % heads)) : -1, 0, 0);
+        }
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(bar_full + 8 * s);
+        if (!more) break;
+        x = -1;
+        if (wait_or_flag(bar_want, i & 1, err, kItemSeconds)) {
+            if (lane == 0) ask_item(answer, bar_ask);
+            if (wait_or_flag(bar_ask, i & 1, err)) x = taken_item(answer);
+            __syncwarp();
+            umma::fence_async_smem();
+        }
+    }
+}
+
+// The i-th item of this block (a full warp; each reader in order).
+__device__ __forceinline__ Item next_item(const ItemRing* ring, int i, uint32_t bar_full, uint32_t bar_empty,
+                                          int32_t* err) {
+    const int s = i % kItems;
+    Item it = {0, 0, 0, 0, 0, -1};
+    if (wait_or_flag(bar_full + 8 * s, (i / kItems) & 1, err, kItemSeconds)) {
+        const int4 a = ring->word[s][0], b = ring->word[s][1];
+        it = Item{a.x, a.y, a.z, a.w, b.x, b.y};
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) umma::mbar_arrive(bar_empty + 8 * s);
+    return it;
 }
 
 // Rows [first, 128) of a 128 x D 16-bit tile (128-byte-swizzled 64-column blocks) set to zero by one warp.
