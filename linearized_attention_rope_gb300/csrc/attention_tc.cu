@@ -172,65 +172,78 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             auto done = [&](uint32_t bar) {
                 if (ok && lead) umma::commit(bar);
             };
-            int use = 0, count[2] = {0, 0}, n_fix = 0;  // ring uses, items with tile t, items
+            // the ring: slot and parity of the next use, in order K 0, V 0, K 1, V 1, ... of every item
+            uint32_t slot = 0, par = 0;
+            struct Use { uint32_t slot, par; };
+            auto next_use = [&]() {
+                const Use u = {slot, par};
+                if (++slot == C::kSlots) {
+                    slot = 0;
+                    par ^= 1u;
+                }
+                return u;
+            };
+            const uint64_t q_tile[2] = {umma::kmajor(base + C::kQ, kRows, 0), umma::kmajor(base + C::kQ + C::kTile, kRows, 0)};
+            const uint64_t k_ring = umma::kmajor(base + C::kRing, kRows, 0);
+            const uint64_t v_ring = umma::mnmajor(base + C::kRing, kRows * 128, 0);
+            auto scores = [&](int t, uint32_t k_slot) {
+                if (!ok) return;
+                const uint64_t a = q_tile[t], b = k_ring + (uint64_t)(k_slot * (C::kTile / 16));
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
+                    umma::mma_lead(tmem + C::kS + t * kRows, a + ks, b + ks, id_s, s > 0, lead);
+                }
+                if (lead) umma::commit(bar_s + 8 * t);
+            };
+            auto values = [&](int t, uint32_t v_slot, bool add) {
+                if (!ok) return;
+                const uint64_t b = v_ring + (uint64_t)(v_slot * (C::kTile / 16));
+#pragma unroll
+                for (int s = 0; s < kRows / 16; ++s)
+                    umma::mma_ts_lead(tmem + C::kO + t * D, tmem + C::kS + t * kRows + 8 * s, b + (uint64_t)(s * 128),
+                                      id_o, add || s > 0, lead);
+            };
+            int count[2] = {0, 0}, n_fix = 0;  // items with tile t, items
             for (int i = 0;; ++i) {
                 const Item it = next_item(items, i, bar_it, bar_ie, err);
                 if (__shfl_sync(0xffffffffu, it.head, 0) < 0) break;
                 const Span sp = span(it);
                 const int n = sp.n;
                 if (n == 0) continue;
-                auto k_tile = [&](int j) { return umma::kmajor(base + C::kRing + slot_of(use + 2 * j) * C::kTile, kRows, 0); };
-                auto v_tile = [&](int j) {
-                    return umma::mnmajor(base + C::kRing + slot_of(use + 2 * j + 1) * C::kTile, kRows * 128, 0);
-                };
-                auto scores = [&](int t, int j, uint64_t b) {
-                    if (ok) {
-                        const uint64_t a = umma::kmajor(base + C::kQ + t * C::kTile, kRows, 0);
+                const Use first = next_use();
+                wait(bar_full + 8 * first.slot, first.par);
 #pragma unroll
-                        for (int s = 0; s < D / 16; ++s) {
-                            const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
-                            umma::mma_lead(tmem + C::kS + t * kRows, a + ks, b + ks, id_s, s > 0, lead);
-                        }
-                    }
-                    done(bar_s + 8 * t);
-                    if (j + 1 == (t ? sp.n1 : sp.n0)) done(bar_qe + 8 * t);
-                };
-                auto values = [&](int t, int j, uint64_t b) {
-                    if (!ok) return;
-#pragma unroll
-                    for (int s = 0; s < kRows / 16; ++s)
-                        umma::mma_ts_lead(tmem + C::kO + t * D, tmem + C::kS + t * kRows + 8 * s,
-                                          b + (uint64_t)(s * 128), id_o, j > 0 || s > 0, lead);
-                };
-                wait(bar_full + 8 * slot_of(use), par_of(use));
                 for (int t = 0; t < 2; ++t) {
-                    if ((t ? sp.n1 : sp.n0) == 0) continue;
+                    const int nt = t ? sp.n1 : sp.n0;
+                    if (nt == 0) continue;
                     wait(bar_q + 8 * t, count[t] & 1);
                     umma::fence_after_sync();
-                    scores(t, 0, k_tile(0));
+                    scores(t, first.slot);
+                    if (nt == 1) done(bar_qe + 8 * t);
                 }
-                done(bar_empty + 8 * slot_of(use));
+                done(bar_empty + 8 * first.slot);
                 for (int j = 0; j < n; ++j) {
                     const bool more = j + 1 < n;
-                    wait(bar_full + 8 * slot_of(use + 2 * j + 1), par_of(use + 2 * j + 1));
-                    if (more) wait(bar_full + 8 * slot_of(use + 2 * j + 2), par_of(use + 2 * j + 2));
+                    const Use v = next_use(), k = more ? next_use() : v;
+                    wait(bar_full + 8 * v.slot, v.par);
+                    if (more) wait(bar_full + 8 * k.slot, k.par);
                     else wait(bar_fix + 8 * (n_fix & 3), (n_fix >> 2) & 1);
-                    const uint64_t vt = v_tile(j), kt = k_tile(j + 1);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const int nt = t ? sp.n1 : sp.n0;
                         if (j >= nt) continue;
-                        named_sync(kBarP + t, 160);
                         if (j == 0 && count[t] > 0) wait(bar_oe + 8 * t, (count[t] - 1) & 1);  // O has been read
+                        named_sync(kBarP + t, 160);
                         umma::fence_after_sync();
-                        values(t, j, vt);
-                        if (j + 1 < nt) scores(t, j + 1, kt);
+                        values(t, v.slot, j > 0);
+                        if (j + 1 < nt) scores(t, k.slot);
                         else done(bar_o + 8 * t);
+                        if (j + 2 == nt) done(bar_qe + 8 * t);  // Q has been read for the last time
                     }
-                    done(bar_empty + 8 * slot_of(use + 2 * j + 1));
-                    if (more) done(bar_empty + 8 * slot_of(use + 2 * j + 2));
+                    done(bar_empty + 8 * v.slot);
+                    if (more) done(bar_empty + 8 * k.slot);
                 }
-                use += 2 * n;
                 count[0] += sp.n0 > 0;
                 count[1] += sp.n1 > 0;
                 ++n_fix;
@@ -266,13 +279,17 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         int count = 0;  // items with this tile
         bool ok = true;
         for (int i = 0;; ++i) {
-            const Item it = next_item(items, i, bar_it, bar_ie, err);
-            if (it.head < 0) break;
-            const Span sp = span(it);
-            const int pos = it.first + t * qb + (row >> lpack), h = it.head + (row & (pack - 1));
-            const int nt = t ? sp.n1 : sp.n0;
-            const bool on = pos < it.lq;
-            const int limit = on ? min(it.lk, pos + it.lk - it.lq + 1) : 0;  // keys the row sees: [0, limit)
+            int nt, limit;  // key tiles of the query tile; keys the row sees: [0, limit)
+            int64_t at;     // the row's place in the output (-1: none)
+            {
+                const Item it = next_item(items, i, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                const Span sp = span(it);
+                const int pos = it.first + t * qb + (row >> lpack);
+                nt = t ? sp.n1 : sp.n0;
+                limit = pos < it.lq ? min(it.lk, pos + it.lk - it.lq + 1) : 0;
+                at = pos < it.lq ? ((int64_t)it.q0 + pos) * A.Hq + it.head + (row & (pack - 1)) : -1;
+            }
             float m = -INFINITY;
             float2 l = make_float2(0.f, 0.f);
             for (int j = 0; j < nt; ++j) {
@@ -342,8 +359,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             // ---- the row's output
             const float sum = l.x + l.y;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int64_t at = ((int64_t)it.q0 + pos) * A.Hq + h;
-            if (on) lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+            if (at >= 0) lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
             if (nt > 0) ok = ok && wait_or_flag(bar_o + 8 * t, count & 1, err);
             umma::fence_after_sync();
 #pragma unroll
@@ -361,7 +377,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     if (lane == 0) umma::mbar_arrive(bar_oe + 8 * t);
                     ++count;
                 }
-                if (on) {
+                if (at >= 0) {
                     __nv_bfloat16* dst = out + at * D + 32 * b;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
