@@ -77,7 +77,7 @@ template <int D> struct Cfg {
     static constexpr int kSlots = D == 128 ? 5 : 8;
     // two fixed tiles (K, V or Q, dO), the ring, two stages of row stats (-lse, then -D; 128 fp32 each), barriers
     static constexpr uint32_t kFix = 0, kRing = 2 * kTile, kStat = kRing + kSlots * kTile, kBar = kStat + 2048;
-    static constexpr uint32_t kSmem = kBar + 256;
+    static constexpr uint32_t kItem = kBar + 320, kSmem = kItem + sizeof(ItemRing);
     static constexpr uint32_t kCols = 512;
 };
 
@@ -101,6 +101,24 @@ __device__ __forceinline__ void load64(uint32_t taddr, float2 (&x)[32]) {
     }
 }
 
+// Products of 128 x 128 x d and 128 x d x 128 elements, issued by the lane with `lead`.
+template <int D>
+__device__ __forceinline__ void outer_product(uint32_t d, uint64_t a, uint64_t b, uint32_t lead) {  // d = a b^T over d
+    const uint32_t idesc = umma::idesc_bf16(kRows, kRows, false, false);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+        const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
+        umma::mma_lead(d, a + ks, b + ks, idesc, s > 0, lead);
+    }
+}
+template <int D>
+__device__ __forceinline__ void inner_product(uint32_t d, uint32_t a_cols, uint64_t b, bool add, uint32_t lead) {
+    const uint32_t idesc = umma::idesc_bf16(kRows, D, false, true);  // d += a b over the 128 rows of b
+#pragma unroll
+    for (int s = 0; s < kRows / 16; ++s)
+        umma::mma_ts_lead(d, half_step(a_cols, s), b + (uint64_t)(s * 128), idesc, add || s > 0, lead);
+}
+
 // ---- dk, dv -----------------------------------------------------------------
 
 template <int D>
@@ -111,27 +129,24 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     const int32_t* __restrict__ cu_k, int lpack, const float2* __restrict__ stats,
                     __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, int32_t* __restrict__ err) {
     using C = Cfg<D>;
+    using Ring = RingPos<C::kSlots>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int qb = kRows >> lpack;
+    const int lqb = 7 - lpack, qb = 1 << lqb, groups = A.G >> lpack;  // positions of a query tile; packed head groups
     if (blockIdx.x == 0) {
         attn_check_table(cu_q, A.n_seqs, A.total_q, err);
         attn_check_table(cu_k, A.n_seqs, A.total_k, err);
     }
-    const AttnBlock B = attn_find_block(A, cu_q, cu_k, kRows, blockIdx.x / A.Hkv, true);
-    if (!B.found) return;  // the whole block
-    const int kv = blockIdx.x % A.Hkv, off = B.lk - B.lq;
-    // query tiles: of each packed head group, those from the first that sees the block's first key
-    const int i0 = max(0, B.first - off) / qb, per = max(0, (B.lq + qb - 1) / qb - i0);
-    const int n = __shfl_sync(0xffffffffu, per * (A.G >> lpack), 0);
-    const int tail = B.lq % qb ? (B.lq % qb) << lpack : kRows;  // rows of a group's last tile
-
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
-    const uint32_t bar_kv = bars, bar_full = bars + 8, bar_empty = bar_full + 8 * C::kSlots;
+    const uint32_t bar_kv = bars, bar_kve = bar_kv + 8, bar_full = bar_kve + 8, bar_empty = bar_full + 8 * C::kSlots;
     const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_dp = bar_s + 8, bar_fix = bar_dp + 8, bar_done = bar_fix + 32;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 248);
+    const uint32_t bar_oe = bar_done + 8, bar_it = bar_oe + 8, bar_ie = bar_it + 8 * kItems, bar_ask = bar_ie + 8 * kItems;
+    const uint32_t bar_want = bar_ask + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 316);
+    ItemRing* items = reinterpret_cast<ItemRing*>(sm + C::kItem);
     if (tid == 0) {
         umma::mbar_init(bar_kv, 1);
+        umma::mbar_init(bar_kve, 1);
         for (int i = 0; i < C::kSlots; ++i) {
             umma::mbar_init(bar_full + 8 * i, 1);
             umma::mbar_init(bar_empty + 8 * i, 1);
@@ -140,6 +155,13 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         umma::mbar_init(bar_dp, 1);
         for (int i = 0; i < 4; ++i) umma::mbar_init(bar_fix + 8 * i, 1);
         umma::mbar_init(bar_done, 1);
+        umma::mbar_init(bar_oe, 8);
+        for (int i = 0; i < kItems; ++i) {
+            umma::mbar_init(bar_it + 8 * i, 1);
+            umma::mbar_init(bar_ie + 8 * i, kItemWarps);
+        }
+        umma::mbar_init(bar_ask, 1);
+        umma::mbar_init(bar_want, 1);
         umma::fence_mbar_init();
     }
     if (warp == 9) umma::tmem_alloc(tmem_slot, C::kCols);
@@ -148,228 +170,300 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     umma::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t cS = tmem, cP = tmem + 128, cV = tmem + 256, cK = cV + D;  // S / P, dP / dS, dV, dK
-    auto slot_of = [&](int use) { return use % C::kSlots; };
-    auto par_of = [&](int use) { return (uint32_t)(use / C::kSlots) & 1u; };
-    const int h0 = kv * A.G;
-    auto first_row = [&](int i) { return (i0 + i % per) * qb; };
-    auto has_tail = [&](int i) { return tail < kRows && i % per == per - 1; };
+
+    // an item's query tiles: of each packed head group, `per` tiles from tile i0, the first that sees the block's
+    // first key; the last has `tail` rows
+    struct Span { int i0, per, n, tail; };
+    auto span = [&](const Item& it) {
+        const int off = it.lk - it.lq, i0 = max(0, it.first - off) >> lqb;
+        const int per = __shfl_sync(0xffffffffu, max(0, ((it.lq + qb - 1) >> lqb) - i0), 0);
+        const int rest = it.lq & (qb - 1);
+        return Span{i0, per, per * groups, __shfl_sync(0xffffffffu, rest ? rest << lpack : kRows, 0)};
+    };
 
     if (warp >= 8) {
         give_registers();
         bool ok = true;
-        if (warp == 8 && n > 0) {
-            // ---- loads: use 2 i of the ring is tile i of Q, use 2 i + 1 of dO.  Rows behind the sequence are
-            //      cleared, whatever they hold (the ring holds at most four tiles, so four barriers keep a tile's
-            //      signal until the products have seen it)
+        if (warp == 8) {
+            // ---- loads: the ring takes Q 0, dO 0, Q 1, dO 1, ... of every item.  Rows behind the sequence are cleared,
+            //      whatever they hold (the ring holds at most four tiles, so four barriers keep a tile's signal until
+            //      the products have seen it)
             static_assert(C::kSlots <= 8, "tiles in the ring");
-            if (lane == 0) {
-                tma::expect_tx(bar_kv, 2 * C::kTile);
-                for (int b = 0; b < D / 64; ++b) {
-                    tma::tensor_load_3d(base + C::kFix + b * (kRows * 128), &map_k, 64 * b, kv, (int)(B.k0 + B.first),
-                                        bar_kv);
-                    tma::tensor_load_3d(base + C::kFix + C::kTile + b * (kRows * 128), &map_v, 64 * b, kv,
-                                        (int)(B.k0 + B.first), bar_kv);
-                }
-            }
-            int u = 0, fixed = 0;
-            for (; u < 2 * n; ++u) {
-                const int i = u >> 1, slot = slot_of(u);
-                if (u >= C::kSlots && !(ok = wait_or_flag(bar_empty + 8 * slot, par_of(u - C::kSlots), err))) break;
-                if (lane == 0) {
-                    tma::expect_tx(bar_full + 8 * slot, C::kTile);
-                    for (int b = 0; b < D / 64; ++b)
-                        tma::tensor_load_3d(base + C::kRing + slot * C::kTile + b * (kRows * 128),
-                                            u & 1 ? &map_do : &map_q, 64 * b, h0 + ((i / per) << lpack),
-                                            (int)B.q0 + first_row(i), bar_full + 8 * slot);
-                }
-                if ((u & 1) && has_tail(i)) {
-                    for (int y = u - 1; y <= u && ok; ++y) {
-                        ok = wait_or_flag(bar_full + 8 * slot_of(y), par_of(y), err);
-                        if (ok) zero_rows<D>(sm + C::kRing + slot_of(y) * C::kTile, tail);
+            Ring ring;
+            int used = 0, fixed = 0, kv_loads = 0;
+            for (int x = 0;; ++x) {
+                const Item it = next_item(items, x, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                const Span sp = span(it);
+                const int ask_at = max(0, sp.n - 2);
+                if (sp.n == 0 && lane == 0) umma::mbar_arrive(bar_want);
+                int r = 0, h = it.head * A.G;
+                for (int i = 0; i < sp.n; ++i) {
+                    if (i == ask_at && lane == 0) umma::mbar_arrive(bar_want);  // time to look for the next item
+                    const int row = it.q0 + ((sp.i0 + r) << lqb);
+                    Ring use[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        use[y] = ring.next();
+                        if (used++ >= C::kSlots) ok = ok && wait_or_flag(bar_empty + 8 * use[y].slot, use[y].par ^ 1u, err);
+                        if (ok && lane == 0) {
+                            tma::expect_tx(bar_full + 8 * use[y].slot, C::kTile);
+                            for (int b = 0; b < D / 64; ++b)
+                                tma::tensor_load_3d(base + C::kRing + use[y].slot * C::kTile + b * (kRows * 128),
+                                                    y ? &map_do : &map_q, 64 * b, h, row, bar_full + 8 * use[y].slot);
+                        }
+                        if (i == 0 && y == 0) {  // the key block, once the last item's scores and dP are formed
+                            if (kv_loads++ > 0) ok = ok && wait_or_flag(bar_kve, kv_loads & 1, err);
+                            if (ok && lane == 0) {
+                                tma::expect_tx(bar_kv, 2 * C::kTile);
+                                for (int b = 0; b < D / 64; ++b) {
+                                    tma::tensor_load_3d(base + C::kFix + b * (kRows * 128), &map_k, 64 * b, it.head,
+                                                        it.k0 + it.first, bar_kv);
+                                    tma::tensor_load_3d(base + C::kFix + C::kTile + b * (kRows * 128), &map_v, 64 * b,
+                                                        it.head, it.k0 + it.first, bar_kv);
+                                }
+                            }
+                        }
                     }
-                    if (!ok) { ++u; break; }
-                    umma::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) umma::mbar_arrive(bar_fix + 8 * (fixed & 3));
-                    ++fixed;
+                    if (++r == sp.per) {
+                        r = 0;
+                        h += 1 << lpack;
+                        if (sp.tail < kRows) {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                ok = ok && wait_or_flag(bar_full + 8 * use[y].slot, use[y].par, err);
+                                if (ok) zero_rows<D>(sm + C::kRing + use[y].slot * C::kTile, sp.tail);
+                            }
+                            umma::fence_async_smem();
+                            __syncwarp();
+                            if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (fixed & 3));
+                            ++fixed;
+                        }
+                    }
                 }
             }
-            if (!ok) {  // copies in flight land before the block ends
-                wait_or_flag(bar_kv, 0, err);
-                for (int i = max(0, u - C::kSlots); i < u; ++i) wait_or_flag(bar_full + 8 * slot_of(i), par_of(i), err);
-            }
-        } else if (warp == 9 && n > 0) {
+        } else if (warp == 9) {
             // ---- products: one lane issues, the warp stays together
             const uint32_t lead = umma::elect_one();
-            const uint32_t id_s = umma::idesc_bf16(kRows, kRows, false, false);
-            const uint32_t id_d = umma::idesc_bf16(kRows, D, false, true);
-            int fixed = 0;
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar, parity, err));
-            };
-            auto ring = [&](int u) { return base + C::kRing + slot_of(u) * C::kTile; };
-            auto ready = [&](int i) {  // Q and dO of tile i, cleared behind the last row
-                wait(bar_full + 8 * slot_of(2 * i), par_of(2 * i));
-                wait(bar_full + 8 * slot_of(2 * i + 1), par_of(2 * i + 1));
-                if (has_tail(i)) {
-                    wait(bar_fix + 8 * (fixed & 3), (fixed >> 2) & 1);
-                    ++fixed;
-                }
-                umma::fence_after_sync();
-            };
-            auto outer = [&](uint32_t d, uint32_t a_tile, uint32_t b_tile) {  // d = a b^T over d
-                if (!ok) return;
-                const uint64_t a = umma::kmajor(a_tile, kRows, 0), b = umma::kmajor(b_tile, kRows, 0);
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
-                    umma::mma_lead(d, a + ks, b + ks, id_s, s > 0, lead);
-                }
-            };
-            auto inner = [&](uint32_t d, uint32_t a_cols, uint32_t b_tile, bool add) {  // d += a b over the rows
-                if (!ok) return;
-                const uint64_t b = umma::mnmajor(b_tile, kRows * 128, 0);
-#pragma unroll
-                for (int s = 0; s < kRows / 16; ++s)
-                    umma::mma_ts_lead(d, half_step(a_cols, s), b + (uint64_t)(s * 128), id_d, add || s > 0, lead);
             };
             auto done = [&](uint32_t bar) {
                 if (ok && lead) umma::commit(bar);
             };
-            wait(bar_kv, 0);
-            ready(0);
-            outer(cS, base + C::kFix, ring(0));
-            done(bar_s);
-            outer(cP, base + C::kFix + C::kTile, ring(1));
-            done(bar_dp);
-            for (int i = 0; i < n; ++i) {
-                const bool more = i + 1 < n;
-                named_sync(kBarP, 288);
-                umma::fence_after_sync();
-                inner(cV, cS, ring(2 * i + 1), i > 0);
-                done(bar_empty + 8 * slot_of(2 * i + 1));
-                if (more) {
-                    ready(i + 1);
-                    outer(cS, base + C::kFix, ring(2 * i + 2));
-                    done(bar_s);
+            const uint64_t k_tile = umma::kmajor(base + C::kFix, kRows, 0);
+            const uint64_t v_tile = umma::kmajor(base + C::kFix + C::kTile, kRows, 0);
+            const uint64_t ring_k = umma::kmajor(base + C::kRing, kRows, 0);
+            const uint64_t ring_mn = umma::mnmajor(base + C::kRing, kRows * 128, 0);
+            auto at = [&](uint64_t ring0, const Ring& u) { return ring0 + (uint64_t)(u.slot * (C::kTile / 16)); };
+            Ring ring;
+            int fixed = 0, count = 0;
+            for (int x = 0;; ++x) {
+                const Item it = next_item(items, x, bar_it, bar_ie, err);
+                if (__shfl_sync(0xffffffffu, it.head, 0) < 0) break;
+                const Span sp = span(it);
+                const int n = sp.n;
+                if (n == 0) continue;
+                int r = 0;
+                auto ready_q = [&](const Ring& q) {  // a tile's Q (a last tile's dO too: both cleared behind the last row)
+                    wait(bar_full + 8 * q.slot, q.par);
+                    if (++r == sp.per) {
+                        r = 0;
+                        if (sp.tail < kRows) {
+                            wait(bar_fix + 8 * (fixed & 3), (fixed >> 2) & 1);
+                            ++fixed;
+                        }
+                    }
+                    umma::fence_after_sync();
+                };
+                auto ready_o = [&](const Ring& o) {
+                    wait(bar_full + 8 * o.slot, o.par);
+                    umma::fence_after_sync();
+                };
+                Ring q = ring.next(), o = ring.next();
+                wait(bar_kv, count & 1);
+                ready_q(q);
+                if (ok) outer_product<D>(cS, k_tile, at(ring_k, q), lead);
+                done(bar_s);
+                ready_o(o);
+                if (ok) outer_product<D>(cP, v_tile, at(ring_k, o), lead);
+                done(bar_dp);
+                if (n == 1) done(bar_kve);
+                if (count > 0) wait(bar_oe, (count - 1) & 1);  // dV and dK have been read
+                for (int i = 0; i < n; ++i) {
+                    const bool more = i + 1 < n;
+                    const Ring q1 = more ? ring.next() : q, o1 = more ? ring.next() : o;
+                    named_sync(kBarP, 288);
+                    umma::fence_after_sync();
+                    if (ok) inner_product<D>(cV, cS, at(ring_mn, o), i > 0, lead);
+                    done(bar_empty + 8 * o.slot);
+                    if (more) {
+                        ready_q(q1);
+                        if (ok) outer_product<D>(cS, k_tile, at(ring_k, q1), lead);
+                        done(bar_s);
+                    }
+                    named_sync(kBarDs, 288);
+                    umma::fence_after_sync();
+                    if (ok) inner_product<D>(cK, cP, at(ring_mn, q), i > 0, lead);
+                    done(bar_empty + 8 * q.slot);
+                    if (more) {
+                        ready_o(o1);
+                        if (ok) outer_product<D>(cP, v_tile, at(ring_k, o1), lead);
+                        done(bar_dp);
+                        if (i + 2 == n) done(bar_kve);  // K and V have been read for the last time
+                    } else {
+                        done(bar_done);
+                    }
+                    q = q1;
+                    o = o1;
                 }
-                named_sync(kBarDs, 288);
-                umma::fence_after_sync();
-                inner(cK, cP, ring(2 * i), i > 0);
-                done(bar_empty + 8 * slot_of(2 * i));
-                if (more) {
-                    outer(cP, base + C::kFix + C::kTile, ring(2 * i + 3));
-                    done(bar_dp);
-                }
+                ++count;
             }
-            done(bar_done);
         } else if (warp == 10) {
             // ---- row stats of each tile (rows behind the sequence: probability 0) in two stages, and "scores ready",
-            //      "score gradients ready" passed on to the elementwise warps.  dP of tile i + 1 is formed after dS of
-            //      tile i is complete, so by then the stage of tile i has been read.
-            auto load = [&](int i, float2 (&x)[4]) {
-                const int r0 = first_row(i), hg = h0 + ((i / per) << lpack);
+            //      "score gradients ready" passed on to the elementwise warps.  dP of a tile is formed after dS of the
+            //      one before it is complete, so by then that one's stage has been read.
+            uint32_t t = 0;  // tiles so far
+            for (int x = 0;; ++x) {
+                const Item it = next_item(items, x, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                const Span sp = span(it);
+                int r = 0, h = it.head * A.G;
+                float2 v[4];
+                auto load = [&]() {
+                    const int r0 = (sp.i0 + r) << lqb;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int r = lane + 32 * y, p = r0 + (r >> lpack);
-                    x[y] = p < B.lq ? __ldg(stats + (B.q0 + p) * A.Hq + hg + (r & ((1 << lpack) - 1)))
-                                    : make_float2(-INFINITY, 0.f);
-                }
-            };
-            float2 x[4];
-            if (n > 0) load(0, x);
-            for (int i = 0; i < n; ++i) {
-                float* st = reinterpret_cast<float*>(sm + C::kStat + (i & 1) * 1024);
+                    for (int y = 0; y < 4; ++y) {
+                        const int row = lane + 32 * y, p = r0 + (row >> lpack);
+                        v[y] = p < it.lq ? __ldg(stats + ((int64_t)it.q0 + p) * A.Hq + h + (row & ((1 << lpack) - 1)))
+                                         : make_float2(-INFINITY, 0.f);
+                    }
+                    if (++r == sp.per) {
+                        r = 0;
+                        h += 1 << lpack;
+                    }
+                };
+                if (sp.n > 0) load();
+                for (int i = 0; i < sp.n; ++i, ++t) {
+                    float* st = reinterpret_cast<float*>(sm + C::kStat + (t & 1) * 1024);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    st[lane + 32 * y] = x[y].x;
-                    st[128 + lane + 32 * y] = x[y].y;
+                    for (int y = 0; y < 4; ++y) {
+                        st[lane + 32 * y] = v[y].x;
+                        st[128 + lane + 32 * y] = v[y].y;
+                    }
+                    if (i + 1 < sp.n) load();
+                    ok = ok && wait_or_flag(bar_s, t & 1, err);
+                    umma::fence_after_sync();
+                    umma::fence_before_sync();
+                    named_arrive(kBarS, 288);
+                    ok = ok && wait_or_flag(bar_dp, t & 1, err);
+                    umma::fence_after_sync();
+                    umma::fence_before_sync();
+                    named_arrive(kBarDp, 288);
                 }
-                if (i + 1 < n) load(i + 1, x);
-                ok = ok && wait_or_flag(bar_s, i & 1, err);
-                umma::fence_after_sync();
-                umma::fence_before_sync();
-                named_arrive(kBarS, 288);
-                ok = ok && wait_or_flag(bar_dp, i & 1, err);
-                umma::fence_after_sync();
-                umma::fence_before_sync();
-                named_arrive(kBarDp, 288);
             }
+        } else {
+            schedule_items(A, cu_q, cu_k, kRows, A.Hkv, true, items, bar_it, bar_ie, bar_ask, bar_want, err,
+                           [](int kv) { return kv; });
         }
-        __syncwarp();
     } else {
         take_registers();
         // ---- elementwise: lane = key, this warpgroup's 64 of the tile's 128 rows
-        const int half = warp >> 2, key = B.first + (tid & 127);
+        const int half = warp >> 2;
         const uint32_t lanes = (uint32_t)((warp & 3) << 5) << 16;
         const uint32_t tS = cS + lanes + half * 64, tP = cP + lanes + half * 64;
         const float2 c2 = make_float2(A.scale * kLog2e, A.scale * kLog2e);
-        for (int i = 0; i < n; ++i) {
-            const float* st = reinterpret_cast<const float*>(sm + C::kStat + (i & 1) * 1024) + half * 64;
-            // rows from column `from` on see the key: row position >= key - off
-            const int from = max(-kRows, min(kRows, key - off - first_row(i))) * (1 << lpack) - half * 64;
-            named_sync(kBarS, 288);
-            umma::fence_after_sync();
-            float2 p[32];
-            load64(tS, p);
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-                const float4 nl = *reinterpret_cast<const float4*>(st + 2 * x);
-                const float2 a = ffma2(p[x], c2, make_float2(nl.x, nl.y)), b = ffma2(p[x + 1], c2, make_float2(nl.z, nl.w));
-                p[x] = make_float2(ex2(a.x), ex2(a.y));
-                p[x + 1] = make_float2(ex2(b.x), ex2(b.y));
+        uint32_t t = 0;  // tiles so far
+        int count = 0;
+        bool ok = true;
+        for (int x = 0;; ++x) {
+            int n, per, ahead;  // tiles; tiles per head group; first row that sees the key, from the first tile's start
+            int64_t at;         // the key's place in the results (-1: none)
+            {
+                const Item it = next_item(items, x, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                const Span sp = span(it);
+                const int key = it.first + (tid & 127);
+                n = sp.n;
+                per = sp.per;
+                ahead = key - (it.lk - it.lq) - (sp.i0 << lqb);
+                at = key < it.lk ? ((int64_t)it.k0 + key) * A.Hkv + it.head : -1;
             }
-            if (__any_sync(0xffffffffu, from > 0)) {
+            for (int i = 0, r = 0; i < n; ++i, ++t) {
+                const float* st = reinterpret_cast<const float*>(sm + C::kStat + (t & 1) * 1024) + half * 64;
+                // rows from column `from` on see the key
+                const int from = max(-kRows, min(kRows, ahead - (r << lqb))) * (1 << lpack) - half * 64;
+                if (++r == per) r = 0;
+                named_sync(kBarS, 288);
+                umma::fence_after_sync();
+                float2 p[32];
+                load64(tS, p);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    p[x].x = 2 * x >= from ? p[x].x : 0.f;
-                    p[x].y = 2 * x + 1 >= from ? p[x].y : 0.f;
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 nl = *reinterpret_cast<const float4*>(st + 2 * e);
+                    const float2 a = ffma2(p[e], c2, make_float2(nl.x, nl.y));
+                    const float2 b = ffma2(p[e + 1], c2, make_float2(nl.z, nl.w));
+                    p[e] = make_float2(ex2(a.x), ex2(a.y));
+                    p[e + 1] = make_float2(ex2(b.x), ex2(b.y));
                 }
-            }
-            uint32_t w[32];
+                if (__any_sync(0xffffffffu, from > 0)) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) w[x] = pack_bf2(p[x].x, p[x].y);
-            umma::tmem_st32_async(tS, w);
-            umma::tmem_wait_st();
-            umma::fence_before_sync();
-            named_arrive(kBarP, 288);
-            named_sync(kBarDp, 288);
+                    for (int e = 0; e < 32; ++e) {
+                        p[e].x = 2 * e >= from ? p[e].x : 0.f;
+                        p[e].y = 2 * e + 1 >= from ? p[e].y : 0.f;
+                    }
+                }
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] = pack_bf2(p[e].x, p[e].y);
+                umma::tmem_st32_async(tS, w);
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                named_arrive(kBarP, 288);
+                named_sync(kBarDp, 288);
+                umma::fence_after_sync();
+                float2 d[32];
+                load64(tP, d);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 nd = *reinterpret_cast<const float4*>(st + 128 + 2 * e);
+                    const float2 a = fmul2(p[e], fadd2(d[e], make_float2(nd.x, nd.y)));
+                    const float2 b = fmul2(p[e + 1], fadd2(d[e + 1], make_float2(nd.z, nd.w)));
+                    w[e] = pack_bf2(a.x, a.y);
+                    w[e + 1] = pack_bf2(b.x, b.y);
+                }
+                umma::tmem_st32_async(tP, w);
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                named_arrive(kBarDs, 288);
+            }
+            // ---- results: dv by the first warpgroup, dk by the second
+            if (n > 0) ok = ok && wait_or_flag(bar_done, count & 1, err);
             umma::fence_after_sync();
-            float2 d[32];
-            load64(tP, d);
+            const float mul = half ? A.scale : 1.f;
+            __nv_bfloat16* dst = (half ? dk : dv) + at * D;
 #pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-                const float4 nd = *reinterpret_cast<const float4*>(st + 128 + 2 * x);
-                const float2 a = fmul2(p[x], fadd2(d[x], make_float2(nd.x, nd.y)));
-                const float2 b = fmul2(p[x + 1], fadd2(d[x + 1], make_float2(nd.z, nd.w)));
-                w[x] = pack_bf2(a.x, a.y);
-                w[x + 1] = pack_bf2(b.x, b.y);
-            }
-            umma::tmem_st32_async(tP, w);
-            umma::tmem_wait_st();
-            umma::fence_before_sync();
-            named_arrive(kBarDs, 288);
-        }
-        // ---- results: dv by the first warpgroup, dk by the second
-        if (n > 0) wait_or_flag(bar_done, 0, err);
-        umma::fence_after_sync();
-        const float mul = half ? A.scale : 1.f;
-        __nv_bfloat16* dst = (half ? dk : dv) + ((B.k0 + key) * A.Hkv + kv) * D;
+            for (int b = 0; b < D / 32; ++b) {
+                float o[32];
+                if (n > 0) {
+                    umma::tmem_ld32((half ? cK : cV) + lanes + 32 * b, o);
+                } else {
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) {
-            float o[32];
-            if (n > 0) {
-                umma::tmem_ld32((half ? cK : cV) + lanes + 32 * b, o);
-            } else {
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (b == D / 32 - 1 && n > 0) {  // dV and dK may be overwritten
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(bar_oe);
+                    ++count;
+                }
+                if (at >= 0) {
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = 0.f;
-            }
-            if (key < B.lk) {
-#pragma unroll
-                for (int x = 0; x < 32; x += 8)
-                    *reinterpret_cast<uint4*>(dst + 32 * b + x) =
-                        make_uint4(pack_bf2(o[x] * mul, o[x + 1] * mul), pack_bf2(o[x + 2] * mul, o[x + 3] * mul),
-                                   pack_bf2(o[x + 4] * mul, o[x + 5] * mul), pack_bf2(o[x + 6] * mul, o[x + 7] * mul));
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(dst + 32 * b + e) = make_uint4(
+                            pack_bf2(o[e] * mul, o[e + 1] * mul), pack_bf2(o[e + 2] * mul, o[e + 3] * mul),
+                            pack_bf2(o[e + 4] * mul, o[e + 5] * mul), pack_bf2(o[e + 6] * mul, o[e + 7] * mul));
+                }
             }
         }
     }
@@ -388,22 +482,20 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                   const int32_t* __restrict__ cu_k, int lpack, const float2* __restrict__ stats,
                   __nv_bfloat16* __restrict__ dq, int32_t* __restrict__ err) {
     using C = Cfg<D>;
+    using Ring = RingPos<C::kSlots>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int qb = kRows >> lpack, n_hg = A.Hq >> lpack;
-    const AttnBlock B = attn_find_block(A, cu_q, cu_k, qb, blockIdx.x / n_hg, false);
-    if (!B.found) return;  // the whole block
-    const int h0 = (int)(blockIdx.x % n_hg) << lpack, kv = h0 / A.G, off = B.lk - B.lq;
-    const int end = max(0, min(B.lk, min(B.first + qb, B.lq) + off));
-    const int n = __shfl_sync(0xffffffffu, (end + kRows - 1) / kRows, 0);
-
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
-    const uint32_t bar_q = bars, bar_full = bars + 8, bar_empty = bar_full + 8 * C::kSlots;
+    const uint32_t bar_q = bars, bar_qe = bar_q + 8, bar_full = bar_qe + 8, bar_empty = bar_full + 8 * C::kSlots;
     const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_se = bar_s + 16, bar_dp = bar_se + 16, bar_fix = bar_dp + 8;
-    const uint32_t bar_done = bar_fix + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 248);
+    const uint32_t bar_done = bar_fix + 32, bar_oe = bar_done + 8, bar_it = bar_oe + 8, bar_ie = bar_it + 8 * kItems;
+    const uint32_t bar_ask = bar_ie + 8 * kItems, bar_want = bar_ask + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 316);
+    ItemRing* items = reinterpret_cast<ItemRing*>(sm + C::kItem);
     if (tid == 0) {
         umma::mbar_init(bar_q, 1);
+        umma::mbar_init(bar_qe, 1);
         for (int i = 0; i < C::kSlots; ++i) {
             umma::mbar_init(bar_full + 8 * i, 1);
             umma::mbar_init(bar_empty + 8 * i, 1);
@@ -413,8 +505,15 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             umma::mbar_init(bar_se + 8 * i, 8);
         }
         umma::mbar_init(bar_dp, 1);
-        umma::mbar_init(bar_fix, 1);
+        for (int i = 0; i < 4; ++i) umma::mbar_init(bar_fix + 8 * i, 1);
         umma::mbar_init(bar_done, 1);
+        umma::mbar_init(bar_oe, 8);
+        for (int i = 0; i < kItems; ++i) {
+            umma::mbar_init(bar_it + 8 * i, 1);
+            umma::mbar_init(bar_ie + 8 * i, kItemWarps);
+        }
+        umma::mbar_init(bar_ask, 1);
+        umma::mbar_init(bar_want, 1);
         umma::fence_mbar_init();
     }
     if (warp == 9) umma::tmem_alloc(tmem_slot, C::kCols);
@@ -423,182 +522,252 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
     umma::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t cS = tmem, cP = tmem + 256, cQ = tmem + 384;  // S (two buffers), dP / dS, dQ
-    auto slot_of = [&](int use) { return use % C::kSlots; };
-    auto par_of = [&](int use) { return (uint32_t)(use / C::kSlots) & 1u; };
+
+    struct Span { int end, n; };  // keys the tile sees: [0, end), in n key tiles
+    auto span = [&](const Item& it) {
+        const int end = max(0, min(it.lk, min(it.first + qb, it.lq) + it.lk - it.lq));
+        return Span{end, __shfl_sync(0xffffffffu, (end + kRows - 1) / kRows, 0)};
+    };
 
     if (warp >= 8) {
         give_registers();
         bool ok = true;
-        if (warp == 8 && n > 0) {
-            // ---- loads: use 2 i of the ring is K tile i, use 2 i + 1 is V tile i
-            if (lane == 0) {
-                tma::expect_tx(bar_q, 2 * C::kTile);
-                for (int b = 0; b < D / 64; ++b) {
-                    tma::tensor_load_3d(base + C::kFix + b * (kRows * 128), &map_q, 64 * b, h0, (int)(B.q0 + B.first),
-                                        bar_q);
-                    tma::tensor_load_3d(base + C::kFix + C::kTile + b * (kRows * 128), &map_do, 64 * b, h0,
-                                        (int)(B.q0 + B.first), bar_q);
+        if (warp == 8) {
+            // ---- loads: the ring takes K 0, V 0, K 1, V 1, ... of every item
+            static_assert(C::kSlots <= 8, "items in the ring");
+            Ring ring;
+            int used = 0, fixed = 0, q_loads = 0;
+            for (int x = 0;; ++x) {
+                const Item it = next_item(items, x, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                const Span sp = span(it);
+                const int kv = it.head / A.G, ask_at = max(0, sp.n - 2);
+                if (sp.n == 0 && lane == 0) umma::mbar_arrive(bar_want);
+                Ring use;
+                for (int i = 0; i < sp.n; ++i) {
+                    if (i == ask_at && lane == 0) umma::mbar_arrive(bar_want);  // time to look for the next item
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const Ring u = ring.next();
+                        if (y == 0) use = u;
+                        if (used++ >= C::kSlots) ok = ok && wait_or_flag(bar_empty + 8 * u.slot, u.par ^ 1u, err);
+                        if (ok && lane == 0) {
+                            tma::expect_tx(bar_full + 8 * u.slot, C::kTile);
+                            for (int b = 0; b < D / 64; ++b)
+                                tma::tensor_load_3d(base + C::kRing + u.slot * C::kTile + b * (kRows * 128),
+                                                    y ? &map_v : &map_k, 64 * b, kv, it.k0 + i * kRows,
+                                                    bar_full + 8 * u.slot);
+                        }
+                        if (i == 0 && y == 0) {  // the query tile, once the last item's scores and dP are formed
+                            if (q_loads++ > 0) ok = ok && wait_or_flag(bar_qe, q_loads & 1, err);
+                            if (ok && lane == 0) {
+                                tma::expect_tx(bar_q, 2 * C::kTile);
+                                for (int b = 0; b < D / 64; ++b) {
+                                    tma::tensor_load_3d(base + C::kFix + b * (kRows * 128), &map_q, 64 * b, it.head,
+                                                        it.q0 + it.first, bar_q);
+                                    tma::tensor_load_3d(base + C::kFix + C::kTile + b * (kRows * 128), &map_do, 64 * b,
+                                                        it.head, it.q0 + it.first, bar_q);
+                                }
+                            }
+                        }
+                    }
+                }
+                if (sp.n > 0) {
+                    // keys behind the last visible one: cleared, whatever they hold (dS is 0 there).  The ring holds
+                    // the tiles of at most four items: four barriers.
+                    ok = ok && wait_or_flag(bar_full + 8 * use.slot, use.par, err);
+                    if (ok) zero_rows<D>(sm + C::kRing + use.slot * C::kTile, sp.end - (sp.n - 1) * kRows);
+                    umma::fence_async_smem();
+                    __syncwarp();
+                    if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (fixed & 3));
+                    ++fixed;
                 }
             }
-            int u = 0;
-            for (; u < 2 * n; ++u) {
-                const int slot = slot_of(u);
-                if (u >= C::kSlots && !(ok = wait_or_flag(bar_empty + 8 * slot, par_of(u - C::kSlots), err))) break;
-                if (lane == 0) {
-                    tma::expect_tx(bar_full + 8 * slot, C::kTile);
-                    for (int b = 0; b < D / 64; ++b)
-                        tma::tensor_load_3d(base + C::kRing + slot * C::kTile + b * (kRows * 128),
-                                            u & 1 ? &map_v : &map_k, 64 * b, kv, (int)B.k0 + (u >> 1) * kRows,
-                                            bar_full + 8 * slot);
-                }
-            }
-            if (ok) {  // keys behind the last visible one: cleared, whatever they hold (dS is 0 there)
-                const int y = 2 * (n - 1);
-                ok = wait_or_flag(bar_full + 8 * slot_of(y), par_of(y), err);
-                if (ok) zero_rows<D>(sm + C::kRing + slot_of(y) * C::kTile, end - (n - 1) * kRows);
-                umma::fence_async_smem();
-                __syncwarp();
-                if (ok && lane == 0) umma::mbar_arrive(bar_fix);
-            }
-            if (!ok) {  // copies in flight land before the block ends
-                wait_or_flag(bar_q, 0, err);
-                for (int i = max(0, u - C::kSlots); i < u; ++i) wait_or_flag(bar_full + 8 * slot_of(i), par_of(i), err);
-            }
-        } else if (warp == 9 && n > 0) {
+        } else if (warp == 9) {
             // ---- products: one lane issues, the warp stays together
             const uint32_t lead = umma::elect_one();
-            const uint32_t id_s = umma::idesc_bf16(kRows, kRows, false, false);
-            const uint32_t id_d = umma::idesc_bf16(kRows, D, false, true);
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 ok = __all_sync(0xffffffffu, ok && wait_or_flag(bar, parity, err));
-            };
-            auto ring = [&](int u) { return base + C::kRing + slot_of(u) * C::kTile; };
-            auto outer = [&](uint32_t d, uint32_t a_tile, uint32_t b_tile) {
-                if (!ok) return;
-                const uint64_t a = umma::kmajor(a_tile, kRows, 0), b = umma::kmajor(b_tile, kRows, 0);
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint64_t ks = (uint64_t)((s >> 2) * (kRows * 128 / 16) + (s & 3) * 2);
-                    umma::mma_lead(d, a + ks, b + ks, id_s, s > 0, lead);
-                }
             };
             auto done = [&](uint32_t bar) {
                 if (ok && lead) umma::commit(bar);
             };
-            auto score = [&](int i) {  // S of tile i into its buffer, free once tile i - 2 has been read
-                if (i >= 2) wait(bar_se + 8 * (i & 1), ((i >> 1) - 1) & 1);
-                wait(bar_full + 8 * slot_of(2 * i), par_of(2 * i));
-                if (i == n - 1) wait(bar_fix, 0);
-                umma::fence_after_sync();
-                outer(cS + (i & 1) * 128, base + C::kFix, ring(2 * i));
-                done(bar_s + 8 * (i & 1));
-            };
-            auto grad = [&](int i) {  // dP of tile i
-                wait(bar_full + 8 * slot_of(2 * i + 1), par_of(2 * i + 1));
-                umma::fence_after_sync();
-                outer(cP, base + C::kFix + C::kTile, ring(2 * i + 1));
-                done(bar_dp);
-                done(bar_empty + 8 * slot_of(2 * i + 1));
-            };
-            wait(bar_q, 0);
-            score(0);
-            grad(0);
-            if (n > 1) score(1);
-            for (int i = 0; i < n; ++i) {
-                named_sync(kBarDs, 288);
-                umma::fence_after_sync();
-                if (ok) {
-                    const uint64_t b = umma::mnmajor(ring(2 * i), kRows * 128, 0);
-#pragma unroll
-                    for (int s = 0; s < kRows / 16; ++s)
-                        umma::mma_ts_lead(cQ, half_step(cP, s), b + (uint64_t)(s * 128), id_d, i > 0 || s > 0, lead);
+            const uint64_t q_tile = umma::kmajor(base + C::kFix, kRows, 0);
+            const uint64_t o_tile = umma::kmajor(base + C::kFix + C::kTile, kRows, 0);
+            const uint64_t ring_k = umma::kmajor(base + C::kRing, kRows, 0);
+            const uint64_t ring_mn = umma::mnmajor(base + C::kRing, kRows * 128, 0);
+            auto at = [&](uint64_t ring0, const Ring& u) { return ring0 + (uint64_t)(u.slot * (C::kTile / 16)); };
+            Ring ring;
+            int fixed = 0, count = 0;
+            uint32_t ts = 0;  // score tiles so far
+            for (int x = 0;; ++x) {
+                const Item it = next_item(items, x, bar_it, bar_ie, err);
+                if (__shfl_sync(0xffffffffu, it.head, 0) < 0) break;
+                const int n = span(it).n;
+                if (n == 0) continue;
+                // S of the item's tile i into the next buffer, free once the tile before last has been read
+                auto score = [&](const Ring& k, int i) {
+                    if (ts >= 2) wait(bar_se + 8 * (ts & 1), ((ts >> 1) - 1) & 1);
+                    wait(bar_full + 8 * k.slot, k.par);
+                    if (i == n - 1) {
+                        wait(bar_fix + 8 * (fixed & 3), (fixed >> 2) & 1);
+                        ++fixed;
+                    }
+                    umma::fence_after_sync();
+                    if (ok) outer_product<D>(cS + (ts & 1) * 128, q_tile, at(ring_k, k), lead);
+                    done(bar_s + 8 * (ts & 1));
+                    ++ts;
+                };
+                auto grad = [&](const Ring& v) {  // dP
+                    wait(bar_full + 8 * v.slot, v.par);
+                    umma::fence_after_sync();
+                    if (ok) outer_product<D>(cP, o_tile, at(ring_k, v), lead);
+                    done(bar_dp);
+                    done(bar_empty + 8 * v.slot);
+                };
+                // K of tiles i, i + 1, i + 2 and V of tiles i + 1, i + 2
+                Ring k0 = ring.next(), v0 = ring.next(), k1 = k0, v1 = v0;
+                wait(bar_q, count & 1);
+                score(k0, 0);
+                grad(v0);
+                if (n == 1) done(bar_qe);
+                if (n > 1) {
+                    k1 = ring.next();
+                    v1 = ring.next();
+                    score(k1, 1);
                 }
-                done(bar_empty + 8 * slot_of(2 * i));
-                if (i + 1 < n) grad(i + 1);
-                if (i + 2 < n) score(i + 2);
+                if (count > 0) wait(bar_oe, (count - 1) & 1);  // dQ has been read
+                for (int i = 0; i < n; ++i) {
+                    Ring k2 = k1, v2 = v1;
+                    if (i + 2 < n) {
+                        k2 = ring.next();
+                        v2 = ring.next();
+                    }
+                    named_sync(kBarDs, 288);
+                    umma::fence_after_sync();
+                    if (ok) inner_product<D>(cQ, cP, at(ring_mn, k0), i > 0, lead);
+                    if (i + 1 < n) {
+                        grad(v1);
+                        if (i + 2 == n) done(bar_qe);  // Q and dO have been read for the last time
+                    } else {
+                        done(bar_done);
+                    }
+                    done(bar_empty + 8 * k0.slot);
+                    if (i + 2 < n) score(k2, i + 2);
+                    k0 = k1;
+                    k1 = k2;
+                    v1 = v2;
+                }
+                ++count;
             }
-            done(bar_done);
         } else if (warp == 10) {
             // ---- "scores ready", "score gradients ready" passed on to the elementwise warps.  Scores run one tile
             //      ahead: two barriers, so that a slow warp never meets the signal of the tile after its own (the one
             //      after that waits until every warp has read this tile's scores)
-            for (int i = 0; i < n; ++i) {
-                ok = ok && wait_or_flag(bar_s + 8 * (i & 1), (i >> 1) & 1, err);
-                umma::fence_after_sync();
-                umma::fence_before_sync();
-                named_arrive(kBarS + (i & 1), 288);
-                ok = ok && wait_or_flag(bar_dp, i & 1, err);
-                umma::fence_after_sync();
-                umma::fence_before_sync();
-                named_arrive(kBarDp, 288);
+            uint32_t t = 0;  // tiles so far
+            for (int x = 0;; ++x) {
+                const Item it = next_item(items, x, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                const int n = span(it).n;
+                for (int i = 0; i < n; ++i, ++t) {
+                    ok = ok && wait_or_flag(bar_s + 8 * (t & 1), (t >> 1) & 1, err);
+                    umma::fence_after_sync();
+                    umma::fence_before_sync();
+                    named_arrive(kBarS + (t & 1), 288);
+                    ok = ok && wait_or_flag(bar_dp, t & 1, err);
+                    umma::fence_after_sync();
+                    umma::fence_before_sync();
+                    named_arrive(kBarDp, 288);
+                }
             }
+        } else {
+            schedule_items(A, cu_q, cu_k, qb, n_hg, false, items, bar_it, bar_ie, bar_ask, bar_want, err,
+                           [&](int hg) { return hg << lpack; });
         }
-        __syncwarp();
     } else {
         take_registers();
         // ---- elementwise: lane = row, this warpgroup's 64 of the tile's 128 keys
-        const int half = warp >> 2, row = tid & 127, pos = B.first + (row >> lpack), h = h0 + (row & ((1 << lpack) - 1));
-        const bool on = pos < B.lq;
-        const int limit = on ? min(B.lk, pos + off + 1) : 0;
+        const int half = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) << 5) << 16;
         const uint32_t tP = cP + lanes + half * 64;
-        const int64_t at = (B.q0 + pos) * A.Hq + h;
-        const float2 st = on ? __ldg(stats + at) : make_float2(-INFINITY, 0.f);
         const float2 c2 = make_float2(A.scale * kLog2e, A.scale * kLog2e);
-        const float2 nl = make_float2(st.x, st.x), nd = make_float2(st.y, st.y);
-        for (int i = 0; i < n; ++i) {
-            const int seen = limit - i * kRows - half * 64;
-            const bool edge = __any_sync(0xffffffffu, seen < 64);
-            named_sync(kBarS + (i & 1), 288);
-            umma::fence_after_sync();
-            float2 p[32];
-            load64(cS + (i & 1) * 128 + lanes + half * 64, p);
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(bar_se + 8 * (i & 1));
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-                const float2 a = ffma2(p[x], c2, nl);
-                p[x] = make_float2(ex2(a.x), ex2(a.y));
+        uint32_t t = 0;  // tiles so far
+        int count = 0;
+        bool ok = true;
+        for (int x = 0;; ++x) {
+            int n, limit;  // key tiles; keys the row sees: [0, limit)
+            int64_t at;    // the row's place in the result (-1: none)
+            {
+                const Item it = next_item(items, x, bar_it, bar_ie, err);
+                if (it.head < 0) break;
+                n = span(it).n;
+                const int pos = it.first + (row >> lpack);
+                limit = pos < it.lq ? min(it.lk, pos + it.lk - it.lq + 1) : 0;
+                at = pos < it.lq ? ((int64_t)it.q0 + pos) * A.Hq + it.head + (row & ((1 << lpack) - 1)) : -1;
             }
-            named_sync(kBarDp, 288);
-            umma::fence_after_sync();
-            float2 d[32];
-            load64(tP, d);
-            uint32_t w[32];
+            const float2 st = at >= 0 ? __ldg(stats + at) : make_float2(-INFINITY, 0.f);
+            const float2 nl = make_float2(st.x, st.x), nd = make_float2(st.y, st.y);
+            for (int i = 0; i < n; ++i, ++t) {
+                const int seen = limit - i * kRows - half * 64;
+                const bool edge = __any_sync(0xffffffffu, seen < 64);
+                named_sync(kBarS + (t & 1), 288);
+                umma::fence_after_sync();
+                float2 p[32];
+                load64(cS + (t & 1) * 128 + lanes + half * 64, p);
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(bar_se + 8 * (t & 1));
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-                float2 a = fmul2(p[x], fadd2(d[x], nd));
-                if (edge) {
-                    a.x = 2 * x < seen ? a.x : 0.f;
-                    a.y = 2 * x + 1 < seen ? a.y : 0.f;
+                for (int e = 0; e < 32; ++e) {
+                    const float2 a = ffma2(p[e], c2, nl);
+                    p[e] = make_float2(ex2(a.x), ex2(a.y));
                 }
-                w[x] = pack_bf2(a.x, a.y);
+                named_sync(kBarDp, 288);
+                umma::fence_after_sync();
+                float2 d[32];
+                load64(tP, d);
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float2 a = fmul2(p[e], fadd2(d[e], nd));
+                    if (edge) {
+                        a.x = 2 * e < seen ? a.x : 0.f;
+                        a.y = 2 * e + 1 < seen ? a.y : 0.f;
+                    }
+                    w[e] = pack_bf2(a.x, a.y);
+                }
+                umma::tmem_st32_async(tP, w);
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                named_arrive(kBarDs, 288);
             }
-            umma::tmem_st32_async(tP, w);
-            umma::tmem_wait_st();
-            umma::fence_before_sync();
-            named_arrive(kBarDs, 288);
-        }
-        if (n > 0) wait_or_flag(bar_done, 0, err);
-        umma::fence_after_sync();
-        // ---- results: half of the columns each
-        __nv_bfloat16* dst = dq + at * D + half * (D / 2);
+            if (n > 0) ok = ok && wait_or_flag(bar_done, count & 1, err);
+            umma::fence_after_sync();
+            // ---- results: half of the columns each
+            __nv_bfloat16* dst = dq + at * D + half * (D / 2);
 #pragma unroll
-        for (int b = 0; b < D / 64; ++b) {
-            float o[32];
-            if (n > 0) {
-                umma::tmem_ld32(cQ + lanes + half * (D / 2) + 32 * b, o);
-            } else {
+            for (int b = 0; b < D / 64; ++b) {
+                float o[32];
+                if (n > 0) {
+                    umma::tmem_ld32(cQ + lanes + half * (D / 2) + 32 * b, o);
+                } else {
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = 0.f;
-            }
-            if (on) {
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (b == D / 64 - 1 && n > 0) {  // dQ may be overwritten
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(bar_oe);
+                    ++count;
+                }
+                if (at >= 0) {
+                    const float m = A.scale;
 #pragma unroll
-                for (int x = 0; x < 32; x += 8)
-                    *reinterpret_cast<uint4*>(dst + 32 * b + x) = make_uint4(
-                        pack_bf2(o[x] * A.scale, o[x + 1] * A.scale), pack_bf2(o[x + 2] * A.scale, o[x + 3] * A.scale),
-                        pack_bf2(o[x + 4] * A.scale, o[x + 5] * A.scale), pack_bf2(o[x + 6] * A.scale, o[x + 7] * A.scale));
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(dst + 32 * b + e) =
+                            make_uint4(pack_bf2(o[e] * m, o[e + 1] * m), pack_bf2(o[e + 2] * m, o[e + 3] * m),
+                                       pack_bf2(o[e + 4] * m, o[e + 5] * m), pack_bf2(o[e + 6] * m, o[e + 7] * m));
+                }
             }
         }
     }

@@ -172,17 +172,9 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             auto done = [&](uint32_t bar) {
                 if (ok && lead) umma::commit(bar);
             };
-            // the ring: slot and parity of the next use, in order K 0, V 0, K 1, V 1, ... of every item
-            uint32_t slot = 0, par = 0;
-            struct Use { uint32_t slot, par; };
-            auto next_use = [&]() {
-                const Use u = {slot, par};
-                if (++slot == C::kSlots) {
-                    slot = 0;
-                    par ^= 1u;
-                }
-                return u;
-            };
+            // the ring is used in the order K 0, V 0, K 1, V 1, ... of every item
+            using Use = RingPos<C::kSlots>;
+            Use ring;
             const uint64_t q_tile[2] = {umma::kmajor(base + C::kQ, kRows, 0), umma::kmajor(base + C::kQ + C::kTile, kRows, 0)};
             const uint64_t k_ring = umma::kmajor(base + C::kRing, kRows, 0);
             const uint64_t v_ring = umma::mnmajor(base + C::kRing, kRows * 128, 0);
@@ -211,7 +203,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 const Span sp = span(it);
                 const int n = sp.n;
                 if (n == 0) continue;
-                const Use first = next_use();
+                const Use first = ring.next();
                 wait(bar_full + 8 * first.slot, first.par);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -225,7 +217,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 done(bar_empty + 8 * first.slot);
                 for (int j = 0; j < n; ++j) {
                     const bool more = j + 1 < n;
-                    const Use v = next_use(), k = more ? next_use() : v;
+                    const Use v = ring.next(), k = more ? ring.next() : v;
                     wait(bar_full + 8 * v.slot, v.par);
                     if (more) wait(bar_full + 8 * k.slot, k.par);
                     else wait(bar_fix + 8 * (n_fix & 3), (n_fix >> 2) & 1);

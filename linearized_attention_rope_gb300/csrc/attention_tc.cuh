@@ -183,6 +183,19 @@ __device__ __forceinline__ Item next_item(const ItemRing* ring, int i, uint32_t 
     return it;
 }
 
+// Position in a ring of n slots that is used over and over: slot, and the parity of its current round.
+template <int N> struct RingPos {
+    uint32_t slot = 0, par = 0;
+    __device__ __forceinline__ RingPos next() {  // this use; moves on
+        const RingPos u = *this;
+        if (++slot == N) {
+            slot = 0;
+            par ^= 1u;
+        }
+        return u;
+    }
+};
+
 // Rows [first, 128) of a 128 x D 16-bit tile (128-byte-swizzled 64-column blocks) set to zero by one warp.
 template <int D>
 __device__ __forceinline__ void zero_rows(unsigned char* tile, int first) {
