@@ -69,8 +69,9 @@ attn_stats_kernel(int64_t rows, const __nv_bfloat16* __restrict__ out, const __n
 }
 
 // Hardware barriers between the elementwise warps (256 threads) and the warp that issues or passes on (32):
-// scores, probabilities (dkdv; dq: scores of odd tiles), score gradients dP and dS ready.
-constexpr int kBarS = 1, kBarP = 2, kBarDp = 3, kBarDs = 4;
+// scores, probabilities, score gradients dP and dS ready; in the dq kernel dP and dS by even and odd tiles
+// (kBarDq, kBarDs, one more each).
+constexpr int kBarS = 1, kBarP = 2, kBarDp = 3, kBarDq = 2, kBarDs = 4;
 
 template <int D> struct Cfg {
     static constexpr uint32_t kTile = kRows * D * 2;
@@ -482,14 +483,17 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                   const int32_t* __restrict__ cu_k, int lpack, const float2* __restrict__ stats,
                   __nv_bfloat16* __restrict__ dq, int32_t* __restrict__ err) {
     using C = Cfg<D>;
-    using Ring = RingPos<C::kSlots>;
+    // K tiles stay until their dQ product, V tiles only for dP: rings of their own, so that V runs ahead
+    constexpr int kKs = C::kSlots - 2, kVs = 2;
+    using RingK = RingPos<kKs>;
+    using RingV = RingPos<kVs>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int qb = kRows >> lpack, n_hg = A.Hq >> lpack;
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
     const uint32_t bar_q = bars, bar_qe = bar_q + 8, bar_full = bar_qe + 8, bar_empty = bar_full + 8 * C::kSlots;
-    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_se = bar_s + 16, bar_dp = bar_se + 16, bar_fix = bar_dp + 8;
-    const uint32_t bar_done = bar_fix + 32, bar_oe = bar_done + 8, bar_it = bar_oe + 8, bar_ie = bar_it + 8 * kItems;
+    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_se = bar_s + 8, bar_dp = bar_se + 8, bar_fix = bar_dp + 8;
+    const uint32_t bar_done = bar_fix + 64, bar_oe = bar_done + 8, bar_it = bar_oe + 8, bar_ie = bar_it + 8 * kItems;
     const uint32_t bar_ask = bar_ie + 8 * kItems, bar_want = bar_ask + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 316);
     ItemRing* items = reinterpret_cast<ItemRing*>(sm + C::kItem);
@@ -500,12 +504,10 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             umma::mbar_init(bar_full + 8 * i, 1);
             umma::mbar_init(bar_empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(bar_s + 8 * i, 1);
-            umma::mbar_init(bar_se + 8 * i, 8);
-        }
+        umma::mbar_init(bar_s, 1);
+        umma::mbar_init(bar_se, 8);
         umma::mbar_init(bar_dp, 1);
-        for (int i = 0; i < 4; ++i) umma::mbar_init(bar_fix + 8 * i, 1);
+        for (int i = 0; i < 8; ++i) umma::mbar_init(bar_fix + 8 * i, 1);
         umma::mbar_init(bar_done, 1);
         umma::mbar_init(bar_oe, 8);
         for (int i = 0; i < kItems; ++i) {
@@ -521,7 +523,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const uint32_t cS = tmem, cP = tmem + 256, cQ = tmem + 384;  // S (two buffers), dP / dS, dQ
+    const uint32_t cS = tmem, cP = tmem + 128, cQ = tmem + 384;  // S, dP / dS (two buffers), dQ
 
     struct Span { int end, n; };  // keys the tile sees: [0, end), in n key tiles
     auto span = [&](const Item& it) {
@@ -533,53 +535,55 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
         give_registers();
         bool ok = true;
         if (warp == 8) {
-            // ---- loads: the ring takes K 0, V 0, K 1, V 1, ... of every item
+            // ---- loads: slots 0 .. of the ring are K tiles, the last two V tiles
             static_assert(C::kSlots <= 8, "items in the ring");
-            Ring ring;
+            RingK rk;
+            RingV rv;
             int used = 0, fixed = 0, q_loads = 0;
+            auto load = [&](const CUtensorMap* map, uint32_t slot, int head, int row) {
+                if (!ok || lane) return;
+                tma::expect_tx(bar_full + 8 * slot, C::kTile);
+                for (int b = 0; b < D / 64; ++b)
+                    tma::tensor_load_3d(base + C::kRing + slot * C::kTile + b * (kRows * 128), map, 64 * b, head, row,
+                                        bar_full + 8 * slot);
+            };
             for (int x = 0;; ++x) {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (it.head < 0) break;
                 const Span sp = span(it);
                 const int kv = it.head / A.G, ask_at = max(0, sp.n - 2);
                 if (sp.n == 0 && lane == 0) umma::mbar_arrive(bar_want);
-                Ring use;
-                for (int i = 0; i < sp.n; ++i) {
+                RingK k;
+                for (int i = 0; i < sp.n; ++i, ++used) {
                     if (i == ask_at && lane == 0) umma::mbar_arrive(bar_want);  // time to look for the next item
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const Ring u = ring.next();
-                        if (y == 0) use = u;
-                        if (used++ >= C::kSlots) ok = ok && wait_or_flag(bar_empty + 8 * u.slot, u.par ^ 1u, err);
+                    k = rk.next();
+                    if (used >= kKs) ok = ok && wait_or_flag(bar_empty + 8 * k.slot, k.par ^ 1u, err);
+                    load(&map_k, k.slot, kv, it.k0 + i * kRows);
+                    if (i == 0) {  // the query tile, once the last item's scores and dP are formed
+                        if (q_loads++ > 0) ok = ok && wait_or_flag(bar_qe, q_loads & 1, err);
                         if (ok && lane == 0) {
-                            tma::expect_tx(bar_full + 8 * u.slot, C::kTile);
-                            for (int b = 0; b < D / 64; ++b)
-                                tma::tensor_load_3d(base + C::kRing + u.slot * C::kTile + b * (kRows * 128),
-                                                    y ? &map_v : &map_k, 64 * b, kv, it.k0 + i * kRows,
-                                                    bar_full + 8 * u.slot);
-                        }
-                        if (i == 0 && y == 0) {  // the query tile, once the last item's scores and dP are formed
-                            if (q_loads++ > 0) ok = ok && wait_or_flag(bar_qe, q_loads & 1, err);
-                            if (ok && lane == 0) {
-                                tma::expect_tx(bar_q, 2 * C::kTile);
-                                for (int b = 0; b < D / 64; ++b) {
-                                    tma::tensor_load_3d(base + C::kFix + b * (kRows * 128), &map_q, 64 * b, it.head,
-                                                        it.q0 + it.first, bar_q);
-                                    tma::tensor_load_3d(base + C::kFix + C::kTile + b * (kRows * 128), &map_do, 64 * b,
-                                                        it.head, it.q0 + it.first, bar_q);
-                                }
+                            tma::expect_tx(bar_q, 2 * C::kTile);
+                            for (int b = 0; b < D / 64; ++b) {
+                                tma::tensor_load_3d(base + C::kFix + b * (kRows * 128), &map_q, 64 * b, it.head,
+                                                    it.q0 + it.first, bar_q);
+                                tma::tensor_load_3d(base + C::kFix + C::kTile + b * (kRows * 128), &map_do, 64 * b,
+                                                    it.head, it.q0 + it.first, bar_q);
                             }
                         }
                     }
+                    const RingV v = rv.next();
+                    if (used >= kVs) ok = ok && wait_or_flag(bar_empty + 8 * (kKs + v.slot), v.par ^ 1u, err);
+                    load(&map_v, kKs + v.slot, kv, it.k0 + i * kRows);
                 }
                 if (sp.n > 0) {
                     // keys behind the last visible one: cleared, whatever they hold (dS is 0 there).  The ring holds
-                    // the tiles of at most four items: four barriers.
-                    ok = ok && wait_or_flag(bar_full + 8 * use.slot, use.par, err);
-                    if (ok) zero_rows<D>(sm + C::kRing + use.slot * C::kTile, sp.end - (sp.n - 1) * kRows);
+                    // the K tiles of at most six items: eight barriers.
+                    static_assert(kKs <= 6, "items in the ring");
+                    ok = ok && wait_or_flag(bar_full + 8 * k.slot, k.par, err);
+                    if (ok) zero_rows<D>(sm + C::kRing + k.slot * C::kTile, sp.end - (sp.n - 1) * kRows);
                     umma::fence_async_smem();
                     __syncwarp();
-                    if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (fixed & 3));
+                    if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (fixed & 7));
                     ++fixed;
                 }
             }
@@ -596,88 +600,74 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             const uint64_t o_tile = umma::kmajor(base + C::kFix + C::kTile, kRows, 0);
             const uint64_t ring_k = umma::kmajor(base + C::kRing, kRows, 0);
             const uint64_t ring_mn = umma::mnmajor(base + C::kRing, kRows * 128, 0);
-            auto at = [&](uint64_t ring0, const Ring& u) { return ring0 + (uint64_t)(u.slot * (C::kTile / 16)); };
-            Ring ring;
+            RingK rk;
+            RingV rv;
             int fixed = 0, count = 0;
-            uint32_t ts = 0;  // score tiles so far
+            uint32_t ts = 0;  // tiles so far
             for (int x = 0;; ++x) {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (__shfl_sync(0xffffffffu, it.head, 0) < 0) break;
                 const int n = span(it).n;
                 if (n == 0) continue;
-                // S of the item's tile i into the next buffer, free once the tile before last has been read
-                auto score = [&](const Ring& k, int i) {
-                    if (ts >= 2) wait(bar_se + 8 * (ts & 1), ((ts >> 1) - 1) & 1);
+                // S and dP of the item's tile i, once the scores of the tile before have been read; dP goes to the
+                // buffer that the tile before last has been taken from.  Returns the slot of its K tile.
+                auto tile = [&](int i) {
+                    const RingK k = rk.next();
+                    const RingV v = rv.next();
                     wait(bar_full + 8 * k.slot, k.par);
                     if (i == n - 1) {
-                        wait(bar_fix + 8 * (fixed & 3), (fixed >> 2) & 1);
+                        wait(bar_fix + 8 * (fixed & 7), (fixed >> 3) & 1);
                         ++fixed;
                     }
+                    if (ts > 0) wait(bar_se, (ts - 1) & 1);
                     umma::fence_after_sync();
-                    if (ok) outer_product<D>(cS + (ts & 1) * 128, q_tile, at(ring_k, k), lead);
-                    done(bar_s + 8 * (ts & 1));
-                    ++ts;
-                };
-                auto grad = [&](const Ring& v) {  // dP
-                    wait(bar_full + 8 * v.slot, v.par);
+                    if (ok) outer_product<D>(cS, q_tile, ring_k + (uint64_t)(k.slot * (C::kTile / 16)), lead);
+                    done(bar_s);
+                    wait(bar_full + 8 * (kKs + v.slot), v.par);
                     umma::fence_after_sync();
-                    if (ok) outer_product<D>(cP, o_tile, at(ring_k, v), lead);
+                    if (ok)
+                        outer_product<D>(cP + (ts & 1) * 128, o_tile,
+                                         ring_k + (uint64_t)((kKs + v.slot) * (C::kTile / 16)), lead);
                     done(bar_dp);
-                    done(bar_empty + 8 * v.slot);
+                    done(bar_empty + 8 * (kKs + v.slot));
+                    if (i == n - 1) done(bar_qe);  // Q and dO have been read for the last time
+                    ++ts;
+                    return k.slot;
                 };
-                // K of tiles i, i + 1, i + 2 and V of tiles i + 1, i + 2
-                Ring k0 = ring.next(), v0 = ring.next(), k1 = k0, v1 = v0;
                 wait(bar_q, count & 1);
-                score(k0, 0);
-                grad(v0);
-                if (n == 1) done(bar_qe);
-                if (n > 1) {
-                    k1 = ring.next();
-                    v1 = ring.next();
-                    score(k1, 1);
-                }
+                uint32_t k = tile(0);
                 if (count > 0) wait(bar_oe, (count - 1) & 1);  // dQ has been read
                 for (int i = 0; i < n; ++i) {
-                    Ring k2 = k1, v2 = v1;
-                    if (i + 2 < n) {
-                        k2 = ring.next();
-                        v2 = ring.next();
-                    }
-                    named_sync(kBarDs, 288);
+                    const uint32_t b = (ts - 1) & 1;  // this tile's buffer and barrier
+                    const uint32_t k1 = i + 1 < n ? tile(i + 1) : k;
+                    named_sync(kBarDs + b, 288);
                     umma::fence_after_sync();
-                    if (ok) inner_product<D>(cQ, cP, at(ring_mn, k0), i > 0, lead);
-                    if (i + 1 < n) {
-                        grad(v1);
-                        if (i + 2 == n) done(bar_qe);  // Q and dO have been read for the last time
-                    } else {
-                        done(bar_done);
-                    }
-                    done(bar_empty + 8 * k0.slot);
-                    if (i + 2 < n) score(k2, i + 2);
-                    k0 = k1;
-                    k1 = k2;
-                    v1 = v2;
+                    if (ok)
+                        inner_product<D>(cQ, cP + b * 128, ring_mn + (uint64_t)(k * (C::kTile / 16)), i > 0, lead);
+                    if (i + 1 == n) done(bar_done);
+                    done(bar_empty + 8 * k);
+                    k = k1;
                 }
                 ++count;
             }
         } else if (warp == 10) {
-            // ---- "scores ready", "score gradients ready" passed on to the elementwise warps.  Scores run one tile
-            //      ahead: two barriers, so that a slow warp never meets the signal of the tile after its own (the one
-            //      after that waits until every warp has read this tile's scores)
+            // ---- "scores ready", "score gradients ready" passed on to the elementwise warps.  dP runs one tile ahead:
+            //      two barriers, so that a slow warp never meets the signal of the tile after its own (the one after
+            //      that waits until every warp has read the next tile's scores)
             uint32_t t = 0;  // tiles so far
             for (int x = 0;; ++x) {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (it.head < 0) break;
                 const int n = span(it).n;
                 for (int i = 0; i < n; ++i, ++t) {
-                    ok = ok && wait_or_flag(bar_s + 8 * (t & 1), (t >> 1) & 1, err);
+                    ok = ok && wait_or_flag(bar_s, t & 1, err);
                     umma::fence_after_sync();
                     umma::fence_before_sync();
-                    named_arrive(kBarS + (t & 1), 288);
+                    named_arrive(kBarS, 288);
                     ok = ok && wait_or_flag(bar_dp, t & 1, err);
                     umma::fence_after_sync();
                     umma::fence_before_sync();
-                    named_arrive(kBarDp, 288);
+                    named_arrive(kBarDq + (t & 1), 288);
                 }
             }
         } else {
@@ -689,7 +679,6 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
         // ---- elementwise: lane = row, this warpgroup's 64 of the tile's 128 keys
         const int half = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) << 5) << 16;
-        const uint32_t tP = cP + lanes + half * 64;
         const float2 c2 = make_float2(A.scale * kLog2e, A.scale * kLog2e);
         uint32_t t = 0;  // tiles so far
         int count = 0;
@@ -710,19 +699,20 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             for (int i = 0; i < n; ++i, ++t) {
                 const int seen = limit - i * kRows - half * 64;
                 const bool edge = __any_sync(0xffffffffu, seen < 64);
-                named_sync(kBarS + (t & 1), 288);
+                const uint32_t tP = cP + (t & 1) * 128 + lanes + half * 64;
+                named_sync(kBarS, 288);
                 umma::fence_after_sync();
                 float2 p[32];
-                load64(cS + (t & 1) * 128 + lanes + half * 64, p);
+                load64(cS + lanes + half * 64, p);
                 umma::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) umma::mbar_arrive(bar_se + 8 * (t & 1));
+                if (lane == 0) umma::mbar_arrive(bar_se);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     const float2 a = ffma2(p[e], c2, nl);
                     p[e] = make_float2(ex2(a.x), ex2(a.y));
                 }
-                named_sync(kBarDp, 288);
+                named_sync(kBarDq + (t & 1), 288);
                 umma::fence_after_sync();
                 float2 d[32];
                 load64(tP, d);
@@ -739,7 +729,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 umma::tmem_st32_async(tP, w);
                 umma::tmem_wait_st();
                 umma::fence_before_sync();
-                named_arrive(kBarDs, 288);
+                named_arrive(kBarDs + (t & 1), 288);
             }
             if (n > 0) ok = ok && wait_or_flag(bar_done, count & 1, err);
             umma::fence_after_sync();
