@@ -324,6 +324,7 @@ HLA_API int hla_attention_decode(const hla_attn_params* p, const hla_cache_param
     if (!rc) rc = check_buffers(cp, cache);
     if (rc) return rc;
     if (n_seqs < 0) return HLA_ERR_INVALID_ARG;
+    if ((uint64_t)cp->n_pages * cp->n_kv_heads * cp->page_size > 0xfffffffeull) return HLA_ERR_UNSUPPORTED;  // rows
     if (n_seqs == 0) return HLA_OK;
     if (!good(q) || !good(lens) || !good(out) || !good(ws)) return HLA_ERR_INVALID_ARG;
     if (ws_bytes < need) return HLA_ERR_WORKSPACE;

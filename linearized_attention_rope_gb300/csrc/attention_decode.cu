@@ -12,19 +12,35 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kGroup = 8;  // query heads of a kv head per block
+constexpr int kDecodeUnit = 64;  // keys the fp32 kernel takes at a time
 
 // ---- fp32 layers ------------------------------------------------------------
 //
 // Scores: eight lanes per key, D / 8 values each, partial dot products joined
 // by three shuffles.  Values: a thread per column pair, the weights read from
 // shared memory.  All in fp32.
+template <int E> __device__ __forceinline__ void load_e4m3(const uint8_t* p, float* f) {
+    uint32_t w[E < 4 ? 1 : E / 4];
+    if constexpr (E == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
+    else if constexpr (E == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+    else if constexpr (E == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    else *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int x = 0; x < E; x += 2) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[x / 4] >> (8 * (x & 2))), __NV_E4M3);
+        const float2 g = __half22float2(__half2(h));
+        f[x] = g.x;
+        f[x + 1] = g.y;
+    }
+}
+
 template <bool E4M3, int D>
 __global__ void __launch_bounds__(kThreads)
 decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict__ q, DecodeLine L,
                   float* __restrict__ out, DecodePart part) {
     constexpr int E = D / 8;  // elements of a key per lane
-    __shared__ float qs[kGroup][D];
-    __shared__ float ps[kGroup][kDecodeUnit];  // scores, then weights
+    __shared__ alignas(16) float qs[kGroup][D];
+    __shared__ alignas(16) float ps[kGroup][kDecodeUnit];  // scores, then weights
     __shared__ float vs[kDecodeUnit];          // scale of each value row
     __shared__ int64_t rows[kDecodeUnit];      // cache rows (-1: none)
     __shared__ float stats[kGroup][2];         // running max, correction
@@ -58,7 +74,7 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
         for (int g = 0; g < kGroup; ++g)
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) acc[g][x] = 0.f;
-        float mrun = -INFINITY, lrun = 0.f;  // threads 0..ng-1: head tid
+        float mrun = -INFINITY, lrun = 0.f;  // of head tid / 16
         for (int64_t w = u; w < e; ++w) {
             const int64_t p0 = (w - useq) * kDecodeUnit;
             const int n = (int)min((int64_t)kDecodeUnit, len - p0);
@@ -76,54 +92,74 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
                 else vs[tid] = 1.f;
             }
             __syncthreads();
-            for (int j = tid / 8; j < kDecodeUnit; j += kThreads / 8) {
-                const int64_t r = rows[j];
-                float kx[E];
-                float ks = 1.f;
-                if (r >= 0) {
-                    if constexpr (E4M3) {
-                        ks = exp2f((float)((int)c.k_exp[r] - 127));
-                        const uint8_t* src = static_cast<const uint8_t*>(c.k) + r * D + (tid & 7) * E;
+            {  // four keys per lane group, all on their way at once
+                constexpr int kN = kDecodeUnit / (kThreads / 8);
+                float kx[kN][E], ks[kN];
 #pragma unroll
-                        for (int x = 0; x < E; x += 2) {
-                            const __half2_raw hv = __nv_cvt_fp8x2_to_halfraw2(
-                                *reinterpret_cast<const __nv_fp8x2_storage_t*>(src + x), __NV_E4M3);
-                            const float2 f = __half22float2(__half2(hv));
-                            kx[x] = f.x;
-                            kx[x + 1] = f.y;
-                        }
+                for (int y = 0; y < kN; ++y) {
+                    const int64_t r = rows[tid / 8 + y * (kThreads / 8)];
+                    ks[y] = 1.f;
+                    if (r < 0) {
+#pragma unroll
+                        for (int x = 0; x < E; ++x) kx[y][x] = 0.f;
+                    } else if constexpr (E4M3) {
+                        ks[y] = exp2f((float)((int)c.k_exp[r] - 127));
+                        load_e4m3<E>(static_cast<const uint8_t*>(c.k) + r * D + (tid & 7) * E, kx[y]);
                     } else {
-                        const float* src = static_cast<const float*>(c.k) + r * D + (tid & 7) * E;
+                        const float* src = static_cast<const float*>(c.k) + r * D + (tid & 7) * 4;
 #pragma unroll
-                        for (int x = 0; x < E; x += 4) load_vec<4>(src + x, kx + x);
+                        for (int x = 0; x < E; x += 4) load_vec<4>(src + x * 8, kx[y] + x);
                     }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < E; ++x) kx[x] = 0.f;
                 }
                 for (int g = 0; g < ng; ++g) {
-                    float d = 0.f;
+                    float d[kN];
 #pragma unroll
-                    for (int x = 0; x < E; ++x) d = fmaf(qs[g][(tid & 7) * E + x], kx[x], d);
+                    for (int y = 0; y < kN; ++y) d[y] = 0.f;
 #pragma unroll
-                    for (int o = 4; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                    if ((tid & 7) == 0) ps[g][j] = r >= 0 ? d * ks : -INFINITY;
+                    for (int x = 0; x < E; x += 4) {
+                        // the lane's elements: E in a row (8-bit rows), else four of every 32
+                        const float4 qv = *reinterpret_cast<const float4*>(&qs[g][E4M3 ? (tid & 7) * E + x : (tid & 7) * 4 + x * 8]);
+#pragma unroll
+                        for (int y = 0; y < kN; ++y) {
+                            d[y] = fmaf(qv.x, kx[y][x], d[y]);
+                            d[y] = fmaf(qv.y, kx[y][x + 1], d[y]);
+                            d[y] = fmaf(qv.z, kx[y][x + 2], d[y]);
+                            d[y] = fmaf(qv.w, kx[y][x + 3], d[y]);
+                        }
+                    }
+#pragma unroll
+                    for (int y = 0; y < kN; ++y) {
+#pragma unroll
+                        for (int o = 4; o; o >>= 1) d[y] += __shfl_xor_sync(0xffffffffu, d[y], o);
+                        const int j = tid / 8 + y * (kThreads / 8);
+                        if ((tid & 7) == 0) ps[g][j] = rows[j] >= 0 ? d[y] * ks[y] : -INFINITY;
+                    }
                 }
             }
             __syncthreads();
-            if (tid < ng) {
-                float m = mrun;
-                for (int j = 0; j < n; ++j) m = fmaxf(m, ps[tid][j]);
-                const float corr = mrun == -INFINITY ? 0.f : exp2f(mrun - m);
-                float sum = 0.f;
-                for (int j = 0; j < kDecodeUnit; ++j) {
-                    const float p = j < n && ps[tid][j] != -INFINITY ? exp2f(ps[tid][j] - m) : 0.f;
-                    sum += p;
-                    ps[tid][j] = p;
+            {  // 16 lanes per head, four keys each
+                const int g = tid >> 4, j = (tid & 15) * 4;
+                const float4 x = *reinterpret_cast<const float4*>(&ps[g][j]);
+                float v[4] = {x.x, x.y, x.z, x.w}, top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    if (j + y >= n || g >= ng) v[y] = -INFINITY;
+                    top = fmaxf(top, v[y]);
                 }
+#pragma unroll
+                for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float m = fmaxf(mrun, top), corr = mrun == -INFINITY ? 0.f : exp2f(mrun - m);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    v[y] = v[y] == -INFINITY ? 0.f : exp2f(v[y] - m);
+                    sum += v[y];
+                }
+#pragma unroll
+                for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                *reinterpret_cast<float4*>(&ps[g][j]) = make_float4(v[0], v[1], v[2], v[3]);
                 lrun = lrun * corr + sum;
                 mrun = m;
-                stats[tid][1] = corr;
+                if ((tid & 15) == 0) stats[g][1] = corr;
             }
             __syncthreads();
 #pragma unroll
@@ -131,30 +167,34 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
                 if (g < ng)
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x) acc[g][x] *= stats[g][1];
-            for (int j = warp; j < n; j += kThreads / 32) {
-                const int64_t r = rows[j];
-                if (r < 0) continue;
-                float vx[D / 32];
-                if constexpr (E4M3) {
-                    const uint8_t* src = static_cast<const uint8_t*>(c.v) + r * D + lane * (D / 32);
+            // values: a warp takes every fourth key, eight on their way at once
+            constexpr int kE = D / 32, kN = 8;
+            for (int j0 = warp; j0 < n; j0 += kN * (kThreads / 32)) {
+                float vx[kN][kE];
 #pragma unroll
-                    for (int x = 0; x < D / 32; x += 2) {
-                        const __half2_raw hv = __nv_cvt_fp8x2_to_halfraw2(
-                            *reinterpret_cast<const __nv_fp8x2_storage_t*>(src + x), __NV_E4M3);
-                        const float2 f = __half22float2(__half2(hv));
-                        vx[x] = f.x * vs[j];
-                        vx[x + 1] = f.y * vs[j];
-                    }
-                } else {
-                    load_vec<D / 32>(static_cast<const float*>(c.v) + r * D + lane * (D / 32), vx);
+                for (int y = 0; y < kN; ++y) {
+                    const int j = j0 + y * (kThreads / 32);
+                    const int64_t r = j < n ? rows[j] : -1;
+#pragma unroll
+                    for (int x = 0; x < kE; ++x) vx[y][x] = 0.f;
+                    if (r < 0) continue;
+                    if constexpr (E4M3) load_e4m3<kE>(static_cast<const uint8_t*>(c.v) + r * D + lane * kE, vx[y]);
+                    else load_vec<kE>(static_cast<const float*>(c.v) + r * D + lane * kE, vx[y]);
                 }
 #pragma unroll
-                for (int g = 0; g < kGroup; ++g)
-                    if (g < ng) {
-                        const float p = ps[g][j];
+                for (int y = 0; y < kN; ++y) {
+                    const int j = min(j0 + y * (kThreads / 32), kDecodeUnit - 1);
+                    const float scale = vs[j];
 #pragma unroll
-                        for (int x = 0; x < D / 32; ++x) acc[g][x] = fmaf(p, vx[x], acc[g][x]);
-                    }
+                    for (int x = 0; x < kE; ++x) vx[y][x] *= scale;
+#pragma unroll
+                    for (int g = 0; g < kGroup; ++g)
+                        if (g < ng) {
+                            const float p = j0 + y * (kThreads / 32) < n ? ps[g][j] : 0.f;
+#pragma unroll
+                            for (int x = 0; x < kE; ++x) acc[g][x] = fmaf(p, vx[y][x], acc[g][x]);
+                        }
+                }
             }
         }
         // join the warps; the block's part of the sequence
@@ -163,9 +203,10 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
             if (g < ng)
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x) osum[warp][g][lane * (D / 32) + x] = acc[g][x];
-        if (tid < ng) {
-            stats[tid][0] = mrun;
-            stats[tid][1] = lrun;
+        __syncthreads();  // the last corrections have been read
+        if ((tid & 15) == 0) {
+            stats[tid >> 4][0] = mrun;
+            stats[tid >> 4][1] = lrun;
         }
         __syncthreads();
         const bool whole = u == useq && e == useq + su;
@@ -180,9 +221,9 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
         }
         if (!whole && tid < ng) {
             float* t = part.st + (slot * A.Hq + kv * A.G + g0 + tid) * 4;
-            t[0] = mrun;
-            t[1] = lrun;
-            t[2] = mrun;
+            t[0] = stats[tid][0];
+            t[1] = stats[tid][1];
+            t[2] = stats[tid][0];
         }
         u = e;
         useq += su;
@@ -210,14 +251,36 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
 // fp16 (11 bits) with the largest product near 1.  bf16 caches: products and
 // weights in bf16 (8 bits, the values' own precision).
 //
+// A warp takes 32 keys at a time (16 of 256 bytes), so that the 12 to 16 warps
+// of an SM keep some 60 KB on their way.
+//
 // References are raised only when a score exceeds them by 2^8 (a vote per
 // tile, no reduction); the weights stay at most 2^8.
 
 constexpr float kLazy = 8.0f;
+constexpr uint32_t kNoRow = 0xffffffffu;
 
-__device__ __forceinline__ uint32_t h2_from_e4m3(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+// Tiles of 16 keys per page, and division by it: i / tiles = i mul >> shift for i < 2^31 (mul = ceil(2^shift /
+// tiles), shift = 31 + ceil(log2 tiles); the excess of mul adds less than 1 / tiles to the quotient).
+struct PageDiv {
+    uint32_t tiles, mul, shift;
+    explicit PageDiv(int page) : tiles((uint32_t)page / 16), shift(31) {
+        while ((1ull << (shift - 31)) < tiles) ++shift;
+        mul = (uint32_t)(((1ull << shift) + tiles - 1) / tiles);
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t i) const { return (uint32_t)(((uint64_t)i * mul) >> shift); }
+};
+__device__ __forceinline__ float ex2(float x) {  // 2 ulp; below 2^-126: 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four e4m3 values to fp16: the first two, the last two.
+__device__ __forceinline__ void h2_from_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -247,14 +310,15 @@ __device__ __forceinline__ float bf16_at(uint32_t w, int hi) { return __uint_as_
 __device__ __forceinline__ float safe_ref(float m) { return m == -INFINITY ? 0.f : m; }
 
 template <bool E4M3, int D>
-__global__ void __launch_bounds__(kThreads, E4M3 ? 4 : 3)
-decode_mma_kernel(AttnDims A, CacheDims C, hla_cache c, const __nv_bfloat16* __restrict__ q, DecodeLine L,
+__global__ void __launch_bounds__(kThreads, D == 64 && E4M3 ? 4 : 3)
+decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_bfloat16* __restrict__ q, DecodeLine L,
                   __nv_bfloat16* __restrict__ out, DecodePart part) {
     constexpr int kRow = D * (E4M3 ? 1 : 2);      // bytes of a cache row
     constexpr int kKp = kRow / 64;                // 16-byte pieces of a key row per lane
     constexpr int kVw = kRow / 32;                // 32-bit words of a value row per lane
     constexpr int kSteps = D / 16, kMt = D / 16;  // k steps of the scores; d tiles of the output
     constexpr int kWarps = kThreads / 32;
+    constexpr int kSub = kRow == 256 ? 1 : 2, kUnit = 16 * kSub * kWarps;  // sub-tiles of 16 keys per warp; keys of a unit
     __shared__ float osum[kWarps][kGroup][D + 4];
     __shared__ float refs[kWarps][kGroup][3];     // M, sum, Mt
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -271,10 +335,8 @@ decode_mma_kernel(AttnDims A, CacheDims C, hla_cache c, const __nv_bfloat16* __r
     const int64_t u1 = (blockIdx.x + 1) * U / nb, u0 = u;
     int64_t useq;
     int s = line_find(L, u, &useq);
-    const int tiles_per_page = C.page / 16;
-
     while (u < u1) {
-        const int64_t len = L.len(s), su = (len + kDecodeUnit - 1) / kDecodeUnit;
+        const int64_t len = L.len(s), su = (len + kUnit - 1) / kUnit;
         if (su == 0) { ++s; continue; }
         const int64_t e = min(u1, useq + su);  // this block's units of the sequence: [u, e)
         // ---- the query, in the order the key pieces are laid out
@@ -323,181 +385,204 @@ decode_mma_kernel(AttnDims A, CacheDims C, hla_cache c, const __nv_bfloat16* __r
         for (int x = 0; x < kMt; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
         float M0 = -INFINITY, M1 = -INFINITY, T0 = -INFINITY, T1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-        // cache row of key 0 of tile i of the sequence; -1: no such tile or page
-        auto page_of = [&](int64_t i) -> int {
-            return i * 16 < len ? __ldg(c.page_table + (int64_t)s * C.max_pages + i / tiles_per_page) : -1;
+        // tiles of 16 keys: the page a tile lies in (-1: past the last key), its cache row (kNoRow: no such page)
+        const uint32_t n_tiles = (uint32_t)((len + 15) / 16);
+        const int32_t* pages = c.page_table + (int64_t)s * C.max_pages;
+        auto page_of = [&](uint32_t i, uint32_t* at) -> int {
+            const uint32_t p = pd.quotient(i);
+            *at = (i - p * pd.tiles) * 16;
+            return i < n_tiles ? __ldg(pages + p) : -1;
         };
-        auto row_of = [&](int64_t i, int page) -> int64_t {
-            if (i * 16 >= len) return -1;
-            if (page < 0 || page >= C.n_pages) {
+        auto row_of = [&](uint32_t i, int page, uint32_t at) -> uint32_t {
+            if (i >= n_tiles) return kNoRow;
+            if ((uint32_t)page >= (uint32_t)C.n_pages) {
                 if (lane == 0) atomicExch(c.err, kErrState);
-                return -1;
+                return kNoRow;
             }
-            return ((int64_t)page * C.Hkv + kv) * C.page + (i % tiles_per_page) * 16;
+            return ((uint32_t)page * C.Hkv + kv) * C.page + at;
         };
-        uint4 kx[2][kKp];
-        uint32_t vx[4][kVw];
-        int ek0 = 0, ek1 = 0, ev0 = 0, ev1 = 0;
-        auto load_k = [&](int64_t row) {
-            if (row < 0) return;
-            const char* p = static_cast<const char*>(c.k) + (row + g) * kRow + t * 16;
+        uint4 kx[kSub][2][kKp];
+        uint32_t vx[kSub][4][kVw];
+        int ex[kSub][4];  // exponent bytes: keys g, g + 8, then values
+        auto load_k = [&](int y, uint32_t row) {
+            if (row == kNoRow) return;
+            const char* p = static_cast<const char*>(c.k) + (size_t)(row + g) * kRow + t * 16;
 #pragma unroll
             for (int i = 0; i < kKp; ++i) {
-                kx[0][i] = __ldcs(reinterpret_cast<const uint4*>(p + i * 64));
-                kx[1][i] = __ldcs(reinterpret_cast<const uint4*>(p + 8 * kRow + i * 64));
+                kx[y][0][i] = __ldcs(reinterpret_cast<const uint4*>(p + i * 64));
+                kx[y][1][i] = __ldcs(reinterpret_cast<const uint4*>(p + 8 * kRow + i * 64));
             }
             if constexpr (E4M3) {
-                ek0 = c.k_exp[row + g];
-                ek1 = c.k_exp[row + g + 8];
-                ev0 = c.v_exp[row + g];
-                ev1 = c.v_exp[row + g + 8];
+                const uint8_t *ke = c.k_exp + (row + g), *ve = c.v_exp + (row + g);
+                ex[y][0] = ke[0];
+                ex[y][1] = ke[8];
+                ex[y][2] = ve[0];
+                ex[y][3] = ve[8];
             }
         };
-        auto load_v = [&](int64_t row, int n) {  // n: keys of the tile; the rows behind them are zeros
-            if (row < 0) return;
+        auto load_v = [&](int y, uint32_t row, int n) {  // n: keys of the tile; the rows behind them are zeros
+            if (row == kNoRow) return;
+            const char* p0 = static_cast<const char*>(c.v) + (size_t)(row + 2 * t) * kRow;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int key = 2 * t + (x & 1) + 8 * (x >> 1);
-                const char* p = static_cast<const char*>(c.v) + (row + key) * kRow;
+                const char* p = p0 + ((x & 1) + 8 * (x >> 1)) * kRow;
                 if constexpr (kVw == 2) {  // 64 one-byte values: 8 bytes per lane
-                    uint2 y = make_uint2(0u, 0u);
-                    if (key < n) y = __ldcs(reinterpret_cast<const uint2*>(p + g * 8));
-                    vx[x][0] = y.x;
-                    vx[x][1] = y.y;
+                    uint2 w = make_uint2(0u, 0u);
+                    if (key < n) w = __ldcs(reinterpret_cast<const uint2*>(p + g * 8));
+                    vx[y][x][0] = w.x;
+                    vx[y][x][1] = w.y;
                 } else {
 #pragma unroll
                     for (int i = 0; i < kVw / 4; ++i) {
-                        uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                        if (key < n) y = __ldcs(reinterpret_cast<const uint4*>(p + i * 128 + g * 16));
-                        vx[x][4 * i] = y.x;
-                        vx[x][4 * i + 1] = y.y;
-                        vx[x][4 * i + 2] = y.z;
-                        vx[x][4 * i + 3] = y.w;
+                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        if (key < n) w = __ldcs(reinterpret_cast<const uint4*>(p + i * 128 + g * 16));
+                        vx[y][x][4 * i] = w.x;
+                        vx[y][x][4 * i + 1] = w.y;
+                        vx[y][x][4 * i + 2] = w.z;
+                        vx[y][x][4 * i + 3] = w.w;
                     }
                 }
             }
         };
-        // tiles of this warp: 4 unit + warp
-        int64_t i = (u - useq) * 4 + warp;
-        const int64_t iend = (e - useq) * 4;
-        int64_t row = row_of(i, page_of(i));
-        int page_next = page_of(i + 4);
-        load_k(row);
-        load_v(row, (int)min((int64_t)16, len - i * 16));
-        for (; i < iend && i * 16 < len; i += 4) {
-            const int n = (int)min((int64_t)16, len - i * 16);
-            const bool more = i + 4 < iend;
-            const int64_t row_next = more ? row_of(i + 4, page_next) : -1;
-            page_next = more ? page_of(i + 8) : -1;
-            const int n_next = (int)min((int64_t)16, len - (i + 4) * 16);
-            if (row >= 0) {
-                float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+        // tiles of this warp: kSub in a row from (4 unit + warp) kSub
+        constexpr uint32_t kStep = kWarps * kSub;
+        uint32_t i = (uint32_t)((u - useq) * kWarps + warp) * kSub;
+        const uint32_t iend = min((uint32_t)(e - useq) * kStep, n_tiles);
+        auto keys_of = [&](uint32_t j) { return (int)min((int64_t)16, len - (int64_t)j * 16); };
+        uint32_t row[kSub], at_next[kSub];
+        int page_next[kSub];
+#pragma unroll
+        for (int y = 0; y < kSub; ++y) {
+            uint32_t at;
+            const int page = page_of(i + y, &at);
+            row[y] = row_of(i + y, page, at);
+            page_next[y] = page_of(i + kStep + y, &at_next[y]);
+            load_k(y, row[y]);
+            load_v(y, row[y], keys_of(i + y));
+        }
+        for (; i < iend; i += kStep) {
+            const bool more = i + kStep < iend;
+            uint32_t row_next[kSub];
+#pragma unroll
+            for (int y = 0; y < kSub; ++y) {
+                row_next[y] = more ? row_of(i + kStep + y, page_next[y], at_next[y]) : kNoRow;
+                if (more) page_next[y] = page_of(i + 2 * kStep + y, &at_next[y]);
+            }
+            // ---- scores of every sub-tile (base-2 logs), and the exponents of its value rows
+            float sc[kSub][4], ve[kSub][2];
+            float h0 = -INFINITY, h1 = -INFINITY, t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < kSub; ++y) {
+                float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+                const int n = row[y] != kNoRow ? keys_of(i + y) : 0;
 #pragma unroll
                 for (int x = 0; x < kKp; ++x) {
-                    const uint32_t a[4] = {kx[0][x].x, kx[0][x].y, kx[0][x].z, kx[0][x].w};
-                    const uint32_t b[4] = {kx[1][x].x, kx[1][x].y, kx[1][x].z, kx[1][x].w};
+                    const uint32_t a[4] = {kx[y][0][x].x, kx[y][0][x].y, kx[y][0][x].z, kx[y][0][x].w};
+                    const uint32_t b[4] = {kx[y][1][x].x, kx[y][1][x].y, kx[y][1][x].z, kx[y][1][x].w};
                     if constexpr (E4M3) {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            mma16816<true>(w & 1 ? sd : sc, h2_from_e4m3(a[w] & 0xffffu), h2_from_e4m3(b[w] & 0xffffu),
-                                           h2_from_e4m3(a[w] >> 16), h2_from_e4m3(b[w] >> 16), qf[x * 4 + w][0],
-                                           qf[x * 4 + w][1]);
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t al, ah, bl, bh;
+                            h2_from_e4m3(a[w], al, ah);
+                            h2_from_e4m3(b[w], bl, bh);
+                            mma16816<true>(w & 1 ? a1 : a0, al, bl, ah, bh, qf[x * 4 + w][0], qf[x * 4 + w][1]);
+                        }
                     } else {
 #pragma unroll
                         for (int w = 0; w < 2; ++w)
-                            mma16816<false>(w & 1 ? sd : sc, a[2 * w], b[2 * w], a[2 * w + 1], b[2 * w + 1],
+                            mma16816<false>(w & 1 ? a1 : a0, a[2 * w], b[2 * w], a[2 * w + 1], b[2 * w + 1],
                                             qf[x * 2 + w][0], qf[x * 2 + w][1]);
                     }
                 }
                 float f0 = 1.f, f1 = 1.f;  // the key rows' powers of two
-                float v0 = 0.f, v1 = 0.f;  // the value rows' exponents
+                ve[y][0] = ve[y][1] = 0.f;
                 if constexpr (E4M3) {
-                    f0 = ek0 ? __uint_as_float((uint32_t)ek0 << 23) : __uint_as_float(0x400000u);
-                    f1 = ek1 ? __uint_as_float((uint32_t)ek1 << 23) : __uint_as_float(0x400000u);
-                    v0 = (float)(ev0 - 127);
-                    v1 = (float)(ev1 - 127);
+                    f0 = ex[y][0] ? __uint_as_float((uint32_t)ex[y][0] << 23) : __uint_as_float(0x400000u);
+                    f1 = ex[y][1] ? __uint_as_float((uint32_t)ex[y][1] << 23) : __uint_as_float(0x400000u);
+                    ve[y][0] = (float)(ex[y][2] - 127);
+                    ve[y][1] = (float)(ex[y][3] - 127);
                 }
-                load_k(row_next);
+                load_k(y, row_next[y]);
                 const bool on0 = g < n, on1 = g + 8 < n;
-                float x0 = on0 ? (sc[0] + sd[0]) * f0 * qs0 : -INFINITY, x1 = on0 ? (sc[1] + sd[1]) * f0 * qs1 : -INFINITY;
-                float x2 = on1 ? (sc[2] + sd[2]) * f1 * qs0 : -INFINITY, x3 = on1 ? (sc[3] + sd[3]) * f1 * qs1 : -INFINITY;
-                float h0 = fmaxf(x0, x2), h1 = fmaxf(x1, x3);
-                float t0 = h0, t1 = h1;
+                sc[y][0] = on0 ? (a0[0] + a1[0]) * f0 * qs0 : -INFINITY;
+                sc[y][1] = on0 ? (a0[1] + a1[1]) * f0 * qs1 : -INFINITY;
+                sc[y][2] = on1 ? (a0[2] + a1[2]) * f1 * qs0 : -INFINITY;
+                sc[y][3] = on1 ? (a0[3] + a1[3]) * f1 * qs1 : -INFINITY;
+                h0 = fmaxf(h0, fmaxf(sc[y][0], sc[y][2]));
+                h1 = fmaxf(h1, fmaxf(sc[y][1], sc[y][3]));
                 if constexpr (E4M3) {
-                    t0 = fmaxf(x0 + v0, x2 + v1);
-                    t1 = fmaxf(x1 + v0, x3 + v1);
+                    t0 = fmaxf(t0, fmaxf(sc[y][0] + ve[y][0], sc[y][2] + ve[y][1]));
+                    t1 = fmaxf(t1, fmaxf(sc[y][1] + ve[y][0], sc[y][3] + ve[y][1]));
                 }
-                bool grow = h0 > M0 + kLazy || h1 > M1 + kLazy;
-                if constexpr (E4M3) grow |= t0 > T0 + kLazy || t1 > T1 + kLazy;
-                if (__any_sync(0xffffffffu, grow)) {
+            }
+            bool grow = h0 > M0 + kLazy || h1 > M1 + kLazy;
+            if constexpr (E4M3) grow |= t0 > T0 + kLazy || t1 > T1 + kLazy;
+            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                    for (int sh = 4; sh < 32; sh <<= 1) {
-                        h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, sh));
-                        h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, sh));
-                        if constexpr (E4M3) {
-                            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, sh));
-                            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, sh));
-                        }
-                    }
-                    const float m0 = fmaxf(M0, h0), m1 = fmaxf(M1, h1);
-                    l0 *= M0 == -INFINITY ? 0.f : exp2f(M0 - m0);
-                    l1 *= M1 == -INFINITY ? 0.f : exp2f(M1 - m1);
-                    M0 = m0;
-                    M1 = m1;
-                    float r0, r1;
+                for (int sh = 4; sh < 32; sh <<= 1) {
+                    h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, sh));
+                    h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, sh));
                     if constexpr (E4M3) {
-                        const float y0 = fmaxf(T0, t0), y1 = fmaxf(T1, t1);
-                        r0 = T0 == -INFINITY ? 0.f : exp2f(T0 - y0);
-                        r1 = T1 == -INFINITY ? 0.f : exp2f(T1 - y1);
-                        T0 = y0;
-                        T1 = y1;
-                    } else {
-                        r0 = T0 == -INFINITY ? 0.f : exp2f(T0 - m0);
-                        r1 = T1 == -INFINITY ? 0.f : exp2f(T1 - m1);
-                        T0 = m0;
-                        T1 = m1;
-                    }
-#pragma unroll
-                    for (int x = 0; x < kMt; ++x) {
-                        o[x][0] *= r0;
-                        o[x][1] *= r1;
-                        o[x][2] *= r0;
-                        o[x][3] *= r1;
+                        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, sh));
+                        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, sh));
                     }
                 }
-                const float ref0 = safe_ref(M0), ref1 = safe_ref(M1);
-                float p0 = exp2f(x0 - ref0), p1 = exp2f(x1 - ref1), p2 = exp2f(x2 - ref0), p3 = exp2f(x3 - ref1);
+                const float m0 = fmaxf(M0, h0), m1 = fmaxf(M1, h1);
+                const float n0 = E4M3 ? fmaxf(T0, t0) : m0, n1 = E4M3 ? fmaxf(T1, t1) : m1;
+                l0 *= M0 == -INFINITY ? 0.f : exp2f(M0 - m0);
+                l1 *= M1 == -INFINITY ? 0.f : exp2f(M1 - m1);
+                const float r0 = T0 == -INFINITY ? 0.f : exp2f(T0 - n0), r1 = T1 == -INFINITY ? 0.f : exp2f(T1 - n1);
+                M0 = m0;
+                M1 = m1;
+                T0 = n0;
+                T1 = n1;
+#pragma unroll
+                for (int x = 0; x < kMt; ++x) {
+                    o[x][0] *= r0;
+                    o[x][1] *= r1;
+                    o[x][2] *= r0;
+                    o[x][3] *= r1;
+                }
+            }
+            // ---- weights, and the values they go to
+            const float ref0 = safe_ref(M0), ref1 = safe_ref(M1), ret0 = safe_ref(T0), ret1 = safe_ref(T1);
+#pragma unroll
+            for (int y = 0; y < kSub; ++y) {
+                float p0 = ex2(sc[y][0] - ref0), p1 = ex2(sc[y][1] - ref1);
+                float p2 = ex2(sc[y][2] - ref0), p3 = ex2(sc[y][3] - ref1);
                 l0 += p0 + p2;
                 l1 += p1 + p3;
                 if constexpr (E4M3) {
-                    const float y0 = safe_ref(T0), y1 = safe_ref(T1);
-                    p0 = exp2f(x0 + v0 - y0);
-                    p1 = exp2f(x1 + v0 - y1);
-                    p2 = exp2f(x2 + v1 - y0);
-                    p3 = exp2f(x3 + v1 - y1);
+                    p0 = ex2(sc[y][0] + (ve[y][0] - ret0));
+                    p1 = ex2(sc[y][1] + (ve[y][0] - ret1));
+                    p2 = ex2(sc[y][2] + (ve[y][1] - ret0));
+                    p3 = ex2(sc[y][3] + (ve[y][1] - ret1));
                 }
                 const uint32_t b0 = transpose8(pack2<E4M3>(p0, p1)), b1 = transpose8(pack2<E4M3>(p2, p3));
+                if (row[y] != kNoRow) {
 #pragma unroll
-                for (int w = 0; w < kVw; ++w) {
-                    if constexpr (E4M3) {
+                    for (int w = 0; w < kVw; ++w) {
+                        if constexpr (E4M3) {
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint32_t lo = __byte_perm(vx[0][w], vx[1][w], y ? 0x7362 : 0x5140);
-                            const uint32_t hi = __byte_perm(vx[2][w], vx[3][w], y ? 0x7362 : 0x5140);
-                            mma16816<true>(o[2 * w + y], h2_from_e4m3(lo & 0xffffu), h2_from_e4m3(lo >> 16),
-                                           h2_from_e4m3(hi & 0xffffu), h2_from_e4m3(hi >> 16), b0, b1);
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t sel = z ? 0x7362 : 0x5140;
+                                uint32_t a0, a1, a2, a3;
+                                h2_from_e4m3(__byte_perm(vx[y][0][w], vx[y][1][w], sel), a0, a1);
+                                h2_from_e4m3(__byte_perm(vx[y][2][w], vx[y][3][w], sel), a2, a3);
+                                mma16816<true>(o[2 * w + z], a0, a1, a2, a3, b0, b1);
+                            }
+                        } else {
+                            mma16816<false>(o[w], __byte_perm(vx[y][0][w], vx[y][1][w], 0x5410),
+                                            __byte_perm(vx[y][0][w], vx[y][1][w], 0x7632),
+                                            __byte_perm(vx[y][2][w], vx[y][3][w], 0x5410),
+                                            __byte_perm(vx[y][2][w], vx[y][3][w], 0x7632), b0, b1);
                         }
-                    } else {
-                        mma16816<false>(o[w], __byte_perm(vx[0][w], vx[1][w], 0x5410),
-                                        __byte_perm(vx[0][w], vx[1][w], 0x7632), __byte_perm(vx[2][w], vx[3][w], 0x5410),
-                                        __byte_perm(vx[2][w], vx[3][w], 0x7632), b0, b1);
                     }
                 }
-            } else {
-                load_k(row_next);
+                load_v(y, row_next[y], keys_of(i + kStep + y));
+                row[y] = row_next[y];
             }
-            load_v(row_next, n_next);
-            row = row_next;
         }
         // ---- join the warps
 #pragma unroll
@@ -570,43 +655,77 @@ decode_mma_kernel(AttnDims A, CacheDims C, hla_cache c, const __nv_bfloat16* __r
 
 // ---- join -------------------------------------------------------------------
 
-// Sequences cut over several blocks: their slots added in order (fixed, so
-// results do not depend on timing); sequences without keys: zeros.
-template <typename T>
-__global__ void __launch_bounds__(128)
+// Sequences cut over several blocks: W warps per sequence and query head take
+// the slots in turn, four in flight each, then are joined in order (fixed, so results do not depend on timing).  Sequences without
+// keys: zeros.
+constexpr int kJoinWarps = 8;
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(kJoinWarps * 32)
 decode_join_kernel(AttnDims A, DecodeLine L, int n_blocks, DecodePart part, T* __restrict__ out) {
-    const int s = blockIdx.x;
+    constexpr int E = D / 32;
+    __shared__ float osum[W][D], lsum[W];
+    const int s = blockIdx.x, lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
+    const int h = W == 1 ? blockIdx.y * kJoinWarps + (threadIdx.x >> 5) : blockIdx.y;
+    if (h >= A.Hq) return;
     int64_t first;
     const int64_t U = line_units(L, s, &first), n = L.units(s);
     pdl_wait();
-    for (int h = blockIdx.y * 4 + (threadIdx.x >> 5); h < A.Hq; h += gridDim.y * 4) {
-        const int lane = threadIdx.x & 31;
-        T* dst = out + ((int64_t)s * A.Hq + h) * A.d;
-        if (n == 0) {
-            for (int x = lane; x < A.d; x += 32) dst[x] = from_f32<T>(0.f);
-            continue;
-        }
-        const int64_t nb = min((int64_t)n_blocks, U);
-        const int64_t c0 = ((first + 1) * nb - 1) / U, c1 = ((first + n) * nb - 1) / U;
-        if (c0 == c1) continue;  // finished by its block
-        auto slot = [&](int64_t c) { return 2 * c + (c * U / nb < first ? 1 : 0); };
-        float m = -INFINITY;
-        for (int64_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, part.st[(slot(c) * A.Hq + h) * 4]);
+    T* dst = out + ((int64_t)s * A.Hq + h) * D;
+    if (n == 0) {
+        for (int x = warp * 32 + lane; x < D; x += W * 32) dst[x] = from_f32<T>(0.f);
+        return;
+    }
+    const int64_t nb = min((int64_t)n_blocks, U);
+    const int c0 = (int)(((first + 1) * nb - 1) / U), c1 = (int)(((first + n) * nb - 1) / U);
+    if (c0 == c1) return;  // finished by its block
+    // slot of block c: 2 c, or 2 c + 1 for the one that reached the sequence from another
+    const int late = c0 * U / nb < first ? 1 : 0;
+    auto at = [&](int c) { return (int64_t)(2 * c + (c == c0 ? late : 0)) * A.Hq + h; };
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, __ldg(part.st + at(c) * 4));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-        const int per = A.d / 32;
-        for (int64_t c = c0; c <= c1; ++c) {
-            const int64_t i = slot(c) * A.Hq + h;
-            const float4 st = *reinterpret_cast<const float4*>(part.st + i * 4);
-            if (st.y == 0.f) continue;  // no keys
-            l = fmaf(exp2f(st.x - m), st.y, l);
-            const float w = exp2f(st.z - m);
-            const float* o = part.o + i * A.d + lane * per;
-            for (int x = 0; x < per; ++x) acc[x] = fmaf(w, o[x], acc[x]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[E], l = 0.f;
+#pragma unroll
+    for (int x = 0; x < E; ++x) acc[x] = 0.f;
+    for (int c = c0 + warp; c <= c1; c += 4 * W) {
+        float4 st[4];
+        float o[4][E];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            st[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c + y * W > c1) continue;
+            const int64_t i = at(c + y * W);
+            st[y] = __ldg(reinterpret_cast<const float4*>(part.st + i * 4));
+            load_vec<E>(part.o + i * D + lane * E, o[y]);
         }
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        for (int x = 0; x < per; ++x) dst[lane * per + x] = from_f32<T>(acc[x] * inv);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if (st[y].y == 0.f) continue;  // no keys
+            l = fmaf(exp2f(st[y].x - m), st[y].y, l);
+            const float w = exp2f(st[y].z - m);
+#pragma unroll
+            for (int x = 0; x < E; ++x) acc[x] = fmaf(w, o[y][x], acc[x]);
+        }
+    }
+    if constexpr (W == 1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int x = 0; x < E; ++x) dst[lane * E + x] = from_f32<T>(acc[x] * inv);
+    } else {
+#pragma unroll
+        for (int x = 0; x < E; ++x) osum[warp][lane * E + x] = acc[x];
+        if (lane == 0) lsum[warp] = l;
+        __syncthreads();
+        if (threadIdx.x < D) {
+            float o = 0.f, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                o += osum[w][threadIdx.x];
+                sum += lsum[w];
+            }
+            dst[threadIdx.x] = from_f32<T>(sum == 0.f ? 0.f : o / sum);
+        }
     }
 }
 
@@ -635,10 +754,14 @@ cudaError_t launch_attention_decode(const AttnDims& A, const CacheDims& C, bool 
     if (e != cudaSuccess) return e;
     n_sm = std::min(n_sm, kMaxSm);
     const int groups = (A.G + kGroup - 1) / kGroup;
-    const DecodeLine L = {lens, A.n_seqs, (int64_t)C.max_pages * C.page};
+    // keys of a unit: what the kernel's four warps take at a time
+    const int unit = sizeof(T) == 4 || (A.d == 128 && !e4m3) ? kDecodeUnit : 2 * kDecodeUnit;
+    // a table beyond 2^31 tiles of 16 positions is more than any memory holds: positions past that are cut as well
+    const DecodeLine L = {lens, A.n_seqs, std::min((int64_t)C.max_pages * C.page, ((int64_t)INT32_MAX - 4096) * 16), unit};
+    const PageDiv pd(C.page);
     int n = 0;
     DecodePart part = {};
-    auto run = [&](auto kernel, DeviceCache& occupancy) {
+    auto run = [&](auto kernel, DeviceCache& occupancy, auto... page) {
         int resident = 0;
         cudaError_t r = device_cached(occupancy, &resident, [&](int, int* v) {
             return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kernel, kThreads, 0);
@@ -646,7 +769,8 @@ cudaError_t launch_attention_decode(const AttnDims& A, const CacheDims& C, bool 
         if (r != cudaSuccess) return r;
         n = blocks_per_head(n_sm, std::max(1, std::min(resident, kMaxResident)), A.Hkv, groups);
         part = {ws, ws + 2 * (size_t)n * A.Hq * A.d};
-        kernel<<<dim3((unsigned)n, (unsigned)A.Hkv, (unsigned)groups), kThreads, 0, st>>>(A, C, c, q, L, out, part);
+        kernel<<<dim3((unsigned)n, (unsigned)A.Hkv, (unsigned)groups), kThreads, 0, st>>>(A, C, page..., c, q, L,
+                                                                                                 out, part);
         return cudaGetLastError();
     };
     static DeviceCache occ[4];
@@ -657,13 +781,19 @@ cudaError_t launch_attention_decode(const AttnDims& A, const CacheDims& C, bool 
             e = e4m3 ? run(decode_f32_kernel<true, 64>, occ[2]) : run(decode_f32_kernel<false, 64>, occ[3]);
     } else {
         if (A.d == 128)
-            e = e4m3 ? run(decode_mma_kernel<true, 128>, occ[0]) : run(decode_mma_kernel<false, 128>, occ[1]);
+            e = e4m3 ? run(decode_mma_kernel<true, 128>, occ[0], pd) : run(decode_mma_kernel<false, 128>, occ[1], pd);
         else
-            e = e4m3 ? run(decode_mma_kernel<true, 64>, occ[2]) : run(decode_mma_kernel<false, 64>, occ[3]);
+            e = e4m3 ? run(decode_mma_kernel<true, 64>, occ[2], pd) : run(decode_mma_kernel<false, 64>, occ[3], pd);
     }
     if (e != cudaSuccess) return e;
-    LaunchCfg lc(dim3((unsigned)A.n_seqs, (unsigned)std::min(65535, (A.Hq + 3) / 4)), dim3(128), 0, st, true);
-    return cudaLaunchKernelEx(&lc.cfg, decode_join_kernel<T>, A, L, n, part, out);
+    // a sequence of average length lies in n / n_seqs + 2 blocks or fewer: with few, a warp adds them; with many, a
+    // block does (one sequence of 131072 keys in 57 blocks: join 35 -> 4 us; 64 sequences of 100: 16 -> 12 us in all)
+    const bool few = n / A.n_seqs + 2 <= 8;
+    LaunchCfg lc(dim3((unsigned)A.n_seqs, few ? (unsigned)((A.Hq + kJoinWarps - 1) / kJoinWarps) : (unsigned)A.Hq),
+                 dim3(kJoinWarps * 32), 0, st, true);
+    auto join = [&](auto kernel) { return cudaLaunchKernelEx(&lc.cfg, kernel, A, L, n, part, out); };
+    if (A.d == 128) return few ? join(decode_join_kernel<T, 128, 1>) : join(decode_join_kernel<T, 128, kJoinWarps>);
+    return few ? join(decode_join_kernel<T, 64, 1>) : join(decode_join_kernel<T, 64, kJoinWarps>);
 }
 template cudaError_t launch_attention_decode<float>(const AttnDims&, const CacheDims&, bool, const hla_cache&,
                                                     const float*, const int64_t*, float*, float*, cudaStream_t);

@@ -1,7 +1,7 @@
 // How a decode step's keys are cut over the thread blocks, shared by its
 // kernels and the join.
 //
-// The keys of all sequences, in units of 64, form one line of U units; with n
+// The keys of all sequences, in units of 64 to 256, form one line of U units; with n
 // blocks (at most U: the rest leave at once) block c takes units [c U / n,
 // (c + 1) U / n) of it, for one kv head.  Blocks are equally
 // loaded whatever the lengths, and only a block's first and last sequence can
@@ -16,15 +16,14 @@
 
 namespace hla {
 
-constexpr int kDecodeUnit = 64;
-
 struct DecodeLine {
     const int64_t* lens;
     int n_seqs;
     int64_t cap;  // positions a page table can hold
+    int unit;     // keys of a unit
     __device__ __forceinline__ int64_t len(int s) const { return clamp_i64(__ldg(lens + s), 0, cap); }
     __device__ __forceinline__ int64_t units(int s) const {
-        return s < n_seqs ? (len(s) + kDecodeUnit - 1) / kDecodeUnit : 0;
+        return s < n_seqs ? (len(s) + unit - 1) / unit : 0;
     }
 };
 
