@@ -7,9 +7,11 @@
 // it.  (The relative step of a floating point value does not depend on the
 // scale; a full-precision scale would gain at most one bit of range.)
 //
-// Memory bound: d / 8 lanes hold a row, 8 values each (16-byte loads of bf16
-// rows, 8-byte stores), the largest magnitude by shuffles; every thread has
-// four rows in flight.
+// Memory bound: a block takes a few tokens; one thread per token finds its
+// sequence and page, then d / 8 lanes hold a row, 8 values each (16-byte loads
+// of bf16 rows, 8-byte stores), the largest magnitude by shuffles; every thread
+// has four rows in flight.  Per-row searches and 64-bit divisions in place of
+// the per-token step took three times as long.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -66,11 +68,11 @@ template <> struct Row8<float> {
     }
 };
 
-// The cache row of packed token t and head h, or -1 (out of range, flagged by
-// one head; or behind the last sequence).
-__device__ __forceinline__ int64_t cache_row(const CacheDims& C, const hla_cache& c, const int32_t* __restrict__ cu,
-                                             const int64_t* __restrict__ start, int64_t t, int h, bool flag,
-                                             bool* listed) {
+// Where packed token t goes: the cache row of head 0 (head h: h pages' rows of
+// one head further, h * page), or -1 (out of range, flagged); listed: whether
+// it belongs to a sequence at all.
+__device__ __forceinline__ int64_t token_row(const CacheDims& C, const hla_cache& c, const int32_t* __restrict__ cu,
+                                             const int64_t* __restrict__ start, int64_t t, bool* listed) {
     const int s = seq_of_token(cu, C.n_seqs, t);
     int64_t a, n;
     seq_range(cu, s, C.total, &a, &n);
@@ -80,10 +82,10 @@ __device__ __forceinline__ int64_t cache_row(const CacheDims& C, const hla_cache
     int page = -1;
     if (p >= 0 && p / C.page < C.max_pages) page = __ldg(c.page_table + (int64_t)s * C.max_pages + p / C.page);
     if (page < 0 || page >= C.n_pages) {
-        if (flag) atomicExch(c.err, kErrState);
+        atomicExch(c.err, kErrState);
         return -1;
     }
-    return ((int64_t)page * C.Hkv + h) * C.page + p % C.page;
+    return (int64_t)page * C.Hkv * C.page + p % C.page;
 }
 
 // Smallest e >= -127 with top <= 448 2^e (top finite, >= 0), from the bits.
@@ -97,15 +99,25 @@ __device__ __forceinline__ float pow2(int e) {  // -127 <= e <= 127
 }
 
 // d / 8 consecutive lanes per row; rows of a token: Hkv of k, then Hkv of v.
+constexpr int kMaxTokens = 32;  // tokens of a block
 template <typename T, bool E4M3, bool READ, int LPR>
 __global__ void __launch_bounds__(kThreads)
-cache_kernel(CacheDims C, hla_cache c, T* k, T* v, const int32_t* __restrict__ cu, const int64_t* __restrict__ start) {
-    constexpr int D = LPR * 8;
-    const int lane8 = (threadIdx.x % LPR) * 8;
-    const int64_t rows = C.total * 2 * C.Hkv, groups = (int64_t)gridDim.x * (kThreads / LPR);
+cache_kernel(CacheDims C, hla_cache c, T* k, T* v, const int32_t* __restrict__ cu, const int64_t* __restrict__ start,
+             int tokens) {
+    constexpr int D = LPR * 8, kRows = kThreads / LPR;  // rows the block handles at once
+    __shared__ int64_t base[kMaxTokens];                // cache row of head 0 (-1: none)
+    __shared__ bool listed[kMaxTokens];
+    const int lane8 = (threadIdx.x % LPR) * 8, per = 2 * C.Hkv;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int nt = (int)min((int64_t)tokens, C.total - t0), rows = nt * per;
     if (blockIdx.x == 0) attn_check_table(cu, C.n_seqs, C.total, c.err);
-    const int64_t base = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-    for (int64_t r0 = base; r0 - base < rows; r0 += groups * kBatch) {  // whole block together
+    if ((int)threadIdx.x < nt) {
+        bool in;
+        base[threadIdx.x] = token_row(C, c, cu, start, t0 + threadIdx.x, &in);
+        listed[threadIdx.x] = in;
+    }
+    __syncthreads();
+    for (int r0 = threadIdx.x / LPR; r0 - (int)(threadIdx.x / LPR) < rows; r0 += kRows * kBatch) {  // whole block together
         Row8<T> x[kBatch];
         int64_t at[kBatch], own[kBatch];  // cache row (-1: none), row of k or v (-1: none)
         uint2 q8[kBatch];
@@ -113,16 +125,14 @@ cache_kernel(CacheDims C, hla_cache c, T* k, T* v, const int32_t* __restrict__ c
         bool isv[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int64_t r = r0 + i * groups;
+            const int r = r0 + i * kRows;
             at[i] = own[i] = -1;
             isv[i] = false;
             if (r >= rows) continue;
-            const int64_t t = r / (2 * C.Hkv);
-            const int hh = (int)(r - t * 2 * C.Hkv), h = hh % C.Hkv;
+            const int t = r / per, hh = r - t * per, h = hh < C.Hkv ? hh : hh - C.Hkv;
             isv[i] = hh >= C.Hkv;
-            bool listed;
-            at[i] = cache_row(C, c, cu, start, t, h, hh == 0, &listed);
-            if (listed) own[i] = t * C.Hkv + h;
+            if (base[t] >= 0) at[i] = base[t] + (int64_t)h * C.page;
+            if (listed[t]) own[i] = (t0 + t) * C.Hkv + h;
             if constexpr (!READ) {
                 if (at[i] >= 0) x[i].load((isv[i] ? v : k) + own[i] * D + lane8);
             } else if (at[i] >= 0) {
@@ -198,12 +208,13 @@ cudaError_t launch_cache(const CacheDims& C, bool e4m3, const hla_cache& c, T* k
     cudaError_t e = device_cached(cache, &n_sm, [](int dev, int* x) { return sm_count(dev, x); });
     if (e != cudaSuccess) return e;
     if (C.total <= 0) return cudaSuccess;
-    const int lpr = C.d / 8;
-    const int64_t rows = C.total * 2 * C.Hkv, per_block = kThreads / lpr;
-    // at most eight blocks per SM; small calls one row per group, so that no SM waits for another's batch
-    const unsigned grid = (unsigned)std::min<int64_t>((rows + per_block - 1) / per_block, (int64_t)n_sm * 8);
+    // Tokens per block: four batches of rows for every thread, fewer where that would leave SMs without a block.
+    const int at_once = kThreads / (C.d / 8) * kBatch;  // rows in flight in a block
+    const int64_t want = std::max<int64_t>(1, 4 * at_once / (2 * C.Hkv)), spread = std::max<int64_t>(1, C.total / (2 * n_sm));
+    const int tokens = (int)std::min<int64_t>(kMaxTokens, std::min(want, spread));
+    const int64_t blocks = (C.total + tokens - 1) / tokens;
     auto run = [&](auto kernel) {
-        kernel<<<grid, kThreads, 0, st>>>(C, c, k, v, cu, start);
+        kernel<<<(unsigned)blocks, kThreads, 0, st>>>(C, c, k, v, cu, start, tokens);
         return cudaGetLastError();
     };
     if (C.d == 128) return e4m3 ? run(cache_kernel<T, true, READ, 16>) : run(cache_kernel<T, false, READ, 16>);
