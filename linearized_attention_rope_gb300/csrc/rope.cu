@@ -8,7 +8,9 @@
 //
 // Memory bound: every element is read and written once.  A block takes a few
 // tokens: it forms their r/2 sines and cosines once in shared memory, for all
-// heads, then streams 16-byte pieces, four in flight per thread.
+// heads; then a thread keeps one 16-byte place of the head and walks the
+// (token, head) pairs, a few in flight.  (32768 tokens, 40 heads of 128, bf16:
+// finding token and head by division and holding both layouts' code, 221 us.)
 #include <algorithm>
 
 #include "attention.cuh"
@@ -18,18 +20,18 @@ namespace hla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // pieces in flight per thread
 
-template <typename T, int V> struct alignas(V * sizeof(T)) PieceV { T x[V]; };
+template <typename T, int V> struct alignas(V * sizeof(T)) Piece { T x[V]; };
 
-// One unit: V pairs (half layout: V elements of each side; interleaved: 2 V
-// consecutive elements), or V or 2 V elements that pass through.
-template <typename T, int V>
+// Sines of pair i V + j: cs[(token V + j) (r / 2 / V) + i], so that neighbouring threads read neighbouring words.
+// IL: interleaved pairs; a thread's V pairs are 2 V elements in a row, else V elements of each half.
+template <typename T, int V, bool IL>
 __global__ void __launch_bounds__(kThreads)
 rope_kernel(const __grid_constant__ RopeDims R, const T* q, const T* k, const int64_t* __restrict__ pos, T* qo,
             T* ko, int tokens, int heads_per_block) {
-    extern __shared__ float2 cs[];  // [tokens][r / 2]
-    const int half = R.r / 2;
+    constexpr int kBatch = V == 8 ? 2 : 4;  // pairs of pieces in flight
+    extern __shared__ float2 cs[];
+    const int half = R.r / 2, places = half / V;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int nt = (int)min((int64_t)tokens, R.total - t0);
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
@@ -37,91 +39,96 @@ rope_kernel(const __grid_constant__ RopeDims R, const T* q, const T* k, const in
         const uint64_t turn = (uint64_t)__ldg(pos + t0 + t) * R.freq[j];
         float s, c;
         sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-        cs[i] = make_float2(c * R.gain, s * R.gain * (float)R.sign);
+        cs[(t * V + j % V) * places + j / V] = make_float2(c * R.gain, s * R.gain * (float)R.sign);
     }
     __syncthreads();
-    // units of a head: half / V rotated, then the copied rest
-    using P = PieceV<T, V>;
+    using P = Piece<T, V>;
     const int h0 = blockIdx.y * heads_per_block, nh = min(heads_per_block, R.Hq + R.Hkv - h0);
-    const int ur = half / V, uc = (R.d - R.r) / V, per_head = ur + uc;
-    const int units = nt * nh * per_head;
-    for (int u0 = threadIdx.x; u0 < units; u0 += kThreads * kBatch) {
-        P a[kBatch], b[kBatch];
-        T* dst[kBatch];
-        int at[kBatch], gap[kBatch];  // cos/sin index (-1: copied); distance of the second piece (0: none)
+    auto source = [&](int t, int h) {
+        return h < R.Hq ? q + (t0 + t) * R.q_in + (int64_t)h * R.d : k + (t0 + t) * R.k_in + (int64_t)(h - R.Hq) * R.d;
+    };
+    auto target = [&](int t, int h) {
+        return h < R.Hq ? qo + (t0 + t) * R.q_out + (int64_t)h * R.d : ko + (t0 + t) * R.k_out + (int64_t)(h - R.Hq) * R.d;
+    };
+    {
+        const int step = kThreads / places, i = threadIdx.x % places;  // heads a block takes at once; this thread's place
+        const int e = IL ? 2 * i * V : i * V, gap = IL ? V : half;
+        int h = threadIdx.x / places, t = h < step ? h / nh : nt;
+        h -= t * nh;
+        while (t < nt) {
+            P a[kBatch], b[kBatch];
+            T* dst[kBatch];
+            int tt[kBatch];
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            const int u = u0 + x * kThreads;
-            gap[x] = -1;
-            if (u >= units) continue;
-            const int th = u / per_head, i = u - th * per_head, t = th / nh, h = h0 + th - t * nh;
-            const bool isq = h < R.Hq;
-            const int64_t row = t0 + t;
-            const T* src = isq ? q + row * R.q_in + (int64_t)h * R.d : k + row * R.k_in + (int64_t)(h - R.Hq) * R.d;
-            dst[x] = isq ? qo + row * R.q_out + (int64_t)h * R.d : ko + row * R.k_out + (int64_t)(h - R.Hq) * R.d;
-            const bool rot = i < ur;
-            const int e = rot ? (R.interleaved ? 2 * i * V : i * V) : R.r + (i - ur) * V;
-            at[x] = rot ? t * half + i * V : -1;
-            gap[x] = rot ? (R.interleaved ? V : half) : 0;
-            dst[x] += e;
-            a[x] = *reinterpret_cast<const P*>(src + e);
-            if (rot) b[x] = *reinterpret_cast<const P*>(src + e + gap[x]);
-        }
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            if (gap[x] < 0) continue;
-            if (at[x] >= 0) {
-                T lo[V], hi[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float2 w = cs[at[x] + j];
-                    const bool il = R.interleaved != 0;
-                    // interleaved: the 2 V elements a[0..V) b[0..V) are V pairs in a row
-                    const T ea = il ? (2 * j < V ? a[x].x[(2 * j) % V] : b[x].x[(2 * j) % V]) : a[x].x[j];
-                    const T eb = il ? (2 * j + 1 < V ? a[x].x[(2 * j + 1) % V] : b[x].x[(2 * j + 1) % V]) : b[x].x[j];
-                    const float fa = to_f32(ea), fb = to_f32(eb);
-                    lo[j] = from_f32<T>(fa * w.x - fb * w.y);
-                    hi[j] = from_f32<T>(fb * w.x + fa * w.y);
+            for (int x = 0; x < kBatch; ++x) {
+                tt[x] = t;
+                if (t < nt) {
+                    const T* src = source(t, h0 + h) + e;
+                    dst[x] = target(t, h0 + h) + e;
+                    a[x] = *reinterpret_cast<const P*>(src);
+                    b[x] = *reinterpret_cast<const P*>(src + gap);
                 }
+                h += step;
+                while (h >= nh && t < nt) {
+                    h -= nh;
+                    ++t;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                if (tt[x] >= nt) continue;
+                P lo, hi;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    if (R.interleaved) {
-                        a[x].x[j] = j & 1 ? hi[j / 2] : lo[j / 2];
-                        b[x].x[j] = (V + j) & 1 ? hi[(V + j) / 2] : lo[(V + j) / 2];
+                    const float2 w = cs[(tt[x] * V + j) * places + i];
+                    // interleaved: elements a[0..V) b[0..V) are V pairs in a row
+                    const T ea = IL ? (2 * j < V ? a[x].x[(2 * j) % V] : b[x].x[(2 * j) % V]) : a[x].x[j];
+                    const T eb = IL ? (2 * j + 1 < V ? a[x].x[(2 * j + 1) % V] : b[x].x[(2 * j + 1) % V]) : b[x].x[j];
+                    const float fa = to_f32(ea), fb = to_f32(eb);
+                    const T ra = from_f32<T>(fa * w.x - fb * w.y), rb = from_f32<T>(fb * w.x + fa * w.y);
+                    if (IL) {
+                        if (2 * j < V) lo.x[(2 * j) % V] = ra; else hi.x[(2 * j) % V] = ra;
+                        if (2 * j + 1 < V) lo.x[(2 * j + 1) % V] = rb; else hi.x[(2 * j + 1) % V] = rb;
                     } else {
-                        a[x].x[j] = lo[j];
-                        b[x].x[j] = hi[j];
+                        lo.x[j] = ra;
+                        hi.x[j] = rb;
                     }
                 }
-                *reinterpret_cast<P*>(dst[x] + gap[x]) = b[x];
+                *reinterpret_cast<P*>(dst[x]) = lo;
+                *reinterpret_cast<P*>(dst[x] + gap) = hi;
             }
-            *reinterpret_cast<P*>(dst[x]) = a[x];
         }
+    }
+    // the elements past the rotated ones, unless they are in place already
+    const int copies = (R.d - R.r) / V;
+    if (copies == 0 || (qo == q && ko == k)) return;
+    for (int u = threadIdx.x; u < nt * nh * copies; u += kThreads) {
+        const int th = u / copies, t = th / nh, h = h0 + th - t * nh, e = R.r + (u - th * copies) * V;
+        const T* src = source(t, h) + e;
+        T* dst = target(t, h) + e;
+        if (dst != src) *reinterpret_cast<P*>(dst) = *reinterpret_cast<const P*>(src);
     }
 }
 
-template <typename T, int V>
+template <typename T, int V, bool IL>
 cudaError_t launch(const RopeDims& R, const T* q, const T* k, const int64_t* pos, T* qo, T* ko, cudaStream_t st) {
     static DeviceCache cache;
     int n_sm = 0;
     cudaError_t e = device_cached(cache, &n_sm, [](int dev, int* v) { return sm_count(dev, v); });
     if (e != cudaSuccess) return e;
-    const int heads = R.Hq + R.Hkv, half = R.r / 2;
-    const int64_t per_token = (int64_t)heads * (half / V + (R.d - R.r) / V);
-    // Tokens per block: enough units for one full batch of every thread, at most 32 KB of sines.  With fewer
-    // tokens than two blocks per SM, a token's heads are spread over blocks instead (each forms the sines again,
-    // which costs less than the idle SMs).
-    int tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kThreads * kBatch / std::max<int64_t>(1, per_token), 4096 / half));
+    const int heads = R.Hq + R.Hkv, half = R.r / 2, at_once = kThreads / (half / V);
+    // Tokens per block: eight (token, head) pairs for every thread, at most 32 KB of sines, and two blocks per SM.
+    // With fewer tokens than that, a token's heads are spread over blocks instead (each forms the sines again, which
+    // costs less than idle SMs).
+    const int64_t want = std::max(1, 8 * at_once / heads);
+    int tokens = (int)std::max<int64_t>(1, std::min<int64_t>({want, 4096 / half, R.total / (2 * n_sm)}));
     int split = 1;
-    if (R.total < 2 * n_sm) {
-        tokens = 1;
-        split = (int)std::max<int64_t>(1, std::min<int64_t>(heads, std::min<int64_t>(2 * n_sm / R.total, per_token / 128)));
-    }
+    if (R.total < 2 * n_sm)
+        split = (int)std::max<int64_t>(1, std::min<int64_t>(2 * n_sm / R.total, (heads + at_once - 1) / at_once));
     const int hpb = (heads + split - 1) / split;
     const int64_t blocks = (R.total + tokens - 1) / tokens;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    rope_kernel<T, V><<<dim3((unsigned)blocks, (unsigned)((heads + hpb - 1) / hpb)), kThreads,
-                        (size_t)tokens * half * sizeof(float2), st>>>(R, q, k, pos, qo, ko, tokens, hpb);
+    rope_kernel<T, V, IL><<<dim3((unsigned)blocks, (unsigned)((heads + hpb - 1) / hpb)), kThreads,
+                            (size_t)tokens * half * sizeof(float2), st>>>(R, q, k, pos, qo, ko, tokens, hpb);
     return cudaGetLastError();
 }
 
@@ -135,8 +142,9 @@ cudaError_t launch_rope(const RopeDims& R, const T* q, const T* k, const int64_t
     // 16-byte pieces where every piece of every head starts on a 16-byte boundary, else single elements
     const uintptr_t p = (uintptr_t)q | (uintptr_t)k | (uintptr_t)qo | (uintptr_t)ko;
     const int64_t s = R.q_in | R.k_in | R.q_out | R.k_out | R.d | (R.r / 2);
-    if (p % 16 == 0 && s % V == 0) return launch<T, V>(R, q, k, pos, qo, ko, st);
-    return launch<T, 1>(R, q, k, pos, qo, ko, st);
+    if (p % 16 == 0 && s % V == 0)
+        return R.interleaved ? launch<T, V, true>(R, q, k, pos, qo, ko, st) : launch<T, V, false>(R, q, k, pos, qo, ko, st);
+    return R.interleaved ? launch<T, 1, true>(R, q, k, pos, qo, ko, st) : launch<T, 1, false>(R, q, k, pos, qo, ko, st);
 }
 template cudaError_t launch_rope<float>(const RopeDims&, const float*, const float*, const int64_t*, float*, float*,
                                         cudaStream_t);
