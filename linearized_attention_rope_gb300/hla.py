@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -413,25 +414,44 @@ def prefill_noalloc_check_error(stream=None) -> int:
 _TORCH = {DTYPE_F32: torch.float32, DTYPE_BF16: torch.bfloat16, DTYPE_E4M3: torch.uint8}
 
 
+def _refuse(what: str):
+    raise HlaError(HLA_ERR_INVALID_ARG, what)
+
+
 def _need(ok, what: str):
     if not ok:
-        raise HlaError(HLA_ERR_INVALID_ARG, what)
+        _refuse(what)
 
 
-def _check_tensor(t, what: str, dtype, shape, device, strided: bool = False) -> int:
+def _check_tensor(t, fn: str, name: str, dtype, shape, device, strided: bool = False) -> int:
     """The token stride of t in elements; t must have the type, shape and device given and be dense, or
     (strided) have dense rows at any token stride."""
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype, f"{what}: expected a {dtype} tensor")
-    _need(tuple(t.shape) == tuple(shape), f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _need(t.device == device, f"{what}: expected on {device}, got {t.device}")
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        _refuse(f"{fn}: {name}: expected a {dtype} tensor")
+    if t.shape != shape:
+        _refuse(f"{fn}: {name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        _refuse(f"{fn}: {name}: expected on {device}, got {t.device}")
     if t.is_contiguous() or t.numel() == 0:
-        return t.shape[1] * t.shape[2] if t.dim() == 3 else 0
-    _need(strided and t.dim() == 3 and t.stride(2) == 1 and t.stride(1) == t.shape[2] and
-          t.stride(0) >= t.shape[1] * t.shape[2], f"{what}: expected dense {'rows' if strided else 'storage'}")
+        return shape[1] * shape[2] if len(shape) == 3 else 0
+    if not (strided and len(shape) == 3 and t.stride(2) == 1 and t.stride(1) == shape[2] and
+            t.stride(0) >= shape[1] * shape[2]):
+        _refuse(f"{fn}: {name}: expected dense {'rows' if strided else 'storage'}")
     return t.stride(0)
 
 
 _HERE_CTX = contextlib.nullcontext()
+
+
+@functools.lru_cache(maxsize=256)
+def _c(params, *strides):
+    """A frozen parameter set's C form, by reference; made once per set and strides, never changed."""
+    return ctypes.byref(params.c(*strides))
+
+
+def _adr(t):
+    """The address of a tensor as an int (0 for none), which ctypes takes as it is."""
+    return None if t is None else t.data_ptr()
 
 
 def _on(device, stream):
@@ -440,13 +460,12 @@ def _on(device, stream):
     _need(device.type == "cuda", f"expected CUDA tensors, got {device}")
     if stream is not None:
         _need(stream.device == device, f"expected a stream of {device}, got one of {stream.device}")
-        return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
-    stream = torch.cuda.current_stream(device)
+        return torch.cuda.stream(stream), stream.cuda_stream
     here = device.index == torch.cuda.current_device()
-    return _HERE_CTX if here else torch.cuda.device(device), ctypes.c_void_p(stream.cuda_stream)
+    return _HERE_CTX if here else torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
 
 
-@dataclass
+@dataclass(frozen=True)
 class RopeParams:
     n_q_heads: int
     n_kv_heads: int
@@ -480,27 +499,26 @@ def _rope(fn, params, q, k, positions, q_out, k_out, stream):
     _need(dt is not None and dt != torch.uint8, f"{fn}: dtype")
     _need(isinstance(positions, torch.Tensor) and positions.dim() == 1, f"{fn}: positions must be a vector")
     n, dev, strides, outs = positions.numel(), positions.device, [0, 0], [q_out, k_out]
-    _check_tensor(positions, f"{fn}: positions", torch.int64, (n,), dev)
+    _check_tensor(positions, fn, "positions", torch.int64, (n,), dev)
     for i, (x, o, heads, name) in enumerate(((q, q_out, params.n_q_heads, "q"), (k, k_out, params.n_kv_heads, "k"))):
         if x is None:
             _need(o is None, f"{fn}: {name}_out without {name}")
             continue
         shape = (n, heads, params.head_dim)
-        strides[i] = _check_tensor(x, f"{fn}: {name}", dt, shape, dev, strided=True)
+        strides[i] = _check_tensor(x, fn, name, dt, shape, dev, strided=True)
         if o is None:
             pass
         elif o.data_ptr() == x.data_ptr():
             _need(o.shape == x.shape and o.dtype == x.dtype and o.stride() == x.stride(), f"{fn}: {name}_out in place")
         else:
-            _check_tensor(o, f"{fn}: {name}_out", dt, shape, dev)
-    c = params.c(*strides)
+            _check_tensor(o, fn, name + "_out", dt, shape, dev)
     ctx, st = _on(dev, stream)
     with ctx:
         for i, x in enumerate((q, k)):
             if x is not None and outs[i] is None:
                 outs[i] = torch.empty(x.shape, dtype=dt, device=dev)
-        _check(getattr(load(), fn)(ctypes.byref(c), _ptr(q), _ptr(k), _ptr(positions), n, _ptr(outs[0]),
-                                   _ptr(outs[1]), st), fn)
+        _check(getattr(load(), fn)(_c(params, *strides), _adr(q), _adr(k), _adr(positions), n, _adr(outs[0]),
+                                   _adr(outs[1]), st), fn)
     return outs[0], outs[1]
 
 
@@ -515,7 +533,7 @@ def rope_backward(params: RopeParams, dq_out, dk_out, positions, dq=None, dk=Non
     return _rope("hla_rope_backward", params, dq_out, dk_out, positions, dq, dk, stream)
 
 
-@dataclass
+@dataclass(frozen=True)
 class AttnParams:
     n_q_heads: int
     n_kv_heads: int
@@ -537,7 +555,7 @@ def _zeroed(n: int, device):
 def attention_workspace_bytes(params: AttnParams, total_q: int, total_k: int, n_seqs: int,
                               backward: bool = False) -> int:
     n = ctypes.c_size_t()
-    _check(load().hla_attention_workspace_bytes(ctypes.byref(params.c()), total_q, total_k, n_seqs, int(backward),
+    _check(load().hla_attention_workspace_bytes(_c(params), total_q, total_k, n_seqs, int(backward),
                                                 ctypes.byref(n)), "hla_attention_workspace_bytes")
     return n.value
 
@@ -559,12 +577,12 @@ def _check_packed(fn, params, q, k, v, cu_q, cu_k, ws):
     _need(all(isinstance(x, torch.Tensor) and x.dim() == 3 for x in (q, k, v)), f"{fn}: q, k, v must be [T, H, d]")
     _need(isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 and cu_q.numel() >= 2, f"{fn}: cu_seqlens_q")
     dev, d, n = q.device, params.head_dim, cu_q.numel() - 1
-    strides = (_check_tensor(q, f"{fn}: q", dt, (q.shape[0], params.n_q_heads, d), dev, strided=True),
-               _check_tensor(k, f"{fn}: k", dt, (k.shape[0], params.n_kv_heads, d), dev, strided=True),
-               _check_tensor(v, f"{fn}: v", dt, (k.shape[0], params.n_kv_heads, d), dev, strided=True))
-    _check_tensor(cu_q, f"{fn}: cu_seqlens_q", torch.int32, (n + 1,), dev)
+    strides = (_check_tensor(q, fn, "q", dt, (q.shape[0], params.n_q_heads, d), dev, strided=True),
+               _check_tensor(k, fn, "k", dt, (k.shape[0], params.n_kv_heads, d), dev, strided=True),
+               _check_tensor(v, fn, "v", dt, (k.shape[0], params.n_kv_heads, d), dev, strided=True))
+    _check_tensor(cu_q, fn, "cu_seqlens_q", torch.int32, (n + 1,), dev)
     if cu_k is not None:
-        _check_tensor(cu_k, f"{fn}: cu_seqlens_k", torch.int32, (n + 1,), dev)
+        _check_tensor(cu_k, fn, "cu_seqlens_k", torch.int32, (n + 1,), dev)
     _check_workspace(fn, ws, dev)
     return strides, q.shape[0], k.shape[0], n
 
@@ -582,9 +600,9 @@ def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=
     strides, tq, tk, n = _check_packed("hla_attention", params, q, k, v, cu_seqlens_q, cu_seqlens_k, ws)
     dev, shape = q.device, (tq, params.n_q_heads, params.head_dim)
     if out is not None:
-        _check_tensor(out, "hla_attention: out", q.dtype, shape, dev)
+        _check_tensor(out, "hla_attention", "out", q.dtype, shape, dev)
     if lse is not None:
-        _check_tensor(lse, "hla_attention: lse", torch.float32, shape[:2], dev)
+        _check_tensor(lse, "hla_attention", "lse", torch.float32, shape[:2], dev)
     ctx, st = _on(dev, stream)
     with ctx:
         if out is None:
@@ -593,8 +611,8 @@ def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=
             lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
         if ws is None:
             ws = alloc_attention_workspace(params, tq, tk, n, device=dev)
-        _check(load().hla_attention(ctypes.byref(params.c(*strides)), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q),
-                                    _ptr(cu_seqlens_k), n, tq, tk, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), st),
+        _check(load().hla_attention(_c(params, *strides), _adr(q), _adr(k), _adr(v), _adr(cu_seqlens_q),
+                                    _adr(cu_seqlens_k), n, tq, tk, _adr(out), _adr(lse), _adr(ws), ws.numel(), st),
                "hla_attention")
     return out, lse
 
@@ -607,25 +625,25 @@ def attention_backward(params: AttnParams, q, k, v, out, lse, dout, cu_seqlens_q
     strides, tq, tk, n = _check_packed(fn, params, q, k, v, cu_seqlens_q, cu_seqlens_k, ws)
     dev = q.device
     for x, name in ((out, "out"), (dout, "dout")):
-        _check_tensor(x, f"{fn}: {name}", q.dtype, tuple(q.shape), dev)
-    _check_tensor(lse, f"{fn}: lse", torch.float32, tuple(q.shape[:2]), dev)
+        _check_tensor(x, fn, name, q.dtype, tuple(q.shape), dev)
+    _check_tensor(lse, fn, "lse", torch.float32, tuple(q.shape[:2]), dev)
     if grads is not None:
         for name, x in zip("qkv", (q, k, v)):
-            _check_tensor(grads.get(name), f"{fn}: grads[{name!r}]", x.dtype, tuple(x.shape), dev)
+            _check_tensor(grads.get(name), fn, "grads." + name, x.dtype, tuple(x.shape), dev)
     ctx, st = _on(dev, stream)
     with ctx:
         if grads is None:
             grads = {name: torch.empty(x.shape, dtype=x.dtype, device=dev) for name, x in zip("qkv", (q, k, v))}
         if ws is None:
             ws = alloc_attention_workspace(params, tq, tk, n, backward=True, device=dev)
-        _check(load().hla_attention_backward(ctypes.byref(params.c(*strides)), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                             _ptr(lse), _ptr(dout), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), n, tq, tk,
-                                             _ptr(grads["q"]), _ptr(grads["k"]), _ptr(grads["v"]), _ptr(ws),
+        _check(load().hla_attention_backward(_c(params, *strides), _adr(q), _adr(k), _adr(v), _adr(out),
+                                             _adr(lse), _adr(dout), _adr(cu_seqlens_q), _adr(cu_seqlens_k), n, tq, tk,
+                                             _adr(grads["q"]), _adr(grads["k"]), _adr(grads["v"]), _adr(ws),
                                              ws.numel(), st), fn)
     return grads
 
 
-@dataclass
+@dataclass(frozen=True)
 class CacheParams:
     n_kv_heads: int
     head_dim: int
@@ -647,12 +665,12 @@ class Cache:
 
     def __init__(self, params: CacheParams, page_table, k=None, v=None, k_exp=None, v_exp=None):
         rows, exps = ctypes.c_size_t(), ctypes.c_size_t()
-        _check(load().hla_cache_bytes(ctypes.byref(params.c()), ctypes.byref(rows), ctypes.byref(exps)),
+        _check(load().hla_cache_bytes(_c(params), ctypes.byref(rows), ctypes.byref(exps)),
                "hla_cache_bytes")
         _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2 and page_table.is_cuda,
               "Cache: page_table must be [n_seqs, max_pages] on the GPU")
         self.params, self.n_seqs, self.device = params, page_table.shape[0], page_table.device
-        _check_tensor(page_table, "Cache: page_table", torch.int32, (self.n_seqs, params.max_pages), self.device)
+        _check_tensor(page_table, "Cache", "page_table", torch.int32, (self.n_seqs, params.max_pages), self.device)
         self.page_table = page_table
         shape = (params.n_pages, params.n_kv_heads, params.page_size, params.head_dim)
         kind = _TORCH[params.cache_dtype]
@@ -664,14 +682,14 @@ class Cache:
             _need(k_exp is None and v_exp is None, "Cache: exponents go with an E4M3 cache")
             self.k_exp = self.v_exp = None
         self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
-        self.c = CCache(*[None if t is None else t.data_ptr() for t in
+        self._buffers = CCache(*[None if t is None else t.data_ptr() for t in
                           (self.k, self.v, self.k_exp, self.v_exp, self.page_table, self.err)])
-        self.cp = params.c()
+        self.c, self.cp = ctypes.byref(self._buffers), _c(params)
 
     def _buffer(self, t, name, dtype, shape):
         if t is None:
             return torch.zeros(shape, dtype=dtype, device=self.device)
-        _check_tensor(t, f"Cache: {name}", dtype, shape, self.device)
+        _check_tensor(t, "Cache", name, dtype, shape, self.device)
         return t
 
     def check_error(self, stream=None) -> int:
@@ -679,7 +697,7 @@ class Cache:
         code = ctypes.c_int32()
         ctx, st = _on(self.device, stream)
         with ctx:
-            rc = load().hla_check_cache_error(ctypes.byref(self.c), st, ctypes.byref(code))
+            rc = load().hla_check_cache_error(self.c, st, ctypes.byref(code))
         if rc not in (HLA_OK, HLA_ERR_STATE, HLA_ERR_TIMEOUT):
             _check(rc, "cache error word")
         return code.value
@@ -687,8 +705,8 @@ class Cache:
 
 def _check_rows(fn, cache, cu_seqlens, start):
     dev = cache.device
-    _check_tensor(cu_seqlens, f"{fn}: cu_seqlens", torch.int32, (cache.n_seqs + 1,), dev)
-    _check_tensor(start, f"{fn}: start", torch.int64, (cache.n_seqs,), dev)
+    _check_tensor(cu_seqlens, fn, "cu_seqlens", torch.int32, (cache.n_seqs + 1,), dev)
+    _check_tensor(start, fn, "start", torch.int64, (cache.n_seqs,), dev)
 
 
 def cache_write(cache: Cache, k, v, cu_seqlens, start, stream=None):
@@ -698,11 +716,11 @@ def cache_write(cache: Cache, k, v, cu_seqlens, start, stream=None):
     _need(isinstance(k, torch.Tensor) and k.dim() == 3, f"{fn}: k must be [T, Hkv, d]")
     shape = (k.shape[0], p.n_kv_heads, p.head_dim)
     for t, name in ((k, "k"), (v, "v")):
-        _check_tensor(t, f"{fn}: {name}", _TORCH[p.dtype], shape, cache.device)
+        _check_tensor(t, fn, name, _TORCH[p.dtype], shape, cache.device)
     ctx, st = _on(cache.device, stream)
     with ctx:
-        _check(load().hla_cache_write(ctypes.byref(cache.cp), ctypes.byref(cache.c), _ptr(k), _ptr(v),
-                                      _ptr(cu_seqlens), _ptr(start), cache.n_seqs, shape[0], st), fn)
+        _check(load().hla_cache_write(cache.cp, cache.c, _adr(k), _adr(v),
+                                      _adr(cu_seqlens), _adr(start), cache.n_seqs, shape[0], st), fn)
 
 
 def cache_read(cache: Cache, cu_seqlens, start, total_tokens: int, k=None, v=None, stream=None):
@@ -713,18 +731,18 @@ def cache_read(cache: Cache, cu_seqlens, start, total_tokens: int, k=None, v=Non
     _need(total_tokens >= 0, f"{fn}: total_tokens")
     for t, name in ((k, "k"), (v, "v")):
         if t is not None:
-            _check_tensor(t, f"{fn}: {name}", dt, shape, cache.device)
+            _check_tensor(t, fn, name, dt, shape, cache.device)
     ctx, st = _on(cache.device, stream)
     with ctx:
         out = [torch.empty(shape, dtype=dt, device=cache.device) if t is None else t for t in (k, v)]
-        _check(load().hla_cache_read(ctypes.byref(cache.cp), ctypes.byref(cache.c), _ptr(cu_seqlens), _ptr(start),
-                                     cache.n_seqs, total_tokens, _ptr(out[0]), _ptr(out[1]), st), fn)
+        _check(load().hla_cache_read(cache.cp, cache.c, _adr(cu_seqlens), _adr(start),
+                                     cache.n_seqs, total_tokens, _adr(out[0]), _adr(out[1]), st), fn)
     return out[0], out[1]
 
 
 def decode_workspace_bytes(params: AttnParams, cache_params: CacheParams) -> int:
     n = ctypes.c_size_t()
-    _check(load().hla_attention_decode_workspace_bytes(ctypes.byref(params.c()), ctypes.byref(cache_params.c()),
+    _check(load().hla_attention_decode_workspace_bytes(_c(params), _c(cache_params),
                                                        ctypes.byref(n)), "hla_attention_decode_workspace_bytes")
     return n.value
 
@@ -739,10 +757,10 @@ def attention_decode(params: AttnParams, cache: Cache, q, lens, out=None, ws=Non
     fn = "hla_attention_decode"
     _need(params.dtype == cache.params.dtype, f"{fn}: the layer's and the cache's row types differ")
     dt, dev, shape = _TORCH[params.dtype], cache.device, (cache.n_seqs, params.n_q_heads, params.head_dim)
-    stride = _check_tensor(q, f"{fn}: q", dt, shape, dev, strided=True)
-    _check_tensor(lens, f"{fn}: lens", torch.int64, (cache.n_seqs,), dev)
+    stride = _check_tensor(q, fn, "q", dt, shape, dev, strided=True)
+    _check_tensor(lens, fn, "lens", torch.int64, (cache.n_seqs,), dev)
     if out is not None:
-        _check_tensor(out, f"{fn}: out", dt, shape, dev)
+        _check_tensor(out, fn, "out", dt, shape, dev)
     _check_workspace(fn, ws, dev)
     ctx, st = _on(dev, stream)
     with ctx:
@@ -750,7 +768,7 @@ def attention_decode(params: AttnParams, cache: Cache, q, lens, out=None, ws=Non
             out = torch.empty(shape, dtype=dt, device=dev)
         if ws is None:
             ws = alloc_decode_workspace(params, cache)
-        _check(load().hla_attention_decode(ctypes.byref(params.c(stride)), ctypes.byref(cache.cp),
-                                           ctypes.byref(cache.c), _ptr(q), _ptr(lens), cache.n_seqs, _ptr(out),
-                                           _ptr(ws), ws.numel(), st), fn)
+        _check(load().hla_attention_decode(_c(params, stride), cache.cp,
+                                           cache.c, _adr(q), _adr(lens), cache.n_seqs, _adr(out),
+                                           _adr(ws), ws.numel(), st), fn)
     return out
