@@ -135,8 +135,9 @@ AttnDims attn_dims(const hla_attn_params* p, int n_seqs, int64_t total_q, int64_
 
 constexpr size_t kWsHead = 256;  // the error word
 
-size_t attn_ws_bytes(const hla_attn_params* p, int64_t total_q, int64_t, int, bool backward) {
+size_t attn_ws_bytes(const hla_attn_params* p, int64_t total_q, int64_t total_k, int n_seqs, bool backward) {
     size_t n = kWsHead;
+    if (!backward && p->dtype == HLA_DTYPE_BF16) n += attention_tc_part_bytes(attn_dims(p, n_seqs, total_q, total_k));
     if (backward) n += ((size_t)total_q * p->n_q_heads * sizeof(float2) + 255) / 256 * 256;  // per row and head
     return n;
 }
@@ -241,10 +242,13 @@ HLA_API int hla_attention(const hla_attn_params* p, const void* q, const void* k
         return status(launch_attention_simt(A, static_cast<const float*>(q), static_cast<const float*>(k),
                                             static_cast<const float*>(v), cu_q, cu_k, static_cast<float*>(out), lse,
                                             err, st));
-    const auto launch = attention_tc_supported(A) ? launch_attention_tc : launch_attention_simt<__nv_bfloat16>;
-    return status(launch(A, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-                         static_cast<const __nv_bfloat16*>(v), cu_q, cu_k, static_cast<__nv_bfloat16*>(out), lse, err,
-                         st));
+    using bf = __nv_bfloat16;
+    const bf *qb = static_cast<const bf*>(q), *kb = static_cast<const bf*>(k), *vb = static_cast<const bf*>(v);
+    // without keys there is nothing for a tensor map to describe: the plain kernel writes the empty rows
+    if (!attention_tc_supported(A))
+        return status(launch_attention_simt(A, qb, kb, vb, cu_q, cu_k, static_cast<bf*>(out), lse, err, st));
+    return status(launch_attention_tc(A, qb, kb, vb, cu_q, cu_k, static_cast<bf*>(out), lse,
+                                      static_cast<char*>(ws) + kWsHead, err, st));
 }
 
 HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, const void* k, const void* v,

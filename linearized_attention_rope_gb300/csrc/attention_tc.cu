@@ -19,6 +19,11 @@
 // O is then rescaled in TMEM by its own softmax thread, after the products
 // before it have completed (they complete before the scores it waits for).
 //
+// With fewer items than half the SMs (a short chunk of a prompt behind many
+// keys), the keys of each item are cut into parts, an item each; a part leaves
+// its rows' outputs in fp32 with their log-sum-exp, and a second kernel adds
+// them in order.
+//
 // Bound by the tensor cores (4 d flops per visible score) together with the
 // softmax's issue slots (about 4 instructions and one exponential per score).
 #include "attention_tc.cuh"
@@ -45,8 +50,9 @@ template <int D>
 __global__ void __launch_bounds__(kBlock, 1)
 attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int lpack,
-                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int32_t* __restrict__ err) {
+                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int lpack, int parts,
+                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
+                    float* __restrict__ part_lse, int32_t* __restrict__ err) {
     using C = Cfg<D>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -92,10 +98,9 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     // what an item's two tiles see: keys [0, end), tile t in nt = n[t] key tiles
     struct Span { int end, n0, n1, n; };
     auto span = [&](const Item& it) {
-        const int off = it.lk - it.lq;
         auto key_end = [&](int t) {
             const int p0 = it.first + t * qb;
-            return p0 < it.lq ? max(0, min(it.lk, min(p0 + qb, it.lq) + off)) : 0;
+            return p0 < it.lq ? max(0, min(it.lk, min(p0 + qb, it.lq) + it.off)) : 0;
         };
         const int e0 = key_end(0), e1 = key_end(1);
         const int n0 = __shfl_sync(0xffffffffu, (e0 + kRows - 1) / kRows, 0);
@@ -259,7 +264,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             }
         } else {
             schedule_items(A, cu_q, cu_k, 2 * qb, n_hg, false, items, bar_it, bar_ie, bar_ask, bar_want, err,
-                           [&](int hg) { return hg << lpack; });
+                           [&](int hg) { return hg << lpack; }, parts);
         }
     } else {
         take_registers();
@@ -272,15 +277,15 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         bool ok = true;
         for (int i = 0;; ++i) {
             int nt, limit;  // key tiles of the query tile; keys the row sees: [0, limit)
-            int64_t at;     // the row's place in the output (-1: none)
+            int64_t at;     // the row's place in the output, or among the parts' (-1: none)
             {
                 const Item it = next_item(items, i, bar_it, bar_ie, err);
                 if (it.head < 0) break;
                 const Span sp = span(it);
                 const int pos = it.first + t * qb + (row >> lpack);
                 nt = t ? sp.n1 : sp.n0;
-                limit = pos < it.lq ? min(it.lk, pos + it.lk - it.lq + 1) : 0;
-                at = pos < it.lq ? ((int64_t)it.q0 + pos) * A.Hq + it.head + (row & (pack - 1)) : -1;
+                limit = pos < it.lq ? min(it.lk, pos + it.off + 1) : 0;
+                at = pos < it.lq ? (it.part * A.total_q + it.q0 + pos) * A.Hq + it.head + (row & (pack - 1)) : -1;
             }
             float m = -INFINITY;
             float2 l = make_float2(0.f, 0.f);
@@ -351,7 +356,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             // ---- the row's output
             const float sum = l.x + l.y;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            if (at >= 0) lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+            if (at >= 0) (parts > 1 ? part_lse : lse)[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
             if (nt > 0) ok = ok && wait_or_flag(bar_o + 8 * t, count & 1, err);
             umma::fence_after_sync();
 #pragma unroll
@@ -369,7 +374,13 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     if (lane == 0) umma::mbar_arrive(bar_oe + 8 * t);
                     ++count;
                 }
-                if (at >= 0) {
+                if (at >= 0 && parts > 1) {
+                    float* dst = part_o + at * D + 32 * b;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(dst + e) =
+                            make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+                } else if (at >= 0) {
                     __nv_bfloat16* dst = out + at * D + 32 * b;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
@@ -385,9 +396,57 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     if (warp == 9) umma::tmem_dealloc(tmem, C::kCols);
 }
 
+// Adds the parts of every row of the sequences, in order; a warp per row and head.
+template <int D>
+__global__ void __launch_bounds__(256)
+attention_join_kernel(AttnDims A, const int32_t* __restrict__ cu_q, int parts, const float* __restrict__ part_o,
+                      const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+    constexpr int E = D / 32;
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), rows = A.total_q * A.Hq;
+    const int lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    const int64_t t = r / A.Hq;
+    int64_t a, n;
+    seq_range(cu_q, seq_of_token(cu_q, A.n_seqs, t), A.total_q, &a, &n);
+    if (t < a || t >= a + n) return;  // behind the last sequence
+    const float l = lane < parts ? __ldg(part_lse + lane * rows + r) : -INFINITY;
+    float m = l;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float w = l == -INFINITY ? 0.f : exp2f((l - m) * kLog2e);  // NaN stays NaN
+    float sum = w, acc[E];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+    for (int x = 0; x < E; ++x) acc[x] = 0.f;
+    for (int p = 0; p < parts; ++p) {
+        const float wp = __shfl_sync(0xffffffffu, w, p);
+        if (wp == 0.f) continue;  // no keys
+        float o[E];
+        load_vec<E>(part_o + (p * rows + r) * D + lane * E, o);
+#pragma unroll
+        for (int x = 0; x < E; ++x) acc[x] = fmaf(wp, o[x], acc[x]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int x = 0; x < E; x += 2)
+        *reinterpret_cast<uint32_t*>(out + r * D + lane * E + x) = pack_bf2(acc[x] * inv, acc[x + 1] * inv);
+    if (lane == 0) lse[r] = sum == 0.f ? -INFINITY : m + logf(sum);
+}
+
+// Items (pairs of query tiles) over all sequences and head groups: at most, and about.
+int64_t items_bound(const AttnDims& A) {
+    const int pack = pack_of(A.G);
+    return (A.total_q / (2 * (kRows / pack)) + A.n_seqs) * (A.Hq / pack);
+}
+int64_t items_about(const AttnDims& A) {
+    const int pack = pack_of(A.G), rows = 2 * (kRows / pack);
+    return std::max<int64_t>(A.n_seqs, (A.total_q + rows - 1) / rows) * (A.Hq / pack);
+}
+
 template <int D>
 cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                   const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out, float* lse, int32_t* err,
+                   const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out, float* lse, void* part_ws, int32_t* err,
                    cudaStream_t st) {
     static DeviceCache cache;
     cudaError_t e = device_cached(cache, nullptr, [](int, int*) {
@@ -405,9 +464,15 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
         !tma::make_map_3d_strided(&mv, v, true, D, (uint64_t)A.Hkv, (uint64_t)A.total_k, (uint64_t)A.sv * 2, 64, 1,
                                   kRows))
         return cudaErrorInvalidValue;
-    const int64_t blocks = (A.total_q / (2 * qb) + A.n_seqs) * (A.Hq / pack);
-    attention_tc_kernel<D><<<(unsigned)blocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mk, mv, cu_q, cu_k, lpack, out,
-                                                                             lse, err);
+    const int parts = attention_tc_parts(A);
+    const int64_t blocks = items_bound(A) * parts, rows = A.total_q * A.Hq;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    float* part_lse = static_cast<float*>(part_ws);
+    float* part_o = part_lse + (parts * rows + 3) / 4 * 4;
+    attention_tc_kernel<D><<<(unsigned)blocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mk, mv, cu_q, cu_k, lpack, parts, out,
+                                                                             lse, part_o, part_lse, err);
+    if (parts > 1)
+        attention_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(A, cu_q, parts, part_o, part_lse, out, lse);
     return cudaGetLastError();
 }
 
@@ -415,11 +480,23 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
 
 bool attention_tc_supported(const AttnDims& A) { return A.total_q > 0 && A.total_k > 0; }
 
+// The keys are cut where items would leave half the SMs without work, into as many parts as fill them (a workspace's
+// size must not depend on the device: 152 SMs), and only where there are keys enough for two parts of eight tiles.
+int attention_tc_parts(const AttnDims& A) {
+    const int64_t items = items_about(A), sms = 152;
+    if (A.total_k < 16 * kRows || 2 * items > sms) return 1;
+    return (int)std::min<int64_t>(32, sms / std::max<int64_t>(1, items));
+}
+size_t attention_tc_part_bytes(const AttnDims& A) {
+    const int64_t parts = attention_tc_parts(A), rows = A.total_q * A.Hq;
+    return parts > 1 ? (size_t)((parts * rows + 3) / 4 * 4 + parts * rows * A.d) * sizeof(float) : 0;
+}
+
 cudaError_t launch_attention_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                 const __nv_bfloat16* v, const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out,
-                                float* lse, int32_t* err, cudaStream_t st) {
-    return A.d == 128 ? launch<128>(A, q, k, v, cu_q, cu_k, out, lse, err, st)
-                      : launch<64>(A, q, k, v, cu_q, cu_k, out, lse, err, st);
+                                float* lse, void* parts, int32_t* err, cudaStream_t st) {
+    return A.d == 128 ? launch<128>(A, q, k, v, cu_q, cu_k, out, lse, parts, err, st)
+                      : launch<64>(A, q, k, v, cu_q, cu_k, out, lse, parts, err, st);
 }
 
 }  // namespace hla

@@ -103,10 +103,12 @@ __device__ __forceinline__ void named_arrive(int id, int threads) {
 // before: items claimed early would be kept from blocks that are free sooner.
 
 struct Item {
-    int q0, k0;  // first query and key row of the sequence
+    int q0, k0;  // first query and key row of the sequence (of the item's part of the keys)
     int lq, lk;  // its lengths
     int first;   // first position of the tile(s)
     int head;    // first query head, or the kv head; -1: no more items
+    int off;     // row i sees keys j <= i + off
+    int part;    // which part of the keys
 };
 constexpr int kItems = 2;       // entries of the ring
 constexpr int kItemWarps = 11;  // warps that read them
@@ -136,25 +138,37 @@ __device__ __forceinline__ int64_t taken_item(uint32_t answer) {
     return got ? (int64_t)x : -1;
 }
 
-// The scheduling warp: `heads` head groups, `rows` positions per item.
+// The scheduling warp: `heads` head groups, `rows` positions per item, whose
+// visible keys are cut into `parts` parts of whole tiles, eight at least (the
+// parts past those get none).
 template <class HeadOf>
 __device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t* cu_q, const int32_t* cu_k, int rows,
                                                int heads, bool by_key, ItemRing* ring, uint32_t bar_full,
                                                uint32_t bar_empty, uint32_t bar_ask, uint32_t bar_want, int32_t* err,
-                                               HeadOf head_of) {
+                                               HeadOf head_of, int parts = 1) {
     const int lane = threadIdx.x & 31;
     const uint32_t answer = umma::smem_addr(&ring->answer);
     int64_t x = blockIdx.x;
     bool more = true;
     for (int i = 0; more; ++i) {
         AttnBlock B = {};
-        if (x >= 0) B = attn_find_block(A, cu_q, cu_k, rows, x / heads, by_key);
+        const int part = parts > 1 && x >= 0 ? (int)(x % parts) : 0;
+        if (x >= 0) B = attn_find_block(A, cu_q, cu_k, rows, x / parts / heads, by_key);
         const int s = i % kItems;
         more = B.found;
         if (i >= kItems && !wait_or_flag(bar_empty + 8 * s, ((i / kItems) - 1) & 1, err, kItemSeconds)) more = false;
+        int k0 = (int)B.k0, lk = B.lk, off = B.lk - B.lq;
+        if (parts > 1) {
+            const int end = max(0, min(B.lk, min(B.first + rows, B.lq) + off)), n = (end + kRows - 1) / kRows;
+            const int cut = max(1, min(parts, n / 8)), a = part < cut ? (int)((int64_t)n * part / cut) * kRows : end;
+            const int b = part < cut ? (int)((int64_t)n * (part + 1) / cut) * kRows : end;
+            k0 += a;
+            lk = min(lk, b) - a;
+            off -= a;
+        }
         if (lane == 0) {
-            ring->word[s][0] = make_int4((int)B.q0, (int)B.k0, B.lq, B.lk);
-            ring->word[s][1] = make_int4(B.first, more ? head_of((int)(x % heads)) : -1, 0, 0);
+            ring->word[s][0] = make_int4((int)B.q0, k0, B.lq, lk);
+            ring->word[s][1] = make_int4(B.first, more ? head_of((int)(x / parts % heads)) : -1, off, part);
         }
         __syncwarp();
         if (lane == 0) umma::mbar_arrive(bar_full + 8 * s);
@@ -173,10 +187,10 @@ __device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t*
 __device__ __forceinline__ Item next_item(const ItemRing* ring, int i, uint32_t bar_full, uint32_t bar_empty,
                                           int32_t* err) {
     const int s = i % kItems;
-    Item it = {0, 0, 0, 0, 0, -1};
+    Item it = {0, 0, 0, 0, 0, -1, 0, 0};
     if (wait_or_flag(bar_full + 8 * s, (i / kItems) & 1, err, kItemSeconds)) {
         const int4 a = ring->word[s][0], b = ring->word[s][1];
-        it = Item{a.x, a.y, a.z, a.w, b.x, b.y};
+        it = Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     }
     __syncwarp();
     if ((threadIdx.x & 31) == 0) umma::mbar_arrive(bar_empty + 8 * s);
@@ -208,9 +222,12 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int first) {
 }  // namespace attn_tc
 
 bool attention_tc_supported(const AttnDims& A);
+// Parts that the keys of each item are cut into, and the bytes of the partial results (0: one part).
+int attention_tc_parts(const AttnDims& A);
+size_t attention_tc_part_bytes(const AttnDims& A);
 cudaError_t launch_attention_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                 const __nv_bfloat16* v, const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out,
-                                float* lse, int32_t* err, cudaStream_t st);
+                                float* lse, void* parts, int32_t* err, cudaStream_t st);
 cudaError_t launch_attention_backward_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                          const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
                                          const __nv_bfloat16* dout, const int32_t* cu_q, const int32_t* cu_k,

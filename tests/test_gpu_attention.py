@@ -113,6 +113,15 @@ def test_chunks_behind_earlier_keys(dtype, d):
     full_check(dtype, d, 4, 2, [1, 40, 130, 3], [300, 41, 390, 3])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (3, 1)])
+def test_few_rows_over_many_keys(d, hq, hkv):
+    # the keys are cut over blocks and joined: rows whose parts differ in number, an empty sequence, a row that sees
+    # its first keys only in the last part
+    full_check("bf16", d, hq, hkv, [1, 17, 0, 40], [5000, 2100, 30, 40])
+    full_check("bf16", d, hq, hkv, [3], [9001])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_rows_that_see_no_key(dtype, d):
