@@ -447,7 +447,8 @@ typedef struct hla_attn_params {
     int64_t v_stride;
 } hla_attn_params;
 
-/* Workspace bytes of hla_attention, or (backward != 0) of
+/* Workspace bytes of hla_attention (more than the error word for few rows over
+ * many keys, whose parts are joined), or (backward != 0) of
  * hla_attention_backward; a workspace serves any call it is large enough for.
  * Its first 16 bytes are the error word: zero them before the first use; calls
  * only ever set it, hla_check_workspace_error reads and clears it.  Two calls
@@ -465,8 +466,9 @@ HLA_API int hla_attention_workspace_bytes(const hla_attn_params* params, int64_t
  *       keys: Lk > Lq).
  *   out [total_q, Hq, d], lse fp32 [total_q, Hq]: the natural log of the sum
  *       of exponentials (what hla_attention_backward needs)
- * A row that sees no key has out 0 and lse -infinity.  Rows at and past c_n
- * are left as they were.  A malformed table is clamped on the device (no
+ * A row that sees no key has out 0 and lse -infinity.  What a row does not see
+ * does not reach it, infinities and NaN included (the padding of a batch may
+ * hold anything).  Rows at and past c_n are left as they were.  A malformed table is clamped on the device (no
  * access out of range) and flagged in the workspace's error word.  bf16 layers
  * run on the tensor cores: fp32 scores and sums, probabilities rounded to bf16
  * for their product with v.  Asynchronous; deterministic. */
@@ -478,6 +480,9 @@ HLA_API int hla_attention(const hla_attn_params* params, const void* q, const vo
  * dq [total_q, Hq, d], dk, dv [total_k, Hkv, d] (a kv head's sums over the
  * query heads that read it), in params->dtype from fp32 sums.  Keys that no
  * row sees have gradients 0; rows at and past c_n are left as they were.
+ * Infinities and NaN of keys do not reach dq of rows before them; those of a
+ * row's dout and q may reach dk and dv of keys up to 127 after it in its own
+ * sequence (bf16 layers).
  * Asynchronous; deterministic (fixed order of sums, no atomics). */
 HLA_API int hla_attention_backward(const hla_attn_params* params, const void* q, const void* k, const void* v,
                                    const void* out, const float* lse, const void* dout,
@@ -548,7 +553,8 @@ HLA_API int hla_attention_decode_workspace_bytes(const hla_attn_params* params, 
  * own key and value written before), into out [n_seqs, Hq, d].  A sequence
  * with no keys has out 0.  Keys whose page is out of range, and positions past
  * max_pages * page_size, are left out and flagged; a negative length counts as
- * 0 and is flagged.  The heads, head_dim and dtype of both parameter sets must
+ * 0 and is flagged.  A cache of more than 2^32 - 2 rows is HLA_ERR_UNSUPPORTED
+ * here.  The heads, head_dim and dtype of both parameter sets must
  * agree.  Asynchronous; deterministic. */
 HLA_API int hla_attention_decode(const hla_attn_params* params, const hla_cache_params* cache_params,
                                  const hla_cache* cache, const void* q, const int64_t* lens, int n_seqs, void* out,

@@ -78,7 +78,7 @@ template <int D> struct Cfg {
     static constexpr int kSlots = D == 128 ? 5 : 8;
     // two fixed tiles (K, V or Q, dO), the ring, two stages of row stats (-lse, then -D; 128 fp32 each), barriers
     static constexpr uint32_t kFix = 0, kRing = 2 * kTile, kStat = kRing + kSlots * kTile, kBar = kStat + 2048;
-    static constexpr uint32_t kItem = kBar + 320, kSmem = kItem + sizeof(ItemRing);
+    static constexpr uint32_t kItem = kBar + 352, kSmem = kItem + sizeof(ItemRing);
     static constexpr uint32_t kCols = 512;
 };
 
@@ -143,7 +143,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_dp = bar_s + 8, bar_fix = bar_dp + 8, bar_done = bar_fix + 32;
     const uint32_t bar_oe = bar_done + 8, bar_it = bar_oe + 8, bar_ie = bar_it + 8 * kItems, bar_ask = bar_ie + 8 * kItems;
     const uint32_t bar_want = bar_ask + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 316);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 344);
     ItemRing* items = reinterpret_cast<ItemRing*>(sm + C::kItem);
     if (tid == 0) {
         umma::mbar_init(bar_kv, 1);
@@ -186,8 +186,8 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         give_registers();
         bool ok = true;
         if (warp == 8) {
-            // ---- loads: the ring takes Q 0, dO 0, Q 1, dO 1, ... of every item.  Rows behind the sequence are cleared,
-            //      whatever they hold (the ring holds at most four tiles, so four barriers keep a tile's signal until
+            // ---- loads: the ring takes Q 0, dO 0, Q 1, dO 1, ... of every item.  Of rows behind the sequence,
+            //      infinities and NaN are cleared: their probability is 0 (the ring holds at most four tiles, so four barriers keep a tile's signal until
             //      the products have seen it)
             static_assert(C::kSlots <= 8, "tiles in the ring");
             Ring ring;
@@ -233,7 +233,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 ok = ok && wait_or_flag(bar_full + 8 * use[y].slot, use[y].par, err);
-                                if (ok) zero_rows<D>(sm + C::kRing + use[y].slot * C::kTile, sp.tail);
+                                if (ok) clear_nonfinite<D>(sm + C::kRing + use[y].slot * C::kTile, sp.tail, kRows, [](int) {});
                             }
                             umma::fence_async_smem();
                             __syncwarp();
@@ -266,7 +266,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 const int n = sp.n;
                 if (n == 0) continue;
                 int r = 0;
-                auto ready_q = [&](const Ring& q) {  // a tile's Q (a last tile's dO too: both cleared behind the last row)
+                auto ready_q = [&](const Ring& q) {  // a tile's Q (of a last tile both, cleared behind the last row)
                     wait(bar_full + 8 * q.slot, q.par);
                     if (++r == sp.per) {
                         r = 0;
@@ -492,10 +492,10 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
     const int qb = kRows >> lpack, n_hg = A.Hq >> lpack;
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
     const uint32_t bar_q = bars, bar_qe = bar_q + 8, bar_full = bar_qe + 8, bar_empty = bar_full + 8 * C::kSlots;
-    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_se = bar_s + 8, bar_dp = bar_se + 8, bar_fix = bar_dp + 8;
-    const uint32_t bar_done = bar_fix + 64, bar_oe = bar_done + 8, bar_it = bar_oe + 8, bar_ie = bar_it + 8 * kItems;
+    const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_se = bar_s + 8, bar_dp = bar_se + 8, bar_fix = bar_dp + 16;
+    const uint32_t bar_clear = bar_fix + 64, bar_done = bar_clear + 16, bar_oe = bar_done + 8, bar_it = bar_oe + 8, bar_ie = bar_it + 8 * kItems;
     const uint32_t bar_ask = bar_ie + 8 * kItems, bar_want = bar_ask + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 316);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 344);
     ItemRing* items = reinterpret_cast<ItemRing*>(sm + C::kItem);
     if (tid == 0) {
         umma::mbar_init(bar_q, 1);
@@ -506,8 +506,11 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
         }
         umma::mbar_init(bar_s, 1);
         umma::mbar_init(bar_se, 8);
-        umma::mbar_init(bar_dp, 1);
         for (int i = 0; i < 8; ++i) umma::mbar_init(bar_fix + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(bar_dp + 8 * i, 1);
+            umma::mbar_init(bar_clear + 8 * i, 1);
+        }
         umma::mbar_init(bar_done, 1);
         umma::mbar_init(bar_oe, 8);
         for (int i = 0; i < kItems; ++i) {
@@ -525,10 +528,13 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t cS = tmem, cP = tmem + 128, cQ = tmem + 384;  // S, dP / dS (two buffers), dQ
 
-    struct Span { int end, n; };  // keys the tile sees: [0, end), in n key tiles
+    // keys the tile sees: [0, end), in n key tiles; from `some` on only some of its rows, in key tiles from `mixed` on
+    struct Span { int end, n, some, mixed; };
     auto span = [&](const Item& it) {
         const int end = max(0, min(it.lk, min(it.first + qb, it.lq) + it.lk - it.lq));
-        return Span{end, __shfl_sync(0xffffffffu, (end + kRows - 1) / kRows, 0)};
+        const int some = max(0, min(end, it.first + it.lk - it.lq + 1));
+        return Span{end, __shfl_sync(0xffffffffu, (end + kRows - 1) / kRows, 0), some,
+                    __shfl_sync(0xffffffffu, some / kRows, 0)};
     };
 
     if (warp >= 8) {
@@ -576,11 +582,11 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                     load(&map_v, kKs + v.slot, kv, it.k0 + i * kRows);
                 }
                 if (sp.n > 0) {
-                    // keys behind the last visible one: cleared, whatever they hold (dS is 0 there).  The ring holds
-                    // the K tiles of at most six items: eight barriers.
+                    // keys behind the last visible one: infinities and NaN cleared (dS is 0 there).  The ring holds the K
+                    // tiles of at most six items: eight barriers.
                     static_assert(kKs <= 6, "items in the ring");
                     ok = ok && wait_or_flag(bar_full + 8 * k.slot, k.par, err);
-                    if (ok) zero_rows<D>(sm + C::kRing + k.slot * C::kTile, sp.end - (sp.n - 1) * kRows);
+                    if (ok) clear_nonfinite<D>(sm + C::kRing + k.slot * C::kTile, sp.end - (sp.n - 1) * kRows, kRows, [](int) {});
                     umma::fence_async_smem();
                     __syncwarp();
                     if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (fixed & 7));
@@ -602,12 +608,13 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             const uint64_t ring_mn = umma::mnmajor(base + C::kRing, kRows * 128, 0);
             RingK rk;
             RingV rv;
-            int fixed = 0, count = 0;
+            int fixed = 0, cleared = 0, count = 0;
             uint32_t ts = 0;  // tiles so far
             for (int x = 0;; ++x) {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (__shfl_sync(0xffffffffu, it.head, 0) < 0) break;
-                const int n = span(it).n;
+                const Span sp = span(it);
+                const int n = sp.n;
                 if (n == 0) continue;
                 // S and dP of the item's tile i, once the scores of the tile before have been read; dP goes to the
                 // buffer that the tile before last has been taken from.  Returns the slot of its K tile.
@@ -628,7 +635,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                     if (ok)
                         outer_product<D>(cP + (ts & 1) * 128, o_tile,
                                          ring_k + (uint64_t)((kKs + v.slot) * (C::kTile / 16)), lead);
-                    done(bar_dp);
+                    done(bar_dp + 8 * (ts & 1));
                     done(bar_empty + 8 * (kKs + v.slot));
                     if (i == n - 1) done(bar_qe);  // Q and dO have been read for the last time
                     ++ts;
@@ -640,6 +647,10 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 for (int i = 0; i < n; ++i) {
                     const uint32_t b = (ts - 1) & 1;  // this tile's buffer and barrier
                     const uint32_t k1 = i + 1 < n ? tile(i + 1) : k;
+                    if (i >= sp.mixed) {
+                        wait(bar_clear + 8 * (cleared & 1), (cleared >> 1) & 1);
+                        ++cleared;
+                    }
                     named_sync(kBarDs + b, 288);
                     umma::fence_after_sync();
                     if (ok)
@@ -652,19 +663,35 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             }
         } else if (warp == 10) {
             // ---- "scores ready", "score gradients ready" passed on to the elementwise warps.  dP runs one tile ahead:
-            //      two barriers, so that a slow warp never meets the signal of the tile after its own (the one after
-            //      that waits until every warp has read the next tile's scores)
+            //      two barriers of either kind, so that no warp, this one included, ever meets the signal of the tile
+            //      after its own (the one after that waits until every warp has read the next tile's scores).  Between
+            //      the two, infinities and NaN in keys that only some of the tile's rows see are cleared for the
+            //      dQ product: the scores are formed already, and dS is 0 in the rows that must not see them, NaN in the
+            //      others.  (At most two tiles wait for their product: two barriers.)
             uint32_t t = 0;  // tiles so far
+            int cleared = 0;
+            RingK rk;
             for (int x = 0;; ++x) {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (it.head < 0) break;
-                const int n = span(it).n;
-                for (int i = 0; i < n; ++i, ++t) {
+                const Span sp = span(it);
+                for (int i = 0; i < sp.n; ++i, ++t) {
+                    const RingK k = rk.next();
                     ok = ok && wait_or_flag(bar_s, t & 1, err);
                     umma::fence_after_sync();
                     umma::fence_before_sync();
                     named_arrive(kBarS, 288);
-                    ok = ok && wait_or_flag(bar_dp, t & 1, err);
+                    if (i >= sp.mixed) {
+                        const int k0 = i * kRows;
+                        if (ok)
+                            clear_nonfinite<D>(sm + C::kRing + k.slot * C::kTile, max(0, sp.some - k0),
+                                               min(kRows, sp.end - k0), [](int) {});
+                        umma::fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) umma::mbar_arrive(bar_clear + 8 * (cleared & 1));
+                        ++cleared;
+                    }
+                    ok = ok && wait_or_flag(bar_dp + 8 * (t & 1), (t >> 1) & 1, err);
                     umma::fence_after_sync();
                     umma::fence_before_sync();
                     named_arrive(kBarDq + (t & 1), 288);

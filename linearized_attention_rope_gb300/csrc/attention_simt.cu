@@ -61,8 +61,9 @@ __device__ __forceinline__ void scores(const float* a, const float* b, int ty, i
     }
 }
 
-// acc[i][c] += sum_k p[row ty 4 + i][k] b[k][column], columns tx 4 + (64 c / 4); p: [64][kB + 4]
-template <int D>
+// acc[i][c] += sum_k p[row ty 4 + i][k] b[k][column], columns tx 4 + (64 c / 4); p: [64][kB + 4].  SKIP: terms with
+// p = 0 are left out, for tiles in which some rows must not see what some of b's rows hold (0 times infinity).
+template <int D, bool SKIP>
 __device__ __forceinline__ void add_rows(const float* p, const float* b, int ty, int tx, float (&acc)[4][D / 16]) {
 #pragma unroll 2
     for (int k = 0; k < kB; k += 4) {
@@ -79,6 +80,7 @@ __device__ __forceinline__ void add_rows(const float* p, const float* b, int ty,
                 const float4 y = *reinterpret_cast<const float4*>(b + (k + kk) * kPitch<D> + tx * 4 + 64 * c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    if (SKIP && w[i][kk] == 0.f) continue;
                     acc[i][4 * c + 0] = fmaf(w[i][kk], y.x, acc[i][4 * c + 0]);
                     acc[i][4 * c + 1] = fmaf(w[i][kk], y.y, acc[i][4 * c + 1]);
                     acc[i][4 * c + 2] = fmaf(w[i][kk], y.z, acc[i][4 * c + 2]);
@@ -171,7 +173,8 @@ attn_fwd_simt_kernel(AttnDims A, const T* __restrict__ q, const T* __restrict__ 
             for (int c = 0; c < D / 16; ++c) acc[i][c] *= corr;
         }
         __syncthreads();
-        add_rows<D>(ps, vs, ty, tx, acc);
+        if (j0 + kB > B.first + off) add_rows<D, true>(ps, vs, ty, tx, acc);
+        else add_rows<D, false>(ps, vs, ty, tx, acc);
     }
     float inv[4];
 #pragma unroll
@@ -271,8 +274,13 @@ attn_dkdv_simt_kernel(AttnDims A, const T* __restrict__ q, const T* __restrict__
                     dt[(tx + 16 * j) * (kB + 4) + ty * 4 + i] = dp[i][j];
                 }
             __syncthreads();
-            add_rows<D>(pt, os, ty, tx, av);
-            add_rows<D>(dt, qs, ty, tx, ak);
+            if (r0 + off < B.first + kB) {
+                add_rows<D, true>(pt, os, ty, tx, av);
+                add_rows<D, true>(dt, qs, ty, tx, ak);
+            } else {
+                add_rows<D, false>(pt, os, ty, tx, av);
+                add_rows<D, false>(dt, qs, ty, tx, ak);
+            }
         }
     }
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
@@ -319,7 +327,8 @@ attn_dq_simt_kernel(AttnDims A, const T* __restrict__ q, const T* __restrict__ k
 #pragma unroll
             for (int j = 0; j < 4; ++j) ds[(ty * 4 + i) * (kB + 4) + tx + 16 * j] = dp[i][j];
         __syncthreads();
-        add_rows<D>(ds, ks, ty, tx, acc);
+        if (j0 + kB > B.first + off) add_rows<D, true>(ds, ks, ty, tx, acc);
+        else add_rows<D, false>(ds, ks, ty, tx, acc);
     }
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
     store_rows<T, D>(dq + B.q0 * A.Hq * D + (int64_t)h * D, (int64_t)A.Hq * D, B.first, B.lq, ty, tx, acc, one);

@@ -5,7 +5,9 @@
 // A block takes two query tiles (128 rows each, see attention_tc.cuh) of one
 // kv head and walks the keys they see in tiles of 128:
 //   warp 8        TMA: both query tiles, then K and V tiles into a ring of
-//                 slots; clears the value rows behind the last visible key
+//                 slots; clears infinities and NaN in value rows that not all
+//                 rows see (a probability of 0 would pass them on; the rows
+//                 that do see them get them back at the end)
 //   warp 9        one thread issues every product; S of both tiles (128
 //                 columns each) and O of both (d columns each) in TMEM
 //   warps 0 - 3   softmax of tile 0, one row per thread
@@ -26,6 +28,8 @@
 //
 // Bound by the tensor cores (4 d flops per visible score) together with the
 // softmax's issue slots (about 4 instructions and one exponential per score).
+#include <type_traits>
+
 #include "attention_tc.cuh"
 
 namespace hla {
@@ -37,11 +41,19 @@ using namespace attn_tc;
 constexpr float kLazy = 8.0f;
 constexpr int kBarS = 1, kBarP = 3;  // hardware barriers: scores ready, probabilities ready (+ tile)
 
+// Of an item: the keys found with infinities or NaN, one bit for each from key `some` on; where its keys lie.
+struct alignas(16) Marks {
+    uint32_t bit[8];
+    int some, kv, k0, pad;
+};
+
 template <int D> struct Cfg {
     static constexpr uint32_t kTile = kRows * D * 2;  // bytes of a tile
     static constexpr int kSlots = D == 128 ? 5 : 8;
     static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBar = kRing + kSlots * kTile;
-    static constexpr uint32_t kSmem = kBar + 320 + sizeof(ItemRing) + 1024;
+    static constexpr int kMarks = 8;  // items whose marks are kept
+    static constexpr uint32_t kMark = kBar + 320 + 96, kSmem = kMark + kMarks * sizeof(Marks) + 1024;
+    static_assert(sizeof(ItemRing) <= 96, "shared memory layout");
     // TMEM columns
     static constexpr uint32_t kS = 0, kO = 256, kCols = 512;
 };
@@ -50,7 +62,8 @@ template <int D>
 __global__ void __launch_bounds__(kBlock, 1)
 attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int lpack, int parts,
+                    const __nv_bfloat16* __restrict__ v, const int32_t* __restrict__ cu_q,
+                    const int32_t* __restrict__ cu_k, int lpack, int parts,
                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
                     float* __restrict__ part_lse, int32_t* __restrict__ err) {
     using C = Cfg<D>;
@@ -96,7 +109,8 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     // what an item's two tiles see: keys [0, end), tile t in nt = n[t] key tiles
-    struct Span { int end, n0, n1, n; };
+    // keys from `some` on are seen by some of the rows only, in key tiles from `mixed` on (the last tile at least)
+    struct Span { int end, n0, n1, n, some, mixed; };
     auto span = [&](const Item& it) {
         auto key_end = [&](int t) {
             const int p0 = it.first + t * qb;
@@ -105,7 +119,8 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         const int e0 = key_end(0), e1 = key_end(1);
         const int n0 = __shfl_sync(0xffffffffu, (e0 + kRows - 1) / kRows, 0);
         const int n1 = __shfl_sync(0xffffffffu, (e1 + kRows - 1) / kRows, 0);
-        return Span{max(e0, e1), n0, n1, max(n0, n1)};
+        const int end = max(e0, e1), some = max(0, min(end, it.first + it.off + 1));
+        return Span{end, n0, n1, max(n0, n1), some, __shfl_sync(0xffffffffu, min(max(n0, n1) - 1, some / kRows), 0)};
     };
     auto slot_of = [&](int use) { return use % C::kSlots; };
     auto par_of = [&](int use) { return (uint32_t)(use / C::kSlots) & 1u; };
@@ -121,6 +136,15 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 if (it.head < 0) break;
                 const Span sp = span(it);
                 const int kv = it.head / A.G, ask_at = max(0, 2 * sp.n - 3);
+                // (kept for eight items; an item is handed out only once every warp has started on the one before last)
+                Marks* marks = reinterpret_cast<Marks*>(sm + C::kMark) + (i & (C::kMarks - 1));
+                if (lane < 8) marks->bit[lane] = 0u;
+                if (lane == 0) {
+                    marks->some = sp.some;
+                    marks->kv = kv;
+                    marks->k0 = it.k0;
+                }
+                __syncwarp();
                 if (sp.n == 0 && lane == 0) umma::mbar_arrive(bar_want);
                 for (int u = 0; u < 2 * sp.n; ++u) {
                     if (u == ask_at && lane == 0) umma::mbar_arrive(bar_want);  // time to look for the next item
@@ -136,6 +160,23 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                                                 u & 1 ? &map_v : &map_k, 64 * b, kv, it.k0 + (u >> 1) * kRows,
                                                 bar_full + 8 * slot);
                     }
+                    if ((u & 1) && (u >> 1) >= sp.mixed) {
+                        // (The ring holds at most four V tiles, so four barriers keep a tile's signal until the products
+                        // have seen it.)
+                        static_assert(C::kSlots <= 8, "tiles in the ring");
+                        const int k0 = (u >> 1) * kRows;
+                        ok = wait_or_flag(bar_full + 8 * slot, par_of(use + u), err);
+                        if (!ok) continue;
+                        unsigned char* tile = sm + C::kRing + slot * C::kTile;
+                        clear_nonfinite<D>(tile, max(0, sp.some - k0), kRows, [&](int row) {
+                            const int key = k0 + row;  // (a row behind the last visible key is cleared only)
+                            if (key < sp.end) atomicOr(marks->bit + ((key - sp.some) >> 5), 1u << ((key - sp.some) & 31));
+                        });
+                        umma::fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) umma::mbar_arrive(bar_fix + 8 * (n_fix & 3));
+                        ++n_fix;
+                    }
                     if (u > 0) continue;
                     for (int t = 0; t < 2 && ok; ++t) {  // the query tiles, once the last item's scores are formed
                         if ((t ? sp.n1 : sp.n0) == 0) continue;
@@ -148,19 +189,6 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                                                     it.head, it.q0 + it.first + t * qb, bar_q + 8 * t);
                         }
                     }
-                }
-                if (sp.n > 0 && ok) {
-                    // the last V tile: rows behind the last visible key weigh 0; clear them, whatever they hold.  (The
-                    // ring holds the tiles of at most four items, so four barriers keep an item's signal until the
-                    // products have seen it.)
-                    static_assert(C::kSlots <= 8, "items in the ring");
-                    const int u = use + 2 * sp.n - 1;
-                    ok = wait_or_flag(bar_full + 8 * slot_of(u), par_of(u), err);
-                    if (ok) zero_rows<D>(sm + C::kRing + slot_of(u) * C::kTile, sp.end - (sp.n - 1) * kRows);
-                    umma::fence_async_smem();
-                    __syncwarp();
-                    if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (n_fix & 3));
-                    ++n_fix;
                 }
                 use += 2 * sp.n;
             }
@@ -201,7 +229,7 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     umma::mma_ts_lead(tmem + C::kO + t * D, tmem + C::kS + t * kRows + 8 * s, b + (uint64_t)(s * 128),
                                       id_o, add || s > 0, lead);
             };
-            int count[2] = {0, 0}, n_fix = 0;  // items with tile t, items
+            int count[2] = {0, 0}, n_fix = 0;  // items with tile t, cleared tiles
             for (int i = 0;; ++i) {
                 const Item it = next_item(items, i, bar_it, bar_ie, err);
                 if (__shfl_sync(0xffffffffu, it.head, 0) < 0) break;
@@ -220,12 +248,16 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     if (nt == 1) done(bar_qe + 8 * t);
                 }
                 done(bar_empty + 8 * first.slot);
-                for (int j = 0; j < n; ++j) {
-                    const bool more = j + 1 < n;
+                // one key tile; the ones that all rows see have a loop of their own, without the wait for the clearing
+                auto step = [&](int j, auto mixed) {
+                    const bool more = !decltype(mixed)::value || j + 1 < n;
                     const Use v = ring.next(), k = more ? ring.next() : v;
                     wait(bar_full + 8 * v.slot, v.par);
                     if (more) wait(bar_full + 8 * k.slot, k.par);
-                    else wait(bar_fix + 8 * (n_fix & 3), (n_fix >> 2) & 1);
+                    if (decltype(mixed)::value) {
+                        wait(bar_fix + 8 * (n_fix & 3), (n_fix >> 2) & 1);
+                        ++n_fix;
+                    }
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const int nt = t ? sp.n1 : sp.n0;
@@ -240,10 +272,12 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     }
                     done(bar_empty + 8 * v.slot);
                     if (more) done(bar_empty + 8 * k.slot);
-                }
+                };
+                int j = 0;
+                for (; j < sp.mixed; ++j) step(j, std::false_type{});
+                for (; j < n; ++j) step(j, std::true_type{});
                 count[0] += sp.n0 > 0;
                 count[1] += sp.n1 > 0;
-                ++n_fix;
             }
         } else if (warp == 10) {
             // ---- "scores ready" passed on to the softmax warps, in the order the products are issued
@@ -389,6 +423,26 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                             pack_bf2(o[e + 4] * inv, o[e + 5] * inv), pack_bf2(o[e + 6] * inv, o[e + 7] * inv));
                 }
             }
+            // infinities and NaN that were kept out of the product: to the rows that see their keys
+            const Marks* marks = reinterpret_cast<const Marks*>(sm + C::kMark) + (i & (C::kMarks - 1));
+            const uint4 lo = *reinterpret_cast<const uint4*>(marks->bit), hi = *reinterpret_cast<const uint4*>(marks->bit + 4);
+            if (nt > 0 && (lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w) != 0u && at >= 0) {
+#pragma unroll 1
+                for (int w = 0; w < 8; ++w)
+#pragma unroll 1
+                    for (uint32_t left = marks->bit[w]; left; left &= left - 1) {
+                        const int key = marks->some + 32 * w + __ffs(left) - 1;
+                        if (key >= limit) continue;
+                        const __nv_bfloat16* src = v + (int64_t)(marks->k0 + key) * A.sv + marks->kv * D;
+#pragma unroll 1
+                        for (int e = 0; e < D; ++e) {
+                            const float x = __bfloat162float(src[e]);
+                            if (fabsf(x) < INFINITY) continue;
+                            if (parts > 1) part_o[at * D + e] += x;
+                            else out[at * D + e] = __float2bfloat16_rn(__bfloat162float(out[at * D + e]) + x);
+                        }
+                    }
+            }
         }
     }
     umma::fence_before_sync();
@@ -469,7 +523,7 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     float* part_lse = static_cast<float*>(part_ws);
     float* part_o = part_lse + (parts * rows + 3) / 4 * 4;
-    attention_tc_kernel<D><<<(unsigned)blocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mk, mv, cu_q, cu_k, lpack, parts, out,
+    attention_tc_kernel<D><<<(unsigned)blocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mk, mv, v, cu_q, cu_k, lpack, parts, out,
                                                                              lse, part_o, part_lse, err);
     if (parts > 1)
         attention_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(A, cu_q, parts, part_o, part_lse, out, lse);

@@ -21,13 +21,13 @@ constexpr int kRows = 128;  // rows of a query tile, keys of a key tile
 constexpr uint32_t kWaitLimit = 1u << 22, kItemSeconds = 60;  // polls per second allowed
 
 // Registers of a block of three warpgroups: 168 a thread at launch; the third
-// (loads and products) gives 96 a thread up, the softmax warpgroups take 48
+// (loads and products) gives 112 a thread up, the softmax warpgroups take 56
 // each.  The launcher checks that the kernel was compiled to that count: an
 // increase beyond what the launch holds would never be granted.
-constexpr int kBlock = 384, kLaunchRegs = 168, kSoftmaxRegs = 216, kIssueRegs = 72;
+constexpr int kBlock = 384, kLaunchRegs = 168, kSoftmaxRegs = 224, kIssueRegs = 56;
 static_assert(2 * kSoftmaxRegs + kIssueRegs == 3 * kLaunchRegs, "register split");
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
 template <class K>
 cudaError_t prepare_kernel(K kernel, size_t smem) {
     cudaFuncAttributes a;
@@ -210,13 +210,52 @@ template <int N> struct RingPos {
     }
 };
 
-// Rows [first, 128) of a 128 x D 16-bit tile (128-byte-swizzled 64-column blocks) set to zero by one warp.
-template <int D>
-__device__ __forceinline__ void zero_rows(unsigned char* tile, int first) {
-    const int lane = threadIdx.x & 31, n = (kRows - first) * 8;  // 16-byte pieces of a column block
-    for (int b = 0; b < D / 64; ++b)
-        for (int i = lane; i < n; i += 32)
-            *reinterpret_cast<uint4*>(tile + b * (kRows * 128) + first * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+// Infinities and NaN in rows [first, last) of a 128 x D bf16 tile
+// (128-byte-swizzled 64-column blocks) set to zero by one warp: rows that some
+// or all rows of the product must not see weigh 0 there, and 0 times infinity
+// would reach them all the same.  found(row) for each row that held any.
+// Looking costs less than clearing: 0 x + acc over a batch of pieces, one
+// packed multiply-add per two elements, is 0 unless an x is infinite or NaN.
+__device__ __forceinline__ uint32_t finite_mask(uint32_t w) {  // of each 16-bit half: all ones where it is finite
+    return ((w & 0x7f80u) != 0x7f80u ? 0x0000ffffu : 0u) | ((w & 0x7f800000u) != 0x7f800000u ? 0xffff0000u : 0u);
+}
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t acc) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    return acc;
+}
+template <int D, class Found>
+__device__ __forceinline__ void clear_nonfinite(unsigned char* tile, int first, int last, Found found) {
+    constexpr int kBatch = 8;  // pieces on their way
+    const int lane = threadIdx.x & 31, n = max(0, last - first) * 8;  // 16-byte pieces of a column block
+    for (int b = 0; b < D / 64; ++b) {
+        uint4* p = reinterpret_cast<uint4*>(tile + b * (kRows * 128) + first * 128);
+#pragma unroll 1
+        for (int i0 = lane; i0 - lane < n; i0 += 32 * kBatch) {
+            uint4 x[kBatch];
+            uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+                x[y] = make_uint4(0u, 0u, 0u, 0u);
+                if (i0 + 32 * y < n) x[y] = p[i0 + 32 * y];
+            }
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+                acc[0] = add_zero_times(x[y].x, acc[0]);
+                acc[1] = add_zero_times(x[y].y, acc[1]);
+                acc[2] = add_zero_times(x[y].z, acc[2]);
+                acc[3] = add_zero_times(x[y].w, acc[3]);
+            }
+            if (((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) == 0u) continue;
+#pragma unroll 1
+            for (int i = i0; i < min(n, i0 + 32 * kBatch); i += 32) {
+                const uint4 w = p[i];
+                const uint4 m = make_uint4(finite_mask(w.x), finite_mask(w.y), finite_mask(w.z), finite_mask(w.w));
+                if ((m.x & m.y & m.z & m.w) == 0xffffffffu) continue;
+                p[i] = make_uint4(w.x & m.x, w.y & m.y, w.z & m.z, w.w & m.w);
+                found(first + (i >> 3));
+            }
+        }
+    }
 }
 
 }  // namespace attn_tc

@@ -206,6 +206,51 @@ def test_other_sequences_stay_out(dtype, d):
         check(dtype, d, y, ref, out[a:b], lse[a:b], {n: t[a:b] for n, t in grads.items()}, [b - a], [b - a])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 2, 2), (128, 4, 1), (128, 3, 1), (64, 8, 1)])
+@pytest.mark.parametrize("n,real", [(70, 50), (300, 130), (260, 255)])
+def test_later_rows_stay_out(dtype, d, hq, hkv, n, real):
+    """A padded batch: the rows from `real` on hold NaN and infinities, as keys, values and queries.  Nothing of them
+    reaches the rows before them: outputs, lse and dq (dk and dv do get the padded rows' gradients: those that
+    dout makes are kept to the rows before)."""
+    x = make(dtype, d, hq, hkv, [n], [n], seed=n)
+    clean = {m: t.clone() for m, t in x.items()}
+    g = ac.gen(n)
+    for m in ("q", "k", "v"):
+        bad = torch.randint(0, 3, x[m][real:].shape, generator=g)
+        x[m][real:] = torch.where(bad == 0, math.nan, torch.where(bad == 1, math.inf, -math.inf)).to(x[m].dtype)
+    out, lse, grads = run(params(dtype, d, hq, hkv), x, [n], [n])
+    y = {m: t[:real] for m, t in clean.items()}
+    ref = ac.attention(y["q"], y["k"], y["v"], [real], [real], dout=y["dout"])
+    ref[2].pop("k"), ref[2].pop("v")
+    check(dtype, d, y, ref, out[:real], lse[:real], {"q": grads["q"][:real]}, [real], [real])
+    assert torch.isnan(out[real:]).all() and torch.isnan(lse[real:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 2, 2), (128, 8, 1)])
+def test_infinite_and_nan_values_reach_the_rows_that_see_them(dtype, d, hq, hkv):
+    n = 200
+    x = make(dtype, d, hq, hkv, [n], [n], seed=7)
+    places = {(3, 0): math.inf, (100, 5): math.nan, (130, d - 1): -math.inf, (150, 9): math.inf, (199, 1): math.nan}
+    clean = x["v"].clone()
+    for (key, col), value in places.items():
+        x["v"][key, :, col] = value
+        clean[key, :, col] = 0.0
+    out, lse, _ = run(params(dtype, d, hq, hkv), x, [n], [n], backward=False)
+    ref = ac.attention(x["q"], x["k"], clean, [n], [n])
+    rows, want = torch.arange(n), ref[0].clone()
+    for (key, col), value in places.items():
+        want[rows >= key, :, col] = value
+    got = out.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[want.isinf()], want[want.isinf()])
+    fine = want.isfinite()
+    u = ac.EPS[TYPE[dtype][1]] / 2
+    tol = (0.0 if dtype == "f32" else u) * ref[3]["out"] + 1e-4 * ref[3]["out"] + 1.01 * u * want.abs().nan_to_num(0, 0, 0)
+    assert ((got - want).abs()[fine] <= tol[fine]).all()
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 def test_slices_of_a_fused_projection(dtype, d):
     hq, hkv, lens = 4, 2, [100, 45]
