@@ -15,6 +15,14 @@
 // what the two extra products cost.  No gradient is summed outside a block, so
 // shared kv heads need no second pass either.
 //
+// D comes from the stored output, whose rounding matters where few keys are
+// seen (O is then as large as a value, and its error moves all of a row's dS the
+// same way): rows that see one key tile get D = sum_j P_ij dP_ij from the dq
+// kernel instead, which runs first and leaves it for the other.  (Rows of more
+// keys: O is smaller by the root of their number.  With the stored output alone
+// dq was off by 2.0 roundings of bf16 for sequences of 10 to 50 rows, with this
+// 1.4: the result's own and that of dS.)
+//
 // P and dS are rounded to bf16 (the inputs' own precision) and are read by the
 // products from TMEM, over the columns of the scores they came from.  Products
 // and elementwise work alternate: while dV and the next S are formed, dS is
@@ -72,6 +80,7 @@ attn_stats_kernel(int64_t rows, const __nv_bfloat16* __restrict__ out, const __n
 // scores, probabilities, score gradients dP and dS ready; in the dq kernel dP and dS by even and odd tiles
 // (kBarDq, kBarDs, one more each).
 constexpr int kBarS = 1, kBarP = 2, kBarDp = 3, kBarDq = 2, kBarDs = 4;
+constexpr int kBarRow = 6;  // the elementwise warps among themselves
 
 template <int D> struct Cfg {
     static constexpr uint32_t kTile = kRows * D * 2;
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(kBlock, 1)
 attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CUtensorMap map_q,
                   const __grid_constant__ CUtensorMap map_do, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const int32_t* __restrict__ cu_q,
-                  const int32_t* __restrict__ cu_k, int lpack, const float2* __restrict__ stats,
+                  const int32_t* __restrict__ cu_k, int lpack, float2* __restrict__ stats,
                   __nv_bfloat16* __restrict__ dq, int32_t* __restrict__ err) {
     using C = Cfg<D>;
     // K tiles stay until their dQ product, V tiles only for dP: rings of their own, so that V runs ahead
@@ -721,8 +730,9 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 limit = pos < it.lq ? min(it.lk, pos + it.lk - it.lq + 1) : 0;
                 at = pos < it.lq ? ((int64_t)it.q0 + pos) * A.Hq + it.head + (row & ((1 << lpack) - 1)) : -1;
             }
-            const float2 st = at >= 0 ? __ldg(stats + at) : make_float2(-INFINITY, 0.f);
-            const float2 nl = make_float2(st.x, st.x), nd = make_float2(st.y, st.y);
+            const float2 st = at >= 0 ? stats[at] : make_float2(-INFINITY, 0.f);
+            const float2 nl = make_float2(st.x, st.x);
+            float2 nd = make_float2(st.y, st.y);
             for (int i = 0; i < n; ++i, ++t) {
                 const int seen = limit - i * kRows - half * 64;
                 const bool edge = __any_sync(0xffffffffu, seen < 64);
@@ -743,6 +753,20 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 umma::fence_after_sync();
                 float2 d[32];
                 load64(tP, d);
+                if (n == 1) {  // D of the row from all of its keys: this half's sum and the other's
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        sum += 2 * e < seen ? p[e].x * d[e].x : 0.f;
+                        sum += 2 * e + 1 < seen ? p[e].y * d[e].y : 0.f;
+                    }
+                    float* halves = reinterpret_cast<float*>(sm + C::kStat);
+                    halves[half * 128 + row] = sum;
+                    named_sync(kBarRow, 256);
+                    sum = halves[row] + halves[128 + row];
+                    nd = make_float2(-sum, -sum);
+                    if (half == 0 && at >= 0) stats[at].y = -sum;
+                }
                 uint32_t w[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -817,10 +841,11 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
                   qblocks = (A.total_q / qb + A.n_seqs) * (A.Hq / pack), sb = (rows * (D / 8) + 255) / 256;
     if (kb > INT32_MAX || qblocks > INT32_MAX || sb > INT32_MAX) return cudaErrorInvalidValue;
     attn_stats_kernel<D><<<(unsigned)sb, 256, 0, st>>>(rows, out, dout, lse, stats);
-    attn_dkdv_tc_kernel<D><<<(unsigned)kb, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, stats, dk,
-                                                                       dv, err);
+    // dq first: it leaves a better D for rows of few keys
     attn_dq_tc_kernel<D><<<(unsigned)qblocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, stats,
                                                                           dq, err);
+    attn_dkdv_tc_kernel<D><<<(unsigned)kb, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, stats, dk,
+                                                                       dv, err);
     return cudaGetLastError();
 }
 
