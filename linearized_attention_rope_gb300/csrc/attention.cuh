@@ -128,15 +128,20 @@ __device__ __forceinline__ void attn_check_table(const int32_t* __restrict__ cu,
     if (bad) atomicExch(err, kErrSeqlens);
 }
 
-// fp32 SIMT kernels (every type, head count and head dim).
+// fp32 layers (attention_f32.cu), and the bytes their gradient needs: dout . out per row and head, and (several query
+// heads per kv head) dk and dv of each query head.
+cudaError_t launch_attention_f32(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
+                                 const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st);
+size_t attention_backward_f32_floats(const AttnDims& A);
+cudaError_t launch_attention_backward_f32(const AttnDims& A, const float* q, const float* k, const float* v,
+                                          const float* out, const float* lse, const float* dout, const int32_t* cu_q,
+                                          const int32_t* cu_k, float* dq, float* dk, float* dv, float* ws, int32_t* err,
+                                          cudaStream_t st);
+// What is left without keys, or without queries: rows of the sequences to zero (x, and y if given), lse to -infinity;
+// the other side's rows and table are checked only.
 template <typename T>
-cudaError_t launch_attention_simt(const AttnDims& A, const T* q, const T* k, const T* v, const int32_t* cu_q,
-                                  const int32_t* cu_k, T* out, float* lse, int32_t* err, cudaStream_t st);
-template <typename T>
-cudaError_t launch_attention_backward_simt(const AttnDims& A, const T* q, const T* k, const T* v, const T* out,
-                                           const float* lse, const T* dout, const int32_t* cu_q,
-                                           const int32_t* cu_k, T* dq, T* dk, T* dv, float* delta, int32_t* err,
-                                           cudaStream_t st);
+cudaError_t launch_attention_empty(int64_t total, int64_t other, int n_seqs, const int32_t* cu, const int32_t* cu_other,
+                                   int heads, int d, T* x, T* y, float* lse, int32_t* err, cudaStream_t st);
 
 struct CacheDims {
     int Hkv, d, page, n_pages, max_pages, n_seqs;

@@ -138,7 +138,9 @@ constexpr size_t kWsHead = 256;  // the error word
 size_t attn_ws_bytes(const hla_attn_params* p, int64_t total_q, int64_t total_k, int n_seqs, bool backward) {
     size_t n = kWsHead;
     if (!backward && p->dtype == HLA_DTYPE_BF16) n += attention_tc_part_bytes(attn_dims(p, n_seqs, total_q, total_k));
-    if (backward) n += ((size_t)total_q * p->n_q_heads * sizeof(float2) + 255) / 256 * 256;  // per row and head
+    if (backward && p->dtype == HLA_DTYPE_BF16) n += (size_t)total_q * p->n_q_heads * sizeof(float2);  // row statistics
+    if (backward && p->dtype == HLA_DTYPE_F32)
+        n += attention_backward_f32_floats(attn_dims(p, n_seqs, total_q, total_k)) * sizeof(float);
     return n;
 }
 
@@ -238,17 +240,19 @@ HLA_API int hla_attention(const hla_attn_params* p, const void* q, const void* k
     const AttnDims A = attn_dims(p, n_seqs, total_q, total_k);
     int32_t* err = static_cast<int32_t*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (p->dtype == HLA_DTYPE_F32)
-        return status(launch_attention_simt(A, static_cast<const float*>(q), static_cast<const float*>(k),
-                                            static_cast<const float*>(v), cu_q, cu_k, static_cast<float*>(out), lse,
-                                            err, st));
     using bf = __nv_bfloat16;
-    const bf *qb = static_cast<const bf*>(q), *kb = static_cast<const bf*>(k), *vb = static_cast<const bf*>(v);
-    // without keys there is nothing for a tensor map to describe: the plain kernel writes the empty rows
-    if (!attention_tc_supported(A))
-        return status(launch_attention_simt(A, qb, kb, vb, cu_q, cu_k, static_cast<bf*>(out), lse, err, st));
-    return status(launch_attention_tc(A, qb, kb, vb, cu_q, cu_k, static_cast<bf*>(out), lse,
-                                      static_cast<char*>(ws) + kWsHead, err, st));
+    const bool f32 = p->dtype == HLA_DTYPE_F32;
+    if (total_k == 0)  // no row sees a key
+        return status(f32 ? launch_attention_empty(total_q, total_k, n_seqs, cu_q, cu_k, A.Hq, A.d,
+                                                   static_cast<float*>(out), static_cast<float*>(nullptr), lse, err, st)
+                          : launch_attention_empty(total_q, total_k, n_seqs, cu_q, cu_k, A.Hq, A.d,
+                                                   static_cast<bf*>(out), static_cast<bf*>(nullptr), lse, err, st));
+    if (f32)
+        return status(launch_attention_f32(A, static_cast<const float*>(q), static_cast<const float*>(k),
+                                           static_cast<const float*>(v), cu_q, cu_k, static_cast<float*>(out), lse, err,
+                                           st));
+    return status(launch_attention_tc(A, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
+                                      cu_q, cu_k, static_cast<bf*>(out), lse, static_cast<char*>(ws) + kWsHead, err, st));
 }
 
 HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, const void* k, const void* v,
@@ -273,19 +277,27 @@ HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, cons
     void* rows_ws = static_cast<char*>(ws) + kWsHead;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     using bf = __nv_bfloat16;
-    if (p->dtype == HLA_DTYPE_BF16 && attention_tc_supported(A))
-        return status(launch_attention_backward_tc(
-            A, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
-            static_cast<const bf*>(out), lse, static_cast<const bf*>(dout), cu_q, cu_k, static_cast<bf*>(dq),
-            static_cast<bf*>(dk), static_cast<bf*>(dv), static_cast<float2*>(rows_ws), err, st));
-    auto run = [&](auto t) {
-        using T = decltype(t);
-        return status(launch_attention_backward_simt(
-            A, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), static_cast<const T*>(out),
-            lse, static_cast<const T*>(dout), cu_q, cu_k, static_cast<T*>(dq), static_cast<T*>(dk),
-            static_cast<T*>(dv), static_cast<float*>(rows_ws), err, st));
-    };
-    return p->dtype == HLA_DTYPE_F32 ? run(float()) : run(bf());
+    const bool f32 = p->dtype == HLA_DTYPE_F32;
+    if (total_q == 0 || total_k == 0) {  // no row sees a key: every gradient is zero
+        auto zero = [&](auto* rq, auto* rk, auto* rv) {
+            cudaError_t e = launch_attention_empty(total_q, total_k, n_seqs, cu_q, cu_k, A.Hq, A.d, rq,
+                                                   decltype(rq)(nullptr), nullptr, err, st);
+            if (e == cudaSuccess)
+                e = launch_attention_empty(total_k, total_q, n_seqs, cu_k, cu_q, A.Hkv, A.d, rk, rv, nullptr, err, st);
+            return status(e);
+        };
+        return f32 ? zero(static_cast<float*>(dq), static_cast<float*>(dk), static_cast<float*>(dv))
+                   : zero(static_cast<bf*>(dq), static_cast<bf*>(dk), static_cast<bf*>(dv));
+    }
+    if (f32)
+        return status(launch_attention_backward_f32(
+            A, static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
+            static_cast<const float*>(out), lse, static_cast<const float*>(dout), cu_q, cu_k, static_cast<float*>(dq),
+            static_cast<float*>(dk), static_cast<float*>(dv), static_cast<float*>(rows_ws), err, st));
+    return status(launch_attention_backward_tc(
+        A, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v), static_cast<const bf*>(out),
+        lse, static_cast<const bf*>(dout), cu_q, cu_k, static_cast<bf*>(dq), static_cast<bf*>(dk), static_cast<bf*>(dv),
+        static_cast<float2*>(rows_ws), err, st));
 }
 
 HLA_API int hla_cache_bytes(const hla_cache_params* p, size_t* rows, size_t* exponents) {

@@ -532,8 +532,6 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
 
 }  // namespace
 
-bool attention_tc_supported(const AttnDims& A) { return A.total_q > 0 && A.total_k > 0; }
-
 // Items that do not fill the SMs leave some idle.  With keys enough for parts of
 // eight tiles, they are cut into the number of parts whose rounds over the SMs
 // take least, counting what the parts' results cost: 0.55 of an item's time

@@ -260,7 +260,6 @@ __device__ __forceinline__ void clear_nonfinite(unsigned char* tile, int first, 
 
 }  // namespace attn_tc
 
-bool attention_tc_supported(const AttnDims& A);
 // Parts that the keys of each item are cut into, and the bytes of the partial results (0: one part).
 int attention_tc_parts(const AttnDims& A);
 size_t attention_tc_part_bytes(const AttnDims& A);

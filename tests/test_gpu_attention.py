@@ -130,6 +130,54 @@ def test_rows_that_see_no_key(dtype, d):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("q_lens,k_lens", [([5, 3], [0, 0]), ([0, 0], [4, 70])])
+def test_no_keys_at_all_or_no_queries(dtype, q_lens, k_lens):
+    # nothing is seen: out and every gradient are 0, lse -infinity; padding is left alone
+    x = make(dtype, 64, 4, 2, q_lens, k_lens, pad_q=2 if sum(q_lens) else 0, pad_k=2 if sum(k_lens) else 0)
+    nq, nk = sum(q_lens), sum(k_lens)
+    g = {n: t.cuda() for n, t in x.items()}
+    prm, cq, ck = params(dtype, 64, 4, 2), ac.cu(q_lens), ac.cu(k_lens)
+    ws = hla.alloc_attention_workspace(prm, g["q"].shape[0], g["k"].shape[0], 2, backward=True)
+    out, lse = torch.full_like(g["q"], 7.0), torch.full(g["q"].shape[:2], 7.0, device="cuda")
+    grads = {n: torch.full_like(g[n], 7.0) for n in "qkv"}
+    hla.attention(prm, g["q"], g["k"], g["v"], cq, ck, out=out, lse=lse, ws=ws)
+    hla.attention_backward(prm, g["q"], g["k"], g["v"], out, lse, g["dout"], cq, ck, grads=grads, ws=ws)
+    assert hla.check_workspace_error(ws) == 0
+    assert (out[:nq] == 0).all() and torch.isneginf(lse[:nq]).all() and (lse[nq:] == 7.0).all()
+    for t, n in ((out, nq), (grads["q"], nq), (grads["k"], nk), (grads["v"], nk)):
+        assert (t[:n] == 0).all() and (t[n:] == 7.0).all()
+    bad = ac.cu([3, 99])  # past the other side's rows, of which there are none
+    if nq:
+        hla.attention(prm, g["q"], g["k"], g["v"], cq, bad, out=out, lse=lse, ws=ws)
+        assert hla.check_workspace_error(ws) != 0
+    hla.attention_backward(prm, g["q"], g["k"], g["v"], out, lse, g["dout"], *((cq, bad) if nq else (bad, ck)),
+                           grads=grads, ws=ws)
+    assert hla.check_workspace_error(ws) != 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_layers_with_many_heads(d):
+    # enough blocks for the wider ones
+    full_check("f32", d, 32, 8, [300, 0, 345])
+    full_check("f32", d, 32, 32, [200, 150, 90], [300, 150, 20])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_layers_with_many_heads_and_nan_outside(d):
+    # the rows of one sequence and the padding hold NaN: the others stay what they are, bit for bit
+    lens = [130, 75, 200]
+    x = make("f32", d, 32, 8, lens, lens, pad_q=30, pad_k=30)
+    want = run(params("f32", d, 32, 8), x, lens, lens)
+    for n in x:
+        x[n][130:205] = math.nan
+        x[n][405:] = math.inf
+    got = run(params("f32", d, 32, 8), x, lens, lens)
+    keep = torch.cat([torch.arange(130), torch.arange(205, 405)]).cuda()
+    for a, b in ((want[0], got[0]), (want[1], got[1]), *((want[2][n], got[2][n]) for n in "qkv")):
+        assert torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_sequences(dtype):
     lens = [(7 * i) % 23 for i in range(75)]
     full_check(dtype, 64, 2, 1, lens)
