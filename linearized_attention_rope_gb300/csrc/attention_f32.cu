@@ -12,12 +12,15 @@
 // Both operands of a product lie in shared memory, rows padded by 16 bytes so
 // that 16 consecutive rows are read without bank conflicts; the next tile is
 // copied (cp.async) while this one is worked on, where shared memory allows two
-// (head dim 64, and the forward pass).  Bound by the fp32 FMA rate and
-// shared-memory reads (two 16-byte reads per 4 x 4 x 4 FMAs); short sequences by
-// the length of the walk, hence the blocks of 32 where 64 would leave SMs idle.
-// 4096 tokens, 8/2 heads of 128: forward 1150 us (30 TFLOP/s of the 80 the FMAs
-// could do), gradient 3853 us (31 of the 7 products done); 813 tokens, 4/2 heads
-// of 64: 31 and 91 us.
+// (head dim 64, and the forward pass).  A block of 32 has one warp per scheduler
+// per group of threads, which waits for every load; so 4 groups (2 at head dim
+// 128) take the tiles in turn and add their sums at the end, in order.
+//
+// Bound by the fp32 FMA rate and shared-memory reads (two 16-byte reads per
+// 4 x 4 x 4 FMAs).  4096 tokens, 8/2 heads of 128: forward 1141 us (30 TFLOP/s of
+// the 80 the FMAs could do), gradient 3904 us (31 with the 7 products it forms);
+// 813 tokens, 4/2 heads of 64, where the walk of one block is what takes the
+// time: 23 and 70 us (one group: 31 and 91).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -28,6 +31,7 @@ namespace {
 
 constexpr int kB = 64;  // keys of a forward tile, rows of a gradient tile
 constexpr int kThreads = 256;
+template <int D> constexpr int kSmallGroups = D == 64 ? 4 : 2;  // groups of a block of 32: what shared memory holds
 
 template <int D> constexpr int kPitch = D + 4;
 constexpr int kPPitch = kB + 4;
@@ -38,10 +42,16 @@ __device__ __forceinline__ void copy_wait(int left) {
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// Rows [first, first + N) of a head to shared memory, asynchronously; rows at or past n are zeros.
-template <int D, int N>
-__device__ __forceinline__ void copy_rows(float* dst, const float* __restrict__ src, int64_t stride, int first, int n) {
-    for (int i = threadIdx.x; i < N * (D / 4); i += blockDim.x) {
+// Waits for the T threads of group g.
+template <int T> __device__ __forceinline__ void group_sync(int g) {
+    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(T) : "memory");
+}
+
+// Rows [first, first + N) of a head to shared memory, asynchronously, by T threads; rows at or past n are zeros.
+template <int D, int N, int T>
+__device__ __forceinline__ void copy_rows(float* dst, const float* __restrict__ src, int64_t stride, int first, int n,
+                                          int tid) {
+    for (int i = tid; i < N * (D / 4); i += T) {
         const int r = i / (D / 4), c = (i % (D / 4)) * 4;
         const bool in = first + r < n;
         const float* from = src + (in ? (int64_t)(first + r) * stride : 0) + c;
@@ -50,24 +60,24 @@ __device__ __forceinline__ void copy_rows(float* dst, const float* __restrict__ 
     }
 }
 
-// s[i][j] = a row (ty MI + i) . b row (tx + 16 j)
-template <int D, int MI, int NJ>
-__device__ __forceinline__ void scores(const float* a, const float* b, int ty, int tx, float (&s)[MI][NJ]) {
+// s[i][j] = a row (ty 4 + i) . b row (tx + NX j)
+template <int D, int NX>
+__device__ __forceinline__ void scores(const float* a, const float* b, int ty, int tx, float (&s)[4][4]) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-        float4 x[MI], y[NJ];
+        float4 x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ty * MI + i) * kPitch<D> + c);
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ty * 4 + i) * kPitch<D> + c);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * kPitch<D> + c);
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + NX * j) * kPitch<D> + c);
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
                 s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
                 s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
@@ -76,8 +86,8 @@ __device__ __forceinline__ void scores(const float* a, const float* b, int ty, i
     }
 }
 
-// acc[i][c] += sum_k p[row ty MI + i][k] b[k][column], columns tx 4 + (64 c / 4), over 64 k.  skip: terms with p = 0 are
-// left out, for tiles in which some rows must not see what some of b's rows hold (0 times infinity).
+// acc[i][4 c + e] += sum_k p[row ty MI + i][k] b[k][column 64 c + 4 tx + e], over 64 k.  skip: terms with p = 0 are left
+// out, for tiles in which some rows must not see what some of b's rows hold (0 times infinity).
 template <int D, int MI, bool SKIP>
 __device__ __forceinline__ void add_rows(const float* p, const float* b, int ty, int tx, float (&acc)[MI][D / 16]) {
 #pragma unroll 2
@@ -136,30 +146,51 @@ __device__ __forceinline__ void store_rows(float* __restrict__ dst, int64_t stri
     }
 }
 
-// BM rows per block, 4 BM threads.
-template <int D, int BM>
-__global__ void __launch_bounds__(BM * 4)
+// Sums of the W groups' values, in order, in group 0; buf is free.
+template <int W, int T, int N>
+__device__ __forceinline__ void group_sums(float* buf, int g, int tid, float (&x)[N]) {
+    if (W == 1) return;
+    if (g > 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) buf[((g - 1) * N + i) * T + tid] = x[i];
+    __syncthreads();
+    if (g == 0)
+#pragma unroll
+        for (int o = 0; o < W - 1; ++o)
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] += buf[(o * N + i) * T + tid];
+    __syncthreads();
+}
+
+// BM rows per block, W groups of 4 BM threads that take the key tiles in turn, ST stages of K and V each.
+template <int D, int BM, int W, int ST>
+__global__ void __launch_bounds__(BM * 4 * W)
 attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                     const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, float* __restrict__ out,
                     float* __restrict__ lse, int32_t* __restrict__ err) {
     extern __shared__ __align__(16) float sm[];
-    float *qs = sm, *kv = qs + BM * kPitch<D>, *ps = kv + 4 * kB * kPitch<D>;  // two stages of K and V
+    constexpr int T = BM * 4, kGroup = ST * 2 * kB * kPitch<D> + BM * kPPitch;
+    const int g = threadIdx.x / T, tid = threadIdx.x % T, ty = tid >> 4, tx = tid & 15;
+    float *qs = sm, *kv = qs + BM * kPitch<D> + g * kGroup, *ps = kv + ST * 2 * kB * kPitch<D>;
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         attn_check_table(cu_q, A.n_seqs, A.total_q, err);
         attn_check_table(cu_k, A.n_seqs, A.total_k, err);
     }
     const AttnBlock B = attn_find_block(A, cu_q, cu_k, BM, blockIdx.x, false);
     if (!B.found) return;
-    const int h = blockIdx.y, hk = h / A.G, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int h = blockIdx.y, hk = h / A.G;
     const int off = B.lk - B.lq, end = min(B.lk, min(B.first + BM, B.lq) + off);  // keys some row sees: [0, end)
     const float *kb = k + B.k0 * A.sk + (int64_t)hk * D, *vb = v + B.k0 * A.sv + (int64_t)hk * D;
     auto load = [&](int stage, int j0) {  // keys that no row of the block sees are zeros: what they hold stays out
-        copy_rows<D, kB>(kv + 2 * stage * kB * kPitch<D>, kb, A.sk, j0, end);
-        copy_rows<D, kB>(kv + (2 * stage + 1) * kB * kPitch<D>, vb, A.sv, j0, end);
+        copy_rows<D, kB, T>(kv + 2 * stage * kB * kPitch<D>, kb, A.sk, j0, end, tid);
+        copy_rows<D, kB, T>(kv + (2 * stage + 1) * kB * kPitch<D>, vb, A.sv, j0, end, tid);
         copy_commit();
     };
-    copy_rows<D, BM>(qs, q + B.q0 * A.sq + (int64_t)h * D, A.sq, B.first, B.lq);
-    if (end > 0) load(0, 0);
+    copy_rows<D, BM, T * W>(qs, q + B.q0 * A.sq + (int64_t)h * D, A.sq, B.first, B.lq, threadIdx.x);
+    copy_commit();
+    load(0, g * kB);
+    copy_wait(1);
+    if (W > 1) __syncthreads();  // the query rows are every group's
     const float cs = A.scale * kLog2e;
     float m[4], l[4], acc[4][D / 16];
 #pragma unroll
@@ -169,14 +200,14 @@ attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __rest
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
     }
-    for (int j0 = 0, stage = 0; j0 < end; j0 += kB, stage ^= 1) {
-        const bool more = j0 + kB < end;
-        if (more) load(stage ^ 1, j0 + kB);
-        copy_wait(more);
-        __syncthreads();
+    for (int j0 = g * kB, stage = 0; j0 < end; j0 += W * kB, stage ^= ST - 1) {
+        const bool more = j0 + W * kB < end;
+        if (ST == 2 && more) load(stage ^ 1, j0 + W * kB);
+        copy_wait(ST == 2 && more);
+        group_sync<T>(g);
         const float *ks = kv + 2 * stage * kB * kPitch<D>, *vs = ks + kB * kPitch<D>;
         float s[4][4];
-        scores<D, 4, 4>(qs, ks, ty, tx, s);
+        scores<D, 16>(qs, ks, ty, tx, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int last = B.first + ty * 4 + i + off;  // last key the row sees
@@ -203,7 +234,32 @@ attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __rest
         }
         __syncwarp();  // a row's weights are written and read by one half of a warp
         add_rows<D, 4>(ps, vs, ty, tx, acc, j0 + kB > B.first + off);
+        group_sync<T>(g);
+        if (ST == 1 && more) load(0, j0 + W * kB);
+    }
+    copy_wait(0);
+    if (W > 1) {  // the groups' references made one, then their sums
         __syncthreads();
+        float* ms = sm;
+        if (tx == 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ms[g * BM + ty * 4 + i] = m[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mn = ms[ty * 4 + i];
+#pragma unroll
+            for (int o = 1; o < W; ++o) mn = fmaxf(mn, ms[o * BM + ty * 4 + i]);
+            const float corr = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
+            m[i] = mn;
+            l[i] *= corr;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) acc[i][c] *= corr;
+        }
+        group_sums<W, T>(sm + W * BM, g, tid, l);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) group_sums<W, T>(sm + W * BM, g, tid, acc[i]);
+        if (g > 0) return;
     }
     float inv[4];
 #pragma unroll
@@ -212,7 +268,6 @@ attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __rest
         const int p = B.first + ty * 4 + i;
         if (tx == 0 && p < B.lq) lse[(B.q0 + p) * A.Hq + h] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
     }
-    copy_wait(0);
     store_rows<D, 4>(out + B.q0 * A.Hq * D + (int64_t)h * D, (int64_t)A.Hq * D, B.first, B.lq, ty, tx, acc, inv);
 }
 
@@ -233,17 +288,17 @@ attn_delta_kernel(int64_t rows, const float* __restrict__ out, const float* __re
 }
 
 // Probabilities and score gradients of a tile from its recomputed scores:
-// s -> p, dp -> ds (times the scale).  lse and delta of rows ty MI + i.
-template <int MI, int NJ>
-__device__ __forceinline__ void tile_grad(float (&s)[MI][NJ], float (&dp)[MI][NJ], const float (&lse2)[MI],
-                                          const float (&dl)[MI], float cs, float scale, int row0, int key0, int ty,
-                                          int tx, int off, int lq, int lk) {
+// s -> p, dp -> ds (times the scale).  lse and delta of rows ty 4 + i, keys tx + NX j.
+template <int NX>
+__device__ __forceinline__ void tile_grad(float (&s)[4][4], float (&dp)[4][4], const float (&lse2)[4],
+                                          const float (&dl)[4], float cs, float scale, int row0, int key0, int ty, int tx,
+                                          int off, int lq, int lk) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int row = row0 + ty * MI + i;
+    for (int i = 0; i < 4; ++i) {
+        const int row = row0 + ty * 4 + i;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int key = key0 + tx + 16 * j;
+        for (int j = 0; j < 4; ++j) {
+            const int key = key0 + tx + NX * j;
             const bool on = row < lq && key < lk && key <= row + off;
             s[i][j] = on ? exp2f(fmaf(s[i][j], cs, -lse2[i])) : 0.f;
             dp[i][j] = on ? s[i][j] * (dp[i][j] - dl[i]) * scale : 0.f;
@@ -251,76 +306,89 @@ __device__ __forceinline__ void tile_grad(float (&s)[MI][NJ], float (&dp)[MI][NJ
     }
 }
 
-// BN keys per block of one query head; ST stages of Q and dO.  dk, dv: [total_k][H][D], H heads of which this block
-// writes head blockIdx.y.
-template <int D, int BN, int ST>
-__global__ void __launch_bounds__(kThreads)
+// BN keys per block of one query head; W groups take the query tiles in turn, ST stages of Q and dO each.  dk, dv:
+// [total_k][H][D], H heads of which this block writes head blockIdx.y.
+template <int D, int BN, int W, int ST>
+__global__ void __launch_bounds__(BN * 4 * W)
 attn_dkdv_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                      const float* __restrict__ lse, const float* __restrict__ dout, const float* __restrict__ delta,
                      const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, float* __restrict__ dk,
                      float* __restrict__ dv, int32_t* __restrict__ err) {
-    constexpr int KN = BN / 16;
+    constexpr int T = BN * 4, NX = BN / 4, kGroup = ST * 2 * kB * kPitch<D> + 2 * BN * kPPitch;
     extern __shared__ __align__(16) float sm[];
-    float *ks = sm, *vs = ks + BN * kPitch<D>, *qo = vs + BN * kPitch<D>;  // ST stages of Q and dO
-    float *pt = qo + ST * 2 * kB * kPitch<D>, *dt = pt + BN * kPPitch;     // [key][row]
+    const int g = threadIdx.x / T, tid = threadIdx.x % T, ty = tid >> 4, tx = tid & 15;  // of the gradients
+    const int sy = tid / NX, sx = tid % NX;                                                // of the scores
+    float *ks = sm, *vs = ks + BN * kPitch<D>, *qo = vs + BN * kPitch<D> + g * kGroup;
+    float *pt = qo + ST * 2 * kB * kPitch<D>, *dt = pt + BN * kPPitch;  // [key][row]
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         attn_check_table(cu_q, A.n_seqs, A.total_q, err);
         attn_check_table(cu_k, A.n_seqs, A.total_k, err);
     }
     const AttnBlock B = attn_find_block(A, cu_q, cu_k, BN, blockIdx.x, true);
     if (!B.found) return;
-    const int h = blockIdx.y, hk = h / A.G, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const int off = B.lk - B.lq;
+    const int h = blockIdx.y, hk = h / A.G, off = B.lk - B.lq;
     const float *qb = q + B.q0 * A.sq + (int64_t)h * D, *ob = dout + B.q0 * A.Hq * D + (int64_t)h * D;
     auto load = [&](int stage, int r0) {
-        copy_rows<D, kB>(qo + 2 * stage * kB * kPitch<D>, qb, A.sq, r0, B.lq);
-        copy_rows<D, kB>(qo + (2 * stage + 1) * kB * kPitch<D>, ob, (int64_t)A.Hq * D, r0, B.lq);
+        copy_rows<D, kB, T>(qo + 2 * stage * kB * kPitch<D>, qb, A.sq, r0, B.lq, tid);
+        copy_rows<D, kB, T>(qo + (2 * stage + 1) * kB * kPitch<D>, ob, (int64_t)A.Hq * D, r0, B.lq, tid);
         copy_commit();
     };
     const int i0 = max(0, B.first - off) / kB * kB;  // first tile of rows that see the block's first key
-    copy_rows<D, BN>(ks, k + B.k0 * A.sk + (int64_t)hk * D, A.sk, B.first, B.lk);
-    copy_rows<D, BN>(vs, v + B.k0 * A.sv + (int64_t)hk * D, A.sv, B.first, B.lk);
-    if (i0 < B.lq) load(0, i0);
-    float ak[KN][D / 16], av[KN][D / 16];
+    copy_rows<D, BN, T * W>(ks, k + B.k0 * A.sk + (int64_t)hk * D, A.sk, B.first, B.lk, threadIdx.x);
+    copy_rows<D, BN, T * W>(vs, v + B.k0 * A.sv + (int64_t)hk * D, A.sv, B.first, B.lk, threadIdx.x);
+    copy_commit();
+    load(0, i0 + g * kB);
+    copy_wait(1);
+    if (W > 1) __syncthreads();
+    float ak[4][D / 16], av[4][D / 16];
 #pragma unroll
-    for (int i = 0; i < KN; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) ak[i][c] = av[i][c] = 0.f;
     const float cs = A.scale * kLog2e;
-    for (int r0 = i0, stage = 0; r0 < B.lq; r0 += kB, stage ^= ST - 1) {
-        const bool more = r0 + kB < B.lq;
-        if (ST == 2 && more) load(stage ^ 1, r0 + kB);
+    for (int r0 = i0 + g * kB, stage = 0; r0 < B.lq; r0 += W * kB, stage ^= ST - 1) {
+        const bool more = r0 + W * kB < B.lq;
+        if (ST == 2 && more) load(stage ^ 1, r0 + W * kB);
         float lse2[4], dl[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t row = B.q0 + min(r0 + ty * 4 + i, B.lq - 1);
+            const int64_t row = B.q0 + min(r0 + sy * 4 + i, B.lq - 1);
             lse2[i] = __ldg(lse + row * A.Hq + h) * kLog2e;
             dl[i] = __ldg(delta + row * A.Hq + h);
         }
         copy_wait(ST == 2 && more);
-        __syncthreads();
+        group_sync<T>(g);
         const float *qs = qo + 2 * stage * kB * kPitch<D>, *os = qs + kB * kPitch<D>;
-        float s[4][KN], dp[4][KN];
-        scores<D, 4, KN>(qs, ks, ty, tx, s);
-        scores<D, 4, KN>(os, vs, ty, tx, dp);
-        tile_grad(s, dp, lse2, dl, cs, A.scale, r0, B.first, ty, tx, off, B.lq, B.lk);
+        float s[4][4], dp[4][4];
+        scores<D, NX>(qs, ks, sy, sx, s);
+        scores<D, NX>(os, vs, sy, sx, dp);
+        tile_grad<NX>(s, dp, lse2, dl, cs, A.scale, r0, B.first, sy, sx, off, B.lq, B.lk);
 #pragma unroll
-        for (int j = 0; j < KN; ++j) {
-            *reinterpret_cast<float4*>(pt + (tx + 16 * j) * kPPitch + ty * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-            *reinterpret_cast<float4*>(dt + (tx + 16 * j) * kPPitch + ty * 4) = make_float4(dp[0][j], dp[1][j], dp[2][j], dp[3][j]);
+        for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<float4*>(pt + (sx + NX * j) * kPPitch + sy * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+            *reinterpret_cast<float4*>(dt + (sx + NX * j) * kPPitch + sy * 4) = make_float4(dp[0][j], dp[1][j], dp[2][j], dp[3][j]);
         }
-        __syncthreads();
+        group_sync<T>(g);
         const bool skip = r0 + off < B.first + BN;
-        add_rows<D, KN>(pt, os, ty, tx, av, skip);
-        add_rows<D, KN>(dt, qs, ty, tx, ak, skip);
-        __syncthreads();
-        if (ST == 1 && more) load(0, r0 + kB);
+        add_rows<D, 4>(pt, os, ty, tx, av, skip);
+        add_rows<D, 4>(dt, qs, ty, tx, ak, skip);
+        group_sync<T>(g);
+        if (ST == 1 && more) load(0, r0 + W * kB);
     }
     copy_wait(0);
+    if (W > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            group_sums<W, T>(sm, g, tid, ak[i]);
+            group_sums<W, T>(sm, g, tid, av[i]);
+        }
+        if (g > 0) return;
+    }
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
     const int64_t H = gridDim.y, to = B.k0 * H * D + (int64_t)h * D;
-    store_rows<D, KN>(dk + to, H * D, B.first, B.lk, ty, tx, ak, one);
-    store_rows<D, KN>(dv + to, H * D, B.first, B.lk, ty, tx, av, one);
+    store_rows<D, 4>(dk + to, H * D, B.first, B.lk, ty, tx, ak, one);
+    store_rows<D, 4>(dv + to, H * D, B.first, B.lk, ty, tx, av, one);
 }
 
 // dk, dv of a kv head: the sums over its query heads, in order; rows of the sequences only.
@@ -346,27 +414,32 @@ attn_group_sum_kernel(AttnDims A, const int32_t* __restrict__ cu_k, const float*
     reinterpret_cast<float4*>(dv)[i] = y;
 }
 
-template <int D, int BM, int ST>
-__global__ void __launch_bounds__(BM * 4)
+template <int D, int BM, int W, int ST>
+__global__ void __launch_bounds__(BM * 4 * W)
 attn_dq_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                    const float* __restrict__ lse, const float* __restrict__ dout, const float* __restrict__ delta,
                    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, float* __restrict__ dq) {
     extern __shared__ __align__(16) float sm[];
-    float *qs = sm, *os = qs + BM * kPitch<D>, *kv = os + BM * kPitch<D>;  // ST stages of K and V
-    float* ds = kv + ST * 2 * kB * kPitch<D>;                               // [row][key]
+    constexpr int T = BM * 4, kGroup = ST * 2 * kB * kPitch<D> + BM * kPPitch;
+    const int g = threadIdx.x / T, tid = threadIdx.x % T, ty = tid >> 4, tx = tid & 15;
+    float *qs = sm, *os = qs + BM * kPitch<D>, *kv = os + BM * kPitch<D> + g * kGroup;
+    float* ds = kv + ST * 2 * kB * kPitch<D>;  // [row][key]
     const AttnBlock B = attn_find_block(A, cu_q, cu_k, BM, blockIdx.x, false);
     if (!B.found) return;
-    const int h = blockIdx.y, hk = h / A.G, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int h = blockIdx.y, hk = h / A.G;
     const int off = B.lk - B.lq, end = min(B.lk, min(B.first + BM, B.lq) + off);
     const float *kb = k + B.k0 * A.sk + (int64_t)hk * D, *vb = v + B.k0 * A.sv + (int64_t)hk * D;
     auto load = [&](int stage, int j0) {
-        copy_rows<D, kB>(kv + 2 * stage * kB * kPitch<D>, kb, A.sk, j0, end);
-        copy_rows<D, kB>(kv + (2 * stage + 1) * kB * kPitch<D>, vb, A.sv, j0, end);
+        copy_rows<D, kB, T>(kv + 2 * stage * kB * kPitch<D>, kb, A.sk, j0, end, tid);
+        copy_rows<D, kB, T>(kv + (2 * stage + 1) * kB * kPitch<D>, vb, A.sv, j0, end, tid);
         copy_commit();
     };
-    copy_rows<D, BM>(qs, q + B.q0 * A.sq + (int64_t)h * D, A.sq, B.first, B.lq);
-    copy_rows<D, BM>(os, dout + B.q0 * A.Hq * D + (int64_t)h * D, (int64_t)A.Hq * D, B.first, B.lq);
-    if (end > 0) load(0, 0);
+    copy_rows<D, BM, T * W>(qs, q + B.q0 * A.sq + (int64_t)h * D, A.sq, B.first, B.lq, threadIdx.x);
+    copy_rows<D, BM, T * W>(os, dout + B.q0 * A.Hq * D + (int64_t)h * D, (int64_t)A.Hq * D, B.first, B.lq, threadIdx.x);
+    copy_commit();
+    load(0, g * kB);
+    copy_wait(1);
+    if (W > 1) __syncthreads();
     float lse2[4], dl[4], acc[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -377,36 +450,44 @@ attn_dq_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restr
         for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
     }
     const float cs = A.scale * kLog2e;
-    for (int j0 = 0, stage = 0; j0 < end; j0 += kB, stage ^= ST - 1) {
-        const bool more = j0 + kB < end;
-        if (ST == 2 && more) load(stage ^ 1, j0 + kB);
+    for (int j0 = g * kB, stage = 0; j0 < end; j0 += W * kB, stage ^= ST - 1) {
+        const bool more = j0 + W * kB < end;
+        if (ST == 2 && more) load(stage ^ 1, j0 + W * kB);
         copy_wait(ST == 2 && more);
-        __syncthreads();
+        group_sync<T>(g);
         const float *ks = kv + 2 * stage * kB * kPitch<D>, *vs = ks + kB * kPitch<D>;
         float s[4][4], dp[4][4];
-        scores<D, 4, 4>(qs, ks, ty, tx, s);
-        scores<D, 4, 4>(os, vs, ty, tx, dp);
-        tile_grad(s, dp, lse2, dl, cs, A.scale, B.first, j0, ty, tx, off, B.lq, B.lk);
+        scores<D, 16>(qs, ks, ty, tx, s);
+        scores<D, 16>(os, vs, ty, tx, dp);
+        tile_grad<16>(s, dp, lse2, dl, cs, A.scale, B.first, j0, ty, tx, off, B.lq, B.lk);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) ds[(ty * 4 + i) * kPPitch + tx + 16 * j] = dp[i][j];
         __syncwarp();
         add_rows<D, 4>(ds, ks, ty, tx, acc, j0 + kB > B.first + off);
-        __syncthreads();
-        if (ST == 1 && more) load(0, j0 + kB);
+        group_sync<T>(g);
+        if (ST == 1 && more) load(0, j0 + W * kB);
     }
     copy_wait(0);
+    if (W > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) group_sums<W, T>(sm, g, tid, acc[i]);
+        if (g > 0) return;
+    }
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
     store_rows<D, 4>(dq + B.q0 * A.Hq * D + (int64_t)h * D, (int64_t)A.Hq * D, B.first, B.lq, ty, tx, acc, one);
 }
 
-template <int D, int BM> constexpr size_t fwd_smem() { return ((BM + 4 * kB) * kPitch<D> + BM * kPPitch) * sizeof(float); }
-template <int D, int BM, int ST> constexpr size_t dq_smem() {
-    return ((2 * BM + ST * 2 * kB) * kPitch<D> + BM * kPPitch) * sizeof(float);
+template <int D, int BM, int W, int ST> constexpr size_t fwd_smem() {
+    return (BM * kPitch<D> + W * (ST * 2 * kB * kPitch<D> + BM * kPPitch)) * sizeof(float);
 }
-template <int D, int BN, int ST> constexpr size_t dkdv_smem() {
-    return ((2 * BN + ST * 2 * kB) * kPitch<D> + 2 * BN * kPPitch) * sizeof(float);
+template <int D, int BM, int W, int ST> constexpr size_t dq_smem() {
+    return (2 * BM * kPitch<D> + W * (ST * 2 * kB * kPitch<D> + BM * kPPitch)) * sizeof(float);
+}
+template <int D, int BN, int W, int ST> constexpr size_t dkdv_smem() {
+    return (2 * BN * kPitch<D> + W * (ST * 2 * kB * kPitch<D> + 2 * BN * kPPitch)) * sizeof(float);
 }
 
 template <class K>
@@ -416,32 +497,32 @@ cudaError_t allow_smem(DeviceCache& cache, K kernel, size_t bytes) {
     });
 }
 
-// Blocks of 32 rows (or keys) where 64 would give fewer than two blocks per SM: half the walk per block for a little
-// more traffic (813 tokens, 4 heads, d 64: forward 54 -> 31 us; 1500 tokens, 32 heads, d 128, 768 blocks: 64 is faster).
+// Blocks of 32 rows (or keys) where 64 would give fewer than two blocks per SM: half the walk per block, by several
+// groups of threads, for a little more traffic (813 tokens, 4/2 heads of 64: forward 54 -> 23 us, gradient 228 -> 70;
+// 1500 tokens, 32/8 heads of 128, 768 blocks: 64 is faster, 642 against 698 us).
 bool small_blocks(int64_t total, int n_seqs, int heads) { return (total / kB + n_seqs) * heads < 2 * 152; }
 
-template <int D, int BM>
+template <int D, int BM, int W, int ST>
 cudaError_t forward(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
                     const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
     static DeviceCache cache;
-    cudaError_t e = allow_smem(cache, attn_fwd_f32_kernel<D, BM>, fwd_smem<D, BM>());
+    cudaError_t e = allow_smem(cache, attn_fwd_f32_kernel<D, BM, W, ST>, fwd_smem<D, BM, W, ST>());
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(A.total_q / BM + A.n_seqs), (unsigned)A.Hq);
-    attn_fwd_f32_kernel<D, BM><<<grid, BM * 4, fwd_smem<D, BM>(), st>>>(A, q, k, v, cu_q, cu_k, out, lse, err);
+    attn_fwd_f32_kernel<D, BM, W, ST><<<grid, BM * 4 * W, fwd_smem<D, BM, W, ST>(), st>>>(A, q, k, v, cu_q, cu_k, out, lse, err);
     return cudaGetLastError();
 }
 
-template <int D, int BN>
+template <int D, int BN, int W, int ST>
 cudaError_t keys_backward(const AttnDims& A, const float* q, const float* k, const float* v, const float* lse,
                           const float* dout, const int32_t* cu_q, const int32_t* cu_k, float* dk, float* dv, float* delta,
                           float* parts, int32_t* err, cudaStream_t st) {
-    constexpr int ST = D == 64 ? 2 : 1;
     static DeviceCache cache;
-    cudaError_t e = allow_smem(cache, attn_dkdv_f32_kernel<D, BN, ST>, dkdv_smem<D, BN, ST>());
+    cudaError_t e = allow_smem(cache, attn_dkdv_f32_kernel<D, BN, W, ST>, dkdv_smem<D, BN, W, ST>());
     if (e != cudaSuccess) return e;
     float *pk = A.G > 1 ? parts : dk, *pv = A.G > 1 ? parts + A.total_k * A.Hq * D : dv;
-    attn_dkdv_f32_kernel<D, BN, ST><<<dim3((unsigned)(A.total_k / BN + A.n_seqs), (unsigned)A.Hq), kThreads,
-                                      dkdv_smem<D, BN, ST>(), st>>>(A, q, k, v, lse, dout, delta, cu_q, cu_k, pk, pv, err);
+    attn_dkdv_f32_kernel<D, BN, W, ST><<<dim3((unsigned)(A.total_k / BN + A.n_seqs), (unsigned)A.Hq), BN * 4 * W,
+                                      dkdv_smem<D, BN, W, ST>(), st>>>(A, q, k, v, lse, dout, delta, cu_q, cu_k, pk, pv, err);
     if (A.G > 1) {
         const int64_t n = A.total_k * A.Hkv * (D / 4);
         attn_group_sum_kernel<D><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(A, cu_k, pk, pv, dk, dv);
@@ -449,16 +530,15 @@ cudaError_t keys_backward(const AttnDims& A, const float* q, const float* k, con
     return cudaGetLastError();
 }
 
-template <int D, int BM>
+template <int D, int BM, int W, int ST>
 cudaError_t rows_backward(const AttnDims& A, const float* q, const float* k, const float* v, const float* lse,
                           const float* dout, const int32_t* cu_q, const int32_t* cu_k, float* dq, float* delta,
                           cudaStream_t st) {
-    constexpr int ST = D == 64 ? 2 : 1;
     static DeviceCache cache;
-    cudaError_t e = allow_smem(cache, attn_dq_f32_kernel<D, BM, ST>, dq_smem<D, BM, ST>());
+    cudaError_t e = allow_smem(cache, attn_dq_f32_kernel<D, BM, W, ST>, dq_smem<D, BM, W, ST>());
     if (e != cudaSuccess) return e;
-    attn_dq_f32_kernel<D, BM, ST><<<dim3((unsigned)(A.total_q / BM + A.n_seqs), (unsigned)A.Hq), BM * 4,
-                                    dq_smem<D, BM, ST>(), st>>>(A, q, k, v, lse, dout, delta, cu_q, cu_k, dq);
+    attn_dq_f32_kernel<D, BM, W, ST><<<dim3((unsigned)(A.total_q / BM + A.n_seqs), (unsigned)A.Hq), BM * 4 * W,
+                                    dq_smem<D, BM, W, ST>(), st>>>(A, q, k, v, lse, dout, delta, cu_q, cu_k, dq);
     return cudaGetLastError();
 }
 
@@ -472,12 +552,12 @@ cudaError_t backward(const AttnDims& A, const float* q, const float* k, const fl
     if (rows > 0) attn_delta_kernel<D><<<(unsigned)((rows + 7) / 8), kThreads, 0, st>>>(rows, out, dout, delta);
     if (A.total_k > 0)
         e = small_blocks(A.total_k, A.n_seqs, A.Hq)
-                ? keys_backward<D, 32>(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv, delta, parts, err, st)
-                : keys_backward<D, 64>(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv, delta, parts, err, st);
+                ? keys_backward<D, 32, kSmallGroups<D>, 1>(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv, delta, parts, err, st)
+                : keys_backward<D, 64, 1, D == 64 ? 2 : 1>(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv, delta, parts, err, st);
     if (e != cudaSuccess || rows == 0) return e;
     return small_blocks(A.total_q, A.n_seqs, A.Hq)
-               ? rows_backward<D, 32>(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, st)
-               : rows_backward<D, 64>(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, st);
+               ? rows_backward<D, 32, kSmallGroups<D>, 1>(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, st)
+               : rows_backward<D, 64, 1, D == 64 ? 2 : 1>(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, st);
 }
 
 // Rows of the sequences set to zero (and lse to -infinity): what attention and its gradient are without keys or queries.
@@ -507,10 +587,10 @@ cudaError_t launch_attention_f32(const AttnDims& A, const float* q, const float*
                                  const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
     const bool small = small_blocks(A.total_q, A.n_seqs, A.Hq);
     if (A.d == 128)
-        return small ? forward<128, 32>(A, q, k, v, cu_q, cu_k, out, lse, err, st)
-                     : forward<128, 64>(A, q, k, v, cu_q, cu_k, out, lse, err, st);
-    return small ? forward<64, 32>(A, q, k, v, cu_q, cu_k, out, lse, err, st)
-                 : forward<64, 64>(A, q, k, v, cu_q, cu_k, out, lse, err, st);
+        return small ? forward<128, 32, kSmallGroups<128>, 1>(A, q, k, v, cu_q, cu_k, out, lse, err, st)
+                     : forward<128, 64, 1, 2>(A, q, k, v, cu_q, cu_k, out, lse, err, st);
+    return small ? forward<64, 32, kSmallGroups<64>, 1>(A, q, k, v, cu_q, cu_k, out, lse, err, st)
+                 : forward<64, 64, 1, 2>(A, q, k, v, cu_q, cu_k, out, lse, err, st);
 }
 size_t attention_backward_f32_floats(const AttnDims& A) {
     return (size_t)((A.total_q * A.Hq + 63) / 64 * 64 + (A.G > 1 ? 2 * A.total_k * A.Hq * A.d : 0));
