@@ -1,5 +1,11 @@
 // Decode step of a full softmax layer: one query token per sequence over the
 // paged cache.  See attention_decode.cuh for the cut over blocks.
+//
+// Bound by the cache's bytes.  32/8 heads of 128: 64 sequences of 8192 tokens of
+// 8-bit rows in 173 us (6.2 TB/s), of bf16 rows in 301 us (7.1), 8 of fp32 rows in
+// 129 us; one sequence of 131072 in 50 us (8-bit) and 83 us (bf16).  8-bit rows
+// take two conversions per four values on the way to the products, which is
+// what keeps them behind bf16's rate.  The join takes 7 to 8 us of these.
 #include <cuda_fp8.h>
 
 #include <algorithm>
