@@ -7,7 +7,6 @@ calling into the library without a built ``libhla.so`` raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -440,9 +439,6 @@ def _check_tensor(t, fn: str, name: str, dtype, shape, device, strided: bool = F
     return t.stride(0)
 
 
-_HERE_CTX = contextlib.nullcontext()
-
-
 @functools.lru_cache(maxsize=256)
 def _c(params, *strides):
     """A frozen parameter set's C form, by reference; made once per set and strides, never changed."""
@@ -454,15 +450,27 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
+# A device's current stream as an int.  (Through torch.cuda.current_stream it takes 2 us, a tenth of a small call.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _here(device, stream):
+    """The current stream of `device` as an int, or None if `stream` or `device` has to be made current first."""
+    if device.type != "cuda":
+        _refuse(f"expected CUDA tensors, got {device}")
+    if stream is not None or device.index != torch.cuda.current_device():
+        return None
+    return _raw_stream(device.index)
+
+
 def _on(device, stream):
-    """(context for the call's allocations and launches, stream argument): `device` current, and `stream`
-    too if one is given, so that buffers allocated here belong to the stream that uses them."""
-    _need(device.type == "cuda", f"expected CUDA tensors, got {device}")
-    if stream is not None:
-        _need(stream.device == device, f"expected a stream of {device}, got one of {stream.device}")
-        return torch.cuda.stream(stream), stream.cuda_stream
-    here = device.index == torch.cuda.current_device()
-    return _HERE_CTX if here else torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    """A context with `device` current, and `stream` too if one is given, so that buffers allocated in it belong
+    to the stream that uses them."""
+    if stream is None:
+        return torch.cuda.device(device)
+    _need(stream.device == device, f"expected a stream of {device}, got one of {stream.device}")
+    return torch.cuda.stream(stream)
 
 
 @dataclass(frozen=True)
@@ -512,13 +520,15 @@ def _rope(fn, params, q, k, positions, q_out, k_out, stream):
             _need(o.shape == x.shape and o.dtype == x.dtype and o.stride() == x.stride(), f"{fn}: {name}_out in place")
         else:
             _check_tensor(o, fn, name + "_out", dt, shape, dev)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        for i, x in enumerate((q, k)):
-            if x is not None and outs[i] is None:
-                outs[i] = torch.empty(x.shape, dtype=dt, device=dev)
-        _check(getattr(load(), fn)(_c(params, *strides), _adr(q), _adr(k), _adr(positions), n, _adr(outs[0]),
-                                   _adr(outs[1]), st), fn)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return _rope(fn, params, q, k, positions, q_out, k_out, None)
+    for i, x in enumerate((q, k)):
+        if x is not None and outs[i] is None:
+            outs[i] = torch.empty(x.shape, dtype=dt, device=dev)
+    _check(getattr(load(), fn)(_c(params, *strides), _adr(q), _adr(k), _adr(positions), n, _adr(outs[0]),
+                               _adr(outs[1]), st), fn)
     return outs[0], outs[1]
 
 
@@ -574,23 +584,26 @@ def _check_packed(fn, params, q, k, v, cu_q, cu_k, ws):
     """Checks the inputs shared by attention and its gradient; returns (strides, total_q, total_k, n_seqs)."""
     dt = _TORCH.get(params.dtype)
     _need(dt is not None and dt != torch.uint8, f"{fn}: dtype")
-    _need(all(isinstance(x, torch.Tensor) and x.dim() == 3 for x in (q, k, v)), f"{fn}: q, k, v must be [T, H, d]")
-    _need(isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 and cu_q.numel() >= 2, f"{fn}: cu_seqlens_q")
-    dev, d, n = q.device, params.head_dim, cu_q.numel() - 1
-    strides = (_check_tensor(q, fn, "q", dt, (q.shape[0], params.n_q_heads, d), dev, strided=True),
-               _check_tensor(k, fn, "k", dt, (k.shape[0], params.n_kv_heads, d), dev, strided=True),
-               _check_tensor(v, fn, "v", dt, (k.shape[0], params.n_kv_heads, d), dev, strided=True))
+    for x in (q, k, v):
+        if not isinstance(x, torch.Tensor) or x.dim() != 3:
+            _refuse(f"{fn}: q, k, v must be [T, H, d]")
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.numel() < 2:
+        _refuse(f"{fn}: cu_seqlens_q")
+    dev, d, n, tq, tk = q.device, params.head_dim, cu_q.numel() - 1, q.shape[0], k.shape[0]
+    strides = (_check_tensor(q, fn, "q", dt, (tq, params.n_q_heads, d), dev, strided=True),
+               _check_tensor(k, fn, "k", dt, (tk, params.n_kv_heads, d), dev, strided=True),
+               _check_tensor(v, fn, "v", dt, (tk, params.n_kv_heads, d), dev, strided=True))
     _check_tensor(cu_q, fn, "cu_seqlens_q", torch.int32, (n + 1,), dev)
     if cu_k is not None:
         _check_tensor(cu_k, fn, "cu_seqlens_k", torch.int32, (n + 1,), dev)
     _check_workspace(fn, ws, dev)
-    return strides, q.shape[0], k.shape[0], n
+    return strides, tq, tk, n
 
 
 def _check_workspace(fn, ws, dev):
-    if ws is not None:
-        _need(isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev,
-              f"{fn}: ws must be a dense uint8 tensor on {dev}")
+    if ws is not None and not (isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.is_contiguous() and
+                               ws.device == dev):
+        _refuse(f"{fn}: ws must be a dense uint8 tensor on {dev}")
 
 
 def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, ws=None, stream=None):
@@ -603,17 +616,19 @@ def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=
         _check_tensor(out, "hla_attention", "out", q.dtype, shape, dev)
     if lse is not None:
         _check_tensor(lse, "hla_attention", "lse", torch.float32, shape[:2], dev)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=dev)
-        if lse is None:
-            lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = alloc_attention_workspace(params, tq, tk, n, device=dev)
-        _check(load().hla_attention(_c(params, *strides), _adr(q), _adr(k), _adr(v), _adr(cu_seqlens_q),
-                                    _adr(cu_seqlens_k), n, tq, tk, _adr(out), _adr(lse), _adr(ws), ws.numel(), st),
-               "hla_attention")
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return attention(params, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, ws)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = alloc_attention_workspace(params, tq, tk, n, device=dev)
+    _check(load().hla_attention(_c(params, *strides), _adr(q), _adr(k), _adr(v), _adr(cu_seqlens_q),
+                                _adr(cu_seqlens_k), n, tq, tk, _adr(out), _adr(lse), _adr(ws), ws.numel(), st),
+           "hla_attention")
     return out, lse
 
 
@@ -630,16 +645,18 @@ def attention_backward(params: AttnParams, q, k, v, out, lse, dout, cu_seqlens_q
     if grads is not None:
         for name, x in zip("qkv", (q, k, v)):
             _check_tensor(grads.get(name), fn, "grads." + name, x.dtype, tuple(x.shape), dev)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if grads is None:
-            grads = {name: torch.empty(x.shape, dtype=x.dtype, device=dev) for name, x in zip("qkv", (q, k, v))}
-        if ws is None:
-            ws = alloc_attention_workspace(params, tq, tk, n, backward=True, device=dev)
-        _check(load().hla_attention_backward(_c(params, *strides), _adr(q), _adr(k), _adr(v), _adr(out),
-                                             _adr(lse), _adr(dout), _adr(cu_seqlens_q), _adr(cu_seqlens_k), n, tq, tk,
-                                             _adr(grads["q"]), _adr(grads["k"]), _adr(grads["v"]), _adr(ws),
-                                             ws.numel(), st), fn)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return attention_backward(params, q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, grads, ws)
+    if grads is None:
+        grads = {name: torch.empty(x.shape, dtype=x.dtype, device=dev) for name, x in zip("qkv", (q, k, v))}
+    if ws is None:
+        ws = alloc_attention_workspace(params, tq, tk, n, backward=True, device=dev)
+    _check(load().hla_attention_backward(_c(params, *strides), _adr(q), _adr(k), _adr(v), _adr(out), _adr(lse),
+                                         _adr(dout), _adr(cu_seqlens_q), _adr(cu_seqlens_k), n, tq, tk,
+                                         _adr(grads["q"]), _adr(grads["k"]), _adr(grads["v"]), _adr(ws), ws.numel(),
+                                         st), fn)
     return grads
 
 
@@ -695,9 +712,11 @@ class Cache:
     def check_error(self, stream=None) -> int:
         """Synchronises, reads and clears the cache's error word; returns it (0 = fine)."""
         code = ctypes.c_int32()
-        ctx, st = _on(self.device, stream)
-        with ctx:
-            rc = load().hla_check_cache_error(self.c, st, ctypes.byref(code))
+        st = _here(self.device, stream)
+        if st is None:
+            with _on(self.device, stream):
+                return self.check_error()
+        rc = load().hla_check_cache_error(self.c, st, ctypes.byref(code))
         if rc not in (HLA_OK, HLA_ERR_STATE, HLA_ERR_TIMEOUT):
             _check(rc, "cache error word")
         return code.value
@@ -717,10 +736,12 @@ def cache_write(cache: Cache, k, v, cu_seqlens, start, stream=None):
     shape = (k.shape[0], p.n_kv_heads, p.head_dim)
     for t, name in ((k, "k"), (v, "v")):
         _check_tensor(t, fn, name, _TORCH[p.dtype], shape, cache.device)
-    ctx, st = _on(cache.device, stream)
-    with ctx:
-        _check(load().hla_cache_write(cache.cp, cache.c, _adr(k), _adr(v),
-                                      _adr(cu_seqlens), _adr(start), cache.n_seqs, shape[0], st), fn)
+    st = _here(cache.device, stream)
+    if st is None:
+        with _on(cache.device, stream):
+            return cache_write(cache, k, v, cu_seqlens, start)
+    _check(load().hla_cache_write(cache.cp, cache.c, _adr(k), _adr(v), _adr(cu_seqlens), _adr(start), cache.n_seqs,
+                                  shape[0], st), fn)
 
 
 def cache_read(cache: Cache, cu_seqlens, start, total_tokens: int, k=None, v=None, stream=None):
@@ -732,11 +753,13 @@ def cache_read(cache: Cache, cu_seqlens, start, total_tokens: int, k=None, v=Non
     for t, name in ((k, "k"), (v, "v")):
         if t is not None:
             _check_tensor(t, fn, name, dt, shape, cache.device)
-    ctx, st = _on(cache.device, stream)
-    with ctx:
-        out = [torch.empty(shape, dtype=dt, device=cache.device) if t is None else t for t in (k, v)]
-        _check(load().hla_cache_read(cache.cp, cache.c, _adr(cu_seqlens), _adr(start),
-                                     cache.n_seqs, total_tokens, _adr(out[0]), _adr(out[1]), st), fn)
+    st = _here(cache.device, stream)
+    if st is None:
+        with _on(cache.device, stream):
+            return cache_read(cache, cu_seqlens, start, total_tokens, k, v)
+    out = [torch.empty(shape, dtype=dt, device=cache.device) if t is None else t for t in (k, v)]
+    _check(load().hla_cache_read(cache.cp, cache.c, _adr(cu_seqlens), _adr(start), cache.n_seqs, total_tokens,
+                                 _adr(out[0]), _adr(out[1]), st), fn)
     return out[0], out[1]
 
 
@@ -762,13 +785,14 @@ def attention_decode(params: AttnParams, cache: Cache, q, lens, out=None, ws=Non
     if out is not None:
         _check_tensor(out, fn, "out", dt, shape, dev)
     _check_workspace(fn, ws, dev)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
-        if ws is None:
-            ws = alloc_decode_workspace(params, cache)
-        _check(load().hla_attention_decode(_c(params, stride), cache.cp,
-                                           cache.c, _adr(q), _adr(lens), cache.n_seqs, _adr(out),
-                                           _adr(ws), ws.numel(), st), fn)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream):
+            return attention_decode(params, cache, q, lens, out, ws)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+    if ws is None:
+        ws = alloc_decode_workspace(params, cache)
+    _check(load().hla_attention_decode(_c(params, stride), cache.cp, cache.c, _adr(q), _adr(lens), cache.n_seqs,
+                                       _adr(out), _adr(ws), ws.numel(), st), fn)
     return out
