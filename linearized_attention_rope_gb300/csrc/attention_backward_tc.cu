@@ -15,18 +15,23 @@
 // what the two extra products cost.  No gradient is summed outside a block, so
 // shared kv heads need no second pass either.
 //
+// P and dS are rounded to bf16 (the inputs' own precision) and are read by the
+// products from TMEM, over the columns of the scores they came from.  The
+// roundings of many keys average out in a sum over them; those of few do not:
+// query tiles that see one key tile (dQ) and sequences of one key tile (dK, dV)
+// take what the rounding leaves as a second bf16 value and a second product
+// (errors of sequences up to 128 keys 1.25 to 1.46 -> 1.00 times the rounding of
+// the result; 19 x 64 tokens 29 -> 31.6 us).
+//
 // D comes from the stored output, whose rounding matters where few keys are
 // seen (O is then as large as a value, and its error moves all of a row's dS the
 // same way): rows that see one key tile get D = sum_j P_ij dP_ij from the dq
 // kernel instead, which runs first and leaves it for the other.  (Rows of more
 // keys: O is smaller by the root of their number.  With the stored output alone
-// dq was off by 2.0 roundings of bf16 for sequences of 10 to 50 rows, with this
-// 1.4: the result's own and that of dS.)
+// dq was off by 2.0 roundings of bf16 for sequences of 10 to 50 rows.)
 //
-// P and dS are rounded to bf16 (the inputs' own precision) and are read by the
-// products from TMEM, over the columns of the scores they came from.  Products
-// and elementwise work alternate: while dV and the next S are formed, dS is
-// computed from dP; while dK and the next dP are formed, the next P.
+// Products and elementwise work alternate: while dV and the next S are formed,
+// dS is computed from dP; while dK and the next dP are formed, the next P.
 //
 // Bound by the tensor cores: 14 d flops per visible score.  bf16, 32/8 heads of
 // 128: 32768 tokens in 18.1 to 18.5 ms (1670 to 1700 TFLOP/s of the 14 d, 1190 to
@@ -125,11 +130,33 @@ __device__ __forceinline__ void outer_product(uint32_t d, uint64_t a, uint64_t b
     }
 }
 template <int D>
-__device__ __forceinline__ void inner_product(uint32_t d, uint32_t a_cols, uint64_t b, bool add, uint32_t lead) {
+__device__ __forceinline__ void inner_product(uint32_t d, uint32_t a_cols, uint64_t b, bool add, bool fine,
+                                              uint32_t lead) {
     const uint32_t idesc = umma::idesc_bf16(kRows, D, false, true);  // d += a b over the 128 rows of b
 #pragma unroll
     for (int s = 0; s < kRows / 16; ++s)
         umma::mma_ts_lead(d, half_step(a_cols, s), b + (uint64_t)(s * 128), idesc, add || s > 0, lead);
+    if (fine)  // the second parts of a
+#pragma unroll
+        for (int s = 0; s < kRows / 16; ++s)
+            umma::mma_ts_lead(d, half_step(a_cols + 32, s), b + (uint64_t)(s * 128), idesc, true, lead);
+}
+
+// A warpgroup's 64 values a lane to its 32 columns for the product, as bf16 (with `fine`: and what that leaves, to the
+// 32 columns behind them).
+__device__ __forceinline__ void store64(uint32_t taddr, const float2 (&x)[32], bool fine) {
+    uint32_t w[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) w[e] = pack_bf2(x[e].x, x[e].y);
+    umma::tmem_st32_async(taddr, w);
+    if (fine) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            w[e] = pack_bf2(x[e].x - __uint_as_float(w[e] << 16), x[e].y - __uint_as_float(w[e] & 0xffff0000u));
+        umma::tmem_st32_async(taddr + 32, w);
+    }
+    umma::tmem_wait_st();
+    umma::fence_before_sync();
 }
 
 // ---- dk, dv -----------------------------------------------------------------
@@ -276,6 +303,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 if (__shfl_sync(0xffffffffu, it.head, 0) < 0) break;
                 const Span sp = span(it);
                 const int n = sp.n;
+                const bool fine = __shfl_sync(0xffffffffu, it.lk, 0) <= kRows;
                 if (n == 0) continue;
                 int r = 0;
                 auto ready_q = [&](const Ring& q) {  // a tile's Q (of a last tile both, cleared behind the last row)
@@ -308,7 +336,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     const Ring q1 = more ? ring.next() : q, o1 = more ? ring.next() : o;
                     named_sync(kBarP, 288);
                     umma::fence_after_sync();
-                    if (ok) inner_product<D>(cV, cS, at(ring_mn, o), i > 0, lead);
+                    if (ok) inner_product<D>(cV, cS, at(ring_mn, o), i > 0, fine, lead);
                     done(bar_empty + 8 * o.slot);
                     if (more) {
                         ready_q(q1);
@@ -317,7 +345,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     }
                     named_sync(kBarDs, 288);
                     umma::fence_after_sync();
-                    if (ok) inner_product<D>(cK, cP, at(ring_mn, q), i > 0, lead);
+                    if (ok) inner_product<D>(cK, cP, at(ring_mn, q), i > 0, fine, lead);
                     done(bar_empty + 8 * q.slot);
                     if (more) {
                         ready_o(o1);
@@ -392,12 +420,14 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         for (int x = 0;; ++x) {
             int n, per, ahead;  // tiles; tiles per head group; first row that sees the key, from the first tile's start
             int64_t at;         // the key's place in the results (-1: none)
+            bool fine;
             {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (it.head < 0) break;
                 const Span sp = span(it);
                 const int key = it.first + (tid & 127);
                 n = sp.n;
+                fine = it.lk <= kRows;
                 per = sp.per;
                 ahead = key - (it.lk - it.lq) - (sp.i0 << lqb);
                 at = key < it.lk ? ((int64_t)it.k0 + key) * A.Hkv + it.head : -1;
@@ -426,12 +456,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                         p[e].y = 2 * e + 1 >= from ? p[e].y : 0.f;
                     }
                 }
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = pack_bf2(p[e].x, p[e].y);
-                umma::tmem_st32_async(tS, w);
-                umma::tmem_wait_st();
-                umma::fence_before_sync();
+                store64(tS, p, fine);
                 named_arrive(kBarP, 288);
                 named_sync(kBarDp, 288);
                 umma::fence_after_sync();
@@ -440,14 +465,10 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     const float4 nd = *reinterpret_cast<const float4*>(st + 128 + 2 * e);
-                    const float2 a = fmul2(p[e], fadd2(d[e], make_float2(nd.x, nd.y)));
-                    const float2 b = fmul2(p[e + 1], fadd2(d[e + 1], make_float2(nd.z, nd.w)));
-                    w[e] = pack_bf2(a.x, a.y);
-                    w[e + 1] = pack_bf2(b.x, b.y);
+                    d[e] = fmul2(p[e], fadd2(d[e], make_float2(nd.x, nd.y)));
+                    d[e + 1] = fmul2(p[e + 1], fadd2(d[e + 1], make_float2(nd.z, nd.w)));
                 }
-                umma::tmem_st32_async(tP, w);
-                umma::tmem_wait_st();
-                umma::fence_before_sync();
+                store64(tP, d, fine);
                 named_arrive(kBarDs, 288);
             }
             // ---- results: dv by the first warpgroup, dk by the second
@@ -666,7 +687,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                     named_sync(kBarDs + b, 288);
                     umma::fence_after_sync();
                     if (ok)
-                        inner_product<D>(cQ, cP + b * 128, ring_mn + (uint64_t)(k * (C::kTile / 16)), i > 0, lead);
+                        inner_product<D>(cQ, cP + b * 128, ring_mn + (uint64_t)(k * (C::kTile / 16)), i > 0, n == 1, lead);
                     if (i + 1 == n) done(bar_done);
                     done(bar_empty + 8 * k);
                     k = k1;
@@ -770,19 +791,15 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                     nd = make_float2(-sum, -sum);
                     if (half == 0 && at >= 0) stats[at].y = -sum;
                 }
-                uint32_t w[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    float2 a = fmul2(p[e], fadd2(d[e], nd));
+                    d[e] = fmul2(p[e], fadd2(d[e], nd));
                     if (edge) {
-                        a.x = 2 * e < seen ? a.x : 0.f;
-                        a.y = 2 * e + 1 < seen ? a.y : 0.f;
+                        d[e].x = 2 * e < seen ? d[e].x : 0.f;
+                        d[e].y = 2 * e + 1 < seen ? d[e].y : 0.f;
                     }
-                    w[e] = pack_bf2(a.x, a.y);
                 }
-                umma::tmem_st32_async(tP, w);
-                umma::tmem_wait_st();
-                umma::fence_before_sync();
+                store64(tP, d, n == 1);
                 named_arrive(kBarDs + (t & 1), 288);
             }
             if (n > 0) ok = ok && wait_or_flag(bar_done, count & 1, err);
