@@ -468,10 +468,11 @@ HLA_API int hla_attention_workspace_bytes(const hla_attn_params* params, int64_t
  *       of exponentials (what hla_attention_backward needs)
  * A row that sees no key has out 0 and lse -infinity.  What a row does not see
  * does not reach it, infinities and NaN included (the padding of a batch may
- * hold anything).  Rows at and past c_n are left as they were.  A malformed table is clamped on the device (no
- * access out of range) and flagged in the workspace's error word.  bf16 layers
- * run on the tensor cores: fp32 scores and sums, probabilities rounded to bf16
- * for their product with v.  Asynchronous; deterministic. */
+ * hold anything).  Rows at and past c_n are left as they were.  A malformed
+ * table is clamped on the device (no access out of range) and flagged in the
+ * workspace's error word.  Outputs must not overlap inputs.  bf16 layers run on
+ * the tensor cores: fp32 scores and sums, probabilities rounded to bf16 for
+ * their product with v.  Asynchronous; deterministic. */
 HLA_API int hla_attention(const hla_attn_params* params, const void* q, const void* k, const void* v,
                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int n_seqs, int64_t total_q,
                           int64_t total_k, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
@@ -482,7 +483,7 @@ HLA_API int hla_attention(const hla_attn_params* params, const void* q, const vo
  * row sees have gradients 0; rows at and past c_n are left as they were.
  * Infinities and NaN of keys do not reach dq of rows before them; those of a
  * row's dout and q may reach dk and dv of keys up to 127 after it in its own
- * sequence (bf16 layers).
+ * sequence (bf16 layers).  Outputs must not overlap inputs or each other.
  * Asynchronous; deterministic (fixed order of sums, no atomics). */
 HLA_API int hla_attention_backward(const hla_attn_params* params, const void* q, const void* k, const void* v,
                                    const void* out, const float* lse, const void* dout,

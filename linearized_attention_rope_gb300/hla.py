@@ -408,7 +408,8 @@ def prefill_noalloc_check_error(stream=None) -> int:
 #
 # These calls check their tensors (type, shape, device, strides) and raise HlaError with
 # HLA_ERR_INVALID_ARG before anything is launched; they run on the tensors' device, on `stream` or that
-# device's current stream.
+# device's current stream.  Of tensors handed to a call on another `stream`, the memory is not given out again
+# before that stream has passed the call.
 
 _TORCH = {DTYPE_F32: torch.float32, DTYPE_BF16: torch.bfloat16, DTYPE_E4M3: torch.uint8}
 
@@ -464,12 +465,15 @@ def _here(device, stream):
     return _raw_stream(device.index)
 
 
-def _on(device, stream):
+def _on(device, stream, *tensors):
     """A context with `device` current, and `stream` too if one is given, so that buffers allocated in it belong
-    to the stream that uses them."""
+    to the stream that uses them; `tensors`, the call's own, stay theirs until that stream is done with them."""
     if stream is None:
         return torch.cuda.device(device)
     _need(stream.device == device, f"expected a stream of {device}, got one of {stream.device}")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -522,7 +526,7 @@ def _rope(fn, params, q, k, positions, q_out, k_out, stream):
             _check_tensor(o, fn, name + "_out", dt, shape, dev)
     st = _here(dev, stream)
     if st is None:
-        with _on(dev, stream):
+        with _on(dev, stream, q, k, positions, q_out, k_out):
             return _rope(fn, params, q, k, positions, q_out, k_out, None)
     for i, x in enumerate((q, k)):
         if x is not None and outs[i] is None:
@@ -618,7 +622,7 @@ def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=
         _check_tensor(lse, "hla_attention", "lse", torch.float32, shape[:2], dev)
     st = _here(dev, stream)
     if st is None:
-        with _on(dev, stream):
+        with _on(dev, stream, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, ws):
             return attention(params, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, ws)
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=dev)
@@ -647,7 +651,7 @@ def attention_backward(params: AttnParams, q, k, v, out, lse, dout, cu_seqlens_q
             _check_tensor(grads.get(name), fn, "grads." + name, x.dtype, tuple(x.shape), dev)
     st = _here(dev, stream)
     if st is None:
-        with _on(dev, stream):
+        with _on(dev, stream, q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, ws, *(grads or {}).values()):
             return attention_backward(params, q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, grads, ws)
     if grads is None:
         grads = {name: torch.empty(x.shape, dtype=x.dtype, device=dev) for name, x in zip("qkv", (q, k, v))}
@@ -699,8 +703,8 @@ class Cache:
             _need(k_exp is None and v_exp is None, "Cache: exponents go with an E4M3 cache")
             self.k_exp = self.v_exp = None
         self.err = torch.zeros(4, dtype=torch.int32, device=self.device)
-        self._buffers = CCache(*[None if t is None else t.data_ptr() for t in
-                          (self.k, self.v, self.k_exp, self.v_exp, self.page_table, self.err)])
+        self.tensors = (self.k, self.v, self.k_exp, self.v_exp, self.page_table, self.err)
+        self._buffers = CCache(*[None if t is None else t.data_ptr() for t in self.tensors])
         self.c, self.cp = ctypes.byref(self._buffers), _c(params)
 
     def _buffer(self, t, name, dtype, shape):
@@ -738,7 +742,7 @@ def cache_write(cache: Cache, k, v, cu_seqlens, start, stream=None):
         _check_tensor(t, fn, name, _TORCH[p.dtype], shape, cache.device)
     st = _here(cache.device, stream)
     if st is None:
-        with _on(cache.device, stream):
+        with _on(cache.device, stream, k, v, cu_seqlens, start, *cache.tensors):
             return cache_write(cache, k, v, cu_seqlens, start)
     _check(load().hla_cache_write(cache.cp, cache.c, _adr(k), _adr(v), _adr(cu_seqlens), _adr(start), cache.n_seqs,
                                   shape[0], st), fn)
@@ -755,7 +759,7 @@ def cache_read(cache: Cache, cu_seqlens, start, total_tokens: int, k=None, v=Non
             _check_tensor(t, fn, name, dt, shape, cache.device)
     st = _here(cache.device, stream)
     if st is None:
-        with _on(cache.device, stream):
+        with _on(cache.device, stream, k, v, cu_seqlens, start, *cache.tensors):
             return cache_read(cache, cu_seqlens, start, total_tokens, k, v)
     out = [torch.empty(shape, dtype=dt, device=cache.device) if t is None else t for t in (k, v)]
     _check(load().hla_cache_read(cache.cp, cache.c, _adr(cu_seqlens), _adr(start), cache.n_seqs, total_tokens,
@@ -787,7 +791,7 @@ def attention_decode(params: AttnParams, cache: Cache, q, lens, out=None, ws=Non
     _check_workspace(fn, ws, dev)
     st = _here(dev, stream)
     if st is None:
-        with _on(dev, stream):
+        with _on(dev, stream, q, lens, out, ws, *cache.tensors):
             return attention_decode(params, cache, q, lens, out, ws)
     if out is None:
         out = torch.empty(shape, dtype=dt, device=dev)

@@ -214,6 +214,49 @@ def test_scale_and_large_scores(dtype):
     full_check(dtype, 64, 2, 1, [150], scale=2.0, seed=5)
 
 
+def test_two_calls_at_once():
+    # two layers' calls on two streams, a workspace each, beside each other: bit for bit what they are alone
+    cases = [("bf16", 128, 8, 2, [900, 700]), ("bf16", 64, 4, 4, [1500])]
+    alone, at_once, keep = [], [], []
+    for dtype, d, hq, hkv, lens in cases:
+        x = make(dtype, d, hq, hkv, lens, lens, seed=d)
+        alone.append(run(params(dtype, d, hq, hkv), x, lens, lens, same=True))
+        keep.append({n: t.cuda() for n, t in x.items()})
+    tables = [ac.cu(c[4]) for c in cases]
+    ws = [hla.alloc_attention_workspace(params(*c[:4]), sum(c[4]), sum(c[4]), len(c[4]), True) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        at_once = []
+        for c, g, cu, w, s in zip(cases, keep, tables, ws, streams):
+            out, lse = hla.attention(params(*c[:4]), g["q"], g["k"], g["v"], cu, ws=w, stream=s)
+            at_once.append((out, lse, hla.attention_backward(params(*c[:4]), g["q"], g["k"], g["v"], out, lse, g["dout"],
+                                                             cu, ws=w, stream=s)))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, at_once):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            assert all(torch.equal(a[2][n], b[2][n]) for n in "qkv")
+
+
+def test_inputs_of_another_stream_are_kept_until_it_is_done():
+    # the caller lets go of its inputs while the call still waits behind other work on its stream
+    x = make("bf16", 64, 4, 2, [300], [300])
+    want, _, _ = run(params("bf16", 64, 4, 2), x, [300], [300], backward=False, same=True)
+    cu, s = ac.cu([300]), torch.cuda.Stream()
+    ws = hla.alloc_attention_workspace(params("bf16", 64, 4, 2), 300, 300, 1)
+    a = torch.randn(4096, 4096, device="cuda")
+    g = {n: x[n].cuda() for n in "qkv"}
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(30):  # some milliseconds
+            a @ a
+    out, _ = hla.attention(params("bf16", 64, 4, 2), g["q"], g["k"], g["v"], cu, ws=ws, stream=s)
+    del g
+    junk = [torch.full_like(want, math.nan) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and len(junk) == 8
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_padding_is_left_alone_and_kept_out(dtype, d):
