@@ -358,6 +358,28 @@ def test_slices_of_a_fused_projection(dtype, d):
         assert torch.equal(grads[n], ref[2][n])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_past_32_bits(dtype):
+    # tokens 2^27 elements apart, the last ones more than 2^32 from the first: the bits of dense rows
+    hq, hkv, d, lens, t = 4, 2, 64, [15, 22], TYPE[dtype][1]
+    x = make(dtype, d, hq, hkv, lens, lens)
+    ref = run(params(dtype, d, hq, hkv), x, lens, lens, same=True)
+    wide = torch.empty(sum(lens) << 27, dtype=t, device="cuda")
+    q, k, v = (wide.as_strided((sum(lens), h, d), (1 << 27, d, 1), at)
+               for h, at in ((hq, 0), (hkv, 1 << 20), (hkv, 1 << 26)))
+    for n, y in zip("qkv", (q, k, v)):
+        y.copy_(x[n])
+    prm, c = params(dtype, d, hq, hkv), ac.cu(lens)
+    out, lse = hla.attention(prm, q, k, v, c)
+    grads = hla.attention_backward(prm, q, k, v, out, lse, x["dout"].cuda(), c)
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    assert all(torch.equal(grads[n], ref[2][n]) for n in "qkv")
+    rp, pos = hla.RopeParams(hq, hkv, d, dtype=TYPE[dtype][0]), torch.arange(sum(lens), device="cuda")
+    want = hla.rope(rp, q.contiguous(), k.contiguous(), pos)
+    hla.rope(rp, q, k, pos, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
 def test_gradient_against_differences():
     # (f(x + e r) - f(x - e r)) / 2e of sum(dout out), summed in float64 from the fp32 layer's outputs, against
     # the gradient's product with r.  Outputs are off by about 50 u32 of their size each, so the quotient by

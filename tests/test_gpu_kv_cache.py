@@ -237,6 +237,28 @@ def test_bad_lengths_and_pages_are_flagged(dtype, kept):
     decode_close(dtype, got, q, [ks[0][keep], ks[1]], [vs[0][keep], vs[1]])
 
 
+@pytest.mark.parametrize("dtype,kept", [("f32", "same"), ("f32", "e4m3"), ("bf16", "same"), ("bf16", "e4m3")])
+def test_pages_past_32_bits(dtype, kept):
+    # the same rows in a small pool and at the end of one of more than 2^32 values: the same bits
+    lens, hkv, d, page, n_pages = [200, 77], 8, 128, 64, (1 << 32) // (8 * 64 * 128) + 40
+    small = new_cache(dtype, kept, hkv, d, page, lens)
+    fill(small, lens)
+    pool = lambda t: None if t is None else torch.empty(n_pages, *t.shape[1:], dtype=t.dtype, device="cuda")  # noqa: E731
+    first = n_pages - small.params.n_pages
+    table = torch.where(small.page_table >= 0, small.page_table + first, -1)
+    prm = hla.CacheParams(hkv, d, page, n_pages, table.shape[1], dtype=small.params.dtype,
+                          cache_dtype=small.params.cache_dtype)
+    big = hla.Cache(prm, table, *(pool(t) for t in (small.k, small.v, small.k_exp, small.v_exp)))
+    fill(big, lens)
+    cu, start = ac.cu(lens), i64([0, 0])
+    for a, b in zip(hla.cache_read(small, cu, start, sum(lens)), hla.cache_read(big, cu, start, sum(lens))):
+        assert torch.equal(a, b)
+    q = ac.randn(9, 2, 16, d, dtype=TYPE[dtype][1]).cuda()
+    ap = hla.AttnParams(16, hkv, d, dtype=TYPE[dtype][0])
+    assert torch.equal(hla.attention_decode(ap, small, q, i64(lens)), hla.attention_decode(ap, big, q, i64(lens)))
+    assert small.check_error() == 0 and big.check_error() == 0
+
+
 @pytest.mark.parametrize("dtype,kept", [("f32", "e4m3"), ("bf16", "e4m3"), ("bf16", "same")])
 def test_decode_repeats_on_a_stream_and_in_a_graph_with_growing_lengths(dtype, kept):
     lens = [700, 90]
