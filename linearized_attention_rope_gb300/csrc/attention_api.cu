@@ -48,8 +48,9 @@ double rope_frequencies(const hla_rope_params* p, double* w) {
     const double low = unset ? 1.0 : p->low, high = unset ? (p->scaling == HLA_ROPE_SCALE_YARN ? 32.0 : 4.0) : p->high;
     auto index = [&](double turns) { return r * std::log(orig / (two_pi * turns)) / (2.0 * std::log(p->base)); };
     const double lo = std::max(0.0, std::floor(index(high))), hi = std::min(r - 1.0, std::ceil(index(low)));
+    const double step = -2.0 * std::log2(p->base) / r;
     for (int i = 0; i < r / 2; ++i) {
-        const double x = std::pow(p->base, -2.0 * i / r);
+        const double x = std::exp2(i * step);  // base^(-2 i / r)
         double keep = 1.0;  // share of the unscaled angle
         if (p->scaling == HLA_ROPE_SCALE_LINEAR) keep = 0.0;
         if (p->scaling == HLA_ROPE_SCALE_BANDS)

@@ -446,6 +446,13 @@ def _c(params, *strides):
     return ctypes.byref(params.c(*strides))
 
 
+def _like(t, stride: int):
+    """An uninitialised dense tensor of t's shape; stride: t's token stride, from _check_tensor."""
+    if stride == t.shape[1] * t.shape[2]:
+        return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _adr(t):
     """The address of a tensor as an int (0 for none), which ctypes takes as it is."""
     return None if t is None else t.data_ptr()
@@ -530,8 +537,8 @@ def _rope(fn, params, q, k, positions, q_out, k_out, stream):
             return _rope(fn, params, q, k, positions, q_out, k_out, None)
     for i, x in enumerate((q, k)):
         if x is not None and outs[i] is None:
-            outs[i] = torch.empty(x.shape, dtype=dt, device=dev)
-    _check(getattr(load(), fn)(_c(params, *strides), _adr(q), _adr(k), _adr(positions), n, _adr(outs[0]),
+            outs[i] = _like(x, strides[i])
+    _check(getattr(load(), fn)(_c(params, *strides), _adr(q), _adr(k), positions.data_ptr(), n, _adr(outs[0]),
                                _adr(outs[1]), st), fn)
     return outs[0], outs[1]
 
@@ -625,14 +632,14 @@ def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=
         with _on(dev, stream, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, ws):
             return attention(params, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, ws)
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=dev)
+        out = _like(q, strides[0])
     if lse is None:
         lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
     if ws is None:
         ws = alloc_attention_workspace(params, tq, tk, n, device=dev)
-    _check(load().hla_attention(_c(params, *strides), _adr(q), _adr(k), _adr(v), _adr(cu_seqlens_q),
-                                _adr(cu_seqlens_k), n, tq, tk, _adr(out), _adr(lse), _adr(ws), ws.numel(), st),
-           "hla_attention")
+    _check(load().hla_attention(_c(params, *strides), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),
+                                _adr(cu_seqlens_k), n, tq, tk, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                ws.numel(), st), "hla_attention")
     return out, lse
 
 
@@ -654,7 +661,7 @@ def attention_backward(params: AttnParams, q, k, v, out, lse, dout, cu_seqlens_q
         with _on(dev, stream, q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, ws, *(grads or {}).values()):
             return attention_backward(params, q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, grads, ws)
     if grads is None:
-        grads = {name: torch.empty(x.shape, dtype=x.dtype, device=dev) for name, x in zip("qkv", (q, k, v))}
+        grads = {name: _like(x, stride) for name, x, stride in zip("qkv", (q, k, v), strides)}
     if ws is None:
         ws = alloc_attention_workspace(params, tq, tk, n, backward=True, device=dev)
     _check(load().hla_attention_backward(_c(params, *strides), _adr(q), _adr(k), _adr(v), _adr(out), _adr(lse),
@@ -794,7 +801,7 @@ def attention_decode(params: AttnParams, cache: Cache, q, lens, out=None, ws=Non
         with _on(dev, stream, q, lens, out, ws, *cache.tensors):
             return attention_decode(params, cache, q, lens, out, ws)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = _like(q, stride)
     if ws is None:
         ws = alloc_decode_workspace(params, cache)
     _check(load().hla_attention_decode(_c(params, stride), cache.cp, cache.c, _adr(q), _adr(lens), cache.n_seqs,
