@@ -1,7 +1,7 @@
 // Packed causal attention and its gradient of fp32 layers, on the CUDA cores:
 // the tensor cores do not form these products exactly.
 //
-// Forward: blocks of 64 or 32 query rows of a head walk 64-key tiles with the
+// Forward: blocks of 64, 32 or 16 query rows of a head walk 64-key tiles with the
 // running maximum and sum; a thread holds 4 x 4 scores.  Gradient: the
 // probabilities are recomputed from lse; one kernel per key block and query
 // head sums dk and dv over the query tiles (over the heads of a group in a
@@ -12,15 +12,16 @@
 // Both operands of a product lie in shared memory, rows padded by 16 bytes so
 // that 16 consecutive rows are read without bank conflicts; the next tile is
 // copied (cp.async) while this one is worked on, where shared memory allows two
-// (head dim 64, and the forward pass).  A block of 32 has one warp per scheduler
-// per group of threads, which waits for every load; so 4 groups (2 at head dim
-// 128) take the tiles in turn and add their sums at the end, in order.
+// (head dim 64, and the forward pass).  A block of 32 or 16 has one warp per
+// scheduler or less per group of threads, which waits for every load; so 4 groups
+// (2 at head dim 128) take the tiles in turn and add their sums at the end, in
+// order.
 //
 // Bound by the fp32 FMA rate and shared-memory reads (two 16-byte reads per
 // 4 x 4 x 4 FMAs).  4096 tokens, 8/2 heads of 128: forward 1141 us (30 TFLOP/s of
 // the 80 the FMAs could do), gradient 3904 us (31 with the 7 products it forms);
 // 813 tokens, 4/2 heads of 64, where the walk of one block is what takes the
-// time: 23 and 70 us (one group: 31 and 91).
+// time: 24 and 63 us (blocks of 32 and one group: 31 and 91).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -31,7 +32,7 @@ namespace {
 
 constexpr int kB = 64;  // keys of a forward tile, rows of a gradient tile
 constexpr int kThreads = 256;
-template <int D> constexpr int kSmallGroups = D == 64 ? 4 : 2;  // groups of a block of 32: what shared memory holds
+template <int D> constexpr int kSmallGroups = D == 64 ? 4 : 2;  // groups of a smaller block: what shared memory holds
 
 template <int D> constexpr int kPitch = D + 4;
 constexpr int kPPitch = kB + 4;
@@ -497,20 +498,36 @@ cudaError_t allow_smem(DeviceCache& cache, K kernel, size_t bytes) {
     });
 }
 
-// Blocks of 32 rows (or keys) where 64 would give fewer than two blocks per SM: half the walk per block, by several
-// groups of threads, for a little more traffic (813 tokens, 4/2 heads of 64: forward 54 -> 23 us, gradient 228 -> 70;
-// 1500 tokens, 32/8 heads of 128, 768 blocks: 64 is faster, 642 against 698 us).
-bool small_blocks(int64_t total, int n_seqs, int heads) { return (total / kB + n_seqs) * heads < 2 * 152; }
+// Rows (or keys) of a block.  64 unless that gives fewer than two blocks per SM, then 32 (half the walk per block, by
+// several groups of threads, for a little more traffic), then, below `least` blocks, 16: half as many blocks as SMs
+// for the forward pass, as many for the gradient.  Forward and gradient, in us:
+//   1500 tokens, 32/8 heads of 128:     642 and 2147 with 64, 698 and 2692 with 32 (blocks of 64: 768)
+//   226 tokens in 2, 32/8 heads of 128:  26 and 75 with 32, 36 and 98 with 16 (blocks of 32: 288)
+//   813 tokens in 2, 4/2 heads of 64:    24 and 70 with 32, 25 and 63 with 16 (108)
+//   1000 tokens, 2/1 heads of 128:       76 and 237 with 32, 53 and 158 with 16 (64)
+int block_rows(int64_t total, int n_seqs, int heads, int least) {
+    if ((total / 64 + n_seqs) * heads >= 2 * 152) return 64;
+    return (total / 32 + n_seqs) * heads >= least ? 32 : 16;
+}
 
 template <int D, int BM, int W, int ST>
-cudaError_t forward(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
-                    const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
+cudaError_t rows_forward(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
+                         const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
     static DeviceCache cache;
     cudaError_t e = allow_smem(cache, attn_fwd_f32_kernel<D, BM, W, ST>, fwd_smem<D, BM, W, ST>());
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(A.total_q / BM + A.n_seqs), (unsigned)A.Hq);
     attn_fwd_f32_kernel<D, BM, W, ST><<<grid, BM * 4 * W, fwd_smem<D, BM, W, ST>(), st>>>(A, q, k, v, cu_q, cu_k, out, lse, err);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t forward(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
+                    const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
+    const int qb = block_rows(A.total_q, A.n_seqs, A.Hq, 76);
+    return (qb == 64   ? rows_forward<D, 64, 1, 2>
+            : qb == 32 ? rows_forward<D, 32, kSmallGroups<D>, 1>
+                       : rows_forward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, cu_q, cu_k, out, lse, err, st);
 }
 
 template <int D, int BN, int W, int ST>
@@ -548,16 +565,18 @@ cudaError_t backward(const AttnDims& A, const float* q, const float* k, const fl
                      float* dv, float* ws, int32_t* err, cudaStream_t st) {
     const int64_t rows = A.total_q * A.Hq;
     float *delta = ws, *parts = ws + (rows + 63) / 64 * 64;
+    const int kb = block_rows(A.total_k, A.n_seqs, A.Hq, 152), qb = block_rows(A.total_q, A.n_seqs, A.Hq, 152);
     cudaError_t e = cudaSuccess;
     if (rows > 0) attn_delta_kernel<D><<<(unsigned)((rows + 7) / 8), kThreads, 0, st>>>(rows, out, dout, delta);
     if (A.total_k > 0)
-        e = small_blocks(A.total_k, A.n_seqs, A.Hq)
-                ? keys_backward<D, 32, kSmallGroups<D>, 1>(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv, delta, parts, err, st)
-                : keys_backward<D, 64, 1, D == 64 ? 2 : 1>(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv, delta, parts, err, st);
+        e = (kb == 64   ? keys_backward<D, 64, 1, D == 64 ? 2 : 1>
+             : kb == 32 ? keys_backward<D, 32, kSmallGroups<D>, 1>
+                        : keys_backward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv, delta, parts,
+                                                                    err, st);
     if (e != cudaSuccess || rows == 0) return e;
-    return small_blocks(A.total_q, A.n_seqs, A.Hq)
-               ? rows_backward<D, 32, kSmallGroups<D>, 1>(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, st)
-               : rows_backward<D, 64, 1, D == 64 ? 2 : 1>(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, st);
+    return (qb == 64   ? rows_backward<D, 64, 1, D == 64 ? 2 : 1>
+            : qb == 32 ? rows_backward<D, 32, kSmallGroups<D>, 1>
+                       : rows_backward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, st);
 }
 
 // Rows of the sequences set to zero (and lse to -infinity): what attention and its gradient are without keys or queries.
@@ -585,12 +604,7 @@ attn_empty_kernel(int64_t total, int64_t other, int n_seqs, const int32_t* __res
 
 cudaError_t launch_attention_f32(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
                                  const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
-    const bool small = small_blocks(A.total_q, A.n_seqs, A.Hq);
-    if (A.d == 128)
-        return small ? forward<128, 32, kSmallGroups<128>, 1>(A, q, k, v, cu_q, cu_k, out, lse, err, st)
-                     : forward<128, 64, 1, 2>(A, q, k, v, cu_q, cu_k, out, lse, err, st);
-    return small ? forward<64, 32, kSmallGroups<64>, 1>(A, q, k, v, cu_q, cu_k, out, lse, err, st)
-                 : forward<64, 64, 1, 2>(A, q, k, v, cu_q, cu_k, out, lse, err, st);
+    return (A.d == 128 ? forward<128> : forward<64>)(A, q, k, v, cu_q, cu_k, out, lse, err, st);
 }
 size_t attention_backward_f32_floats(const AttnDims& A) {
     return (size_t)((A.total_q * A.Hq + 63) / 64 * 64 + (A.G > 1 ? 2 * A.total_k * A.Hq * A.d : 0));

@@ -163,6 +163,14 @@ def test_fp32_layers_with_many_heads(d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,lens", [(1, 1, [300]), (4, 2, [330, 201, 0, 15]), (8, 4, [260, 400]), (12, 4, [700, 160])])
+def test_fp32_layers_by_block_size(d, hq, hkv, lens):
+    # few, more and enough blocks of the smaller sizes
+    full_check("f32", d, hq, hkv, lens)
+    full_check("f32", d, hq, hkv, [n // 2 for n in lens], lens)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_fp32_layers_with_many_heads_and_nan_outside(d):
     # the rows of one sequence and the padding hold NaN: the others stay what they are, bit for bit
     lens = [130, 75, 200]
