@@ -139,7 +139,7 @@ constexpr size_t kWsHead = 256;  // the error word
 size_t attn_ws_bytes(const hla_attn_params* p, int64_t total_q, int64_t total_k, int n_seqs, bool backward) {
     size_t n = kWsHead;
     if (!backward && p->dtype == HLA_DTYPE_BF16) n += attention_tc_part_bytes(attn_dims(p, n_seqs, total_q, total_k));
-    if (backward && p->dtype == HLA_DTYPE_BF16) n += (size_t)total_q * p->n_q_heads * sizeof(float2);  // row statistics
+    if (backward && p->dtype == HLA_DTYPE_BF16) n += attention_backward_tc_bytes(attn_dims(p, n_seqs, total_q, total_k));
     if (backward && p->dtype == HLA_DTYPE_F32)
         n += attention_backward_f32_floats(attn_dims(p, n_seqs, total_q, total_k)) * sizeof(float);
     return n;
@@ -298,7 +298,7 @@ HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, cons
     return status(launch_attention_backward_tc(
         A, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v), static_cast<const bf*>(out),
         lse, static_cast<const bf*>(dout), cu_q, cu_k, static_cast<bf*>(dq), static_cast<bf*>(dk), static_cast<bf*>(dv),
-        static_cast<float2*>(rows_ws), err, st));
+        rows_ws, err, st));
 }
 
 HLA_API int hla_cache_bytes(const hla_cache_params* p, size_t* rows, size_t* exponents) {

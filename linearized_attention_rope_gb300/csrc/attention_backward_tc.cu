@@ -12,8 +12,9 @@
 // That is 7 products in place of the 5 that one pass would take with dQ added
 // to memory from many blocks: fp32 atomics would make results depend on the
 // order of arrival, and their traffic (4 bytes d per row and key tile) exceeds
-// what the two extra products cost.  No gradient is summed outside a block, so
-// shared kv heads need no second pass either.
+// what the two extra products cost.  Shared kv heads are summed in the block;
+// only where key blocks are few are the rows of one cut over blocks, whose sums
+// a third kernel adds in order.
 //
 // P and dS are rounded to bf16 (the inputs' own precision) and are read by the
 // products from TMEM, over the columns of the scores they came from.  The
@@ -166,8 +167,9 @@ __global__ void __launch_bounds__(kBlock, 1)
 attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_do, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const int32_t* __restrict__ cu_q,
-                    const int32_t* __restrict__ cu_k, int lpack, const float2* __restrict__ stats,
-                    __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, int32_t* __restrict__ err) {
+                    const int32_t* __restrict__ cu_k, int lpack, int parts, const float2* __restrict__ stats,
+                    __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, float* __restrict__ part_dk,
+                    float* __restrict__ part_dv, int32_t* __restrict__ err) {
     using C = Cfg<D>;
     using Ring = RingPos<C::kSlots>;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -212,13 +214,16 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     const uint32_t cS = tmem, cP = tmem + 128, cV = tmem + 256, cK = cV + D;  // S / P, dP / dS, dV, dK
 
     // an item's query tiles: of each packed head group, `per` tiles from tile i0, the first that sees the block's
-    // first key; the last has `tail` rows
-    struct Span { int i0, per, n, tail; };
+    // first key; the last has `tail` rows.  Of these n, from tile r of head h's group on (parts: the item's share)
+    struct Span { int i0, per, n, tail, r, h; };
     auto span = [&](const Item& it) {
         const int off = it.lk - it.lq, i0 = max(0, it.first - off) >> lqb;
         const int per = __shfl_sync(0xffffffffu, max(0, ((it.lq + qb - 1) >> lqb) - i0), 0);
-        const int rest = it.lq & (qb - 1);
-        return Span{i0, per, per * groups, __shfl_sync(0xffffffffu, rest ? rest << lpack : kRows, 0)};
+        const int rest = it.lq & (qb - 1), tail = __shfl_sync(0xffffffffu, rest ? rest << lpack : kRows, 0);
+        if (parts == 1 || per == 0) return Span{i0, per, per * groups, tail, 0, it.head * A.G};
+        const int part = __shfl_sync(0xffffffffu, it.part, 0);
+        const int a = (int)((int64_t)per * groups * part / parts), b = (int)((int64_t)per * groups * (part + 1) / parts);
+        return Span{i0, per, b - a, tail, a % per, it.head * A.G + (a / per << lpack)};
     };
 
     if (warp >= 8) {
@@ -237,7 +242,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 const Span sp = span(it);
                 const int ask_at = max(0, sp.n - 2);
                 if (sp.n == 0 && lane == 0) umma::mbar_arrive(bar_want);
-                int r = 0, h = it.head * A.G;
+                int r = sp.r, h = sp.h;
                 for (int i = 0; i < sp.n; ++i) {
                     if (i == ask_at && lane == 0) umma::mbar_arrive(bar_want);  // time to look for the next item
                     const int row = it.q0 + ((sp.i0 + r) << lqb);
@@ -305,7 +310,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 const int n = sp.n;
                 const bool fine = __shfl_sync(0xffffffffu, it.lk, 0) <= kRows;
                 if (n == 0) continue;
-                int r = 0;
+                int r = sp.r;
                 auto ready_q = [&](const Ring& q) {  // a tile's Q (of a last tile both, cleared behind the last row)
                     wait(bar_full + 8 * q.slot, q.par);
                     if (++r == sp.per) {
@@ -369,7 +374,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (it.head < 0) break;
                 const Span sp = span(it);
-                int r = 0, h = it.head * A.G;
+                int r = sp.r, h = sp.h;
                 float2 v[4];
                 auto load = [&]() {
                     const int r0 = (sp.i0 + r) << lqb;
@@ -405,7 +410,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             }
         } else {
             schedule_items(A, cu_q, cu_k, kRows, A.Hkv, true, items, bar_it, bar_ie, bar_ask, bar_want, err,
-                           [](int kv) { return kv; });
+                           [](int kv) { return kv; }, parts);
         }
     } else {
         take_registers();
@@ -418,8 +423,9 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         int count = 0;
         bool ok = true;
         for (int x = 0;; ++x) {
-            int n, per, ahead;  // tiles; tiles per head group; first row that sees the key, from the first tile's start
-            int64_t at;         // the key's place in the results (-1: none)
+            int n, per, r;  // tiles; tiles per head group; the first one's place in it
+            int ahead;      // first row that sees the key, from the group's first tile's start
+            int64_t at;     // the key's place in the results, or among the parts' (-1: none)
             bool fine;
             {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
@@ -429,10 +435,11 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 n = sp.n;
                 fine = it.lk <= kRows;
                 per = sp.per;
+                r = sp.r;
                 ahead = key - (it.lk - it.lq) - (sp.i0 << lqb);
-                at = key < it.lk ? ((int64_t)it.k0 + key) * A.Hkv + it.head : -1;
+                at = key < it.lk ? (it.part * A.total_k + it.k0 + key) * A.Hkv + it.head : -1;
             }
-            for (int i = 0, r = 0; i < n; ++i, ++t) {
+            for (int i = 0; i < n; ++i, ++t) {
                 const float* st = reinterpret_cast<const float*>(sm + C::kStat + (t & 1) * 1024) + half * 64;
                 // rows from column `from` on see the key
                 const int from = max(-kRows, min(kRows, ahead - (r << lqb))) * (1 << lpack) - half * 64;
@@ -476,6 +483,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
             umma::fence_after_sync();
             const float mul = half ? A.scale : 1.f;
             __nv_bfloat16* dst = (half ? dk : dv) + at * D;
+            float* part = (half ? part_dk : part_dv) + at * D;
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
                 float o[32];
@@ -491,7 +499,12 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     if (lane == 0) umma::mbar_arrive(bar_oe);
                     ++count;
                 }
-                if (at >= 0) {
+                if (at >= 0 && parts > 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(part + 32 * b + e) =
+                            make_float4(o[e] * mul, o[e + 1] * mul, o[e + 2] * mul, o[e + 3] * mul);
+                } else if (at >= 0) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         *reinterpret_cast<uint4*>(dst + 32 * b + e) = make_uint4(
@@ -504,6 +517,32 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     umma::fence_before_sync();
     __syncthreads();
     if (warp == 9) umma::tmem_dealloc(tmem, C::kCols);
+}
+
+// dk and dv from the parts of their rows, in order; eight values per thread, keys of the sequences only.
+template <int D>
+__global__ void __launch_bounds__(256)
+attn_dkdv_join_kernel(AttnDims A, const int32_t* __restrict__ cu_k, int parts, const float* __restrict__ part_dk,
+                      const float* __restrict__ part_dv, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+    const int64_t n = A.total_k * A.Hkv * (D / 8), i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t t = i / (D / 8) / A.Hkv;
+    int64_t a, len;
+    seq_range(cu_k, seq_of_token(cu_k, A.n_seqs, t), A.total_k, &a, &len);
+    if (t < a || t >= a + len) return;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const float* src = y ? part_dv : part_dk;
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+        for (int p = 0; p < parts; ++p) {
+            const float4 u = reinterpret_cast<const float4*>(src)[2 * (p * n + i)];
+            const float4 w = reinterpret_cast<const float4*>(src)[2 * (p * n + i) + 1];
+            lo = make_float4(lo.x + u.x, lo.y + u.y, lo.z + u.z, lo.w + u.w);
+            hi = make_float4(hi.x + w.x, hi.y + w.y, hi.z + w.z, hi.w + w.w);
+        }
+        reinterpret_cast<uint4*>(y ? dv : dk)[i] =
+            make_uint4(pack_bf2(lo.x, lo.y), pack_bf2(lo.z, lo.w), pack_bf2(hi.x, hi.y), pack_bf2(hi.z, hi.w));
+    }
 }
 
 // ---- dq ---------------------------------------------------------------------
@@ -837,11 +876,36 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
     if (warp == 9) umma::tmem_dealloc(tmem, C::kCols);
 }
 
+// Parts that the rows of each key block are cut into, a block each, their sums joined: a causal sequence's first key
+// block walks all of its query tiles, the last one a few, so few key blocks per SM leave most SMs waiting for the first.
+// In tiles (about a microsecond each), for equal sequences: the longest walk or the SMs' share, whichever is more; three
+// for the join's launch, and 0.06 for every part written and read.  Gradients in us, one part and the rule's:
+//   900 tokens, 16/1 heads of 128: 166 and 50 (15 parts)    82 + 752 + 5 + 782, 8/1 of 64: 72 and 37 (6)
+//   4096, 4/1 of 128: 205 and 88 (8)                        1024, 32/8 of 128: 72 and 64 (3)
+//   2048, 32/8 of 128: 147 and 123 (2)                      4096, 32/8 of 128: whole
+//   200 + 150, 8/2 of 128: whole, 32.7 (in two parts 33.7)
+// (A workspace's size must not depend on the device: 152 SMs.)
+int key_parts(const AttnDims& A) {
+    const double items = (double)std::max<int64_t>(A.n_seqs, (A.total_k + kRows - 1) / kRows) * A.Hkv;
+    const double walk = (double)A.total_q * A.G / kRows / A.n_seqs;
+    int best = 1;
+    double least = std::max(walk, items * walk / (2 * 152));
+    for (int p = 2; p <= 16; ++p) {
+        const double cost = std::max(walk / p, items * walk / (2 * 152)) + 3.0 + 0.06 * items * p;
+        if (cost < least) {
+            least = cost;
+            best = p;
+        }
+    }
+    return best;
+}
+size_t stat_bytes(const AttnDims& A) { return ((size_t)A.total_q * A.Hq * sizeof(float2) + 255) / 256 * 256; }
+
 template <int D>
 cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
                    const __nv_bfloat16* out, const float* lse, const __nv_bfloat16* dout, const int32_t* cu_q,
-                   const int32_t* cu_k, __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, float2* stats,
-                   int32_t* err, cudaStream_t st) {
+                   const int32_t* cu_k, __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, int32_t* err,
+                   cudaStream_t st) {
     static DeviceCache c1, c2;
     cudaError_t e = device_cached(c1, nullptr, [](int, int*) { return prepare_kernel(attn_dkdv_tc_kernel<D>, Cfg<D>::kSmem); });
     if (e == cudaSuccess)
@@ -857,27 +921,39 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
         !tma::make_map_3d_strided(&mk, k, true, D, Hkv, A.total_k, (uint64_t)A.sk * 2, 64, 1, kRows) ||
         !tma::make_map_3d_strided(&mv, v, true, D, Hkv, A.total_k, (uint64_t)A.sv * 2, 64, 1, kRows))
         return cudaErrorInvalidValue;
-    const int64_t rows = A.total_q * A.Hq, kb = (A.total_k / kRows + A.n_seqs) * A.Hkv,
+    const int parts = key_parts(A);
+    float2* stats = static_cast<float2*>(ws);
+    float *part_dk = reinterpret_cast<float*>(static_cast<char*>(ws) + stat_bytes(A)),
+          *part_dv = part_dk + parts * A.total_k * A.Hkv * D;
+    const int64_t rows = A.total_q * A.Hq, kb = (A.total_k / kRows + A.n_seqs) * A.Hkv * parts,
                   qblocks = (A.total_q / qb + A.n_seqs) * (A.Hq / pack), sb = (rows * (D / 8) + 255) / 256;
     if (kb > INT32_MAX || qblocks > INT32_MAX || sb > INT32_MAX) return cudaErrorInvalidValue;
     attn_stats_kernel<D><<<(unsigned)sb, 256, 0, st>>>(rows, out, dout, lse, stats);
     // dq first: it leaves a better D for rows of few keys
     attn_dq_tc_kernel<D><<<(unsigned)qblocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, stats,
                                                                           dq, err);
-    attn_dkdv_tc_kernel<D><<<(unsigned)kb, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, stats, dk,
-                                                                       dv, err);
+    attn_dkdv_tc_kernel<D><<<(unsigned)kb, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, parts, stats,
+                                                                       dk, dv, part_dk, part_dv, err);
+    if (parts > 1) {
+        const int64_t n = A.total_k * A.Hkv * (D / 8);
+        attn_dkdv_join_kernel<D><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(A, cu_k, parts, part_dk, part_dv, dk, dv);
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
 
+size_t attention_backward_tc_bytes(const AttnDims& A) {
+    const int64_t parts = key_parts(A);
+    return stat_bytes(A) + (parts > 1 ? (size_t)(2 * parts * A.total_k * A.Hkv * A.d) * sizeof(float) : 0);
+}
 cudaError_t launch_attention_backward_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                          const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
                                          const __nv_bfloat16* dout, const int32_t* cu_q, const int32_t* cu_k,
-                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, float2* stats,
-                                         int32_t* err, cudaStream_t st) {
-    return A.d == 128 ? launch<128>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, stats, err, st)
-                      : launch<64>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, stats, err, st);
+                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, int32_t* err,
+                                         cudaStream_t st) {
+    return A.d == 128 ? launch<128>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, err, st)
+                      : launch<64>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, err, st);
 }
 
 }  // namespace hla

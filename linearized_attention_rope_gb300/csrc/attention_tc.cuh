@@ -138,9 +138,10 @@ __device__ __forceinline__ int64_t taken_item(uint32_t answer) {
     return got ? (int64_t)x : -1;
 }
 
-// The scheduling warp: `heads` head groups, `rows` positions per item, whose
-// visible keys are cut into `parts` parts of whole tiles, eight at least (the
-// parts past those get none).
+// The scheduling warp: `heads` head groups, `rows` positions per item, each in
+// `parts` parts: of query positions, the visible keys are cut into parts of
+// whole tiles, eight at least (the parts past those get none); of keys, the
+// reader cuts the rows that see them.
 template <class HeadOf>
 __device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t* cu_q, const int32_t* cu_k, int rows,
                                                int heads, bool by_key, ItemRing* ring, uint32_t bar_full,
@@ -158,7 +159,7 @@ __device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t*
         more = B.found;
         if (i >= kItems && !wait_or_flag(bar_empty + 8 * s, ((i / kItems) - 1) & 1, err, kItemSeconds)) more = false;
         int k0 = (int)B.k0, lk = B.lk, off = B.lk - B.lq;
-        if (parts > 1) {
+        if (parts > 1 && !by_key) {
             const int end = max(0, min(B.lk, min(B.first + rows, B.lq) + off)), n = (end + kRows - 1) / kRows;
             const int cut = max(1, min(parts, n / 8)), a = part < cut ? (int)((int64_t)n * part / cut) * kRows : end;
             const int b = part < cut ? (int)((int64_t)n * (part + 1) / cut) * kRows : end;
@@ -260,16 +261,17 @@ __device__ __forceinline__ void clear_nonfinite(unsigned char* tile, int first, 
 
 }  // namespace attn_tc
 
-// Parts that the keys of each item are cut into, and the bytes of the partial results (0: one part).
+// Parts that the work of each item is cut into where items are few, and the bytes of the partial results (0: one part).
 int attention_tc_parts(const AttnDims& A);
 size_t attention_tc_part_bytes(const AttnDims& A);
 cudaError_t launch_attention_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                 const __nv_bfloat16* v, const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out,
                                 float* lse, void* parts, int32_t* err, cudaStream_t st);
+size_t attention_backward_tc_bytes(const AttnDims& A);  // -lse and -D per row and head; partial dk and dv
 cudaError_t launch_attention_backward_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                          const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
                                          const __nv_bfloat16* dout, const int32_t* cu_q, const int32_t* cu_k,
-                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, float2* stats,
-                                         int32_t* err, cudaStream_t st);
+                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, int32_t* err,
+                                         cudaStream_t st);
 
 }  // namespace hla

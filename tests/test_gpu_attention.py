@@ -122,6 +122,21 @@ def test_few_rows_over_many_keys(d, hq, hkv):
     full_check("bf16", d, hq, hkv, [3], [9001])
 
 
+@pytest.mark.parametrize("d,hq,hkv,lens", [(64, 1, 1, [2500]), (128, 1, 1, [2200, 2050])])
+def test_whole_prompts_of_few_heads(d, hq, hkv, lens):
+    # the keys are cut as well; early items have fewer parts than the longest
+    full_check("bf16", d, hq, hkv, lens)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,q_lens,k_lens", [(8, 1, [700, 0, 300], None), (16, 1, [900], None),
+                                                  (6, 2, [1500, 7], None), (32, 1, [130, 260], [130, 700]),
+                                                  (24, 2, [500], [200])])
+def test_few_key_blocks_of_many_rows(d, hq, hkv, q_lens, k_lens):
+    # the rows that see a key block are cut over blocks and joined: whole head groups and pieces of them
+    full_check("bf16", d, hq, hkv, q_lens, k_lens)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_rows_that_see_no_key(dtype, d):
