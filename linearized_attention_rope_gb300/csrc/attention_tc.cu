@@ -31,8 +31,8 @@
 // O is then rescaled in TMEM by its own softmax thread, after the products
 // before it have completed (they complete before the scores it waits for).
 //
-// With fewer items than half the SMs (a short chunk of a prompt behind many
-// keys), the keys of each item are cut into parts, an item each; a part leaves
+// With fewer items than SMs (a short chunk of a prompt behind many keys, few
+// heads), the keys of each item are cut into parts, an item each; a part leaves
 // its rows' outputs in fp32 with their log-sum-exp, and a second kernel adds
 // them in order.
 //
@@ -548,21 +548,28 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
 }  // namespace
 
 // Items that do not fill the SMs leave some idle.  With keys enough for parts of
-// eight tiles, they are cut into the number of parts whose rounds over the SMs
-// take least, counting what the parts' results cost: 0.55 of an item's time
-// per item and SM, which separates the cases measured (700 rows behind 20000
-// keys, 88 items: 239 us whole, 187 in three parts; 1512 rows behind 23000, 192
-// items: 196 whole, 218 in three; one row of 131072: 8 items in 19 parts).
-// Only rows that are few beside the keys: a whole prompt's items differ in
-// length and even out by themselves.  (A workspace's size must not depend on
-// the device: 152 SMs.)
+// eight tiles, they are cut into the number of parts that takes least:
+// - rows that are few beside the keys: rounds over the SMs, plus what the parts'
+//   results cost, 0.55 of an item's time per item and SM, which separates the
+//   cases measured (700 rows behind 20000 keys, 88 items: 239 us whole, 187 in
+//   three parts; 1512 rows behind 23000, 192 items: 196 whole, 218 in three; one
+//   row of 131072: 8 items in 19 parts);
+// - whole prompts, whose items differ in length: the longest walk at 1.5 us a
+//   tile, plus 4 us and a microsecond per MB of results (4096 tokens, 1 head of
+//   128: 51 us whole, 34 in four parts; 6000, 2/1 heads of 64: 67 and 35; 2048,
+//   8/2 of 128: 30 and, in two, 39).
+// (A workspace's size must not depend on the device: 152 SMs.)
 int attention_tc_parts(const AttnDims& A) {
-    const int64_t items = items_about(A), sms = 152;
-    if (A.total_k < 16 * kRows * (int64_t)A.n_seqs || 4 * A.total_q > A.total_k || items > sms) return 1;
+    const int64_t items = items_about(A), sms = 152, tiles = A.total_k / (kRows * (int64_t)A.n_seqs);
+    if (tiles < 16 || items > sms) return 1;
+    const bool few = 4 * A.total_q <= A.total_k;
+    const int64_t most = few ? std::min<int64_t>(32, std::max<int64_t>(4, sms / items))
+                             : std::min<int64_t>({4, sms / items, tiles / 8});
     int best = 1;
-    double least = 1.0;
-    for (int p = 2; p <= 32 && p <= std::max<int64_t>(4, sms / items); ++p) {
-        const double cost = (double)((items * p + sms - 1) / sms) / p + 0.55 * items / sms;
+    double least = few ? 1.0 : 1.5 * tiles;
+    for (int p = 2; p <= most; ++p) {
+        const double cost = few ? (double)((items * p + sms - 1) / sms) / p + 0.55 * items / sms
+                                : 1.5 * tiles / p + 4.0 + 4e-6 * A.total_q * A.Hq * A.d * p;
         if (cost < least) {
             least = cost;
             best = p;
