@@ -365,6 +365,44 @@ def test_infinite_and_nan_values_reach_the_rows_that_see_them(dtype, d, hq, hkv)
     assert ((got - want).abs()[fine] <= tol[fine]).all()
 
 
+@pytest.mark.parametrize("d,hq,hkv,n,real", [(64, 1, 1, 2500, 1700), (128, 8, 1, 900, 640), (64, 16, 1, 700, 130)])
+def test_later_rows_stay_out_where_the_work_is_cut(d, hq, hkv, n, real):
+    # keys cut into parts (long prompts of few heads), rows cut into parts (few key blocks): as above
+    x = make("bf16", d, hq, hkv, [n], [n], seed=n)
+    clean = {m: t.clone() for m, t in x.items()}
+    g = ac.gen(n)
+    for m in ("q", "k", "v"):
+        bad = torch.randint(0, 3, x[m][real:].shape, generator=g)
+        x[m][real:] = torch.where(bad == 0, math.nan, torch.where(bad == 1, math.inf, -math.inf)).to(x[m].dtype)
+    out, lse, grads = run(params("bf16", d, hq, hkv), x, [n], [n])
+    y = {m: t[:real] for m, t in clean.items()}
+    ref = ac.attention(y["q"], y["k"], y["v"], [real], [real], dout=y["dout"])
+    ref[2].pop("k"), ref[2].pop("v")
+    check("bf16", d, y, ref, out[:real], lse[:real], {"q": grads["q"][:real]}, [real], [real])
+    assert torch.isnan(out[real:]).all() and torch.isnan(lse[real:]).all()
+
+
+def test_infinite_and_nan_values_reach_the_rows_that_see_them_in_parts():
+    n, d = 2500, 64
+    x = make("bf16", d, 1, 1, [n], [n], seed=7)
+    places = {(3, 0): math.inf, (700, 5): math.nan, (1500, d - 1): -math.inf, (2400, 9): math.inf, (2499, 1): math.nan}
+    clean = x["v"].clone()
+    for (key, col), value in places.items():
+        x["v"][key, :, col] = value
+        clean[key, :, col] = 0.0
+    out, lse, _ = run(params("bf16", d, 1, 1), x, [n], [n], backward=False)
+    ref = ac.attention(x["q"], x["k"], clean, [n], [n])
+    rows, want = torch.arange(n), ref[0].clone()
+    for (key, col), value in places.items():
+        want[rows >= key, :, col] = value
+    got = out.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[want.isinf()], want[want.isinf()])
+    fine, u = want.isfinite(), ac.EPS[torch.bfloat16] / 2
+    tol = (u + 1e-4) * ref[3]["out"] + 1.01 * u * want.abs().nan_to_num(0, 0, 0)
+    assert ((got - want).abs()[fine] <= tol[fine]).all()
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 def test_slices_of_a_fused_projection(dtype, d):
     hq, hkv, lens = 4, 2, [100, 45]
