@@ -254,8 +254,9 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
 // lose bits of 2^-25 of it).  A key row's power of two goes onto its score, a
 // value row's into the exponent of its weight: weights are 2^(s - M) 2^ev /
 // 2^(Mt - M), with a reference Mt of their own, so rows of any size meet in
-// fp16 (11 bits) with the largest product near 1.  bf16 caches: products and
-// weights in bf16 (8 bits, the values' own precision).
+// fp16 (11 bits) with the largest product near 1.  bf16 caches: products in bf16,
+// weights in two bf16 parts (with one, outputs of a few heads were off by up to
+// 1.5 times the rounding of the result; the second costs nothing beside the loads).
 //
 // A warp takes 32 keys at a time (16 of 256 bytes), so that the 12 to 16 warps
 // of an SM keep some 60 KB on their way.
@@ -313,6 +314,15 @@ template <bool F16> __device__ __forceinline__ uint32_t pack2(float a, float b) 
     }
 }
 __device__ __forceinline__ float bf16_at(uint32_t w, int hi) { return __uint_as_float(hi ? w & 0xffff0000u : w << 16); }
+// A weight >= 0 in two bf16 parts: its upper half (of a pair), and what that leaves; not 0, so that an infinite value
+// times either is that infinity.
+__device__ __forceinline__ uint32_t top2(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float rest(float p) {
+    const float r = fmaxf(p - __uint_as_float(__float_as_uint(p) & 0xffff0000u), 1.17549435e-38f);
+    return p == 0.f ? 0.f : r;
+}
 __device__ __forceinline__ float safe_ref(float m) { return m == -INFINITY ? 0.f : m; }
 
 template <bool E4M3, int D>
@@ -565,7 +575,16 @@ decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_b
                     p2 = ex2(sc[y][2] + (ve[y][1] - ret0));
                     p3 = ex2(sc[y][3] + (ve[y][1] - ret1));
                 }
-                const uint32_t b0 = transpose8(pack2<E4M3>(p0, p1)), b1 = transpose8(pack2<E4M3>(p2, p3));
+                uint32_t b0, b1, c0 = 0u, c1 = 0u;  // bf16 weights in two parts
+                if constexpr (E4M3) {
+                    b0 = transpose8(pack2<true>(p0, p1));
+                    b1 = transpose8(pack2<true>(p2, p3));
+                } else {
+                    b0 = transpose8(top2(p0, p1));
+                    b1 = transpose8(top2(p2, p3));
+                    c0 = transpose8(pack2<false>(rest(p0), rest(p1)));
+                    c1 = transpose8(pack2<false>(rest(p2), rest(p3)));
+                }
                 if (row[y] != kNoRow) {
 #pragma unroll
                     for (int w = 0; w < kVw; ++w) {
@@ -579,10 +598,12 @@ decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_b
                                 mma16816<true>(o[2 * w + z], a0, a1, a2, a3, b0, b1);
                             }
                         } else {
-                            mma16816<false>(o[w], __byte_perm(vx[y][0][w], vx[y][1][w], 0x5410),
-                                            __byte_perm(vx[y][0][w], vx[y][1][w], 0x7632),
-                                            __byte_perm(vx[y][2][w], vx[y][3][w], 0x5410),
-                                            __byte_perm(vx[y][2][w], vx[y][3][w], 0x7632), b0, b1);
+                            const uint32_t a0 = __byte_perm(vx[y][0][w], vx[y][1][w], 0x5410);
+                            const uint32_t a1 = __byte_perm(vx[y][0][w], vx[y][1][w], 0x7632);
+                            const uint32_t a2 = __byte_perm(vx[y][2][w], vx[y][3][w], 0x5410);
+                            const uint32_t a3 = __byte_perm(vx[y][2][w], vx[y][3][w], 0x7632);
+                            mma16816<false>(o[w], a0, a1, a2, a3, c0, c1);
+                            mma16816<false>(o[w], a0, a1, a2, a3, b0, b1);
                         }
                     }
                 }
