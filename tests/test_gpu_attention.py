@@ -107,6 +107,23 @@ def test_lengths_around_the_tiles(dtype, d, lens):
     full_check(dtype, d, 4, 2, lens)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,lens", [(1, 1, [3]), (8, 2, [0, 4, 6, 4]), (4, 4, [40, 128, 17]), (16, 1, [90])])
+def test_short_prompts_are_rounded_once(d, hq, hkv, lens):
+    # one key tile: probabilities and score gradients in two bf16 parts (2^-16 of them left), so that results are off by
+    # their own rounding, u of their size, and by the rest: out, dv 2^-16 mag, dq, dk that and their dS, 2^-15 mag,
+    # plus the fp32 sums (as above)
+    x = make("bf16", d, hq, hkv, lens, lens)
+    out, lse, grads = run(params("bf16", d, hq, hkv), x, lens, lens, same=True)
+    r_out, _, r_grads, mag = ac.attention(x["q"], x["k"], x["v"], lens, lens, dout=x["dout"])
+    S = float(x["q"].double().norm(dim=-1).max() * x["k"].double().norm(dim=-1).max()) / math.sqrt(d)
+    fp, u = 3 * (2 * d * S + 32 + max(lens) * hq // hkv) * U32, ac.EPS[torch.bfloat16] / 2
+    for name, got, want in [("out", out, r_out)] + [(n, grads[n], r_grads[n]) for n in "qkv"]:
+        part = 2.0 ** -15 if name in ("q", "k") else 2.0 ** -16
+        off = (got.cpu().double() - want).abs()
+        assert (off <= (part + fp) * mag[name] + 1.01 * u * want.abs()).all(), name
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_chunks_behind_earlier_keys(dtype, d):
