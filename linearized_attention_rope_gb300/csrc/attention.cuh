@@ -128,10 +128,51 @@ __device__ __forceinline__ void attn_check_table(const int32_t* __restrict__ cu,
     if (bad) atomicExch(err, kErrSeqlens);
 }
 
-// fp32 layers (attention_f32.cu), and the bytes their gradient needs: dout . out per row and head, and (several query
+// Adds the parts (32 at most) of every row of the sequences, in order; a warp per row and head.
+template <int D, typename T>
+__global__ void __launch_bounds__(256)
+attention_join_kernel(AttnDims A, const int32_t* __restrict__ cu_q, int parts, const float* __restrict__ part_o,
+                      const float* __restrict__ part_lse, T* __restrict__ out, float* __restrict__ lse) {
+    constexpr int E = D / 32;
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), rows = A.total_q * A.Hq;
+    const int lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    const int64_t t = r / A.Hq;
+    int64_t a, n;
+    seq_range(cu_q, seq_of_token(cu_q, A.n_seqs, t), A.total_q, &a, &n);
+    if (t < a || t >= a + n) return;  // behind the last sequence
+    const float l = lane < parts ? __ldg(part_lse + lane * rows + r) : -INFINITY;
+    float m = l;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float w = l == -INFINITY ? 0.f : exp2f((l - m) * kLog2e);  // NaN stays NaN
+    float sum = w, acc[E];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+    for (int x = 0; x < E; ++x) acc[x] = 0.f;
+    for (int p = 0; p < parts; ++p) {
+        const float wp = __shfl_sync(0xffffffffu, w, p);
+        if (wp == 0.f) continue;  // no keys
+        float o[E];
+        load_vec<E>(part_o + (p * rows + r) * D + lane * E, o);
+#pragma unroll
+        for (int x = 0; x < E; ++x) acc[x] = fmaf(wp, o[x], acc[x]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    struct alignas(E * sizeof(T)) { T x[E]; } y;
+#pragma unroll
+    for (int x = 0; x < E; ++x) y.x[x] = from_f32<T>(acc[x] * inv);
+    *reinterpret_cast<decltype(y)*>(out + r * D + lane * E) = y;
+    if (lane == 0) lse[r] = sum == 0.f ? -INFINITY : m + logf(sum);
+}
+
+// fp32 layers (attention_f32.cu), the bytes of partial results (0: one part), and those their gradient needs: dout . out per row and head, and (several query
 // heads per kv head) dk and dv of each query head.
 cudaError_t launch_attention_f32(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
-                                 const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st);
+                                 const int32_t* cu_k, float* out, float* lse, float* part_ws, int32_t* err,
+                                 cudaStream_t st);
+size_t attention_f32_part_bytes(const AttnDims& A);
 size_t attention_backward_f32_floats(const AttnDims& A);
 cudaError_t launch_attention_backward_f32(const AttnDims& A, const float* q, const float* k, const float* v,
                                           const float* out, const float* lse, const float* dout, const int32_t* cu_q,

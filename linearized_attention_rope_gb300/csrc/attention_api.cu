@@ -139,6 +139,7 @@ constexpr size_t kWsHead = 256;  // the error word
 size_t attn_ws_bytes(const hla_attn_params* p, int64_t total_q, int64_t total_k, int n_seqs, bool backward) {
     size_t n = kWsHead;
     if (!backward && p->dtype == HLA_DTYPE_BF16) n += attention_tc_part_bytes(attn_dims(p, n_seqs, total_q, total_k));
+    if (!backward && p->dtype == HLA_DTYPE_F32) n += attention_f32_part_bytes(attn_dims(p, n_seqs, total_q, total_k));
     if (backward && p->dtype == HLA_DTYPE_BF16) n += attention_backward_tc_bytes(attn_dims(p, n_seqs, total_q, total_k));
     if (backward && p->dtype == HLA_DTYPE_F32)
         n += attention_backward_f32_floats(attn_dims(p, n_seqs, total_q, total_k)) * sizeof(float);
@@ -250,8 +251,8 @@ HLA_API int hla_attention(const hla_attn_params* p, const void* q, const void* k
                                                    static_cast<bf*>(out), static_cast<bf*>(nullptr), lse, err, st));
     if (f32)
         return status(launch_attention_f32(A, static_cast<const float*>(q), static_cast<const float*>(k),
-                                           static_cast<const float*>(v), cu_q, cu_k, static_cast<float*>(out), lse, err,
-                                           st));
+                                           static_cast<const float*>(v), cu_q, cu_k, static_cast<float*>(out), lse,
+                                           reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHead), err, st));
     return status(launch_attention_tc(A, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
                                       cu_q, cu_k, static_cast<bf*>(out), lse, static_cast<char*>(ws) + kWsHead, err, st));
 }

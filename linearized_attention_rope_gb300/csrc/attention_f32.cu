@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kB = 64;  // keys of a forward tile, rows of a gradient tile
 constexpr int kThreads = 256;
+constexpr int kPartTiles = 8;  // key tiles of a part, at least
 template <int D> constexpr int kSmallGroups = D == 64 ? 4 : 2;  // groups of a smaller block: what shared memory holds
 
 template <int D> constexpr int kPitch = D + 4;
@@ -163,12 +164,13 @@ __device__ __forceinline__ void group_sums(float* buf, int g, int tid, float (&x
     __syncthreads();
 }
 
-// BM rows per block, W groups of 4 BM threads that take the key tiles in turn, ST stages of K and V each.
+// BM rows per block, W groups of 4 BM threads that take the key tiles in turn, ST stages of K and V each.  parts > 1:
+// block z takes a part of whole tiles (those past the row's parts none) and leaves its results in out and lse, [parts][...].
 template <int D, int BM, int W, int ST>
 __global__ void __launch_bounds__(BM * 4 * W)
 attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                     const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, float* __restrict__ out,
-                    float* __restrict__ lse, int32_t* __restrict__ err) {
+                    float* __restrict__ lse, int parts, int32_t* __restrict__ err) {
     extern __shared__ __align__(16) float sm[];
     constexpr int T = BM * 4, kGroup = ST * 2 * kB * kPitch<D> + BM * kPPitch;
     const int g = threadIdx.x / T, tid = threadIdx.x % T, ty = tid >> 4, tx = tid & 15;
@@ -181,6 +183,19 @@ attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __rest
     if (!B.found) return;
     const int h = blockIdx.y, hk = h / A.G;
     const int off = B.lk - B.lq, end = min(B.lk, min(B.first + BM, B.lq) + off);  // keys some row sees: [0, end)
+    int t0 = 0, t1 = (max(0, end) + kB - 1) / kB;                                 // this block's key tiles
+    if (parts > 1) {
+        const int n = t1, cut = max(1, min(parts, n / kPartTiles)), z = blockIdx.z;
+        t0 = z < cut ? n * z / cut : n;
+        t1 = z < cut ? n * (z + 1) / cut : n;
+        out += z * A.total_q * A.Hq * D;
+        lse += z * A.total_q * A.Hq;
+        if (t0 >= t1) {  // no tiles: the join looks at lse only
+            const int p = B.first + (int)threadIdx.x;
+            if ((int)threadIdx.x < BM && p < B.lq) lse[(B.q0 + p) * A.Hq + h] = -INFINITY;
+            return;
+        }
+    }
     const float *kb = k + B.k0 * A.sk + (int64_t)hk * D, *vb = v + B.k0 * A.sv + (int64_t)hk * D;
     auto load = [&](int stage, int j0) {  // keys that no row of the block sees are zeros: what they hold stays out
         copy_rows<D, kB, T>(kv + 2 * stage * kB * kPitch<D>, kb, A.sk, j0, end, tid);
@@ -189,7 +204,7 @@ attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __rest
     };
     copy_rows<D, BM, T * W>(qs, q + B.q0 * A.sq + (int64_t)h * D, A.sq, B.first, B.lq, threadIdx.x);
     copy_commit();
-    load(0, g * kB);
+    load(0, (t0 + g) * kB);
     copy_wait(1);
     if (W > 1) __syncthreads();  // the query rows are every group's
     const float cs = A.scale * kLog2e;
@@ -201,8 +216,8 @@ attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __rest
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
     }
-    for (int j0 = g * kB, stage = 0; j0 < end; j0 += W * kB, stage ^= ST - 1) {
-        const bool more = j0 + W * kB < end;
+    for (int j0 = (t0 + g) * kB, stage = 0; j0 < t1 * kB; j0 += W * kB, stage ^= ST - 1) {
+        const bool more = j0 + W * kB < t1 * kB;
         if (ST == 2 && more) load(stage ^ 1, j0 + W * kB);
         copy_wait(ST == 2 && more);
         group_sync<T>(g);
@@ -510,24 +525,42 @@ int block_rows(int64_t total, int n_seqs, int heads, int least) {
     return (total / 32 + n_seqs) * heads >= least ? 32 : 16;
 }
 
+// Parts that the keys of few rows (chunks behind earlier keys) are cut into at most, a block each, joined in order: one
+// for every kPartTiles tiles that a single sequence could have, where the blocks would not fill the SMs twice.  Forward:
+// 186 rows in 5, one of them 31 behind 3506 keys, 8/4 heads of 128, 250 -> 58 us; 64 rows behind 8128, 32/8 of 128, 567 ->
+// 289; one row of 3000, one head of 64, 77 -> 23; 5 x 100 behind 900, 4/2 of 64, 42 -> 43; 4 x 1 behind 2000, 32/8 of 128,
+// 145 -> 158.
+int row_parts(const AttnDims& A) {
+    const int64_t blocks = (A.total_q / 32 + A.n_seqs) * A.Hq;
+    if (4 * A.total_q > A.total_k || blocks >= 2 * 152) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(32, A.total_k / (kPartTiles * kB)));
+}
+
 template <int D, int BM, int W, int ST>
 cudaError_t rows_forward(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
-                         const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
+                         const int32_t* cu_k, float* out, float* lse, int parts, int32_t* err, cudaStream_t st) {
     static DeviceCache cache;
     cudaError_t e = allow_smem(cache, attn_fwd_f32_kernel<D, BM, W, ST>, fwd_smem<D, BM, W, ST>());
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(A.total_q / BM + A.n_seqs), (unsigned)A.Hq);
-    attn_fwd_f32_kernel<D, BM, W, ST><<<grid, BM * 4 * W, fwd_smem<D, BM, W, ST>(), st>>>(A, q, k, v, cu_q, cu_k, out, lse, err);
+    const dim3 grid((unsigned)(A.total_q / BM + A.n_seqs), (unsigned)A.Hq, (unsigned)parts);
+    attn_fwd_f32_kernel<D, BM, W, ST><<<grid, BM * 4 * W, fwd_smem<D, BM, W, ST>(), st>>>(A, q, k, v, cu_q, cu_k, out, lse, parts,
+                                                                                        err);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t forward(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
-                    const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
-    const int qb = block_rows(A.total_q, A.n_seqs, A.Hq, 76);
-    return (qb == 64   ? rows_forward<D, 64, 1, 2>
-            : qb == 32 ? rows_forward<D, 32, kSmallGroups<D>, 1>
-                       : rows_forward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, cu_q, cu_k, out, lse, err, st);
+                    const int32_t* cu_k, float* out, float* lse, float* part_ws, int32_t* err, cudaStream_t st) {
+    const int qb = block_rows(A.total_q, A.n_seqs, A.Hq, 76), parts = row_parts(A);
+    const int64_t rows = A.total_q * A.Hq;
+    float *part_lse = part_ws, *part_o = part_ws + (parts * rows + 3) / 4 * 4;
+    const cudaError_t e = (qb == 64   ? rows_forward<D, 64, 1, 2>
+                           : qb == 32 ? rows_forward<D, 32, kSmallGroups<D>, 1>
+                                      : rows_forward<D, 16, kSmallGroups<D>, 1>)(
+        A, q, k, v, cu_q, cu_k, parts > 1 ? part_o : out, parts > 1 ? part_lse : lse, parts, err, st);
+    if (e != cudaSuccess || parts == 1) return e;
+    attention_join_kernel<D, float><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(A, cu_q, parts, part_o, part_lse, out, lse);
+    return cudaGetLastError();
 }
 
 template <int D, int BN, int W, int ST>
@@ -603,8 +636,13 @@ attn_empty_kernel(int64_t total, int64_t other, int n_seqs, const int32_t* __res
 }  // namespace
 
 cudaError_t launch_attention_f32(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
-                                 const int32_t* cu_k, float* out, float* lse, int32_t* err, cudaStream_t st) {
-    return (A.d == 128 ? forward<128> : forward<64>)(A, q, k, v, cu_q, cu_k, out, lse, err, st);
+                                 const int32_t* cu_k, float* out, float* lse, float* part_ws, int32_t* err,
+                                 cudaStream_t st) {
+    return (A.d == 128 ? forward<128> : forward<64>)(A, q, k, v, cu_q, cu_k, out, lse, part_ws, err, st);
+}
+size_t attention_f32_part_bytes(const AttnDims& A) {
+    const int64_t parts = row_parts(A), rows = A.total_q * A.Hq;
+    return parts > 1 ? (size_t)((parts * rows + 3) / 4 * 4 + parts * rows * A.d) * sizeof(float) : 0;
 }
 size_t attention_backward_f32_floats(const AttnDims& A) {
     return (size_t)((A.total_q * A.Hq + 63) / 64 * 64 + (A.G > 1 ? 2 * A.total_k * A.Hq * A.d : 0));

@@ -491,44 +491,6 @@ attention_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     if (warp == 9) umma::tmem_dealloc(tmem, C::kCols);
 }
 
-// Adds the parts of every row of the sequences, in order; a warp per row and head.
-template <int D>
-__global__ void __launch_bounds__(256)
-attention_join_kernel(AttnDims A, const int32_t* __restrict__ cu_q, int parts, const float* __restrict__ part_o,
-                      const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
-    constexpr int E = D / 32;
-    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), rows = A.total_q * A.Hq;
-    const int lane = threadIdx.x & 31;
-    if (r >= rows) return;
-    const int64_t t = r / A.Hq;
-    int64_t a, n;
-    seq_range(cu_q, seq_of_token(cu_q, A.n_seqs, t), A.total_q, &a, &n);
-    if (t < a || t >= a + n) return;  // behind the last sequence
-    const float l = lane < parts ? __ldg(part_lse + lane * rows + r) : -INFINITY;
-    float m = l;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float w = l == -INFINITY ? 0.f : exp2f((l - m) * kLog2e);  // NaN stays NaN
-    float sum = w, acc[E];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-    for (int x = 0; x < E; ++x) acc[x] = 0.f;
-    for (int p = 0; p < parts; ++p) {
-        const float wp = __shfl_sync(0xffffffffu, w, p);
-        if (wp == 0.f) continue;  // no keys
-        float o[E];
-        load_vec<E>(part_o + (p * rows + r) * D + lane * E, o);
-#pragma unroll
-        for (int x = 0; x < E; ++x) acc[x] = fmaf(wp, o[x], acc[x]);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int x = 0; x < E; x += 2)
-        *reinterpret_cast<uint32_t*>(out + r * D + lane * E + x) = pack_bf2(acc[x] * inv, acc[x + 1] * inv);
-    if (lane == 0) lse[r] = sum == 0.f ? -INFINITY : m + logf(sum);
-}
-
 // Items (pairs of query tiles) over all sequences and head groups: at most, and about.
 int64_t items_bound(const AttnDims& A) {
     const int pack = pack_of(A.G);
@@ -567,7 +529,7 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
     attention_tc_kernel<D><<<(unsigned)blocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mk, mv, v, cu_q, cu_k, lpack, parts, out,
                                                                              lse, part_o, part_lse, err);
     if (parts > 1)
-        attention_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(A, cu_q, parts, part_o, part_lse, out, lse);
+        attention_join_kernel<D, __nv_bfloat16><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(A, cu_q, parts, part_o, part_lse, out, lse);
     return cudaGetLastError();
 }
 

@@ -146,6 +146,15 @@ def test_whole_prompts_of_few_heads(d, hq, hkv, lens):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 4), (12, 2)])
+def test_few_rows_over_many_keys_in_fp32(d, hq, hkv):
+    # keys cut over blocks and joined: sequences of more, fewer and no parts, a row that sees a few keys of the first
+    full_check("f32", d, hq, hkv, [5, 46, 0, 31, 12], [656, 46, 700, 3537, 6])
+    full_check("f32", d, hq, hkv, [3], [9001])
+    full_check("f32", d, hq, hkv, [70], [530])
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("hq,hkv,q_lens,k_lens", [(8, 1, [700, 0, 300], None), (16, 1, [900], None),
                                                   (6, 2, [1500, 7], None), (32, 1, [130, 260], [130, 700]),
                                                   (24, 2, [500], [200])])
