@@ -167,8 +167,8 @@ attention_join_kernel(AttnDims A, const int32_t* __restrict__ cu_q, int parts, c
     if (lane == 0) lse[r] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
-// fp32 layers (attention_f32.cu), the bytes of partial results (0: one part), and those their gradient needs: dout . out per row and head, and (several query
-// heads per kv head) dk and dv of each query head.
+// fp32 layers (attention_f32.cu), the bytes of partial results (0: one part), and those their gradient needs: dout . out per row and head, (several query
+// heads per kv head) dk and dv of each query head, and dq of each part.
 cudaError_t launch_attention_f32(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
                                  const int32_t* cu_k, float* out, float* lse, float* part_ws, int32_t* err,
                                  cudaStream_t st);

@@ -164,6 +164,9 @@ __device__ __forceinline__ void group_sums(float* buf, int g, int tid, float (&x
     __syncthreads();
 }
 
+// Parts of a block's n key tiles: at least kPartTiles in each.
+__device__ __forceinline__ int parts_of(int n, int parts) { return max(1, min(parts, n / kPartTiles)); }
+
 // BM rows per block, W groups of 4 BM threads that take the key tiles in turn, ST stages of K and V each.  parts > 1:
 // block z takes a part of whole tiles (those past the row's parts none) and leaves its results in out and lse, [parts][...].
 template <int D, int BM, int W, int ST>
@@ -185,7 +188,7 @@ attn_fwd_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __rest
     const int off = B.lk - B.lq, end = min(B.lk, min(B.first + BM, B.lq) + off);  // keys some row sees: [0, end)
     int t0 = 0, t1 = (max(0, end) + kB - 1) / kB;                                 // this block's key tiles
     if (parts > 1) {
-        const int n = t1, cut = max(1, min(parts, n / kPartTiles)), z = blockIdx.z;
+        const int n = t1, cut = parts_of(n, parts), z = blockIdx.z;
         t0 = z < cut ? n * z / cut : n;
         t1 = z < cut ? n * (z + 1) / cut : n;
         out += z * A.total_q * A.Hq * D;
@@ -434,7 +437,7 @@ template <int D, int BM, int W, int ST>
 __global__ void __launch_bounds__(BM * 4 * W)
 attn_dq_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                    const float* __restrict__ lse, const float* __restrict__ dout, const float* __restrict__ delta,
-                   const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, float* __restrict__ dq) {
+                   const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, float* __restrict__ dq, int parts) {
     extern __shared__ __align__(16) float sm[];
     constexpr int T = BM * 4, kGroup = ST * 2 * kB * kPitch<D> + BM * kPPitch;
     const int g = threadIdx.x / T, tid = threadIdx.x % T, ty = tid >> 4, tx = tid & 15;
@@ -444,6 +447,14 @@ attn_dq_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restr
     if (!B.found) return;
     const int h = blockIdx.y, hk = h / A.G;
     const int off = B.lk - B.lq, end = min(B.lk, min(B.first + BM, B.lq) + off);
+    int t0 = 0, t1 = (max(0, end) + kB - 1) / kB;  // this block's key tiles
+    if (parts > 1) {                               // (the sum takes as many parts of the row's as have tiles)
+        const int n = t1, cut = parts_of(n, parts), z = blockIdx.z;
+        if (z >= cut) return;
+        t0 = n * z / cut;
+        t1 = n * (z + 1) / cut;
+        dq += z * A.total_q * A.Hq * D;
+    }
     const float *kb = k + B.k0 * A.sk + (int64_t)hk * D, *vb = v + B.k0 * A.sv + (int64_t)hk * D;
     auto load = [&](int stage, int j0) {
         copy_rows<D, kB, T>(kv + 2 * stage * kB * kPitch<D>, kb, A.sk, j0, end, tid);
@@ -453,7 +464,7 @@ attn_dq_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restr
     copy_rows<D, BM, T * W>(qs, q + B.q0 * A.sq + (int64_t)h * D, A.sq, B.first, B.lq, threadIdx.x);
     copy_rows<D, BM, T * W>(os, dout + B.q0 * A.Hq * D + (int64_t)h * D, (int64_t)A.Hq * D, B.first, B.lq, threadIdx.x);
     copy_commit();
-    load(0, g * kB);
+    load(0, (t0 + g) * kB);
     copy_wait(1);
     if (W > 1) __syncthreads();
     float lse2[4], dl[4], acc[4][D / 16];
@@ -466,8 +477,8 @@ attn_dq_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restr
         for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
     }
     const float cs = A.scale * kLog2e;
-    for (int j0 = g * kB, stage = 0; j0 < end; j0 += W * kB, stage ^= ST - 1) {
-        const bool more = j0 + W * kB < end;
+    for (int j0 = (t0 + g) * kB, stage = 0; j0 < t1 * kB; j0 += W * kB, stage ^= ST - 1) {
+        const bool more = j0 + W * kB < t1 * kB;
         if (ST == 2 && more) load(stage ^ 1, j0 + W * kB);
         copy_wait(ST == 2 && more);
         group_sync<T>(g);
@@ -494,6 +505,29 @@ attn_dq_f32_kernel(AttnDims A, const float* __restrict__ q, const float* __restr
     }
     const float one[4] = {1.f, 1.f, 1.f, 1.f};
     store_rows<D, 4>(dq + B.q0 * A.Hq * D + (int64_t)h * D, (int64_t)A.Hq * D, B.first, B.lq, ty, tx, acc, one);
+}
+
+// dq of the sequences' rows from the parts of their blocks of BM rows, in order.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+attn_dq_sum_kernel(AttnDims A, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int bm, int parts,
+                   const float* __restrict__ part, float* __restrict__ dq) {
+    const int64_t per = (int64_t)A.Hq * (D / 4), n = A.total_q * per, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= n) return;
+    const int64_t t = i / per;
+    const int s = seq_of_token(cu_q, A.n_seqs, t);
+    int64_t a, lq, b, lk;
+    seq_range(cu_q, s, A.total_q, &a, &lq);
+    seq_range(cu_k, s, A.total_k, &b, &lk);
+    if (t < a || t >= a + lq) return;
+    const int64_t rows = min((t - a) / bm * bm + bm, lq), end = min(lk, rows + lk - lq);
+    const int cut = parts_of((int)((max((int64_t)0, end) + kB - 1) / kB), parts);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int z = 0; z < cut; ++z) {
+        const float4 u = reinterpret_cast<const float4*>(part)[z * n + i];
+        x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+    }
+    reinterpret_cast<float4*>(dq)[i] = x;
 }
 
 template <int D, int BM, int W, int ST> constexpr size_t fwd_smem() {
@@ -529,7 +563,7 @@ int block_rows(int64_t total, int n_seqs, int heads, int least) {
 // for every kPartTiles tiles that a single sequence could have, where the blocks would not fill the SMs twice.  Forward:
 // 186 rows in 5, one of them 31 behind 3506 keys, 8/4 heads of 128, 250 -> 58 us; 64 rows behind 8128, 32/8 of 128, 567 ->
 // 289; one row of 3000, one head of 64, 77 -> 23; 5 x 100 behind 900, 4/2 of 64, 42 -> 43; 4 x 1 behind 2000, 32/8 of 128,
-// 145 -> 158.
+// 145 -> 158.  Gradient (dq): 327 -> 158, 1109 -> 1081, 107 -> 46, 98 -> 110, 689 -> 700.
 int row_parts(const AttnDims& A) {
     const int64_t blocks = (A.total_q / 32 + A.n_seqs) * A.Hq;
     if (4 * A.total_q > A.total_k || blocks >= 2 * 152) return 1;
@@ -583,12 +617,18 @@ cudaError_t keys_backward(const AttnDims& A, const float* q, const float* k, con
 template <int D, int BM, int W, int ST>
 cudaError_t rows_backward(const AttnDims& A, const float* q, const float* k, const float* v, const float* lse,
                           const float* dout, const int32_t* cu_q, const int32_t* cu_k, float* dq, float* delta,
-                          cudaStream_t st) {
+                          float* part, int parts, cudaStream_t st) {
     static DeviceCache cache;
     cudaError_t e = allow_smem(cache, attn_dq_f32_kernel<D, BM, W, ST>, dq_smem<D, BM, W, ST>());
     if (e != cudaSuccess) return e;
-    attn_dq_f32_kernel<D, BM, W, ST><<<dim3((unsigned)(A.total_q / BM + A.n_seqs), (unsigned)A.Hq), BM * 4 * W,
-                                    dq_smem<D, BM, W, ST>(), st>>>(A, q, k, v, lse, dout, delta, cu_q, cu_k, dq);
+    const dim3 grid((unsigned)(A.total_q / BM + A.n_seqs), (unsigned)A.Hq, (unsigned)parts);
+    attn_dq_f32_kernel<D, BM, W, ST><<<grid, BM * 4 * W, dq_smem<D, BM, W, ST>(), st>>>(
+        A, q, k, v, lse, dout, delta, cu_q, cu_k, parts > 1 ? part : dq, parts);
+    if (parts > 1) {
+        const int64_t n = A.total_q * A.Hq * (D / 4);
+        attn_dq_sum_kernel<D><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(A, cu_q, cu_k, BM, parts, part,
+                                                                                              dq);
+    }
     return cudaGetLastError();
 }
 
@@ -598,6 +638,7 @@ cudaError_t backward(const AttnDims& A, const float* q, const float* k, const fl
                      float* dv, float* ws, int32_t* err, cudaStream_t st) {
     const int64_t rows = A.total_q * A.Hq;
     float *delta = ws, *parts = ws + (rows + 63) / 64 * 64;
+    float* dq_part = parts + (A.G > 1 ? 2 * A.total_k * A.Hq * D : 0);
     const int kb = block_rows(A.total_k, A.n_seqs, A.Hq, 152), qb = block_rows(A.total_q, A.n_seqs, A.Hq, 152);
     cudaError_t e = cudaSuccess;
     if (rows > 0) attn_delta_kernel<D><<<(unsigned)((rows + 7) / 8), kThreads, 0, st>>>(rows, out, dout, delta);
@@ -609,7 +650,8 @@ cudaError_t backward(const AttnDims& A, const float* q, const float* k, const fl
     if (e != cudaSuccess || rows == 0) return e;
     return (qb == 64   ? rows_backward<D, 64, 1, D == 64 ? 2 : 1>
             : qb == 32 ? rows_backward<D, 32, kSmallGroups<D>, 1>
-                       : rows_backward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, st);
+                       : rows_backward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, dq_part,
+                                                                  row_parts(A), st);
 }
 
 // Rows of the sequences set to zero (and lse to -infinity): what attention and its gradient are without keys or queries.
@@ -645,7 +687,8 @@ size_t attention_f32_part_bytes(const AttnDims& A) {
     return parts > 1 ? (size_t)((parts * rows + 3) / 4 * 4 + parts * rows * A.d) * sizeof(float) : 0;
 }
 size_t attention_backward_f32_floats(const AttnDims& A) {
-    return (size_t)((A.total_q * A.Hq + 63) / 64 * 64 + (A.G > 1 ? 2 * A.total_k * A.Hq * A.d : 0));
+    const int64_t rows = A.total_q * A.Hq, parts = row_parts(A);
+    return (size_t)((rows + 63) / 64 * 64 + (A.G > 1 ? 2 * A.total_k * A.Hq * A.d : 0) + (parts > 1 ? parts * rows * A.d : 0));
 }
 cudaError_t launch_attention_backward_f32(const AttnDims& A, const float* q, const float* k, const float* v,
                                           const float* out, const float* lse, const float* dout, const int32_t* cu_q,
