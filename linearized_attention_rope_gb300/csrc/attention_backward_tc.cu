@@ -231,8 +231,8 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         bool ok = true;
         if (warp == 8) {
             // ---- loads: the ring takes Q 0, dO 0, Q 1, dO 1, ... of every item.  Of rows behind the sequence,
-            //      infinities and NaN are cleared: their probability is 0 (the ring holds at most four tiles, so four barriers keep a tile's signal until
-            //      the products have seen it)
+            //      infinities and NaN are cleared: their probability is 0 (the ring holds at most four tiles, so four
+            //      barriers keep a tile's signal until the products have seen it)
             static_assert(C::kSlots <= 8, "tiles in the ring");
             Ring ring;
             int used = 0, fixed = 0, kv_loads = 0;
@@ -565,7 +565,8 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
     const uint32_t base = umma::smem_addr(sm), bars = base + C::kBar;
     const uint32_t bar_q = bars, bar_qe = bar_q + 8, bar_full = bar_qe + 8, bar_empty = bar_full + 8 * C::kSlots;
     const uint32_t bar_s = bar_empty + 8 * C::kSlots, bar_se = bar_s + 8, bar_dp = bar_se + 8, bar_fix = bar_dp + 16;
-    const uint32_t bar_clear = bar_fix + 64, bar_done = bar_clear + 16, bar_oe = bar_done + 8, bar_it = bar_oe + 8, bar_ie = bar_it + 8 * kItems;
+    const uint32_t bar_clear = bar_fix + 64, bar_done = bar_clear + 16, bar_oe = bar_done + 8, bar_it = bar_oe + 8;
+    const uint32_t bar_ie = bar_it + 8 * kItems;
     const uint32_t bar_ask = bar_ie + 8 * kItems, bar_want = bar_ask + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 344);
     ItemRing* items = reinterpret_cast<ItemRing*>(sm + C::kItem);
