@@ -17,8 +17,8 @@
 // (2 at head dim 128) take the tiles in turn and add their sums at the end, in
 // order.
 //
-// Bound by the fp32 FMA rate and shared-memory reads (two 16-byte reads per
-// 4 x 4 x 4 FMAs).  4096 tokens, 8/2 heads of 128: forward 1141 us (30 TFLOP/s of
+// Bound by shared-memory reads (eight of 16 bytes per 64 FMAs, at a quarter of a
+// warp a cycle) and the fp32 FMA rate.  4096 tokens, 8/2 heads of 128: forward 1141 us (30 TFLOP/s of
 // the 80 the FMAs could do), gradient 3904 us (31 with the 7 products it forms);
 // 813 tokens, 4/2 heads of 64, where the walk of one block is what takes the
 // time: 24 and 63 us (blocks of 32 and one group: 31 and 91).

@@ -45,9 +45,9 @@
 // Bound by the tensor cores (4 d flops per visible score) together with the
 // softmax's issue slots (about 4 instructions and one exponential per score).
 // bf16, 32/8 heads of 128: 32768 tokens in 5.1 to 5.3 ms (1670 to 1710 TFLOP/s; a large library
-// product sustains 1695), 4096 in 105 us (1306: 512 items of 1 to 32 key tiles
+// product sustains 1695), 4096 in 104 to 108 us (1300: 512 items of 1 to 32 key tiles
 // over 152 SMs, and the half of each edge tile that the mask throws away).
-// 4 x 4096 tokens, 32/8 heads of 64: 266 us (half the flops per exponential).
+// 4 x 4096 tokens, 32/8 heads of 64: 270 us (half the flops per exponential).
 // 64 rows over 131072 keys: 105 us.
 #include <type_traits>
 
