@@ -9,6 +9,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_decode.cuh"
 
@@ -252,19 +253,29 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
 // E4M3 rows become fp16 exactly.  The query is scaled by a power of two per
 // head into fp16 (bf16 has 8 bits, fp16 11; elements 2^-14 below the largest
 // lose bits of 2^-25 of it).  A key row's power of two goes onto its score, a
-// value row's into the exponent of its weight: weights are 2^(s - M) 2^ev /
-// 2^(Mt - M), with a reference Mt of their own, so rows of any size meet in
-// fp16 (11 bits) with the largest product near 1.  bf16 caches: products in bf16,
+// value row's into the exponent of its weight, 2^x with x = s + ev - Mt and a
+// reference Mt of their own.  Weights are fp16 too: 11 bits of them from
+// 2^(kTop + 1) down to 2^-14 (x = -kBand), steps of 2^-24 below.  A weight's error there, 2^-39 of
+// Mt's, is 2^-31 of the sum of weights at most while the value rows' exponents are
+// within kLike of each other.  But a key whose value row is large in one column sets Mt
+// for all of them, and the weights that this leaves too few bits may be all that the
+// other columns have: a warp whose rows differ by more goes over them again, kBand powers
+// of two of weights at a time (64 x 8192 tokens 191 -> 362 us, most of it read from L2).
+// (Always exact, by values and two-part weights in bf16, to which no instruction
+// converts: 64 x 8192 tokens 185 -> 273 us; light weights looked for one by one:
+// 223, for want of registers.)  bf16 caches: products in bf16,
 // weights in two bf16 parts (with one, outputs of a few heads were off by up to
 // 1.5 times the rounding of the result; the second costs nothing beside the loads).
 //
 // A warp takes 32 keys at a time (16 of 256 bytes), so that the 12 to 16 warps
 // of an SM keep some 60 KB on their way.
 //
-// References are raised only when a score exceeds them by 2^8 (a vote per
-// tile, no reduction); the weights stay at most 2^8.
+// References are raised only when a score exceeds them by 2^8 (8-bit rows: 2), by a
+// vote per tile, no reduction.
 
-constexpr float kLazy = 8.0f;
+constexpr float kLazy = 8.0f, kLazyT = 1.0f;
+constexpr float kTop = 14.0f, kBand = 28.0f, kLeast = -126.0f;  // weights of 2^kLeast of the reference and less are 0
+constexpr uint32_t kLike = 8;
 constexpr uint32_t kNoRow = 0xffffffffu;
 
 // Tiles of 16 keys per page, and division by it: i / tiles = i mul >> shift for i < 2^31 (mul = ceil(2^shift /
@@ -322,6 +333,11 @@ __device__ __forceinline__ uint32_t top2(float a, float b) {
 __device__ __forceinline__ float rest(float p) {
     const float r = fmaxf(p - __uint_as_float(__float_as_uint(p) & 0xffff0000u), 1.17549435e-38f);
     return p == 0.f ? 0.f : r;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 __device__ __forceinline__ float safe_ref(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -396,10 +412,8 @@ decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_b
             qs0 = __shfl_sync(0xffffffffu, qscale, 8 * t);
             qs1 = __shfl_sync(0xffffffffu, qscale, 8 * t + 4);
         }
-        float o[kMt][4];
-#pragma unroll
-        for (int x = 0; x < kMt; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
-        float M0 = -INFINITY, M1 = -INFINITY, T0 = -INFINITY, T1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float o[kMt][4], M0, M1, T0, T1, l0, l1;
+        uint32_t spread = 0u;  // of the value rows' exponents (bytes): the largest, and 256 less the smallest but 0
 
         // tiles of 16 keys: the page a tile lies in (-1: past the last key), its cache row (kNoRow: no such page)
         const uint32_t n_tiles = (uint32_t)((len + 15) / 16);
@@ -419,7 +433,16 @@ decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_b
         };
         uint4 kx[kSub][2][kKp];
         uint32_t vx[kSub][4][kVw];
-        int ex[kSub][4];  // exponent bytes: keys g, g + 8, then values
+        // exponent bytes of both tiles: of tile lane / 16, keys' (bit 3 of the lane 0) or values', keys 2 (lane % 8) and the next
+        uint32_t ex = 0u;
+        const uint8_t* ex_base = (lane & 8 ? c.v_exp : c.k_exp) + 2 * (lane & 7);
+        auto load_ex = [&](const uint32_t (&r)[kSub]) {
+            const uint32_t mine = lane < 16 ? r[0] : r[kSub - 1];
+            return mine == kNoRow ? 0u : (uint32_t)*reinterpret_cast<const uint16_t*>(ex_base + mine);
+        };
+        auto ex_of = [&](int y, int kind, int key) {  // keys g and g + 8: key 0 and 8
+            return __byte_perm(__shfl_sync(0xffffffffu, ex, y * 16 + kind * 8 + (g + key) / 2), 0u, 0x4440 + (g & 1));
+        };
         auto load_k = [&](int y, uint32_t row) {
             if (row == kNoRow) return;
             const char* p = static_cast<const char*>(c.k) + (size_t)(row + g) * kRow + t * 16;
@@ -427,13 +450,6 @@ decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_b
             for (int i = 0; i < kKp; ++i) {
                 kx[y][0][i] = __ldcs(reinterpret_cast<const uint4*>(p + i * 64));
                 kx[y][1][i] = __ldcs(reinterpret_cast<const uint4*>(p + 8 * kRow + i * 64));
-            }
-            if constexpr (E4M3) {
-                const uint8_t *ke = c.k_exp + (row + g), *ve = c.v_exp + (row + g);
-                ex[y][0] = ke[0];
-                ex[y][1] = ke[8];
-                ex[y][2] = ve[0];
-                ex[y][3] = ve[8];
             }
         };
         auto load_v = [&](int y, uint32_t row, int n) {  // n: keys of the tile; the rows behind them are zeros
@@ -463,152 +479,196 @@ decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_b
         };
         // tiles of this warp: kSub in a row from (4 unit + warp) kSub
         constexpr uint32_t kStep = kWarps * kSub;
-        uint32_t i = (uint32_t)((u - useq) * kWarps + warp) * kSub;
         const uint32_t iend = min((uint32_t)(e - useq) * kStep, n_tiles);
         auto keys_of = [&](uint32_t j) { return (int)min((int64_t)16, len - (int64_t)j * 16); };
-        uint32_t row[kSub], at_next[kSub];
-        int page_next[kSub];
+        // One pass over them.  BANDS: of the weights with x in (-kBand, 0] - up only (all above, with up = 0); whether there
+        // are lighter ones.
+        auto walk = [&](auto bands, float up) {
+            constexpr bool BANDS = decltype(bands)::value;
+            bool lighter = false;
 #pragma unroll
-        for (int y = 0; y < kSub; ++y) {
-            uint32_t at;
-            const int page = page_of(i + y, &at);
-            row[y] = row_of(i + y, page, at);
-            page_next[y] = page_of(i + kStep + y, &at_next[y]);
-            load_k(y, row[y]);
-            load_v(y, row[y], keys_of(i + y));
-        }
-        for (; i < iend; i += kStep) {
-            const bool more = i + kStep < iend;
-            uint32_t row_next[kSub];
+            for (int x = 0; x < kMt; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+            M0 = M1 = T0 = T1 = -INFINITY;
+            l0 = l1 = 0.f;
+            uint32_t i = (uint32_t)((u - useq) * kWarps + warp) * kSub;
+            uint32_t row[kSub], at_next[kSub];
+            int page_next[kSub];
 #pragma unroll
             for (int y = 0; y < kSub; ++y) {
-                row_next[y] = more ? row_of(i + kStep + y, page_next[y], at_next[y]) : kNoRow;
-                if (more) page_next[y] = page_of(i + 2 * kStep + y, &at_next[y]);
+                uint32_t at;
+                const int page = page_of(i + y, &at);
+                row[y] = row_of(i + y, page, at);
+                page_next[y] = page_of(i + kStep + y, &at_next[y]);
+                load_k(y, row[y]);
+                load_v(y, row[y], keys_of(i + y));
             }
-            // ---- scores of every sub-tile (base-2 logs), and the exponents of its value rows
-            float sc[kSub][4], ve[kSub][2];
-            float h0 = -INFINITY, h1 = -INFINITY, t0 = -INFINITY, t1 = -INFINITY;
+            if constexpr (E4M3) ex = load_ex(row);
+            for (; i < iend; i += kStep) {
+                const bool more = i + kStep < iend;
+                uint32_t row_next[kSub];
 #pragma unroll
-            for (int y = 0; y < kSub; ++y) {
-                float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
-                const int n = row[y] != kNoRow ? keys_of(i + y) : 0;
-#pragma unroll
-                for (int x = 0; x < kKp; ++x) {
-                    const uint32_t a[4] = {kx[y][0][x].x, kx[y][0][x].y, kx[y][0][x].z, kx[y][0][x].w};
-                    const uint32_t b[4] = {kx[y][1][x].x, kx[y][1][x].y, kx[y][1][x].z, kx[y][1][x].w};
-                    if constexpr (E4M3) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            uint32_t al, ah, bl, bh;
-                            h2_from_e4m3(a[w], al, ah);
-                            h2_from_e4m3(b[w], bl, bh);
-                            mma16816<true>(w & 1 ? a1 : a0, al, bl, ah, bh, qf[x * 4 + w][0], qf[x * 4 + w][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < 2; ++w)
-                            mma16816<false>(w & 1 ? a1 : a0, a[2 * w], b[2 * w], a[2 * w + 1], b[2 * w + 1],
-                                            qf[x * 2 + w][0], qf[x * 2 + w][1]);
-                    }
+                for (int y = 0; y < kSub; ++y) {
+                    row_next[y] = more ? row_of(i + kStep + y, page_next[y], at_next[y]) : kNoRow;
+                    if (more) page_next[y] = page_of(i + 2 * kStep + y, &at_next[y]);
                 }
-                float f0 = 1.f, f1 = 1.f;  // the key rows' powers of two
-                ve[y][0] = ve[y][1] = 0.f;
+                uint32_t ex_next = 0u;
                 if constexpr (E4M3) {
-                    f0 = ex[y][0] ? __uint_as_float((uint32_t)ex[y][0] << 23) : __uint_as_float(0x400000u);
-                    f1 = ex[y][1] ? __uint_as_float((uint32_t)ex[y][1] << 23) : __uint_as_float(0x400000u);
-                    ve[y][0] = (float)(ex[y][2] - 127);
-                    ve[y][1] = (float)(ex[y][3] - 127);
+                    ex_next = load_ex(row_next);
+                    // (bytes of rows behind the last key count as 0)
+                    const int n = min(2, keys_of(i + (lane >> 4)) - 2 * (lane & 7));
+                    const uint32_t a = lane & 8 && n > 0 ? ex & 0xffu : 0u, b = lane & 8 && n > 1 ? ex >> 8 : 0u;
+                    spread = max_u16x2(spread, max(a, b) | max(256u - a & 0xffu, 256u - b & 0xffu) << 16);
                 }
-                load_k(y, row_next[y]);
-                const bool on0 = g < n, on1 = g + 8 < n;
-                sc[y][0] = on0 ? (a0[0] + a1[0]) * f0 * qs0 : -INFINITY;
-                sc[y][1] = on0 ? (a0[1] + a1[1]) * f0 * qs1 : -INFINITY;
-                sc[y][2] = on1 ? (a0[2] + a1[2]) * f1 * qs0 : -INFINITY;
-                sc[y][3] = on1 ? (a0[3] + a1[3]) * f1 * qs1 : -INFINITY;
-                h0 = fmaxf(h0, fmaxf(sc[y][0], sc[y][2]));
-                h1 = fmaxf(h1, fmaxf(sc[y][1], sc[y][3]));
-                if constexpr (E4M3) {
-                    t0 = fmaxf(t0, fmaxf(sc[y][0] + ve[y][0], sc[y][2] + ve[y][1]));
-                    t1 = fmaxf(t1, fmaxf(sc[y][1] + ve[y][0], sc[y][3] + ve[y][1]));
-                }
-            }
-            bool grow = h0 > M0 + kLazy || h1 > M1 + kLazy;
-            if constexpr (E4M3) grow |= t0 > T0 + kLazy || t1 > T1 + kLazy;
-            if (__any_sync(0xffffffffu, grow)) {
+                // ---- scores of every sub-tile (base-2 logs), and the exponents of its value rows
+                float sc[kSub][4], ve[kSub][2];
+                float h0 = -INFINITY, h1 = -INFINITY, t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1) {
-                    h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, sh));
-                    h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, sh));
-                    if constexpr (E4M3) {
-                        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, sh));
-                        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, sh));
-                    }
-                }
-                const float m0 = fmaxf(M0, h0), m1 = fmaxf(M1, h1);
-                const float n0 = E4M3 ? fmaxf(T0, t0) : m0, n1 = E4M3 ? fmaxf(T1, t1) : m1;
-                l0 *= M0 == -INFINITY ? 0.f : exp2f(M0 - m0);
-                l1 *= M1 == -INFINITY ? 0.f : exp2f(M1 - m1);
-                const float r0 = T0 == -INFINITY ? 0.f : exp2f(T0 - n0), r1 = T1 == -INFINITY ? 0.f : exp2f(T1 - n1);
-                M0 = m0;
-                M1 = m1;
-                T0 = n0;
-                T1 = n1;
+                for (int y = 0; y < kSub; ++y) {
+                    float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+                    const int n = row[y] != kNoRow ? keys_of(i + y) : 0;
 #pragma unroll
-                for (int x = 0; x < kMt; ++x) {
-                    o[x][0] *= r0;
-                    o[x][1] *= r1;
-                    o[x][2] *= r0;
-                    o[x][3] *= r1;
-                }
-            }
-            // ---- weights, and the values they go to
-            const float ref0 = safe_ref(M0), ref1 = safe_ref(M1), ret0 = safe_ref(T0), ret1 = safe_ref(T1);
-#pragma unroll
-            for (int y = 0; y < kSub; ++y) {
-                float p0 = ex2(sc[y][0] - ref0), p1 = ex2(sc[y][1] - ref1);
-                float p2 = ex2(sc[y][2] - ref0), p3 = ex2(sc[y][3] - ref1);
-                l0 += p0 + p2;
-                l1 += p1 + p3;
-                if constexpr (E4M3) {
-                    p0 = ex2(sc[y][0] + (ve[y][0] - ret0));
-                    p1 = ex2(sc[y][1] + (ve[y][0] - ret1));
-                    p2 = ex2(sc[y][2] + (ve[y][1] - ret0));
-                    p3 = ex2(sc[y][3] + (ve[y][1] - ret1));
-                }
-                uint32_t b0, b1, c0 = 0u, c1 = 0u;  // bf16 weights in two parts
-                if constexpr (E4M3) {
-                    b0 = transpose8(pack2<true>(p0, p1));
-                    b1 = transpose8(pack2<true>(p2, p3));
-                } else {
-                    b0 = transpose8(top2(p0, p1));
-                    b1 = transpose8(top2(p2, p3));
-                    c0 = transpose8(pack2<false>(rest(p0), rest(p1)));
-                    c1 = transpose8(pack2<false>(rest(p2), rest(p3)));
-                }
-                if (row[y] != kNoRow) {
-#pragma unroll
-                    for (int w = 0; w < kVw; ++w) {
+                    for (int x = 0; x < kKp; ++x) {
+                        const uint32_t a[4] = {kx[y][0][x].x, kx[y][0][x].y, kx[y][0][x].z, kx[y][0][x].w};
+                        const uint32_t b[4] = {kx[y][1][x].x, kx[y][1][x].y, kx[y][1][x].z, kx[y][1][x].w};
                         if constexpr (E4M3) {
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const uint32_t sel = z ? 0x7362 : 0x5140;
-                                uint32_t a0, a1, a2, a3;
-                                h2_from_e4m3(__byte_perm(vx[y][0][w], vx[y][1][w], sel), a0, a1);
-                                h2_from_e4m3(__byte_perm(vx[y][2][w], vx[y][3][w], sel), a2, a3);
-                                mma16816<true>(o[2 * w + z], a0, a1, a2, a3, b0, b1);
+                            for (int w = 0; w < 4; ++w) {
+                                uint32_t al, ah, bl, bh;
+                                h2_from_e4m3(a[w], al, ah);
+                                h2_from_e4m3(b[w], bl, bh);
+                                mma16816<true>(w & 1 ? a1 : a0, al, bl, ah, bh, qf[x * 4 + w][0], qf[x * 4 + w][1]);
                             }
                         } else {
-                            const uint32_t a0 = __byte_perm(vx[y][0][w], vx[y][1][w], 0x5410);
-                            const uint32_t a1 = __byte_perm(vx[y][0][w], vx[y][1][w], 0x7632);
-                            const uint32_t a2 = __byte_perm(vx[y][2][w], vx[y][3][w], 0x5410);
-                            const uint32_t a3 = __byte_perm(vx[y][2][w], vx[y][3][w], 0x7632);
-                            mma16816<false>(o[w], a0, a1, a2, a3, c0, c1);
-                            mma16816<false>(o[w], a0, a1, a2, a3, b0, b1);
+#pragma unroll
+                            for (int w = 0; w < 2; ++w)
+                                mma16816<false>(w & 1 ? a1 : a0, a[2 * w], b[2 * w], a[2 * w + 1], b[2 * w + 1],
+                                                qf[x * 2 + w][0], qf[x * 2 + w][1]);
                         }
                     }
+                    float f0 = 1.f, f1 = 1.f;  // the key rows' powers of two
+                    ve[y][0] = ve[y][1] = 0.f;
+                    if constexpr (E4M3) {
+                        const uint32_t e0 = ex_of(y, 0, 0), e1 = ex_of(y, 0, 8);
+                        f0 = e0 ? __uint_as_float(e0 << 23) : __uint_as_float(0x400000u);
+                        f1 = e1 ? __uint_as_float(e1 << 23) : __uint_as_float(0x400000u);
+                        ve[y][0] = (float)((int)ex_of(y, 1, 0) - 127);
+                        ve[y][1] = (float)((int)ex_of(y, 1, 8) - 127);
+                    }
+                    load_k(y, row_next[y]);
+                    const bool on0 = g < n, on1 = g + 8 < n;
+                    sc[y][0] = on0 ? (a0[0] + a1[0]) * f0 * qs0 : -INFINITY;
+                    sc[y][1] = on0 ? (a0[1] + a1[1]) * f0 * qs1 : -INFINITY;
+                    sc[y][2] = on1 ? (a0[2] + a1[2]) * f1 * qs0 : -INFINITY;
+                    sc[y][3] = on1 ? (a0[3] + a1[3]) * f1 * qs1 : -INFINITY;
+                    h0 = fmaxf(h0, fmaxf(sc[y][0], sc[y][2]));
+                    h1 = fmaxf(h1, fmaxf(sc[y][1], sc[y][3]));
+                    if constexpr (E4M3) {
+                        t0 = fmaxf(t0, fmaxf(sc[y][0] + ve[y][0], sc[y][2] + ve[y][1]));
+                        t1 = fmaxf(t1, fmaxf(sc[y][1] + ve[y][0], sc[y][3] + ve[y][1]));
+                    }
                 }
-                load_v(y, row_next[y], keys_of(i + kStep + y));
-                row[y] = row_next[y];
+                bool grow = h0 > M0 + kLazy || h1 > M1 + kLazy;
+                if constexpr (E4M3) grow |= t0 > T0 + kLazyT || t1 > T1 + kLazyT;
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int sh = 4; sh < 32; sh <<= 1) {
+                        h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, sh));
+                        h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, sh));
+                        if constexpr (E4M3) {
+                            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, sh));
+                            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, sh));
+                        }
+                    }
+                    const float m0 = fmaxf(M0, h0), m1 = fmaxf(M1, h1);
+                    const float n0 = E4M3 ? fmaxf(T0, t0) : m0, n1 = E4M3 ? fmaxf(T1, t1) : m1;
+                    l0 *= M0 == -INFINITY ? 0.f : exp2f(M0 - m0);
+                    l1 *= M1 == -INFINITY ? 0.f : exp2f(M1 - m1);
+                    const float r0 = T0 == -INFINITY ? 0.f : exp2f(T0 - n0), r1 = T1 == -INFINITY ? 0.f : exp2f(T1 - n1);
+                    M0 = m0;
+                    M1 = m1;
+                    T0 = n0;
+                    T1 = n1;
+#pragma unroll
+                    for (int x = 0; x < kMt; ++x) {
+                        o[x][0] *= r0;
+                        o[x][1] *= r1;
+                        o[x][2] *= r0;
+                        o[x][3] *= r1;
+                    }
+                }
+                // ---- weights, and the values they go to
+                const float ref0 = safe_ref(M0), ref1 = safe_ref(M1), ret0 = safe_ref(T0) - kTop, ret1 = safe_ref(T1) - kTop;
+#pragma unroll
+                for (int y = 0; y < kSub; ++y) {
+                    float p0 = ex2(sc[y][0] - ref0), p1 = ex2(sc[y][1] - ref1);
+                    float p2 = ex2(sc[y][2] - ref0), p3 = ex2(sc[y][3] - ref1);
+                    l0 += p0 + p2;
+                    l1 += p1 + p3;
+                    if constexpr (E4M3) {
+                        auto weight = [&](float s, float p, float ev, float top) {
+                            const float z = s + (ev - top) + up;
+                            if constexpr (!BANDS) return ex2(z);
+                            lighter |= z <= kTop - kBand && z - up > kTop + kLeast && p > 0.f;
+                            return z <= kTop - kBand || (z > kTop && up > 0.f) ? 0.f : ex2(z);
+                        };
+                        p0 = weight(sc[y][0], p0, ve[y][0], ret0);
+                        p1 = weight(sc[y][1], p1, ve[y][0], ret1);
+                        p2 = weight(sc[y][2], p2, ve[y][1], ret0);
+                        p3 = weight(sc[y][3], p3, ve[y][1], ret1);
+                    }
+                    uint32_t b0, b1, c0 = 0u, c1 = 0u;  // bf16 weights in two parts
+                    if constexpr (E4M3) {
+                        b0 = transpose8(pack2<true>(p0, p1));
+                        b1 = transpose8(pack2<true>(p2, p3));
+                    } else {
+                        b0 = transpose8(top2(p0, p1));
+                        b1 = transpose8(top2(p2, p3));
+                        c0 = transpose8(pack2<false>(rest(p0), rest(p1)));
+                        c1 = transpose8(pack2<false>(rest(p2), rest(p3)));
+                    }
+                    if (row[y] != kNoRow) {
+#pragma unroll
+                        for (int w = 0; w < kVw; ++w) {
+                            if constexpr (E4M3) {
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    const uint32_t sel = z ? 0x7362 : 0x5140;
+                                    uint32_t a0, a1, a2, a3;
+                                    h2_from_e4m3(__byte_perm(vx[y][0][w], vx[y][1][w], sel), a0, a1);
+                                    h2_from_e4m3(__byte_perm(vx[y][2][w], vx[y][3][w], sel), a2, a3);
+                                    mma16816<true>(o[2 * w + z], a0, a1, a2, a3, b0, b1);
+                                }
+                            } else {
+                                const uint32_t a0 = __byte_perm(vx[y][0][w], vx[y][1][w], 0x5410);
+                                const uint32_t a1 = __byte_perm(vx[y][0][w], vx[y][1][w], 0x7632);
+                                const uint32_t a2 = __byte_perm(vx[y][2][w], vx[y][3][w], 0x5410);
+                                const uint32_t a3 = __byte_perm(vx[y][2][w], vx[y][3][w], 0x7632);
+                                mma16816<false>(o[w], a0, a1, a2, a3, c0, c1);
+                                mma16816<false>(o[w], a0, a1, a2, a3, b0, b1);
+                            }
+                        }
+                    }
+                    load_v(y, row_next[y], keys_of(i + kStep + y));
+                    row[y] = row_next[y];
+                }
+                ex = ex_next;
+            }
+            return lighter;
+        };
+        walk(std::false_type{}, 0.f);
+        if constexpr (E4M3) {
+            if (__reduce_max_sync(0xffffffffu, spread & 0xffffu) + __reduce_max_sync(0xffffffffu, spread >> 16) > 256u + kLike) {
+                volatile float kept[kMt * 4];  // in local memory
+                for (int x = 0; x < kMt * 4; ++x) kept[x] = 0.f;
+                float down = 1.f;
+                bool more = true;
+                for (float up = 0.f; more; up += kBand, down *= 0x1p-28f) {
+                    more = __any_sync(0xffffffffu, walk(std::true_type{}, up));
+#pragma unroll
+                    for (int x = 0; x < kMt * 4; ++x) kept[x] = fmaf(down, o[x / 4][x % 4], kept[x]);
+                }
+#pragma unroll
+                for (int x = 0; x < kMt * 4; ++x) o[x / 4][x % 4] = kept[x];
             }
         }
         // ---- join the warps
@@ -632,8 +692,9 @@ decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_b
             int d0;
             if constexpr (E4M3) d0 = g * (D / 8) + 2 * x;
             else d0 = ((x >> 2) * 8 + g) * 8 + 2 * (x & 3);
-            *reinterpret_cast<float2*>(&osum[warp][2 * t][d0]) = make_float2(o[x][0], o[x][2]);
-            *reinterpret_cast<float2*>(&osum[warp][2 * t + 1][d0]) = make_float2(o[x][1], o[x][3]);
+            constexpr float f = E4M3 ? 0x1p-14f : 1.f;  // 2^-kTop
+            *reinterpret_cast<float2*>(&osum[warp][2 * t][d0]) = make_float2(o[x][0] * f, o[x][2] * f);
+            *reinterpret_cast<float2*>(&osum[warp][2 * t + 1][d0]) = make_float2(o[x][1] * f, o[x][3] * f);
         }
         __syncthreads();
         const bool whole = u == useq && e == useq + su;

@@ -202,6 +202,36 @@ def test_decode_large_scores_and_sizes(dtype, kept):
     decode_close(dtype, hla.attention_decode(prm, cache, q.cuda(), i64(lens)), q, ks, vs, scale=3.0)
 
 
+@pytest.mark.parametrize("dtype,kept", [("bf16", "e4m3"), ("bf16", "same"), ("f32", "e4m3")])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,length", [(1, 5000), (64, 700), (3, 16)])
+@pytest.mark.parametrize("gap,ratio", [(0, 40), (10, 7), (13, 12), (14, 30), (20, 12), (30, 0), (0, 90)])
+def test_decode_small_weights_beside_a_large_value(dtype, kept, d, n, length, gap, ratio):
+    # in every sequence one key scores `gap` (base 2) above the others, and its value row is 2^ratio times theirs, in one
+    # column only: the other columns are the other keys', however small their share of the weights
+    lens = [length] * n
+    cache = new_cache(dtype, kept, 1, d, 64, lens)
+    t, total = TYPE[dtype][1], sum(lens)
+    k, v = torch.zeros(total, 1, d), ac.randn(5, total, 1, d).float()
+    v[..., 0] = 0.0
+    for i in range(n):
+        at = i * length + (37 * i + 3) % length
+        k[at, 0, 0] = 8.0
+        v[at] = 0.0
+        v[at, 0, 0] = 1.5 * 2.0 ** ratio
+    k, v = k.to(t), v.to(t)
+    hla.cache_write(cache, k.cuda(), v.cuda(), ac.cu(lens), i64([0] * n))
+    if kept == "e4m3":
+        k, v = (ac.quantise(x.double())[0] for x in (k, v))
+    q = torch.zeros(n, 4, d, dtype=t)
+    q[..., 0] = 1.0
+    scale = max(gap, 2.0 ** -10) * math.log(2) / 8
+    prm = hla.AttnParams(4, 1, d, dtype=TYPE[dtype][0], scale=scale)
+    got = hla.attention_decode(prm, cache, q.cuda(), i64(lens))
+    assert cache.check_error() == 0
+    decode_close(dtype, got, q, k.double().split(lens), v.double().split(lens), scale=prm.c().scale)
+
+
 @pytest.mark.parametrize("dtype,kept", [("f32", "e4m3"), ("bf16", "e4m3"), ("bf16", "same")])
 def test_what_lies_behind_the_last_key_stays_out(dtype, kept):
     # the rest of the last page holds NaN codes (E4M3) or NaN
