@@ -101,17 +101,18 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
             __syncthreads();
             {  // four keys per lane group, all on their way at once
                 constexpr int kN = kDecodeUnit / (kThreads / 8);
-                float kx[kN][E], ks[kN];
+                float kx[kN][E];
 #pragma unroll
                 for (int y = 0; y < kN; ++y) {
                     const int64_t r = rows[tid / 8 + y * (kThreads / 8)];
-                    ks[y] = 1.f;
                     if (r < 0) {
 #pragma unroll
                         for (int x = 0; x < E; ++x) kx[y][x] = 0.f;
                     } else if constexpr (E4M3) {
-                        ks[y] = exp2f((float)((int)c.k_exp[r] - 127));
+                        const float ks = exp2f((float)((int)c.k_exp[r] - 127));
                         load_e4m3<E>(static_cast<const uint8_t*>(c.k) + r * D + (tid & 7) * E, kx[y]);
+#pragma unroll
+                        for (int x = 0; x < E; ++x) kx[y][x] *= ks;
                     } else {
                         const float* src = static_cast<const float*>(c.k) + r * D + (tid & 7) * 4;
 #pragma unroll
@@ -139,7 +140,7 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
 #pragma unroll
                         for (int o = 4; o; o >>= 1) d[y] += __shfl_xor_sync(0xffffffffu, d[y], o);
                         const int j = tid / 8 + y * (kThreads / 8);
-                        if ((tid & 7) == 0) ps[g][j] = rows[j] >= 0 ? d[y] * ks[y] : -INFINITY;
+                        if ((tid & 7) == 0) ps[g][j] = rows[j] >= 0 ? d[y] : -INFINITY;
                     }
                 }
             }
@@ -555,11 +556,12 @@ decode_mma_kernel(AttnDims A, CacheDims C, PageDiv pd, hla_cache c, const __nv_b
                         ve[y][1] = (float)((int)ex_of(y, 1, 8) - 127);
                     }
                     load_k(y, row_next[y]);
+                    // (the factors' product first: a sum of 8-bit products times either may leave the range that the score does not)
                     const bool on0 = g < n, on1 = g + 8 < n;
-                    sc[y][0] = on0 ? (a0[0] + a1[0]) * f0 * qs0 : -INFINITY;
-                    sc[y][1] = on0 ? (a0[1] + a1[1]) * f0 * qs1 : -INFINITY;
-                    sc[y][2] = on1 ? (a0[2] + a1[2]) * f1 * qs0 : -INFINITY;
-                    sc[y][3] = on1 ? (a0[3] + a1[3]) * f1 * qs1 : -INFINITY;
+                    sc[y][0] = on0 ? (a0[0] + a1[0]) * (f0 * qs0) : -INFINITY;
+                    sc[y][1] = on0 ? (a0[1] + a1[1]) * (f0 * qs1) : -INFINITY;
+                    sc[y][2] = on1 ? (a0[2] + a1[2]) * (f1 * qs0) : -INFINITY;
+                    sc[y][3] = on1 ? (a0[3] + a1[3]) * (f1 * qs1) : -INFINITY;
                     h0 = fmaxf(h0, fmaxf(sc[y][0], sc[y][2]));
                     h1 = fmaxf(h1, fmaxf(sc[y][1], sc[y][3]));
                     if constexpr (E4M3) {

@@ -232,6 +232,25 @@ def test_decode_small_weights_beside_a_large_value(dtype, kept, d, n, length, ga
     decode_close(dtype, got, q, k.double().split(lens), v.double().split(lens), scale=prm.c().scale)
 
 
+@pytest.mark.parametrize("dtype,kept", [("bf16", "e4m3"), ("bf16", "same"), ("f32", "e4m3"), ("f32", "same")])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("up,down", [(125, -110), (-120, 105), (100, -100)])
+def test_decode_of_keys_and_queries_of_any_size(dtype, kept, d, up, down):
+    # keys near one end of the range and queries near the other: scores of ordinary size
+    lens = [300, 20]
+    cache = new_cache(dtype, kept, 2, d, 16, lens)
+    t, n = TYPE[dtype][1], sum(lens)
+    k = (ac.randn(1, n, 2, d).clamp(-3.5, 3.5) * 2.0 ** up).to(t)
+    v = ac.randn(2, n, 2, d).to(t)
+    hla.cache_write(cache, k.cuda(), v.cuda(), ac.cu(lens), i64([0, 0]))
+    if kept == "e4m3":
+        k, v = (ac.quantise(x.double())[0] for x in (k, v))
+    q = (ac.randn(9, 2, 8, d) * 2.0 ** down).to(t)
+    scale = 2.0 ** -(up + down) / math.sqrt(d)
+    got = hla.attention_decode(hla.AttnParams(8, 2, d, dtype=TYPE[dtype][0], scale=scale), cache, q.cuda(), i64(lens))
+    decode_close(dtype, got, q, k.double().split(lens), v.double().split(lens), scale=scale)
+
+
 @pytest.mark.parametrize("dtype,kept", [("f32", "e4m3"), ("bf16", "e4m3"), ("bf16", "same")])
 def test_what_lies_behind_the_last_key_stays_out(dtype, kept):
     # the rest of the last page holds NaN codes (E4M3) or NaN
