@@ -111,6 +111,20 @@ def test_extremes_of_the_row_size(dtype):
     assert k[5, 0, 0] == -448 * 2.0 ** -127 or dtype == "bf16"
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_row_whose_finite_values_are_all_zero(dtype, bad):
+    # kept at 2^-127: an infinity becomes the largest 8-bit float there (a normal number of either type), NaN stays
+    x = torch.zeros(1, 1, 64, dtype=TYPE[dtype][1])
+    x[0, 0, 5] = bad
+    cache = new_cache(dtype, "e4m3", 1, 64, 16, [1])
+    hla.cache_write(cache, x.cuda(), -x.cuda(), ac.cu([1]), i64([0]))
+    for got, sign in zip(hla.cache_read(cache, ac.cu([1]), i64([0]), 1), (1, -1)):
+        got = got.cpu().double()[0, 0]
+        assert (got[:5] == 0).all() and (got[6:] == 0).all()
+        assert torch.isnan(got[5]) if math.isnan(bad) else got[5] == math.copysign(448 * 2.0 ** -127, sign * bad)
+
+
 def test_rows_out_of_range_are_skipped_and_flagged():
     cache = new_cache("bf16", "e4m3", 2, 64, 16, [20, 20], extra_pages=1)
     cache.page_table[1, 1] = 1000  # a page that is not there
