@@ -214,25 +214,30 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
     const uint32_t cS = tmem, cP = tmem + 128, cV = tmem + 256, cK = cV + D;  // S / P, dP / dS, dV, dK
 
     // an item's query tiles: of each packed head group, `per` tiles from tile i0, the first that sees the block's
-    // first key; the last has `tail` rows.  Of these n, from tile r of head h's group on (parts: the item's share)
-    struct Span { int i0, per, n, tail, r, h; };
+    // first key, from its row `lead` on; the last has `tail` rows.  Of these n, from tile r of head h's group on (parts:
+    // the item's share)
+    struct Span {
+        int i0, per, n, lead, tail, r, h;
+        __device__ bool edge(int r) const { return (r == 0 && lead > 0) || (r == per - 1 && tail < kRows); }
+    };
     auto span = [&](const Item& it) {
-        const int off = it.lk - it.lq, i0 = max(0, it.first - off) >> lqb;
+        const int off = it.lk - it.lq, p0 = max(0, it.first - off), i0 = p0 >> lqb;
         const int per = __shfl_sync(0xffffffffu, max(0, ((it.lq + qb - 1) >> lqb) - i0), 0);
+        const int lead = __shfl_sync(0xffffffffu, (p0 & (qb - 1)) << lpack, 0);
         const int rest = it.lq & (qb - 1), tail = __shfl_sync(0xffffffffu, rest ? rest << lpack : kRows, 0);
-        if (parts == 1 || per == 0) return Span{i0, per, per * groups, tail, 0, it.head * A.G};
+        if (parts == 1 || per == 0) return Span{i0, per, per * groups, lead, tail, 0, it.head * A.G};
         const int part = __shfl_sync(0xffffffffu, it.part, 0);
         const int a = (int)((int64_t)per * groups * part / parts), b = (int)((int64_t)per * groups * (part + 1) / parts);
-        return Span{i0, per, b - a, tail, a % per, it.head * A.G + (a / per << lpack)};
+        return Span{i0, per, b - a, lead, tail, a % per, it.head * A.G + (a / per << lpack)};
     };
 
     if (warp >= 8) {
         give_registers();
         bool ok = true;
         if (warp == 8) {
-            // ---- loads: the ring takes Q 0, dO 0, Q 1, dO 1, ... of every item.  Of rows behind the sequence,
-            //      infinities and NaN are cleared: their probability is 0 (the ring holds at most four tiles, so four
-            //      barriers keep a tile's signal until the products have seen it)
+            // ---- loads: the ring takes Q 0, dO 0, Q 1, dO 1, ... of every item.  Of rows behind the sequence, and of
+            //      those that see no key of the block, infinities and NaN are cleared: their probability is 0 (the ring
+            //      holds at most four tiles, so four barriers keep a tile's signal until the products have seen it)
             static_assert(C::kSlots <= 8, "tiles in the ring");
             Ring ring;
             int used = 0, fixed = 0, kv_loads = 0;
@@ -270,20 +275,22 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                             }
                         }
                     }
+                    if (sp.edge(r)) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            unsigned char* tile = sm + C::kRing + use[y].slot * C::kTile;
+                            ok = ok && wait_or_flag(bar_full + 8 * use[y].slot, use[y].par, err);
+                            if (ok && r == 0) clear_nonfinite<D>(tile, 0, sp.lead, [](int) {});
+                            if (ok && r == sp.per - 1) clear_nonfinite<D>(tile, sp.tail, kRows, [](int) {});
+                        }
+                        umma::fence_async_smem();
+                        __syncwarp();
+                        if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (fixed & 3));
+                        ++fixed;
+                    }
                     if (++r == sp.per) {
                         r = 0;
                         h += 1 << lpack;
-                        if (sp.tail < kRows) {
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                ok = ok && wait_or_flag(bar_full + 8 * use[y].slot, use[y].par, err);
-                                if (ok) clear_nonfinite<D>(sm + C::kRing + use[y].slot * C::kTile, sp.tail, kRows, [](int) {});
-                            }
-                            umma::fence_async_smem();
-                            __syncwarp();
-                            if (ok && lane == 0) umma::mbar_arrive(bar_fix + 8 * (fixed & 3));
-                            ++fixed;
-                        }
                     }
                 }
             }
@@ -311,15 +318,13 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 const bool fine = __shfl_sync(0xffffffffu, it.lk, 0) <= kRows;
                 if (n == 0) continue;
                 int r = sp.r;
-                auto ready_q = [&](const Ring& q) {  // a tile's Q (of a last tile both, cleared behind the last row)
+                auto ready_q = [&](const Ring& q) {  // a tile's Q (of a first or last tile both, cleared)
                     wait(bar_full + 8 * q.slot, q.par);
-                    if (++r == sp.per) {
-                        r = 0;
-                        if (sp.tail < kRows) {
-                            wait(bar_fix + 8 * (fixed & 3), (fixed >> 2) & 1);
-                            ++fixed;
-                        }
+                    if (sp.edge(r)) {
+                        wait(bar_fix + 8 * (fixed & 3), (fixed >> 2) & 1);
+                        ++fixed;
                     }
+                    if (++r == sp.per) r = 0;
                     umma::fence_after_sync();
                 };
                 auto ready_o = [&](const Ring& o) {
@@ -443,6 +448,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 const float* st = reinterpret_cast<const float*>(sm + C::kStat + (t & 1) * 1024) + half * 64;
                 // rows from column `from` on see the key
                 const int from = max(-kRows, min(kRows, ahead - (r << lqb))) * (1 << lpack) - half * 64;
+                const bool edge = __any_sync(0xffffffffu, from > 0);
                 if (++r == per) r = 0;
                 named_sync(kBarS, 288);
                 umma::fence_after_sync();
@@ -456,7 +462,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     p[e] = make_float2(ex2(a.x), ex2(a.y));
                     p[e + 1] = make_float2(ex2(b.x), ex2(b.y));
                 }
-                if (__any_sync(0xffffffffu, from > 0)) {
+                if (edge) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         p[e].x = 2 * e >= from ? p[e].x : 0.f;
@@ -474,6 +480,13 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                     const float4 nd = *reinterpret_cast<const float4*>(st + 128 + 2 * e);
                     d[e] = fmul2(p[e], fadd2(d[e], make_float2(nd.x, nd.y)));
                     d[e + 1] = fmul2(p[e + 1], fadd2(d[e + 1], make_float2(nd.z, nd.w)));
+                }
+                if (edge) {  // (0 times a dP that overflowed is no 0)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        d[e].x = 2 * e >= from ? d[e].x : 0.f;
+                        d[e].y = 2 * e + 1 >= from ? d[e].y : 0.f;
+                    }
                 }
                 store64(tP, d, fine);
                 named_arrive(kBarDs, 288);

@@ -429,6 +429,60 @@ def test_infinite_and_nan_values_reach_the_rows_that_see_them_in_parts():
     assert ((got - want).abs()[fine] <= tol[fine]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 1, 1), (128, 3, 1), (64, 4, 1), (128, 16, 1)])
+@pytest.mark.parametrize("lq,lk,row", [(256, 257, 0), (300, 301, 130), (200, 391, 77), (200, 391, 7), (500, 430, 127), (300, 300, 40),
+                                       (900, 1000, 33)])
+def test_non_finite_rows_reach_no_further_than_the_keys_beside_theirs(dtype, d, hq, hkv, lq, lk, row):
+    # infinities and NaN in one row's dout and q: dk and dv of the keys from 128 after the last one that it sees (fp32: from
+    # the next one) are those of the other rows
+    x = make(dtype, d, hq, hkv, [lq], [lk], seed=lq)
+    clean = {n: t.clone() for n, t in x.items()}
+    clean["q"][row], clean["dout"][row] = 0.0, 0.0  # adds nothing to dk and dv of keys that it does not see
+    x["dout"][row], x["q"][row] = math.inf, math.nan
+    out, lse, grads = run(params(dtype, d, hq, hkv), x, [lq], [lk])
+    ref = ac.attention(clean["q"], clean["k"], clean["v"], [lq], [lk], dout=clean["dout"])
+    first = min(lk, max(0, row + lk - lq + 1) + (0 if dtype == "f32" else 127))
+    keep, rows = torch.arange(first, lk), torch.cat([torch.arange(row), torch.arange(row + 1, lq)])
+    y = {n: clean[n] for n in clean}
+    for part in (2, 3):
+        for n in "kv":
+            ref[part][n] = ref[part][n][keep]
+        ref[part]["q"] = ref[part]["q"][rows]
+    r_out, r_lse = ref[0][rows], ref[1][rows]
+    ref[3]["out"] = ref[3]["out"][rows]
+    u, L = ac.EPS[TYPE[dtype][1]] / 2, max(lk, lq * hq // hkv)
+    S = float(y["q"].double().norm(dim=-1).max() * y["k"].double().norm(dim=-1).max()) / math.sqrt(d)
+    fp, half = (2 * d * S + L + 32) * U32, 0.0 if dtype == "f32" else u  # as in the head of test_gpu_attention.py
+    got = {"out": out.cpu()[rows], "q": grads["q"].cpu()[rows], "k": grads["k"].cpu()[keep], "v": grads["v"].cpu()[keep]}
+    want = {"out": r_out, **ref[2]}
+    for name, g in got.items():
+        tol = ((3 if name in "qk" else 1) * half + 3 * fp) * ref[3][name] + 1.01 * u * want[name].abs()
+        assert ((g.double() - want[name]).abs() <= tol).all(), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 2, 1), (128, 3, 3)])
+def test_a_large_dout_reaches_the_keys_that_its_row_sees(dtype, d, hq, hkv):
+    # one row's dout and q are so large that their products overflow: dk and dv of the keys behind it are the other rows'
+    n, row = 300, 140
+    x = make(dtype, d, hq, hkv, [n], [n], seed=3)
+    clean = {m: t.clone() for m, t in x.items()}
+    clean["q"][row], clean["dout"][row] = 0.0, 0.0
+    big = torch.finfo(TYPE[dtype][1]).max
+    for m in ("q", "dout"):
+        x[m][row] = torch.where(ac.randn(9, *x[m][row].shape) < 0, -big, big).to(x[m].dtype)
+    _, _, grads = run(params(dtype, d, hq, hkv), x, [n], [n])
+    ref = ac.attention(clean["q"], clean["k"], clean["v"], [n], [n], dout=clean["dout"])
+    u = ac.EPS[TYPE[dtype][1]] / 2
+    S = float(clean["q"].double().norm(dim=-1).max() * clean["k"].double().norm(dim=-1).max()) / math.sqrt(d)
+    fp, half = (2 * d * S + n * hq // hkv + 32) * U32, 0.0 if dtype == "f32" else u
+    for name in "kv":
+        want, mag = ref[2][name][row + 1:], ref[3][name][row + 1:]
+        tol = ((3 if name == "k" else 1) * half + 3 * fp) * mag + 1.01 * u * want.abs()
+        assert ((grads[name].cpu().double()[row + 1:] - want).abs() <= tol).all(), name
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 def test_slices_of_a_fused_projection(dtype, d):
     hq, hkv, lens = 4, 2, [100, 45]
