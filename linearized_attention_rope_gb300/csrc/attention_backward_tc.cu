@@ -430,6 +430,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
         for (int x = 0;; ++x) {
             int n, per, r;  // tiles; tiles per head group; the first one's place in it
             int ahead;      // first row that sees the key, from the group's first tile's start
+            int tail;       // rows of the last tile
             int64_t at;     // the key's place in the results, or among the parts' (-1: none)
             bool fine;
             {
@@ -440,15 +441,18 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 n = sp.n;
                 fine = it.lk <= kRows;
                 per = sp.per;
+                tail = sp.tail;
                 r = sp.r;
                 ahead = key - (it.lk - it.lq) - (sp.i0 << lqb);
                 at = key < it.lk ? (it.part * A.total_k + it.k0 + key) * A.Hkv + it.head : -1;
             }
             for (int i = 0; i < n; ++i, ++t) {
                 const float* st = reinterpret_cast<const float*>(sm + C::kStat + (t & 1) * 1024) + half * 64;
-                // rows from column `from` on see the key
+                // rows from column `from` up to `to` see the key
                 const int from = max(-kRows, min(kRows, ahead - (r << lqb))) * (1 << lpack) - half * 64;
-                const bool edge = __any_sync(0xffffffffu, from > 0);
+                const int to = (r == per - 1 ? tail : kRows) - half * 64;
+                const uint32_t seen = max(0, to - from);
+                const bool edge = __any_sync(0xffffffffu, from > 0 || to < 64);
                 if (++r == per) r = 0;
                 named_sync(kBarS, 288);
                 umma::fence_after_sync();
@@ -465,8 +469,8 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 if (edge) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        p[e].x = 2 * e >= from ? p[e].x : 0.f;
-                        p[e].y = 2 * e + 1 >= from ? p[e].y : 0.f;
+                        p[e].x = (uint32_t)(2 * e - from) < seen ? p[e].x : 0.f;
+                        p[e].y = (uint32_t)(2 * e + 1 - from) < seen ? p[e].y : 0.f;
                     }
                 }
                 store64(tS, p, fine);
@@ -484,8 +488,8 @@ attn_dkdv_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ 
                 if (edge) {  // (0 times a dP that overflowed is no 0)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        d[e].x = 2 * e >= from ? d[e].x : 0.f;
-                        d[e].y = 2 * e + 1 >= from ? d[e].y : 0.f;
+                        d[e].x = (uint32_t)(2 * e - from) < seen ? d[e].x : 0.f;
+                        d[e].y = (uint32_t)(2 * e + 1 - from) < seen ? d[e].y : 0.f;
                     }
                 }
                 store64(tP, d, fine);

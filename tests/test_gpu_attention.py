@@ -483,6 +483,23 @@ def test_a_large_dout_reaches_the_keys_that_its_row_sees(dtype, d, hq, hkv):
         assert ((grads[name].cpu().double()[row + 1:] - want).abs() <= tol).all(), name
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 2, 1), (128, 3, 3), (64, 8, 1)])
+def test_finite_rows_of_any_size_stay_out(dtype, d, hq, hkv):
+    # the padding and the sequence in between hold the type's largest values, whose products overflow
+    lens = [50, 90, 141]
+    x = make(dtype, d, hq, hkv, lens, lens, pad_q=30, pad_k=41)
+    big = torch.finfo(TYPE[dtype][1]).max
+    for n in x:
+        sign = torch.where(ac.randn(9, *x[n].shape) < 0, -big, big).to(x[n].dtype)
+        x[n][50:140], x[n][281:] = sign[50:140], sign[281:]
+    out, lse, grads = run(params(dtype, d, hq, hkv), x, lens, lens)
+    for a, b in ((0, 50), (140, 281)):
+        y = {n: t[a:b] for n, t in x.items()}
+        ref = ac.attention(y["q"], y["k"], y["v"], [b - a], [b - a], dout=y["dout"])
+        check(dtype, d, y, ref, out[a:b], lse[a:b], {n: t[a:b] for n, t in grads.items()}, [b - a], [b - a])
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 def test_slices_of_a_fused_projection(dtype, d):
     hq, hkv, lens = 4, 2, [100, 45]
