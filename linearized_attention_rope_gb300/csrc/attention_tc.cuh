@@ -18,7 +18,7 @@ namespace hla {
 namespace attn_tc {
 
 constexpr int kRows = 128;  // rows of a query tile, keys of a key tile
-constexpr uint32_t kWaitLimit = 1u << 22, kItemSeconds = 60;  // polls per second allowed
+constexpr uint32_t kWaitLimit = 1u << 22;  // polls per second allowed
 
 // Registers of a block of three warpgroups: 168 a thread at launch; the third
 // (loads and products) gives 112 a thread up, the softmax warpgroups take 56
@@ -63,17 +63,27 @@ __device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Waits with a bound (polls, and two seconds); a wait that runs out is recorded and ends the caller's role.
-// Inlined: a function call would not leave its caller the registers of setmaxnreg.
-// The waits for the next item, which last as long as the items before it, get a minute.
-__device__ __forceinline__ bool wait_or_flag(uint32_t mbar, uint32_t parity, int32_t* err, uint32_t seconds = 2) {
+// Waits with a bound (polls, and two seconds); a wait that runs out is recorded, and the caller's role goes on without
+// waiting.  The last poll comes after the time has been found to be up, so that a lane sees what the others of its warp
+// saw before (a vote per wait: 4096 tokens with gradient 457 -> 469 us).  Inlined: a function call would not leave its
+// caller the registers of setmaxnreg.
+__device__ __forceinline__ bool wait_or_flag(uint32_t mbar, uint32_t parity, int32_t* err) {
     if (umma::mbar_try_wait(mbar, parity)) return true;
     const uint64_t t0 = umma::global_ns();
 #pragma unroll 1
-    for (uint32_t i = 0; i < kWaitLimit * seconds; ++i) {
+    for (uint32_t i = 0; i < kWaitLimit * 2; ++i) {
         if (umma::mbar_try_wait(mbar, parity)) return true;
-        if (umma::global_ns() - t0 > 1000000000ull * seconds) break;
+        if (umma::global_ns() - t0 > 2000000000ull) break;
     }
+    if (umma::mbar_try_wait(mbar, parity)) return true;
+    atomicExch(err, kErrTimeout);
+    return false;
+}
+// A full warp's wait with a bound on the polls alone: time in which the whole block stands still does not count.
+__device__ __forceinline__ bool wait_polls(uint32_t mbar, uint32_t parity, int32_t* err, uint32_t polls) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < polls; ++i)
+        if (__all_sync(0xffffffffu, umma::mbar_try_wait(mbar, parity))) return true;
     atomicExch(err, kErrTimeout);
     return false;
 }
@@ -81,8 +91,10 @@ __device__ __forceinline__ bool wait_or_flag(uint32_t mbar, uint32_t parity, int
 // Hardware barriers 1 .. 15 among some of the block's warps: `sync` waits,
 // `arrive` does not.  A warp that waits this way takes no issue slots, where
 // one that polls an mbarrier slows the warps beside it.  They cannot time out,
-// so whoever arrives does so in every round, whatever has happened; only
-// mbarrier waits, which are bounded, can fail.
+// so whoever arrives does so in every round of every item that is handed out,
+// whatever has happened: only mbarrier waits, which are bounded, can fail, and a
+// role whose wait failed goes on without waiting.  All roles must then see the
+// same items (below).
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -101,6 +113,12 @@ __device__ __forceinline__ void named_arrive(int id, int threads) {
 // start while the last products and results of this one are under way.
 // The next item is asked for when the loads of this one come to an end, not
 // before: items claimed early would be kept from blocks that are free sooner.
+//
+// A role that gave up waiting for an item which the others then get would leave
+// them at a hardware barrier for ever.  So the roles wait longer than the
+// scheduling warp can take to hand out an item or the end, all its own waits run out;
+// and where it finds that a role has not taken the item before last, it hands out nothing
+// more, so that no role does.
 
 struct Item {
     int q0, k0;  // first query and key row of the sequence (of the item's part of the keys)
@@ -112,6 +130,10 @@ struct Item {
 };
 constexpr int kItems = 2;       // entries of the ring
 constexpr int kItemWarps = 11;  // warps that read them
+constexpr uint32_t kItemPolls = 60 * kWaitLimit;    // of a wait of the scheduling warp: as long as an item may take
+constexpr uint32_t kReaderPolls = 6 * kItemPolls;   // of a wait for an item
+// at half the scheduling warp's rate: its waits for a free entry, for a request, and for the request's answer
+static_assert(kReaderPolls / 2 > 2 * kItemPolls + 2 * kWaitLimit, "roles wait longer than the scheduling warp");
 struct ItemRing {
     int4 word[kItems][2];
     uint4 answer;  // of a request for the next item
@@ -157,7 +179,7 @@ __device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t*
         if (x >= 0) B = attn_find_block(A, cu_q, cu_k, rows, x / parts / heads, by_key);
         const int s = i % kItems;
         more = B.found;
-        if (i >= kItems && !wait_or_flag(bar_empty + 8 * s, ((i / kItems) - 1) & 1, err, kItemSeconds)) more = false;
+        if (i >= kItems && !wait_polls(bar_empty + 8 * s, ((i / kItems) - 1) & 1, err, kItemPolls)) break;
         int k0 = (int)B.k0, lk = B.lk, off = B.lk - B.lq;
         if (parts > 1 && !by_key) {
             const int end = max(0, min(B.lk, min(B.first + rows, B.lq) + off)), n = (end + kRows - 1) / kRows;
@@ -175,9 +197,9 @@ __device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t*
         if (lane == 0) umma::mbar_arrive(bar_full + 8 * s);
         if (!more) break;
         x = -1;
-        if (wait_or_flag(bar_want, i & 1, err, kItemSeconds)) {
+        if (wait_polls(bar_want, i & 1, err, kItemPolls)) {
             if (lane == 0) ask_item(answer, bar_ask);
-            if (wait_or_flag(bar_ask, i & 1, err)) x = taken_item(answer);
+            if (__any_sync(0xffffffffu, wait_or_flag(bar_ask, i & 1, err))) x = taken_item(answer);
             __syncwarp();
             umma::fence_async_smem();
         }
@@ -189,7 +211,7 @@ __device__ __forceinline__ Item next_item(const ItemRing* ring, int i, uint32_t 
                                           int32_t* err) {
     const int s = i % kItems;
     Item it = {0, 0, 0, 0, 0, -1, 0, 0};
-    if (wait_or_flag(bar_full + 8 * s, (i / kItems) & 1, err, kItemSeconds)) {
+    if (wait_polls(bar_full + 8 * s, (i / kItems) & 1, err, kReaderPolls)) {
         const int4 a = ring->word[s][0], b = ring->word[s][1];
         it = Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     }
