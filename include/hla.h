@@ -447,12 +447,17 @@ typedef struct hla_attn_params {
     int64_t v_stride;
 } hla_attn_params;
 
-/* Workspace bytes of hla_attention (more than the error word for few rows over
- * many keys, whose parts are joined), or (backward != 0) of
- * hla_attention_backward; a workspace serves any call it is large enough for.
- * Its first 16 bytes are the error word: zero them before the first use; calls
- * only ever set it, hla_check_workspace_error reads and clears it.  Two calls
- * that may run at the same time need a workspace each. */
+/* Workspace bytes of hla_attention, or (backward != 0) of
+ * hla_attention_backward: for few rows over many keys, and for few heads, more
+ * than for large calls, since such work is cut into parts whose results lie in
+ * the workspace.  With less than that, a call takes as many parts as there is
+ * room for (slower; the bits of a result depend on the number of parts); the
+ * least is 256 bytes, and for the gradient what one part needs, which grows
+ * with total_q and total_k: the workspace of the largest call serves every smaller one.
+ * Below that a call returns HLA_ERR_WORKSPACE.  The first 16 bytes are the error
+ * word: zero them before the first use; calls only ever set it,
+ * hla_check_workspace_error reads and clears it.  Two calls that may run at the
+ * same time need a workspace each. */
 HLA_API int hla_attention_workspace_bytes(const hla_attn_params* params, int64_t total_q, int64_t total_k,
                                           int n_seqs, int backward, size_t* bytes);
 
@@ -472,7 +477,7 @@ HLA_API int hla_attention_workspace_bytes(const hla_attn_params* params, int64_t
  * table is clamped on the device (no access out of range) and flagged in the
  * workspace's error word.  Outputs must not overlap inputs.  bf16 layers run on
  * the tensor cores: fp32 scores and sums, probabilities rounded to bf16 for
- * their product with v.  Asynchronous; deterministic. */
+ * their product with v.  Asynchronous; deterministic (for a workspace size). */
 HLA_API int hla_attention(const hla_attn_params* params, const void* q, const void* k, const void* v,
                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int n_seqs, int64_t total_q,
                           int64_t total_k, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);

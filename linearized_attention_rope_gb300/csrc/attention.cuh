@@ -167,17 +167,24 @@ attention_join_kernel(AttnDims A, const int32_t* __restrict__ cu_q, int parts, c
     if (lane == 0) lse[r] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
-// fp32 layers (attention_f32.cu), the bytes of partial results (0: one part), and those their gradient needs: dout . out per row and head, (several query
-// heads per kv head) dk and dv of each query head, and dq of each part.
+// The most parts, up to `most`, whose results fit into `room` bytes; bytes(parts), 0 for one.
+template <class Bytes> int parts_within(int most, size_t room, Bytes bytes) {
+    while (most > 1 && bytes(most) > room) --most;
+    return most;
+}
+
+// fp32 layers (attention_f32.cu).  The bytes of partial results of as many parts as suit the sizes (0: one part; `room`
+// bytes are there, and as many parts are taken as they hold), and the floats that the gradient needs: dout . out per row and head, (several
+// query heads per kv head) dk and dv of each query head, and (parts) dq of each part.
 cudaError_t launch_attention_f32(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
-                                 const int32_t* cu_k, float* out, float* lse, float* part_ws, int32_t* err,
+                                 const int32_t* cu_k, float* out, float* lse, float* part_ws, size_t room, int32_t* err,
                                  cudaStream_t st);
 size_t attention_f32_part_bytes(const AttnDims& A);
-size_t attention_backward_f32_floats(const AttnDims& A);
+size_t attention_backward_f32_floats(const AttnDims& A, bool parts);
 cudaError_t launch_attention_backward_f32(const AttnDims& A, const float* q, const float* k, const float* v,
                                           const float* out, const float* lse, const float* dout, const int32_t* cu_q,
-                                          const int32_t* cu_k, float* dq, float* dk, float* dv, float* ws, int32_t* err,
-                                          cudaStream_t st);
+                                          const int32_t* cu_k, float* dq, float* dk, float* dv, float* ws, size_t room,
+                                          int32_t* err, cudaStream_t st);
 // What is left without keys, or without queries: rows of the sequences to zero (x, and y if given), lse to -infinity;
 // the other side's rows and table are checked only.
 template <typename T>

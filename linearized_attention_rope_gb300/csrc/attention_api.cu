@@ -136,14 +136,13 @@ AttnDims attn_dims(const hla_attn_params* p, int n_seqs, int64_t total_q, int64_
 
 constexpr size_t kWsHead = 256;  // the error word
 
-size_t attn_ws_bytes(const hla_attn_params* p, int64_t total_q, int64_t total_k, int n_seqs, bool backward) {
-    size_t n = kWsHead;
-    if (!backward && p->dtype == HLA_DTYPE_BF16) n += attention_tc_part_bytes(attn_dims(p, n_seqs, total_q, total_k));
-    if (!backward && p->dtype == HLA_DTYPE_F32) n += attention_f32_part_bytes(attn_dims(p, n_seqs, total_q, total_k));
-    if (backward && p->dtype == HLA_DTYPE_BF16) n += attention_backward_tc_bytes(attn_dims(p, n_seqs, total_q, total_k));
-    if (backward && p->dtype == HLA_DTYPE_F32)
-        n += attention_backward_f32_floats(attn_dims(p, n_seqs, total_q, total_k)) * sizeof(float);
-    return n;
+// parts: with the results of as many parts as suit the sizes, else of one, which is the least that a call needs.
+size_t attn_ws_bytes(const hla_attn_params* p, int64_t total_q, int64_t total_k, int n_seqs, bool backward, bool parts) {
+    const AttnDims A = attn_dims(p, n_seqs, total_q, total_k);
+    const bool f32 = p->dtype == HLA_DTYPE_F32;
+    if (backward)
+        return kWsHead + (f32 ? attention_backward_f32_floats(A, parts) * sizeof(float) : attention_backward_tc_bytes(A, parts));
+    return kWsHead + (!parts ? 0 : f32 ? attention_f32_part_bytes(A) : attention_tc_part_bytes(A));
 }
 
 bool sizes_ok(int n_seqs, int64_t total_q, int64_t total_k) {
@@ -223,7 +222,7 @@ HLA_API int hla_attention_workspace_bytes(const hla_attn_params* p, int64_t tota
     const int rc = check_attn(p);
     if (rc) return rc;
     if (!sizes_ok(n_seqs, total_q, total_k) || !bytes) return HLA_ERR_INVALID_ARG;
-    *bytes = attn_ws_bytes(p, total_q, total_k, n_seqs, backward != 0);
+    *bytes = attn_ws_bytes(p, total_q, total_k, n_seqs, backward != 0, true);
     return HLA_OK;
 }
 
@@ -236,7 +235,7 @@ HLA_API int hla_attention(const hla_attn_params* p, const void* q, const void* k
     if (cu_k ? !aligned16(cu_k) : total_k != total_q) return HLA_ERR_INVALID_ARG;
     if (total_q > 0 && (!good(q) || !good(out) || !good(lse))) return HLA_ERR_INVALID_ARG;
     if (total_k > 0 && (!good(k) || !good(v))) return HLA_ERR_INVALID_ARG;
-    if (ws_bytes < attn_ws_bytes(p, total_q, total_k, n_seqs, false)) return HLA_ERR_WORKSPACE;
+    if (ws_bytes < attn_ws_bytes(p, total_q, total_k, n_seqs, false, false)) return HLA_ERR_WORKSPACE;
     if (total_q == 0) return HLA_OK;
     if (!cu_k) cu_k = cu_q;
     const AttnDims A = attn_dims(p, n_seqs, total_q, total_k);
@@ -252,9 +251,10 @@ HLA_API int hla_attention(const hla_attn_params* p, const void* q, const void* k
     if (f32)
         return status(launch_attention_f32(A, static_cast<const float*>(q), static_cast<const float*>(k),
                                            static_cast<const float*>(v), cu_q, cu_k, static_cast<float*>(out), lse,
-                                           reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHead), err, st));
+                                           reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHead), ws_bytes - kWsHead, err, st));
     return status(launch_attention_tc(A, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
-                                      cu_q, cu_k, static_cast<bf*>(out), lse, static_cast<char*>(ws) + kWsHead, err, st));
+                                      cu_q, cu_k, static_cast<bf*>(out), lse, static_cast<char*>(ws) + kWsHead, ws_bytes - kWsHead, err,
+                                      st));
 }
 
 HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, const void* k, const void* v,
@@ -271,7 +271,7 @@ HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, cons
     const void* keys[] = {k, v, dk, dv};
     for (const void* x : keys)
         if (total_k > 0 && !good(x)) return HLA_ERR_INVALID_ARG;
-    if (ws_bytes < attn_ws_bytes(p, total_q, total_k, n_seqs, true)) return HLA_ERR_WORKSPACE;
+    if (ws_bytes < attn_ws_bytes(p, total_q, total_k, n_seqs, true, false)) return HLA_ERR_WORKSPACE;
     if (total_q == 0 && total_k == 0) return HLA_OK;
     if (!cu_k) cu_k = cu_q;
     const AttnDims A = attn_dims(p, n_seqs, total_q, total_k);
@@ -295,11 +295,11 @@ HLA_API int hla_attention_backward(const hla_attn_params* p, const void* q, cons
         return status(launch_attention_backward_f32(
             A, static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
             static_cast<const float*>(out), lse, static_cast<const float*>(dout), cu_q, cu_k, static_cast<float*>(dq),
-            static_cast<float*>(dk), static_cast<float*>(dv), static_cast<float*>(rows_ws), err, st));
+            static_cast<float*>(dk), static_cast<float*>(dv), static_cast<float*>(rows_ws), ws_bytes - kWsHead, err, st));
     return status(launch_attention_backward_tc(
         A, static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v), static_cast<const bf*>(out),
         lse, static_cast<const bf*>(dout), cu_q, cu_k, static_cast<bf*>(dq), static_cast<bf*>(dk), static_cast<bf*>(dv),
-        rows_ws, err, st));
+        rows_ws, ws_bytes - kWsHead, err, st));
 }
 
 HLA_API int hla_cache_bytes(const hla_cache_params* p, size_t* rows, size_t* exponents) {

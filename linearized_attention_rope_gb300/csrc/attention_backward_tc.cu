@@ -918,12 +918,15 @@ int key_parts(const AttnDims& A) {
     return best;
 }
 size_t stat_bytes(const AttnDims& A) { return ((size_t)A.total_q * A.Hq * sizeof(float2) + 255) / 256 * 256; }
+size_t bytes_of(const AttnDims& A, int64_t parts) {
+    return stat_bytes(A) + (parts > 1 ? (size_t)(2 * parts * A.total_k * A.Hkv * A.d) * sizeof(float) : 0);
+}
 
 template <int D>
 cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
                    const __nv_bfloat16* out, const float* lse, const __nv_bfloat16* dout, const int32_t* cu_q,
-                   const int32_t* cu_k, __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, int32_t* err,
-                   cudaStream_t st) {
+                   const int32_t* cu_k, __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, size_t room,
+                   int32_t* err, cudaStream_t st) {
     static DeviceCache c1, c2;
     cudaError_t e = device_cached(c1, nullptr, [](int, int*) { return prepare_kernel(attn_dkdv_tc_kernel<D>, Cfg<D>::kSmem); });
     if (e == cudaSuccess)
@@ -939,7 +942,7 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
         !tma::make_map_3d_strided(&mk, k, true, D, Hkv, A.total_k, (uint64_t)A.sk * 2, 64, 1, kRows) ||
         !tma::make_map_3d_strided(&mv, v, true, D, Hkv, A.total_k, (uint64_t)A.sv * 2, 64, 1, kRows))
         return cudaErrorInvalidValue;
-    const int parts = key_parts(A);
+    const int parts = parts_within(key_parts(A), room, [&](int p) { return bytes_of(A, p); });
     float2* stats = static_cast<float2*>(ws);
     float *part_dk = reinterpret_cast<float*>(static_cast<char*>(ws) + stat_bytes(A)),
           *part_dv = part_dk + parts * A.total_k * A.Hkv * D;
@@ -961,17 +964,14 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
 
 }  // namespace
 
-size_t attention_backward_tc_bytes(const AttnDims& A) {
-    const int64_t parts = key_parts(A);
-    return stat_bytes(A) + (parts > 1 ? (size_t)(2 * parts * A.total_k * A.Hkv * A.d) * sizeof(float) : 0);
-}
+size_t attention_backward_tc_bytes(const AttnDims& A, bool parts) { return bytes_of(A, parts ? key_parts(A) : 1); }
 cudaError_t launch_attention_backward_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                          const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
                                          const __nv_bfloat16* dout, const int32_t* cu_q, const int32_t* cu_k,
-                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, int32_t* err,
-                                         cudaStream_t st) {
-    return A.d == 128 ? launch<128>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, err, st)
-                      : launch<64>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, err, st);
+                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, size_t room,
+                                         int32_t* err, cudaStream_t st) {
+    return A.d == 128 ? launch<128>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, room, err, st)
+                      : launch<64>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, room, err, st);
 }
 
 }  // namespace hla

@@ -570,6 +570,15 @@ int row_parts(const AttnDims& A) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(32, A.total_k / (kPartTiles * kB)));
 }
 
+size_t part_bytes(const AttnDims& A, int64_t parts) {  // of the forward pass
+    const int64_t rows = A.total_q * A.Hq;
+    return parts > 1 ? (size_t)((parts * rows + 3) / 4 * 4 + parts * rows * A.d) * sizeof(float) : 0;
+}
+size_t backward_floats(const AttnDims& A, int64_t parts) {
+    const int64_t rows = A.total_q * A.Hq;
+    return (size_t)((rows + 63) / 64 * 64 + (A.G > 1 ? 2 * A.total_k * A.Hq * A.d : 0) + (parts > 1 ? parts * rows * A.d : 0));
+}
+
 template <int D, int BM, int W, int ST>
 cudaError_t rows_forward(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
                          const int32_t* cu_k, float* out, float* lse, int parts, int32_t* err, cudaStream_t st) {
@@ -584,8 +593,10 @@ cudaError_t rows_forward(const AttnDims& A, const float* q, const float* k, cons
 
 template <int D>
 cudaError_t forward(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
-                    const int32_t* cu_k, float* out, float* lse, float* part_ws, int32_t* err, cudaStream_t st) {
-    const int qb = block_rows(A.total_q, A.n_seqs, A.Hq, 76), parts = row_parts(A);
+                    const int32_t* cu_k, float* out, float* lse, float* part_ws, size_t room, int32_t* err,
+                    cudaStream_t st) {
+    const int qb = block_rows(A.total_q, A.n_seqs, A.Hq, 76);
+    const int parts = parts_within(row_parts(A), room, [&](int p) { return part_bytes(A, p); });
     const int64_t rows = A.total_q * A.Hq;
     float *part_lse = part_ws, *part_o = part_ws + (parts * rows + 3) / 4 * 4;
     const cudaError_t e = (qb == 64   ? rows_forward<D, 64, 1, 2>
@@ -635,8 +646,9 @@ cudaError_t rows_backward(const AttnDims& A, const float* q, const float* k, con
 template <int D>
 cudaError_t backward(const AttnDims& A, const float* q, const float* k, const float* v, const float* out,
                      const float* lse, const float* dout, const int32_t* cu_q, const int32_t* cu_k, float* dq, float* dk,
-                     float* dv, float* ws, int32_t* err, cudaStream_t st) {
+                     float* dv, float* ws, size_t room, int32_t* err, cudaStream_t st) {
     const int64_t rows = A.total_q * A.Hq;
+    const int cut = parts_within(row_parts(A), room, [&](int p) { return backward_floats(A, p) * sizeof(float); });
     float *delta = ws, *parts = ws + (rows + 63) / 64 * 64;
     float* dq_part = parts + (A.G > 1 ? 2 * A.total_k * A.Hq * D : 0);
     const int kb = block_rows(A.total_k, A.n_seqs, A.Hq, 152), qb = block_rows(A.total_q, A.n_seqs, A.Hq, 152);
@@ -651,7 +663,7 @@ cudaError_t backward(const AttnDims& A, const float* q, const float* k, const fl
     return (qb == 64   ? rows_backward<D, 64, 1, D == 64 ? 2 : 1>
             : qb == 32 ? rows_backward<D, 32, kSmallGroups<D>, 1>
                        : rows_backward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, dq_part,
-                                                                  row_parts(A), st);
+                                                                  cut, st);
 }
 
 // Rows of the sequences set to zero (and lse to -infinity): what attention and its gradient are without keys or queries.
@@ -678,24 +690,18 @@ attn_empty_kernel(int64_t total, int64_t other, int n_seqs, const int32_t* __res
 }  // namespace
 
 cudaError_t launch_attention_f32(const AttnDims& A, const float* q, const float* k, const float* v, const int32_t* cu_q,
-                                 const int32_t* cu_k, float* out, float* lse, float* part_ws, int32_t* err,
+                                 const int32_t* cu_k, float* out, float* lse, float* part_ws, size_t room, int32_t* err,
                                  cudaStream_t st) {
-    return (A.d == 128 ? forward<128> : forward<64>)(A, q, k, v, cu_q, cu_k, out, lse, part_ws, err, st);
+    return (A.d == 128 ? forward<128> : forward<64>)(A, q, k, v, cu_q, cu_k, out, lse, part_ws, room, err, st);
 }
-size_t attention_f32_part_bytes(const AttnDims& A) {
-    const int64_t parts = row_parts(A), rows = A.total_q * A.Hq;
-    return parts > 1 ? (size_t)((parts * rows + 3) / 4 * 4 + parts * rows * A.d) * sizeof(float) : 0;
-}
-size_t attention_backward_f32_floats(const AttnDims& A) {
-    const int64_t rows = A.total_q * A.Hq, parts = row_parts(A);
-    return (size_t)((rows + 63) / 64 * 64 + (A.G > 1 ? 2 * A.total_k * A.Hq * A.d : 0) + (parts > 1 ? parts * rows * A.d : 0));
-}
+size_t attention_f32_part_bytes(const AttnDims& A) { return part_bytes(A, row_parts(A)); }
+size_t attention_backward_f32_floats(const AttnDims& A, bool parts) { return backward_floats(A, parts ? row_parts(A) : 1); }
 cudaError_t launch_attention_backward_f32(const AttnDims& A, const float* q, const float* k, const float* v,
                                           const float* out, const float* lse, const float* dout, const int32_t* cu_q,
-                                          const int32_t* cu_k, float* dq, float* dk, float* dv, float* ws, int32_t* err,
-                                          cudaStream_t st) {
-    return A.d == 128 ? backward<128>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, err, st)
-                      : backward<64>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, err, st);
+                                          const int32_t* cu_k, float* dq, float* dk, float* dv, float* ws, size_t room,
+                                          int32_t* err, cudaStream_t st) {
+    return A.d == 128 ? backward<128>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, room, err, st)
+                      : backward<64>(A, q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, ws, room, err, st);
 }
 
 template <typename T>

@@ -501,40 +501,6 @@ int64_t items_about(const AttnDims& A) {
     return std::max<int64_t>(A.n_seqs, (A.total_q + rows - 1) / rows) * (A.Hq / pack);
 }
 
-template <int D>
-cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                   const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out, float* lse, void* part_ws, int32_t* err,
-                   cudaStream_t st) {
-    static DeviceCache cache;
-    cudaError_t e = device_cached(cache, nullptr, [](int, int*) {
-        return prepare_kernel(attention_tc_kernel<D>, Cfg<D>::kSmem);
-    });
-    if (e != cudaSuccess) return e;
-    const int pack = pack_of(A.G), qb = kRows / pack;
-    int lpack = 0;
-    while ((1 << lpack) < pack) ++lpack;
-    CUtensorMap mq, mk, mv;
-    if (!tma::make_map_3d_strided(&mq, q, true, D, (uint64_t)A.Hq, (uint64_t)A.total_q, (uint64_t)A.sq * 2, 64,
-                                  (uint32_t)pack, (uint32_t)qb) ||
-        !tma::make_map_3d_strided(&mk, k, true, D, (uint64_t)A.Hkv, (uint64_t)A.total_k, (uint64_t)A.sk * 2, 64, 1,
-                                  kRows) ||
-        !tma::make_map_3d_strided(&mv, v, true, D, (uint64_t)A.Hkv, (uint64_t)A.total_k, (uint64_t)A.sv * 2, 64, 1,
-                                  kRows))
-        return cudaErrorInvalidValue;
-    const int parts = attention_tc_parts(A);
-    const int64_t blocks = items_bound(A) * parts, rows = A.total_q * A.Hq;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    float* part_lse = static_cast<float*>(part_ws);
-    float* part_o = part_lse + (parts * rows + 3) / 4 * 4;
-    attention_tc_kernel<D><<<(unsigned)blocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mk, mv, v, cu_q, cu_k, lpack, parts, out,
-                                                                             lse, part_o, part_lse, err);
-    if (parts > 1)
-        attention_join_kernel<D, __nv_bfloat16><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(A, cu_q, parts, part_o, part_lse, out, lse);
-    return cudaGetLastError();
-}
-
-}  // namespace
-
 // Items that do not fill the SMs leave some idle.  With keys enough for parts of
 // eight tiles, they are cut into the number of parts that takes least:
 // - rows that are few beside the keys: rounds over the SMs, plus what the parts'
@@ -547,7 +513,7 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
 //   128: 51 us whole, 34 in four parts; 6000, 2/1 heads of 64: 67 and 35; 2048,
 //   8/2 of 128: 30 and, in two, 39).
 // (A workspace's size must not depend on the device: 152 SMs.)
-int attention_tc_parts(const AttnDims& A) {
+int tc_parts(const AttnDims& A) {
     const int64_t items = items_about(A), sms = 152, tiles = A.total_k / (kRows * (int64_t)A.n_seqs);
     if (tiles < 16 || items > sms) return 1;
     const bool few = 4 * A.total_q <= A.total_k;
@@ -565,16 +531,52 @@ int attention_tc_parts(const AttnDims& A) {
     }
     return best;
 }
-size_t attention_tc_part_bytes(const AttnDims& A) {
-    const int64_t parts = attention_tc_parts(A), rows = A.total_q * A.Hq;
+size_t part_bytes(const AttnDims& A, int64_t parts) {
+    const int64_t rows = A.total_q * A.Hq;
     return parts > 1 ? (size_t)((parts * rows + 3) / 4 * 4 + parts * rows * A.d) * sizeof(float) : 0;
 }
 
+template <int D>
+cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                   const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out, float* lse, void* part_ws, size_t room,
+                   int32_t* err, cudaStream_t st) {
+    static DeviceCache cache;
+    cudaError_t e = device_cached(cache, nullptr, [](int, int*) {
+        return prepare_kernel(attention_tc_kernel<D>, Cfg<D>::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    const int pack = pack_of(A.G), qb = kRows / pack;
+    int lpack = 0;
+    while ((1 << lpack) < pack) ++lpack;
+    CUtensorMap mq, mk, mv;
+    if (!tma::make_map_3d_strided(&mq, q, true, D, (uint64_t)A.Hq, (uint64_t)A.total_q, (uint64_t)A.sq * 2, 64,
+                                  (uint32_t)pack, (uint32_t)qb) ||
+        !tma::make_map_3d_strided(&mk, k, true, D, (uint64_t)A.Hkv, (uint64_t)A.total_k, (uint64_t)A.sk * 2, 64, 1,
+                                  kRows) ||
+        !tma::make_map_3d_strided(&mv, v, true, D, (uint64_t)A.Hkv, (uint64_t)A.total_k, (uint64_t)A.sv * 2, 64, 1,
+                                  kRows))
+        return cudaErrorInvalidValue;
+    const int parts = parts_within(tc_parts(A), room, [&](int p) { return part_bytes(A, p); });
+    const int64_t blocks = items_bound(A) * parts, rows = A.total_q * A.Hq;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    float* part_lse = static_cast<float*>(part_ws);
+    float* part_o = part_lse + (parts * rows + 3) / 4 * 4;
+    attention_tc_kernel<D><<<(unsigned)blocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mk, mv, v, cu_q, cu_k, lpack, parts, out,
+                                                                             lse, part_o, part_lse, err);
+    if (parts > 1)
+        attention_join_kernel<D, __nv_bfloat16><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(A, cu_q, parts, part_o, part_lse, out, lse);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attention_tc_part_bytes(const AttnDims& A) { return part_bytes(A, tc_parts(A)); }
+
 cudaError_t launch_attention_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                 const __nv_bfloat16* v, const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out,
-                                float* lse, void* parts, int32_t* err, cudaStream_t st) {
-    return A.d == 128 ? launch<128>(A, q, k, v, cu_q, cu_k, out, lse, parts, err, st)
-                      : launch<64>(A, q, k, v, cu_q, cu_k, out, lse, parts, err, st);
+                                float* lse, void* parts, size_t room, int32_t* err, cudaStream_t st) {
+    return A.d == 128 ? launch<128>(A, q, k, v, cu_q, cu_k, out, lse, parts, room, err, st)
+                      : launch<64>(A, q, k, v, cu_q, cu_k, out, lse, parts, room, err, st);
 }
 
 }  // namespace hla

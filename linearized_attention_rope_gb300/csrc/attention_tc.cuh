@@ -283,17 +283,17 @@ __device__ __forceinline__ void clear_nonfinite(unsigned char* tile, int first, 
 
 }  // namespace attn_tc
 
-// Parts that the work of each item is cut into where items are few, and the bytes of the partial results (0: one part).
-int attention_tc_parts(const AttnDims& A);
+// The bytes of partial results of as many parts as suit the sizes (0: one part).  The launches take as many as fit into
+// `room` bytes; the gradient needs those of one part (`parts` false) in any case: -lse and -D per row and head.
 size_t attention_tc_part_bytes(const AttnDims& A);
 cudaError_t launch_attention_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                 const __nv_bfloat16* v, const int32_t* cu_q, const int32_t* cu_k, __nv_bfloat16* out,
-                                float* lse, void* parts, int32_t* err, cudaStream_t st);
-size_t attention_backward_tc_bytes(const AttnDims& A);  // -lse and -D per row and head; partial dk and dv
+                                float* lse, void* parts, size_t room, int32_t* err, cudaStream_t st);
+size_t attention_backward_tc_bytes(const AttnDims& A, bool parts);
 cudaError_t launch_attention_backward_tc(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                          const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
                                          const __nv_bfloat16* dout, const int32_t* cu_q, const int32_t* cu_k,
-                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, int32_t* err,
-                                         cudaStream_t st);
+                                         __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, size_t room,
+                                         int32_t* err, cudaStream_t st);
 
 }  // namespace hla

@@ -575,6 +575,8 @@ def _zeroed(n: int, device):
 
 def attention_workspace_bytes(params: AttnParams, total_q: int, total_k: int, n_seqs: int,
                               backward: bool = False) -> int:
+    """hla_attention_workspace_bytes: with which a call of these sizes takes the parts that suit it.  The workspace of the
+    largest call serves every smaller one, in as many parts as it has room for."""
     n = ctypes.c_size_t()
     _check(load().hla_attention_workspace_bytes(_c(params), total_q, total_k, n_seqs, int(backward),
                                                 ctypes.byref(n)), "hla_attention_workspace_bytes")

@@ -586,6 +586,33 @@ def test_runs_agree_bit_for_bit_on_any_stream_and_in_a_graph(dtype, d):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("q_lens,k_lens,hq,hkv", [([3], [9001], 4, 2), ([40, 1], [2000, 3100], 8, 4), ([700, 0, 300], [700, 5, 300], 8, 1)])
+def test_the_workspace_of_a_large_call_serves_smaller_ones(dtype, q_lens, k_lens, hq, hkv):
+    # work cut into parts takes what parts the workspace has room for; with less than one part needs it is refused
+    d, n = 64, len(q_lens)
+    prm, x = params(dtype, d, hq, hkv), make(dtype, d, hq, hkv, q_lens, k_lens, seed=3)
+    g, cq, ck = {m: t.cuda() for m, t in x.items()}, ac.cu(q_lens), ac.cu(k_lens)
+    ref = ac.attention(x["q"], x["k"], x["v"], q_lens, k_lens, dout=x["dout"])
+    own, least = ([hla.attention_workspace_bytes(prm, sum(q_lens), sum(k_lens), m, b) for b in (False, True)]
+                  for m in (n, 1000))  # (of many sequences there are enough blocks: one part)
+    large = [hla.attention_workspace_bytes(prm, 20000, 20000, 8, b) for b in (False, True)]
+    assert all(a >= b for a, b in zip(large, least)) and (own != least or dtype == "f32")
+    for share in (0.0, 0.3, 0.7, 1.0):
+        size = [max(256, int(a + share * (b - a)) // 16 * 16) for a, b in zip(least, own)]
+        ws = [torch.zeros(s + 64, dtype=torch.uint8, device="cuda") for s in size]
+        for w, s in zip(ws, size):
+            w[s:] = 123
+        out, lse = hla.attention(prm, g["q"], g["k"], g["v"], cq, ck, ws=ws[0][:size[0]])
+        grads = hla.attention_backward(prm, g["q"], g["k"], g["v"], out, lse, g["dout"], cq, ck, ws=ws[1][:size[1]])
+        check(dtype, d, x, ref, out, lse, grads, q_lens, k_lens)
+        assert all((w[s:] == 123).all() and hla.check_workspace_error(w) == 0 for w, s in zip(ws, size))
+    for fn, args in ((hla.attention, ()), (hla.attention_backward, (out, lse, g["dout"]))):
+        with pytest.raises(hla.HlaError) as e:
+            fn(prm, g["q"], g["k"], g["v"], *args, cq, ck, ws=ws[0][:240])
+        assert e.value.status == hla.HLA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("table", [[0, 50, 40, 100], [5, 50, 60, 100], [0, 50, 60, 300], [0, -7, 1 << 30, 20]])
 def test_malformed_tables_are_flagged(dtype, table):
     x = make(dtype, 64, 2, 1, [100], [100])
