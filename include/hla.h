@@ -453,7 +453,8 @@ typedef struct hla_attn_params {
  * the workspace.  With less than that, a call takes as many parts as there is
  * room for (slower; the bits of a result depend on the number of parts); the
  * least is 256 bytes, and for the gradient what one part needs, which grows
- * with total_q and total_k: the workspace of the largest call serves every smaller one.
+ * with total_q, total_k and n_seqs: the workspace of the largest call serves
+ * every smaller one.
  * Below that a call returns HLA_ERR_WORKSPACE.  The first 16 bytes are the error
  * word: zero them before the first use; calls only ever set it,
  * hla_check_workspace_error reads and clears it.  Two calls that may run at the

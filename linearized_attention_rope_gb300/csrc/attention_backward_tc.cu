@@ -24,12 +24,16 @@
 // (errors of sequences up to 128 keys 1.25 to 1.46 -> 1.00 times the rounding of
 // the result; 19 x 64 tokens 29 -> 31.6 us).
 //
-// D comes from the stored output, whose rounding matters where few keys are
-// seen (O is then as large as a value, and its error moves all of a row's dS the
-// same way): rows that see one key tile get D = sum_j P_ij dP_ij from the dq
-// kernel instead, which runs first and leaves it for the other.  (Rows of more
-// keys: O is smaller by the root of their number.  With the stored output alone
-// dq was off by 2.0 roundings of bf16 for sequences of 10 to 50 rows.)
+// D of the stored output carries that output's rounding, which moves all of a row's dS the same way.  Where those nearly
+// cancel it is all that is left: one key that takes almost all of a row (O is then that key's value), values with a common
+// part (O as large as they are, while dP - D is not).  The dq kernel, which runs first, therefore sums D = sum_j P_ij dP_ij
+// as well, and leaves it for dk and dv.  Rows that see one key tile take it for dQ at once.  In query tiles of more keys the
+// difference of the two, which is the sum of a row's dS, is taken out of dQ as if all keys were the mean of 16 that every
+// row sees (so what keys have in common cancels, as it does with dS that add up to 0); and where it is more than 4 u (u = 2^-8, bf16's) times the 2-norm of a
+// row's dS, the tile is listed and done again with the better D.  (Values without a common part: 0.6 u, nothing is listed.
+// With the stored output alone, dq of rows with P = 1 - 2^-10 was off by 1.2 times its size, that of keys and values
+// shifted by 4 by 0.1 to 0.2, now 0.003 to 0.005.  The sums and the second launch: 4096 tokens, 32/8 heads of 128,
+// 340 -> 354 us; 4 x 4096, heads of 64, 930 -> 1047.)
 //
 // Products and elementwise work alternate: while dV and the next S are formed,
 // dS is computed from dP; while dK and the next dP are formed, the next P.
@@ -63,8 +67,9 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
 template <int D>
 __global__ void __launch_bounds__(256)
 attn_stats_kernel(int64_t rows, const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
-                  const float* __restrict__ lse, float2* __restrict__ stats) {
+                  const float* __restrict__ lse, float2* __restrict__ stats, int* __restrict__ again) {
     constexpr int L = D / 8;  // lanes per row
+    if (blockIdx.x == 0 && threadIdx.x == 0) *again = 0;  // the list of query tiles to be done again
     const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
     float s = 0.f;
     if (r < rows) {
@@ -96,7 +101,8 @@ template <int D> struct Cfg {
     static constexpr int kSlots = D == 128 ? 5 : 8;
     // two fixed tiles (K, V or Q, dO), the ring, two stages of row stats (-lse, then -D; 128 fp32 each), barriers
     static constexpr uint32_t kFix = 0, kRing = 2 * kTile, kStat = kRing + kSlots * kTile, kBar = kStat + 2048;
-    static constexpr uint32_t kItem = kBar + 352, kSmem = kItem + sizeof(ItemRing);
+    static constexpr uint32_t kItem = kBar + 352, kMean = kItem + 80, kSmem = kMean + D * 4;  // kMean: a key, fp32
+    static_assert(sizeof(ItemRing) <= 80 && kSmem <= 227 * 1024, "shared memory layout");
     static constexpr uint32_t kCols = 512;
 };
 
@@ -564,14 +570,24 @@ attn_dkdv_join_kernel(AttnDims A, const int32_t* __restrict__ cu_k, int parts, c
 
 // ---- dq ---------------------------------------------------------------------
 
+__device__ __forceinline__ float sum4(const float2 (&x)[4]) {
+    const float2 y = fadd2(fadd2(x[0], x[1]), fadd2(x[2], x[3]));
+    return y.x + y.y;
+}
+constexpr float kApart = 0x1p-12f;  // (4 u)^2
+
 template <int D>
 __global__ void __launch_bounds__(kBlock, 1)
 attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CUtensorMap map_q,
                   const __grid_constant__ CUtensorMap map_do, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const int32_t* __restrict__ cu_q,
-                  const int32_t* __restrict__ cu_k, int lpack, float2* __restrict__ stats,
-                  __nv_bfloat16* __restrict__ dq, int32_t* __restrict__ err) {
+                  const int32_t* __restrict__ cu_k, int lpack, const __nv_bfloat16* __restrict__ k, float2* stats,
+                  __nv_bfloat16* __restrict__ dq, int* again, bool second, int32_t* __restrict__ err) {
     using C = Cfg<D>;
+    if (second) {  // the listed tiles
+        pdl_wait();
+        if ((int)blockIdx.x >= again[0]) return;
+    }
     // K tiles stay until their dQ product, V tiles only for dP: rings of their own, so that V runs ahead
     constexpr int kKs = C::kSlots - 2, kVs = 2;
     using RingK = RingPos<kKs>;
@@ -586,8 +602,10 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
     const uint32_t bar_ie = bar_it + 8 * kItems;
     const uint32_t bar_ask = bar_ie + 8 * kItems, bar_want = bar_ask + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kBar + 344);
+    int* noted = reinterpret_cast<int*>(sm + C::kBar + 340);  // the item listed last, and one
     ItemRing* items = reinterpret_cast<ItemRing*>(sm + C::kItem);
     if (tid == 0) {
+        *noted = 0;
         umma::mbar_init(bar_q, 1);
         umma::mbar_init(bar_qe, 1);
         for (int i = 0; i < C::kSlots; ++i) {
@@ -789,7 +807,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             }
         } else {
             schedule_items(A, cu_q, cu_k, qb, n_hg, false, items, bar_it, bar_ie, bar_ask, bar_want, err,
-                           [&](int hg) { return hg << lpack; });
+                           [&](int hg) { return hg << lpack; }, 1, true, second ? again : nullptr);
         }
     } else {
         take_registers();
@@ -803,10 +821,23 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
         for (int x = 0;; ++x) {
             int n, limit;  // key tiles; keys the row sees: [0, limit)
             int64_t at;    // the row's place in the result (-1: none)
+            int number;
+            // of 16 keys that every row of the tile sees (spread over those), this thread's column of its share
+            constexpr int kShare = 16 * D / 256;
+            unsigned short common[kShare];  // (read before the tiles, used behind them)
             {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (it.head < 0) break;
                 n = span(it).n;
+                number = it.part;
+                const int seen = it.first + it.lk - it.lq + 1;
+                const unsigned short* col = reinterpret_cast<const unsigned short*>(k) + it.k0 * A.sk + it.head / A.G * D + tid / (16 / kShare);
+#pragma unroll
+                for (int y = 0; y < kShare; ++y) {
+                    const int key = (int)((2 * (tid % (16 / kShare) * kShare + y) + 1) * (int64_t)seen / 32);
+                    common[y] = 0;
+                    if (n > 1 && !second && seen > 0) common[y] = __ldg(col + key * A.sk);
+                }
                 const int pos = it.first + (row >> lpack);
                 limit = pos < it.lq ? min(it.lk, pos + it.lk - it.lq + 1) : 0;
                 at = pos < it.lq ? ((int64_t)it.q0 + pos) * A.Hq + it.head + (row & ((1 << lpack) - 1)) : -1;
@@ -814,6 +845,10 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             const float2 st = at >= 0 ? stats[at] : make_float2(-INFINITY, 0.f);
             const float2 nl = make_float2(st.x, st.x);
             float2 nd = make_float2(st.y, st.y);
+            float2 sum[4], sq[4];  // of P dP and of dS^2, this half's (four each: a chain of 32 FMAs takes longer than the rest)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) sum[y] = sq[y] = make_float2(0.f, 0.f);
+            float *halves = reinterpret_cast<float*>(sm + C::kStat), *mean = reinterpret_cast<float*>(sm + C::kMean);
             for (int i = 0; i < n; ++i, ++t) {
                 const int seen = limit - i * kRows - half * 64;
                 const bool edge = __any_sync(0xffffffffu, seen < 64);
@@ -834,19 +869,22 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 umma::fence_after_sync();
                 float2 d[32];
                 load64(tP, d);
-                if (n == 1) {  // D of the row from all of its keys: this half's sum and the other's
-                    float sum = 0.f;
+                if (edge) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        sum += 2 * e < seen ? p[e].x * d[e].x : 0.f;
-                        sum += 2 * e + 1 < seen ? p[e].y * d[e].y : 0.f;
+                        sum[e & 3].x += 2 * e < seen ? p[e].x * d[e].x : 0.f;
+                        sum[e & 3].y += 2 * e + 1 < seen ? p[e].y * d[e].y : 0.f;
                     }
-                    float* halves = reinterpret_cast<float*>(sm + C::kStat);
-                    halves[half * 128 + row] = sum;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sum[e & 3] = ffma2(p[e], d[e], sum[e & 3]);
+                }
+                if (n == 1) {  // D of the row from all of its keys: this half's sum and the other's
+                    halves[half * 128 + row] = sum4(sum);
                     named_sync(kBarRow, 256);
-                    sum = halves[row] + halves[128 + row];
-                    nd = make_float2(-sum, -sum);
-                    if (half == 0 && at >= 0) stats[at].y = -sum;
+                    const float D_row = halves[row] + halves[128 + row];
+                    nd = make_float2(-D_row, -D_row);
+                    if (half == 0 && at >= 0) stats[at].y = -D_row;
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -855,9 +893,30 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                         d[e].x = 2 * e < seen ? d[e].x : 0.f;
                         d[e].y = 2 * e + 1 < seen ? d[e].y : 0.f;
                     }
+                    sq[e & 3] = ffma2(d[e], d[e], sq[e & 3]);
                 }
                 store64(tP, d, n == 1);
                 named_arrive(kBarDs + (t & 1), 288);
+            }
+            float off = 0.f;
+            if (n > 1 && !second) {  // D for dk and dv; the tile again if dq cannot do with the other
+                halves[half * 128 + row] = sum4(sum);
+                halves[256 + half * 128 + row] = sum4(sq);
+                float c = 0.f;
+#pragma unroll
+                for (int y = 0; y < kShare; ++y) c += __uint_as_float((uint32_t)common[y] << 16);
+#pragma unroll
+                for (int y = 1; y < 16 / kShare; y *= 2) c += __shfl_xor_sync(0xffffffffu, c, y);
+                if (tid % (16 / kShare) == 0) mean[tid / (16 / kShare)] = c * 0.0625f;
+                named_sync(kBarRow, 256);
+                const float D_row = halves[row] + halves[128 + row];
+                off = D_row + st.y;
+                const bool apart = at >= 0 && off * off > kApart * (halves[256 + row] + halves[384 + row]);
+                if (half == 0) {
+                    if (at >= 0) stats[at].y = -D_row;
+                    if (__any_sync(0xffffffffu, apart) && lane == 0 && atomicExch(noted, number + 1) != number + 1)
+                        again[1 + atomicAdd(again, 1)] = number;
+                }
             }
             if (n > 0) ok = ok && wait_or_flag(bar_done, count & 1, err);
             umma::fence_after_sync();
@@ -880,6 +939,15 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 }
                 if (at >= 0) {
                     const float m = A.scale;
+                    if (n > 1 && !second)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 c = *reinterpret_cast<const float4*>(mean + half * (D / 2) + 32 * b + e);
+                            o[e] = fmaf(-off, c.x, o[e]);
+                            o[e + 1] = fmaf(-off, c.y, o[e + 1]);
+                            o[e + 2] = fmaf(-off, c.z, o[e + 2]);
+                            o[e + 3] = fmaf(-off, c.w, o[e + 3]);
+                        }
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         *reinterpret_cast<uint4*>(dst + 32 * b + e) =
@@ -918,8 +986,13 @@ int key_parts(const AttnDims& A) {
     return best;
 }
 size_t stat_bytes(const AttnDims& A) { return ((size_t)A.total_q * A.Hq * sizeof(float2) + 255) / 256 * 256; }
+int64_t query_tiles(const AttnDims& A) {  // at most
+    const int pack = pack_of(A.G);
+    return (A.total_q / (kRows / pack) + A.n_seqs) * (A.Hq / pack);
+}
+size_t list_bytes(const AttnDims& A) { return ((size_t)(1 + query_tiles(A)) * sizeof(int) + 255) / 256 * 256; }
 size_t bytes_of(const AttnDims& A, int64_t parts) {
-    return stat_bytes(A) + (parts > 1 ? (size_t)(2 * parts * A.total_k * A.Hkv * A.d) * sizeof(float) : 0);
+    return stat_bytes(A) + list_bytes(A) + (parts > 1 ? (size_t)(2 * parts * A.total_k * A.Hkv * A.d) * sizeof(float) : 0);
 }
 
 template <int D>
@@ -927,8 +1000,10 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
                    const __nv_bfloat16* out, const float* lse, const __nv_bfloat16* dout, const int32_t* cu_q,
                    const int32_t* cu_k, __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, void* ws, size_t room,
                    int32_t* err, cudaStream_t st) {
-    static DeviceCache c1, c2;
-    cudaError_t e = device_cached(c1, nullptr, [](int, int*) { return prepare_kernel(attn_dkdv_tc_kernel<D>, Cfg<D>::kSmem); });
+    static DeviceCache c1, c2, c3;
+    int n_sm = 0;
+    cudaError_t e = device_cached(c3, &n_sm, [](int dev, int* v) { return sm_count(dev, v); });
+    if (e == cudaSuccess) e = device_cached(c1, nullptr, [](int, int*) { return prepare_kernel(attn_dkdv_tc_kernel<D>, Cfg<D>::kSmem); });
     if (e == cudaSuccess)
         e = device_cached(c2, nullptr, [](int, int*) { return prepare_kernel(attn_dq_tc_kernel<D>, Cfg<D>::kSmem); });
     if (e != cudaSuccess) return e;
@@ -944,15 +1019,23 @@ cudaError_t launch(const AttnDims& A, const __nv_bfloat16* q, const __nv_bfloat1
         return cudaErrorInvalidValue;
     const int parts = parts_within(key_parts(A), room, [&](int p) { return bytes_of(A, p); });
     float2* stats = static_cast<float2*>(ws);
-    float *part_dk = reinterpret_cast<float*>(static_cast<char*>(ws) + stat_bytes(A)),
+    int* again = reinterpret_cast<int*>(static_cast<char*>(ws) + stat_bytes(A));
+    float *part_dk = reinterpret_cast<float*>(static_cast<char*>(ws) + stat_bytes(A) + list_bytes(A)),
           *part_dv = part_dk + parts * A.total_k * A.Hkv * D;
     const int64_t rows = A.total_q * A.Hq, kb = (A.total_k / kRows + A.n_seqs) * A.Hkv * parts,
-                  qblocks = (A.total_q / qb + A.n_seqs) * (A.Hq / pack), sb = (rows * (D / 8) + 255) / 256;
+                  qblocks = query_tiles(A), sb = (rows * (D / 8) + 255) / 256;
     if (kb > INT32_MAX || qblocks > INT32_MAX || sb > INT32_MAX) return cudaErrorInvalidValue;
-    attn_stats_kernel<D><<<(unsigned)sb, 256, 0, st>>>(rows, out, dout, lse, stats);
-    // dq first: it leaves a better D for rows of few keys
-    attn_dq_tc_kernel<D><<<(unsigned)qblocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, stats,
-                                                                          dq, err);
+    attn_stats_kernel<D><<<(unsigned)sb, 256, 0, st>>>(rows, out, dout, lse, stats, again);
+    // dq first: it leaves a better D for dk and dv, and a list of tiles that need it themselves (sequences of one key tile
+    // have used it)
+    attn_dq_tc_kernel<D><<<(unsigned)qblocks, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, k, stats,
+                                                                          dq, again, false, err);
+    if (A.total_k > kRows) {
+        LaunchCfg lc(dim3((unsigned)std::min<int64_t>(qblocks, n_sm)), dim3(kBlock), Cfg<D>::kSmem, st, true);
+        e = cudaLaunchKernelEx(&lc.cfg, attn_dq_tc_kernel<D>, A, mq, mo, mk, mv, cu_q, cu_k, lpack, k, stats, dq, again, true,
+                               err);
+        if (e != cudaSuccess) return e;
+    }
     attn_dkdv_tc_kernel<D><<<(unsigned)kb, kBlock, Cfg<D>::kSmem, st>>>(A, mq, mo, mk, mv, cu_q, cu_k, lpack, parts, stats,
                                                                        dk, dv, part_dk, part_dv, err);
     if (parts > 1) {

@@ -126,7 +126,7 @@ struct Item {
     int first;   // first position of the tile(s)
     int head;    // first query head, or the kv head; -1: no more items
     int off;     // row i sees keys j <= i + off
-    int part;    // which part of the keys
+    int part;    // which part of the keys; or the item's number (`numbered`)
 };
 constexpr int kItems = 2;       // entries of the ring
 constexpr int kItemWarps = 11;  // warps that read them
@@ -163,19 +163,22 @@ __device__ __forceinline__ int64_t taken_item(uint32_t answer) {
 // The scheduling warp: `heads` head groups, `rows` positions per item, each in
 // `parts` parts: of query positions, the visible keys are cut into parts of
 // whole tiles, eight at least (the parts past those get none); of keys, the
-// reader cuts the rows that see them.
+// reader cuts the rows that see them.  Given a list (its length, then item numbers), the
+// grid's blocks take its items in turn.
 template <class HeadOf>
 __device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t* cu_q, const int32_t* cu_k, int rows,
                                                int heads, bool by_key, ItemRing* ring, uint32_t bar_full,
                                                uint32_t bar_empty, uint32_t bar_ask, uint32_t bar_want, int32_t* err,
-                                               HeadOf head_of, int parts = 1) {
+                                               HeadOf head_of, int parts = 1, bool numbered = false,
+                                               const int* list = nullptr) {
     const int lane = threadIdx.x & 31;
     const uint32_t answer = umma::smem_addr(&ring->answer);
-    int64_t x = blockIdx.x;
+    int64_t x = blockIdx.x, listed = x;
+    if (list) x = listed < list[0] ? list[1 + listed] : -1;
     bool more = true;
     for (int i = 0; more; ++i) {
         AttnBlock B = {};
-        const int part = parts > 1 && x >= 0 ? (int)(x % parts) : 0;
+        const int part = numbered ? (int)x : parts > 1 && x >= 0 ? (int)(x % parts) : 0;
         if (x >= 0) B = attn_find_block(A, cu_q, cu_k, rows, x / parts / heads, by_key);
         const int s = i % kItems;
         more = B.found;
@@ -198,6 +201,11 @@ __device__ __forceinline__ void schedule_items(const AttnDims& A, const int32_t*
         if (!more) break;
         x = -1;
         if (wait_polls(bar_want, i & 1, err, kItemPolls)) {
+            if (list) {
+                listed += gridDim.x;
+                if (listed < list[0]) x = list[1 + listed];
+                continue;
+            }
             if (lane == 0) ask_item(answer, bar_ask);
             if (__any_sync(0xffffffffu, wait_or_flag(bar_ask, i & 1, err))) x = taken_item(answer);
             __syncwarp();

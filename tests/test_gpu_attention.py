@@ -263,6 +263,57 @@ def test_scale_and_large_scores(dtype):
     full_check(dtype, 64, 2, 1, [150], scale=2.0, seed=5)
 
 
+def dq_bound(d, x, lens, scale):
+    """dq in 64 bits, and the 2-norm that its rounding errors add up to over the whole tensor, for D of 32 bits: per row,
+    independent roundings of ds to bf16 (u / sqrt(3) of each) in the sum with k, of the result, and a D that may be off by
+    four times u times the 2-norm of the row's ds, times sum p k less the mean of 16 keys that the row's whole tile sees."""
+    u, want, size = ac.EPS[torch.bfloat16] / 2, [], 0.0
+    a = 0
+    for n in lens:
+        q, k, v, do = (x[m][a:a + n].double() for m in ("q", "k", "v", "dout"))
+        g = q.shape[1] // k.shape[1]
+        for h in range(q.shape[1]):
+            kk, vv = k[:, h // g], v[:, h // g]
+            s = (q[:, h] @ kk.T * scale).masked_fill(torch.ones(n, n).triu(1).bool(), -math.inf)
+            p = torch.softmax(s, 1)
+            dp = do[:, h] @ vv.T
+            ds = p * (dp - (p * dp).sum(1, keepdim=True)) * scale
+            dq = ds @ kk
+            want.append(dq)
+            size += float((ds ** 2 @ kk ** 2 + dq ** 2).sum()) * u * u / 3
+            tile = 128 // min(16, g & -g)  # positions
+            seen = torch.arange(n)[:, None] // tile * tile + 1
+            mean = kk[(2 * torch.arange(16) + 1) * seen // 32].mean(1)
+            size += float((16 * u * u * (ds ** 2).sum(1, keepdim=True) * (p @ kk - mean) ** 2).sum())
+        a += n
+    return want, math.sqrt(size)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 2, 1), (128, 1, 1), (128, 4, 1)])
+@pytest.mark.parametrize("lens", [[700], [200, 333]])
+@pytest.mark.parametrize("kind", ["peaked", "shifted", "flat"])
+def test_gradient_of_rows_whose_score_gradients_nearly_cancel(d, hq, hkv, lens, kind):
+    # rows of several key tiles where one key takes almost all (out is nearly a value, and dp - D nearly 0), and values and
+    # keys with a common part (out as large as a value, which cancels in ds): dq must not carry the rounding of out
+    x = make("bf16", d, hq, hkv, lens, lens, seed=17)
+    n, scale = sum(lens), 1 / math.sqrt(d)
+    if kind == "peaked":  # the row's query is its own key, long enough for a share of 1 - 2^-10 or so
+        t = 9.0 + math.log(n)
+        kk = x["k"].double().repeat_interleave(hq // hkv, 1)
+        x["q"] = (kk * (t / scale / (kk ** 2).sum(-1, keepdim=True))).bfloat16()
+    if kind == "shifted":
+        x["k"], x["v"] = (x[m] + 4 * ac.randn(3, 1, hkv, d, dtype=torch.bfloat16) for m in "kv")
+    want, size = dq_bound(d, x, lens, scale)
+    _, _, grads = run(params("bf16", d, hq, hkv), x, lens, lens)
+    off, a, got = 0.0, 0, grads["q"].cpu().double()
+    for i, m in enumerate(lens):
+        for h in range(hq):
+            off += float(((got[a:a + m, h] - want[i * hq + h]) ** 2).sum())
+        a += m
+    total = math.sqrt(sum(float((w ** 2).sum()) for w in want))
+    assert math.sqrt(off) <= 1.2 * size + 2e-5 * total
+
+
 def test_two_calls_at_once():
     # two layers' calls on two streams, a workspace each, beside each other: bit for bit what they are alone
     cases = [("bf16", 128, 8, 2, [900, 700]), ("bf16", 64, 4, 4, [1500])]
