@@ -28,12 +28,15 @@
 // cancel it is all that is left: one key that takes almost all of a row (O is then that key's value), values with a common
 // part (O as large as they are, while dP - D is not).  The dq kernel, which runs first, therefore sums D = sum_j P_ij dP_ij
 // as well, and leaves it for dk and dv.  Rows that see one key tile take it for dQ at once.  In query tiles of more keys the
-// difference of the two, which is the sum of a row's dS, is taken out of dQ as if all keys were the mean of 16 that every
-// row sees (so what keys have in common cancels, as it does with dS that add up to 0); and where it is more than 4 u (u = 2^-8, bf16's) times the 2-norm of a
-// row's dS, the tile is listed and done again with the better D.  (Values without a common part: 0.6 u, nothing is listed.
-// With the stored output alone, dq of rows with P = 1 - 2^-10 was off by 1.2 times its size, that of keys and values
-// shifted by 4 by 0.1 to 0.2, now 0.003 to 0.005.  The sums and the second launch: 4096 tokens, 32/8 heads of 128,
-// 340 -> 354 us; 4 x 4096, heads of 64, 930 -> 1047.)
+// difference of the two, which is the sum of a row's dS, is taken out of dQ as if all keys were the mean of 64 that every
+// row sees, so that what keys have in common cancels as it does with dS that add up to 0.  What is left is the difference
+// times how far that mean is from the row's own weighted mean of the keys, about their spread times sqrt(1 / 64 + sum P^2);
+// query tiles in which that is more than 16 u (u = 2^-8, bf16's) of a row's dQ are listed and done again with the better D.
+// (With the stored output alone, dq of rows with P = 1 - 2^-10 was off by 1.2 times its size, that of keys and values
+// shifted by 4 by 0.1 to 0.2; now 0.003 to 0.005 and 0.006 to 0.009.  4096 tokens, 32/8 heads of 128: 340 -> 362 us, 370 with
+// values and keys shifted by 1, 503 by 4, where 6 of 10 tiles are done again; 4 x 4096, heads of 64: 930 -> 1073.  Every
+// tile again where the difference exceeds 4 u of the 2-norm of dS: 354, 530, 531 and 1047, and values shifted by 0.1 are enough
+// for a third of the tiles.)
 //
 // Products and elementwise work alternate: while dV and the next S are formed,
 // dS is computed from dP; while dK and the next dP are formed, the next P.
@@ -101,7 +104,7 @@ template <int D> struct Cfg {
     static constexpr int kSlots = D == 128 ? 5 : 8;
     // two fixed tiles (K, V or Q, dO), the ring, two stages of row stats (-lse, then -D; 128 fp32 each), barriers
     static constexpr uint32_t kFix = 0, kRing = 2 * kTile, kStat = kRing + kSlots * kTile, kBar = kStat + 2048;
-    static constexpr uint32_t kItem = kBar + 352, kMean = kItem + 80, kSmem = kMean + D * 4;  // kMean: a key, fp32
+    static constexpr uint32_t kItem = kBar + 352, kMean = kItem + 80, kSmem = kMean + D * 4 + 32;  // kMean: a key and 8 sums, fp32
     static_assert(sizeof(ItemRing) <= 80 && kSmem <= 227 * 1024, "shared memory layout");
     static constexpr uint32_t kCols = 512;
 };
@@ -574,7 +577,11 @@ __device__ __forceinline__ float sum4(const float2 (&x)[4]) {
     const float2 y = fadd2(fadd2(x[0], x[1]), fadd2(x[2], x[3]));
     return y.x + y.y;
 }
-constexpr float kApart = 0x1p-12f;  // (4 u)^2
+__device__ __forceinline__ float2 pair(uint32_t w) {  // of bf16
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+constexpr float kApart = 0x1p-8f;  // (16 u)^2
+constexpr int kSample = 64;        // keys
 
 template <int D>
 __global__ void __launch_bounds__(kBlock, 1)
@@ -822,21 +829,22 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             int n, limit;  // key tiles; keys the row sees: [0, limit)
             int64_t at;    // the row's place in the result (-1: none)
             int number;
-            // of 16 keys that every row of the tile sees (spread over those), this thread's column of its share
-            constexpr int kShare = 16 * D / 256;
-            unsigned short common[kShare];  // (read before the tiles, used behind them)
+            // of kSample keys that every row of the tile sees (spread over those), two columns of this thread's share (read
+            // before the tiles, used behind them)
+            constexpr int kShares = 512 / D, kShare = kSample / kShares;
+            uint32_t common[kShare];
             {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (it.head < 0) break;
                 n = span(it).n;
                 number = it.part;
                 const int seen = it.first + it.lk - it.lq + 1;
-                const unsigned short* col = reinterpret_cast<const unsigned short*>(k) + it.k0 * A.sk + it.head / A.G * D + tid / (16 / kShare);
+                const __nv_bfloat16* col = k + it.k0 * A.sk + it.head / A.G * D + tid / kShares * 2;
 #pragma unroll
                 for (int y = 0; y < kShare; ++y) {
-                    const int key = (int)((2 * (tid % (16 / kShare) * kShare + y) + 1) * (int64_t)seen / 32);
-                    common[y] = 0;
-                    if (n > 1 && !second && seen > 0) common[y] = __ldg(col + key * A.sk);
+                    const int key = (int)((2 * (tid % kShares * kShare + y) + 1) * (int64_t)seen / (2 * kSample));
+                    common[y] = 0u;
+                    if (n > 1 && !second) common[y] = __ldg(reinterpret_cast<const uint32_t*>(col + key * A.sk));
                 }
                 const int pos = it.first + (row >> lpack);
                 limit = pos < it.lq ? min(it.lk, pos + it.lk - it.lq + 1) : 0;
@@ -845,9 +853,9 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             const float2 st = at >= 0 ? stats[at] : make_float2(-INFINITY, 0.f);
             const float2 nl = make_float2(st.x, st.x);
             float2 nd = make_float2(st.y, st.y);
-            float2 sum[4], sq[4];  // of P dP and of dS^2, this half's (four each: a chain of 32 FMAs takes longer than the rest)
+            float2 sum[4], pp[4];  // of P dP and of P^2, this half's (four each: a chain of 32 FMAs takes longer than the rest)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) sum[y] = sq[y] = make_float2(0.f, 0.f);
+            for (int y = 0; y < 4; ++y) sum[y] = pp[y] = make_float2(0.f, 0.f);
             float *halves = reinterpret_cast<float*>(sm + C::kStat), *mean = reinterpret_cast<float*>(sm + C::kMean);
             for (int i = 0; i < n; ++i, ++t) {
                 const int seen = limit - i * kRows - half * 64;
@@ -865,6 +873,9 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                     const float2 a = ffma2(p[e], c2, nl);
                     p[e] = make_float2(ex2(a.x), ex2(a.y));
                 }
+                if (!edge)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) pp[e & 3] = ffma2(p[e], p[e], pp[e & 3]);
                 named_sync(kBarDq + (t & 1), 288);
                 umma::fence_after_sync();
                 float2 d[32];
@@ -874,6 +885,8 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                     for (int e = 0; e < 32; ++e) {
                         sum[e & 3].x += 2 * e < seen ? p[e].x * d[e].x : 0.f;
                         sum[e & 3].y += 2 * e + 1 < seen ? p[e].y * d[e].y : 0.f;
+                        pp[e & 3].x += 2 * e < seen ? p[e].x * p[e].x : 0.f;
+                        pp[e & 3].y += 2 * e + 1 < seen ? p[e].y * p[e].y : 0.f;
                     }
                 } else {
 #pragma unroll
@@ -893,35 +906,47 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                         d[e].x = 2 * e < seen ? d[e].x : 0.f;
                         d[e].y = 2 * e + 1 < seen ? d[e].y : 0.f;
                     }
-                    sq[e & 3] = ffma2(d[e], d[e], sq[e & 3]);
                 }
                 store64(tP, d, n == 1);
                 named_arrive(kBarDs + (t & 1), 288);
             }
-            float off = 0.f;
-            if (n > 1 && !second) {  // D for dk and dv; the tile again if dq cannot do with the other
+            float off = 0.f, far = 0.f;  // sum of the row's dS; square of what the mean key may be off as their weighted mean
+            if (n > 1 && !second) {      // D for dk and dv, and what of dQ goes with a wrong one
                 halves[half * 128 + row] = sum4(sum);
-                halves[256 + half * 128 + row] = sum4(sq);
-                float c = 0.f;
+                halves[256 + half * 128 + row] = sum4(pp);
+                float2 c = make_float2(0.f, 0.f);
+                float spread = 0.f;
 #pragma unroll
-                for (int y = 0; y < kShare; ++y) c += __uint_as_float((uint32_t)common[y] << 16);
+                for (int y = 0; y < kShare; ++y) c = fadd2(c, pair(common[y]));
 #pragma unroll
-                for (int y = 1; y < 16 / kShare; y *= 2) c += __shfl_xor_sync(0xffffffffu, c, y);
-                if (tid % (16 / kShare) == 0) mean[tid / (16 / kShare)] = c * 0.0625f;
+                for (int y = 1; y < kShares; y *= 2) {
+                    c.x += __shfl_xor_sync(0xffffffffu, c.x, y);
+                    c.y += __shfl_xor_sync(0xffffffffu, c.y, y);
+                }
+                c = make_float2(c.x / kSample, c.y / kSample);
+#pragma unroll
+                for (int y = 0; y < kShare; ++y) {
+                    const float2 x = pair(common[y]);
+                    spread += (x.x - c.x) * (x.x - c.x) + (x.y - c.y) * (x.y - c.y);
+                }
+#pragma unroll
+                for (int y = 16; y; y >>= 1) spread += __shfl_xor_sync(0xffffffffu, spread, y);
+                if (tid % kShares == 0) *reinterpret_cast<float2*>(mean + tid / kShares * 2) = c;
+                if (lane == 0) mean[D + warp] = spread;
                 named_sync(kBarRow, 256);
                 const float D_row = halves[row] + halves[128 + row];
                 off = D_row + st.y;
-                const bool apart = at >= 0 && off * off > kApart * (halves[256 + row] + halves[384 + row]);
-                if (half == 0) {
-                    if (at >= 0) stats[at].y = -D_row;
-                    if (__any_sync(0xffffffffu, apart) && lane == 0 && atomicExch(noted, number + 1) != number + 1)
-                        again[1 + atomicAdd(again, 1)] = number;
-                }
+                spread = 0.f;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) spread += mean[D + y];
+                far = spread / (2 * kSample) * (1.f / kSample + halves[256 + row] + halves[384 + row]);  // (of half the columns)
+                if (half == 0 && at >= 0) stats[at].y = -D_row;
             }
             if (n > 0) ok = ok && wait_or_flag(bar_done, count & 1, err);
             umma::fence_after_sync();
             // ---- results: half of the columns each
             __nv_bfloat16* dst = dq + at * D + half * (D / 2);
+            float norm = 0.f;
 #pragma unroll
             for (int b = 0; b < D / 64; ++b) {
                 float o[32];
@@ -947,6 +972,7 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                             o[e + 1] = fmaf(-off, c.y, o[e + 1]);
                             o[e + 2] = fmaf(-off, c.z, o[e + 2]);
                             o[e + 3] = fmaf(-off, c.w, o[e + 3]);
+                            norm += (o[e] * o[e] + o[e + 1] * o[e + 1]) + (o[e + 2] * o[e + 2] + o[e + 3] * o[e + 3]);
                         }
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
@@ -955,6 +981,10 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                                        pack_bf2(o[e + 4] * m, o[e + 5] * m), pack_bf2(o[e + 6] * m, o[e + 7] * m));
                 }
             }
+            // the tile again where a row may be off by more
+            if (n > 1 && !second && __any_sync(0xffffffffu, at >= 0 && off * off * far > kApart * norm) && lane == 0 &&
+                atomicExch(noted, number + 1) != number + 1)
+                again[1 + atomicAdd(again, 1)] = number;
         }
     }
     umma::fence_before_sync();
