@@ -420,8 +420,9 @@ HLA_API int hla_rope_frequencies(const hla_rope_params* params, double* w, doubl
  * NULL, with its output) to the positions given per token (int64, device, any
  * value): a pair (a, b) at angle t becomes gain (a cos t - b sin t, b cos t +
  * a sin t).  In place where an output is its input's address.  Angles are
- * formed as 64-bit fractions of a turn, so far positions lose nothing.  The
- * outputs must not overlap the inputs in any other way.  Asynchronous. */
+ * formed as 64-bit fractions of a turn: exact products with frequencies of
+ * double precision, off by about 2^-53 of p w_i at any position p.
+ * The outputs must not overlap the inputs in any other way.  Asynchronous. */
 HLA_API int hla_rope(const hla_rope_params* params, const void* q, const void* k, const int64_t* positions,
                      int64_t total_tokens, void* q_out, void* k_out, void* stream);
 

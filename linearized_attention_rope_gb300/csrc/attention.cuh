@@ -9,7 +9,7 @@ namespace hla {
 constexpr int kMaxRopePairs = 128;
 
 // Angles per position as 64-bit fractions of a turn: position p's angle is
-// the top bits of p * freq (mod 2^64, i.e. mod one turn).
+// p * freq mod 2^64, i.e. mod one turn.
 struct RopeDims {
     int Hq, Hkv, d, r;
     int interleaved;

@@ -2,9 +2,12 @@
 //
 // A pair (a, b) at position p becomes gain (a cos t - b sin t, b cos t +
 // a sin t), t = p w_i; the gradient rotates back.  The angle is formed as a
-// fraction of a turn in 64-bit fixed point, p * freq mod 2^64, which keeps
-// 2^-64 of a turn per position at any distance and needs no range reduction
-// and no fp64 unit; its top 32 bits go to sincospif.
+// fraction of a turn in 64-bit fixed point, p * freq mod 2^64: the product is
+// exact at any position and needs no range reduction and no fp64 unit.  (freq is
+// w_i / 2 pi with a double's precision, so an angle is off by about 2^-53 of
+// itself before whole turns are taken off.)  The nearest quarter of a turn is
+// taken off before the rest is rounded to fp32 for sincospif: rounded as a whole
+// the angle is off by up to 9e-8 wherever it lies, sines near their zeros too.
 //
 // Memory bound: every element is read and written once.  A block takes a few
 // tokens: it forms their r/2 sines and cosines once in shared memory, for all
@@ -38,8 +41,11 @@ rope_kernel(const __grid_constant__ RopeDims R, const T* q, const T* k, const in
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int t = i / half, j = i - t * half;
         const uint64_t turn = (uint64_t)__ldg(pos + t0 + t) * R.freq[j];
-        float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+        const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);  // 0 .. 3
+        float x, y;
+        sincospif((float)(int64_t)(turn - ((uint64_t)quarter << 62)) * 0x1p-63f, &x, &y);  // half turns, within a quarter
+        const float c = quarter & 1 ? (quarter & 2 ? x : -x) : (quarter & 2 ? -y : y);
+        const float s = quarter & 1 ? (quarter & 2 ? -y : y) : (quarter & 2 ? -x : x);
         cs[(t * V + j % V) * places + j / V] = make_float2(c * R.gain, s * R.gain * (float)R.sign);
     }
     __syncthreads();

@@ -78,6 +78,23 @@ def test_far_positions_and_every_scaling():
         assert (got.cpu().double() - ref).abs().max() <= 2 * gain * q.abs().max() * (2.0 ** 40 * 2 ** -52 * 7 + 1e-6)
 
 
+def test_sines_near_half_a_turn_keep_their_bits():
+    # the pair (1, 0) of angular frequency 1 becomes (cos p, sin p).  Positions whose angle lies near a half or a whole
+    # turn: the sine is small, and off by a rounding of the angle's distance from there (2^-24 of it), 2 ulp of the
+    # function's (2^-22 of it), and the frequency's double (p 2^-53, and as much for the product); likewise cosines near a quarter
+    p = torch.arange(100000, dtype=torch.int64)
+    prm = hla.RopeParams(1, 0, 2, dtype=hla.DTYPE_F32, base=10000.0)
+    q = torch.zeros(len(p), 1, 2)
+    q[..., 0] = 1.0
+    got = hla.rope(prm, q.cuda(), None, p.cuda())[0].cpu().double()[:, 0]
+    for i, want in ((0, p.double().cos()), (1, p.double().sin())):
+        near = want.abs() < 2.0 ** -6
+        assert near.sum() > 500
+        tol = want.abs() * 5 * 2.0 ** -24 + p * 2.0 ** -52
+        over = ((got[:, i] - want).abs() - tol)[near]
+        assert (over <= 0).all(), float(over.max())
+
+
 def test_frequencies_against_their_definitions():
     r, base, f, orig = 64, 500000.0, 8.0, 8192
     plain = [base ** (-2 * i / r) for i in range(r // 2)]
