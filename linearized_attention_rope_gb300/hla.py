@@ -434,7 +434,7 @@ def _check_tensor(t, fn: str, name: str, dtype, shape, device, strided: bool = F
         _refuse(f"{fn}: {name}: expected on {device}, got {t.device}")
     if t.is_contiguous() or t.numel() == 0:
         return shape[1] * shape[2] if len(shape) == 3 else 0
-    if not (strided and len(shape) == 3 and t.stride(2) == 1 and t.stride(1) == shape[2] and
+    if not (strided and len(shape) == 3 and t.stride(2) == 1 and (t.stride(1) == shape[2] or shape[1] == 1) and
             t.stride(0) >= shape[1] * shape[2]):
         _refuse(f"{fn}: {name}: expected dense {'rows' if strided else 'storage'}")
     return t.stride(0)

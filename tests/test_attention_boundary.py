@@ -170,3 +170,17 @@ def test_binding_refuses_wrong_tensors(lib):
     refused(hla.rope, rp, q, k, torch.zeros(7, dtype=torch.int64))
     refused(hla.rope, rp, None, k, torch.zeros(8, dtype=torch.int64), q_out=q)
     refused(hla.Cache, hla.CacheParams(2, 64, 16, 4, 2), torch.zeros(1, 2, dtype=torch.int32))
+
+
+def test_rows_of_one_head_at_any_stride():
+    # the stride of a dimension of size one says nothing: a fused [T, 1, 3, d] projection's q, k, v
+    wide = torch.zeros(5, 1, 3, 64)
+    for i in range(3):
+        t = wide[:, :, i]
+        assert t.stride() == (192, 192, 1)
+        assert hla._check_tensor(t, "f", "t", torch.float32, (5, 1, 64), t.device, strided=True) == 192
+    with pytest.raises(hla.HlaError):
+        hla._check_tensor(wide[:, :, 0], "f", "t", torch.float32, (5, 1, 64), wide.device)  # where dense rows are asked for
+    two = torch.zeros(5, 2, 3, 64)[:, :, 0]
+    with pytest.raises(hla.HlaError):
+        hla._check_tensor(two, "f", "t", torch.float32, (5, 2, 64), two.device, strided=True)
