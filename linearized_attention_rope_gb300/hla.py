@@ -622,7 +622,9 @@ def _check_workspace(fn, ws, dev):
 def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, ws=None, stream=None):
     """hla_attention: (out [Tq, Hq, d], lse [Tq, Hq] fp32) of causal attention over packed sequences.  q, k, v
     may be slices of one fused projection.  cu_seqlens_k: the key rows' offsets where they differ from the
-    query rows' (chunks of prompts behind earlier keys)."""
+    query rows' (chunks of prompts behind earlier keys).  Without `ws` one is allocated for the call, and what the device
+    flags (a malformed table, a wait that ran out) cannot be read: where that may happen, pass a workspace and ask
+    check_workspace_error."""
     strides, tq, tk, n = _check_packed("hla_attention", params, q, k, v, cu_seqlens_q, cu_seqlens_k, ws)
     dev, shape = q.device, (tq, params.n_q_heads, params.head_dim)
     if out is not None:
@@ -648,7 +650,8 @@ def attention(params: AttnParams, q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=
 def attention_backward(params: AttnParams, q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k=None, grads=None,
                        ws=None, stream=None):
     """hla_attention_backward: {"q", "k", "v"} gradients of sum(dout * out), dense, in the layer's type, from
-    attention's inputs and results.  `grads` (same dict) and `ws` may be passed in to be reused."""
+    attention's inputs and results.  `grads` (same dict) and `ws` may be passed in to be reused; without `ws`, what the
+    device flags cannot be read (as for attention)."""
     fn = "hla_attention_backward"
     strides, tq, tk, n = _check_packed(fn, params, q, k, v, cu_seqlens_q, cu_seqlens_k, ws)
     dev = q.device
