@@ -11,8 +11,8 @@
 //         dP = dO V^T, dQ += dS K
 // That is 7 products in place of the 5 that one pass would take with dQ added
 // to memory from many blocks: fp32 atomics would make results depend on the
-// order of arrival, and their traffic (4 bytes d per row and key tile) exceeds
-// what the two extra products cost.  Shared kv heads are summed in the block;
+// order of arrival.  (Adding them in turn, a fixed order, was not tried; the
+// traffic is 4 bytes d per row and key tile either way.)  Shared kv heads are summed in the block;
 // only where key blocks are few are the rows of one cut over blocks, whose sums
 // a third kernel adds in order.
 //

@@ -1,7 +1,7 @@
 // How a decode step's keys are cut over the thread blocks, shared by its
 // kernels and the join.
 //
-// The keys of all sequences, in units of 64 to 256, form one line of U units; with n
+// The keys of all sequences, in units of 64 or 128, form one line of U units; with n
 // blocks (at most U: the rest leave at once) block c takes units [c U / n,
 // (c + 1) U / n) of it, for one kv head.  Blocks are equally
 // loaded whatever the lengths, and only a block's first and last sequence can

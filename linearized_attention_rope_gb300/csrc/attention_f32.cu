@@ -1,5 +1,6 @@
 // Packed causal attention and its gradient of fp32 layers, on the CUDA cores:
-// the tensor cores do not form these products exactly.
+// the tensor cores do not form these products exactly.  (Operands split into
+// three bf16 parts, six products, were not tried.)
 //
 // Forward: blocks of 64, 32 or 16 query rows of a head walk 64-key tiles with the
 // running maximum and sum; a thread holds 4 x 4 scores.  Gradient: the
@@ -17,8 +18,8 @@
 // (2 at head dim 128) take the tiles in turn and add their sums at the end, in
 // order.
 //
-// Bound by shared-memory reads (eight of 16 bytes per 64 FMAs, at a quarter of a
-// warp a cycle) and the fp32 FMA rate.  4096 tokens, 8/2 heads of 128: forward 1141 us (30 TFLOP/s of
+// Bound by shared-memory reads: eight of 16 bytes per 64 FMAs, at a quarter of a
+// warp a cycle, which the 4 x 4 scores of a thread set (larger ones would need fewer).  4096 tokens, 8/2 heads of 128: forward 1141 us (30 TFLOP/s of
 // the 80 the FMAs could do), gradient 3904 us (31 with the 7 products it forms);
 // 813 tokens, 4/2 heads of 64, where the walk of one block is what takes the
 // time: 24 and 63 us (blocks of 32 and one group: 31 and 91).
@@ -560,7 +561,8 @@ int block_rows(int64_t total, int n_seqs, int heads, int least) {
 }
 
 // Parts that the keys of few rows (chunks behind earlier keys) are cut into at most, a block each, joined in order: one
-// for every kPartTiles tiles that a single sequence could have, where the blocks would not fill the SMs twice.  Forward:
+// for every kPartTiles tiles that a single sequence could have, where the blocks would not fill the SMs twice.  How the keys
+// are spread over the sequences is known on the device only: equal lengths lose a little by it, unequal ones gain much.  Forward:
 // 186 rows in 5, one of them 31 behind 3506 keys, 8/4 heads of 128, 250 -> 58 us; 64 rows behind 8128, 32/8 of 128, 567 ->
 // 289; one row of 3000, one head of 64, 77 -> 23; 5 x 100 behind 900, 4/2 of 64, 42 -> 43; 4 x 1 behind 2000, 32/8 of 128,
 // 145 -> 158.  Gradient (dq): 327 -> 158, 1109 -> 1081, 107 -> 46, 98 -> 110, 689 -> 700.
@@ -652,14 +654,12 @@ cudaError_t backward(const AttnDims& A, const float* q, const float* k, const fl
     float *delta = ws, *parts = ws + (rows + 63) / 64 * 64;
     float* dq_part = parts + (A.G > 1 ? 2 * A.total_k * A.Hq * D : 0);
     const int kb = block_rows(A.total_k, A.n_seqs, A.Hq, 152), qb = block_rows(A.total_q, A.n_seqs, A.Hq, 152);
-    cudaError_t e = cudaSuccess;
-    if (rows > 0) attn_delta_kernel<D><<<(unsigned)((rows + 7) / 8), kThreads, 0, st>>>(rows, out, dout, delta);
-    if (A.total_k > 0)
-        e = (kb == 64   ? keys_backward<D, 64, 1, D == 64 ? 2 : 1>
-             : kb == 32 ? keys_backward<D, 32, kSmallGroups<D>, 1>
-                        : keys_backward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv, delta, parts,
-                                                                    err, st);
-    if (e != cudaSuccess || rows == 0) return e;
+    attn_delta_kernel<D><<<(unsigned)((rows + 7) / 8), kThreads, 0, st>>>(rows, out, dout, delta);
+    const cudaError_t e = (kb == 64   ? keys_backward<D, 64, 1, D == 64 ? 2 : 1>
+                           : kb == 32 ? keys_backward<D, 32, kSmallGroups<D>, 1>
+                                      : keys_backward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, lse, dout, cu_q, cu_k, dk, dv,
+                                                                                  delta, parts, err, st);
+    if (e != cudaSuccess) return e;
     return (qb == 64   ? rows_backward<D, 64, 1, D == 64 ? 2 : 1>
             : qb == 32 ? rows_backward<D, 32, kSmallGroups<D>, 1>
                        : rows_backward<D, 16, kSmallGroups<D>, 1>)(A, q, k, v, lse, dout, cu_q, cu_k, dq, delta, dq_part,

@@ -35,19 +35,19 @@
 // the rounded value and what that leaves, in two products: the roundings of a
 // few keys do not average out as those of many do (outputs of a few rows were
 // off by up to 1.5 times the rounding of the result, now by 1.00; 19 x 64 tokens
-// 11.6 -> 12.3 us, 4 x 4096 385 -> 394).
+// 11.6 -> 12.3 us, 4 x 4096 385 -> 394).  Rows of more tiles keep the one: up to 1.5
+// where few of their keys have weight.
 //
 // With fewer items than SMs (a short chunk of a prompt behind many keys, few
 // heads), the keys of each item are cut into parts, an item each; a part leaves
 // its rows' outputs in fp32 with their log-sum-exp, and a second kernel adds
 // them in order.
 //
-// Bound by the tensor cores (4 d flops per visible score) together with the
-// softmax's issue slots (about 4 instructions and one exponential per score).
-// bf16, 32/8 heads of 128: 32768 tokens in 5.1 to 5.3 ms (1670 to 1710 TFLOP/s; a large library
-// product sustains 1695), 4096 in 104 to 108 us (1300: 512 items of 1 to 32 key tiles
-// over 152 SMs, and the half of each edge tile that the mask throws away).
-// 4 x 4096 tokens, 32/8 heads of 64: 270 us (half the flops per exponential).
+// Long prompts are bound by the tensor cores: bf16, 32/8 heads of 128, 32768 tokens in 5.2 to 5.4 ms (1620 to
+// 1690 TFLOP/s; a large library product sustains 1695).  4096 in 104 to 108 us (1300): there neither they (54 %
+// active) nor the issue slots (1.2 instructions of 4 a cycle) are the limit, nor the masked half of the edge tiles (3 %
+// more key tiles than the visible scores need) or the items' lengths; 4 x 4096 tokens, 32/8 heads of 64, 270 us, the
+// same (35 % and 1.5).  What is, the exponentials' rate or the chain of steps within a tile, has not been measured.
 // 64 rows over 131072 keys: 105 us.
 #include <type_traits>
 
