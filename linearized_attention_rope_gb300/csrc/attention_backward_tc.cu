@@ -33,8 +33,8 @@
 // times how far that mean is from the row's own weighted mean of the keys, about their spread times sqrt(1 / 64 + sum P^2);
 // query tiles in which that is more than 16 u (u = 2^-8, bf16's) of a row's dQ are listed and done again with the better D.
 // (With the stored output alone, dq of rows with P = 1 - 2^-10 was off by 1.2 times its size, that of keys and values
-// shifted by 4 by 0.1 to 0.2; now 0.003 to 0.005 and 0.006 to 0.009.  4096 tokens, 32/8 heads of 128: 340 -> 362 us, 370 with
-// values and keys shifted by 1, 503 by 4, where 6 of 10 tiles are done again; 4 x 4096, heads of 64: 930 -> 1073.  Every
+// shifted by 4 by 0.1 to 0.2; now 0.003 to 0.005 and 0.006 to 0.009.  4096 tokens, 32/8 heads of 128: 340 -> 358 us, 362 with
+// values and keys shifted by 1, 498 by 4, where 6 of 10 tiles are done again; 4 x 4096, heads of 64: 930 -> 1060.  Every
 // tile again where the difference exceeds 4 u of the 2-norm of dS: 354, 530, 531 and 1047, and values shifted by 0.1 are enough
 // for a third of the tiles.)
 //
@@ -833,18 +833,21 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
             // before the tiles, used behind them)
             constexpr int kShares = 512 / D, kShare = kSample / kShares;
             uint32_t common[kShare];
+            bool few;  // fewer than that: too few to judge by
             {
                 const Item it = next_item(items, x, bar_it, bar_ie, err);
                 if (it.head < 0) break;
                 n = span(it).n;
                 number = it.part;
                 const int seen = it.first + it.lk - it.lq + 1;
+                few = seen < kSample;
+                const int step = max(1, seen / kSample), x0 = tid % kShares * kShare;
                 const __nv_bfloat16* col = k + it.k0 * A.sk + it.head / A.G * D + tid / kShares * 2;
 #pragma unroll
                 for (int y = 0; y < kShare; ++y) {
-                    const int key = (int)((2 * (tid % kShares * kShare + y) + 1) * (int64_t)seen / (2 * kSample));
                     common[y] = 0u;
-                    if (n > 1 && !second) common[y] = __ldg(reinterpret_cast<const uint32_t*>(col + key * A.sk));
+                    if (n > 1 && !second)
+                        common[y] = __ldg(reinterpret_cast<const uint32_t*>(col + min((x0 + y) * step, seen - 1) * A.sk));
                 }
                 const int pos = it.first + (row >> lpack);
                 limit = pos < it.lq ? min(it.lk, pos + it.lk - it.lq + 1) : 0;
@@ -982,7 +985,8 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 }
             }
             // the tile again where a row may be off by more
-            if (n > 1 && !second && __any_sync(0xffffffffu, at >= 0 && off * off * far > kApart * norm) && lane == 0 &&
+            const bool apart = few ? off != 0.f : off * off * far > kApart * norm;
+            if (n > 1 && !second && __any_sync(0xffffffffu, at >= 0 && apart) && lane == 0 &&
                 atomicExch(noted, number + 1) != number + 1)
                 again[1 + atomicAdd(again, 1)] = number;
         }

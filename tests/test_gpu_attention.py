@@ -314,6 +314,13 @@ def test_gradient_of_rows_whose_score_gradients_nearly_cancel(d, hq, hkv, lens, 
     assert math.sqrt(off) <= 1.2 * size + 2e-5 * total
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(64, 7, 1), (128, 5, 1), (64, 3, 3), (64, 14, 2)])
+@pytest.mark.parametrize("lq,lk", [(241, 242), (560, 561), (259, 260), (300, 310), (300, 340), (300, 364)])
+def test_gradient_of_a_first_tile_that_sees_few_keys_whole(d, hq, hkv, lq, lk):
+    # two key tiles, but only one to 64 keys that every row of the query tile sees
+    full_check("bf16", d, hq, hkv, [lq], [lk], scale=0.3, seed=lq + d)
+
+
 def test_two_calls_at_once():
     # two layers' calls on two streams, a workspace each, beside each other: bit for bit what they are alone
     cases = [("bf16", 128, 8, 2, [900, 700]), ("bf16", 64, 4, 4, [1500])]
