@@ -488,6 +488,9 @@ HLA_API int hla_attention(const hla_attn_params* params, const void* q, const vo
  * dq [total_q, Hq, d], dk, dv [total_k, Hkv, d] (a kv head's sums over the
  * query heads that read it), in params->dtype from fp32 sums.  Keys that no
  * row sees have gradients 0; rows at and past c_n are left as they were.
+ * bf16 layers: P and dS rounded to bf16 for their products; dq and dk where
+ * dS nearly cancels are not left with the rounding of `out` (dq to about
+ * 4 x 2^-8 of its size).
  * Infinities and NaN of keys do not reach dq of rows before them; those of a
  * row's dout and q may reach dk and dv of keys up to 127 after it in its own
  * sequence (bf16 layers).  Outputs must not overlap inputs or each other.

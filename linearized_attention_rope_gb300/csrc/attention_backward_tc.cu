@@ -27,16 +27,17 @@
 // D of the stored output carries that output's rounding, which moves all of a row's dS the same way.  Where those nearly
 // cancel it is all that is left: one key that takes almost all of a row (O is then that key's value), values with a common
 // part (O as large as they are, while dP - D is not).  The dq kernel, which runs first, therefore sums D = sum_j P_ij dP_ij
-// as well, and leaves it for dk and dv.  Rows that see one key tile take it for dQ at once.  In query tiles of more keys the
-// difference of the two, which is the sum of a row's dS, is taken out of dQ as if all keys were the mean of 64 that every
-// row sees, so that what keys have in common cancels as it does with dS that add up to 0.  What is left is the difference
-// times how far that mean is from the row's own weighted mean of the keys, about their spread times sqrt(1 / 64 + sum P^2);
-// query tiles in which that is more than 16 u (u = 2^-8, bf16's) of a row's dQ are listed and done again with the better D.
+// as well, and leaves it for dk and dv.  Rows that see one key tile take it for dQ at once.  For query tiles of more keys:
+//   - the difference of the two, which is the sum of a row's dS, is taken out of dQ as if all keys were the mean of 64 that
+//     every row sees (as much of it as stands out from its standard error), so that what keys have in common cancels as it
+//     does with dS that add up to 0; not for rows of a few keys (sum P^2 of 1/16 and more), whose own may be far from it;
+//   - what is left in dQ is the difference times how far that is from the row's weighted mean of the keys, about their
+//     spread times sqrt(1 / 64 + sum P^2).  Tiles in which it adds up, over the 32 rows of a warp, to more than 4 u (u = 2^-8,
+//     bf16's) of their dQ, in 2-norms, are listed and done again with the better D.
 // (With the stored output alone, dq of rows with P = 1 - 2^-10 was off by 1.2 times its size, that of keys and values
-// shifted by 4 by 0.1 to 0.2; now 0.003 to 0.005 and 0.006 to 0.009.  4096 tokens, 32/8 heads of 128: 340 -> 358 us, 362 with
-// values and keys shifted by 1, 498 by 4, where 6 of 10 tiles are done again; 4 x 4096, heads of 64: 930 -> 1060.  Every
-// tile again where the difference exceeds 4 u of the 2-norm of dS: 354, 530, 531 and 1047, and values shifted by 0.1 are enough
-// for a third of the tiles.)
+// shifted by 4 by 0.1 to 0.2; now 0.003 to 0.005 and 0.006 to 0.009.  4096 tokens, 32/8 heads of 128: 340 -> 360 us, 361 to 367
+// with queries 8 times as long or values and keys shifted by 0.3, 404 where one long tile is done again, 530 where all
+// are; 32768 tokens shifted by 1, where 8 of 10 are, 18.5 -> 27.1 ms; 4 x 4096, heads of 64: 930 -> 1073.)
 //
 // Products and elementwise work alternate: while dV and the next S are formed,
 // dS is computed from dP; while dK and the next dP are formed, the next P.
@@ -104,7 +105,7 @@ template <int D> struct Cfg {
     static constexpr int kSlots = D == 128 ? 5 : 8;
     // two fixed tiles (K, V or Q, dO), the ring, two stages of row stats (-lse, then -D; 128 fp32 each), barriers
     static constexpr uint32_t kFix = 0, kRing = 2 * kTile, kStat = kRing + kSlots * kTile, kBar = kStat + 2048;
-    static constexpr uint32_t kItem = kBar + 352, kMean = kItem + 80, kSmem = kMean + D * 4 + 32;  // kMean: a key and 8 sums, fp32
+    static constexpr uint32_t kItem = kBar + 352, kMean = kItem + 80, kSmem = kMean + D * 4 + 64;  // kMean: a key and 16 sums, fp32
     static_assert(sizeof(ItemRing) <= 80 && kSmem <= 227 * 1024, "shared memory layout");
     static constexpr uint32_t kCols = 512;
 };
@@ -580,8 +581,15 @@ __device__ __forceinline__ float sum4(const float2 (&x)[4]) {
 __device__ __forceinline__ float2 pair(uint32_t w) {  // of bf16
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-constexpr float kApart = 0x1p-8f;  // (16 u)^2
+constexpr float kApart = 0x1p-12f;  // (4 u)^2
 constexpr int kSample = 64;        // keys
+constexpr float kEven = 0x1p-4f;   // sum of P^2 of rows whose keys are many
+// The part of a mean c of kSample values, whose squared differences from it add up to v, that is more than two standard
+// errors: c (1 - 4 v / (kSample c)^2), 0 if that is negative.
+__device__ __forceinline__ float beyond(float c, float v) {
+    const float x = kSample * c, r = 4.f * v;
+    return x * x > r ? c - r / x / kSample : 0.f;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kBlock, 1)
@@ -913,12 +921,12 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                 store64(tP, d, n == 1);
                 named_arrive(kBarDs + (t & 1), 288);
             }
-            float off = 0.f, far = 0.f;  // sum of the row's dS; square of what the mean key may be off as their weighted mean
+            // sum of the row's dS; as much of it as is taken out by the mean key; square of what is left of the keys
+            float off = 0.f, even = 0.f, far = 0.f;
             if (n > 1 && !second) {      // D for dk and dv, and what of dQ goes with a wrong one
                 halves[half * 128 + row] = sum4(sum);
                 halves[256 + half * 128 + row] = sum4(pp);
                 float2 c = make_float2(0.f, 0.f);
-                float spread = 0.f;
 #pragma unroll
                 for (int y = 0; y < kShare; ++y) c = fadd2(c, pair(common[y]));
 #pragma unroll
@@ -927,22 +935,48 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                     c.y += __shfl_xor_sync(0xffffffffu, c.y, y);
                 }
                 c = make_float2(c.x / kSample, c.y / kSample);
+                float2 v = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < kShare; ++y) {
                     const float2 x = pair(common[y]);
-                    spread += (x.x - c.x) * (x.x - c.x) + (x.y - c.y) * (x.y - c.y);
+                    v.x += (x.x - c.x) * (x.x - c.x);
+                    v.y += (x.y - c.y) * (x.y - c.y);
                 }
+                float spread = v.x + v.y;
 #pragma unroll
-                for (int y = 16; y; y >>= 1) spread += __shfl_xor_sync(0xffffffffu, spread, y);
-                if (tid % kShares == 0) *reinterpret_cast<float2*>(mean + tid / kShares * 2) = c;
-                if (lane == 0) mean[D + warp] = spread;
+                for (int y = 1; y < kShares; y *= 2) {
+                    v.x += __shfl_xor_sync(0xffffffffu, v.x, y);
+                    v.y += __shfl_xor_sync(0xffffffffu, v.y, y);
+                }
+                // of the mean, what stands out from its standard error (one large key does not make a mean)
+                const float2 m = make_float2(beyond(c.x, v.x), beyond(c.y, v.y));
+                float rest = (c.x - m.x) * (c.x - m.x) + (c.y - m.y) * (c.y - m.y), whole = c.x * c.x + c.y * c.y;
+#pragma unroll
+                for (int y = 16; y; y >>= 1) {
+                    spread += __shfl_xor_sync(0xffffffffu, spread, y);
+                    rest += __shfl_xor_sync(0xffffffffu, rest, y);
+                    whole += __shfl_xor_sync(0xffffffffu, whole, y);
+                }
+                if (tid % kShares == 0) *reinterpret_cast<float2*>(mean + tid / kShares * 2) = m;
+                if (lane == 0) {
+                    mean[D + warp] = spread;
+                    mean[D + 8 + warp] = __uint_as_float(pack_bf2(rest, whole));
+                }
                 named_sync(kBarRow, 256);
                 const float D_row = halves[row] + halves[128 + row];
                 off = D_row + st.y;
-                spread = 0.f;
+                spread = rest = whole = 0.f;
 #pragma unroll
-                for (int y = 0; y < 8; ++y) spread += mean[D + y];
-                far = spread / (2 * kSample) * (1.f / kSample + halves[256 + row] + halves[384 + row]);  // (of half the columns)
+                for (int y = 0; y < 8; ++y) {
+                    spread += mean[D + y];
+                    const float2 two = pair(__float_as_uint(mean[D + 8 + y]));
+                    rest += two.x;
+                    whole += two.y;
+                }
+                // Rows of a few keys may have nothing of the mean in some column: they keep dQ as it is.  (Of half the columns.)
+                const float squares = halves[256 + row] + halves[384 + row];
+                even = squares < kEven ? off : 0.f;
+                far = 0.5f * (spread / kSample * (1.f / kSample + squares) + (squares < kEven ? rest : whole) / kShares);
                 if (half == 0 && at >= 0) stats[at].y = -D_row;
             }
             if (n > 0) ok = ok && wait_or_flag(bar_done, count & 1, err);
@@ -971,10 +1005,10 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             const float4 c = *reinterpret_cast<const float4*>(mean + half * (D / 2) + 32 * b + e);
-                            o[e] = fmaf(-off, c.x, o[e]);
-                            o[e + 1] = fmaf(-off, c.y, o[e + 1]);
-                            o[e + 2] = fmaf(-off, c.z, o[e + 2]);
-                            o[e + 3] = fmaf(-off, c.w, o[e + 3]);
+                            o[e] = fmaf(-even, c.x, o[e]);
+                            o[e + 1] = fmaf(-even, c.y, o[e + 1]);
+                            o[e + 2] = fmaf(-even, c.z, o[e + 2]);
+                            o[e + 3] = fmaf(-even, c.w, o[e + 3]);
                             norm += (o[e] * o[e] + o[e + 1] * o[e + 1]) + (o[e + 2] * o[e + 2] + o[e + 3] * o[e + 3]);
                         }
 #pragma unroll
@@ -984,11 +1018,22 @@ attn_dq_tc_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ CU
                                        pack_bf2(o[e + 4] * m, o[e + 5] * m), pack_bf2(o[e + 6] * m, o[e + 7] * m));
                 }
             }
-            // the tile again where a row may be off by more
-            const bool apart = few ? off != 0.f : off * off * far > kApart * norm;
-            if (n > 1 && !second && __any_sync(0xffffffffu, at >= 0 && apart) && lane == 0 &&
-                atomicExch(noted, number + 1) != number + 1)
-                again[1 + atomicAdd(again, 1)] = number;
+            // the tile again where a warp's rows may be off by more
+            if (n > 1 && !second) {
+                float wrong = at >= 0 ? off * off * far : 0.f;
+                norm = at >= 0 ? norm : 0.f;
+                if (few) {  // (any difference will do)
+                    wrong = at >= 0 ? off * off : 0.f;
+                    norm = 0.f;
+                }
+#pragma unroll
+                for (int y = 16; y; y >>= 1) {
+                    wrong += __shfl_xor_sync(0xffffffffu, wrong, y);
+                    norm += __shfl_xor_sync(0xffffffffu, norm, y);
+                }
+                if (wrong > kApart * norm && lane == 0 && atomicExch(noted, number + 1) != number + 1)
+                    again[1 + atomicAdd(again, 1)] = number;
+            }
         }
     }
     umma::fence_before_sync();
