@@ -42,10 +42,10 @@
 // Products and elementwise work alternate: while dV and the next S are formed,
 // dS is computed from dP; while dK and the next dP are formed, the next P.
 //
-// Bound by the tensor cores: 14 d flops per visible score.  bf16, 32/8 heads of
-// 128: 32768 tokens in 18.1 to 18.5 ms (1670 to 1700 TFLOP/s of the 14 d, 1190 to
-// 1210 of the 10 d that the formulas need), 4096 in 340 us: rows' statistics 16, dq 150 (tensor pipe active
-// 59 %), dk and dv 170 (70 %).  4 x 4096 tokens, 32/8 heads of 64: 920 us.
+// 14 d flops per visible score.  Long sequences are bound by the tensor cores: bf16, 32/8 heads of 128, 32768 tokens in 18.7 to
+// 19.0 ms (1620 to 1650 TFLOP/s of the 14 d, 1160 to 1180 of the 10 d that the formulas need).  4096 in 360 us: rows'
+// statistics 16, dq 174 (tensor pipe active 52 %), dk and dv 177 (68 %); 4 x 4096 tokens, 32/8 heads of 64, 1073 us (29
+// and 42 %, 1.6 and 1.3 instructions of 4 a cycle), where neither is the limit; what is has not been measured.
 #include "attention_tc.cuh"
 
 namespace hla {

@@ -1,11 +1,11 @@
 // Decode step of a full softmax layer: one query token per sequence over the
 // paged cache.  See attention_decode.cuh for the cut over blocks.
 //
-// Bound by the cache's bytes.  32/8 heads of 128: 64 sequences of 8192 tokens of
-// 8-bit rows in 173 us (6.2 TB/s), of bf16 rows in 301 us (7.1), 8 of fp32 rows in
-// 129 us; one sequence of 131072 in 50 us (8-bit) and 83 us (bf16).  8-bit rows
-// take two conversions per four values on the way to the products, which is
-// what keeps them behind bf16's rate.  The join takes 7 to 8 us of these.
+// bf16 layers are bound by the cache's bytes.  32/8 heads of 128: 64 sequences of 8192 tokens of 8-bit rows in 182 us
+// (5.9 TB/s; heads of 64 122 us, 4.5), of bf16 rows in 305 us (7.0); one sequence of 131072 in 55 us (8-bit) and 86 us
+// (bf16).  8-bit rows take two conversions per four values on the way to the products, which is what keeps them behind
+// bf16's rate.  The join takes 7 to 8 us of these.  fp32 layers wait at four barriers per 64 keys with nothing on its way
+// across them: 8 x 8192 tokens of fp32 rows 132 us (4.1 TB/s), of 8-bit rows, whose conversions come on top, 209 us (0.65).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -261,10 +261,10 @@ decode_f32_kernel(AttnDims A, CacheDims C, hla_cache c, const float* __restrict_
 // within kLike of each other.  But a key whose value row is large in one column sets Mt
 // for all of them, and the weights that this leaves too few bits may be all that the
 // other columns have: a warp whose rows differ by more goes over them again, kBand powers
-// of two of weights at a time (64 x 8192 tokens 191 -> 362 us, most of it read from L2).
+// of two of weights at a time (64 x 8192 tokens 182 -> 348 us, part of it read from L2).
 // (Always exact, by values and two-part weights in bf16, to which no instruction
-// converts: 64 x 8192 tokens 185 -> 273 us; light weights looked for one by one:
-// 223, for want of registers.)  bf16 caches: products in bf16,
+// converts: 64 x 8192 tokens, timed one by one, 186 -> 273 us, where this takes 191; light weights looked for
+// one by one: 223, for want of registers.)  bf16 caches: products in bf16,
 // weights in two bf16 parts (with one, outputs of a few heads were off by up to
 // 1.5 times the rounding of the result; the second costs nothing beside the loads).
 //
