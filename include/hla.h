@@ -574,6 +574,159 @@ HLA_API int hla_attention_decode(const hla_attn_params* params, const hla_cache_
 /* As hla_check_device_error, for a cache's error word. */
 HLA_API int hla_check_cache_error(const hla_cache* cache, void* stream, int32_t* code);
 
+/* ---------------------------------------------------------------------------
+ * What stands around a layer's mixing: the norm in front of it (or of its
+ * heads) with the residual's addition, the frozen projections in 4 bits, and a
+ * gated linear recurrence as the mixing of layers that keep a vector of state.
+ * ------------------------------------------------------------------------- */
+
+/* Root-mean-square norm of rows of n_cols values, n_heads of them per token (1:
+ * the hidden rows; more: every head of q or k).  dtype of x, residual, weight,
+ * sum; out_dtype: dtype, or HLA_DTYPE_E4M3 (8-bit floats with one power of two
+ * per `group` values: 32, 128 (n_cols a multiple of it) or 0, the whole row
+ * (n_cols a multiple of 16); then x, residual, weight, sum start on 16 bytes and
+ * the strides are multiples of 16 bytes).  offset: added to the weight (some
+ * backbones keep weight - 1).  x_stride, residual_stride: elements from a token
+ * to the next (0: dense; otherwise at least n_heads * n_cols).  Outputs are
+ * dense.  n_cols up to 2^20. */
+typedef struct hla_norm_params {
+    int n_cols;
+    int n_heads;
+    int dtype;
+    int out_dtype;
+    int group;
+    float eps;
+    float offset;
+    int reserved; /* 0 */
+    int64_t x_stride;
+    int64_t residual_stride;
+} hla_norm_params;
+
+/* s = x + residual, rounded to dtype; out = s / sqrt(mean(s^2) + eps) * (offset +
+ * weight), from fp32 sums.
+ *   x, residual [tokens, n_heads, n_cols]   residual may be NULL (s = x)
+ *   weight [n_cols]          NULL: out = s / sqrt(mean(s^2) + eps)
+ *   out [tokens, n_heads, n_cols]           out_dtype
+ *   exp uint8 [tokens, n_heads, n_cols / group] (1 for group 0; E4M3, else NULL):
+ *       a value is its 8-bit float times 2^(byte - 127), the smallest power that
+ *       keeps the group's finite values within 448 (infinities become the
+ *       largest, NaN stays NaN)
+ *   sum [tokens, n_heads, n_cols]           s; needed with a residual, else NULL
+ * sum (or out, of type dtype) may be x or the residual itself where that is dense;
+ * outputs must not overlap anything in another way.  Asynchronous;
+ * deterministic. */
+HLA_API int hla_rms_norm(const hla_norm_params* params, const void* x, const void* residual, const void* weight,
+                         int64_t tokens, void* out, uint8_t* exp, void* sum, void* stream);
+
+/* Workspace bytes of hla_rms_norm_backward with a weight (no error word; it
+ * grows with n_cols alone). */
+HLA_API int hla_rms_norm_backward_workspace_bytes(const hla_norm_params* params, size_t* bytes);
+
+/* Gradients of sum(dout . out) (+ sum(dsum . sum), dsum may be NULL) with respect
+ * to s (the gradient of x and of the residual alike) and the weight: s is
+ * hla_rms_norm's `sum` (or x, without a residual; x_stride applies), dout, dsum
+ * and dx [tokens, n_heads, n_cols] dense in dtype, dweight fp32 [n_cols] (NULL:
+ * not wanted; it needs the weight).  Of 8-bit outputs, dout is the gradient of the
+ * values that they stand for.  dx may be dout or dsum.  ws may be NULL without
+ * dweight.  Asynchronous; deterministic. */
+HLA_API int hla_rms_norm_backward(const hla_norm_params* params, const void* s, const void* weight, const void* dout,
+                                  const void* dsum, int64_t tokens, void* dx, float* dweight, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t of n_channels values,
+ * states in fp32.  gate_dim: channels in a row that share a gate (1, or 64 or 128
+ * of a head; n_channels a multiple of it).  dtype of x and out (and their
+ * gradients), gate_dtype of g: F32 or BF16 each.  x_stride, g_stride: elements
+ * from a token to the next (0: dense; otherwise at least n_channels, n_channels /
+ * gate_dim).  out, dout and the gradients are dense. */
+typedef struct hla_recurrence_params {
+    int n_channels;
+    int gate_dim;
+    int dtype;
+    int gate_dtype;
+    int64_t x_stride;
+    int64_t g_stride;
+} hla_recurrence_params;
+
+/* Workspace bytes of hla_recurrence and hla_recurrence_backward; that of the
+ * largest call serves every smaller one of the same params.  The first 16 bytes
+ * are the error word, as in hla_attention_workspace_bytes.  Two calls that may
+ * run at the same time need a workspace each. */
+HLA_API int hla_recurrence_workspace_bytes(const hla_recurrence_params* params, int64_t total_tokens, size_t* bytes);
+
+/* The recurrence over n_seqs packed sequences (cu_seqlens as for hla_attention).
+ *   g [total, n_channels / gate_dim]   the logarithms of the gates (0 or less in a
+ *                      layer that forgets; -infinity: the state starts anew)
+ *   x [total, n_channels]
+ *   h0 fp32 [n_seqs, n_channels]       the states in front; NULL: zeros
+ *   out [total, n_channels]            h_t, rounded to dtype
+ *   h_last fp32 [n_seqs, n_channels]   the states behind each sequence's last row (h0
+ *                      of a sequence without rows); may be NULL, may be h0 itself
+ *   states fp32 [ceil(total / 64), n_channels]: for hla_recurrence_backward, the
+ *                      state in front of every 64th row; may be NULL
+ * An infinity or NaN makes later rows of its own channel and sequence NaN or
+ * infinite, and no others (of a gate that channels share: of those channels).
+ * Rows at and past c_n are left as they were.  A malformed table is clamped on
+ * the device and flagged in the workspace's error word; rows whose place it
+ * leaves open are undefined.  Outputs must not overlap inputs otherwise.
+ * Asynchronous; deterministic. */
+HLA_API int hla_recurrence(const hla_recurrence_params* params, const void* g, const void* x, const float* h0,
+                           const int32_t* cu_seqlens, int n_seqs, int64_t total_tokens, void* out, float* h_last,
+                           float* states, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of sum(dout . h) + sum(dh_last . h_last) (h before its rounding to
+ * dtype; dh_last may be NULL) with respect to g (dg, gate_dtype: sums over the
+ * channels that share a gate), x (dx) and h0 (dh0 fp32, may be NULL; may be
+ * dh_last itself), from the inputs and the states that hla_recurrence kept.
+ * Asynchronous; deterministic. */
+HLA_API int hla_recurrence_backward(const hla_recurrence_params* params, const void* g, const void* x, const float* h0,
+                                    const float* states, const int32_t* cu_seqlens, int n_seqs, int64_t total_tokens,
+                                    const void* dout, const float* dh_last, void* dg, void* dx, float* dh0, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* One token per sequence: h [n_seqs, n_channels] fp32 becomes exp(g) h + x, and
+ * out [n_seqs, n_channels] is h rounded to dtype.  g, x as above, one row per
+ * sequence.  Asynchronous. */
+HLA_API int hla_recurrence_step(const hla_recurrence_params* params, const void* g, const void* x, float* h, int n_seqs,
+                                void* out, void* stream);
+
+/* Products with frozen weights in 4 bits.  W [n_out, n_in]: W[n][k] = scale (q - 8)
+ * + offset, q in 0 .. 15, with a scale (and offset) per row n and group of inputs.
+ * group: 32, 64 or 128; n_in a multiple of it.  dtype of out, scales, offsets.
+ * x_dtype: dtype, or HLA_DTYPE_E4M3 with a power of two per x_group inputs (32,
+ * 128 or 0, the whole row), as hla_rms_norm writes them.  x_stride: elements from
+ * a token to the next (0: dense; otherwise at least n_in). */
+typedef struct hla_linear4_params {
+    int n_in;
+    int n_out;
+    int group;
+    int dtype;
+    int x_dtype;
+    int x_group;
+    int64_t x_stride;
+} hla_linear4_params;
+
+/* Workspace bytes of hla_linear4 (no error word; may be 0, and grows with
+ * tokens).  Two calls that may run at the same time need one each. */
+HLA_API int hla_linear4_workspace_bytes(const hla_linear4_params* params, int64_t tokens, size_t* bytes);
+
+/* out [tokens, n_out] = x W^T, from fp32 sums.
+ *   x [tokens, n_in], x_exp uint8 [tokens, n_in / x_group] (E4M3, else NULL)
+ *   w uint8 [n_out, n_in / 2]: inputs 2i (low half) and 2i + 1
+ *   scales, offsets [n_out, n_in / group]   offsets may be NULL (0)
+ * Meant for the tokens of a decode step: the weights are read once per 64 tokens.
+ * Asynchronous; deterministic. */
+HLA_API int hla_linear4(const hla_linear4_params* params, const void* x, const uint8_t* x_exp, const uint8_t* w,
+                        const void* scales, const void* offsets, int64_t tokens, void* out, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Weights [n_out, n_in] (dtype, dense, finite) to 4 bits.  offsets NULL: scale =
+ * max |w| / 7 of the group, q = 1 .. 15; else scale = (max - min) / 15, offset =
+ * min + 8 scale, q = 0 .. 15; scale and offset rounded to dtype, then q to the
+ * nearest.  Asynchronous. */
+HLA_API int hla_linear4_quantize(const hla_linear4_params* params, const void* weight, uint8_t* w, void* scales,
+                                 void* offsets, void* stream);
+
 /* Synchronises `stream`, reads the state's device error word into *code
  * (may be NULL), clears it, and returns HLA_OK if it was zero, else the
  * matching HLA_ERR_* status. */

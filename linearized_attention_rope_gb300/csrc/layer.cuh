@@ -1,0 +1,71 @@
+// Shared definitions of what stands around a layer's mixing: root-mean-square
+// norms, the gated recurrence, products with 4-bit weights.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "hla_common.cuh"
+
+namespace hla {
+
+template <typename T, int V> struct alignas(V * sizeof(T)) Piece { T x[V]; };
+
+// Groups of values as 8-bit floats (e4m3) times a power of two, as the cache
+// keeps its rows: the smallest e >= -127 with top <= 448 2^e (top finite, >= 0).
+__device__ __forceinline__ int group_exponent(float top) {
+    const uint32_t b = __float_as_uint(top);
+    return max((int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u), -127);
+}
+__device__ __forceinline__ float group_pow2(int e) {  // -127 <= e <= 127
+    return e > -127 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(0x400000u);
+}
+
+struct NormDims {
+    int64_t rows, sx, sr;  // rows of n_cols values; token strides of x and the residual
+    int cols, heads, group;
+    float eps, offset;
+};
+// out8: 8-bit rows with exponents exp (else out); residual, sum, weight may be null.
+template <typename T>
+cudaError_t launch_norm(const NormDims& N, const T* x, const T* residual, const T* weight, T* out, uint8_t* out8,
+                        uint8_t* exp, T* sum, cudaStream_t st);
+// part: fp32 [norm_parts(cols)][cols]
+template <typename T>
+cudaError_t launch_norm_backward(const NormDims& N, const T* s, const T* weight, const T* dout, const T* dsum, T* dx,
+                                 float* dweight, float* part, cudaStream_t st);
+constexpr int kNormParts = 1024;  // blocks of a norm's gradient, at most
+
+// The gated recurrence.  Gates: one per channel (gate_dim 1) or per gate_dim (64, 128) channels.
+constexpr int kStateRows = 64;  // rows between the states that a gradient starts from
+struct RecDims {
+    int64_t total, sx, sg;  // rows; token strides of x and g
+    int channels, gate_dim, n_seqs;
+};
+// Bytes of carries between tiles (0: one tile in time, or none), for both directions.
+size_t recurrence_carry_bytes(const RecDims& R, bool f32);
+template <typename T, typename G>
+cudaError_t launch_recurrence(const RecDims& R, const G* g, const T* x, const float* h0, const int32_t* cu, T* out,
+                              float* h_last, float* states, char* carry, int32_t* err, cudaStream_t st);
+template <typename T, typename G>
+cudaError_t launch_recurrence_backward(const RecDims& R, const G* g, const T* x, const float* h0, const float* states,
+                                       const int32_t* cu, const T* dout, const float* dh_last, G* dg, T* dx,
+                                       float* dh0, char* carry, int32_t* err, cudaStream_t st);
+template <typename T, typename G>
+cudaError_t launch_recurrence_step(const RecDims& R, const G* g, const T* x, float* h, T* out, cudaStream_t st);
+
+// Products with 4-bit weights: w [n_out][n_in / 2] bytes, the even input in the low half; scales and offsets
+// [n_out][n_in / group].  Rows of x as bf16 parts in `parts` where they are not bf16 on 16-byte boundaries.
+struct Linear4Dims {
+    int64_t rows, sx;  // tokens; token stride of x in elements
+    int n_in, n_out, group, x_group;
+};
+enum class Rows4 { kF32, kBf16, kE4m3 };
+int linear4_parts(Rows4 kind);
+template <typename T>
+cudaError_t launch_linear4(const Linear4Dims& L, Rows4 kind, const void* x, const uint8_t* x_exp, const uint8_t* w,
+                           const T* scales, const T* offsets, T* out, __nv_bfloat16* parts, cudaStream_t st);
+template <typename T>
+cudaError_t launch_linear4_quantize(const Linear4Dims& L, const T* weight, uint8_t* w, T* scales, T* offsets,
+                                    cudaStream_t st);
+
+}  // namespace hla

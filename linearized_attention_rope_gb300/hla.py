@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 from dataclasses import dataclass
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -87,6 +88,23 @@ class CCacheParams(ctypes.Structure):
                 ("max_pages", ctypes.c_int), ("reserved", ctypes.c_int)]
 
 
+class CNormParams(ctypes.Structure):
+    _fields_ = [("n_cols", ctypes.c_int), ("n_heads", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("out_dtype", ctypes.c_int), ("group", ctypes.c_int), ("eps", ctypes.c_float),
+                ("offset", ctypes.c_float), ("reserved", ctypes.c_int), ("x_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64)]
+
+
+class CRecurrenceParams(ctypes.Structure):
+    _fields_ = [("n_channels", ctypes.c_int), ("gate_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("gate_dtype", ctypes.c_int), ("x_stride", ctypes.c_int64), ("g_stride", ctypes.c_int64)]
+
+
+class CLinear4Params(ctypes.Structure):
+    _fields_ = [("n_in", ctypes.c_int), ("n_out", ctypes.c_int), ("group", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("x_dtype", ctypes.c_int), ("x_group", ctypes.c_int), ("x_stride", ctypes.c_int64)]
+
+
 class CCache(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("k", "v", "k_exp", "v_exp", "page_table", "err")]
 
@@ -138,6 +156,7 @@ def load():
         lib.hla_prefill_noalloc_check_error.restype = ctypes.c_int
         RP, AP, CP = (ctypes.POINTER(t) for t in (CRopeParams, CAttnParams, CCacheParams))
         C, i64, size_p = ctypes.POINTER(CCache), ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)
+        NP, GP, WP = (ctypes.POINTER(t) for t in (CNormParams, CRecurrenceParams, CLinear4Params))
         for name, args in {
                 "hla_rope_frequencies": [RP, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)],
                 "hla_rope": [RP, _vp, _vp, _vp, i64, _vp, _vp, _vp],
@@ -151,7 +170,17 @@ def load():
                 "hla_cache_read": [CP, C, _vp, _vp, ctypes.c_int, i64, _vp, _vp, _vp],
                 "hla_attention_decode_workspace_bytes": [AP, CP, size_p],
                 "hla_attention_decode": [AP, CP, C, _vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp],
-                "hla_check_cache_error": [C, _vp, ctypes.POINTER(ctypes.c_int32)]}.items():
+                "hla_check_cache_error": [C, _vp, ctypes.POINTER(ctypes.c_int32)],
+                "hla_rms_norm": [NP, _vp, _vp, _vp, i64, _vp, _vp, _vp, _vp],
+                "hla_rms_norm_backward_workspace_bytes": [NP, size_p],
+                "hla_rms_norm_backward": [NP, _vp, _vp, _vp, _vp, i64, _vp, _vp, _vp, ctypes.c_size_t, _vp],
+                "hla_recurrence_workspace_bytes": [GP, i64, size_p],
+                "hla_recurrence": [GP] + [_vp] * 4 + [ctypes.c_int, i64] + [_vp] * 4 + [ctypes.c_size_t, _vp],
+                "hla_recurrence_backward": [GP] + [_vp] * 5 + [ctypes.c_int, i64] + [_vp] * 6 + [ctypes.c_size_t, _vp],
+                "hla_recurrence_step": [GP, _vp, _vp, _vp, ctypes.c_int, _vp, _vp],
+                "hla_linear4_workspace_bytes": [WP, i64, size_p],
+                "hla_linear4": [WP] + [_vp] * 5 + [i64, _vp, _vp, ctypes.c_size_t, _vp],
+                "hla_linear4_quantize": [WP] + [_vp] * 5}.items():
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ctypes.c_int
         for fn in ("hla_state_bytes", "hla_prefill_workspace_bytes", "hla_state_init", "hla_prefill",
@@ -812,3 +841,356 @@ def attention_decode(params: AttnParams, cache: Cache, q, lens, out=None, ws=Non
     _check(load().hla_attention_decode(_c(params, stride), cache.cp, cache.c, _adr(q), _adr(lens), cache.n_seqs,
                                        _adr(out), _adr(ws), ws.numel(), st), fn)
     return out
+
+
+# ---- around the mixing: norms, the gated recurrence, products with 4-bit weights ------------------------
+
+
+def _check_matrix(t, fn: str, name: str, dtype, shape, device) -> int:
+    """The row stride of t in elements, as _check_tensor takes strided rows, for [rows, columns] as well."""
+    if len(shape) == 3:
+        return _check_tensor(t, fn, name, dtype, shape, device, strided=True)
+    if isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype == dtype and t.device == device and t.shape == shape and \
+            t.stride(1) == 1 and t.stride(0) >= shape[1] and shape[0] > 1:
+        return t.stride(0)
+    _check_tensor(t, fn, name, dtype, shape, device)
+    return shape[1]
+
+
+def _sized(t, fn: str, name: str, *dims):
+    """Refuses what is no tensor of one of the numbers of dimensions given."""
+    _need(isinstance(t, torch.Tensor) and t.dim() in dims, f"{fn}: {name}: expected a tensor of {dims} dimensions")
+
+
+def _dense(t, stride: int):
+    """An uninitialised dense tensor of t's shape; stride: t's, from _check_matrix."""
+    if stride == t.stride(0) and t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _bytes(fn: str, params, *sizes) -> int:
+    n = ctypes.c_size_t()
+    _check(getattr(load(), fn)(_c(params), *sizes, ctypes.byref(n)), fn)
+    return n.value
+
+
+@dataclass(frozen=True)
+class NormParams:
+    n_cols: int
+    n_heads: int = 1            # rows of n_cols per token: 1, or the heads of q or k
+    dtype: int = DTYPE_BF16
+    out_dtype: int = -1         # -1: dtype; DTYPE_E4M3: 8-bit floats with a power of two per group
+    group: int = 0              # E4M3: 32, 128, or 0 (the whole row)
+    eps: float = 1e-6
+    offset: float = 0.0         # added to the weight
+
+    def c(self, x_stride: int = 0, residual_stride: int = 0) -> CNormParams:
+        return CNormParams(self.n_cols, self.n_heads, self.dtype, self.dtype if self.out_dtype < 0 else self.out_dtype,
+                           self.group, self.eps, self.offset, 0, x_stride, residual_stride)
+
+
+class Normed(NamedTuple):
+    """out, exp (the exponents of 8-bit rows, else None), sum (x + residual; None without a residual)."""
+    out: torch.Tensor
+    exp: Optional[torch.Tensor]
+    sum: Optional[torch.Tensor]
+
+
+def _norm_rows(params: NormParams, fn: str, x, name: str):
+    """Checks the rows x: [T, n_cols], or [T, n_heads, n_cols] for more heads than one."""
+    dt = _TORCH.get(params.dtype)
+    _need(dt is not None and dt != torch.uint8, f"{fn}: dtype")
+    _sized(x, fn, name, 2 if params.n_heads == 1 else 3)
+    shape = (x.shape[0], params.n_cols) if params.n_heads == 1 else (x.shape[0], params.n_heads, params.n_cols)
+    return dt, shape, _check_matrix(x, fn, name, dt, shape, x.device)
+
+
+def rms_norm(params: NormParams, x, weight=None, residual=None, out=None, exp=None, sum=None, stream=None) -> Normed:
+    """hla_rms_norm: x (and residual) [T, n_cols], or [T, n_heads, n_cols], where tokens may be slices of a wider tensor;
+    weight [n_cols].  The sum may be written over x or the residual (sum=residual), out over x, where those are
+    dense."""
+    fn, eight = "hla_rms_norm", params.out_dtype == DTYPE_E4M3
+    dt, shape, xs = _norm_rows(params, fn, x, "x")
+    dev, rs = x.device, 0
+    if weight is not None:
+        _check_tensor(weight, fn, "weight", dt, (params.n_cols,), dev)
+    if residual is not None:
+        rs = _check_matrix(residual, fn, "residual", dt, shape, dev)
+        if sum is not None:
+            _check_tensor(sum, fn, "sum", dt, shape, dev)
+    else:
+        _need(sum is None, f"{fn}: sum without residual")
+    if out is not None:
+        _check_tensor(out, fn, "out", torch.uint8 if eight else dt, shape, dev)
+    groups = shape[:-1] + (params.n_cols // params.group if params.group else 1,) if eight else None
+    if exp is not None:
+        _need(eight, f"{fn}: exponents go with 8-bit rows")
+        _check_tensor(exp, fn, "exp", torch.uint8, groups, dev)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream, x, weight, residual, out, exp, sum):
+            return rms_norm(params, x, weight, residual, out, exp, sum)
+    if residual is not None and sum is None:
+        sum = _dense(x, xs)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.uint8, device=dev) if eight else _dense(x, xs)
+    if eight and exp is None:
+        exp = torch.empty(groups, dtype=torch.uint8, device=dev)
+    _check(load().hla_rms_norm(_c(params, xs, rs), _adr(x), _adr(residual), _adr(weight), shape[0], _adr(out), _adr(exp),
+                               _adr(sum), st), fn)
+    return Normed(out, exp, sum)
+
+
+def norm_workspace_bytes(params: NormParams) -> int:
+    return _bytes("hla_rms_norm_backward_workspace_bytes", params)
+
+
+def alloc_norm_workspace(params: NormParams, device="cuda"):
+    """A workspace for rms_norm_backward."""
+    return torch.empty(norm_workspace_bytes(params), dtype=torch.uint8, device=device)
+
+
+def rms_norm_backward(params: NormParams, s, dout, weight=None, dsum=None, dx=None, dweight=None, ws=None, stream=None):
+    """hla_rms_norm_backward: (dx, dweight) from s (rms_norm's sum, or its x without a residual), dout and, where the sum
+    is used further, its gradient dsum.  dx is the gradient of x and of the residual; dweight [n_cols] fp32, None
+    without a weight.  dx may be dout or dsum."""
+    fn = "hla_rms_norm_backward"
+    dt, shape, xs = _norm_rows(params, fn, s, "s")
+    dev = s.device
+    for t, name in ((dout, "dout"), (dsum, "dsum"), (dx, "dx")):
+        if t is not None or name == "dout":
+            _check_tensor(t, fn, name, dt, shape, dev)
+    if weight is not None:
+        _check_tensor(weight, fn, "weight", dt, (params.n_cols,), dev)
+    if dweight is not None:
+        _need(weight is not None, f"{fn}: dweight without weight")
+        _check_tensor(dweight, fn, "dweight", torch.float32, (params.n_cols,), dev)
+    _check_workspace(fn, ws, dev)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream, s, dout, weight, dsum, dx, dweight, ws):
+            return rms_norm_backward(params, s, dout, weight, dsum, dx, dweight, ws)
+    if dx is None:
+        dx = torch.empty_like(dout)
+    if weight is not None:
+        if dweight is None:
+            dweight = torch.empty(params.n_cols, dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = alloc_norm_workspace(params, dev)
+    _check(load().hla_rms_norm_backward(_c(params, xs), _adr(s), _adr(weight), _adr(dout), _adr(dsum), shape[0], _adr(dx),
+                                        _adr(dweight), _adr(ws), 0 if ws is None else ws.numel(), st), fn)
+    return dx, dweight
+
+
+@dataclass(frozen=True)
+class RecurrenceParams:
+    n_channels: int
+    gate_dim: int = 1           # channels in a row that share a gate: 1, 64, 128
+    dtype: int = DTYPE_BF16
+    gate_dtype: int = DTYPE_F32
+
+    def c(self, x_stride: int = 0, g_stride: int = 0) -> CRecurrenceParams:
+        return CRecurrenceParams(self.n_channels, self.gate_dim, self.dtype, self.gate_dtype, x_stride, g_stride)
+
+
+RECURRENCE_STATE_ROWS = 64
+
+
+def recurrence_workspace_bytes(params: RecurrenceParams, total_tokens: int) -> int:
+    return _bytes("hla_recurrence_workspace_bytes", params, total_tokens)
+
+
+def alloc_recurrence_workspace(params: RecurrenceParams, total_tokens: int, device="cuda"):
+    """A workspace for recurrence and recurrence_backward of up to total_tokens, its error word zeroed;
+    check_workspace_error reads it."""
+    return _zeroed(recurrence_workspace_bytes(params, total_tokens), device)
+
+
+def alloc_recurrence_states(params: RecurrenceParams, total_tokens: int, device="cuda"):
+    """The states that recurrence keeps for recurrence_backward."""
+    return torch.empty((-(-total_tokens // RECURRENCE_STATE_ROWS), params.n_channels), dtype=torch.float32, device=device)
+
+
+def _recurrence_rows(params: RecurrenceParams, fn: str, g, x):
+    """Checks g [T, n_channels / gate_dim] and x [T, n_channels]; returns their types, T and strides."""
+    dt, gt = _TORCH.get(params.dtype), _TORCH.get(params.gate_dtype)
+    _need(dt is not None and gt is not None and torch.uint8 not in (dt, gt), f"{fn}: dtype")
+    _sized(x, fn, "x", 2)
+    n, c = x.shape[0], params.n_channels
+    _need(params.gate_dim > 0, f"{fn}: gate_dim")
+    return dt, gt, n, (_check_matrix(x, fn, "x", dt, (n, c), x.device),
+                       _check_matrix(g, fn, "g", gt, (n, c // params.gate_dim), x.device))
+
+
+def _check_states(params, fn, n, cu_seqlens, h0, states, dev, **rows):
+    """Checks the table, the fp32 states per sequence (h0 and `rows`) and those per 64 rows; returns n_seqs."""
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        _refuse(f"{fn}: cu_seqlens")
+    n_seqs = cu_seqlens.numel() - 1
+    _check_tensor(cu_seqlens, fn, "cu_seqlens", torch.int32, (n_seqs + 1,), dev)
+    for name, t in (("h0", h0), *rows.items()):
+        if t is not None:
+            _check_tensor(t, fn, name, torch.float32, (n_seqs, params.n_channels), dev)
+    if states is not None:
+        _check_tensor(states, fn, "states", torch.float32, (-(-n // RECURRENCE_STATE_ROWS), params.n_channels), dev)
+    return n_seqs
+
+
+def recurrence(params: RecurrenceParams, g, x, cu_seqlens, h0=None, out=None, h_last=None, states=None, ws=None,
+               stream=None):
+    """hla_recurrence: (out [T, n_channels], h_last [n_seqs, n_channels] fp32) of h = exp(g) h + x over packed sequences,
+    from h0 (None: zeros).  g [T, n_channels / gate_dim] and x [T, n_channels] may be slices of a wider projection;
+    h_last=h0 writes the states in place.  states (alloc_recurrence_states): kept for recurrence_backward.  Without `ws`
+    one is allocated for the call, and what the device flags cannot be read."""
+    fn = "hla_recurrence"
+    dt, _, n, strides = _recurrence_rows(params, fn, g, x)
+    dev = x.device
+    n_seqs = _check_states(params, fn, n, cu_seqlens, h0, states, dev, h_last=h_last)
+    if out is not None:
+        _check_tensor(out, fn, "out", dt, tuple(x.shape), dev)
+    _check_workspace(fn, ws, dev)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream, g, x, cu_seqlens, h0, out, h_last, states, ws):
+            return recurrence(params, g, x, cu_seqlens, h0, out, h_last, states, ws)
+    if out is None:
+        out = _dense(x, strides[0])
+    if h_last is None:
+        h_last = torch.empty((n_seqs, params.n_channels), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = alloc_recurrence_workspace(params, n, dev)
+    _check(load().hla_recurrence(_c(params, *strides), _adr(g), _adr(x), _adr(h0), _adr(cu_seqlens), n_seqs, n, _adr(out),
+                                 _adr(h_last), _adr(states), _adr(ws), ws.numel(), st), fn)
+    return out, h_last
+
+
+def recurrence_backward(params: RecurrenceParams, g, x, states, dout, cu_seqlens, h0=None, dh_last=None, grads=None,
+                        ws=None, stream=None):
+    """hla_recurrence_backward: {"g", "x"} gradients (and "h0", fp32, where h0 is given) of sum(dout * h) +
+    sum(dh_last * h_last), from recurrence's inputs and the states it kept.  `grads` (same dict) and `ws` may be
+    passed in to be reused."""
+    fn = "hla_recurrence_backward"
+    dt, gt, n, strides = _recurrence_rows(params, fn, g, x)
+    dev, given = x.device, grads or {}
+    _need(states is not None, f"{fn}: states")
+    n_seqs = _check_states(params, fn, n, cu_seqlens, h0, states, dev, dh_last=dh_last, dh0=given.get("h0"))
+    _check_tensor(dout, fn, "dout", dt, tuple(x.shape), dev)
+    if grads is not None:
+        _check_tensor(given.get("g"), fn, "grads.g", gt, tuple(g.shape), dev)
+        _check_tensor(given.get("x"), fn, "grads.x", dt, tuple(x.shape), dev)
+        _need((given.get("h0") is not None) == (h0 is not None), f"{fn}: grads.h0 goes with h0")
+    _check_workspace(fn, ws, dev)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream, g, x, states, dout, cu_seqlens, h0, dh_last, ws, *given.values()):
+            return recurrence_backward(params, g, x, states, dout, cu_seqlens, h0, dh_last, grads, ws)
+    if grads is None:
+        grads = {"g": _dense(g, strides[1]), "x": torch.empty_like(dout)}
+        if h0 is not None:
+            grads["h0"] = torch.empty_like(h0)
+    if ws is None:
+        ws = alloc_recurrence_workspace(params, n, dev)
+    _check(load().hla_recurrence_backward(_c(params, *strides), _adr(g), _adr(x), _adr(h0), _adr(states),
+                                          _adr(cu_seqlens), n_seqs, n, _adr(dout), _adr(dh_last), _adr(grads["g"]),
+                                          _adr(grads["x"]), _adr(grads.get("h0")), _adr(ws), ws.numel(), st), fn)
+    return grads
+
+
+def recurrence_step(params: RecurrenceParams, g, x, h, out=None, stream=None):
+    """hla_recurrence_step: one token per sequence; h [n_seqs, n_channels] fp32 becomes exp(g) h + x in place, and out
+    is h in the layer's type."""
+    fn = "hla_recurrence_step"
+    dt, _, n, strides = _recurrence_rows(params, fn, g, x)
+    dev = x.device
+    _check_tensor(h, fn, "h", torch.float32, (n, params.n_channels), dev)
+    if out is not None:
+        _check_tensor(out, fn, "out", dt, tuple(x.shape), dev)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream, g, x, h, out):
+            return recurrence_step(params, g, x, h, out)
+    if out is None:
+        out = _dense(x, strides[0])
+    _check(load().hla_recurrence_step(_c(params, *strides), _adr(g), _adr(x), _adr(h), n, _adr(out), st), fn)
+    return out
+
+
+@dataclass(frozen=True)
+class Linear4Params:
+    n_in: int
+    n_out: int
+    group: int = 128            # inputs that share a scale: 32, 64, 128
+    dtype: int = DTYPE_BF16     # of out, scales, offsets (and x)
+    x_dtype: int = -1           # -1: dtype; DTYPE_E4M3: 8-bit rows with a power of two per x_group
+    x_group: int = 0            # E4M3: 32, 128, or 0 (the whole row)
+
+    def c(self, x_stride: int = 0) -> CLinear4Params:
+        return CLinear4Params(self.n_in, self.n_out, self.group, self.dtype,
+                              self.dtype if self.x_dtype < 0 else self.x_dtype, self.x_group, x_stride)
+
+
+def linear4_workspace_bytes(params: Linear4Params, tokens: int) -> int:
+    return _bytes("hla_linear4_workspace_bytes", params, tokens)
+
+
+def alloc_linear4_workspace(params: Linear4Params, tokens: int, device="cuda"):
+    """A workspace for linear4 of up to `tokens` rows."""
+    return torch.empty(max(256, linear4_workspace_bytes(params, tokens)), dtype=torch.uint8, device=device)
+
+
+def _linear4_weights(params: Linear4Params, fn: str, w, scales, offsets, dev):
+    dt = _TORCH.get(params.dtype)
+    _need(dt is not None and dt != torch.uint8 and params.group > 0, f"{fn}: dtype or group")
+    _check_tensor(w, fn, "w", torch.uint8, (params.n_out, params.n_in // 2), dev)
+    shape = (params.n_out, params.n_in // params.group)
+    _check_tensor(scales, fn, "scales", dt, shape, dev)
+    if offsets is not None:
+        _check_tensor(offsets, fn, "offsets", dt, shape, dev)
+    return dt
+
+
+def linear4(params: Linear4Params, x, w, scales, offsets=None, x_exp=None, out=None, ws=None, stream=None):
+    """hla_linear4: out [T, n_out] = x W^T with W = scales (q - 8) + offsets; x [T, n_in] (tokens may be slices of a wider
+    tensor; 8-bit rows: uint8, with x_exp [T, n_in / x_group]), w uint8 [n_out, n_in / 2]."""
+    fn, eight = "hla_linear4", params.x_dtype == DTYPE_E4M3
+    _sized(x, fn, "x", 2)
+    dev, n = x.device, x.shape[0]
+    dt = _linear4_weights(params, fn, w, scales, offsets, dev)
+    stride = _check_matrix(x, fn, "x", torch.uint8 if eight else dt, (n, params.n_in), dev)
+    _need(eight == (x_exp is not None), f"{fn}: exponents go with 8-bit rows")
+    if eight:
+        _check_tensor(x_exp, fn, "x_exp", torch.uint8, (n, params.n_in // params.x_group if params.x_group else 1), dev)
+    if out is not None:
+        _check_tensor(out, fn, "out", dt, (n, params.n_out), dev)
+    _check_workspace(fn, ws, dev)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream, x, w, scales, offsets, x_exp, out, ws):
+            return linear4(params, x, w, scales, offsets, x_exp, out, ws)
+    if out is None:
+        out = torch.empty((n, params.n_out), dtype=dt, device=dev)
+    if ws is None and (dt != torch.bfloat16 or eight or stride % 8 or x.data_ptr() % 16):
+        ws = alloc_linear4_workspace(params, n, dev)
+    _check(load().hla_linear4(_c(params, stride), _adr(x), _adr(x_exp), _adr(w), _adr(scales), _adr(offsets), n, _adr(out),
+                              _adr(ws), 0 if ws is None else ws.numel(), st), fn)
+    return out
+
+
+def linear4_quantize(params: Linear4Params, weight, with_offsets: bool = False, stream=None):
+    """hla_linear4_quantize: (w, scales, offsets or None) of weight [n_out, n_in] in the layer's type."""
+    fn = "hla_linear4_quantize"
+    dt = _TORCH.get(params.dtype)
+    _need(dt is not None and dt != torch.uint8 and params.group > 0, f"{fn}: dtype or group")
+    _sized(weight, fn, "weight", 2)
+    dev = weight.device
+    _check_tensor(weight, fn, "weight", dt, (params.n_out, params.n_in), dev)
+    st = _here(dev, stream)
+    if st is None:
+        with _on(dev, stream, weight):
+            return linear4_quantize(params, weight, with_offsets)
+    w = torch.empty((params.n_out, params.n_in // 2), dtype=torch.uint8, device=dev)
+    scales, offsets = (torch.empty((params.n_out, params.n_in // params.group), dtype=dt, device=dev) if on else None
+                       for on in (True, with_offsets))
+    _check(load().hla_linear4_quantize(_c(params), _adr(weight), _adr(w), _adr(scales), _adr(offsets), st), fn)
+    return w, scales, offsets

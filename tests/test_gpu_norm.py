@@ -1,0 +1,188 @@
+"""GPU root-mean-square norms against the 64-bit form: widths from one value to rows that pass a block's registers, heads,
+8-bit rows, strides, in place, infinities and NaN, gradients, graphs and streams."""
+import pytest
+import torch
+
+import layer_cases as lc
+from linearized_attention_rope_gb300 import hla
+
+pytestmark = pytest.mark.gpu
+F32, BF16, E4M3 = hla.DTYPE_F32, hla.DTYPE_BF16, hla.DTYPE_E4M3
+TYPE = {F32: torch.float32, BF16: torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    assert torch.cuda.is_available(), "the gpu-marked tests need a CUDA device"
+    from linearized_attention_rope_gb300 import build
+
+    build.build()
+
+
+def shape(prm, n):
+    return (n, prm.n_cols) if prm.n_heads == 1 else (n, prm.n_heads, prm.n_cols)
+
+
+def inputs(prm, n, seed=1):
+    dt = TYPE[prm.dtype]
+    x = lc.randn(seed, *shape(prm, n)) * torch.exp2(lc.randn(seed + 1, n, *[1] * (len(shape(prm, n)) - 1)))
+    return x.to(dt), lc.randn(seed + 2, *shape(prm, n), dtype=dt), (1 + 0.3 * lc.randn(seed + 3, prm.n_cols)).to(dt)
+
+
+# cols, heads, tokens: a value, odd widths, a warp's, blocks of one, two and four pieces a thread, sixteen single values,
+# rows past the registers
+SIZES = [(1, 1, 3), (7, 1, 33), (64, 8, 5), (128, 3, 130), (100, 1, 9), (256, 1, 1), (1000, 2, 17), (1024, 1, 40),
+         (2056, 1, 3), (4096, 1, 65), (4100, 1, 5), (5120, 1, 700), (8191, 1, 3), (16384, 1, 4), (17000, 1, 2),
+         (33001, 1, 2), (65536, 1, 2)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,heads,n", SIZES)
+@pytest.mark.parametrize("residual,weight,offset", [(True, True, 0.0), (False, True, 1.0), (True, False, 0.0)])
+def test_norm_matches_64_bit(dtype, cols, heads, n, residual, weight, offset):
+    prm = hla.NormParams(cols, n_heads=heads, dtype=dtype, eps=1e-5, offset=offset)
+    x, r, w = inputs(prm, n)
+    got = hla.rms_norm(prm, x.cuda(), weight=w.cuda() if weight else None, residual=r.cuda() if residual else None)
+    s = (x + r) if residual else x
+    assert got.exp is None and (got.sum is None) == (not residual)
+    if residual:  # one rounding of an fp32 sum
+        assert torch.equal(got.sum.cpu(), s)
+    y, err = lc.norm(s.double(), w.double() if weight else None, 1e-5, offset)
+    lc.close(got.out, y, err)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,heads,n,group", [(32, 1, 5, 32), (64, 4, 9, 32), (128, 2, 33, 128), (128, 1, 7, 0),
+                                                (160, 1, 6, 32), (4096, 1, 64, 32), (4096, 1, 3, 128), (5120, 1, 9, 0),
+                                                (16, 1, 2, 0), (16384, 1, 3, 128), (33024, 1, 2, 128), (40000, 1, 2, 32),
+                                                (40000, 1, 2, 0)])
+def test_norm_to_8_bits(dtype, cols, heads, n, group):
+    prm = hla.NormParams(cols, n_heads=heads, dtype=dtype, out_dtype=E4M3, group=group)
+    x, r, w = inputs(prm, n)
+    x[0] = 0
+    r[0] = 0  # a row of zeros: exponent byte 0
+    got = hla.rms_norm(prm, x.cuda(), weight=w.cuda(), residual=r.cuda())
+    s = x + r
+    assert torch.equal(got.sum.cpu(), s) and got.out.dtype == torch.uint8
+    y, err = lc.norm(s.double(), w.double(), 1e-6, 0.0)
+    assert lc.eight(y, err, got.out, got.exp, group) == (True, True, True)
+    assert got.exp[0].max() == 0 and (got.out[0] & 127).max() == 0  # a negative weight makes -0
+
+
+def test_8_bit_rows_with_infinities_and_nan():
+    # an infinity makes the mean infinite: the row's finite values become 0 and it NaN; a NaN makes the whole row NaN
+    for group in (0, 32):
+        prm = hla.NormParams(64, dtype=F32, out_dtype=E4M3, group=group)
+        x = torch.ones(3, 64)
+        x[0, 5], x[1, 7] = float("inf"), float("nan")
+        got = hla.rms_norm(prm, x.cuda())
+        v = got.out.view(torch.float8_e4m3fn).float().cpu()
+        assert v[0, 5].isnan() and v[0].nan_to_num(0).abs().max() == 0
+        assert v[1].isnan().all() and v[2].isfinite().all()
+
+
+def test_strided_and_unaligned_rows():
+    # q, k and v of one fused projection: norm of q's and k's heads in place of their slices, and rows one value in
+    wide = lc.randn(1, 50, 14 * 64, dtype=torch.bfloat16).cuda()
+    for lo, heads in ((0, 8), (8, 4), (12, 1)):
+        prm = hla.NormParams(64, n_heads=heads)
+        x = wide[:, lo * 64:(lo + heads) * 64]
+        x = x.view(50, heads, 64) if heads > 1 else x
+        y, err = lc.norm(x.cpu().double(), None, 1e-6, 0.0)
+        lc.close(hla.rms_norm(prm, x).out, y, err)
+    for dtype in (F32, BF16):
+        flat = lc.randn(2, 20 * 301 + 1, dtype=TYPE[dtype]).cuda()
+        x = flat[1:].view(20, 301)[:, :300]
+        y, err = lc.norm(x.cpu().double(), None, 1e-6, 0.0)
+        lc.close(hla.rms_norm(hla.NormParams(300, dtype=dtype), x).out, y, err)
+        got, _ = hla.rms_norm_backward(hla.NormParams(300, dtype=dtype), x, x.contiguous())
+        dx, err, _, _ = lc.norm_grad(x.cpu().double(), None, x.cpu().double(), None, 1e-6, 0.0)
+        lc.close(got, dx, err)
+    with pytest.raises(hla.HlaError):  # 8-bit rows start on 16 bytes
+        hla.rms_norm(hla.NormParams(64, out_dtype=E4M3, group=32), wide[:, 1:65])
+
+
+@pytest.mark.parametrize("cols", [128, 4096, 8191, 33001])
+def test_in_place(cols):
+    prm = hla.NormParams(cols)
+    x, r, w = (t.cuda() for t in inputs(prm, 20))
+    ref = hla.rms_norm(prm, x, weight=w, residual=r)
+    for target in ("residual", "x"):
+        a, b = x.clone(), r.clone()
+        got = hla.rms_norm(prm, a, weight=w, residual=b, sum=b if target == "residual" else a)
+        assert torch.equal(got.out, ref.out) and torch.equal(b if target == "residual" else a, ref.sum)
+    a, b = x.clone(), r.clone()
+    got = hla.rms_norm(prm, a, weight=w, residual=b, sum=b, out=a)  # the stream and the branch, both in place
+    assert torch.equal(a, ref.out) and torch.equal(b, ref.sum)
+    a = x.clone()
+    hla.rms_norm(prm, a, weight=w, out=a)
+    assert torch.equal(a, hla.rms_norm(prm, x, weight=w).out)
+    dx, dw = hla.rms_norm_backward(prm, x, r, weight=w, dsum=ref.out)
+    for target in (0, 1):
+        a, b = r.clone(), ref.out.clone()
+        got, gw = hla.rms_norm_backward(prm, x, a, weight=w, dsum=b, dx=(a, b)[target])
+        assert torch.equal(got, dx) and torch.equal(gw, dw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,heads,n", SIZES + [(128, 32, 600), (64, 1, 20011)])
+@pytest.mark.parametrize("dsum,weight,offset", [(True, True, 0.0), (False, True, 1.0), (True, False, 0.0)])
+def test_norm_gradient_matches_64_bit(dtype, cols, heads, n, dsum, weight, offset):
+    prm = hla.NormParams(cols, n_heads=heads, dtype=dtype, eps=1e-5, offset=offset)
+    x, ds, w = inputs(prm, n)
+    dout = lc.randn(7, *shape(prm, n), dtype=TYPE[dtype])
+    dx, dw = hla.rms_norm_backward(prm, x.cuda(), dout.cuda(), weight=w.cuda() if weight else None,
+                                   dsum=ds.cuda() if dsum else None)
+    ref = lc.norm_grad(x.double(), w.double() if weight else None, dout.double(), ds.double() if dsum else None, 1e-5, offset)
+    lc.close(dx, ref[0], ref[1])
+    assert (dw is None) == (not weight)
+    if weight:
+        lc.close(dw, ref[2], ref[3])
+        again = hla.rms_norm_backward(prm, x.cuda(), dout.cuda(), weight=w.cuda(), dsum=ds.cuda() if dsum else None)
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)  # fixed order of sums
+
+
+def test_no_rows():
+    prm, w = hla.NormParams(128), torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    assert hla.rms_norm(prm, x, weight=w, residual=x).out.shape == (0, 128)
+    dx, dw = hla.rms_norm_backward(prm, x, x, weight=w)
+    assert dx.shape == (0, 128) and float(dw.abs().max()) == 0.0
+
+
+def test_rows_past_32_bits():
+    # the last rows of a batch whose elements pass 2^32
+    n, cols = (1 << 20) + 1, 4096
+    x = torch.zeros(n, cols, dtype=torch.bfloat16, device="cuda")
+    tail = lc.randn(1, 3, cols, dtype=torch.bfloat16)
+    x[-3:] = tail.cuda()
+    prm = hla.NormParams(cols)
+    out = hla.rms_norm(prm, x, out=x).out
+    y, err = lc.norm(tail.double(), None, 1e-6, 0.0)
+    lc.close(out[-3:], y, err)
+    assert float(out[:8].abs().max()) == 0.0
+
+
+def test_graph_and_stream():
+    prm = hla.NormParams(4096, out_dtype=E4M3, group=32)
+    x, r, w = (t.cuda() for t in inputs(prm, 30))
+    ref = hla.rms_norm(prm, x, weight=w, residual=r)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = hla.rms_norm(prm, x, weight=w, residual=r, stream=side)
+    side.synchronize()
+    assert torch.equal(got.out, ref.out) and torch.equal(got.exp, ref.exp)
+    plain = hla.NormParams(4096)
+    ws = hla.alloc_norm_workspace(plain)
+    want = hla.rms_norm_backward(plain, x, r, weight=w, ws=ws)
+    a = torch.zeros_like(x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = hla.rms_norm(prm, a, weight=w, residual=r)
+        dx, dw = hla.rms_norm_backward(plain, a, r, weight=w, ws=ws)
+    for _ in range(2):
+        a.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.out, ref.out) and torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+        a.zero_()
