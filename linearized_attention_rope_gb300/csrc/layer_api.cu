@@ -52,6 +52,10 @@ NormDims norm_dims(const hla_norm_params* p, int64_t tokens) {
     N.group = p->group;
     N.eps = p->eps;
     N.offset = p->offset;
+    if (N.sx == dense && N.sr == dense) {  // heads of dense tokens are rows like any other
+        N.heads = 1;
+        N.sx = N.sr = N.cols;
+    }
     return N;
 }
 bool rows_ok(const hla_norm_params* p, int64_t tokens) {

@@ -11,7 +11,10 @@
 // reads them twice.
 // The gradient's blocks stay and walk the rows, so that a thread adds up dw of
 // its own columns in registers; the blocks' sums are added in order by a second
-// launch.
+// launch.  A thread has one piece of a row where 1024 threads can (then the next
+// row is on its way while this one is reduced), else two or four that it reads
+// again behind the reduction, from L2: registers are what a row's length is
+// limited by.
 #include <algorithm>
 
 #include "layer.cuh"
@@ -77,49 +80,55 @@ __device__ __forceinline__ void store_8_bits(uint8_t* p, const float* y, float i
     }
 }
 
+// Where a row starts, given the token stride.
+__device__ __forceinline__ int64_t row_at(const NormDims& N, int64_t row, int64_t stride) {
+    if (N.heads == 1) return row * stride;
+    const int64_t token = row / N.heads;
+    return token * stride + (row - token * N.heads) * N.cols;
+}
+
+template <int V, int P> struct Bound {
+    static constexpr int threads = V == 1 || P > 1 ? 1024 : 256;
+    static constexpr int blocks = (V > 1 && P == 1 ? 1536 : 1024) / threads;
+};
+
 // A row's P pieces of V values per thread, piece p at (p tpr + thread) V.  Eight bits: a group's values lie in
 // neighbouring lanes of one piece index (its pieces are a power of two that divides 32, and tpr is a multiple of it).
 template <typename T, int V, int P, bool E4M3>
-__global__ void __launch_bounds__(P > 1 || V == 1 ? 1024 : 256)
+__global__ void __launch_bounds__(Bound<V, P>::threads, Bound<V, P>::blocks)
 norm_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict__ weight, T* out, uint8_t* out8,
             uint8_t* exps, T* sum, int tpr) {
     using Pc = Piece<T, V>;
     __shared__ float sm[64];
-    const int lane = threadIdx.x % tpr;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const int group = tpr > 32 ? 0 : threadIdx.x / tpr, lane = threadIdx.x - group * tpr;
+    const int64_t row = tpr > 32 ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / tpr) + group;
     const bool on = row < N.rows;
-    const int64_t token = on ? row / N.heads : 0;
-    const int head = on ? (int)(row - token * N.heads) : 0;
-    const T* xr = x + token * N.sx + (int64_t)head * N.cols;
-    const T* rr = residual + token * N.sr + (int64_t)head * N.cols;
+    const T* xr = x + (on ? row_at(N, row, N.sx) : 0);
     const int64_t dense = (on ? row : 0) * N.cols;
-    Pc a[P], b[P], w[P];
+    Pc a[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int e = (p * tpr + lane) * V;
-        if (on && e < N.cols) {
-            a[p] = *reinterpret_cast<const Pc*>(xr + e);
-            if (residual) b[p] = *reinterpret_cast<const Pc*>(rr + e);
-        }
+        a[p] = on && e < N.cols ? *reinterpret_cast<const Pc*>(xr + e) : Pc{};
     }
+    if (residual) {
+        const T* rr = residual + (on ? row_at(N, row, N.sr) : 0);
+        Pc b[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int e = (p * tpr + lane) * V;
-        if (weight && e < N.cols) w[p] = *reinterpret_cast<const Pc*>(weight + e);
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * tpr + lane) * V;
+            b[p] = on && e < N.cols ? *reinterpret_cast<const Pc*>(rr + e) : Pc{};
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int j = 0; j < V; ++j) a[p].x[j] = from_f32<T>(to_f32(a[p].x[j]) + to_f32(b[p].x[j]));
     }
     float v[1] = {0.f};
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int e = (p * tpr + lane) * V;
-        if (on && e < N.cols) {
-            if (residual) {
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-                for (int j = 0; j < V; ++j) a[p].x[j] = from_f32<T>(to_f32(a[p].x[j]) + to_f32(b[p].x[j]));
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[0] += to_f32(a[p].x[j]) * to_f32(a[p].x[j]);
-        }
-    }
+        for (int j = 0; j < V; ++j) v[0] += to_f32(a[p].x[j]) * to_f32(a[p].x[j]);
     row_sum(v, tpr, sm);
     const float r = 1.f / sqrtf(v[0] / (float)N.cols + N.eps);
     // the sum is written once the whole row has been read: it may lie where x or the residual does
@@ -130,10 +139,15 @@ norm_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict
             if (on && e < N.cols) *reinterpret_cast<Pc*>(sum + dense + e) = a[p];
         }
     }
-    auto values = [&](int p, float* y) {
+    auto values = [&](int p, int e, float (&y)[V]) {
+        if (weight) {
+            const Pc w = e < N.cols ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            y[j] = to_f32(a[p].x[j]) * r * (weight ? N.offset + to_f32(w[p].x[j]) : 1.f);
+            for (int j = 0; j < V; ++j) y[j] = to_f32(a[p].x[j]) * r * (N.offset + to_f32(w.x[j]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[j] = to_f32(a[p].x[j]) * r;
+        }
     };
     if constexpr (!E4M3) {
 #pragma unroll
@@ -141,7 +155,7 @@ norm_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict
             const int e = (p * tpr + lane) * V;
             if (!on || e >= N.cols) continue;
             float y[V];
-            values(p, y);
+            values(p, e, y);
             Pc o;
 #pragma unroll
             for (int j = 0; j < V; ++j) o.x[j] = from_f32<T>(y[j]);
@@ -149,27 +163,43 @@ norm_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict
         }
     } else {
         const int per = N.group ? N.cols / N.group : 1;  // exponents of a row
-        float y[P][V], top[P], all = 0.f;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const bool here = on && (p * tpr + lane) * V < N.cols;
-            values(p, y[p]);
-            top[p] = 0.f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) top[p] = fmaxf(top[p], here ? finite_size(y[p][j]) : 0.f);
-            if (N.group) {
-                for (int o = N.group / V / 2; o; o >>= 1) top[p] = fmaxf(top[p], __shfl_xor_sync(0xffffffffu, top[p], o));
-            }
-            all = fmaxf(all, top[p]);
-        }
-        if (!N.group) all = row_max(all, tpr, sm + 32);
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int e = (p * tpr + lane) * V;
-            if (!on || e >= N.cols) continue;
-            const int q = group_exponent(N.group ? top[p] : all);
-            store_8_bits<V>(out8 + dense + e, y[p], group_pow2(-q));
+        auto store = [&](int e, const float (&y)[V], float top) {
+            if (!on || e >= N.cols) return;
+            const int q = group_exponent(top);
+            store_8_bits<V>(out8 + dense + e, y, group_pow2(-q));
             if (N.group ? e % N.group == 0 : e == 0) exps[row * per + (N.group ? e / N.group : 0)] = (uint8_t)(q + 127);
+        };
+        auto size = [&](const float (&y)[V]) {  // (columns past the row's are 0)
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) top = fmaxf(top, finite_size(y[j]));
+            return top;
+        };
+        float y[V];
+        if (N.group) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int e = (p * tpr + lane) * V;
+                values(p, e, y);
+                float top = on && e < N.cols ? size(y) : 0.f;
+                for (int o = N.group / V / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                store(e, y, top);
+            }
+        } else {
+            float all = 0.f;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int e = (p * tpr + lane) * V;
+                values(p, e, y);
+                if (on && e < N.cols) all = fmaxf(all, size(y));
+            }
+            all = row_max(all, tpr, sm + 32);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int e = (p * tpr + lane) * V;
+                values(p, e, y);
+                store(e, y, all);
+            }
         }
     }
 }
@@ -227,70 +257,83 @@ norm_long_kernel(const NormDims N, const T* x, const T* residual, const T* __res
 }
 
 // The gradient.  part [gridDim.x][cols]: this block's sums of dy s r.
-template <typename T, int V, int P>
-__global__ void __launch_bounds__(P > 1 || V == 1 ? 1024 : 256)
+// MOST: threads of a block, at most.
+template <typename T, int V, int P, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == kNarrow ? 6 : 1)
 norm_backward_kernel(const NormDims N, const T* s, const T* __restrict__ weight, const T* dout, const T* dsum, T* dx,
                      float* part, int tpr) {
     using Pc = Piece<T, V>;
-    __shared__ float sm[64];
+    constexpr bool kAgain = P * V * sizeof(T) > 16;                             // pieces are read again, not held
+    constexpr bool kAhead = P == 1 && V * (MOST == 1024 ? 8 / sizeof(T) : 1) <= 8;  // the next row's are loaded early
+    constexpr int H = kAgain ? 1 : P;
+    __shared__ float sm[2][64];
     extern __shared__ float cols_sm[];  // rows of a warp or less: the sums of every group of lanes
-    const int lane = threadIdx.x % tpr, groups = blockDim.x / tpr, group = threadIdx.x / tpr;
+    const int groups = tpr > 32 ? 1 : blockDim.x / tpr, group = tpr > 32 ? 0 : threadIdx.x / tpr;
+    const int lane = threadIdx.x - group * tpr;
     const float inv = 1.f / (float)N.cols;
-    Pc w[P];
+    Pc w[H];
     float acc[P][V];
+    auto factor = [&](int p, int e) {
+        return weight && e < N.cols ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
+    };
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        const int e = (p * tpr + lane) * V;
-        if (weight && e < N.cols) w[p] = *reinterpret_cast<const Pc*>(weight + e);
+        if (!kAgain) w[kAgain ? 0 : p] = factor(p, (p * tpr + lane) * V);
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[p][j] = 0.f;
     }
-    for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < N.rows; row0 += (int64_t)gridDim.x * groups) {
+    const float one = weight ? N.offset : 1.f;  // (without a weight w is 0)
+    const int64_t step = (int64_t)gridDim.x * groups;
+    Pc a[H], d[H], g[H];
+    auto load = [&](int64_t row, int p, Pc& a, Pc& d, Pc& g, bool with_sum) {
+        const int e = (p * tpr + lane) * V;
+        const bool on = row < N.rows && e < N.cols;
+        a = on ? *reinterpret_cast<const Pc*>(s + row_at(N, row, N.sx) + e) : Pc{};
+        d = on ? *reinterpret_cast<const Pc*>(dout + row * N.cols + e) : Pc{};
+        if (with_sum) g = on && dsum ? *reinterpret_cast<const Pc*>(dsum + row * N.cols + e) : Pc{};
+    };
+    if (kAhead) load((int64_t)blockIdx.x * groups + group, 0, a[0], d[0], g[0], true);
+    int turn = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < N.rows; row0 += step, turn ^= 1) {
         const int64_t row = row0 + group;
-        const bool on = row < N.rows;
-        const int64_t token = on ? row / N.heads : 0;
-        const int head = on ? (int)(row - token * N.heads) : 0;
-        const T* sr = s + token * N.sx + (int64_t)head * N.cols;
-        const int64_t dense = (on ? row : 0) * N.cols;
-        Pc a[P], d[P], g[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int e = (p * tpr + lane) * V;
-            if (on && e < N.cols) {
-                a[p] = *reinterpret_cast<const Pc*>(sr + e);
-                d[p] = *reinterpret_cast<const Pc*>(dout + dense + e);
-                if (dsum) g[p] = *reinterpret_cast<const Pc*>(dsum + dense + e);
-            }
-        }
+        Pc a1, d1, g1;
+        if constexpr (kAhead) load(row + step, 0, a1, d1, g1, true);
         float v[2] = {0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int e = (p * tpr + lane) * V;
-            if (!on || e >= N.cols) continue;
+            const int h = kAgain ? 0 : p;
+            if constexpr (!kAhead) load(row, p, a[h], d[h], g[h], !kAgain);
+            if constexpr (kAgain) w[h] = factor(p, (p * tpr + lane) * V);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float x = to_f32(a[p].x[j]);
+                const float x = to_f32(a[h].x[j]);
                 v[0] += x * x;
-                v[1] += (weight ? N.offset + to_f32(w[p].x[j]) : 1.f) * to_f32(d[p].x[j]) * x;
+                v[1] += (one + to_f32(w[h].x[j])) * to_f32(d[h].x[j]) * x;
             }
         }
-        row_sum(v, tpr, sm);
+        row_sum(v, tpr, sm[turn]);  // (sums of the row before last have been read by all)
         const float r = 1.f / sqrtf(v[0] * inv + N.eps), c = v[1] * inv * r * r;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int e = (p * tpr + lane) * V;
-            if (!on || e >= N.cols) continue;
+            const int e = (p * tpr + lane) * V, h = kAgain ? 0 : p;
+            if constexpr (kAgain) {
+                load(row, p, a[h], d[h], g[h], true);
+                w[h] = factor(p, e);
+            }
             Pc o;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float x = to_f32(a[p].x[j]), dy = to_f32(d[p].x[j]);
-                const float f = weight ? N.offset + to_f32(w[p].x[j]) : 1.f;
-                o.x[j] = from_f32<T>((f * dy - x * c) * r + (dsum ? to_f32(g[p].x[j]) : 0.f));
+                const float x = to_f32(a[h].x[j]), dy = to_f32(d[h].x[j]);
+                o.x[j] = from_f32<T>(((one + to_f32(w[h].x[j])) * dy - x * c) * r + to_f32(g[h].x[j]));
                 acc[p][j] += dy * (x * r);
             }
-            *reinterpret_cast<Pc*>(dx + dense + e) = o;
+            if (row < N.rows && e < N.cols) *reinterpret_cast<Pc*>(dx + row * N.cols + e) = o;
         }
-        if (tpr > 32) __syncthreads();  // sm is written again
+        if constexpr (kAhead) {
+            a[0] = a1;
+            d[0] = d1;
+            g[0] = g1;
+        }
     }
     if (!part) return;
     float* mine = part + (int64_t)blockIdx.x * N.cols;
@@ -373,7 +416,7 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* __restric
 struct RowShape {
     int tpr, p;
 };
-RowShape row_shape(int pieces, bool single) {
+RowShape row_shape(int pieces, bool single, bool backward) {
     if (pieces <= 32) {
         int t = 4;
         while (t < pieces) t *= 2;
@@ -381,8 +424,8 @@ RowShape row_shape(int pieces, bool single) {
     }
     auto threads = [&](int p) { return ((pieces + p - 1) / p + 31) / 32 * 32; };
     if (single) return pieces <= 4096 ? RowShape{threads(4), 4} : pieces <= 16384 ? RowShape{threads(16), 16} : RowShape{0, 0};
-    if (pieces <= 128) return {threads(1), 1};
-    if (pieces <= 512) return {threads(2), 2};
+    if (pieces <= (backward ? 1024 : 256)) return {threads(1), 1};
+    if (pieces <= 2048) return {threads(2), 2};
     return pieces <= 4096 ? RowShape{threads(4), 4} : RowShape{0, 0};
 }
 
@@ -408,11 +451,18 @@ cudaError_t backward(const NormDims& N, const T* s, const T* weight, const T* do
     cudaError_t e = device_cached(cache, &n_sm, [](int dev, int* v) { return sm_count(dev, v); });
     if (e != cudaSuccess) return e;
     const int threads = tpr <= 32 ? kNarrow : tpr, groups = threads / tpr;
-    const int resident = std::max(1, std::min(1024 / threads, 8));
+    const int resident = std::max(1, 768 / threads);
     *blocks = (int)std::min<int64_t>({(N.rows + groups - 1) / groups, (int64_t)n_sm * resident, kNormParts});
     const size_t sm = groups > 1 ? (size_t)groups * N.cols * sizeof(float) : 0;  // at most 128 threads x 8 values
-    norm_backward_kernel<T, V, P><<<*blocks, threads, sm, st>>>(N, s, weight, dout, dsum, dx, part, tpr);
-    return cudaGetLastError();
+    auto go = [&](auto most) {
+        norm_backward_kernel<T, V, P, decltype(most)::value><<<*blocks, threads, sm, st>>>(N, s, weight, dout, dsum, dx, part, tpr);
+        return cudaGetLastError();
+    };
+    if constexpr (V > 1 && P == 1) {
+        if (threads <= kNarrow) return go(std::integral_constant<int, kNarrow>());
+        if (threads <= 768) return go(std::integral_constant<int, 768>());
+    }
+    return go(std::integral_constant<int, 1024>());
 }
 
 template <typename T>
@@ -430,7 +480,7 @@ cudaError_t launch_norm(const NormDims& N, const T* x, const T* residual, const 
     constexpr int V = 16 / (int)sizeof(T);
     const uintptr_t a = (uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)out | (uintptr_t)sum;
     const bool vec = wide<T>(N, a);
-    const RowShape r = row_shape(vec ? N.cols / V : N.cols, !vec);
+    const RowShape r = row_shape(vec ? N.cols / V : N.cols, !vec, false);
     auto run = [&](auto v, auto p) {
         return forward<T, decltype(v)::value, decltype(p)::value>(N, x, residual, weight, out, out8, exps, sum, r.tpr, st);
     };
@@ -455,7 +505,7 @@ cudaError_t launch_norm_backward(const NormDims& N, const T* s, const T* weight,
     if (N.rows > 0) {
         const uintptr_t a = (uintptr_t)s | (uintptr_t)weight | (uintptr_t)dout | (uintptr_t)dsum | (uintptr_t)dx;
         const bool vec = wide<T>(N, a);
-        const RowShape r = row_shape(vec ? N.cols / V : N.cols, !vec);
+        const RowShape r = row_shape(vec ? N.cols / V : N.cols, !vec, true);
         auto run = [&](auto v, auto p) {
             return backward<T, decltype(v)::value, decltype(p)::value>(N, s, weight, dout, dsum, dx, part, r.tpr, &blocks, st);
         };
