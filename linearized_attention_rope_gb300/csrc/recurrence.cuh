@@ -13,8 +13,8 @@
 // state in front of them.
 //
 // The state in front of a tile: every tile publishes (A, B) and, once it knows
-// it, the state behind it.  A tile looks at up to eight tiles before it; the
-// nearest with a state is carried forward by the (A, B) of those between, tile
+// it, the state behind it.  A tile looks at the eight tiles before it, then at up to
+// 32 (four channels a lane: 16); the nearest with a state is carried forward by the (A, B) of those between, tile
 // after tile.  That is what each of those tiles does itself, rounding for
 // rounding, so that results do not depend on which of them was found.  Tiles
 // are handed out in order of time, so that those waited for are running.  Every
@@ -42,7 +42,6 @@ namespace hla {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kLook = kWarps;       // tiles before a tile that it looks at, one per warp
 constexpr int kPolls = 1 << 20;     // looks at a tile that has nothing yet (about 0.7 us each)
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -217,65 +216,65 @@ __device__ __forceinline__ void check_table(const int32_t* __restrict__ cu, cons
 // (A, B), or its state where that does not depend on what is in front.  Called by the whole block.
 template <int NP>
 __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, int slab, float2 (&c)[NP], int32_t* err) {
+    constexpr int kDeep = 4 / NP, kLook = kDeep * kWarps;  // a warp looks at the tile 1 + warp before this one, 9 + warp ...
     __shared__ float2 pa[kLook][NP][32], pb[kLook][NP][32];
-    __shared__ int status[kLook];
+    __shared__ int status[kLook];  // 0 nothing yet, 1 (A, B), 2 the state, 3 given up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pred = k - 1 - warp;
-    int have = 0, polls = 0, m;
-    bool late = false;
+    int polls = 0, m, deep = 1;
+    for (int i = threadIdx.x; i < kLook; i += kThreads) status[i] = 0;
+    __syncthreads();
     for (;;) {
-        if (pred < 0) {
-            if (!have)
+        for (int d = 0; d < deep; ++d) {
+            const int i = d * kWarps + warp, pred = k - 1 - i;
+            const int had = status[i];  // (written by this warp alone)
+            if (had >= 2) continue;
+            int have = had;
+            if (pred < 0) {
 #pragma unroll
-                for (int p = 0; p < NP; ++p) pb[warp][p][lane] = splat(0.f);
-            have = 2;
-        } else if (have < 2 && !late) {
-            const int64_t at = (((int64_t)pred * n_slabs + slab) * 32 + lane) * 2 * NP;
-            do {
-                float2 s[NP], a[NP], b[NP];
-                bool is = true, has = true;
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    is &= get_words(S.state + at + 2 * p, &s[p]);
-                    if (!have) {
-                        has &= get_words(S.map + 2 * at + 4 * p, &a[p]);
-                        has &= get_words(S.map + 2 * at + 4 * p + 2, &b[p]);
-                    }
-                }
-                if (__all_sync(kFull, is)) {
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) pb[warp][p][lane] = s[p];
-                    have = 2;
-                } else if (!have && __all_sync(kFull, has)) {
+                for (int p = 0; p < NP; ++p) pb[i][p][lane] = splat(0.f);
+                have = 2;
+            } else {
+                const int64_t at = (((int64_t)pred * n_slabs + slab) * 32 + lane) * 2 * NP;
+                do {
+                    float2 s[NP], a[NP], b[NP];
+                    bool is = true, has = true;
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        pa[warp][p][lane] = a[p];
-                        pb[warp][p][lane] = b[p];
+                        is &= get_words(S.state + at + 2 * p, &s[p]);
+                        if (!have) {
+                            has &= get_words(S.map + 2 * at + 4 * p, &a[p]);
+                            has &= get_words(S.map + 2 * at + 4 * p + 2, &b[p]);
+                        }
                     }
-                    have = 1;
-                }
-                late = ++polls > kPolls;
-            } while (!have && !late);
+                    if (__all_sync(kFull, is)) {
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) pb[i][p][lane] = s[p];
+                        have = 2;
+                    } else if (!have && __all_sync(kFull, has)) {
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) {
+                            pa[i][p][lane] = a[p];
+                            pb[i][p][lane] = b[p];
+                        }
+                        have = 1;
+                    }
+                    if (have < 2 && ++polls > kPolls) have = 3;
+                } while (!have);
+            }
+            __syncwarp();
+            if (lane == 0) status[i] = have;
         }
-        if (lane == 0) status[warp] = late && have < 2 ? 3 : have;
         __syncthreads();
         bool gone = false;
         m = kLook;
-#pragma unroll
-        for (int w = kLook - 1; w >= 0; --w) {
+        for (int w = deep * kWarps - 1; w >= 0; --w) {  // (every one has something by now)
             const int s = status[w];
             gone |= s == 3;
             m = s == 2 ? w : m;
         }
-        if (m < kLook) {
-            bool fit = true;  // every tile between has its (A, B), unless a wait ran out
-            for (int w = 0; w < m; ++w) fit &= status[w] == 1;
-            if (fit) break;
-        }
-        if (gone) {
-            m = -1;
-            break;
-        }
+        if (gone) m = -1;
+        if (m < kLook) break;
+        if (deep < kDeep) ++deep;
         __syncthreads();  // before status is written again
     }
     if (m < 0) {
@@ -286,6 +285,7 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
     }
 #pragma unroll
     for (int p = 0; p < NP; ++p) c[p] = pb[m][p][lane];
+#pragma unroll 4
     for (int w = m - 1; w >= 0; --w)
 #pragma unroll
         for (int p = 0; p < NP; ++p) c[p] = ffma2(pa[w][p][lane], c[p], pb[w][p][lane]);
@@ -393,17 +393,19 @@ struct Gates {
             w[0] = splat(far ? 0.f : 1.f);
             v[0][0] = far ? splat(expf(g)) : mild(splat(g));
         } else {
+            auto gate = [&](int i, int p) {
+                float2 g = two(raw[i], p);
+                if (EDGE && !(valid >> i & 1)) g = splat(0.f);
+                return g;
+            };
 #pragma unroll
             for (int i = 0; i < ROWS; ++i)
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    float2 g = two(raw[i], p);
-                    if (EDGE && !(valid >> i & 1)) g = splat(0.f);
-                    const float2 d = add2(g, splat(kMid));
+                    const float2 g = gate(i, p), d = add2(g, splat(kMid));
                     off[p].x = fmaxf(off[p].x, fabsf(d.x));
                     off[p].y = fmaxf(off[p].y, fabsf(d.y));
                     sum[p] = add2(sum[p], g);
-                    v[i][p] = mild(g);
                 }
             bool far = false, big = false;
 #pragma unroll
@@ -413,19 +415,28 @@ struct Gates {
                 far |= most > kMid;
                 big |= most > kBig - kMid;
             }
-            if (!__any_sync(kFull, far)) return;
-            big = __any_sync(kFull, big);
+            auto put = [&](int i, int p, float2 y, float2 a) {
+                v[i][p] = make_float2(off[p].x > kMid ? a.x : y.x, off[p].y > kMid ? a.y : y.y);
+            };
+            if (!__any_sync(kFull, far)) {
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i)
+                for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    float2 g = two(raw[i], p), a;
-                    if (EDGE && !(valid >> i & 1)) g = splat(0.f);
-                    if (big) a = make_float2(expf(g.x), expf(g.y));
-                    else a = strong(g);
-                    v[i][p].x = off[p].x > kMid ? a.x : v[i][p].x;
-                    v[i][p].y = off[p].y > kMid ? a.y : v[i][p].y;
-                }
+                    for (int p = 0; p < NP; ++p) v[i][p] = mild(gate(i, p));
+            } else if (!__any_sync(kFull, big)) {
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) put(i, p, mild(gate(i, p)), strong(gate(i, p)));
+            } else {
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        const float2 g = gate(i, p);
+                        put(i, p, mild(g), make_float2(expf(g.x), expf(g.y)));
+                    }
+            }
         }
     }
     __device__ __forceinline__ float2 at(int i, int p) const {
