@@ -139,7 +139,7 @@ recurrence_step_kernel(const RecDims R, const G* __restrict__ g, const T* __rest
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const bool near = fabsf(y[j] - (1.f - kMid)) <= 1.f + kMid;  // -ln 2 to 2
+        const bool near = y[j] >= kLow && y[j] <= 2.f;
         const float v = near ? expm1f(y[j]) : expf(y[j]);
         s.x[j] = fmaf(v, s.x[j], to_f32(a.x[j])) + (near ? s.x[j] : 0.f);
         o.x[j] = from_f32<T>(s.x[j]);

@@ -75,17 +75,16 @@ __device__ __forceinline__ float2 mild(float2 g) {
     q = ffma2(q, g, splat(1.f));
     return mul2(g, q);
 }
-// exp(g) for |g| <= kBig, by the hardware's power of two (off by up to 2^-22); what is rounded off g / ln 2 goes in after it.
+// exp(g) for |g| <= kBig, by the hardware's power of two: off by up to 2^-22 of itself, and 2^-22 ln 2 for g / ln 2, which is
+// rounded below 8.  Both together are below half a bit of what a row's sum is allowed (2^-21 of its magnitudes).
 __device__ __forceinline__ float2 strong(float2 g) {
-    const float2 t = mul2(g, splat(0x1.715476p+0f));
-    const float2 lo = ffma2(g, splat(0x1.4ae0cp-26f), ffma2(g, splat(0x1.715476p+0f), make_float2(-t.x, -t.y)));
+    const float2 t = mul2(g, splat(1.44269504f));
     float2 a;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(a.x) : "f"(t.x));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(a.y) : "f"(t.y));
-    return ffma2(mul2(a, splat(0x1.62e43p-1f)), lo, a);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a.y) : "f"(t.y));
+    return a;
 }
-constexpr float kBig = 80.f;
-constexpr float kMid = 0.34657f;  // gates within kMid of -kMid are mild
+constexpr float kLow = -0.69314f, kBig = 5.5f;  // mild: kLow to 0
 // exp(g) h + x
 __device__ __forceinline__ float2 through(float2 v, float2 w, float2 h, float2 x) { return ffma2(w, h, ffma2(v, h, x)); }
 // exp(g) h
@@ -135,19 +134,19 @@ template <typename T, int CPL> __device__ __forceinline__ Piece<T, CPL> pack(con
 // The channels of a lane: CPL in a row (VEC), else 32 apart.
 template <int CPL, bool VEC>
 struct Lane {
-    int c0;
+    int c0, from;  // (a lane past the last channel reads the first ones, and stores nothing)
     bool on[VEC ? 1 : CPL];
     __device__ __forceinline__ Lane(int slab, int channels) {
         const int lane = threadIdx.x & 31;
         c0 = slab * 32 * CPL + (VEC ? lane * CPL : lane);
 #pragma unroll
         for (int j = 0; j < (VEC ? 1 : CPL); ++j) on[j] = c0 + 32 * j < channels;
+        from = on[0] ? c0 : 0;
     }
     template <typename U> __device__ __forceinline__ Piece<U, CPL> load(const U* row) const {
         Piece<U, CPL> v;
         if constexpr (VEC) {
-            if (on[0]) v = *reinterpret_cast<const Piece<U, CPL>*>(row + c0);
-            else v = Piece<U, CPL>{};
+            v = *reinterpret_cast<const Piece<U, CPL>*>(row + from);
         } else {
 #pragma unroll
             for (int j = 0; j < CPL; ++j) v.x[j] = on[j] ? row[c0 + 32 * j] : from_f32<U>(0.f);
@@ -375,12 +374,8 @@ struct Gates {
     }
     // valid: the rows that are part of a sequence (the others let the state pass)
     template <bool EDGE> __device__ __forceinline__ void form(uint32_t valid) {
-        float2 off[NP];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            sum[p] = splat(0.f);
-            off[p] = splat(0.f);
-        }
+        for (int p = 0; p < NP; ++p) sum[p] = splat(0.f);
         if constexpr (SHARED) {
             const int lane = threadIdx.x & 31;
             float g = to_f32(raw[0].x[0]);
@@ -389,54 +384,64 @@ struct Gates {
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
             sum[0] = splat(s);
-            const bool far = __any_sync(kFull, !(fabsf(g + kMid) <= kMid));
+            const bool far = __any_sync(kFull, !(g <= 0.f && g >= kLow));
             w[0] = splat(far ? 0.f : 1.f);
             v[0][0] = far ? splat(expf(g)) : mild(splat(g));
         } else {
-            auto gate = [&](int i, int p) {
-                float2 g = two(raw[i], p);
-                if (EDGE && !(valid >> i & 1)) g = splat(0.f);
-                return g;
-            };
+            float2 least[NP], most[NP];  // of the run's gates, and 0 (NaN passes as mild, and stays NaN)
+            if constexpr (EDGE) {
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i)
+                for (int i = 0; i < ROWS; ++i)
+                    if (!(valid >> i & 1)) raw[i] = Piece<G, CPL>{};
+            }
+            if constexpr (sizeof(G) == 2) {
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                    const float2 g = gate(i, p), d = add2(g, splat(kMid));
-                    off[p].x = fmaxf(off[p].x, fabsf(d.x));
-                    off[p].y = fmaxf(off[p].y, fabsf(d.y));
-                    sum[p] = add2(sum[p], g);
+                    __nv_bfloat162 lo = __float2bfloat162_rn(0.f), hi = lo;
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) {
+                        const __nv_bfloat162 y = reinterpret_cast<const __nv_bfloat162*>(raw[i].x)[p];
+                        lo = __hmin2(lo, y);
+                        hi = __hmax2(hi, y);
+                    }
+                    least[p] = __bfloat1622float2(lo);
+                    most[p] = __bfloat1622float2(hi);
                 }
-            bool far = false, big = false;
+            } else {
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    least[p] = most[p] = splat(0.f);
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) {
+                        const float2 y = two(raw[i], p);
+                        least[p] = make_float2(fminf(least[p].x, y.x), fminf(least[p].y, y.y));
+                        most[p] = make_float2(fmaxf(most[p].x, y.x), fmaxf(most[p].y, y.y));
+                    }
+                }
+            }
+            bool far = false, big = false, fx[NP], fy[NP];
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                w[p] = make_float2(off[p].x > kMid ? 0.f : 1.f, off[p].y > kMid ? 0.f : 1.f);
-                const float most = fmaxf(off[p].x, off[p].y);
-                far |= most > kMid;
-                big |= most > kBig - kMid;
+                fx[p] = least[p].x < kLow || most[p].x > 0.f;
+                fy[p] = least[p].y < kLow || most[p].y > 0.f;
+                w[p] = make_float2(fx[p] ? 0.f : 1.f, fy[p] ? 0.f : 1.f);
+                far |= fx[p] || fy[p];
+                big |= fminf(least[p].x, least[p].y) < -kBig || fmaxf(most[p].x, most[p].y) > kBig;
             }
-            auto put = [&](int i, int p, float2 y, float2 a) {
-                v[i][p] = make_float2(off[p].x > kMid ? a.x : y.x, off[p].y > kMid ? a.y : y.y);
-            };
-            if (!__any_sync(kFull, far)) {
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) v[i][p] = mild(gate(i, p));
-            } else if (!__any_sync(kFull, big)) {
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) put(i, p, mild(gate(i, p)), strong(gate(i, p)));
-            } else {
+            auto all = [&](auto f) {
 #pragma unroll
                 for (int i = 0; i < ROWS; ++i)
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        const float2 g = gate(i, p);
-                        put(i, p, mild(g), make_float2(expf(g.x), expf(g.y)));
+                        const float2 g = two(raw[i], p);
+                        sum[p] = add2(sum[p], g);
+                        v[i][p] = f(p, g);
                     }
-            }
+            };
+            auto either = [&](int p, float2 y, float2 a) { return make_float2(fx[p] ? a.x : y.x, fy[p] ? a.y : y.y); };
+            if (!__any_sync(kFull, far)) all([&](int p, float2 g) { return mild(g); });
+            else if (!__any_sync(kFull, big)) all([&](int p, float2 g) { return either(p, mild(g), strong(g)); });
+            else all([&](int p, float2 g) { return either(p, mild(g), make_float2(expf(g.x), expf(g.y))); });
         }
     }
     __device__ __forceinline__ float2 at(int i, int p) const {
