@@ -275,20 +275,13 @@ cudaError_t launch_linear4(const Linear4Dims& L, Rows4 kind, const void* x, cons
         rows = parts;
         D.sx = L.n_in;
     }
+    if (L.rows > 8) return launch_linear4_tc<T>(D, linear4_parts(kind), rows, w, scales, offsets, out, st);
     const int64_t stride = L.rows * L.n_in;
-    auto go = [&](auto rt, auto mt, auto group, auto np, auto offs) {
-        return run<T, decltype(rt)::value, decltype(mt)::value, decltype(group)::value, decltype(np)::value,
-                   decltype(offs)::value>(D, rows, stride, w, scales, offsets, out, st);
-    };
-    auto with_rows = [&](auto group, auto np, auto offs) {
-        using std::integral_constant;
-        if (L.rows <= 8) return go(integral_constant<int, 1>(), integral_constant<int, 1>(), group, np, offs);
-        if (L.rows <= 16) return go(integral_constant<int, 2>(), integral_constant<int, 2>(), group, np, offs);
-        if (L.rows <= 32) return go(integral_constant<int, 2>(), integral_constant<int, 4>(), group, np, offs);
-        return go(integral_constant<int, 1>(), integral_constant<int, 8>(), group, np, offs);
+    auto go = [&](auto group, auto np, auto offs) {
+        return run<T, 1, 1, decltype(group)::value, decltype(np)::value, decltype(offs)::value>(D, rows, stride, w, scales, offsets, out, st);
     };
     auto with_offsets = [&](auto group, auto np) {
-        return offsets ? with_rows(group, np, std::true_type()) : with_rows(group, np, std::false_type());
+        return offsets ? go(group, np, std::true_type()) : go(group, np, std::false_type());
     };
     auto with_group = [&](auto np) {
         if (L.group == 128) return with_offsets(std::integral_constant<int, 128>(), np);

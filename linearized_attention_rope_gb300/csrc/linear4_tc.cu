@@ -1,0 +1,401 @@
+// Products of more than eight rows with 4-bit weights on the 5th-generation tensor cores.
+//
+// D [128 rows of W, N tokens] = A B^T per group of inputs: A = q - 8 in bf16 (exact, as every product is), B the
+// tokens' rows.  A row's sums of a group are read back, scaled in fp32 and added to the row's own registers, so that no
+// weight is rounded; offsets times the group's sums of x, which a product with ones gives.
+//
+// A block takes 128 rows and, in a cluster of C blocks, a C-th of the inputs, 128 at a time:
+//   one warp     brings tiles of W (128 x 64 bytes) and of x (N x 128, in two blocks of 64) by TMA through a ring;
+//   four warps   take their rows' words from the ring, form q - 8 and put 64 inputs at a time into tensor memory, which
+//                A is read from (three such buffers), so that shared memory holds a weight in half a byte only;
+//   one warp     issues the products, a group into one of two or four buffers of sums;
+//   four (eight) warps read a group's sums (32 tokens a thread at most), scale and add them up.
+// The cluster's sums are added through distributed shared memory, in order of its blocks.
+//
+// Bound, with 16 tokens, by the weights' bytes; with 64 by what an SM issues per 64 inputs of 128 rows: about 130
+// instructions of each unpacking warp and 60 of each adding warp.
+#include <algorithm>
+
+#include "layer.cuh"
+#include "tma.cuh"
+#include "umma.cuh"
+
+namespace hla {
+
+namespace {
+
+constexpr int kTile = 128;           // rows of W
+constexpr uint32_t kPolls = 1u << 22;
+constexpr int kABuf = 3;             // buffers of A, 64 inputs in 32 columns each
+constexpr uint32_t kOnes = 96;       // columns: A, ones, sums
+constexpr uint32_t kSums = 128;
+
+template <int N, int PARTS, bool OFFS>
+struct Shape {
+    static constexpr int kAdd = N > 32 ? 8 : 4;  // adding warps
+    static constexpr int kPer = N > 32 ? 32 : N;  // tokens of an adding thread
+    static constexpr int kWarps = 6 + kAdd, kThreads = 32 * kWarps;
+    static constexpr int kBufs = (N == 16 || (N == 32 && !OFFS)) ? 4 : 2;  // of sums
+    static constexpr uint32_t kCols = kSums + kBufs * N * (OFFS ? 2 : 1) > 256 ? 512 : 256;
+    static constexpr int kW = kTile * 64, kX = N * 128;  // bytes of a stage's W, of 64 inputs of x
+    static constexpr int kStage = kW + 2 * PARTS * kX;
+    static constexpr int kStages = std::max(2, std::min(8, 102400 / kStage));
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage;
+    static constexpr size_t kNeed = std::max<size_t>(kSmem, 1024 + (size_t)N * kTile * 4);
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t local, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+// Eight weights of a word less 8, as four pairs of bf16: 0x4300 | q is 128 + q.
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t* o) {
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu, off = 0x43084308u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t y = (__byte_perm(even, odd, i | 4 << 4 | (4 + i) << 8 | 4 << 12) & 0x00ff00ffu) | 0x43004300u;
+        const __nv_bfloat162 d = __hsub2(reinterpret_cast<const __nv_bfloat162&>(y), reinterpret_cast<const __nv_bfloat162&>(off));
+        o[i] = reinterpret_cast<const uint32_t&>(d);
+    }
+}
+
+// A place in a ring of n barriers, and the parity of the phase it is in.
+struct Ring {
+    int i = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            turn ^= 1;
+        }
+    }
+};
+
+template <typename T, int N, int PARTS, bool OFFS>
+__global__ void __launch_bounds__(Shape<N, PARTS, OFFS>::kThreads, Shape<N, PARTS, OFFS>::kCols == 256 && PARTS == 1 ? 2 : 1)
+linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Linear4Dims L,
+                  const T* __restrict__ scales, const T* __restrict__ offsets, T* __restrict__ out, int n_split) {
+    using S = Shape<N, PARTS, OFFS>;
+    extern __shared__ uint8_t raw[];
+    __shared__ alignas(8) uint64_t bars[2 * S::kStages + 2 * kABuf + 2 * S::kBufs + 1];
+    __shared__ uint32_t tmem_at;
+    __shared__ int bad;
+    const uint32_t ring = (umma::smem_addr(raw) + 1023u) & ~1023u;
+    float* const part = reinterpret_cast<float*>(raw + (ring - umma::smem_addr(raw)));  // [token][row], at the end
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = n_split > 1 ? cluster_rank() : 0;
+    const int n0 = blockIdx.x / n_split * kTile;
+    const int64_t m0 = (int64_t)blockIdx.y * N;
+    const int n_groups = L.n_in / L.group, stages = (L.n_in + 127) / 128, halves = (L.n_in + 63) / 64;
+    const int s0 = (int)((int64_t)stages * rank / n_split), s1 = (int)((int64_t)stages * (rank + 1) / n_split);
+    const int h0 = 2 * s0, h1 = min(2 * s1, halves);
+    auto bar = [&](int i) { return umma::smem_addr(bars + i); };
+    const int kFull = 0, kEmpty = S::kStages, kAFull = 2 * S::kStages, kAEmpty = kAFull + kABuf, kDFull = kAEmpty + kABuf,
+              kDEmpty = kDFull + S::kBufs, kEnd = kDEmpty + S::kBufs;
+    if (threadIdx.x == 0) {
+        bad = 0;
+        for (int i = 0; i < S::kStages; ++i) {
+            umma::mbar_init(bar(kFull + i), 1);
+            umma::mbar_init(bar(kEmpty + i), 5);  // four unpacking warps, and the products
+        }
+        for (int i = 0; i < kABuf; ++i) {
+            umma::mbar_init(bar(kAFull + i), 4);
+            umma::mbar_init(bar(kAEmpty + i), 1);
+        }
+        for (int i = 0; i < S::kBufs; ++i) {
+            umma::mbar_init(bar(kDFull + i), 1);
+            umma::mbar_init(bar(kDEmpty + i), S::kAdd);
+        }
+        umma::mbar_init(bar(kEnd), 1);
+        umma::fence_mbar_init();
+    }
+    if (warp == 0) umma::tmem_alloc(&tmem_at, S::kCols);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = tmem_at;
+    // Every wait ends: one that runs out leaves the block's outputs NaN.
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        const bool ok = umma::mbar_try_wait(bar(i), parity) ||
+                        (!*(volatile int*)&bad && umma::mbar_wait(bar(i), parity, kPolls));
+        if (!__all_sync(0xffffffffu, ok)) {
+            bad = 1;
+            return false;
+        }
+        return true;
+    };
+    float2 acc[S::kPer / 2];
+#pragma unroll
+    for (int i = 0; i < S::kPer / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+
+    if (warp < 4) {  // unpacking
+        const int row = warp * 32 + lane;
+        if constexpr (OFFS) {
+            uint32_t ones[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ones[i] = 0x3f803f80u;
+            umma::tmem_st16_async(tmem + ((uint32_t)warp << 21) + kOnes, ones);
+        }
+        Ring in, a;
+        bool go = true;
+        for (int s = s0; s < s1 && go; ++s) {
+            go = wait(kFull + in.i, in.turn);
+            if (!go) break;
+            const uint32_t at = ring + in.i * S::kStage + row * 64;
+            for (int h = 0; h < 2 && 2 * s + h < h1; ++h) {
+                uint32_t w[8];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)  // 16-byte chunks, swizzled over 64 bytes
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                                 : "r"(at + (((uint32_t)(2 * h + c) ^ ((uint32_t)row >> 1 & 3u)) << 4)));
+                go = wait(kAEmpty + a.i, a.turn ^ 1);
+                if (!go) break;
+                umma::fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) unpack8(w[4 * c + i], o + 4 * i);
+                    umma::tmem_st16_async(tmem + ((uint32_t)warp << 21) + a.i * 32 + 16 * c, o);
+                }
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(bar(kAFull + a.i));
+                a.next(kABuf);
+            }
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(bar(kEmpty + in.i));
+            in.next(S::kStages);
+        }
+    } else if (warp == 4) {  // loads
+        Ring in;
+        int loaded = 0;
+        for (int s = s0; s < s1; ++s) {
+            if (!wait(kEmpty + in.i, in.turn ^ 1)) break;
+            if (lane == 0) {
+                const uint32_t at = ring + in.i * S::kStage, full = bar(kFull + in.i);
+                const int hs = min(2, h1 - 2 * s);
+                tma::expect_tx(full, S::kW + hs * PARTS * S::kX);
+                tma::tensor_load_2d(at, &map_w, s * 64, n0, full);
+                for (int h = 0; h < hs; ++h)
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+                        tma::tensor_load_2d(at + S::kW + (h * PARTS + p) * S::kX, &map_x, s * 128 + h * 64,
+                                            (int)(p * L.rows + m0), full);
+            }
+            __syncwarp();
+            ++loaded;
+            in.next(S::kStages);
+        }
+        if (*(volatile int*)&bad) {  // copies in flight end before the block does
+            Ring r;
+            for (int k = 0; k < loaded; ++k) {
+                if (k + S::kStages >= loaded) umma::mbar_wait(bar(kFull + r.i), r.turn, kPolls);
+                r.next(S::kStages);
+            }
+        }
+    } else if (warp == 5) {  // products
+        const uint32_t lead = umma::elect_one(), idesc = umma::idesc_bf16(kTile, N, false, false);
+        Ring in, a, d;
+        const int per = L.group / 16;  // products of a group
+        bool go = true, open = false;
+        for (int h = h0; h < h1 && go; ++h) {
+            if ((h & 1) == 0) go = wait(kFull + in.i, in.turn);
+            go = go && wait(kAFull + a.i, a.turn);
+            if (!go) break;
+            umma::fence_after_sync();
+            const uint32_t xb = ring + in.i * S::kStage + S::kW + (h & 1) * PARTS * S::kX;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int step = h * 4 + k;
+                if (!open) {
+                    go = wait(kDEmpty + d.i, d.turn ^ 1);
+                    if (!go) break;
+                    umma::fence_after_sync();
+                }
+                const uint32_t sums = tmem + kSums + d.i * N * (OFFS ? 2 : 1);
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) {
+                    const uint64_t b = umma::kmajor(xb + p * S::kX, N, k);
+                    umma::mma_ts_lead(sums, tmem + a.i * 32 + 8 * k, b, idesc, open || p > 0, lead);
+                    if constexpr (OFFS) umma::mma_ts_lead(sums + N, tmem + kOnes, b, idesc, open || p > 0, lead);
+                }
+                open = true;
+                if ((step + 1) % per == 0 || (h + 1 == h1 && k == 3)) {
+                    if (lead) umma::commit(bar(kDFull + d.i));
+                    d.next(S::kBufs);
+                    open = false;
+                }
+            }
+            if (!go) break;
+            if (lead) umma::commit(bar(kAEmpty + a.i));
+            a.next(kABuf);
+            if ((h & 1) || h + 1 == h1) {
+                if (lead) umma::commit(bar(kEmpty + in.i));
+                in.next(S::kStages);
+            }
+            __syncwarp();
+        }
+        if (!go) {  // (otherwise every product has been waited for, by those who add)
+            if (lead) umma::commit(bar(kEnd));
+            __syncwarp();
+            umma::mbar_wait(bar(kEnd), 0, kPolls);
+        }
+    } else {  // adding
+        const int u = warp - 6, quad = warp & 3, t0 = (u >> 2) * S::kPer;
+        const int row = n0 + quad * 32 + lane;
+        const int64_t at = (int64_t)min(row, L.n_out - 1) * n_groups;
+        const int g0 = s0 * 128 / L.group, g1 = (h1 * 64 + L.group - 1) / L.group;
+        auto scale_at = [&](const T* p, int g) { return to_f32(p[at + min(g, n_groups - 1)]); };
+        float sc = scale_at(scales, g0), of = OFFS ? scale_at(offsets, g0) : 0.f;
+        Ring d;
+        for (int g = g0; g < g1; ++g) {
+            const float sc1 = scale_at(scales, g + 1), of1 = OFFS ? scale_at(offsets, g + 1) : 0.f;
+            if (!wait(kDFull + d.i, d.turn)) break;
+            umma::fence_after_sync();
+            const uint32_t sums = tmem + ((uint32_t)quad << 21) + kSums + d.i * N * (OFFS ? 2 : 1) + t0;
+#pragma unroll
+            for (int k = 0; k < (OFFS ? 2 : 1); ++k) {
+                const float2 f = make_float2(k ? of : sc, k ? of : sc);
+#pragma unroll
+                for (int c = 0; c < S::kPer; c += 16) {
+                    float v[16];
+                    umma::tmem_ld16(sums + k * N + c, v);
+                    if (k == (OFFS ? 1 : 0) && c + 16 == S::kPer) {
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) umma::mbar_arrive(bar(kDEmpty + d.i));
+                    }
+                    if (g < n_groups) {  // (half a tile may lie behind the last group)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[c / 2 + i] = ffma2(f, make_float2(v[2 * i], v[2 * i + 1]), acc[c / 2 + i]);
+                    }
+                }
+            }
+            d.next(S::kBufs);
+            sc = sc1;
+            of = of1;
+        }
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const bool failed = bad;
+    if (warp == 0) umma::tmem_dealloc(tmem, S::kCols);
+    const float nan = __int_as_float(0x7fc00000);
+    if (n_split == 1) {
+        if (warp < 6) return;
+        const int u = warp - 6, t0 = (u >> 2) * S::kPer, row = n0 + (warp & 3) * 32 + lane;
+        if (row >= L.n_out) return;
+#pragma unroll
+        for (int i = 0; i < S::kPer; ++i) {
+            const int64_t t = m0 + t0 + i;
+            const float y = i & 1 ? acc[i / 2].y : acc[i / 2].x;
+            if (t < L.rows) out[t * L.n_out + row] = from_f32<T>(failed ? nan : y);
+        }
+        return;
+    }
+    if (warp >= 6) {
+        const int u = warp - 6, t0 = (u >> 2) * S::kPer, row = (warp & 3) * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < S::kPer; ++i) part[(t0 + i) * kTile + row] = failed ? nan : i & 1 ? acc[i / 2].y : acc[i / 2].x;
+    }
+    cluster_sync_all();
+    const int t0 = (int)(N * rank / n_split), t1 = (int)(N * (rank + 1) / n_split);
+    for (int i = t0 * kTile + threadIdx.x; i < t1 * kTile; i += S::kThreads) {
+        const int64_t t = m0 + i / kTile;
+        const int row = n0 + i % kTile;
+        if (t >= L.rows || row >= L.n_out) continue;
+        float y = 0.f;
+        for (int c = 0; c < n_split; ++c) y += ld_cluster(umma::smem_addr(part + i), c);
+        out[t * L.n_out + row] = from_f32<T>(y);
+    }
+    cluster_sync_all();  // no block leaves while its sums are read
+}
+
+template <typename T, int N, int PARTS, bool OFFS>
+cudaError_t run(const CUtensorMap& map_w, const CUtensorMap& map_x, const Linear4Dims& L, const T* scales, const T* offsets,
+                T* out, int n_split, cudaStream_t st) {
+    using S = Shape<N, PARTS, OFFS>;
+    static DeviceCache cache;
+    cudaError_t e = device_cached(cache, nullptr, [](int, int*) {
+        return cudaFuncSetAttribute(linear4_tc_kernel<T, N, PARTS, OFFS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kNeed);
+    });
+    if (e != cudaSuccess) return e;
+    const int tiles = (L.n_out + kTile - 1) / kTile;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * n_split), (unsigned)((L.rows + N - 1) / N));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kNeed;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)n_split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = n_split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear4_tc_kernel<T, N, PARTS, OFFS>, map_w, map_x, L, scales, offsets, out, n_split);
+}
+
+// Blocks of a cluster: of 1, 2, 4 and 8 the one with the shortest sum of rounds (two blocks an SM) by tiles, where a block
+// spends about six tiles' time on its start and its end.
+int split(const Linear4Dims& L, int64_t tiles) {
+    const int64_t stages = (L.n_in + 127) / 128;
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int c = 1; c <= 8; c *= 2) {
+        if (c > 1 && c > stages) break;
+        const int64_t cost = (tiles * c + 303) / 304 * ((stages + c - 1) / c + 6);
+        if (cost < least) {
+            least = cost;
+            best = c;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat16* x, const uint8_t* w, const T* scales,
+                              const T* offsets, T* out, cudaStream_t st) {
+    const int n = L.rows <= 16 ? 16 : L.rows <= 32 ? 32 : 64;
+    CUtensorMap map_w, map_x;
+    if (!tma::make_map_2d(&map_w, w, 1, (uint64_t)L.n_in / 2, (uint64_t)L.n_out, (uint64_t)L.n_in / 2, 64, kTile) ||
+        !tma::make_map_2d(&map_x, x, 2, (uint64_t)L.n_in, (uint64_t)L.rows * parts, (uint64_t)L.sx * 2, 64, (uint32_t)n))
+        return cudaErrorInvalidValue;
+    const int c = split(L, (int64_t)((L.n_out + kTile - 1) / kTile) * ((L.rows + n - 1) / n));
+    auto go = [&](auto nn, auto np, auto offs) {
+        return run<T, decltype(nn)::value, decltype(np)::value, decltype(offs)::value>(map_w, map_x, L, scales, offsets, out, c, st);
+    };
+    auto with_parts = [&](auto nn, auto offs) {
+        return parts == 3 ? go(nn, std::integral_constant<int, 3>(), offs) : go(nn, std::integral_constant<int, 1>(), offs);
+    };
+    auto with_rows = [&](auto offs) {
+        if (n == 16) return with_parts(std::integral_constant<int, 16>(), offs);
+        if (n == 32) return with_parts(std::integral_constant<int, 32>(), offs);
+        return with_parts(std::integral_constant<int, 64>(), offs);
+    };
+    return offsets ? with_rows(std::true_type()) : with_rows(std::false_type());
+}
+
+template cudaError_t launch_linear4_tc<float>(const Linear4Dims&, int, const __nv_bfloat16*, const uint8_t*, const float*,
+                                              const float*, float*, cudaStream_t);
+template cudaError_t launch_linear4_tc<__nv_bfloat16>(const Linear4Dims&, int, const __nv_bfloat16*, const uint8_t*,
+                                                      const __nv_bfloat16*, const __nv_bfloat16*, __nv_bfloat16*, cudaStream_t);
+
+}  // namespace hla

@@ -264,15 +264,16 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
             if (lane == 0) status[i] = have;
         }
         __syncthreads();
-        bool gone = false;
-        m = kLook;
-        for (int w = deep * kWarps - 1; w >= 0; --w) {  // (every one has something by now)
-            const int s = status[w];
-            gone |= s == 3;
-            m = s == 2 ? w : m;
+        const int got = status[lane % kLook];
+        const unsigned ready = __ballot_sync(kFull, got == 2);
+        if (__any_sync(kFull, got == 3)) {
+            m = -1;
+            break;
         }
-        if (gone) m = -1;
-        if (m < kLook) break;
+        if (ready) {  // (the tiles between have their (A, B))
+            m = __ffs(ready) - 1;
+            break;
+        }
         if (deep < kDeep) ++deep;
         __syncthreads();  // before status is written again
     }

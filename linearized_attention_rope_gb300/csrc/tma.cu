@@ -43,5 +43,20 @@ bool make_map_3d_strided(CUtensorMap* map, const void* base, bool bf16, uint64_t
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_2d(CUtensorMap* map, const void* base, int bytes, uint64_t n0, uint64_t n1, uint64_t stride1, uint32_t b0,
+                 uint32_t b1) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    const uint32_t inner = b0 * (uint32_t)bytes;
+    if (!fn || !base || n0 == 0 || n1 == 0 || (inner != 64 && inner != 128)) return false;
+    const cuuint64_t dims[2] = {n0, n1};
+    const cuuint64_t strides[1] = {stride1};
+    const cuuint32_t box[2] = {b0, b1};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(map, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+              dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace tma
 }  // namespace hla

@@ -25,6 +25,10 @@ bool make_map_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t n0, uin
 // The same with the byte stride between the outermost rows (a multiple of 16) given.
 bool make_map_3d_strided(CUtensorMap* map, const void* base, bool bf16, uint64_t n0, uint64_t n1, uint64_t n2,
                          uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2);
+// A 2-D map over [n1][n0] of bytes (bytes = 1) or bf16 (2), `stride1` bytes (a multiple of 16) from a row to the next, with box
+// (b0, b1); b0 values are 64 bytes, swizzled over those, or 128, over those.
+bool make_map_2d(CUtensorMap* map, const void* base, int bytes, uint64_t n0, uint64_t n1, uint64_t stride1, uint32_t b0,
+                 uint32_t b1);
 // The (64, 1, 64) fp16 box used for chunks of 64 token rows.
 inline bool make_map_f16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2) {
     return make_map_3d(map, base, false, n0, n1, n2, 64, 1, 64);
@@ -48,6 +52,14 @@ __device__ __forceinline__ void tensor_load_3d(uint32_t dst, const CUtensorMap* 
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
         "[%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(mbar)
+        : "memory");
+}
+
+// Box (x, y) of a 2-D map.
+__device__ __forceinline__ void tensor_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
         : "memory");
 }
 
