@@ -127,13 +127,13 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     const uint32_t tmem = tmem_at;
     // Every wait ends: one that runs out leaves the block's outputs NaN.
     auto wait = [&](int i, uint32_t parity) -> bool {
-        const bool ok = umma::mbar_try_wait(bar(i), parity) ||
-                        (!*(volatile int*)&bad && umma::mbar_wait(bar(i), parity, kPolls));
-        if (!__all_sync(0xffffffffu, ok)) {
-            bad = 1;
-            return false;
-        }
-        return true;
+#pragma unroll 1
+        for (int k = 0; k < 256; ++k)  // (the bounded wait below reads the time, which takes longer than most waits do)
+            if (__all_sync(0xffffffffu, umma::mbar_try_wait(bar(i), parity))) return true;
+        const bool ok = !*(volatile int*)&bad && umma::mbar_wait(bar(i), parity, kPolls);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        bad = 1;
+        return false;
     };
     float2 acc[S::kPer / 2];
 #pragma unroll
@@ -153,13 +153,15 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             go = wait(kFull + in.i, in.turn);
             if (!go) break;
             const uint32_t at = ring + in.i * S::kStage + row * 64;
-            for (int h = 0; h < 2 && 2 * s + h < h1; ++h) {
-                uint32_t w[8];
+            uint32_t w[16];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)  // 16-byte chunks, swizzled over 64 bytes
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
-                                 : "r"(at + (((uint32_t)(2 * h + c) ^ ((uint32_t)row >> 1 & 3u)) << 4)));
+            for (int c = 0; c < 4; ++c)  // 16-byte chunks, swizzled over 64 bytes
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                             : "r"(at + (((uint32_t)c ^ ((uint32_t)row >> 1 & 3u)) << 4)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (2 * s + h >= h1) break;
                 go = wait(kAEmpty + a.i, a.turn ^ 1);
                 if (!go) break;
                 umma::fence_after_sync();
@@ -167,7 +169,7 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 for (int c = 0; c < 2; ++c) {
                     uint32_t o[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) unpack8(w[4 * c + i], o + 4 * i);
+                    for (int i = 0; i < 4; ++i) unpack8(w[8 * h + 4 * c + i], o + 4 * i);
                     umma::tmem_st16_async(tmem + ((uint32_t)warp << 21) + a.i * 32 + 16 * c, o);
                 }
                 umma::tmem_wait_st();
@@ -176,8 +178,7 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 if (lane == 0) umma::mbar_arrive(bar(kAFull + a.i));
                 a.next(kABuf);
             }
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(bar(kEmpty + in.i));
+            if (lane == 0) umma::mbar_arrive(bar(kEmpty + in.i));  // (after the last __syncwarp: every lane has its words)
             in.next(S::kStages);
         }
     } else if (warp == 4) {  // loads
@@ -209,46 +210,49 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         }
     } else if (warp == 5) {  // products
         const uint32_t lead = umma::elect_one(), idesc = umma::idesc_bf16(kTile, N, false, false);
-        Ring in, a, d;
-        const int per = L.group / 16;  // products of a group
-        bool go = true, open = false;
-        for (int h = h0; h < h1 && go; ++h) {
-            if ((h & 1) == 0) go = wait(kFull + in.i, in.turn);
-            go = go && wait(kAFull + a.i, a.turn);
-            if (!go) break;
-            umma::fence_after_sync();
-            const uint32_t xb = ring + in.i * S::kStage + S::kW + (h & 1) * PARTS * S::kX;
+        const uint64_t b0 = umma::kmajor(ring + S::kW, N, 0);
+        // A group's sums over PER products; straight code, as one warp issues for all others (with the group's size as a
+        // variable a product took 250 cycles to issue).
+        auto issue = [&](auto per) -> bool {
+            constexpr int PER = decltype(per)::value;
+            Ring in, a, d;
+            for (int h = h0; h < h1; ++h) {
+                if ((h & 1) == 0 && !wait(kFull + in.i, in.turn)) return false;
+                if (!wait(kAFull + a.i, a.turn)) return false;
+                const uint64_t b = b0 + (uint64_t)((in.i * S::kStage + (h & 1) * PARTS * S::kX) >> 4);
+                const uint32_t at = tmem + a.i * 32;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int step = h * 4 + k;
-                if (!open) {
-                    go = wait(kDEmpty + d.i, d.turn ^ 1);
-                    if (!go) break;
-                    umma::fence_after_sync();
-                }
-                const uint32_t sums = tmem + kSums + d.i * N * (OFFS ? 2 : 1);
+                for (int k = 0; k < 4; ++k) {
+                    const bool first = PER == 8 ? k == 0 && (h & 1) == 0 : k % PER == 0;
+                    if (PER == 8 ? k == 0 : k % PER == 0) {
+                        if (first && !wait(kDEmpty + d.i, d.turn ^ 1)) return false;
+                        umma::fence_after_sync();
+                    }
+                    const uint32_t sums = tmem + kSums + d.i * N * (OFFS ? 2 : 1);
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    const uint64_t b = umma::kmajor(xb + p * S::kX, N, k);
-                    umma::mma_ts_lead(sums, tmem + a.i * 32 + 8 * k, b, idesc, open || p > 0, lead);
-                    if constexpr (OFFS) umma::mma_ts_lead(sums + N, tmem + kOnes, b, idesc, open || p > 0, lead);
+                    for (int p = 0; p < PARTS; ++p) {
+                        umma::mma_ts_lead(sums, at + 8 * k, b + p * (S::kX >> 4) + 2 * k, idesc, !first || p > 0, lead);
+                        if constexpr (OFFS)
+                            umma::mma_ts_lead(sums + N, tmem + kOnes, b + p * (S::kX >> 4) + 2 * k, idesc, !first || p > 0, lead);
+                    }
+                    if (PER == 8 ? k == 3 && (h & 1) : k % PER == PER - 1) {
+                        if (lead) umma::commit(bar(kDFull + d.i));
+                        d.next(S::kBufs);
+                    }
                 }
-                open = true;
-                if ((step + 1) % per == 0 || (h + 1 == h1 && k == 3)) {
-                    if (lead) umma::commit(bar(kDFull + d.i));
-                    d.next(S::kBufs);
-                    open = false;
+                if (lead) umma::commit(bar(kAEmpty + a.i));
+                a.next(kABuf);
+                if ((h & 1) || h + 1 == h1) {
+                    if (lead) umma::commit(bar(kEmpty + in.i));
+                    in.next(S::kStages);
                 }
+                __syncwarp();
             }
-            if (!go) break;
-            if (lead) umma::commit(bar(kAEmpty + a.i));
-            a.next(kABuf);
-            if ((h & 1) || h + 1 == h1) {
-                if (lead) umma::commit(bar(kEmpty + in.i));
-                in.next(S::kStages);
-            }
-            __syncwarp();
-        }
+            return true;
+        };
+        const bool go = L.group == 128  ? issue(std::integral_constant<int, 8>())
+                        : L.group == 64 ? issue(std::integral_constant<int, 4>())
+                                        : issue(std::integral_constant<int, 2>());
         if (!go) {  // (otherwise every product has been waited for, by those who add)
             if (lead) umma::commit(bar(kEnd));
             __syncwarp();
