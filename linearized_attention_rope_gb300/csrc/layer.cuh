@@ -20,6 +20,41 @@ __device__ __forceinline__ float group_pow2(int e) {  // -127 <= e <= 127
     return e > -127 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(0x400000u);
 }
 
+// Thread-block clusters along x.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at the same shared-memory offset as `local` in block `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster(const float* local, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+struct ClusterCfg {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    ClusterCfg(dim3 grid, int threads, size_t smem, cudaStream_t st, int blocks) {
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)blocks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = blocks > 1 ? 1 : 0;
+    }
+    ClusterCfg(const ClusterCfg&) = delete;
+    ClusterCfg& operator=(const ClusterCfg&) = delete;
+};
+
 struct NormDims {
     int64_t rows, sx, sr;  // rows of n_cols values; token strides of x and the residual
     int cols, heads, group;
@@ -54,11 +89,16 @@ template <typename T, typename G>
 cudaError_t launch_recurrence_step(const RecDims& R, const G* g, const T* x, float* h, T* out, cudaStream_t st);
 
 // Products with 4-bit weights: w [n_out][n_in / 2] bytes, the even input in the low half; scales and offsets
-// [n_out][n_in / group].  Rows of x as bf16 parts in `parts` where they are not bf16 on 16-byte boundaries.
+// [n_out][n_in / group].  More than kFewRows rows of x as bf16 parts in
+// `parts`, where they are not bf16 on 16-byte boundaries.
 struct Linear4Dims {
     int64_t rows, sx;  // tokens; token stride of x in elements
     int n_in, n_out, group, x_group;
 };
+constexpr int64_t kFewRows = 16;  // that no rows are laid out for
+// Blocks of a cluster that share a tile's inputs: of 1, 2, 4 and 8 the one with the least sum of rounds (of `blocks` at a
+// time) by steps, where a block's start and end take as long as `ends` steps.
+int linear4_split(int64_t tiles, int64_t stages, int64_t blocks, int64_t ends);
 enum class Rows4 { kF32, kBf16, kE4m3 };
 int linear4_parts(Rows4 kind);
 template <typename T>

@@ -1,18 +1,17 @@
-// Products of a few rows with 4-bit weights: y = x W^T, W[n][k] = scale (q - 8)
-// + offset, a scale (and offset) per row n and group of 32, 64 or 128 inputs k.
+// Products of up to sixteen rows with 4-bit weights: y = x W^T, W[n][k] = scale (q - 8) + offset, a scale (and offset)
+// per row n and group of 32, 64 or 128 inputs k.  (More rows: linear4_tc.cu, for which rows are laid out here.)
 //
-// Bound by the weights' bytes: half a byte each, read once per 64 rows of x.
-// Products on the warp-level tensor instruction (m16n8k16, bf16 in, fp32 sums):
-// the 16 rows are rows of W, the 8 columns tokens.  q - 8 is exact in bf16 and so
-// is every product; a group's sum is scaled in fp32 as it is added to the row's.
-// (Scaled weights would have to be rounded to bf16 each.)  Which k a lane's
-// operands stand for is free, as long as both operands agree: a lane takes 16
-// bytes of a weight row as they lie, and the same 32 inputs of its token.
-// Offsets: the group's sum of x, from a product with ones, times the offset.
+// Bound by the weights' bytes, half a byte each.  Products on the warp-level tensor instruction (m16n8k16, bf16 in,
+// fp32 sums): the 16 rows are rows of W, the 8 columns tokens; a weight goes from memory to its one lane's registers,
+// which tensor memory would have it leave again.  q - 8 is exact in bf16 and so is every product; a group's sum is scaled
+// in fp32 as it is added to the row's.  (Scaled weights would have to be rounded to bf16 each.)  Which k a lane's
+// operands stand for is free, as long as both agree: a lane takes words of a weight row as they lie.
 //
-// fp32 rows enter as three bf16 parts, cut off 8 bits at a time (nothing is
-// lost), 8-bit rows as bf16 (exact, too): a small launch before the product
-// writes the parts.
+// A block takes 128 or 256 rows, 16 or 32 a warp, and, in a cluster of C, a C-th of the inputs; the tokens' inputs and the
+// rows' scales come into shared memory 1024 inputs at a time, in the order in which lanes read them: fp32 rows as three
+// bf16 parts, cut off 8 bits at a time (nothing is lost), 8-bit rows as bf16 (exact, too).  Offsets are multiplied by the
+// group's sum of x, formed on that way.  Weights are two steps (of 128 inputs) ahead of the products.  The cluster's
+// sums are added through distributed shared memory, in order of its blocks.
 #include <algorithm>
 
 #include "layer.cuh"
@@ -21,7 +20,7 @@ namespace hla {
 
 namespace {
 
-constexpr int kWarps4 = 8;
+constexpr int kWarps4 = 8, kThreads4 = 32 * kWarps4;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -35,36 +34,77 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t w, int s) {
     return reinterpret_cast<const uint32_t&>(d);
 }
 
-// RT: tiles of 16 weight rows of a block; MT: tiles of 8 tokens; PARTS: of x.
-// A block's eight warps take the row tiles' groups of 128 inputs in turn, and add up at the end, in order.
-template <typename T, int RT, int MT, int GROUP, int PARTS, bool OFFS>
-__global__ void __launch_bounds__(32 * kWarps4)
-linear4_kernel(const Linear4Dims L, const __nv_bfloat16* __restrict__ x, int64_t part_stride, const uint8_t* __restrict__ w,
-               const T* __restrict__ scales, const T* __restrict__ offsets, T* __restrict__ out) {
-    constexpr int kWords = GROUP / 32;  // 32-bit words of a lane per group: 8 inputs each
-    extern __shared__ float sums[];     // [warp][token][row]
+// fp32 as three bf16 parts; an infinity or NaN is in the first alone.
+__device__ __forceinline__ void three_parts(float v, __nv_bfloat16 (&o)[3]) {
+    const bool fine = (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u;
+    if (v != v) v = __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+        const float top = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+        o[s] = from_f32<__nv_bfloat16>(top);
+        v = fine ? v - top : 0.f;
+    }
+}
+
+template <typename T, typename X, int RT, int MT, int GROUP, bool OFFS>
+struct Plan {
+    static constexpr int kParts = sizeof(X) == 4 ? 3 : 1;
+    static constexpr int kSteps = sizeof(X) == 4 ? 4 : 8;  // of 128 inputs, in shared memory
+    static constexpr int kRows = 16 * RT * kWarps4, kTok = 8 * MT;
+    static constexpr int kPitch = kSteps * 256 + 64;  // bytes of a token: two rows' 64 bytes lie in different banks
+    static constexpr int kGroups = kSteps * (128 / GROUP);
+    static constexpr int kScalePitch = kRows + 2;
+    static constexpr size_t kX = (size_t)kParts * kTok * kPitch, kScale = (size_t)kGroups * kScalePitch * sizeof(T);
+    static constexpr size_t kIn = kX + kScale * (OFFS ? 2 : 1) + (OFFS ? (size_t)kGroups * kTok * 4 : 0);
+    static constexpr size_t kSmem = std::max<size_t>(kIn, (size_t)kTok * kRows * 4);
+};
+
+template <typename T, typename X, int RT, int MT, int GROUP, bool OFFS>
+__global__ void __launch_bounds__(kThreads4, 2)
+linear4_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t* __restrict__ exps, const uint8_t* __restrict__ w,
+               const T* __restrict__ scales, const T* __restrict__ offsets, T* __restrict__ out, int n_split, bool vec) {
+    using S = Plan<T, X, RT, MT, GROUP, OFFS>;
+    constexpr int kWords = GROUP / 32, kSub = 128 / GROUP;  // words of a lane per group, groups of a step
+    extern __shared__ __align__(16) uint8_t sm[];
+    T* const sm_scale = reinterpret_cast<T*>(sm + S::kX);                // [group][row]
+    T* const sm_off = sm_scale + S::kScale / sizeof(T);
+    float* const sm_sum = reinterpret_cast<float*>(sm + S::kX + 2 * S::kScale);  // [group][token]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const int n0 = blockIdx.x * 16 * RT;
-    const int64_t m0 = (int64_t)blockIdx.y * 8 * MT;
-    const int n_groups = L.n_in / GROUP;
+    const uint32_t rank = n_split > 1 ? cluster_rank() : 0;
+    const int n0 = blockIdx.x / n_split * S::kRows, n_groups = L.n_in / GROUP, stages = (L.n_in + 127) / 128;
+    const int s0 = (int)((int64_t)stages * rank / n_split), s1 = (int)((int64_t)stages * (rank + 1) / n_split);
     const uint8_t* wr[RT][2];
-    int64_t sr[RT][2];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int n = min(n0 + r * 16 + h * 8 + gq, L.n_out - 1);
-            wr[r][h] = w + (int64_t)n * (L.n_in / 2) + tq * (kWords * 4);
-            sr[r][h] = (int64_t)n * n_groups;
-        }
-    const __nv_bfloat16* xr[MT];
-    bool on[MT];
+        for (int h = 0; h < 2; ++h)
+            wr[r][h] = w + (int64_t)min(n0 + warp * 16 * RT + r * 16 + h * 8 + gq, L.n_out - 1) * (L.n_in / 2) + tq * (kWords * 4);
+    uint32_t q[2][RT][2][4];
+    auto fetch = [&](uint32_t (&v)[RT][2][4], int s) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int64_t t = m0 + m * 8 + gq;
-        on[m] = t < L.rows;
-        xr[m] = x + (on[m] ? t : 0) * L.sx + tq * (kWords * 8);
-    }
+        for (int g = 0; g < kSub; ++g) {
+            // (a group may lie behind the last one: zeros there, and nothing to multiply)
+            const bool on = s < s1 && (GROUP == 128 || s * kSub + g < n_groups);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t* p = wr[r][h] + (int64_t)s * 64 + g * (GROUP / 2);
+                    uint32_t* o = v[r][h] + g * kWords;
+                    if constexpr (kWords == 4) {
+                        const uint4 y = on ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+                        o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
+                    } else if constexpr (kWords == 2) {
+                        const uint2 y = on ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+                        o[0] = y.x; o[1] = y.y;
+                    } else {
+                        o[0] = on ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0;
+                    }
+                }
+        }
+    };
+    fetch(q[0], s0);
+    fetch(q[1], s0 + 1);
     float acc[RT][MT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -72,95 +112,171 @@ linear4_kernel(const Linear4Dims L, const __nv_bfloat16* __restrict__ x, int64_t
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][m][i] = 0.f;
-    const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    for (int c0 = s0; c0 < s1; c0 += S::kSteps) {
+        __syncthreads();
+        // the tokens' inputs, 8 at a time, where the lane that takes them has its four lanes' words in a row
 #pragma unroll 2
-    for (int g = warp; g < n_groups; g += kWarps4) {
-        uint32_t q[RT][2][kWords];
-        float sc[RT][2], of[RT][2];
+        for (int j = threadIdx.x; j < S::kTok * S::kSteps * 16; j += kThreads4) {
+            const int t = j / (S::kSteps * 16), c = j % (S::kSteps * 16);
+            const int64_t row = (int64_t)blockIdx.y * S::kTok + t;
+            const int k = c0 * 128 + c * 8;
+            float v[8];
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t* p = reinterpret_cast<const uint32_t*>(wr[r][h] + (int64_t)g * (GROUP / 2));
-                if constexpr (kWords == 4) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-                    q[r][h][0] = v.x; q[r][h][1] = v.y; q[r][h][2] = v.z; q[r][h][3] = v.w;
-                } else if constexpr (kWords == 2) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-                    q[r][h][0] = v.x; q[r][h][1] = v.y;
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            if (row < L.rows && k < L.n_in) {
+                const X* p = x + row * L.sx + k;
+                Piece<X, 8> y;
+                if (vec) {
+                    y = *reinterpret_cast<const Piece<X, 8>*>(p);
                 } else {
-                    q[r][h][0] = __ldg(p);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y.x[i] = p[i];
                 }
-                sc[r][h] = to_f32(scales[sr[r][h] + g]);
-                if (OFFS) of[r][h] = to_f32(offsets[sr[r][h] + g]);
+                if constexpr (sizeof(X) == 1) {
+                    const int group = L.x_group ? L.x_group : L.n_in;
+                    const float f = group_pow2((int)exps[row * (L.n_in / group) + k / group] - 127);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)y.x[i], __NV_E4M3))) * f;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = to_f32(y.x[i]);
+                }
             }
-        float part[RT][MT][4], total[MT][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                total[m][i] = 0.f;
-#pragma unroll
-                for (int r = 0; r < RT; ++r) part[r][m][i] = 0.f;
-            }
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-            uint32_t a[RT][2][4];
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    a[r][s][0] = nibbles(q[r][0][k], 8 * s);
-                    a[r][s][1] = nibbles(q[r][1][k], 8 * s);
-                    a[r][s][2] = nibbles(q[r][0][k], 8 * s + 4);
-                    a[r][s][3] = nibbles(q[r][1][k], 8 * s + 4);
-                }
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (on[m]) v = __ldg(reinterpret_cast<const uint4*>(xr[m] + p * part_stride + (int64_t)g * GROUP + k * 8));
-                    const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
-                    const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        mma16816(part[r][m], a[r][0], b0, b1);
-                        mma16816(part[r][m], a[r][1], b2, b3);
-                    }
-                    if (OFFS) {
-                        mma16816(total[m], ones, b0, b1);
-                        mma16816(total[m], ones, b2, b3);
-                    }
-                }
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
+            constexpr int kIn = GROUP / 8;  // pieces of a group
+            const int in = c % 16 % kIn, at = c / 16 * 16 + (c % 16 / kIn * kWords + in % kWords) * 4 + in / kWords;
+            if constexpr (S::kParts == 1) {
+                Piece<__nv_bfloat16, 8> o;  // pairs (i, i + 4), as the weights' nibbles are taken
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    acc[r][m][i] = fmaf(sc[r][i >> 1], part[r][m][i], acc[r][m][i]);
-                    if (OFFS) acc[r][m][i] = fmaf(of[r][i >> 1], total[m][i], acc[r][m][i]);
+                    o.x[2 * i] = from_f32<__nv_bfloat16>(v[i]);
+                    o.x[2 * i + 1] = from_f32<__nv_bfloat16>(v[i + 4]);
                 }
+                *reinterpret_cast<Piece<__nv_bfloat16, 8>*>(sm + t * S::kPitch + at * 16) = o;
+            } else {
+                Piece<__nv_bfloat16, 8> o[3];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    __nv_bfloat16 lo[3], hi[3];
+                    three_parts(v[i], lo);
+                    three_parts(v[i + 4], hi);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        o[p].x[2 * i] = lo[p];
+                        o[p].x[2 * i + 1] = hi[p];
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    *reinterpret_cast<Piece<__nv_bfloat16, 8>*>(sm + (p * S::kTok + t) * S::kPitch + at * 16) = o[p];
+            }
+            if constexpr (OFFS) {
+                float y = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+#pragma unroll
+                for (int o = kIn / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                if (in == 0) sm_sum[c / kIn * S::kTok + t] = y;
+            }
+        }
+#pragma unroll 4
+        for (int i = threadIdx.x; i < S::kRows * S::kGroups; i += kThreads4) {
+            const int row = i / S::kGroups, g = i % S::kGroups, gg = c0 * kSub + g;
+            const int64_t from = (int64_t)min(n0 + row, L.n_out - 1) * n_groups + gg;
+            sm_scale[g * S::kScalePitch + row] = gg < n_groups ? scales[from] : from_f32<T>(0.f);
+            if constexpr (OFFS) sm_off[g * S::kScalePitch + row] = gg < n_groups ? offsets[from] : from_f32<T>(0.f);
+        }
+        __syncthreads();
+        auto step = [&](uint32_t (&v)[RT][2][4], int st) {
+#pragma unroll
+            for (int g = 0; g < kSub; ++g) {
+                float part[RT][MT][4];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) part[r][m][i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) {
+                    uint32_t a[RT][2][4];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const uint32_t lo = v[r][0][g * kWords + k], hi = v[r][1][g * kWords + k];
+                            a[r][s][0] = nibbles(lo, 8 * s);
+                            a[r][s][1] = nibbles(hi, 8 * s);
+                            a[r][s][2] = nibbles(lo, 8 * s + 4);
+                            a[r][s][3] = nibbles(hi, 8 * s + 4);
+                        }
+#pragma unroll
+                    for (int p = 0; p < S::kParts; ++p)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const uint4 b = *reinterpret_cast<const uint4*>(
+                                sm + (p * S::kTok + m * 8 + gq) * S::kPitch + (st * 16 + (g * kWords + k) * 4 + tq) * 16);
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) {
+                                mma16816(part[r][m], a[r][0], b.x, b.y);
+                                mma16816(part[r][m], a[r][1], b.z, b.w);
+                            }
+                        }
+                }
+                const int gi = st * kSub + g, row = warp * 16 * RT + gq;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    float2 sum;
+                    if constexpr (OFFS) sum = *reinterpret_cast<const float2*>(sm_sum + gi * S::kTok + m * 8 + tq * 2);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = gi * S::kScalePitch + row + r * 16 + h * 8;
+                            const float sc = to_f32(sm_scale[at]);
+                            float2 y = make_float2(acc[r][m][2 * h], acc[r][m][2 * h + 1]);
+                            y = ffma2(make_float2(sc, sc), make_float2(part[r][m][2 * h], part[r][m][2 * h + 1]), y);
+                            if constexpr (OFFS) {
+                                const float of = to_f32(sm_off[at]);
+                                y = ffma2(make_float2(of, of), sum, y);
+                            }
+                            acc[r][m][2 * h] = y.x;
+                            acc[r][m][2 * h + 1] = y.y;
+                        }
+                }
+            }
+        };
+        // (a group behind the last one: scale, offset and inputs are 0)
+        for (int st = 0; st < S::kSteps && c0 + st < s1; st += 2) {
+            step(q[0], st);
+            fetch(q[0], c0 + st + 2);
+            if (c0 + st + 1 < s1) {
+                step(q[1], st + 1);
+                fetch(q[1], c0 + st + 3);
+            }
+        }
     }
-    constexpr int kRows = 16 * RT, kTok = 8 * MT, kPitch = kRows + 1;
+    __syncthreads();
+    float* const sums = reinterpret_cast<float*>(sm);  // [token][row]
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                sums[(warp * kTok + m * 8 + tq * 2 + (i & 1)) * kPitch + r * 16 + (i >> 1) * 8 + gq] = acc[r][m][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRows * kTok; i += 32 * kWarps4) {
-        const int t = i / kRows, n = i - t * kRows;
-        if (m0 + t >= L.rows || n0 + n >= L.n_out) continue;
+                sums[(m * 8 + tq * 2 + (i & 1)) * S::kRows + warp * 16 * RT + r * 16 + (i >> 1) * 8 + gq] = acc[r][m][i];
+    if (n_split > 1) cluster_sync_all();
+    else __syncthreads();
+    const int t0 = (int)(S::kTok * rank / n_split), t1 = (int)(S::kTok * (rank + 1) / n_split);
+    for (int i = t0 * S::kRows + threadIdx.x; i < t1 * S::kRows; i += kThreads4) {
+        const int64_t t = (int64_t)blockIdx.y * S::kTok + i / S::kRows;
+        const int n = n0 + i % S::kRows;
+        if (t >= L.rows || n >= L.n_out) continue;
         float y = 0.f;
-#pragma unroll
-        for (int u = 0; u < kWarps4; ++u) y += sums[(u * kTok + t) * kPitch + n];
-        out[(m0 + t) * L.n_out + n0 + n] = from_f32<T>(y);
+        if (n_split == 1) y = sums[i];
+        else
+            for (int c = 0; c < n_split; ++c) y += ld_cluster(sums + i, c);
+        out[t * L.n_out + n] = from_f32<T>(y);
     }
+    if (n_split > 1) cluster_sync_all();  // no block leaves while its sums are read
 }
 
 // Rows as bf16 parts [parts][rows][n_in]: eight inputs a thread.
@@ -183,15 +299,10 @@ linear4_rows_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t*
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         if constexpr (sizeof(X) == 4) {
-            float v = p[j];
-            const bool fine = (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u;
-            if (v != v) v = __uint_as_float(0x7fc00000u);
+            __nv_bfloat16 y[3];
+            three_parts(p[j], y);
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-                const float top = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-                o[s].x[j] = from_f32<__nv_bfloat16>(top);
-                v = fine ? v - top : 0.f;
-            }
+            for (int s = 0; s < 3; ++s) o[s].x[j] = y[s];
         } else if constexpr (sizeof(X) == 1) {
             const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)p[j], __NV_E4M3);
             o[0].x[j] = from_f32<__nv_bfloat16>(__half2float(__half(h)) * scale);
@@ -240,21 +351,54 @@ linear4_quantize_kernel(const Linear4Dims L, const T* __restrict__ weight, uint8
     }
 }
 
-template <typename T, int RT, int MT, int GROUP, int PARTS, bool OFFS>
-cudaError_t run(const Linear4Dims& L, const __nv_bfloat16* x, int64_t part_stride, const uint8_t* w, const T* scales,
-                const T* offsets, T* out, cudaStream_t st) {
-    constexpr size_t sm = (size_t)kWarps4 * 8 * MT * (16 * RT + 1) * sizeof(float);
+template <typename T, typename X, int MT, int GROUP, bool OFFS>
+cudaError_t run(const Linear4Dims& L, const X* x, const uint8_t* exps, const uint8_t* w, const T* scales, const T* offsets,
+                T* out, cudaStream_t st) {
+    using S = Plan<T, X, 2, MT, GROUP, OFFS>;
+    const auto kernel = linear4_kernel<T, X, 2, MT, GROUP, OFFS>;
     static DeviceCache cache;
-    cudaError_t e = device_cached(cache, nullptr, [](int, int*) {
-        return cudaFuncSetAttribute(linear4_kernel<T, RT, MT, GROUP, PARTS, OFFS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    cudaError_t e = device_cached(cache, nullptr, [&](int, int*) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((L.n_out + 16 * RT - 1) / (16 * RT)), (unsigned)((L.rows + 8 * MT - 1) / (8 * MT)));
-    linear4_kernel<T, RT, MT, GROUP, PARTS, OFFS><<<grid, 32 * kWarps4, sm, st>>>(L, x, part_stride, w, scales, offsets, out);
-    return cudaGetLastError();
+    const int tiles = (L.n_out + S::kRows - 1) / S::kRows, c = linear4_split(tiles, (L.n_in + 127) / 128, 152, 2);
+    ClusterCfg cfg(dim3((unsigned)(tiles * c), (unsigned)((L.rows + S::kTok - 1) / S::kTok)), kThreads4, S::kSmem, st, c);
+    const bool vec = (uintptr_t)x % (8 * sizeof(X) > 16 ? 16 : 8 * sizeof(X)) == 0 && L.sx % 8 == 0;
+    return cudaLaunchKernelEx(&cfg.cfg, kernel, L, x, exps, w, scales, offsets, out, c, vec);
+}
+
+template <typename T, typename X>
+cudaError_t few(const Linear4Dims& L, const X* x, const uint8_t* exps, const uint8_t* w, const T* scales, const T* offsets,
+                T* out, cudaStream_t st) {
+    auto go = [&](auto mt, auto group, auto offs) {
+        return run<T, X, decltype(mt)::value, decltype(group)::value, decltype(offs)::value>(L, x, exps, w, scales, offsets, out, st);
+    };
+    auto with_offsets = [&](auto mt, auto group) {
+        return offsets ? go(mt, group, std::true_type()) : go(mt, group, std::false_type());
+    };
+    auto with_group = [&](auto mt) {
+        if (L.group == 128) return with_offsets(mt, std::integral_constant<int, 128>());
+        if (L.group == 64) return with_offsets(mt, std::integral_constant<int, 64>());
+        return with_offsets(mt, std::integral_constant<int, 32>());
+    };
+    return L.rows <= 8 ? with_group(std::integral_constant<int, 1>()) : with_group(std::integral_constant<int, 2>());
 }
 
 }  // namespace
+
+int linear4_split(int64_t tiles, int64_t stages, int64_t blocks, int64_t ends) {
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int c = 1; c <= 8; c *= 2) {
+        if (c > 1 && c > stages) break;
+        const int64_t cost = (tiles * c + blocks - 1) / blocks * ((stages + c - 1) / c + ends);
+        if (cost < least) {
+            least = cost;
+            best = c;
+        }
+    }
+    return best;
+}
 
 int linear4_parts(Rows4 kind) { return kind == Rows4::kF32 ? 3 : 1; }
 
@@ -262,6 +406,10 @@ template <typename T>
 cudaError_t launch_linear4(const Linear4Dims& L, Rows4 kind, const void* x, const uint8_t* x_exp, const uint8_t* w,
                            const T* scales, const T* offsets, T* out, __nv_bfloat16* parts, cudaStream_t st) {
     if (L.rows == 0) return cudaSuccess;
+    if (L.rows <= kFewRows) {
+        if (kind == Rows4::kE4m3) return few<T>(L, static_cast<const uint8_t*>(x), x_exp, w, scales, offsets, out, st);
+        return few<T>(L, static_cast<const T*>(x), x_exp, w, scales, offsets, out, st);
+    }
     Linear4Dims D = L;
     const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(x);
     if (kind != Rows4::kBf16 || (uintptr_t)x % 16 || L.sx % 8) {
@@ -275,21 +423,7 @@ cudaError_t launch_linear4(const Linear4Dims& L, Rows4 kind, const void* x, cons
         rows = parts;
         D.sx = L.n_in;
     }
-    if (L.rows > 8) return launch_linear4_tc<T>(D, linear4_parts(kind), rows, w, scales, offsets, out, st);
-    const int64_t stride = L.rows * L.n_in;
-    auto go = [&](auto group, auto np, auto offs) {
-        return run<T, 1, 1, decltype(group)::value, decltype(np)::value, decltype(offs)::value>(D, rows, stride, w, scales, offsets, out, st);
-    };
-    auto with_offsets = [&](auto group, auto np) {
-        return offsets ? go(group, np, std::true_type()) : go(group, np, std::false_type());
-    };
-    auto with_group = [&](auto np) {
-        if (L.group == 128) return with_offsets(std::integral_constant<int, 128>(), np);
-        if (L.group == 64) return with_offsets(std::integral_constant<int, 64>(), np);
-        return with_offsets(std::integral_constant<int, 32>(), np);
-    };
-    if (kind == Rows4::kF32) return with_group(std::integral_constant<int, 3>());
-    return with_group(std::integral_constant<int, 1>());
+    return launch_linear4_tc<T>(D, linear4_parts(kind), rows, w, scales, offsets, out, st);
 }
 
 template <typename T>

@@ -1,4 +1,4 @@
-// Products of more than eight rows with 4-bit weights on the 5th-generation tensor cores.
+// Products of more than sixteen rows with 4-bit weights on the 5th-generation tensor cores.
 //
 // D [128 rows of W, N tokens] = A B^T per group of inputs: A = q - 8 in bf16 (exact, as every product is), B the
 // tokens' rows.  A row's sums of a group are read back, scaled in fp32 and added to the row's own registers, so that no
@@ -12,7 +12,7 @@
 //   four (eight) warps read a group's sums (32 tokens a thread at most), scale and add them up.
 // The cluster's sums are added through distributed shared memory, in order of its blocks.
 //
-// Bound, with 16 tokens, by the weights' bytes; with 64 by what an SM issues per 64 inputs of 128 rows: about 130
+// Bound by what an SM issues per 64 inputs of 128 rows: about 130
 // instructions of each unpacking warp and 60 of each adding warp.
 #include <algorithm>
 
@@ -33,9 +33,9 @@ constexpr uint32_t kSums = 128;
 template <int N, int PARTS, bool OFFS>
 struct Shape {
     static constexpr int kAdd = N > 32 ? 8 : 4;  // adding warps
-    static constexpr int kPer = N > 32 ? 32 : N;  // tokens of an adding thread
+    static constexpr int kPer = 32;              // tokens of an adding thread
     static constexpr int kWarps = 6 + kAdd, kThreads = 32 * kWarps;
-    static constexpr int kBufs = (N == 16 || (N == 32 && !OFFS)) ? 4 : 2;  // of sums
+    static constexpr int kBufs = N == 32 && !OFFS ? 4 : 2;  // of sums
     static constexpr uint32_t kCols = kSums + kBufs * N * (OFFS ? 2 : 1) > 256 ? 512 : 256;
     static constexpr int kW = kTile * 64, kX = N * 128;  // bytes of a stage's W, of 64 inputs of x
     static constexpr int kStage = kW + 2 * PARTS * kX;
@@ -44,21 +44,6 @@ struct Shape {
     static constexpr size_t kNeed = std::max<size_t>(kSmem, 1024 + (size_t)N * kTile * 4);
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t local, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
 // Eight weights of a word less 8, as four pairs of bf16: 0x4300 | q is 128 + q.
 __device__ __forceinline__ void unpack8(uint32_t w, uint32_t* o) {
     const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu, off = 0x43084308u;
@@ -325,7 +310,7 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         const int row = n0 + i % kTile;
         if (t >= L.rows || row >= L.n_out) continue;
         float y = 0.f;
-        for (int c = 0; c < n_split; ++c) y += ld_cluster(umma::smem_addr(part + i), c);
+        for (int c = 0; c < n_split; ++c) y += ld_cluster(part + i, c);
         out[t * L.n_out + row] = from_f32<T>(y);
     }
     cluster_sync_all();  // no block leaves while its sums are read
@@ -341,35 +326,8 @@ cudaError_t run(const CUtensorMap& map_w, const CUtensorMap& map_x, const Linear
     });
     if (e != cudaSuccess) return e;
     const int tiles = (L.n_out + kTile - 1) / kTile;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * n_split), (unsigned)((L.rows + N - 1) / N));
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kNeed;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)n_split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = n_split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, linear4_tc_kernel<T, N, PARTS, OFFS>, map_w, map_x, L, scales, offsets, out, n_split);
-}
-
-// Blocks of a cluster: of 1, 2, 4 and 8 the one with the shortest sum of rounds (two blocks an SM) by tiles, where a block
-// spends about six tiles' time on its start and its end.
-int split(const Linear4Dims& L, int64_t tiles) {
-    const int64_t stages = (L.n_in + 127) / 128;
-    int best = 1;
-    int64_t least = INT64_MAX;
-    for (int c = 1; c <= 8; c *= 2) {
-        if (c > 1 && c > stages) break;
-        const int64_t cost = (tiles * c + 303) / 304 * ((stages + c - 1) / c + 6);
-        if (cost < least) {
-            least = cost;
-            best = c;
-        }
-    }
-    return best;
+    ClusterCfg cfg(dim3((unsigned)(tiles * n_split), (unsigned)((L.rows + N - 1) / N)), S::kThreads, S::kNeed, st, n_split);
+    return cudaLaunchKernelEx(&cfg.cfg, linear4_tc_kernel<T, N, PARTS, OFFS>, map_w, map_x, L, scales, offsets, out, n_split);
 }
 
 }  // namespace
@@ -377,12 +335,13 @@ int split(const Linear4Dims& L, int64_t tiles) {
 template <typename T>
 cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat16* x, const uint8_t* w, const T* scales,
                               const T* offsets, T* out, cudaStream_t st) {
-    const int n = L.rows <= 16 ? 16 : L.rows <= 32 ? 32 : 64;
+    const int n = L.rows <= 32 ? 32 : 64;
     CUtensorMap map_w, map_x;
     if (!tma::make_map_2d(&map_w, w, 1, (uint64_t)L.n_in / 2, (uint64_t)L.n_out, (uint64_t)L.n_in / 2, 64, kTile) ||
         !tma::make_map_2d(&map_x, x, 2, (uint64_t)L.n_in, (uint64_t)L.rows * parts, (uint64_t)L.sx * 2, 64, (uint32_t)n))
         return cudaErrorInvalidValue;
-    const int c = split(L, (int64_t)((L.n_out + kTile - 1) / kTile) * ((L.rows + n - 1) / n));
+    // (two blocks an SM)
+    const int c = linear4_split((int64_t)((L.n_out + kTile - 1) / kTile) * ((L.rows + n - 1) / n), (L.n_in + 127) / 128, 304, 6);
     auto go = [&](auto nn, auto np, auto offs) {
         return run<T, decltype(nn)::value, decltype(np)::value, decltype(offs)::value>(map_w, map_x, L, scales, offsets, out, c, st);
     };
@@ -390,7 +349,6 @@ cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat
         return parts == 3 ? go(nn, std::integral_constant<int, 3>(), offs) : go(nn, std::integral_constant<int, 1>(), offs);
     };
     auto with_rows = [&](auto offs) {
-        if (n == 16) return with_parts(std::integral_constant<int, 16>(), offs);
         if (n == 32) return with_parts(std::integral_constant<int, 32>(), offs);
         return with_parts(std::integral_constant<int, 64>(), offs);
     };
