@@ -6,9 +6,9 @@
 //
 // A block takes 128 rows and, in a cluster of C blocks, a C-th of the inputs, 128 at a time:
 //   one warp     brings tiles of W (128 x 64 bytes) and of x (N x 128, in two blocks of 64) by TMA through a ring;
-//   four warps   take their rows' words from the ring, form q - 8 and put 64 inputs at a time into tensor memory, which
-//                A is read from (three such buffers), so that shared memory holds a weight in half a byte only;
-//   one warp     issues the products, a group into one of two or four buffers of sums;
+//   four or eight warps  take their rows' words from the ring, form q - 8 and put them into tensor memory, which A is
+//                read from (two buffers), so that shared memory holds a weight in half a byte only;
+//   one warp     issues the products, a group into one of two to four buffers of sums;
 //   four (eight) warps read a group's sums (32 tokens a thread at most), scale and add them up.
 // The cluster's sums are added through distributed shared memory, in order of its blocks.
 //
@@ -26,16 +26,18 @@ namespace {
 
 constexpr int kTile = 128;           // rows of W
 constexpr uint32_t kPolls = 1u << 22;
-constexpr int kABuf = 3;             // buffers of A, 64 inputs in 32 columns each
-constexpr uint32_t kOnes = 96;       // columns: A, ones, sums
-constexpr uint32_t kSums = 128;
+constexpr uint32_t kOnes = 128;      // columns: two buffers of A (128 inputs in 64 columns each), ones, sums
 
 template <int N, int PARTS, bool OFFS>
 struct Shape {
     static constexpr int kAdd = N > 32 ? 8 : 4;  // adding warps
-    static constexpr int kPer = 32;              // tokens of an adding thread
-    static constexpr int kWarps = 6 + kAdd, kThreads = 32 * kWarps;
-    static constexpr int kBufs = N == 32 && !OFFS ? 4 : 2;  // of sums
+    static constexpr int kPer = N > 32 ? 32 : N;  // tokens of an adding thread
+    // Sets of four unpacking warps, a buffer of A in turn.  64 tokens: one, for the registers that adding takes.
+    static constexpr int kSets = N > 32 ? 1 : 2;
+    static constexpr int kLoad = 4 * kSets, kIssue = kLoad + 1, kAdd0 = kLoad + 2;  // warps
+    static constexpr int kWarps = kAdd0 + kAdd, kThreads = 32 * kWarps;
+    static constexpr uint32_t kSums = OFFS ? 160 : 128;
+    static constexpr int kBufs = OFFS ? (N == 16 ? 3 : 2) : (N == 64 ? 2 : 4);  // of sums
     static constexpr uint32_t kCols = kSums + kBufs * N * (OFFS ? 2 : 1) > 256 ? 512 : 256;
     static constexpr int kW = kTile * 64, kX = N * 128;  // bytes of a stage's W, of 64 inputs of x
     static constexpr int kStage = kW + 2 * PARTS * kX;
@@ -73,7 +75,7 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                   const T* __restrict__ scales, const T* __restrict__ offsets, T* __restrict__ out, int n_split) {
     using S = Shape<N, PARTS, OFFS>;
     extern __shared__ uint8_t raw[];
-    __shared__ alignas(8) uint64_t bars[2 * S::kStages + 2 * kABuf + 2 * S::kBufs + 1];
+    __shared__ alignas(8) uint64_t bars[2 * S::kStages + 4 + 2 * S::kBufs + 1];
     __shared__ uint32_t tmem_at;
     __shared__ int bad;
     const uint32_t ring = (umma::smem_addr(raw) + 1023u) & ~1023u;
@@ -84,9 +86,9 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     const int64_t m0 = (int64_t)blockIdx.y * N;
     const int n_groups = L.n_in / L.group, stages = (L.n_in + 127) / 128, halves = (L.n_in + 63) / 64;
     const int s0 = (int)((int64_t)stages * rank / n_split), s1 = (int)((int64_t)stages * (rank + 1) / n_split);
-    const int h0 = 2 * s0, h1 = min(2 * s1, halves);
+    const int h1 = min(2 * s1, halves);  // (64 inputs each)
     auto bar = [&](int i) { return umma::smem_addr(bars + i); };
-    const int kFull = 0, kEmpty = S::kStages, kAFull = 2 * S::kStages, kAEmpty = kAFull + kABuf, kDFull = kAEmpty + kABuf,
+    const int kFull = 0, kEmpty = S::kStages, kAFull = 2 * S::kStages, kAEmpty = kAFull + 2, kDFull = kAEmpty + 2,
               kDEmpty = kDFull + S::kBufs, kEnd = kDEmpty + S::kBufs;
     if (threadIdx.x == 0) {
         bad = 0;
@@ -94,7 +96,7 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             umma::mbar_init(bar(kFull + i), 1);
             umma::mbar_init(bar(kEmpty + i), 5);  // four unpacking warps, and the products
         }
-        for (int i = 0; i < kABuf; ++i) {
+        for (int i = 0; i < 2; ++i) {
             umma::mbar_init(bar(kAFull + i), 4);
             umma::mbar_init(bar(kAEmpty + i), 1);
         }
@@ -124,19 +126,22 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 #pragma unroll
     for (int i = 0; i < S::kPer / 2; ++i) acc[i] = make_float2(0.f, 0.f);
 
-    if (warp < 4) {  // unpacking
-        const int row = warp * 32 + lane;
+    if (warp < S::kLoad) {  // unpacking
+        const int row = (warp & 3) * 32 + lane, set = warp >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         if constexpr (OFFS) {
-            uint32_t ones[16];
+            if (set == 0) {
+                uint32_t ones[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ones[i] = 0x3f803f80u;
-            umma::tmem_st16_async(tmem + ((uint32_t)warp << 21) + kOnes, ones);
+                for (int i = 0; i < 16; ++i) ones[i] = 0x3f803f80u;
+                umma::tmem_st16_async(lanes + kOnes, ones);
+            }
         }
-        Ring in, a;
-        bool go = true;
-        for (int s = s0; s < s1 && go; ++s) {
-            go = wait(kFull + in.i, in.turn);
-            if (!go) break;
+        Ring in;
+        for (int i = 0; i < set; ++i) in.next(S::kStages);
+        for (int s = s0 + set; s < s1; s += S::kSets) {
+            const int i = s - s0, buf = i & 1;
+            if (!wait(kFull + in.i, in.turn)) break;
             const uint32_t at = ring + in.i * S::kStage + row * 64;
             uint32_t w[16];
 #pragma unroll
@@ -144,29 +149,25 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
                              : "r"(at + (((uint32_t)c ^ ((uint32_t)row >> 1 & 3u)) << 4)));
+            if (!wait(kAEmpty + buf, (uint32_t)(i >> 1 & 1) ^ 1)) break;
+            umma::fence_after_sync();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (2 * s + h >= h1) break;
-                go = wait(kAEmpty + a.i, a.turn ^ 1);
-                if (!go) break;
-                umma::fence_after_sync();
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[16];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[16];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) unpack8(w[8 * h + 4 * c + i], o + 4 * i);
-                    umma::tmem_st16_async(tmem + ((uint32_t)warp << 21) + a.i * 32 + 16 * c, o);
-                }
-                umma::tmem_wait_st();
-                umma::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive(bar(kAFull + a.i));
-                a.next(kABuf);
+                for (int k = 0; k < 4; ++k) unpack8(w[4 * c + k], o + 4 * k);
+                umma::tmem_st16_async(lanes + buf * 64 + 16 * c, o);
             }
-            if (lane == 0) umma::mbar_arrive(bar(kEmpty + in.i));  // (after the last __syncwarp: every lane has its words)
-            in.next(S::kStages);
+            umma::tmem_wait_st();
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                umma::mbar_arrive(bar(kAFull + buf));
+                umma::mbar_arrive(bar(kEmpty + in.i));
+            }
+            for (int k = 0; k < S::kSets; ++k) in.next(S::kStages);
         }
-    } else if (warp == 4) {  // loads
+    } else if (warp == S::kLoad) {  // loads
         Ring in;
         int loaded = 0;
         for (int s = s0; s < s1; ++s) {
@@ -193,44 +194,46 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 r.next(S::kStages);
             }
         }
-    } else if (warp == 5) {  // products
+    } else if (warp == S::kIssue) {  // products
         const uint32_t lead = umma::elect_one(), idesc = umma::idesc_bf16(kTile, N, false, false);
         const uint64_t b0 = umma::kmajor(ring + S::kW, N, 0);
         // A group's sums over PER products; straight code, as one warp issues for all others (with the group's size as a
         // variable a product took 250 cycles to issue).
         auto issue = [&](auto per) -> bool {
             constexpr int PER = decltype(per)::value;
-            Ring in, a, d;
-            for (int h = h0; h < h1; ++h) {
-                if ((h & 1) == 0 && !wait(kFull + in.i, in.turn)) return false;
-                if (!wait(kAFull + a.i, a.turn)) return false;
-                const uint64_t b = b0 + (uint64_t)((in.i * S::kStage + (h & 1) * PARTS * S::kX) >> 4);
-                const uint32_t at = tmem + a.i * 32;
+            Ring in, d;
+            for (int s = s0; s < s1; ++s) {
+                const int i = s - s0, buf = i & 1;
+                // (those who unpacked the weights had waited for the stage, x and all)
+                if (!wait(kAFull + buf, (uint32_t)(i >> 1 & 1))) return false;
+                const uint64_t b = b0 + (uint64_t)(in.i * S::kStage >> 4);
+                const uint32_t at = tmem + buf * 64;
+                const bool half = 2 * s + 1 >= h1;  // a tile that ends after 64 inputs
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool first = PER == 8 ? k == 0 && (h & 1) == 0 : k % PER == 0;
-                    if (PER == 8 ? k == 0 : k % PER == 0) {
-                        if (first && !wait(kDEmpty + d.i, d.turn ^ 1)) return false;
+                for (int k = 0; k < 8; ++k) {
+                    if (k == 4 && half) break;
+                    const bool first = k % PER == 0;
+                    if (first) {
+                        if (!wait(kDEmpty + d.i, d.turn ^ 1)) return false;
                         umma::fence_after_sync();
                     }
-                    const uint32_t sums = tmem + kSums + d.i * N * (OFFS ? 2 : 1);
+                    const uint32_t sums = tmem + S::kSums + d.i * N * (OFFS ? 2 : 1);
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) {
-                        umma::mma_ts_lead(sums, at + 8 * k, b + p * (S::kX >> 4) + 2 * k, idesc, !first || p > 0, lead);
-                        if constexpr (OFFS)
-                            umma::mma_ts_lead(sums + N, tmem + kOnes, b + p * (S::kX >> 4) + 2 * k, idesc, !first || p > 0, lead);
+                        const uint64_t bk = b + ((k >> 2) * PARTS + p) * (S::kX >> 4) + 2 * (k & 3);
+                        umma::mma_ts_lead(sums, at + 8 * k, bk, idesc, !first || p > 0, lead);
+                        if constexpr (OFFS) umma::mma_ts_lead(sums + N, tmem + kOnes, bk, idesc, !first || p > 0, lead);
                     }
-                    if (PER == 8 ? k == 3 && (h & 1) : k % PER == PER - 1) {
+                    if (k % PER == PER - 1) {
                         if (lead) umma::commit(bar(kDFull + d.i));
                         d.next(S::kBufs);
                     }
                 }
-                if (lead) umma::commit(bar(kAEmpty + a.i));
-                a.next(kABuf);
-                if ((h & 1) || h + 1 == h1) {
-                    if (lead) umma::commit(bar(kEmpty + in.i));
-                    in.next(S::kStages);
+                if (lead) {
+                    umma::commit(bar(kAEmpty + buf));
+                    umma::commit(bar(kEmpty + in.i));
                 }
+                in.next(S::kStages);
                 __syncwarp();
             }
             return true;
@@ -244,7 +247,7 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             umma::mbar_wait(bar(kEnd), 0, kPolls);
         }
     } else {  // adding
-        const int u = warp - 6, quad = warp & 3, t0 = (u >> 2) * S::kPer;
+        const int u = warp - S::kAdd0, quad = warp & 3, t0 = (u >> 2) * S::kPer;
         const int row = n0 + quad * 32 + lane;
         const int64_t at = (int64_t)min(row, L.n_out - 1) * n_groups;
         const int g0 = s0 * 128 / L.group, g1 = (h1 * 64 + L.group - 1) / L.group;
@@ -255,7 +258,7 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             const float sc1 = scale_at(scales, g + 1), of1 = OFFS ? scale_at(offsets, g + 1) : 0.f;
             if (!wait(kDFull + d.i, d.turn)) break;
             umma::fence_after_sync();
-            const uint32_t sums = tmem + ((uint32_t)quad << 21) + kSums + d.i * N * (OFFS ? 2 : 1) + t0;
+            const uint32_t sums = tmem + ((uint32_t)quad << 21) + S::kSums + d.i * N * (OFFS ? 2 : 1) + t0;
 #pragma unroll
             for (int k = 0; k < (OFFS ? 2 : 1); ++k) {
                 const float2 f = make_float2(k ? of : sc, k ? of : sc);
@@ -287,8 +290,8 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     if (warp == 0) umma::tmem_dealloc(tmem, S::kCols);
     const float nan = __int_as_float(0x7fc00000);
     if (n_split == 1) {
-        if (warp < 6) return;
-        const int u = warp - 6, t0 = (u >> 2) * S::kPer, row = n0 + (warp & 3) * 32 + lane;
+        if (warp < S::kAdd0) return;
+        const int u = warp - S::kAdd0, t0 = (u >> 2) * S::kPer, row = n0 + (warp & 3) * 32 + lane;
         if (row >= L.n_out) return;
 #pragma unroll
         for (int i = 0; i < S::kPer; ++i) {
@@ -298,8 +301,8 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         }
         return;
     }
-    if (warp >= 6) {
-        const int u = warp - 6, t0 = (u >> 2) * S::kPer, row = (warp & 3) * 32 + lane;
+    if (warp >= S::kAdd0) {
+        const int u = warp - S::kAdd0, t0 = (u >> 2) * S::kPer, row = (warp & 3) * 32 + lane;
 #pragma unroll
         for (int i = 0; i < S::kPer; ++i) part[(t0 + i) * kTile + row] = failed ? nan : i & 1 ? acc[i / 2].y : acc[i / 2].x;
     }
@@ -335,7 +338,7 @@ cudaError_t run(const CUtensorMap& map_w, const CUtensorMap& map_x, const Linear
 template <typename T>
 cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat16* x, const uint8_t* w, const T* scales,
                               const T* offsets, T* out, cudaStream_t st) {
-    const int n = L.rows <= 32 ? 32 : 64;
+    const int n = L.rows <= 16 ? 16 : L.rows <= 32 ? 32 : 64;
     CUtensorMap map_w, map_x;
     if (!tma::make_map_2d(&map_w, w, 1, (uint64_t)L.n_in / 2, (uint64_t)L.n_out, (uint64_t)L.n_in / 2, 64, kTile) ||
         !tma::make_map_2d(&map_x, x, 2, (uint64_t)L.n_in, (uint64_t)L.rows * parts, (uint64_t)L.sx * 2, 64, (uint32_t)n))
@@ -349,6 +352,7 @@ cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat
         return parts == 3 ? go(nn, std::integral_constant<int, 3>(), offs) : go(nn, std::integral_constant<int, 1>(), offs);
     };
     auto with_rows = [&](auto offs) {
+        if (n == 16) return with_parts(std::integral_constant<int, 16>(), offs);
         if (n == 32) return with_parts(std::integral_constant<int, 32>(), offs);
         return with_parts(std::integral_constant<int, 64>(), offs);
     };
