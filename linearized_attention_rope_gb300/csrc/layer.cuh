@@ -29,13 +29,24 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The float at the same shared-memory offset as `local` in block `rank` of the cluster.
+// Sum over the cluster's n blocks (1, 2, 4, 8), in their order, of the float at the same shared-memory offset as `local`.
 __device__ __forceinline__ float ld_cluster(const float* local, uint32_t rank) {
     uint32_t a;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
     return v;
+}
+template <int N> __device__ __forceinline__ float cluster_sum_of(const float* local) {
+    float v[N], y = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) v[c] = ld_cluster(local, c);
+#pragma unroll
+    for (int c = 0; c < N; ++c) y += v[c];
+    return y;
+}
+__device__ __forceinline__ float cluster_sum(const float* local, int n) {
+    return n == 2 ? cluster_sum_of<2>(local) : n == 4 ? cluster_sum_of<4>(local) : cluster_sum_of<8>(local);
 }
 struct ClusterCfg {
     cudaLaunchConfig_t cfg = {};

@@ -266,15 +266,12 @@ linear4_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t* __re
     if (n_split > 1) cluster_sync_all();
     else __syncthreads();
     const int t0 = (int)(S::kTok * rank / n_split), t1 = (int)(S::kTok * (rank + 1) / n_split);
+#pragma unroll 4
     for (int i = t0 * S::kRows + threadIdx.x; i < t1 * S::kRows; i += kThreads4) {
         const int64_t t = (int64_t)blockIdx.y * S::kTok + i / S::kRows;
         const int n = n0 + i % S::kRows;
         if (t >= L.rows || n >= L.n_out) continue;
-        float y = 0.f;
-        if (n_split == 1) y = sums[i];
-        else
-            for (int c = 0; c < n_split; ++c) y += ld_cluster(sums + i, c);
-        out[t * L.n_out + n] = from_f32<T>(y);
+        out[t * L.n_out + n] = from_f32<T>(n_split == 1 ? sums[i] : cluster_sum(sums + i, n_split));
     }
     if (n_split > 1) cluster_sync_all();  // no block leaves while its sums are read
 }

@@ -308,13 +308,12 @@ linear4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     }
     cluster_sync_all();
     const int t0 = (int)(N * rank / n_split), t1 = (int)(N * (rank + 1) / n_split);
+#pragma unroll 4
     for (int i = t0 * kTile + threadIdx.x; i < t1 * kTile; i += S::kThreads) {
         const int64_t t = m0 + i / kTile;
         const int row = n0 + i % kTile;
         if (t >= L.rows || row >= L.n_out) continue;
-        float y = 0.f;
-        for (int c = 0; c < n_split; ++c) y += ld_cluster(part + i, c);
-        out[t * L.n_out + row] = from_f32<T>(y);
+        out[t * L.n_out + row] = from_f32<T>(cluster_sum(part + i, n_split));
     }
     cluster_sync_all();  // no block leaves while its sums are read
 }
