@@ -11,13 +11,14 @@
 // reads them twice.
 // The gradient's blocks stay and walk the rows, so that a thread adds up dw of
 // its own columns in registers; the blocks' sums are added in order by a second
-// launch.  A thread has one piece of a row where 1024 threads can (then the next
-// row is on its way while this one is reduced), else two or four that it reads
-// again behind the reduction, from L2: registers are what a row's length is
-// limited by.
+// launch.  Rows come through a ring in shared memory, filled by bulk copies, in
+// the gradient and where the norm has more than three rows a block: loads go on
+// while a row is reduced, and neither pass holds the row in registers.
 #include <algorithm>
 
 #include "layer.cuh"
+#include "tma.cuh"
+#include "umma.cuh"
 
 namespace hla {
 
@@ -92,44 +93,54 @@ template <int V, int P> struct Bound {
     static constexpr int blocks = (V > 1 && P == 1 ? 1536 : 1024) / threads;
 };
 
-// A row's P pieces of V values per thread, piece p at (p tpr + thread) V.  Eight bits: a group's values lie in
-// neighbouring lanes of one piece index (its pieces are a power of two that divides 32, and tpr is a multiple of it).
-template <typename T, int V, int P, bool E4M3>
-__global__ void __launch_bounds__(Bound<V, P>::threads, Bound<V, P>::blocks)
-norm_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict__ weight, T* out, uint8_t* out8,
-            uint8_t* exps, T* sum, int tpr) {
+template <typename T, int V> __device__ __forceinline__ void add_to(Piece<T, V>& a, const Piece<T, V>& b) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) a.x[j] = from_f32<T>(to_f32(a.x[j]) + to_f32(b.x[j]));
+}
+
+// A ring of row buffers that bulk copies fill.  Every wait ends; after one that ran out a block loads no more and its rows
+// are NaN.
+constexpr int kStages = 8;
+constexpr uint32_t kPolls = 1u << 22;
+__device__ __forceinline__ void start_ring(uint64_t* full, int stages, int* dead) {
+    if (threadIdx.x == 0) {
+        *dead = 0;
+        for (int i = 0; i < stages; ++i) umma::mbar_init(umma::smem_addr(full + i), 1);
+        umma::fence_mbar_init();
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ bool wait_ring(uint64_t* full, uint32_t turn, int* dead) {
+    const uint32_t bar = umma::smem_addr(full);
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (umma::mbar_try_wait(bar, turn)) return true;
+    if (!*(volatile int*)dead && umma::mbar_wait(bar, turn, kPolls)) return true;
+    *dead = 1;
+    return false;
+}
+// Copies in flight end before the block does.  (After a wait that ran out; else every buffer has been waited for.)
+__device__ __forceinline__ void end_ring(uint64_t* full, int stages, int dead) {
+    if (!dead) return;
+    for (int i = 0; i < 2 * stages; ++i) umma::mbar_wait(umma::smem_addr(full + i % stages), i / stages, kPolls / 8, 100000000ull);
+}
+
+// A row's P pieces of V values per thread, piece p at (p tpr + thread) V: the sum of squares, then the sum and the outputs.
+// Eight bits: a group's values lie in neighbouring lanes of one piece index (its pieces are a power of two that divides
+// 32, and tpr is a multiple of it).  `between` runs once every thread of the row has its pieces.
+template <typename T, int V, int P, bool E4M3, typename F>
+__device__ __forceinline__ void norm_row(const NormDims& N, Piece<T, V> (&a)[P], const T* __restrict__ weight, T* out,
+                                         uint8_t* out8, uint8_t* exps, T* sum, int64_t row, bool on, int lane, int tpr,
+                                         float* sm, F between) {
     using Pc = Piece<T, V>;
-    __shared__ float sm[64];
-    const int group = tpr > 32 ? 0 : threadIdx.x / tpr, lane = threadIdx.x - group * tpr;
-    const int64_t row = tpr > 32 ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / tpr) + group;
-    const bool on = row < N.rows;
-    const T* xr = x + (on ? row_at(N, row, N.sx) : 0);
     const int64_t dense = (on ? row : 0) * N.cols;
-    Pc a[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int e = (p * tpr + lane) * V;
-        a[p] = on && e < N.cols ? *reinterpret_cast<const Pc*>(xr + e) : Pc{};
-    }
-    if (residual) {
-        const T* rr = residual + (on ? row_at(N, row, N.sr) : 0);
-        Pc b[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int e = (p * tpr + lane) * V;
-            b[p] = on && e < N.cols ? *reinterpret_cast<const Pc*>(rr + e) : Pc{};
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int j = 0; j < V; ++j) a[p].x[j] = from_f32<T>(to_f32(a[p].x[j]) + to_f32(b[p].x[j]));
-    }
     float v[1] = {0.f};
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int j = 0; j < V; ++j) v[0] += to_f32(a[p].x[j]) * to_f32(a[p].x[j]);
     row_sum(v, tpr, sm);
+    between();
     const float r = 1.f / sqrtf(v[0] / (float)N.cols + N.eps);
     // the sum is written once the whole row has been read: it may lie where x or the residual does
     if (sum) {
@@ -204,6 +215,86 @@ norm_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict
     }
 }
 
+template <typename T, int V, int P, bool E4M3>
+__global__ void __launch_bounds__(Bound<V, P>::threads, Bound<V, P>::blocks)
+norm_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict__ weight, T* out, uint8_t* out8,
+            uint8_t* exps, T* sum, int tpr) {
+    using Pc = Piece<T, V>;
+    __shared__ float sm[64];
+    const int group = tpr > 32 ? 0 : threadIdx.x / tpr, lane = threadIdx.x - group * tpr;
+    const int64_t row = tpr > 32 ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / tpr) + group;
+    const bool on = row < N.rows;
+    const T* xr = x + (on ? row_at(N, row, N.sx) : 0);
+    Pc a[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int e = (p * tpr + lane) * V;
+        a[p] = on && e < N.cols ? *reinterpret_cast<const Pc*>(xr + e) : Pc{};
+    }
+    if (residual) {
+        const T* rr = residual + (on ? row_at(N, row, N.sr) : 0);
+        Pc b[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * tpr + lane) * V;
+            b[p] = on && e < N.cols ? *reinterpret_cast<const Pc*>(rr + e) : Pc{};
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) add_to(a[p], b[p]);
+    }
+    norm_row<T, V, P, E4M3>(N, a, weight, out, out8, exps, sum, row, on, lane, tpr, sm, [] {});
+}
+
+// Many rows of a block each: blocks stay, and the rows to come are on their way into a ring in shared memory (x, then the
+// residual), so that loads do not stop while a row is reduced.
+template <typename T, int V, int P, bool E4M3>
+__global__ void __launch_bounds__(512, 2)
+norm_ring_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict__ weight, T* out, uint8_t* out8,
+                 uint8_t* exps, T* sum, int stages) {
+    using Pc = Piece<T, V>;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float sm[2][64];
+    __shared__ alignas(8) uint64_t full[kStages];
+    __shared__ int dead;
+    const int lane = threadIdx.x, tpr = blockDim.x;
+    const uint32_t bytes = (uint32_t)N.cols * sizeof(T), each = residual ? 2 * bytes : bytes;
+    auto load = [&](int64_t row, int st) {
+        if (row >= N.rows) return;
+        const uint32_t bar = umma::smem_addr(full + st), at = umma::smem_addr(ring) + st * each;
+        tma::expect_tx(bar, each);
+        tma::bulk_load(at, x + row_at(N, row, N.sx), bytes, bar);
+        if (residual) tma::bulk_load(at + bytes, residual + row_at(N, row, N.sr), bytes, bar);
+    };
+    start_ring(full, stages, &dead);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages; ++i) load(blockIdx.x + (int64_t)i * gridDim.x, i);
+    int st = 0, turn = 0, odd = 0;
+    for (int64_t row = blockIdx.x; row < N.rows; row += gridDim.x) {
+        const bool there = wait_ring(full + st, turn, &dead);
+        const T* xr = reinterpret_cast<const T*>(ring + (size_t)st * each);
+        Pc a[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * tpr + lane) * V;
+            a[p] = Pc{};
+            if (e < N.cols) {
+                a[p] = *reinterpret_cast<const Pc*>(xr + e);
+                if (residual) add_to(a[p], *reinterpret_cast<const Pc*>(xr + N.cols + e));
+                if (!there) a[p].x[0] = from_f32<T>(__int_as_float(0x7fc00000));
+            }
+        }
+        norm_row<T, V, P, E4M3>(N, a, weight, out, out8, exps, sum, row, true, lane, tpr, sm[odd], [&] {
+            if (threadIdx.x == 0 && !dead) load(row + (int64_t)stages * gridDim.x, st);
+        });
+        odd ^= 1;
+        if (++st == stages) {
+            st = 0;
+            turn ^= 1;
+        }
+    }
+    end_ring(full, stages, dead);
+}
+
 // Rows too long for the registers of a block: the sum of squares, then the row again (from the sums just written, each
 // by the thread that reads it).
 template <typename T, bool E4M3>
@@ -257,109 +348,190 @@ norm_long_kernel(const NormDims N, const T* x, const T* residual, const T* __res
 }
 
 // The gradient.  part [gridDim.x][cols]: this block's sums of dy s r.
-// MOST: threads of a block, at most.
-template <typename T, int V, int P, int MOST>
-__global__ void __launch_bounds__(MOST, MOST == kNarrow ? 6 : 1)
+// A block's sums of dw, one group of lanes after the other, to its own row of part.
+template <int V, int P>
+__device__ __forceinline__ void put_part(const float (&acc)[P][V], float* part, int cols, int groups, int group, int lane, int tpr,
+                                         float* cols_sm) {
+    if (!part) return;
+    float* mine = part + (int64_t)blockIdx.x * cols;
+    float* to = groups == 1 ? mine : cols_sm + group * cols;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int e = (p * tpr + lane) * V;
+        if (e >= cols) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) to[e + j] = acc[p][j];
+    }
+    if (groups == 1) return;
+    __syncthreads();
+    for (int e = threadIdx.x; e < cols; e += blockDim.x) {
+        float y = 0.f;
+        for (int k = 0; k < groups; ++k) y += cols_sm[k * cols + e];
+        mine[e] = y;
+    }
+}
+
+template <typename T, int V, int P>
+__global__ void __launch_bounds__(1024, 1)
 norm_backward_kernel(const NormDims N, const T* s, const T* __restrict__ weight, const T* dout, const T* dsum, T* dx,
                      float* part, int tpr) {
     using Pc = Piece<T, V>;
-    constexpr bool kAgain = P * V * sizeof(T) > 16;                             // pieces are read again, not held
-    constexpr bool kAhead = P == 1 && V * (MOST == 1024 ? 8 / sizeof(T) : 1) <= 8;  // the next row's are loaded early
-    constexpr int H = kAgain ? 1 : P;
     __shared__ float sm[2][64];
     extern __shared__ float cols_sm[];  // rows of a warp or less: the sums of every group of lanes
     const int groups = tpr > 32 ? 1 : blockDim.x / tpr, group = tpr > 32 ? 0 : threadIdx.x / tpr;
     const int lane = threadIdx.x - group * tpr;
     const float inv = 1.f / (float)N.cols;
-    Pc w[H];
     float acc[P][V];
-    auto factor = [&](int p, int e) {
-        return weight && e < N.cols ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
-    };
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        if (!kAgain) w[kAgain ? 0 : p] = factor(p, (p * tpr + lane) * V);
+    for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[p][j] = 0.f;
-    }
     const float one = weight ? N.offset : 1.f;  // (without a weight w is 0)
-    const int64_t step = (int64_t)gridDim.x * groups;
-    Pc a[H], d[H], g[H];
-    auto load = [&](int64_t row, int p, Pc& a, Pc& d, Pc& g, bool with_sum) {
-        const int e = (p * tpr + lane) * V;
-        const bool on = row < N.rows && e < N.cols;
-        a = on ? *reinterpret_cast<const Pc*>(s + row_at(N, row, N.sx) + e) : Pc{};
-        d = on ? *reinterpret_cast<const Pc*>(dout + row * N.cols + e) : Pc{};
-        if (with_sum) g = on && dsum ? *reinterpret_cast<const Pc*>(dsum + row * N.cols + e) : Pc{};
-    };
-    if (kAhead) load((int64_t)blockIdx.x * groups + group, 0, a[0], d[0], g[0], true);
     int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < N.rows; row0 += step, turn ^= 1) {
+    for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < N.rows; row0 += (int64_t)gridDim.x * groups, turn ^= 1) {
         const int64_t row = row0 + group;
-        Pc a1, d1, g1;
-        if constexpr (kAhead) load(row + step, 0, a1, d1, g1, true);
+        auto load = [&](int e, Pc& a, Pc& d, Pc& w) {
+            const bool on = row < N.rows && e < N.cols;
+            a = on ? *reinterpret_cast<const Pc*>(s + row_at(N, row, N.sx) + e) : Pc{};
+            d = on ? *reinterpret_cast<const Pc*>(dout + row * N.cols + e) : Pc{};
+            w = on && weight ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
+        };
+        Pc a, d, w;
         float v[2] = {0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int h = kAgain ? 0 : p;
-            if constexpr (!kAhead) load(row, p, a[h], d[h], g[h], !kAgain);
-            if constexpr (kAgain) w[h] = factor(p, (p * tpr + lane) * V);
+            load((p * tpr + lane) * V, a, d, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float x = to_f32(a[h].x[j]);
+                const float x = to_f32(a.x[j]);
                 v[0] += x * x;
-                v[1] += (one + to_f32(w[h].x[j])) * to_f32(d[h].x[j]) * x;
+                v[1] += (one + to_f32(w.x[j])) * to_f32(d.x[j]) * x;
             }
         }
         row_sum(v, tpr, sm[turn]);  // (sums of the row before last have been read by all)
         const float r = 1.f / sqrtf(v[0] * inv + N.eps), c = v[1] * inv * r * r;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int e = (p * tpr + lane) * V, h = kAgain ? 0 : p;
-            if constexpr (kAgain) {
-                load(row, p, a[h], d[h], g[h], true);
-                w[h] = factor(p, e);
-            }
+            const int e = (p * tpr + lane) * V;
+            if (P > 1) load(e, a, d, w);
+            const bool on = row < N.rows && e < N.cols;
+            const Pc g = on && dsum ? *reinterpret_cast<const Pc*>(dsum + row * N.cols + e) : Pc{};
             Pc o;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float x = to_f32(a[h].x[j]), dy = to_f32(d[h].x[j]);
-                o.x[j] = from_f32<T>(((one + to_f32(w[h].x[j])) * dy - x * c) * r + to_f32(g[h].x[j]));
+                const float x = to_f32(a.x[j]), dy = to_f32(d.x[j]);
+                o.x[j] = from_f32<T>(((one + to_f32(w.x[j])) * dy - x * c) * r + to_f32(g.x[j]));
                 acc[p][j] += dy * (x * r);
             }
-            if (row < N.rows && e < N.cols) *reinterpret_cast<Pc*>(dx + row * N.cols + e) = o;
-        }
-        if constexpr (kAhead) {
-            a[0] = a1;
-            d[0] = d1;
-            g[0] = g1;
+            if (on) *reinterpret_cast<Pc*>(dx + row * N.cols + e) = o;
         }
     }
-    if (!part) return;
-    float* mine = part + (int64_t)blockIdx.x * N.cols;
-    if (groups == 1) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int e = (p * tpr + lane) * V;
-            if (e >= N.cols) continue;
-#pragma unroll
-            for (int j = 0; j < V; ++j) mine[e + j] = acc[p][j];
-        }
-        return;
-    }
+    put_part<V, P>(acc, part, N.cols, groups, group, lane, tpr, cols_sm);
+}
+
+// The same from a ring of row buffers (s, dout and dsum), which both passes over a row read.  NARROW: a warp or less takes
+// a row, and a buffer holds `per` dense rows; else one.
+template <typename T, int P, bool NARROW>
+__global__ void __launch_bounds__(NARROW ? kNarrow : 512, NARROW ? 8 : 2)
+norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ weight, const T* dout, const T* dsum, T* dx,
+                          float* part, int tpr, int stages, int per) {
+    constexpr int V = 16 / (int)sizeof(T);
+    using Pc = Piece<T, V>;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float sm[2][64];
+    __shared__ alignas(8) uint64_t full[kStages];
+    __shared__ int dead;
+    const int groups = NARROW ? blockDim.x / tpr : 1, group = NARROW ? threadIdx.x / tpr : 0;
+    const int lane = threadIdx.x - group * tpr;
+    const float inv = 1.f / (float)N.cols;
+    const uint32_t row_bytes = (uint32_t)N.cols * sizeof(T), each = row_bytes * per;
+    const int n_in = dsum ? 3 : 2;
+    const int64_t items = (N.rows + per - 1) / per;
+    auto load = [&](int64_t item, int st) {
+        if (item >= items) return;
+        const int64_t row = item * per;
+        const uint32_t n = (uint32_t)min((int64_t)per, N.rows - row) * row_bytes;
+        const uint32_t bar = umma::smem_addr(full + st), at = umma::smem_addr(ring) + st * n_in * each;
+        tma::expect_tx(bar, n * n_in);
+        tma::bulk_load(at, s + row_at(N, row, N.sx), n, bar);
+        tma::bulk_load(at + each, dout + row * N.cols, n, bar);
+        if (dsum) tma::bulk_load(at + 2 * each, dsum + row * N.cols, n, bar);
+    };
+    start_ring(full, stages, &dead);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages; ++i) load(blockIdx.x + (int64_t)i * gridDim.x, i);
+    constexpr bool kHold = P * V <= 8;  // the weights stay in registers
+    Pc w[kHold ? P : 1];
+    float acc[P][V];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int e = (p * tpr + lane) * V;
-        if (e >= N.cols) continue;
+        if (kHold) w[kHold ? p : 0] = weight && e < N.cols ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
 #pragma unroll
-        for (int j = 0; j < V; ++j) cols_sm[group * N.cols + e + j] = acc[p][j];
+        for (int j = 0; j < V; ++j) acc[p][j] = 0.f;
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < N.cols; e += blockDim.x) {
-        float y = 0.f;
-        for (int k = 0; k < groups; ++k) y += cols_sm[k * N.cols + e];
-        mine[e] = y;
+    const float one = weight ? N.offset : 1.f;
+    int st = 0, turn = 0, odd = 0;
+    int64_t before = -1;  // the item whose buffer can be filled again, its stage the one before
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const bool there = wait_ring(full + st, turn, &dead);
+        const T* base = reinterpret_cast<const T*>(ring + (size_t)st * n_in * each);
+        const int64_t row0 = item * per;
+        for (int k = 0; k < per; k += groups) {
+            const int at = k + group;
+            const bool on = at < per && row0 + at < N.rows;
+            const T* sr = base + (size_t)(on ? at : 0) * N.cols;
+            const T* dr = sr + (size_t)per * N.cols;
+            float v[2] = {there ? 0.f : __int_as_float(0x7fc00000), 0.f};
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int e = (p * tpr + lane) * V;
+                if (e >= N.cols) continue;
+                const Pc a = *reinterpret_cast<const Pc*>(sr + e), d = *reinterpret_cast<const Pc*>(dr + e);
+                const Pc f = kHold ? w[kHold ? p : 0] : weight ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float x = to_f32(a.x[j]);
+                    v[0] += x * x;
+                    v[1] += (one + to_f32(f.x[j])) * to_f32(d.x[j]) * x;
+                }
+            }
+            row_sum(v, tpr, sm[odd]);
+            odd ^= 1;
+            if (!NARROW && threadIdx.x == 0 && before >= 0 && !dead)  // every thread has left the buffer before
+                load(before + (int64_t)stages * gridDim.x, (st ? st : stages) - 1);
+            const float r = 1.f / sqrtf(v[0] * inv + N.eps), c = v[1] * inv * r * r;
+            const int64_t to = (row0 + at) * N.cols;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int e = (p * tpr + lane) * V;
+                if (!on || e >= N.cols) continue;
+                const Pc a = *reinterpret_cast<const Pc*>(sr + e), d = *reinterpret_cast<const Pc*>(dr + e);
+                const Pc f = kHold ? w[kHold ? p : 0] : weight ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
+                Pc g = Pc{}, o;
+                if (dsum) g = *reinterpret_cast<const Pc*>(dr + (size_t)per * N.cols + e);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float x = to_f32(a.x[j]), dy = to_f32(d.x[j]);
+                    o.x[j] = from_f32<T>(((one + to_f32(f.x[j])) * dy - x * c) * r + to_f32(g.x[j]));
+                    acc[p][j] += dy * (x * r);
+                }
+                *reinterpret_cast<Pc*>(dx + to + e) = o;
+            }
+        }
+        if (NARROW) {
+            __syncthreads();
+            if (threadIdx.x == 0 && !dead) load(item + (int64_t)stages * gridDim.x, st);
+        }
+        before = item;
+        if (++st == stages) {
+            st = 0;
+            turn ^= 1;
+        }
     }
+    if (NARROW) __syncthreads();  // the ring's memory is used again
+    put_part<V, P>(acc, part, N.cols, groups, group, lane, tpr, reinterpret_cast<float*>(ring));
+    end_ring(full, stages, dead);
 }
 
 // Rows too long for registers: twice over the row; a block's sums of dw lie in its own row of part.
@@ -416,7 +588,7 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* __restric
 struct RowShape {
     int tpr, p;
 };
-RowShape row_shape(int pieces, bool single, bool backward) {
+RowShape row_shape(int pieces, bool single) {
     if (pieces <= 32) {
         int t = 4;
         while (t < pieces) t *= 2;
@@ -424,9 +596,38 @@ RowShape row_shape(int pieces, bool single, bool backward) {
     }
     auto threads = [&](int p) { return ((pieces + p - 1) / p + 31) / 32 * 32; };
     if (single) return pieces <= 4096 ? RowShape{threads(4), 4} : pieces <= 16384 ? RowShape{threads(16), 16} : RowShape{0, 0};
-    if (pieces <= (backward ? 1024 : 256)) return {threads(1), 1};
+    if (pieces <= 256) return {threads(1), 1};
     if (pieces <= 2048) return {threads(2), 2};
     return pieces <= 4096 ? RowShape{threads(4), 4} : RowShape{0, 0};
+}
+
+// A ring's stages and blocks an SM for rows of `each` bytes in all: two blocks where those have two stages each.
+struct RingShape {
+    int stages, blocks;
+};
+constexpr size_t kRingBytes = 204800;
+RingShape ring_shape(int threads, size_t each) {
+    const int blocks = threads <= 512 && 4 * each <= kRingBytes ? 2 : 1;
+    return {(int)std::min<size_t>(kStages, kRingBytes / blocks / each), blocks};
+}
+
+template <typename T, int P>
+cudaError_t forward_ring(const NormDims& N, const T* x, const T* residual, const T* weight, T* out, uint8_t* out8,
+                         uint8_t* exps, T* sum, int threads, const RingShape& ring, int n_sm, cudaStream_t st) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const size_t sm = (size_t)ring.stages * N.cols * sizeof(T) * (residual ? 2 : 1);
+    const int blocks = n_sm * ring.blocks;
+    auto go = [&](auto eight) {
+        const auto kernel = norm_ring_kernel<T, V, P, decltype(eight)::value>;
+        static DeviceCache cache;
+        cudaError_t e = device_cached(cache, nullptr, [&](int, int*) {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+        });
+        if (e != cudaSuccess) return e;
+        kernel<<<blocks, threads, sm, st>>>(N, x, residual, weight, out, out8, exps, sum, ring.stages);
+        return cudaGetLastError();
+    };
+    return out8 ? go(std::true_type()) : go(std::false_type());
 }
 
 template <typename T, int V, int P>
@@ -445,24 +646,28 @@ cudaError_t forward(const NormDims& N, const T* x, const T* residual, const T* w
 
 template <typename T, int V, int P>
 cudaError_t backward(const NormDims& N, const T* s, const T* weight, const T* dout, const T* dsum, T* dx, float* part,
-                     int tpr, int* blocks, cudaStream_t st) {
-    static DeviceCache cache;
-    int n_sm = 0;
-    cudaError_t e = device_cached(cache, &n_sm, [](int dev, int* v) { return sm_count(dev, v); });
-    if (e != cudaSuccess) return e;
+                     int tpr, int n_sm, int* blocks, cudaStream_t st) {
     const int threads = tpr <= 32 ? kNarrow : tpr, groups = threads / tpr;
-    const int resident = std::max(1, 768 / threads);
-    *blocks = (int)std::min<int64_t>({(N.rows + groups - 1) / groups, (int64_t)n_sm * resident, kNormParts});
+    *blocks = (int)std::min<int64_t>({(N.rows + groups - 1) / groups, (int64_t)n_sm * (1024 / threads), kNormParts});
     const size_t sm = groups > 1 ? (size_t)groups * N.cols * sizeof(float) : 0;  // at most 128 threads x 8 values
-    auto go = [&](auto most) {
-        norm_backward_kernel<T, V, P, decltype(most)::value><<<*blocks, threads, sm, st>>>(N, s, weight, dout, dsum, dx, part, tpr);
-        return cudaGetLastError();
-    };
-    if constexpr (V > 1 && P == 1) {
-        if (threads <= kNarrow) return go(std::integral_constant<int, kNarrow>());
-        if (threads <= 768) return go(std::integral_constant<int, 768>());
-    }
-    return go(std::integral_constant<int, 1024>());
+    norm_backward_kernel<T, V, P><<<*blocks, threads, sm, st>>>(N, s, weight, dout, dsum, dx, part, tpr);
+    return cudaGetLastError();
+}
+
+template <typename T, int P, bool NARROW>
+cudaError_t backward_ring(const NormDims& N, const T* s, const T* weight, const T* dout, const T* dsum, T* dx, float* part,
+                          int threads, int tpr, int stages, int resident, int per, int n_sm, int* blocks, cudaStream_t st) {
+    const auto kernel = norm_backward_ring_kernel<T, P, NARROW>;
+    static DeviceCache cache;
+    cudaError_t e = device_cached(cache, nullptr, [&](int, int*) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+    });
+    if (e != cudaSuccess) return e;
+    *blocks = (int)std::min<int64_t>({(N.rows + per - 1) / per, (int64_t)n_sm * resident, kNormParts});
+    size_t sm = (size_t)stages * per * N.cols * sizeof(T) * (dsum ? 3 : 2);
+    if (NARROW) sm = std::max(sm, (size_t)(threads / tpr) * N.cols * sizeof(float));
+    kernel<<<*blocks, threads, sm, st>>>(N, s, weight, dout, dsum, dx, part, tpr, stages, per);
+    return cudaGetLastError();
 }
 
 template <typename T>
@@ -480,7 +685,7 @@ cudaError_t launch_norm(const NormDims& N, const T* x, const T* residual, const 
     constexpr int V = 16 / (int)sizeof(T);
     const uintptr_t a = (uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)out | (uintptr_t)sum;
     const bool vec = wide<T>(N, a);
-    const RowShape r = row_shape(vec ? N.cols / V : N.cols, !vec, false);
+    const RowShape r = row_shape(vec ? N.cols / V : N.cols, !vec);
     auto run = [&](auto v, auto p) {
         return forward<T, decltype(v)::value, decltype(p)::value>(N, x, residual, weight, out, out8, exps, sum, r.tpr, st);
     };
@@ -490,6 +695,21 @@ cudaError_t launch_norm(const NormDims& N, const T* x, const T* residual, const 
         if (out8) norm_long_kernel<T, true><<<(unsigned)N.rows, 1024, 0, st>>>(N, x, residual, weight, out, out8, exps, sum);
         else norm_long_kernel<T, false><<<(unsigned)N.rows, 1024, 0, st>>>(N, x, residual, weight, out, out8, exps, sum);
         return cudaGetLastError();
+    }
+    if (vec && r.tpr > 32) {
+        static DeviceCache cache;
+        int n_sm = 0;
+        const cudaError_t e = device_cached(cache, &n_sm, [](int dev, int* v) { return sm_count(dev, v); });
+        if (e != cudaSuccess) return e;
+        const int p = N.cols / V <= 256 ? 1 : N.cols / V <= 1024 ? 2 : 4, threads = (N.cols / V + 32 * p - 1) / (32 * p) * 32;
+        const RingShape ring = ring_shape(threads, (size_t)N.cols * sizeof(T) * (residual ? 2 : 1));
+        // (up to three rows a block: a block a row starts sooner)
+        if (threads <= 512 && ring.stages >= 2 && N.rows > (int64_t)3 * n_sm * ring.blocks) {
+            auto go = [&](auto pp) {
+                return forward_ring<T, decltype(pp)::value>(N, x, residual, weight, out, out8, exps, sum, threads, ring, n_sm, st);
+            };
+            return p == 1 ? go(One()) : p == 2 ? go(std::integral_constant<int, 2>()) : go(std::integral_constant<int, 4>());
+        }
     }
     if (!vec) return r.p == 1 ? run(One(), One()) : r.p == 4 ? run(One(), std::integral_constant<int, 4>()) : run(One(), std::integral_constant<int, 16>());
     return r.p == 1 ? run(Vec(), One()) : r.p == 2 ? run(Vec(), std::integral_constant<int, 2>()) : run(Vec(), std::integral_constant<int, 4>());
@@ -502,28 +722,57 @@ cudaError_t launch_norm_backward(const NormDims& N, const T* s, const T* weight,
     if (!dweight) part = nullptr;
     int blocks = 0;
     cudaError_t e = cudaSuccess;
+    auto finish = [&](cudaError_t e) {  // the blocks' sums
+        if (e != cudaSuccess || !dweight) return e;
+        norm_parts_kernel<<<(unsigned)((N.cols + 31) / 32), 1024, 0, st>>>(part, blocks, N.cols, dweight);
+        return cudaGetLastError();
+    };
     if (N.rows > 0) {
         const uintptr_t a = (uintptr_t)s | (uintptr_t)weight | (uintptr_t)dout | (uintptr_t)dsum | (uintptr_t)dx;
         const bool vec = wide<T>(N, a);
-        const RowShape r = row_shape(vec ? N.cols / V : N.cols, !vec, true);
-        auto run = [&](auto v, auto p) {
-            return backward<T, decltype(v)::value, decltype(p)::value>(N, s, weight, dout, dsum, dx, part, r.tpr, &blocks, st);
-        };
+        static DeviceCache cache;
+        int n_sm = 0;
+        e = device_cached(cache, &n_sm, [](int dev, int* v) { return sm_count(dev, v); });
+        if (e != cudaSuccess) return e;
+        const int pieces = vec ? N.cols / V : N.cols, n_in = dsum ? 3 : 2;
+        const RowShape r = row_shape(pieces, !vec);
+        const size_t row_bytes = (size_t)N.cols * sizeof(T);
         using One = std::integral_constant<int, 1>;
-        using Vec = std::integral_constant<int, V>;
+        using Two = std::integral_constant<int, 2>;
+        using Four = std::integral_constant<int, 4>;
+        auto run = [&](auto v, auto p) {
+            return backward<T, decltype(v)::value, decltype(p)::value>(N, s, weight, dout, dsum, dx, part, r.tpr, n_sm, &blocks, st);
+        };
+        if (vec && r.tpr <= 32 && r.tpr > 0 && N.heads == 1 && N.sx == N.cols) {
+            // buffers of about 8 KB a tensor, a multiple of the rows that the block's lanes take at once
+            const int groups = kNarrow / r.tpr, per = std::max<int>(groups, (int)(8192 / row_bytes) / groups * groups);
+            const int stages = 2;
+            const int resident = (int)std::min<size_t>(8, kRingBytes / (stages * per * row_bytes * n_in + 1024));
+            return finish(backward_ring<T, 1, true>(N, s, weight, dout, dsum, dx, part, kNarrow, r.tpr, stages, resident, per, n_sm,
+                                                    &blocks, st));
+        }
+        if (vec && r.tpr > 32) {
+            const int p = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 4, threads = (pieces + 32 * p - 1) / (32 * p) * 32;
+            const RingShape ring = ring_shape(threads, row_bytes * n_in);
+            if (threads <= 512 && ring.stages >= 2) {
+                auto go = [&](auto pp) {
+                    return backward_ring<T, decltype(pp)::value, false>(N, s, weight, dout, dsum, dx, part, threads, threads, ring.stages,
+                                                                        ring.blocks, 1, n_sm, &blocks, st);
+                };
+                return finish(p == 1 ? go(One()) : p == 2 ? go(Two()) : go(Four()));
+            }
+        }
         if (r.tpr == 0) {
             blocks = (int)std::min<int64_t>(N.rows, 304);
             norm_backward_long_kernel<T><<<blocks, 1024, 0, st>>>(N, s, weight, dout, dsum, dx, part);
             e = cudaGetLastError();
         } else if (!vec) {
-            e = r.p == 1 ? run(One(), One()) : r.p == 4 ? run(One(), std::integral_constant<int, 4>()) : run(One(), std::integral_constant<int, 16>());
+            e = r.p == 1 ? run(One(), One()) : r.p == 4 ? run(One(), Four()) : run(One(), std::integral_constant<int, 16>());
         } else {
-            e = r.p == 1 ? run(Vec(), One()) : r.p == 2 ? run(Vec(), std::integral_constant<int, 2>()) : run(Vec(), std::integral_constant<int, 4>());
+            e = r.p == 1 ? run(std::integral_constant<int, V>(), One()) : run(std::integral_constant<int, V>(), Four());
         }
     }
-    if (e != cudaSuccess || !dweight) return e;
-    norm_parts_kernel<<<(unsigned)((N.cols + 31) / 32), 1024, 0, st>>>(part, blocks, N.cols, dweight);
-    return cudaGetLastError();
+    return finish(e);
 }
 
 #define HLA_NORM(T)                                                                                                  \
