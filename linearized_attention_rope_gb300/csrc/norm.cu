@@ -429,10 +429,23 @@ norm_backward_kernel(const NormDims N, const T* s, const T* __restrict__ weight,
     put_part<V, P>(acc, part, N.cols, groups, group, lane, tpr, cols_sm);
 }
 
+// A piece in fp32, two values at a time.
+template <typename T, int V> __device__ __forceinline__ void pairs(const Piece<T, V>& a, float2 (&o)[V / 2]) {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(a.x)[j];
+            o[j] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        } else {
+            o[j] = make_float2(a.x[2 * j], a.x[2 * j + 1]);
+        }
+    }
+}
+
 // The same from a ring of row buffers (s, dout and dsum), which both passes over a row read.  NARROW: a warp or less takes
 // a row, and a buffer holds `per` dense rows; else one.
 template <typename T, int P, bool NARROW>
-__global__ void __launch_bounds__(NARROW ? kNarrow : 512, NARROW ? 8 : 2)
+__global__ void __launch_bounds__(NARROW ? kNarrow : P == 1 ? 256 : 512, NARROW ? 6 : 2)
 norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ weight, const T* dout, const T* dsum, T* dx,
                           float* part, int tpr, int stages, int per) {
     constexpr int V = 16 / (int)sizeof(T);
@@ -460,17 +473,23 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
     start_ring(full, stages, &dead);
     if (threadIdx.x == 0)
         for (int i = 0; i < stages; ++i) load(blockIdx.x + (int64_t)i * gridDim.x, i);
-    constexpr bool kHold = P * V <= 8;  // the weights stay in registers
-    Pc w[kHold ? P : 1];
-    float acc[P][V];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int e = (p * tpr + lane) * V;
-        if (kHold) w[kHold ? p : 0] = weight && e < N.cols ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[p][j] = 0.f;
-    }
+    constexpr bool kHold = P * V <= 8, kRow = P == 1;  // the factors, the row stay in registers between the passes
+    constexpr int H = V / 2;
+    constexpr int K = kHold ? P : 1;
+    float2 f[K][H], x[H], dy[H], acc[P][H];
     const float one = weight ? N.offset : 1.f;
+    auto factors = [&](int h, int e) {
+        const Pc w = weight && e < N.cols ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
+#pragma unroll
+        for (int j = 0; j < H; ++j) f[h][j] = make_float2(one + to_f32(w.x[2 * j]), one + to_f32(w.x[2 * j + 1]));
+    };
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < H; ++j) acc[p][j] = make_float2(0.f, 0.f);
+    if (kHold)
+#pragma unroll
+        for (int p = 0; p < K; ++p) factors(p, (p * tpr + lane) * V);
     int st = 0, turn = 0, odd = 0;
     int64_t before = -1;  // the item whose buffer can be filled again, its stage the one before
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -482,39 +501,49 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
             const bool on = at < per && row0 + at < N.rows;
             const T* sr = base + (size_t)(on ? at : 0) * N.cols;
             const T* dr = sr + (size_t)per * N.cols;
-            float v[2] = {there ? 0.f : __int_as_float(0x7fc00000), 0.f};
+            auto take = [&](int h, int e) {
+                const Pc a = *reinterpret_cast<const Pc*>(sr + e), d = *reinterpret_cast<const Pc*>(dr + e);
+                pairs<T, V>(a, x);
+                pairs<T, V>(d, dy);
+                if (!kHold) factors(h, e);
+            };
+            float2 v0 = make_float2(there ? 0.f : __int_as_float(0x7fc00000), 0.f), v1 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                const int e = (p * tpr + lane) * V;
+                const int e = (p * tpr + lane) * V, h = kHold ? p : 0;
                 if (e >= N.cols) continue;
-                const Pc a = *reinterpret_cast<const Pc*>(sr + e), d = *reinterpret_cast<const Pc*>(dr + e);
-                const Pc f = kHold ? w[kHold ? p : 0] : weight ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
+                take(h, e);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float x = to_f32(a.x[j]);
-                    v[0] += x * x;
-                    v[1] += (one + to_f32(f.x[j])) * to_f32(d.x[j]) * x;
+                for (int j = 0; j < H; ++j) {
+                    v0 = ffma2(x[j], x[j], v0);
+                    v1 = ffma2(mul2(f[h][j], dy[j]), x[j], v1);
                 }
             }
+            float v[2] = {v0.x + v0.y, v1.x + v1.y};
             row_sum(v, tpr, sm[odd]);
             odd ^= 1;
             if (!NARROW && threadIdx.x == 0 && before >= 0 && !dead)  // every thread has left the buffer before
                 load(before + (int64_t)stages * gridDim.x, (st ? st : stages) - 1);
-            const float r = 1.f / sqrtf(v[0] * inv + N.eps), c = v[1] * inv * r * r;
+            const float r = rsqrtf(v[0] * inv + N.eps), cr = -v[1] * inv * r * r * r;
+            const float2 r2 = make_float2(r, r), cr2 = make_float2(cr, cr);
             const int64_t to = (row0 + at) * N.cols;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                const int e = (p * tpr + lane) * V;
+                const int e = (p * tpr + lane) * V, h = kHold ? p : 0;
                 if (!on || e >= N.cols) continue;
-                const Pc a = *reinterpret_cast<const Pc*>(sr + e), d = *reinterpret_cast<const Pc*>(dr + e);
-                const Pc f = kHold ? w[kHold ? p : 0] : weight ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
-                Pc g = Pc{}, o;
-                if (dsum) g = *reinterpret_cast<const Pc*>(dr + (size_t)per * N.cols + e);
+                if (!kRow) take(h, e);
+                float2 g[H];
+                if (dsum) pairs<T, V>(*reinterpret_cast<const Pc*>(dr + (size_t)per * N.cols + e), g);
+                Pc o;
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float x = to_f32(a.x[j]), dy = to_f32(d.x[j]);
-                    o.x[j] = from_f32<T>(((one + to_f32(f.x[j])) * dy - x * c) * r + to_f32(g.x[j]));
-                    acc[p][j] += dy * (x * r);
+                for (int j = 0; j < H; ++j) {  // dy r: times f for dx, times x for dw
+                    const float2 u = mul2(dy[j], r2);
+                    float2 y = mul2(x[j], cr2);
+                    if (dsum) y = ffma2(x[j], cr2, g[j]);
+                    y = ffma2(f[h][j], u, y);
+                    acc[p][j] = ffma2(u, x[j], acc[p][j]);
+                    o.x[2 * j] = from_f32<T>(y.x);
+                    o.x[2 * j + 1] = from_f32<T>(y.y);
                 }
                 *reinterpret_cast<Pc*>(dx + to + e) = o;
             }
@@ -530,7 +559,15 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
         }
     }
     if (NARROW) __syncthreads();  // the ring's memory is used again
-    put_part<V, P>(acc, part, N.cols, groups, group, lane, tpr, reinterpret_cast<float*>(ring));
+    float sums[P][V];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            sums[p][2 * j] = acc[p][j].x;
+            sums[p][2 * j + 1] = acc[p][j].y;
+        }
+    put_part<V, P>(sums, part, N.cols, groups, group, lane, tpr, reinterpret_cast<float*>(ring));
     end_ring(full, stages, dead);
 }
 
@@ -747,7 +784,7 @@ cudaError_t launch_norm_backward(const NormDims& N, const T* s, const T* weight,
             // buffers of about 8 KB a tensor, a multiple of the rows that the block's lanes take at once
             const int groups = kNarrow / r.tpr, per = std::max<int>(groups, (int)(8192 / row_bytes) / groups * groups);
             const int stages = 2;
-            const int resident = (int)std::min<size_t>(8, kRingBytes / (stages * per * row_bytes * n_in + 1024));
+            const int resident = (int)std::min<size_t>(6, kRingBytes / (stages * per * row_bytes * n_in + 1024));
             return finish(backward_ring<T, 1, true>(N, s, weight, dout, dsum, dx, part, kNarrow, r.tpr, stages, resident, per, n_sm,
                                                     &blocks, st));
         }
