@@ -6,7 +6,7 @@ namespace hla {
 namespace {
 
 template <typename T, typename G, int CPL, bool SHARED, bool VEC, int ROWS>
-__global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, ROWS == 8 ? (CPL == 4 ? 3 : 4) : VEC && sizeof(T) == 2 ? 3 : 2)
 recurrence_kernel(const RecDims R, const G* __restrict__ g, const T* __restrict__ x, const float* h0,
                   const int32_t* __restrict__ cu, T* __restrict__ out, float* h_last, float* __restrict__ states,
                   const Carry S, int n_time, int n_slabs, int32_t* err) {

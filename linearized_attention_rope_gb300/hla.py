@@ -850,21 +850,23 @@ def _check_matrix(t, fn: str, name: str, dtype, shape, device) -> int:
     """The row stride of t in elements, as _check_tensor takes strided rows, for [rows, columns] as well."""
     if len(shape) == 3:
         return _check_tensor(t, fn, name, dtype, shape, device, strided=True)
-    if isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype == dtype and t.device == device and t.shape == shape and \
-            t.stride(1) == 1 and t.stride(0) >= shape[1] and shape[0] > 1:
-        return t.stride(0)
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and shape[0] > 1:
+        rows, one = t.stride()
+        if one == 1 and rows >= shape[1]:
+            return rows
     _check_tensor(t, fn, name, dtype, shape, device)
     return shape[1]
 
 
 def _sized(t, fn: str, name: str, *dims):
     """Refuses what is no tensor of one of the numbers of dimensions given."""
-    _need(isinstance(t, torch.Tensor) and t.dim() in dims, f"{fn}: {name}: expected a tensor of {dims} dimensions")
+    if not isinstance(t, torch.Tensor) or t.dim() not in dims:
+        _refuse(f"{fn}: {name}: expected a tensor of {dims} dimensions")
 
 
-def _dense(t, stride: int):
-    """An uninitialised dense tensor of t's shape; stride: t's, from _check_matrix."""
-    if stride == t.stride(0) and t.is_contiguous():
+def _dense(t):
+    """An uninitialised dense tensor of t's shape."""
+    if t.is_contiguous():
         return torch.empty_like(t)
     return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
@@ -900,7 +902,8 @@ class Normed(NamedTuple):
 def _norm_rows(params: NormParams, fn: str, x, name: str):
     """Checks the rows x: [T, n_cols], or [T, n_heads, n_cols] for more heads than one."""
     dt = _TORCH.get(params.dtype)
-    _need(dt is not None and dt != torch.uint8, f"{fn}: dtype")
+    if dt is None or dt == torch.uint8:
+        _refuse(f"{fn}: dtype")
     _sized(x, fn, name, 2 if params.n_heads == 1 else 3)
     shape = (x.shape[0], params.n_cols) if params.n_heads == 1 else (x.shape[0], params.n_heads, params.n_cols)
     return dt, shape, _check_matrix(x, fn, name, dt, shape, x.device)
@@ -932,9 +935,9 @@ def rms_norm(params: NormParams, x, weight=None, residual=None, out=None, exp=No
         with _on(dev, stream, x, weight, residual, out, exp, sum):
             return rms_norm(params, x, weight, residual, out, exp, sum)
     if residual is not None and sum is None:
-        sum = _dense(x, xs)
+        sum = _dense(x)
     if out is None:
-        out = torch.empty(shape, dtype=torch.uint8, device=dev) if eight else _dense(x, xs)
+        out = torch.empty(shape, dtype=torch.uint8, device=dev) if eight else _dense(x)
     if eight and exp is None:
         exp = torch.empty(groups, dtype=torch.uint8, device=dev)
     _check(load().hla_rms_norm(_c(params, xs, rs), _adr(x), _adr(residual), _adr(weight), shape[0], _adr(out), _adr(exp),
@@ -1012,15 +1015,22 @@ def alloc_recurrence_states(params: RecurrenceParams, total_tokens: int, device=
     return torch.empty((-(-total_tokens // RECURRENCE_STATE_ROWS), params.n_channels), dtype=torch.float32, device=device)
 
 
-def _recurrence_rows(params: RecurrenceParams, fn: str, g, x):
-    """Checks g [T, n_channels / gate_dim] and x [T, n_channels]; returns their types, T and strides."""
+@functools.lru_cache(maxsize=256)
+def _recurrence_types(params: RecurrenceParams, fn: str):
+    """The types of x and g, and the gates of a row."""
     dt, gt = _TORCH.get(params.dtype), _TORCH.get(params.gate_dtype)
     _need(dt is not None and gt is not None and torch.uint8 not in (dt, gt), f"{fn}: dtype")
-    _sized(x, fn, "x", 2)
-    n, c = x.shape[0], params.n_channels
     _need(params.gate_dim > 0, f"{fn}: gate_dim")
-    return dt, gt, n, (_check_matrix(x, fn, "x", dt, (n, c), x.device),
-                       _check_matrix(g, fn, "g", gt, (n, c // params.gate_dim), x.device))
+    return dt, gt, params.n_channels // params.gate_dim
+
+
+def _recurrence_rows(params: RecurrenceParams, fn: str, g, x):
+    """Checks g [T, n_channels / gate_dim] and x [T, n_channels]; returns their types, T and strides."""
+    dt, gt, gates = _recurrence_types(params, fn)
+    _sized(x, fn, "x", 2)
+    n, dev = x.shape[0], x.device
+    return dt, gt, n, (_check_matrix(x, fn, "x", dt, (n, params.n_channels), dev),
+                       _check_matrix(g, fn, "g", gt, (n, gates), dev))
 
 
 def _check_states(params, fn, n, cu_seqlens, h0, states, dev, **rows):
@@ -1055,7 +1065,7 @@ def recurrence(params: RecurrenceParams, g, x, cu_seqlens, h0=None, out=None, h_
         with _on(dev, stream, g, x, cu_seqlens, h0, out, h_last, states, ws):
             return recurrence(params, g, x, cu_seqlens, h0, out, h_last, states, ws)
     if out is None:
-        out = _dense(x, strides[0])
+        out = _dense(x)
     if h_last is None:
         h_last = torch.empty((n_seqs, params.n_channels), dtype=torch.float32, device=dev)
     if ws is None:
@@ -1086,7 +1096,7 @@ def recurrence_backward(params: RecurrenceParams, g, x, states, dout, cu_seqlens
         with _on(dev, stream, g, x, states, dout, cu_seqlens, h0, dh_last, ws, *given.values()):
             return recurrence_backward(params, g, x, states, dout, cu_seqlens, h0, dh_last, grads, ws)
     if grads is None:
-        grads = {"g": _dense(g, strides[1]), "x": torch.empty_like(dout)}
+        grads = {"g": _dense(g), "x": torch.empty_like(dout)}
         if h0 is not None:
             grads["h0"] = torch.empty_like(h0)
     if ws is None:
@@ -1111,7 +1121,7 @@ def recurrence_step(params: RecurrenceParams, g, x, h, out=None, stream=None):
         with _on(dev, stream, g, x, h, out):
             return recurrence_step(params, g, x, h, out)
     if out is None:
-        out = _dense(x, strides[0])
+        out = _dense(x)
     _check(load().hla_recurrence_step(_c(params, *strides), _adr(g), _adr(x), _adr(h), n, _adr(out), st), fn)
     return out
 
@@ -1141,7 +1151,8 @@ def alloc_linear4_workspace(params: Linear4Params, tokens: int, device="cuda"):
 
 def _linear4_weights(params: Linear4Params, fn: str, w, scales, offsets, dev):
     dt = _TORCH.get(params.dtype)
-    _need(dt is not None and dt != torch.uint8 and params.group > 0, f"{fn}: dtype or group")
+    if dt is None or dt == torch.uint8 or params.group <= 0:
+        _refuse(f"{fn}: dtype or group")
     _check_tensor(w, fn, "w", torch.uint8, (params.n_out, params.n_in // 2), dev)
     shape = (params.n_out, params.n_in // params.group)
     _check_tensor(scales, fn, "scales", dt, shape, dev)
@@ -1158,7 +1169,8 @@ def linear4(params: Linear4Params, x, w, scales, offsets=None, x_exp=None, out=N
     dev, n = x.device, x.shape[0]
     dt = _linear4_weights(params, fn, w, scales, offsets, dev)
     stride = _check_matrix(x, fn, "x", torch.uint8 if eight else dt, (n, params.n_in), dev)
-    _need(eight == (x_exp is not None), f"{fn}: exponents go with 8-bit rows")
+    if eight != (x_exp is not None):
+        _refuse(f"{fn}: exponents go with 8-bit rows")
     if eight:
         _check_tensor(x_exp, fn, "x_exp", torch.uint8, (n, params.n_in // params.x_group if params.x_group else 1), dev)
     if out is not None:
