@@ -126,7 +126,7 @@ struct Linear4Dims {
     int64_t rows, sx;  // tokens; token stride of x in elements
     int n_in, n_out, group, x_group;
 };
-constexpr int64_t kFewRows = 8;  // that no rows are laid out for
+constexpr int64_t kFewRows = 16;  // that no rows are laid out for
 // Blocks of a cluster that share a tile's inputs: of 1, 2, 4 and 8 the one with the least sum of rounds (of `blocks` at a
 // time) by steps, where a block's start and end take as long as `ends` steps.
 int linear4_split(int64_t tiles, int64_t stages, int64_t blocks, int64_t ends);

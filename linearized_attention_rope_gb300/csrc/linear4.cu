@@ -7,7 +7,7 @@
 // in fp32 as it is added to the row's.  (Scaled weights would have to be rounded to bf16 each.)  Which k a lane's
 // operands stand for is free, as long as both agree: a lane takes words of a weight row as they lie.
 //
-// A block takes 128 or 256 rows, 16 or 32 a warp, and, in a cluster of C, a C-th of the inputs; the tokens' inputs and the
+// A block takes 128 rows, 16 a warp, and, in a cluster of C, a C-th of the inputs; the tokens' inputs and the
 // rows' scales come into shared memory 1024 inputs at a time, in the order in which lanes read them: fp32 rows as three
 // bf16 parts, cut off 8 bits at a time (nothing is lost), 8-bit rows as bf16 (exact, too).  Offsets are multiplied by the
 // group's sum of x, formed on that way.  Weights are two steps (of 128 inputs) ahead of the products.  The cluster's
@@ -21,6 +21,7 @@ namespace hla {
 namespace {
 
 constexpr int kWarps4 = 8, kThreads4 = 32 * kWarps4;
+constexpr int kAhead = 2;  // steps of weights under way
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -32,6 +33,12 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t w, int s) {
     const uint32_t y = ((w >> s) & 0x000f000fu) | 0x43004300u, off = 0x43084308u;
     const __nv_bfloat162 d = __hsub2(reinterpret_cast<const __nv_bfloat162&>(y), reinterpret_cast<const __nv_bfloat162&>(off));
     return reinterpret_cast<const uint32_t&>(d);
+}
+
+__device__ __forceinline__ uint4 load_far(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
 
 // fp32 as three bf16 parts; an infinity or NaN is in the first alone.
@@ -46,11 +53,11 @@ __device__ __forceinline__ void three_parts(float v, __nv_bfloat16 (&o)[3]) {
     }
 }
 
-template <typename T, typename X, int RT, int MT, int GROUP, bool OFFS>
+template <typename T, typename X, int MT, int GROUP, bool OFFS>
 struct Plan {
     static constexpr int kParts = sizeof(X) == 4 ? 3 : 1;
     static constexpr int kSteps = sizeof(X) == 4 ? 4 : 8;  // of 128 inputs, in shared memory
-    static constexpr int kRows = 16 * RT * kWarps4, kTok = 8 * MT;
+    static constexpr int kRows = 16 * kWarps4, kTok = 8 * MT;
     static constexpr int kPitch = kSteps * 256 + 64;  // bytes of a token: two rows' 64 bytes lie in different banks
     static constexpr int kGroups = kSteps * (128 / GROUP);
     static constexpr int kScalePitch = kRows + 2;
@@ -59,11 +66,11 @@ struct Plan {
     static constexpr size_t kSmem = std::max<size_t>(kIn, (size_t)kTok * kRows * 4);
 };
 
-template <typename T, typename X, int RT, int MT, int GROUP, bool OFFS>
-__global__ void __launch_bounds__(kThreads4, 2)
+template <typename T, typename X, int MT, int GROUP, bool OFFS>
+__global__ void __launch_bounds__(kThreads4, 3)
 linear4_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t* __restrict__ exps, const uint8_t* __restrict__ w,
                const T* __restrict__ scales, const T* __restrict__ offsets, T* __restrict__ out, int n_split, bool vec) {
-    using S = Plan<T, X, RT, MT, GROUP, OFFS>;
+    using S = Plan<T, X, MT, GROUP, OFFS>;
     constexpr int kWords = GROUP / 32, kSub = 128 / GROUP;  // words of a lane per group, groups of a step
     extern __shared__ __align__(16) uint8_t sm[];
     T* const sm_scale = reinterpret_cast<T*>(sm + S::kX);                // [group][row]
@@ -73,45 +80,40 @@ linear4_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t* __re
     const uint32_t rank = n_split > 1 ? cluster_rank() : 0;
     const int n0 = blockIdx.x / n_split * S::kRows, n_groups = L.n_in / GROUP, stages = (L.n_in + 127) / 128;
     const int s0 = (int)((int64_t)stages * rank / n_split), s1 = (int)((int64_t)stages * (rank + 1) / n_split);
-    const uint8_t* wr[RT][2];
+    const uint8_t* wr[2];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            wr[r][h] = w + (int64_t)min(n0 + warp * 16 * RT + r * 16 + h * 8 + gq, L.n_out - 1) * (L.n_in / 2) + tq * (kWords * 4);
-    uint32_t q[2][RT][2][4];
-    auto fetch = [&](uint32_t (&v)[RT][2][4], int s) {
+    for (int h = 0; h < 2; ++h)
+        wr[h] = w + (int64_t)min(n0 + warp * 16 + h * 8 + gq, L.n_out - 1) * (L.n_in / 2) + tq * (kWords * 4);
+    const int x_shift = L.x_group == 32 ? 5 : 7, x_groups = L.x_group ? L.n_in >> x_shift : 1;  // of a row's exponents
+    uint32_t q[kAhead][2][4];
+    auto fetch = [&](uint32_t (&v)[2][4], int s) {
 #pragma unroll
         for (int g = 0; g < kSub; ++g) {
             // (a group may lie behind the last one: zeros there, and nothing to multiply)
             const bool on = s < s1 && (GROUP == 128 || s * kSub + g < n_groups);
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t* p = wr[r][h] + (int64_t)s * 64 + g * (GROUP / 2);
-                    uint32_t* o = v[r][h] + g * kWords;
-                    if constexpr (kWords == 4) {
-                        const uint4 y = on ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-                        o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
-                    } else if constexpr (kWords == 2) {
-                        const uint2 y = on ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-                        o[0] = y.x; o[1] = y.y;
-                    } else {
-                        o[0] = on ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0;
-                    }
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* p = wr[h] + (int64_t)s * 64 + g * (GROUP / 2);
+                uint32_t* o = v[h] + g * kWords;
+                if constexpr (kWords == 4) {
+                    const uint4 y = on ? load_far(p) : make_uint4(0, 0, 0, 0);
+                    o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
+                } else if constexpr (kWords == 2) {
+                    const uint2 y = on ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+                    o[0] = y.x; o[1] = y.y;
+                } else {
+                    o[0] = on ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0;
                 }
+            }
         }
     };
-    fetch(q[0], s0);
-    fetch(q[1], s0 + 1);
-    float acc[RT][MT][4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int d = 0; d < kAhead; ++d) fetch(q[d], s0 + d);
+    float acc[MT][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][m][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
     for (int c0 = s0; c0 < s1; c0 += S::kSteps) {
         __syncthreads();
         // the tokens' inputs, 8 at a time, where the lane that takes them has its four lanes' words in a row
@@ -120,9 +122,7 @@ linear4_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t* __re
             const int t = j / (S::kSteps * 16), c = j % (S::kSteps * 16);
             const int64_t row = (int64_t)blockIdx.y * S::kTok + t;
             const int k = c0 * 128 + c * 8;
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            float2 v[4] = {};  // inputs 2i, 2i + 1
             if (row < L.rows && k < L.n_in) {
                 const X* p = x + row * L.sx + k;
                 Piece<X, 8> y;
@@ -133,33 +133,36 @@ linear4_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t* __re
                     for (int i = 0; i < 8; ++i) y.x[i] = p[i];
                 }
                 if constexpr (sizeof(X) == 1) {
-                    const int group = L.x_group ? L.x_group : L.n_in;
-                    const float f = group_pow2((int)exps[row * (L.n_in / group) + k / group] - 127);
+                    const float f = group_pow2((int)exps[row * x_groups + (L.x_group ? k >> x_shift : 0)] - 127);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)y.x[i], __NV_E4M3))) * f;
+                    for (int i = 0; i < 4; ++i) {
+                        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(reinterpret_cast<const __nv_fp8x2_storage_t*>(y.x)[i], __NV_E4M3);
+                        v[i] = mul2(__half22float2(__half2(h)), make_float2(f, f));
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = to_f32(y.x[i]);
+                    for (int i = 0; i < 4; ++i) v[i] = make_float2(to_f32(y.x[2 * i]), to_f32(y.x[2 * i + 1]));
                 }
             }
             constexpr int kIn = GROUP / 8;  // pieces of a group
             const int in = c % 16 % kIn, at = c / 16 * 16 + (c % 16 / kIn * kWords + in % kWords) * 4 + in / kWords;
+            // pairs (i, i + 4), as the weights' nibbles are taken
             if constexpr (S::kParts == 1) {
-                Piece<__nv_bfloat16, 8> o;  // pairs (i, i + 4), as the weights' nibbles are taken
+                uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o.x[2 * i] = from_f32<__nv_bfloat16>(v[i]);
-                    o.x[2 * i + 1] = from_f32<__nv_bfloat16>(v[i + 4]);
+                for (int i = 0; i < 2; ++i) {
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(v[i].x, v[i + 2].x), b = __floats2bfloat162_rn(v[i].y, v[i + 2].y);
+                    o[2 * i] = reinterpret_cast<const uint32_t&>(a);
+                    o[2 * i + 1] = reinterpret_cast<const uint32_t&>(b);
                 }
-                *reinterpret_cast<Piece<__nv_bfloat16, 8>*>(sm + t * S::kPitch + at * 16) = o;
+                *reinterpret_cast<uint4*>(sm + t * S::kPitch + at * 16) = make_uint4(o[0], o[1], o[2], o[3]);
             } else {
                 Piece<__nv_bfloat16, 8> o[3];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     __nv_bfloat16 lo[3], hi[3];
-                    three_parts(v[i], lo);
-                    three_parts(v[i + 4], hi);
+                    three_parts(i & 1 ? v[i / 2].y : v[i / 2].x, lo);
+                    three_parts(i & 1 ? v[i / 2 + 2].y : v[i / 2 + 2].x, hi);
 #pragma unroll
                     for (int p = 0; p < 3; ++p) {
                         o[p].x[2 * i] = lo[p];
@@ -171,98 +174,87 @@ linear4_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t* __re
                     *reinterpret_cast<Piece<__nv_bfloat16, 8>*>(sm + (p * S::kTok + t) * S::kPitch + at * 16) = o[p];
             }
             if constexpr (OFFS) {
-                float y = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+                const float2 z = add2(add2(v[0], v[1]), add2(v[2], v[3]));
+                float y = z.x + z.y;
 #pragma unroll
                 for (int o = kIn / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
                 if (in == 0) sm_sum[c / kIn * S::kTok + t] = y;
             }
         }
+        const int g = threadIdx.x % S::kGroups, gg = c0 * kSub + g;
 #pragma unroll 4
-        for (int i = threadIdx.x; i < S::kRows * S::kGroups; i += kThreads4) {
-            const int row = i / S::kGroups, g = i % S::kGroups, gg = c0 * kSub + g;
+        for (int row = threadIdx.x / S::kGroups; row < S::kRows; row += kThreads4 / S::kGroups) {
             const int64_t from = (int64_t)min(n0 + row, L.n_out - 1) * n_groups + gg;
             sm_scale[g * S::kScalePitch + row] = gg < n_groups ? scales[from] : from_f32<T>(0.f);
             if constexpr (OFFS) sm_off[g * S::kScalePitch + row] = gg < n_groups ? offsets[from] : from_f32<T>(0.f);
         }
         __syncthreads();
-        auto step = [&](uint32_t (&v)[RT][2][4], int st) {
+        auto step = [&](uint32_t (&v)[2][4], int st) {
 #pragma unroll
             for (int g = 0; g < kSub; ++g) {
-                float part[RT][MT][4];
+                float part[MT][4];
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) part[r][m][i] = 0.f;
+                    for (int i = 0; i < 4; ++i) part[m][i] = 0.f;
 #pragma unroll
                 for (int k = 0; k < kWords; ++k) {
-                    uint32_t a[RT][2][4];
+                    uint32_t a[2][4];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            const uint32_t lo = v[r][0][g * kWords + k], hi = v[r][1][g * kWords + k];
-                            a[r][s][0] = nibbles(lo, 8 * s);
-                            a[r][s][1] = nibbles(hi, 8 * s);
-                            a[r][s][2] = nibbles(lo, 8 * s + 4);
-                            a[r][s][3] = nibbles(hi, 8 * s + 4);
-                        }
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t lo = v[0][g * kWords + k], hi = v[1][g * kWords + k];
+                        a[s][0] = nibbles(lo, 8 * s);
+                        a[s][1] = nibbles(hi, 8 * s);
+                        a[s][2] = nibbles(lo, 8 * s + 4);
+                        a[s][3] = nibbles(hi, 8 * s + 4);
+                    }
 #pragma unroll
                     for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             const uint4 b = *reinterpret_cast<const uint4*>(
                                 sm + (p * S::kTok + m * 8 + gq) * S::kPitch + (st * 16 + (g * kWords + k) * 4 + tq) * 16);
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                mma16816(part[r][m], a[r][0], b.x, b.y);
-                                mma16816(part[r][m], a[r][1], b.z, b.w);
-                            }
+                            mma16816(part[m], a[0], b.x, b.y);
+                            mma16816(part[m], a[1], b.z, b.w);
                         }
                 }
-                const int gi = st * kSub + g, row = warp * 16 * RT + gq;
+                const int gi = st * kSub + g, row = warp * 16 + gq;
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     float2 sum;
                     if constexpr (OFFS) sum = *reinterpret_cast<const float2*>(sm_sum + gi * S::kTok + m * 8 + tq * 2);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int at = gi * S::kScalePitch + row + r * 16 + h * 8;
-                            const float sc = to_f32(sm_scale[at]);
-                            float2 y = make_float2(acc[r][m][2 * h], acc[r][m][2 * h + 1]);
-                            y = ffma2(make_float2(sc, sc), make_float2(part[r][m][2 * h], part[r][m][2 * h + 1]), y);
-                            if constexpr (OFFS) {
-                                const float of = to_f32(sm_off[at]);
-                                y = ffma2(make_float2(of, of), sum, y);
-                            }
-                            acc[r][m][2 * h] = y.x;
-                            acc[r][m][2 * h + 1] = y.y;
+                    for (int h = 0; h < 2; ++h) {
+                        const int at = gi * S::kScalePitch + row + h * 8;
+                        const float sc = to_f32(sm_scale[at]);
+                        float2 y = make_float2(acc[m][2 * h], acc[m][2 * h + 1]);
+                        y = ffma2(make_float2(sc, sc), make_float2(part[m][2 * h], part[m][2 * h + 1]), y);
+                        if constexpr (OFFS) {
+                            const float of = to_f32(sm_off[at]);
+                            y = ffma2(make_float2(of, of), sum, y);
                         }
+                        acc[m][2 * h] = y.x;
+                        acc[m][2 * h + 1] = y.y;
+                    }
                 }
             }
         };
         // (a group behind the last one: scale, offset and inputs are 0)
-        for (int st = 0; st < S::kSteps && c0 + st < s1; st += 2) {
-            step(q[0], st);
-            fetch(q[0], c0 + st + 2);
-            if (c0 + st + 1 < s1) {
-                step(q[1], st + 1);
-                fetch(q[1], c0 + st + 3);
-            }
-        }
+        for (int st = 0; st < S::kSteps; st += kAhead)
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d)
+                if (c0 + st + d < s1) {
+                    step(q[d], st + d);
+                    fetch(q[d], c0 + st + d + kAhead);
+                }
     }
     __syncthreads();
     float* const sums = reinterpret_cast<float*>(sm);  // [token][row]
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sums[(m * 8 + tq * 2 + (i & 1)) * S::kRows + warp * 16 * RT + r * 16 + (i >> 1) * 8 + gq] = acc[r][m][i];
+        for (int i = 0; i < 4; ++i)
+            sums[(m * 8 + tq * 2 + (i & 1)) * S::kRows + warp * 16 + (i >> 1) * 8 + gq] = acc[m][i];
     if (n_split > 1) cluster_sync_all();
     else __syncthreads();
     const int t0 = (int)(S::kTok * rank / n_split), t1 = (int)(S::kTok * (rank + 1) / n_split);
@@ -351,14 +343,14 @@ linear4_quantize_kernel(const Linear4Dims L, const T* __restrict__ weight, uint8
 template <typename T, typename X, int MT, int GROUP, bool OFFS>
 cudaError_t run(const Linear4Dims& L, const X* x, const uint8_t* exps, const uint8_t* w, const T* scales, const T* offsets,
                 T* out, cudaStream_t st) {
-    using S = Plan<T, X, 2, MT, GROUP, OFFS>;
-    const auto kernel = linear4_kernel<T, X, 2, MT, GROUP, OFFS>;
+    using S = Plan<T, X, MT, GROUP, OFFS>;
+    const auto kernel = linear4_kernel<T, X, MT, GROUP, OFFS>;
     static DeviceCache cache;
     cudaError_t e = device_cached(cache, nullptr, [&](int, int*) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    const int tiles = (L.n_out + S::kRows - 1) / S::kRows, c = linear4_split(tiles, (L.n_in + 127) / 128, 152, 2);
+    const int tiles = (L.n_out + S::kRows - 1) / S::kRows, c = linear4_split(tiles, (L.n_in + 127) / 128, 456, 4);
     ClusterCfg cfg(dim3((unsigned)(tiles * c), (unsigned)((L.rows + S::kTok - 1) / S::kTok)), kThreads4, S::kSmem, st, c);
     const bool vec = (uintptr_t)x % (8 * sizeof(X) > 16 ? 16 : 8 * sizeof(X)) == 0 && L.sx % 8 == 0;
     return cudaLaunchKernelEx(&cfg.cfg, kernel, L, x, exps, w, scales, offsets, out, c, vec);

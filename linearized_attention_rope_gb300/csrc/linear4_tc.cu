@@ -31,13 +31,13 @@ constexpr uint32_t kOnes = 128;      // columns: two buffers of A (128 inputs in
 template <int N, int PARTS, bool OFFS>
 struct Shape {
     static constexpr int kAdd = N > 32 ? 8 : 4;  // adding warps
-    static constexpr int kPer = N > 32 ? 32 : N;  // tokens of an adding thread
+    static constexpr int kPer = 32;             // tokens of an adding thread
     // Sets of four unpacking warps, a buffer of A in turn.  64 tokens: one, for the registers that adding takes.
     static constexpr int kSets = N > 32 ? 1 : 2;
     static constexpr int kLoad = 4 * kSets, kIssue = kLoad + 1, kAdd0 = kLoad + 2;  // warps
     static constexpr int kWarps = kAdd0 + kAdd, kThreads = 32 * kWarps;
     static constexpr uint32_t kSums = OFFS ? 160 : 128;
-    static constexpr int kBufs = OFFS ? (N == 16 ? 3 : 2) : (N == 64 ? 2 : 4);  // of sums
+    static constexpr int kBufs = OFFS || N == 64 ? 2 : 4;  // of sums
     static constexpr uint32_t kCols = kSums + kBufs * N * (OFFS ? 2 : 1) > 256 ? 512 : 256;
     static constexpr int kW = kTile * 64, kX = N * 128;  // bytes of a stage's W, of 64 inputs of x
     static constexpr int kStage = kW + 2 * PARTS * kX;
@@ -337,7 +337,7 @@ cudaError_t run(const CUtensorMap& map_w, const CUtensorMap& map_x, const Linear
 template <typename T>
 cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat16* x, const uint8_t* w, const T* scales,
                               const T* offsets, T* out, cudaStream_t st) {
-    const int n = L.rows <= 16 ? 16 : L.rows <= 32 ? 32 : 64;
+    const int n = L.rows <= 32 ? 32 : 64;
     CUtensorMap map_w, map_x;
     if (!tma::make_map_2d(&map_w, w, 1, (uint64_t)L.n_in / 2, (uint64_t)L.n_out, (uint64_t)L.n_in / 2, 64, kTile) ||
         !tma::make_map_2d(&map_x, x, 2, (uint64_t)L.n_in, (uint64_t)L.rows * parts, (uint64_t)L.sx * 2, 64, (uint32_t)n))
@@ -351,7 +351,6 @@ cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat
         return parts == 3 ? go(nn, std::integral_constant<int, 3>(), offs) : go(nn, std::integral_constant<int, 1>(), offs);
     };
     auto with_rows = [&](auto offs) {
-        if (n == 16) return with_parts(std::integral_constant<int, 16>(), offs);
         if (n == 32) return with_parts(std::integral_constant<int, 32>(), offs);
         return with_parts(std::integral_constant<int, 64>(), offs);
     };
