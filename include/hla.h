@@ -638,7 +638,7 @@ HLA_API int hla_rms_norm_backward(const hla_norm_params* params, const void* s, 
  * of a head; n_channels a multiple of it).  dtype of x and out (and their
  * gradients), gate_dtype of g: F32 or BF16 each.  x_stride, g_stride: elements
  * from a token to the next (0: dense; otherwise at least n_channels, n_channels /
- * gate_dim).  out, dout and the gradients are dense. */
+ * gate_dim, and below 2^32).  out, dout and the gradients are dense. */
 typedef struct hla_recurrence_params {
     int n_channels;
     int gate_dim;

@@ -69,7 +69,7 @@ int check_recurrence(const hla_recurrence_params* p) {
     if (!is_type(p->dtype) || !is_type(p->gate_dtype)) return HLA_ERR_UNSUPPORTED;
     if (!stride_ok(p->x_stride, p->n_channels) || !stride_ok(p->g_stride, p->n_channels / p->gate_dim))
         return HLA_ERR_INVALID_ARG;
-    return HLA_OK;
+    return p->x_stride > UINT32_MAX || p->g_stride > UINT32_MAX ? HLA_ERR_UNSUPPORTED : HLA_OK;
 }
 
 RecDims rec_dims(const hla_recurrence_params* p, int n_seqs, int64_t total) {

@@ -56,8 +56,8 @@ __device__ __forceinline__ float2 mild(float2 g) {
     q = ffma2(q, g, splat(1.f));
     return mul2(g, q);
 }
-// exp(g) for |g| <= kBig, by the hardware's power of two: off by up to 2^-22 of itself, and 2^-22 ln 2 for g / ln 2, which is
-// rounded below 8.  Both together are below half a bit of what a row's sum is allowed (2^-21 of its magnitudes).
+// exp(g) for |g| <= kBig, by the hardware's power of two: off by up to 2^-22 of itself, and by 2^-22 ln 2 where g / ln 2 is
+// rounded (below 8), which with the row's own rounding is less than the 2^-21 of its magnitudes that a row may add.
 __device__ __forceinline__ float2 strong(float2 g) {
     const float2 t = mul2(g, splat(1.44269504f));
     float2 a;

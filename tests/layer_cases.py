@@ -61,9 +61,10 @@ def eight(y, tol, values, exps, group):
 
 def recurrence(g, x, lens, group, h0=None, dout=None, dh_last=None):
     """The rows one after another in float64, and the sizes of their errors in fp32: e = exp(g) - 1 is off by 4 U of
-    itself, a row adds two roundings (and a run's map as many), so that a row adds at most 8 U of the same recurrence
-    over magnitudes, and earlier errors pass on through the gates.  (Where e is used it is above -1/2, so that e h, which is
-    rounded, is no larger than exp(g) h.)"""
+    itself and takes two roundings of a row; exp(g), which a run with a gate below -ln 2 uses, is off by up to 7 U of itself
+    and takes one: a row adds at most 8 U of the same recurrence over magnitudes (a run's map, once for 8 rows or more, is
+    off by less than those rows may be), and earlier errors pass on through the gates.  (Where e is used it is above -1/2,
+    so that e h, which is rounded, is no larger than exp(g) h.)"""
     n, c = x.shape
     a = g.exp().repeat_interleave(group, 1) if group > 1 else g.exp()
     h, mag, err = (torch.zeros(n + 1, c, dtype=torch.float64) for _ in range(3))

@@ -105,6 +105,31 @@ def test_infinities_and_nan_stay_with_their_token():
         assert got[3].isnan().all() and not got[7].isfinite().any()
 
 
+@pytest.mark.parametrize("n,dtype", [(40, BF16), (61, F32), (129, BF16)])
+def test_many_rows_in_a_graph_and_on_two_streams(n, dtype):
+    prm = hla.Linear4Params(1088, 700, 64, dtype)
+    w, s, o = weights(prm, True)
+    xs = [rows(prm, n, seed)[0].cuda() for seed in (5, 8)]
+    w, s, o = w.cuda(), s.cuda(), o.cuda()
+    want = [hla.linear4(prm, x, w, s, offsets=o) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    for x, stream in zip(xs, streams):
+        stream.wait_stream(torch.cuda.current_stream())
+        got.append(hla.linear4(prm, x, w, s, offsets=o, stream=stream))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    x, ws = xs[0].clone(), hla.alloc_linear4_workspace(prm, n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = hla.linear4(prm, x, w, s, offsets=o, ws=ws)
+    for i in (0, 1):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i])
+
+
 def test_no_tokens():
     prm = hla.Linear4Params(128, 8)
     w, s, _ = weights(prm, False)

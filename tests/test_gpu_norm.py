@@ -124,6 +124,34 @@ def test_in_place(cols):
         assert torch.equal(got, dx) and torch.equal(gw, dw)
 
 
+# more rows than the blocks that stay take at three each: one, two and four pieces a thread
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,n", [(264, 1000), (2056, 1300), (4096, 1001), (8200, 960), (16384, 930)])
+@pytest.mark.parametrize("residual,group", [(True, -1), (False, -1), (True, 0), (True, 32)])
+def test_many_rows(dtype, cols, n, residual, group):
+    if group == 32 and cols % 32:
+        cols -= cols % 32
+    prm = hla.NormParams(cols, dtype=dtype, out_dtype=-1 if group < 0 else E4M3, group=max(group, 0))
+    x, r, w = inputs(prm, n)
+    s = x + r if residual else x
+    y, err = lc.norm(s.double(), w.double(), 1e-6, 0.0)
+    a, b = x.cuda(), r.cuda()
+    got = hla.rms_norm(prm, a, weight=w.cuda(), residual=b if residual else None)
+    if residual:
+        assert torch.equal(got.sum.cpu(), s)
+    if group >= 0:
+        assert lc.eight(y, err, got.out, got.exp, group) == (True, True, True)
+        return
+    lc.close(got.out, y, err)
+    wide = torch.zeros(n, cols + 64, dtype=TYPE[dtype], device="cuda")  # rows of a wider tensor, the same values
+    wide[:, 64:] = a
+    again = hla.rms_norm(prm, wide[:, 64:], weight=w.cuda(), residual=b if residual else None)
+    assert torch.equal(again.out, got.out)
+    if residual:  # the stream and the branch, both in place
+        hla.rms_norm(prm, a, weight=w.cuda(), residual=b, sum=b, out=a)
+        assert torch.equal(a, got.out) and torch.equal(b, got.sum)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("cols,heads,n", SIZES + [(128, 32, 600), (64, 1, 20011)])
 @pytest.mark.parametrize("dsum,weight,offset", [(True, True, 0.0), (False, True, 1.0), (True, False, 0.0)])

@@ -114,6 +114,15 @@ def test_recurrence_pointer_refusals(lib):
     assert step(n=-1) == INV and step(n=0, g=None) == hla.HLA_OK
 
 
+def test_recurrence_strides_past_32_bits(lib):
+    def call(xs, gs):
+        p = hla.RecurrenceParams(64).c(xs, gs)
+        return lib.hla_recurrence(ctypes.byref(p), FAKE, FAKE, None, FAKE, 0, 4, FAKE, None, None, FAKE, 1 << 30, None)
+
+    assert call(1 << 32, 0) == UNS and call(0, 1 << 33) == UNS
+    assert call((1 << 32) - 1, 0) == INV  # (no sequences)
+
+
 def test_recurrence_workspace_grows(lib):
     # the workspace of the largest call serves every smaller one
     for prm in (hla.RecurrenceParams(64), hla.RecurrenceParams(4096), hla.RecurrenceParams(8192, gate_dim=128),
