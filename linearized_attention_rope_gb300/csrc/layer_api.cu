@@ -141,7 +141,7 @@ HLA_API int hla_rms_norm_backward_workspace_bytes(const hla_norm_params* p, size
     const int rc = check_norm(p);
     if (rc) return rc;
     if (!bytes) return HLA_ERR_INVALID_ARG;
-    *bytes = (size_t)kNormParts * p->n_cols * sizeof(float);
+    *bytes = (size_t)norm_parts(p->n_cols) * p->n_cols * sizeof(float);
     return HLA_OK;
 }
 

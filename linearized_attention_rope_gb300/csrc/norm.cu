@@ -12,8 +12,13 @@
 // The gradient's blocks stay and walk the rows, so that a thread adds up dw of
 // its own columns in registers; the blocks' sums are added in order by a second
 // launch.  Rows come through a ring in shared memory, filled by bulk copies, in
-// the gradient and where the norm has more than three rows a block: loads go on
-// while a row is reduced, and neither pass holds the row in registers.
+// the gradient and where the norm of 16-bit rows has more than three rows a
+// block: loads go on while a row is reduced.
+// Measured: 32767 rows of 5120 bf16 with the residual 213 us, 94 % of the copy
+// rate (a block a row: 259); 4097 rows of 4096 fp32 42 us, 96 %; gradients: 524352
+// heads of 128 bf16 72 us (83 %), 4097 rows of 4096 fp32 with the stream's 48 us
+// (84 %), 32767 rows of 5120 bf16 302 us (66 %: two pieces a thread, whose sums of
+// dw and factors take the registers).
 #include <algorithm>
 
 #include "layer.cuh"
@@ -443,9 +448,11 @@ template <typename T, int V> __device__ __forceinline__ void pairs(const Piece<T
 }
 
 // The same from a ring of row buffers (s, dout and dsum), which both passes over a row read.  NARROW: a warp or less takes
-// a row, and a buffer holds `per` dense rows; else one.
-template <typename T, int P, bool NARROW>
-__global__ void __launch_bounds__(NARROW ? kNarrow : P == 1 ? 256 : 512, NARROW ? 6 : 2)
+// a row, and a buffer holds `per` dense rows; else one.  SMALL: a block of up to 128 threads, which keep their piece of the
+// row in registers between the passes (100000 rows of 512 bf16: 121 us, read again 149); larger blocks read it again and are
+// twice as many (65536 rows of 1024 fp32: 180 us, kept 231).
+template <typename T, int P, bool NARROW, bool SMALL>
+__global__ void __launch_bounds__(SMALL ? kNarrow : P == 1 ? 256 : 512, NARROW ? 6 : SMALL || P == 1 ? 4 : 2)
 norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ weight, const T* dout, const T* dsum, T* dx,
                           float* part, int tpr, int stages, int per) {
     constexpr int V = 16 / (int)sizeof(T);
@@ -473,7 +480,7 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
     start_ring(full, stages, &dead);
     if (threadIdx.x == 0)
         for (int i = 0; i < stages; ++i) load(blockIdx.x + (int64_t)i * gridDim.x, i);
-    constexpr bool kHold = P * V <= 8, kRow = P == 1;  // the factors, the row stay in registers between the passes
+    constexpr bool kHold = P * V <= 8, kRow = SMALL;  // the factors, the row stay in registers between the passes
     constexpr int H = V / 2;
     constexpr int K = kHold ? P : 1;
     float2 f[K][H], x[H], dy[H], acc[P][H];
@@ -638,13 +645,13 @@ RowShape row_shape(int pieces, bool single) {
     return pieces <= 4096 ? RowShape{threads(4), 4} : RowShape{0, 0};
 }
 
-// A ring's stages and blocks an SM for rows of `each` bytes in all: two blocks where those have two stages each.
+// A ring's stages and blocks an SM for rows of `each` bytes in all: `resident` threads' worth of blocks, of two stages at least.
 struct RingShape {
     int stages, blocks;
 };
 constexpr size_t kRingBytes = 204800;
-RingShape ring_shape(int threads, size_t each) {
-    const int blocks = threads <= 512 && 4 * each <= kRingBytes ? 2 : 1;
+RingShape ring_shape(int threads, size_t each, int resident) {
+    const int blocks = (int)std::max<size_t>(1, std::min<size_t>(resident / threads, kRingBytes / (2 * each)));
     return {(int)std::min<size_t>(kStages, kRingBytes / blocks / each), blocks};
 }
 
@@ -685,22 +692,22 @@ template <typename T, int V, int P>
 cudaError_t backward(const NormDims& N, const T* s, const T* weight, const T* dout, const T* dsum, T* dx, float* part,
                      int tpr, int n_sm, int* blocks, cudaStream_t st) {
     const int threads = tpr <= 32 ? kNarrow : tpr, groups = threads / tpr;
-    *blocks = (int)std::min<int64_t>({(N.rows + groups - 1) / groups, (int64_t)n_sm * (1024 / threads), kNormParts});
+    *blocks = (int)std::min<int64_t>({(N.rows + groups - 1) / groups, (int64_t)n_sm * (1024 / threads), norm_parts(N.cols)});
     const size_t sm = groups > 1 ? (size_t)groups * N.cols * sizeof(float) : 0;  // at most 128 threads x 8 values
     norm_backward_kernel<T, V, P><<<*blocks, threads, sm, st>>>(N, s, weight, dout, dsum, dx, part, tpr);
     return cudaGetLastError();
 }
 
-template <typename T, int P, bool NARROW>
+template <typename T, int P, bool NARROW, bool SMALL>
 cudaError_t backward_ring(const NormDims& N, const T* s, const T* weight, const T* dout, const T* dsum, T* dx, float* part,
                           int threads, int tpr, int stages, int resident, int per, int n_sm, int* blocks, cudaStream_t st) {
-    const auto kernel = norm_backward_ring_kernel<T, P, NARROW>;
+    const auto kernel = norm_backward_ring_kernel<T, P, NARROW, SMALL>;
     static DeviceCache cache;
     cudaError_t e = device_cached(cache, nullptr, [&](int, int*) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
     });
     if (e != cudaSuccess) return e;
-    *blocks = (int)std::min<int64_t>({(N.rows + per - 1) / per, (int64_t)n_sm * resident, kNormParts});
+    *blocks = (int)std::min<int64_t>({(N.rows + per - 1) / per, (int64_t)n_sm * resident, norm_parts(N.cols)});
     size_t sm = (size_t)stages * per * N.cols * sizeof(T) * (dsum ? 3 : 2);
     if (NARROW) sm = std::max(sm, (size_t)(threads / tpr) * N.cols * sizeof(float));
     kernel<<<*blocks, threads, sm, st>>>(N, s, weight, dout, dsum, dx, part, tpr, stages, per);
@@ -733,14 +740,15 @@ cudaError_t launch_norm(const NormDims& N, const T* x, const T* residual, const 
         else norm_long_kernel<T, false><<<(unsigned)N.rows, 1024, 0, st>>>(N, x, residual, weight, out, out8, exps, sum);
         return cudaGetLastError();
     }
-    if (vec && r.tpr > 32) {
+    if constexpr (sizeof(T) == 2) if (vec && r.tpr > 32) {
         static DeviceCache cache;
         int n_sm = 0;
         const cudaError_t e = device_cached(cache, &n_sm, [](int dev, int* v) { return sm_count(dev, v); });
         if (e != cudaSuccess) return e;
         const int p = N.cols / V <= 256 ? 1 : N.cols / V <= 1024 ? 2 : 4, threads = (N.cols / V + 32 * p - 1) / (32 * p) * 32;
-        const RingShape ring = ring_shape(threads, (size_t)N.cols * sizeof(T) * (residual ? 2 : 1));
-        // (up to three rows a block: a block a row starts sooner)
+        const RingShape ring = ring_shape(threads, (size_t)N.cols * sizeof(T) * (residual ? 2 : 1), 1024);
+        // Up to three rows a block a block a row starts sooner (640 rows of 4096: 8.4 and 8.4 us, 7680: 44 with the ring, 52
+        // without); rows of fp32 go through registers as fast (65536 of 1024: 156 us, 169 with the ring).
         if (threads <= 512 && ring.stages >= 2 && N.rows > (int64_t)3 * n_sm * ring.blocks) {
             auto go = [&](auto pp) {
                 return forward_ring<T, decltype(pp)::value>(N, x, residual, weight, out, out8, exps, sum, threads, ring, n_sm, st);
@@ -785,18 +793,19 @@ cudaError_t launch_norm_backward(const NormDims& N, const T* s, const T* weight,
             const int groups = kNarrow / r.tpr, per = std::max<int>(groups, (int)(8192 / row_bytes) / groups * groups);
             const int stages = 2;
             const int resident = (int)std::min<size_t>(6, kRingBytes / (stages * per * row_bytes * n_in + 1024));
-            return finish(backward_ring<T, 1, true>(N, s, weight, dout, dsum, dx, part, kNarrow, r.tpr, stages, resident, per, n_sm,
+            return finish(backward_ring<T, 1, true, true>(N, s, weight, dout, dsum, dx, part, kNarrow, r.tpr, stages, resident, per, n_sm,
                                                     &blocks, st));
         }
         if (vec && r.tpr > 32) {
             const int p = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 4, threads = (pieces + 32 * p - 1) / (32 * p) * 32;
-            const RingShape ring = ring_shape(threads, row_bytes * n_in);
+            const RingShape ring = ring_shape(threads, row_bytes * n_in, threads <= kNarrow ? 512 : 1024);
             if (threads <= 512 && ring.stages >= 2) {
-                auto go = [&](auto pp) {
-                    return backward_ring<T, decltype(pp)::value, false>(N, s, weight, dout, dsum, dx, part, threads, threads, ring.stages,
+                auto go = [&](auto pp, auto small) {
+                    return backward_ring<T, decltype(pp)::value, false, decltype(small)::value>(N, s, weight, dout, dsum, dx, part, threads, threads, ring.stages,
                                                                         ring.blocks, 1, n_sm, &blocks, st);
                 };
-                return finish(p == 1 ? go(One()) : p == 2 ? go(Two()) : go(Four()));
+                return finish(p == 1 ? (threads <= kNarrow ? go(One(), std::true_type()) : go(One(), std::false_type()))
+                              : p == 2 ? go(Two(), std::false_type()) : go(Four(), std::false_type()));
             }
         }
         if (r.tpr == 0) {
