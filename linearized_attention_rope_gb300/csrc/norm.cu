@@ -452,7 +452,7 @@ template <typename T, int V> __device__ __forceinline__ void pairs(const Piece<T
 // row in registers between the passes (100000 rows of 512 bf16: 121 us, read again 149); larger blocks read it again and are
 // twice as many (65536 rows of 1024 fp32: 180 us, kept 231).
 template <typename T, int P, bool NARROW, bool SMALL>
-__global__ void __launch_bounds__(SMALL ? kNarrow : P == 1 ? 256 : 512, NARROW ? 6 : SMALL || P == 1 ? 4 : 2)
+__global__ void __launch_bounds__(SMALL ? kNarrow : P == 1 ? 256 : 1024, NARROW ? 6 : SMALL || P == 1 ? 4 : 1)
 norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ weight, const T* dout, const T* dsum, T* dx,
                           float* part, int tpr, int stages, int per) {
     constexpr int V = 16 / (int)sizeof(T);
@@ -797,15 +797,15 @@ cudaError_t launch_norm_backward(const NormDims& N, const T* s, const T* weight,
                                                     &blocks, st));
         }
         if (vec && r.tpr > 32) {
-            const int p = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 4, threads = (pieces + 32 * p - 1) / (32 * p) * 32;
+            const int p = pieces <= 256 ? 1 : 2, threads = (pieces + 32 * p - 1) / (32 * p) * 32;
             const RingShape ring = ring_shape(threads, row_bytes * n_in, threads <= kNarrow ? 512 : 1024);
-            if (threads <= 512 && ring.stages >= 2) {
+            if (threads <= 1024 && ring.stages >= 2) {
                 auto go = [&](auto pp, auto small) {
                     return backward_ring<T, decltype(pp)::value, false, decltype(small)::value>(N, s, weight, dout, dsum, dx, part, threads, threads, ring.stages,
                                                                         ring.blocks, 1, n_sm, &blocks, st);
                 };
                 return finish(p == 1 ? (threads <= kNarrow ? go(One(), std::true_type()) : go(One(), std::false_type()))
-                              : p == 2 ? go(Two(), std::false_type()) : go(Four(), std::false_type()));
+                              : go(Two(), std::false_type()));
             }
         }
         if (r.tpr == 0) {
