@@ -253,7 +253,7 @@ norm_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict
 // Many rows of a block each: blocks stay, and the rows to come are on their way into a ring in shared memory (x, then the
 // residual), so that loads do not stop while a row is reduced.
 template <typename T, int V, int P, bool E4M3>
-__global__ void __launch_bounds__(512, 2)
+__global__ void __launch_bounds__(P == 1 ? 256 : 1024, P == 1 ? 4 : 1)
 norm_ring_kernel(const NormDims N, const T* x, const T* residual, const T* __restrict__ weight, T* out, uint8_t* out8,
                  uint8_t* exps, T* sum, int stages) {
     using Pc = Piece<T, V>;
@@ -745,15 +745,15 @@ cudaError_t launch_norm(const NormDims& N, const T* x, const T* residual, const 
         int n_sm = 0;
         const cudaError_t e = device_cached(cache, &n_sm, [](int dev, int* v) { return sm_count(dev, v); });
         if (e != cudaSuccess) return e;
-        const int p = N.cols / V <= 256 ? 1 : N.cols / V <= 1024 ? 2 : 4, threads = (N.cols / V + 32 * p - 1) / (32 * p) * 32;
+        const int p = N.cols / V <= 256 ? 1 : 2, threads = (N.cols / V + 32 * p - 1) / (32 * p) * 32;
         const RingShape ring = ring_shape(threads, (size_t)N.cols * sizeof(T) * (residual ? 2 : 1), 1024);
         // Up to three rows a block a block a row starts sooner (640 rows of 4096: 8.4 and 8.4 us, 7680: 44 with the ring, 52
         // without); rows of fp32 go through registers as fast (65536 of 1024: 156 us, 169 with the ring).
-        if (threads <= 512 && ring.stages >= 2 && N.rows > (int64_t)3 * n_sm * ring.blocks) {
+        if (threads <= 1024 && ring.stages >= 2 && N.rows > (int64_t)3 * n_sm * ring.blocks) {
             auto go = [&](auto pp) {
                 return forward_ring<T, decltype(pp)::value>(N, x, residual, weight, out, out8, exps, sum, threads, ring, n_sm, st);
             };
-            return p == 1 ? go(One()) : p == 2 ? go(std::integral_constant<int, 2>()) : go(std::integral_constant<int, 4>());
+            return p == 1 ? go(One()) : go(std::integral_constant<int, 2>());
         }
     }
     if (!vec) return r.p == 1 ? run(One(), One()) : r.p == 4 ? run(One(), std::integral_constant<int, 4>()) : run(One(), std::integral_constant<int, 16>());
