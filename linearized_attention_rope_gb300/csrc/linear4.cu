@@ -12,6 +12,11 @@
 // bf16 parts, cut off 8 bits at a time (nothing is lost), 8-bit rows as bf16 (exact, too).  Offsets are multiplied by the
 // group's sum of x, formed on that way.  Weights are two steps (of 128 inputs) ahead of the products.  The cluster's
 // sums are added through distributed shared memory, in order of its blocks.
+//
+// Measured: 16 8-bit rows through 8192 x 28672 with offsets 63 us (1.9 TB/s; 69 on tcgen05, whose 128-row tiles are read
+// back for 16 tokens), one row through 4096 x 4096 8 us.  A pair of weights takes a shift, a merge and a difference, the first
+// two at half rate: the ALU pipe is busy half of the time, the load/store pipe as much, and neither 32 rows a warp (64), sixteen
+// warps a block (63 to 67) nor more weights under way changed that.
 #include <algorithm>
 
 #include "layer.cuh"

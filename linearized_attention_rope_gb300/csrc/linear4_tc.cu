@@ -12,8 +12,9 @@
 //   four (eight) warps read a group's sums (32 tokens a thread at most), scale and add them up.
 // The cluster's sums are added through distributed shared memory, in order of its blocks.
 //
-// Bound by what an SM issues per 64 inputs of 128 rows: about 130
-// instructions of each unpacking warp and 60 of each adding warp.
+// Bound by the chain of waits of a tile of 128 inputs, about 1600 cycles with unpacking, products and adding in step: 61 rows
+// through 5120 x 10240 35 us, of which the 20 tiles of a block take 17 and the cluster's sums 4 (blocks that share an SM 27).
+// Buffers of 64 inputs 39 us; one wait for all loads of a group's sums 44.
 #include <algorithm>
 
 #include "layer.cuh"

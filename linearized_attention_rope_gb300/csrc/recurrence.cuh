@@ -13,12 +13,13 @@
 // state in front of them.
 //
 // The state in front of a tile: every tile publishes (A, B) and, once it knows
-// it, the state behind it.  A tile looks at the eight tiles before it, then at up to
-// 32 (four channels a lane: 16); the nearest with a state is carried forward by the (A, B) of those between, tile
-// after tile.  That is what each of those tiles does itself, rounding for
-// rounding, so that results do not depend on which of them was found.  Tiles
-// are handed out in order of time, so that those waited for are running.  Every
-// word carries its own flag: no fences, and one trip through L2 per look.
+// it, the state behind it.  A tile looks at the eight tiles before it, then at
+// up to 32 (four channels a lane: 16); the nearest with a state is carried
+// forward by the (A, B) of those between, tile after tile.  That is what each of
+// those tiles does itself, rounding for rounding, so that results do not depend
+// on which of them was found.  Tiles are handed out in order of time, so that
+// those waited for are running.  Every word carries its own flag: no fences, and
+// one trip through L2 per look.
 //
 // Gates of a run and channel enter as v = exp(g) - 1, with the state added (w =
 // 1), where all of them are within [-ln 2, 0]: a state that decays slowly (|g| of
@@ -26,8 +27,9 @@
 // be off by up to 2^-25 in every row, the same way for the same gate.  Otherwise
 // as v = exp(g) (w = 0), so that a closed gate leaves nothing of the state, not
 // even a rounding.  Either way a row is w h + (v h + x): two packed FMAs for two
-// channels.  Instructions are what this kernel has few of: at the copy rate an SM
-// has about 35 for 32 values of a row.
+// channels.  Instructions are what these kernels have few of: a row of 64 channels
+// takes 34 in the forward pass, a warp's run another 800, and at the copy rate an
+// SM has about 55 for a row of bf16 values and gates.
 //
 // The gradient runs the tiles from the last to the first.  States in front of
 // its rows come from those that the forward pass kept every 64 rows.
@@ -440,7 +442,8 @@ struct Gates {
 struct Tiles {
     int cpl, rows, n_slabs, n_time;
 };
-// Runs of `most` rows where that makes two tiles for every SM (152), else of 8 rows, so that small calls spread.
+// Runs of `most` rows where that makes two tiles for every SM (152), else of 8 rows, so that small calls spread (us, forward and
+// gradient, 1024 channels: 640 rows 8.5 and 9.0 in runs of 8, 9.1 and 10.5 in runs of 16; 2432 rows 14.2 and 16.3, 12.7 and 13.7).
 inline Tiles tiles(const RecDims& R, int most) {
     Tiles t;
     t.cpl = R.gate_dim == 128 ? 4 : 2;
