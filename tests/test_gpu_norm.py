@@ -153,6 +153,23 @@ def test_many_rows(dtype, cols, n, residual, group):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,heads,n", [(512, 3, 1100), (1024, 2, 700), (128, 5, 900)])
+def test_many_heads_of_a_wider_tensor(dtype, cols, heads, n):
+    prm = hla.NormParams(cols, n_heads=heads, dtype=dtype)
+    x, _, w = inputs(prm, n)
+    dout = lc.randn(7, *shape(prm, n), dtype=TYPE[dtype])
+    wide = torch.zeros(n, (heads + 2) * cols, dtype=TYPE[dtype], device="cuda")
+    wide[:, cols:-cols] = x.reshape(n, -1).cuda()
+    part = wide[:, cols:-cols].view(n, heads, cols)
+    y, err = lc.norm(x.double(), w.double(), 1e-6, 0.0)
+    lc.close(hla.rms_norm(prm, part, weight=w.cuda()).out, y, err)
+    dx, dw = hla.rms_norm_backward(prm, part, dout.cuda(), weight=w.cuda())
+    ref = lc.norm_grad(x.double(), w.double(), dout.double(), None, 1e-6, 0.0)
+    lc.close(dx, ref[0], ref[1])
+    lc.close(dw, ref[2], ref[3])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("cols,heads,n", SIZES + [(128, 32, 600), (64, 1, 20011)])
 @pytest.mark.parametrize("dsum,weight,offset", [(True, True, 0.0), (False, True, 1.0), (True, False, 0.0)])
 def test_norm_gradient_matches_64_bit(dtype, cols, heads, n, dsum, weight, offset):
