@@ -618,8 +618,8 @@ typedef struct hla_norm_params {
 HLA_API int hla_rms_norm(const hla_norm_params* params, const void* x, const void* residual, const void* weight,
                          int64_t tokens, void* out, uint8_t* exp, void* sum, void* stream);
 
-/* Workspace bytes of hla_rms_norm_backward with a weight (no error word; it
- * grows with n_cols alone). */
+/* Workspace bytes of hla_rms_norm_backward with a weight (no error word; they
+ * depend on n_cols alone). */
 HLA_API int hla_rms_norm_backward_workspace_bytes(const hla_norm_params* params, size_t* bytes);
 
 /* Gradients of sum(dout . out) (+ sum(dsum . sum), dsum may be NULL) with respect
