@@ -28,7 +28,12 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 
-template <typename T, int V> struct alignas(V * sizeof(T)) Piece { T x[V]; };
+// V values in a row, loaded and stored at once.  At most 16 bytes: callers' rows are checked for 16 bytes and no more, and a
+// wider type promises the compiler an alignment for which it may choose a wider access.
+template <typename T, int V> struct alignas(V * sizeof(T)) Piece {
+    static_assert(V * sizeof(T) <= 16, "a piece is one access of up to 16 bytes");
+    T x[V];
+};
 
 // Groups of values as 8-bit floats (e4m3) times a power of two, as the cache
 // keeps its rows: the smallest e >= -127 with top <= 448 2^e (top finite, >= 0).

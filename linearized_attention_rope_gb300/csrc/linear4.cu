@@ -130,23 +130,25 @@ linear4_kernel(const Linear4Dims L, const X* __restrict__ x, const uint8_t* __re
             float2 v[4] = {};  // inputs 2i, 2i + 1
             if (row < L.rows && k < L.n_in) {
                 const X* p = x + row * L.sx + k;
-                Piece<X, 8> y;
+                constexpr int kAt = sizeof(X) == 4 ? 4 : 8;  // values of a load: fp32 rows lie on 16 bytes, not on 32
+                Piece<X, kAt> y[8 / kAt];
                 if (vec) {
-                    y = *reinterpret_cast<const Piece<X, 8>*>(p);
+#pragma unroll
+                    for (int i = 0; i < 8 / kAt; ++i) y[i] = reinterpret_cast<const Piece<X, kAt>*>(p)[i];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y.x[i] = p[i];
+                    for (int i = 0; i < 8; ++i) y[i / kAt].x[i % kAt] = p[i];
                 }
                 if constexpr (sizeof(X) == 1) {
                     const float f = group_pow2((int)exps[row * x_groups + (L.x_group ? k >> x_shift : 0)] - 127);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(reinterpret_cast<const __nv_fp8x2_storage_t*>(y.x)[i], __NV_E4M3);
+                        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(reinterpret_cast<const __nv_fp8x2_storage_t*>(y[0].x)[i], __NV_E4M3);
                         v[i] = mul2(__half22float2(__half2(h)), make_float2(f, f));
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = make_float2(to_f32(y.x[2 * i]), to_f32(y.x[2 * i + 1]));
+                    for (int i = 0; i < 4; ++i) v[i] = make_float2(to_f32(y[2 * i / kAt].x[2 * i % kAt]), to_f32(y[2 * i / kAt].x[2 * i % kAt + 1]));
                 }
             }
             constexpr int kIn = GROUP / 8;  // pieces of a group
@@ -358,7 +360,7 @@ cudaError_t run(const Linear4Dims& L, const X* x, const uint8_t* exps, const uin
     // (three blocks an SM; one row through 4096 x 4096: 8.2 us, 9.3 where one block and two steps are counted)
     const int tiles = (L.n_out + S::kRows - 1) / S::kRows, c = linear4_split(tiles, (L.n_in + 127) / 128, 456, 4);
     ClusterCfg cfg(dim3((unsigned)(tiles * c), (unsigned)((L.rows + S::kTok - 1) / S::kTok)), kThreads4, S::kSmem, st, c);
-    const bool vec = (uintptr_t)x % (8 * sizeof(X) > 16 ? 16 : 8 * sizeof(X)) == 0 && L.sx % 8 == 0;
+    const bool vec = (uintptr_t)x % std::min<size_t>(16, 8 * sizeof(X)) == 0 && L.sx % 8 == 0;
     return cudaLaunchKernelEx(&cfg.cfg, kernel, L, x, exps, w, scales, offsets, out, c, vec);
 }
 

@@ -91,6 +91,21 @@ def test_strided_and_unaligned_rows():
     lc.close(got, *lc.linear4(odd[:, :256].double(), w, s, None, 128, 1))
 
 
+@pytest.mark.parametrize("n", [1, 9, 20])
+@pytest.mark.parametrize("lo", [0, 1, 4, 8])
+@pytest.mark.parametrize("offsets", [False, True])
+def test_fp32_rows_of_a_wider_tensor(n, lo, offsets):
+    # rows that start on 32, on 4 and on 16 bytes, a multiple of 32 bytes apart: no access may be wider than what they start on
+    prm = hla.Linear4Params(384, 48, 64, F32)
+    w, s, o = weights(prm, offsets)
+    wide = lc.randn(3, n, 400, dtype=torch.float32)
+    x, dev = wide[:, lo:lo + 384], wide.cuda()[:, lo:lo + 384]
+    assert dev.data_ptr() % 32 == 4 * lo % 32
+    got = hla.linear4(prm, dev, w.cuda(), s.cuda(), offsets=None if o is None else o.cuda())
+    lc.close(got, *lc.linear4(x.double(), w, s, o, 64, 3))
+    assert torch.equal(got, call(prm, x.contiguous(), None, w, s, o))
+
+
 def test_infinities_and_nan_stay_with_their_token():
     for dtype in (BF16, F32):
         prm = hla.Linear4Params(256, 40, dtype=dtype)
