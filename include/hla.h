@@ -668,8 +668,10 @@ HLA_API int hla_recurrence_workspace_bytes(const hla_recurrence_params* params, 
  * infinite, and no others (of a gate that channels share: of those channels).
  * Rows at and past c_n are left as they were.  A malformed table is clamped on
  * the device and flagged in the workspace's error word; rows whose place it
- * leaves open are undefined.  Outputs must not overlap inputs otherwise.
- * Asynchronous; deterministic. */
+ * leaves open are undefined.  A wait for earlier rows that runs out is flagged
+ * there too and leaves NaN in the rows and states behind them (and in
+ * hla_recurrence_backward's gradients of the rows in front).  Outputs must not
+ * overlap inputs otherwise.  Asynchronous; deterministic. */
 HLA_API int hla_recurrence(const hla_recurrence_params* params, const void* g, const void* x, const float* h0,
                            const int32_t* cu_seqlens, int n_seqs, int64_t total_tokens, void* out, float* h_last,
                            float* states, void* ws, size_t ws_bytes, void* stream);

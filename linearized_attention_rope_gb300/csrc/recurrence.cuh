@@ -262,8 +262,9 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
     }
     if (m < 0) {
         if (threadIdx.x == 0) atomicExch(err, kErrTimeout);
+        // NaN, so that what depends on the state is not taken for an answer where nobody reads the error word
 #pragma unroll
-        for (int p = 0; p < NP; ++p) c[p] = splat(0.f);
+        for (int p = 0; p < NP; ++p) c[p] = splat(__int_as_float(0x7fc00000));
         return;
     }
 #pragma unroll
