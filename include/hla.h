@@ -666,6 +666,7 @@ HLA_API int hla_recurrence_workspace_bytes(const hla_recurrence_params* params, 
  *                      state in front of every 64th row; may be NULL
  * An infinity or NaN makes later rows of its own channel and sequence NaN or
  * infinite, and no others (of a gate that channels share: of those channels).
+ * A gate whose exponential passes fp32's range (g above 88.7) is an infinity.
  * Rows at and past c_n are left as they were.  A malformed table is clamped on
  * the device and flagged in the workspace's error word; rows whose place it
  * leaves open are undefined.  A wait for earlier rows that runs out is flagged

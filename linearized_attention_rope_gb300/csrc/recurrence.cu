@@ -16,6 +16,7 @@ recurrence_kernel(const RecDims R, const G* __restrict__ g, const T* __restrict_
                   const Carry S, int n_time, int n_slabs, int32_t* err) {
     constexpr int NP = CPL / 2;
     __shared__ Runs<NP> runs;
+    __shared__ Sums<NP> sums;
     const int tile = take_tile(S.ticket, n_time), k = tile / n_slabs, slab = tile - k * n_slabs;
     const int warp = threadIdx.x >> 5;
     const int64_t t0 = ((int64_t)k * kWarps + warp) * ROWS;
@@ -66,14 +67,15 @@ recurrence_kernel(const RecDims R, const G* __restrict__ g, const T* __restrict_
             for (int p = 0; p < NP; ++p) B[p] = through(e.at(i, p), e.keep(p), B[p], two(xs[i], p));
         }
     }
-    float2 A[NP];
+    float2 A[NP], total[NP];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) A[p] = e.product(p);
+    for (int p = 0; p < NP; ++p) sums[warp][p][threadIdx.x & 31] = total[p] = e.total(p);
+    const bool root = factors<NP>(total, A);
     runs.put(warp, A, B, rows.first != 0);
-    __syncthreads();
+    const bool roots = __syncthreads_or(root);
     float2 h[NP];
-    tile_carry<NP>(S, runs, k, n_time, n_slabs, slab, h, err);
-    for (int w = 0; w < warp; ++w) runs.pass(w, h);
+    tile_carry<NP>(S, runs, sums, roots, k, n_time, n_slabs, slab, h, err);
+    runs.pass(0, warp, roots, h);
     if (states && t0 % kStateRows == 0 && t0 < R.total) at.store(states + t0 / kStateRows * R.channels, h);
     T* o = out + t0 * R.channels;
     const uint32_t so = (uint32_t)R.channels;

@@ -73,6 +73,36 @@ __device__ __forceinline__ float2 through(float2 v, float2 w, float2 h, float2 x
 // exp(g) h
 __device__ __forceinline__ float2 times(float2 v, float2 w, float2 h) { return ffma2(w, h, mul2(v, h)); }
 
+// The factor exp(s) of a run or tile whose gates add up to s: itself up to exp(+-80), else minus its square root, which is a
+// normal number as far as a state that it is applied to can stay one (at most exp(88): a normal state that grows by more than
+// exp(176) passes fp32's range).  So that 0 stays 0 and what shrinks or grows by more than fp32 holds comes out as row by row.
+// The paths for roots cost the others 2 to 3 % (registers): 131071 rows of 1024 bf16 channels 250 us, 244 without them.
+constexpr float kFactor = 80.f;
+__device__ __forceinline__ float factor(float s) {
+    const bool in = fabsf(s) <= kFactor;
+    const float e = expf(in ? s : 0.5f * s > 88.f ? 88.f : 0.5f * s);
+    return in || e == 0.f ? e : -e;
+}
+__device__ __forceinline__ bool is_root(float2 a) { return a.x < 0.f || a.y < 0.f; }
+// Factors of a warp's sums; whether some lane's is a root (or 0, or NaN).
+template <int NP> __device__ __forceinline__ bool factors(const float2 (&s)[NP], float2 (&a)[NP]) {
+    bool in = true;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        in = in && fabsf(s[p].x) <= kFactor && fabsf(s[p].y) <= kFactor;
+        a[p] = make_float2(expf(s[p].x), expf(s[p].y));
+    }
+    if (__all_sync(kFull, in)) return false;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) a[p] = make_float2(factor(s[p].x), factor(s[p].y));
+    return true;
+}
+// a c + b for a of those factors
+__device__ __forceinline__ float2 apply(float2 a, float2 c, float2 b) {
+    const float2 f = make_float2(a.x < 0.f ? -a.x : 1.f, a.y < 0.f ? -a.y : 1.f);
+    return ffma2(make_float2(fabsf(a.x), fabsf(a.y)), mul2(f, c), b);
+}
+
 // Two values, each in a word with its own flag (0 where it has not been written).
 __device__ __forceinline__ void put_words(uint64_t* p, float2 v) {
     asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"((uint64_t)1 << 32 | __float_as_uint(v.x)),
@@ -200,16 +230,17 @@ template <int NP>
 __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, int slab, float2 (&c)[NP], int32_t* err) {
     constexpr int kDeep = 4 / NP, kLook = kDeep * kWarps;  // a warp looks at the tile 1 + warp before this one, 9 + warp ...
     __shared__ float2 pa[kLook][NP][32], pb[kLook][NP][32];
-    __shared__ int status[kLook];  // 0 nothing yet, 1 (A, B), 2 the state, 3 given up
+    __shared__ int status[kLook];  // 0 nothing yet, 1 (A, B), 2 the state, 3 given up; 5 (A, B) with a root
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int polls = 0, m, deep = 1;
+    bool roots;
     for (int i = threadIdx.x; i < kLook; i += kThreads) status[i] = 0;
     __syncthreads();
     for (;;) {
         for (int d = 0; d < deep; ++d) {
             const int i = d * kWarps + warp, pred = k - 1 - i;
             const int had = status[i];  // (written by this warp alone)
-            if (had >= 2) continue;
+            if ((had & 3) >= 2) continue;
             int have = had;
             if (pred < 0) {
 #pragma unroll
@@ -219,13 +250,14 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
                 const int64_t at = (((int64_t)pred * n_slabs + slab) * 32 + lane) * 2 * NP;
                 do {
                     float2 s[NP], a[NP], b[NP];
-                    bool is = true, has = true;
+                    bool is = true, has = true, root = false;
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
                         is &= get_words(S.state + at + 2 * p, &s[p]);
                         if (!have) {
                             has &= get_words(S.map + 2 * at + 4 * p, &a[p]);
                             has &= get_words(S.map + 2 * at + 4 * p + 2, &b[p]);
+                            root |= is_root(a[p]);
                         }
                     }
                     if (__all_sync(kFull, is)) {
@@ -238,9 +270,9 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
                             pa[i][p][lane] = a[p];
                             pb[i][p][lane] = b[p];
                         }
-                        have = 1;
+                        have = __any_sync(kFull, root) ? 5 : 1;
                     }
-                    if (have < 2 && ++polls > kPolls) have = 3;
+                    if ((have & 3) < 2 && ++polls > kPolls) have = 3;
                 } while (!have);
             }
             __syncwarp();
@@ -249,6 +281,7 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
         __syncthreads();
         const int got = status[lane % kLook];
         const unsigned ready = __ballot_sync(kFull, got == 2);
+        roots = __any_sync(kFull, got == 5);
         if (__any_sync(kFull, got == 3)) {
             m = -1;
             break;
@@ -269,6 +302,13 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
     }
 #pragma unroll
     for (int p = 0; p < NP; ++p) c[p] = pb[m][p][lane];
+    if (roots) {
+#pragma unroll 1
+        for (int w = m - 1; w >= 0; --w)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) c[p] = apply(pa[w][p][lane], c[p], pb[w][p][lane]);
+        return;
+    }
 #pragma unroll 4
     for (int w = m - 1; w >= 0; --w)
 #pragma unroll
@@ -289,21 +329,36 @@ struct Runs {
         }
         if (lane == 0) cut[w] = is_cut;
     }
-    __device__ __forceinline__ void pass(int w, float2 (&c)[NP]) const {
+    // from run w0 to run w1; roots: some A of the tile is one
+    __device__ __forceinline__ void pass(int w0, int w1, bool roots, float2 (&c)[NP]) const {
         const int lane = threadIdx.x & 31;
-        const bool is = cut[w];
+        if (roots) {
+#pragma unroll 1
+            for (int w = w0; w < w1; ++w)
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const float2 y = b[w][p][lane], z = ffma2(a[w][p][lane], c[p], y);
-            c[p] = is ? y : z;
+                for (int p = 0; p < NP; ++p) {
+                    const float2 y = b[w][p][lane];
+                    c[p] = cut[w] ? y : apply(a[w][p][lane], c[p], y);
+                }
+            return;
+        }
+        for (int w = w0; w < w1; ++w) {
+            const bool is = cut[w];
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const float2 y = b[w][p][lane], z = ffma2(a[w][p][lane], c[p], y);
+                c[p] = is ? y : z;
+            }
         }
     }
 };
+// The sums of the runs' gates, of which a tile's A is formed.
+template <int NP> using Sums = float2[kWarps][NP][32];
 
 // Publishes tile k's map (or state, where a run of it is cut), takes the state in front of it, publishes the one behind.
 template <int NP>
-__device__ __forceinline__ void tile_carry(const Carry& S, const Runs<NP>& runs, int k, int n_time, int n_slabs, int slab,
-                                           float2 (&c)[NP], int32_t* err) {
+__device__ __forceinline__ void tile_carry(const Carry& S, const Runs<NP>& runs, const Sums<NP>& sums, bool roots, int k,
+                                           int n_time, int n_slabs, int slab, float2 (&c)[NP], int32_t* err) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int p = 0; p < NP; ++p) c[p] = splat(0.f);
@@ -312,17 +367,18 @@ __device__ __forceinline__ void tile_carry(const Carry& S, const Runs<NP>& runs,
     bool cut = false;
     const int64_t at = (((int64_t)k * n_slabs + slab) * 32 + lane) * 2 * NP;
     if (threadIdx.x < 32 && k + 1 < n_time) {
+        float2 total[NP];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            A[p] = splat(1.f);
-            B[p] = splat(0.f);
+            total[p] = B[p] = splat(0.f);
         }
+        runs.pass(0, kWarps, roots, B);
         for (int w = 0; w < kWarps; ++w) {
-            runs.pass(w, B);
             cut |= runs.cut[w] != 0;
 #pragma unroll
-            for (int p = 0; p < NP; ++p) A[p] = mul2(A[p], runs.a[w][p][lane]);
+            for (int p = 0; p < NP; ++p) total[p] = add2(total[p], sums[w][p][lane]);
         }
+        factors<NP>(total, A);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             if (cut) {
@@ -336,7 +392,7 @@ __device__ __forceinline__ void tile_carry(const Carry& S, const Runs<NP>& runs,
     look_back<NP>(S, k, n_slabs, slab, c, err);
     if (threadIdx.x < 32 && k + 1 < n_time && !cut)
 #pragma unroll
-        for (int p = 0; p < NP; ++p) put_words(S.state + at + 2 * p, ffma2(A[p], c[p], B[p]));
+        for (int p = 0; p < NP; ++p) put_words(S.state + at + 2 * p, apply(A[p], c[p], B[p]));
 }
 
 // A warp's gates as (v, w): v per row and pair of channels, or (SHARED) row i's in lane i; w per pair.
@@ -434,10 +490,7 @@ struct Gates {
         else return v[i][p];
     }
     __device__ __forceinline__ float2 keep(int p) const { return w[SHARED ? 0 : p]; }
-    __device__ __forceinline__ float2 product(int p) const {  // of the run's gates
-        const float2 s = sum[SHARED ? 0 : p];
-        return make_float2(expf(s.x), expf(s.y));
-    }
+    __device__ __forceinline__ float2 total(int p) const { return sum[SHARED ? 0 : p]; }
 };
 
 struct Tiles {

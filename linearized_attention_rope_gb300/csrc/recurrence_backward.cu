@@ -35,6 +35,7 @@ recurrence_backward_kernel(const RecDims R, const G* __restrict__ g, const T* __
                            const float* dh_last, G* __restrict__ dg, T* __restrict__ dx, float* dh0, const Carry S,
                            int n_time, int n_slabs, int32_t* err) {
     constexpr int NP = CPL / 2;
+    __shared__ Sums<NP> sums;
     __shared__ Runs<NP> ahead, back;  // forward in time; backward, in the order in which tiles are handed out
     const int tile = take_tile(S.ticket, n_time), k = tile / n_slabs, slab = tile - k * n_slabs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -115,13 +116,14 @@ recurrence_backward_kernel(const RecDims R, const G* __restrict__ g, const T* __
             for (int p = 0; p < NP; ++p) M[p] = times(e.at(i, p), e.keep(p), add2(two(ds[i], p), M[p]));
         }
     }
-    float2 A[NP];
+    float2 A[NP], total[NP];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) A[p] = e.product(p);
+    for (int p = 0; p < NP; ++p) sums[kWarps - 1 - warp][p][threadIdx.x & 31] = total[p] = e.total(p);
+    const bool root = factors<NP>(total, A);
     ahead.put(warp, A, B, rows.first != 0);
     back.put(kWarps - 1 - warp, A, M, rows.last != 0);
-    __syncthreads();
-    for (int w = warp / kPer * kPer; w < warp; ++w) ahead.pass(w, h);
+    const bool roots = __syncthreads_or(root);
+    ahead.pass(warp / kPer * kPer, warp, roots, h);
     float2 u[ROWS][NP];  // exp(g_t) h_{t-1}
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -134,8 +136,8 @@ recurrence_backward_kernel(const RecDims R, const G* __restrict__ g, const T* __
         }
     }
     float2 m[NP];
-    tile_carry<NP>(S, back, k, n_time, n_slabs, slab, m, err);
-    for (int w = 0; w < kWarps - 1 - warp; ++w) back.pass(w, m);
+    tile_carry<NP>(S, back, sums, roots, k, n_time, n_slabs, slab, m, err);
+    back.pass(0, kWarps - 1 - warp, roots, m);
     T* px = dx + t0 * R.channels;
     G* pg = dg + t0 * R.channels;
     if (!edge) {

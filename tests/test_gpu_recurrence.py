@@ -195,6 +195,51 @@ def test_a_closed_gate_leaves_nothing():
     lc.close(out, *ref["out"])
 
 
+def compare(prm, v, lens, names=("out", "h_last", "g", "x", "h0")):
+    """v: g, x, dout and, or None, h0 and dh_last, on the CPU; forward pass and gradient against the rows in 64 bits."""
+    ref = lc.recurrence(v["g"].double(), v["x"].double(), lens, prm.gate_dim, d64(v["h0"]), v["dout"].double(),
+                        d64(v["dh_last"]))
+    dev = {k: None if t is None else t.cuda() for k, t in v.items()}
+    states, cu = hla.alloc_recurrence_states(prm, sum(lens)), lc.cu(lens)
+    got = dict(zip(("out", "h_last"), hla.recurrence(prm, dev["g"], dev["x"], cu, h0=dev["h0"], states=states)))
+    got.update(hla.recurrence_backward(prm, dev["g"], dev["x"], states, dev["dout"], cu, h0=dev["h0"],
+                                       dh_last=dev["dh_last"]))
+    for name in names:
+        if name in got:
+            lc.close(got[name], *ref[name])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("c,gate_dim", [(64, 1), (70, 1), (128, 64), (128, 128)])
+@pytest.mark.parametrize("gate", [0.5, 3.0, 6.0, 80.0])
+def test_growing_gates_leave_states_of_zero_alone(dtype, c, gate_dim, gate):
+    # hundreds of rows with gates above 1 and nothing in them: what a run multiplies its state by passes fp32's range, the
+    # states do not.  In between, seven rows with inputs, over the border of a tile and between closed gates
+    prm = hla.RecurrenceParams(c, gate_dim, dtype, F32)
+    lens, n = [100, 600], 700
+    g = torch.full((n, c // gate_dim), gate) * (1 - 0.25 * torch.rand(n, c // gate_dim, generator=lc.gen(1)))
+    x, dout = torch.zeros(n, c), torch.zeros(n, c)
+    if gate < 10:
+        x[381:388], dout[381:388] = lc.randn(2, 7, c).float(), lc.randn(3, 7, c).float()
+        g[380], g[388] = float("-inf"), float("-inf")
+    dt = TYPE[dtype]
+    compare(prm, dict(g=g, x=x.to(dt), dout=dout.to(dt), h0=None, dh_last=None), lens)
+
+
+@pytest.mark.parametrize("c,gate_dim", [(64, 1), (70, 1), (128, 64), (128, 128)])
+def test_states_that_grow_and_shrink_by_more_than_fp32_holds(c, gate_dim):
+    # tiles of 64 rows up and down by exp(90) and more, from 1e-30, and one down by exp(105), from 1e38: every state is a
+    # normal number, the factors of those tiles are not
+    prm = hla.RecurrenceParams(c, gate_dim, F32, F32)
+    rate = 0.97 + 0.03 * torch.rand(c // gate_dim, generator=lc.gen(4))
+    up = torch.where(torch.arange(500) % 128 < 64, 1.47, -1.47)[:, None] * rate
+    down = torch.where(torch.arange(200) // 64 == 1, -1.65, 0.0)[:, None] * rate
+    size = 1 + torch.rand(1, c, generator=lc.gen(5))
+    for g, first, last in ((up, 1e-30, 1e10), (down, 1e38, 1e30)):
+        zero = torch.zeros(len(g), c)
+        compare(prm, dict(g=g, x=zero, dout=zero, h0=first * size, dh_last=last * size.flip(1)), [len(g)])
+
+
 def test_gates_of_every_size():
     # one row behind a state of 1: exp(g), to the last bit's neighbour
     g = torch.cat([-torch.logspace(-12, 2.2, 5000, dtype=torch.float64), torch.logspace(-8, 1.9, 500, dtype=torch.float64),
