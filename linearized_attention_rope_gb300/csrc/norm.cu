@@ -426,7 +426,7 @@ norm_backward_kernel(const NormDims N, const T* s, const T* __restrict__ weight,
             for (int j = 0; j < V; ++j) {
                 const float x = to_f32(a.x[j]), dy = to_f32(d.x[j]);
                 o.x[j] = from_f32<T>(((one + to_f32(w.x[j])) * dy - x * c) * r + to_f32(g.x[j]));
-                acc[p][j] += dy * (x * r);
+                acc[p][j] += on ? dy * (x * r) : 0.f;  // (without eps r is infinite where there is no row)
             }
             if (on) *reinterpret_cast<Pc*>(dx + row * N.cols + e) = o;
         }

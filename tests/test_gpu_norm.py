@@ -187,6 +187,21 @@ def test_norm_gradient_matches_64_bit(dtype, cols, heads, n, dsum, weight, offse
         assert torch.equal(again[0], dx) and torch.equal(again[1], dw)  # fixed order of sums
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,heads,n,pad", [(100, 1, 9, 0), (7, 1, 5, 0), (33, 1, 2, 0), (128, 3, 7, 128), (64, 1, 33, 8), (1000, 1, 3, 1)])
+def test_gradient_without_eps(dtype, cols, heads, n, pad):
+    # rows that do not fill the last block, dense or slices of a wider tensor: what lies past the last row has no size
+    prm = hla.NormParams(cols, n_heads=heads, dtype=dtype, eps=0.0)
+    x, _, w = inputs(prm, n)
+    dout = lc.randn(7, *shape(prm, n), dtype=TYPE[dtype])
+    wide = torch.zeros(n, heads * cols + pad, dtype=TYPE[dtype], device="cuda")
+    wide[:, pad:] = x.reshape(n, -1).cuda()
+    dx, dw = hla.rms_norm_backward(prm, wide[:, pad:].view(shape(prm, n)), dout.cuda(), weight=w.cuda())
+    ref = lc.norm_grad(x.double(), w.double(), dout.double(), None, 0.0, 0.0)
+    lc.close(dx, ref[0], ref[1])
+    lc.close(dw, ref[2], ref[3])
+
+
 def test_no_rows():
     prm, w = hla.NormParams(128), torch.ones(128, dtype=torch.bfloat16, device="cuda")
     x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
