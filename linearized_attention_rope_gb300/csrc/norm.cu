@@ -531,8 +531,9 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
             odd ^= 1;
             if (!NARROW && threadIdx.x == 0 && before >= 0 && !dead)  // every thread has left the buffer before
                 load(before + (int64_t)stages * gridDim.x, (st ? st : stages) - 1);
-            const float r = rsqrtf(v[0] * inv + N.eps), cr = -v[1] * inv * r * r * r;
-            const float2 r2 = make_float2(r, r), cr2 = make_float2(cr, cr);
+            // c: mean of f dy x r, which is of dy's size whatever the row's (r^3 for x would pass fp32's range for small rows)
+            const float r = rsqrtf(v[0] * inv + N.eps), c = -v[1] * inv * r;
+            const float2 r2 = make_float2(r, r), c2 = make_float2(c, c);
             const int64_t to = (row0 + at) * N.cols;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
@@ -543,12 +544,10 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
                 if (dsum) pairs<T, V>(*reinterpret_cast<const Pc*>(dr + (size_t)per * N.cols + e), g);
                 Pc o;
 #pragma unroll
-                for (int j = 0; j < H; ++j) {  // dy r: times f for dx, times x for dw
-                    const float2 u = mul2(dy[j], r2);
-                    float2 y = mul2(x[j], cr2);
-                    if (dsum) y = ffma2(x[j], cr2, g[j]);
-                    y = ffma2(f[h][j], u, y);
-                    acc[p][j] = ffma2(u, x[j], acc[p][j]);
+                for (int j = 0; j < H; ++j) {
+                    const float2 u = mul2(x[j], r2), t = ffma2(u, c2, mul2(f[h][j], dy[j]));
+                    const float2 y = dsum ? ffma2(t, r2, g[j]) : mul2(t, r2);
+                    acc[p][j] = ffma2(dy[j], u, acc[p][j]);
                     o.x[2 * j] = from_f32<T>(y.x);
                     o.x[2 * j + 1] = from_f32<T>(y.y);
                 }

@@ -188,6 +188,23 @@ def test_norm_gradient_matches_64_bit(dtype, cols, heads, n, dsum, weight, offse
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,heads,n", [(128, 1, 40), (100, 1, 9), (1000, 1, 33), (1024, 1, 300), (5120, 1, 200), (16384, 1, 3),
+                                          (33001, 1, 2)])
+@pytest.mark.parametrize("dsum", [False, True])
+def test_gradient_of_tiny_rows_without_eps(dtype, cols, heads, n, dsum):
+    # rows of 2e-18 (their squares are normal numbers) and gradients of 1e6 that lie along them: mean(w dy x) / rms^3 passes
+    # fp32's range, the gradient does not
+    prm = hla.NormParams(cols, dtype=dtype, eps=0.0)
+    unit = lc.randn(1, n, cols)
+    x, dout = (2e-18 * unit).to(TYPE[dtype]), (1e6 * (unit + lc.randn(2, n, cols))).to(TYPE[dtype])
+    w, ds = (1 + 0.3 * lc.randn(3, cols)).to(TYPE[dtype]), (1e23 * lc.randn(4, n, cols)).to(TYPE[dtype])
+    dx, dw = hla.rms_norm_backward(prm, x.cuda(), dout.cuda(), weight=w.cuda(), dsum=ds.cuda() if dsum else None)
+    ref = lc.norm_grad(x.double(), w.double(), dout.double(), ds.double() if dsum else None, 0.0, 0.0)
+    lc.close(dx, ref[0], ref[1])
+    lc.close(dw, ref[2], ref[3])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("cols,heads,n,pad", [(100, 1, 9, 0), (7, 1, 5, 0), (33, 1, 2, 0), (128, 3, 7, 128), (64, 1, 33, 8), (1000, 1, 3, 1)])
 def test_gradient_without_eps(dtype, cols, heads, n, pad):
     # rows that do not fill the last block, dense or slices of a wider tensor: what lies past the last row has no size
