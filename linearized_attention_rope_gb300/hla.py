@@ -954,10 +954,12 @@ def alloc_norm_workspace(params: NormParams, device="cuda"):
     return torch.empty(norm_workspace_bytes(params), dtype=torch.uint8, device=device)
 
 
-def rms_norm_backward(params: NormParams, s, dout, weight=None, dsum=None, dx=None, dweight=None, ws=None, stream=None):
+def rms_norm_backward(params: NormParams, s, dout, weight=None, dsum=None, dx=None, dweight=None, ws=None, stream=None,
+                      need_dweight: bool = True):
     """hla_rms_norm_backward: (dx, dweight) from s (rms_norm's sum, or its x without a residual), dout and, where the sum
     is used further, its gradient dsum.  dx is the gradient of x and of the residual; dweight [n_cols] fp32, None
-    without a weight.  dx may be dout or dsum."""
+    without a weight or with need_dweight False (the norm of a frozen backbone: no sums, no workspace).  dx may be dout
+    or dsum."""
     fn = "hla_rms_norm_backward"
     dt, shape, xs = _norm_rows(params, fn, s, "s")
     dev = s.device
@@ -967,16 +969,16 @@ def rms_norm_backward(params: NormParams, s, dout, weight=None, dsum=None, dx=No
     if weight is not None:
         _check_tensor(weight, fn, "weight", dt, (params.n_cols,), dev)
     if dweight is not None:
-        _need(weight is not None, f"{fn}: dweight without weight")
+        _need(weight is not None and need_dweight, f"{fn}: dweight without weight, or not wanted")
         _check_tensor(dweight, fn, "dweight", torch.float32, (params.n_cols,), dev)
     _check_workspace(fn, ws, dev)
     st = _here(dev, stream)
     if st is None:
         with _on(dev, stream, s, dout, weight, dsum, dx, dweight, ws):
-            return rms_norm_backward(params, s, dout, weight, dsum, dx, dweight, ws)
+            return rms_norm_backward(params, s, dout, weight, dsum, dx, dweight, ws, None, need_dweight)
     if dx is None:
         dx = torch.empty_like(dout)
-    if weight is not None:
+    if weight is not None and need_dweight:
         if dweight is None:
             dweight = torch.empty(params.n_cols, dtype=torch.float32, device=dev)
         if ws is None:

@@ -219,6 +219,24 @@ def test_gradient_without_eps(dtype, cols, heads, n, pad):
     lc.close(dw, ref[2], ref[3])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,heads,n", [(7, 1, 33), (128, 3, 130), (1024, 1, 40), (5120, 1, 700), (33001, 1, 2)])
+def test_gradient_of_a_frozen_norm(dtype, cols, heads, n):
+    # dx alone: the same bits, and nothing written to a workspace
+    prm = hla.NormParams(cols, n_heads=heads, dtype=dtype)
+    x, ds, w = (t.cuda() for t in inputs(prm, n))
+    dout = lc.randn(7, *shape(prm, n), dtype=TYPE[dtype]).cuda()
+    want, _ = hla.rms_norm_backward(prm, x, dout, weight=w, dsum=ds)
+    ws = torch.full((hla.norm_workspace_bytes(prm),), 7, dtype=torch.uint8, device="cuda")
+    dx, dw = hla.rms_norm_backward(prm, x, dout, weight=w, dsum=ds, ws=ws, need_dweight=False)
+    assert dw is None and torch.equal(dx, want) and bool((ws == 7).all())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    dx, dw = hla.rms_norm_backward(prm, x, dout, weight=w, dsum=ds, stream=side, need_dweight=False)
+    side.synchronize()
+    assert dw is None and torch.equal(dx, want)
+
+
 def test_no_rows():
     prm, w = hla.NormParams(128), torch.ones(128, dtype=torch.bfloat16, device="cuda")
     x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")

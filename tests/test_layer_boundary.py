@@ -188,6 +188,13 @@ def test_tensor_refusals(lib):
         assert e.value.status == INV, i
 
 
+def test_a_gradient_that_is_not_wanted_has_no_place(lib):
+    b = torch.zeros(4, 128, dtype=torch.bfloat16)
+    with pytest.raises(hla.HlaError, match="not wanted") as e:
+        hla.rms_norm_backward(hla.NormParams(128), b, b, weight=b[0], dweight=torch.zeros(128), need_dweight=False)
+    assert e.value.status == INV
+
+
 def test_reference_gradients_against_differences():
     # the 64-bit forms' gradients against central differences of the forms: the difference is off by step^2 of the third
     # derivative (about 1e-10 here) and by 1e-16 / step of the values
