@@ -104,8 +104,10 @@ cudaError_t launch_norm(const NormDims& N, const T* x, const T* residual, const 
 template <typename T>
 cudaError_t launch_norm_backward(const NormDims& N, const T* s, const T* weight, const T* dout, const T* dsum, T* dx,
                                  float* dweight, float* part, cudaStream_t st);
-// Blocks of a norm's gradient, at most: twelve an SM where rows are short (100000 rows of 512 bf16: 106 us, 122 with 1024).
-constexpr int norm_parts(int cols) { return cols <= 1024 ? 1824 : 1024; }
+// Blocks of a norm's gradient, at most.  Up to 1024 columns twelve an SM (of 152; rows of 512 bf16 take eight: 100000 of them
+// 103 us, 122 with 1024 blocks in all), then as many as a block of cols / 16 threads leaves room for, six at most; two past
+// 16384 columns, where rows are read twice.
+constexpr int norm_parts(int cols) { return 152 * (cols <= 1024 ? 12 : cols > 16384 ? 2 : cols <= 2730 ? 6 : 16384 / cols); }
 
 // The gated recurrence.  Gates: one per channel (gate_dim 1) or per gate_dim (64, 128) channels.
 constexpr int kStateRows = 64;  // rows between the states that a gradient starts from

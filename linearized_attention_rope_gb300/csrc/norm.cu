@@ -808,7 +808,7 @@ cudaError_t launch_norm_backward(const NormDims& N, const T* s, const T* weight,
             }
         }
         if (r.tpr == 0) {
-            blocks = (int)std::min<int64_t>(N.rows, 304);
+            blocks = (int)std::min<int64_t>(N.rows, norm_parts(N.cols));
             norm_backward_long_kernel<T><<<blocks, 1024, 0, st>>>(N, s, weight, dout, dsum, dx, part);
             e = cudaGetLastError();
         } else if (!vec) {

@@ -237,6 +237,23 @@ def test_gradient_of_a_frozen_norm(dtype, cols, heads, n):
     assert dw is None and torch.equal(dx, want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,n", [(7, 20000), (130, 8000), (512, 5000), (1025, 1500), (2560, 1500), (2736, 1200), (4100, 900),
+                                    (5120, 700), (8191, 500), (16384, 400), (16390, 400), (33001, 320)])
+def test_gradient_stays_in_its_workspace(dtype, cols, n):
+    # as many rows as keep every block: their sums fit what the size is given as, and nothing behind it is written
+    prm = hla.NormParams(cols, dtype=dtype)
+    need = hla.norm_workspace_bytes(prm)
+    ws = torch.full((need + (1 << 20),), 7, dtype=torch.uint8, device="cuda")
+    x, dout = (torch.randn(n, cols, device="cuda").to(TYPE[dtype]) for _ in range(2))
+    w = torch.ones(cols, dtype=TYPE[dtype], device="cuda")
+    _, dw = hla.rms_norm_backward(prm, x, dout, weight=w, ws=ws[:need])
+    assert bool((ws[need:] == 7).all()) and bool(dw.isfinite().all())
+    with pytest.raises(hla.HlaError) as e:
+        hla.rms_norm_backward(prm, x, dout, weight=w, ws=ws[:need - 16])
+    assert e.value.status == hla.HLA_ERR_WORKSPACE
+
+
 def test_no_rows():
     prm, w = hla.NormParams(128), torch.ones(128, dtype=torch.bfloat16, device="cuda")
     x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")

@@ -188,6 +188,12 @@ def test_tensor_refusals(lib):
         assert e.value.status == INV, i
 
 
+@pytest.mark.parametrize("cols,rows", [(1, 1824), (1024, 1824), (1025, 912), (2730, 912), (2731, 760), (4096, 608), (5120, 456),
+                                       (8192, 304), (16384, 152), (16385, 304), (1 << 20, 304)])
+def test_norm_workspace_holds_what_blocks_write(lib, cols, rows):
+    assert hla.norm_workspace_bytes(hla.NormParams(cols)) == 4 * cols * rows
+
+
 def test_a_gradient_that_is_not_wanted_has_no_place(lib):
     b = torch.zeros(4, 128, dtype=torch.bfloat16)
     with pytest.raises(hla.HlaError, match="not wanted") as e:
