@@ -603,7 +603,9 @@ typedef struct hla_norm_params {
 } hla_norm_params;
 
 /* s = x + residual, rounded to dtype; out = s / sqrt(mean(s^2) + eps) * (offset +
- * weight), from fp32 sums.
+ * weight), from fp32 sums: a row whose sum of squares passes 2^128 (values of
+ * 1.8e19 / sqrt(n_cols)) has an infinite mean and finite values become 0; without
+ * eps a row needs a mean of 2^-126 at least (values of 1.1e-19).
  *   x, residual [tokens, n_heads, n_cols]   residual may be NULL (s = x)
  *   weight [n_cols]          NULL: out = s / sqrt(mean(s^2) + eps)
  *   out [tokens, n_heads, n_cols]           out_dtype
@@ -713,7 +715,10 @@ typedef struct hla_linear4_params {
  * tokens).  Two calls that may run at the same time need one each. */
 HLA_API int hla_linear4_workspace_bytes(const hla_linear4_params* params, int64_t tokens, size_t* bytes);
 
-/* out [tokens, n_out] = x W^T, from fp32 sums.
+/* out [tokens, n_out] = x W^T, from fp32 sums.  A group's products with q - 8 (and
+ * with offsets its values) are summed before the scale: |x| has to be below 2^118
+ * (3.3e35).  Larger values, infinities and NaN make outputs of their own token
+ * infinite or NaN, also where x W^T is not, and no others.
  *   x [tokens, n_in], x_exp uint8 [tokens, n_in / x_group] (E4M3, else NULL)
  *   w uint8 [n_out, n_in / 2]: inputs 2i (low half) and 2i + 1
  *   scales, offsets [n_out, n_in / group]   offsets may be NULL (0)

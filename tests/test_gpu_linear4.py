@@ -106,6 +106,25 @@ def test_fp32_rows_of_a_wider_tensor(n, lo, offsets):
     assert torch.equal(got, call(prm, x.contiguous(), None, w, s, o))
 
 
+@pytest.mark.parametrize("n", [3, 11, 24, 61])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("offsets", [False, True])
+def test_the_largest_rows(n, dtype, group, offsets):
+    # values of up to 2^118, all of one sign, through weights of one sign: the largest sums that a group can have
+    prm = hla.Linear4Params(384, 40, group, dtype)
+    _, s, o = weights(prm, offsets)
+    w = torch.zeros(40, 192, dtype=torch.uint8)  # q - 8 = -8
+    w[20:] = 0xff                                # 7
+    s, o = s * 2.0 ** -20, o if o is None else o * 2.0 ** -20
+    big = 2.0 ** 118 * (1 - torch.finfo(TYPE[dtype]).eps)
+    x = torch.full((n, 384), big, dtype=torch.float64)
+    x[1] *= -1
+    x[2] = big * torch.rand(384, generator=lc.gen(3), dtype=torch.float64)
+    x = x.to(TYPE[dtype])
+    lc.close(call(prm, x, None, w, s, o), *lc.linear4(x.double(), w, s, o, group, 3))
+
+
 def test_infinities_and_nan_stay_with_their_token():
     for dtype in (BF16, F32):
         prm = hla.Linear4Params(256, 40, dtype=dtype)

@@ -81,6 +81,22 @@ def test_8_bit_rows_with_infinities_and_nan():
         assert v[1].isnan().all() and v[2].isfinite().all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [128, 1000, 5120, 8191, 33001])
+def test_rows_at_the_ends_of_fp32(dtype, cols):
+    # rows whose sum of squares is just below 2^128, just above 2^-126 a value without eps, and past 2^128
+    prm = hla.NormParams(cols, dtype=dtype, eps=0.0)
+    x = lc.randn(1, 3, cols).clamp(-4, 4) / 4 + torch.where(lc.randn(2, 3, cols) > 0, 1.0, -1.0)  # 1 in size, 2 at most
+    x[0] *= 0.4 * 2.0 ** 64 / cols ** 0.5
+    x[1] *= 2.0 ** -62
+    x[2] *= 2.0 ** 66
+    x = x.to(TYPE[dtype])
+    y, err = lc.norm(x.double(), None, 0.0, 0.0)
+    got = hla.rms_norm(prm, x.cuda()).out
+    lc.close(got[:2], y[:2], err[:2])
+    assert float(got[2].abs().max()) == 0.0
+
+
 def test_strided_and_unaligned_rows():
     # q, k and v of one fused projection: norm of q's and k's heads in place of their slices, and rows one value in
     wide = lc.randn(1, 50, 14 * 64, dtype=torch.bfloat16).cuda()
