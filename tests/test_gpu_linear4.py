@@ -106,6 +106,40 @@ def test_fp32_rows_of_a_wider_tensor(n, lo, offsets):
     assert torch.equal(got, call(prm, x.contiguous(), None, w, s, o))
 
 
+@pytest.mark.parametrize("n", [11, 24, 61, 65])
+@pytest.mark.parametrize("dtype,x_dtype,x_group", [(BF16, -1, 0), (F32, -1, 0), (BF16, E4M3, 32), (F32, E4M3, 0)])
+@pytest.mark.parametrize("width", [600, 603])
+def test_rows_of_a_wider_tensor(n, dtype, x_dtype, x_group, width):
+    # up to sixteen rows and more, on 16 bytes and off them, a multiple of 16 bytes apart and not
+    prm = hla.Linear4Params(320, 48, 64, dtype, x_dtype, x_group)
+    w, s, o = weights(prm, True)
+    x, e, v = rows(prm, n)
+    want = call(prm, x, e, w, s, o)
+    lc.close(want, *lc.linear4(v, w, s, o, 64, 3))
+    for lo in (0, 1, 4, 8, 16):
+        wide = torch.zeros(n, width, dtype=x.dtype, device="cuda")
+        wide[:, lo:lo + 320] = x.cuda()
+        got = hla.linear4(prm, wide[:, lo:lo + 320], w.cuda(), s.cuda(), offsets=o.cuda(), x_exp=None if e is None else e.cuda())
+        assert torch.equal(got, want), lo
+
+
+@pytest.mark.parametrize("n", [24, 61, 65])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("offsets", [False, True])
+def test_infinities_and_nan_stay_with_their_token_of_many(n, dtype, offsets):
+    prm = hla.Linear4Params(256, 140, 64, dtype)
+    w, s, o = weights(prm, offsets)
+    x, _, v = rows(prm, n)
+    bad = x.clone()
+    at = [0, 7, n - 8, n - 1]
+    bad[0, 100], bad[7, 5], bad[n - 8], bad[n - 1, 255] = float("nan"), float("inf"), torch.finfo(x.dtype).max, float("-inf")
+    got = call(prm, bad, None, w, s, o)
+    keep = [i for i in range(n) if i not in at]
+    y, err = lc.linear4(v, w, s, o, 64, 3)
+    lc.close(got[keep], y[keep], err[keep])
+    assert got[0].isnan().all() and not got[[7, n - 1]].isfinite().any()
+
+
 @pytest.mark.parametrize("n", [3, 11, 24, 61])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("group", [32, 128])

@@ -118,6 +118,33 @@ def test_strided_and_unaligned_rows():
         hla.rms_norm(hla.NormParams(64, out_dtype=E4M3, group=32), wide[:, 1:65])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,heads,n", [(128, 1, 9), (128, 3, 33), (1024, 1, 4000), (4096, 1, 2000), (5120, 1, 5), (301, 1, 7),
+                                          (17000, 1, 2), (33001, 1, 2)])
+@pytest.mark.parametrize("lo", [0, 8, 1])
+def test_a_residual_of_a_wider_tensor(dtype, cols, heads, n, lo):
+    # the residual, and then x as well, as slices; into the layer's type and into 8 bits where the slices lie on 16 bytes
+    prm = hla.NormParams(cols, n_heads=heads, dtype=dtype)
+    x, r, w = inputs(prm, n)
+    want = hla.rms_norm(prm, x.cuda(), weight=w.cuda(), residual=r.cuda())
+    y, err = lc.norm((x + r).double(), w.double(), 1e-6, 0.0)
+    lc.close(want.out, y, err)
+
+    def part(t, pad):
+        wide = torch.full((n, heads * cols + pad), float("nan"), dtype=t.dtype, device="cuda")
+        wide[:, lo:lo + heads * cols] = t.reshape(n, -1).cuda()
+        return wide[:, lo:lo + heads * cols].view(shape(prm, n))
+
+    for a, b in ((x.cuda(), part(r, 16)), (part(x, 32), part(r, 16)), (part(x, 32), r.cuda())):
+        got = hla.rms_norm(prm, a, weight=w.cuda(), residual=b)
+        assert torch.equal(got.sum, want.sum)
+        lc.close(got.out, y, err)
+        if lo != 1 and cols % 128 == 0:
+            eight = hla.NormParams(cols, n_heads=heads, dtype=dtype, out_dtype=E4M3, group=32)
+            got = hla.rms_norm(eight, a, weight=w.cuda(), residual=b)
+            assert torch.equal(got.sum, want.sum) and lc.eight(y, err, got.out, got.exp, 32) == (True, True, True)
+
+
 @pytest.mark.parametrize("cols", [128, 4096, 8191, 33001])
 def test_in_place(cols):
     prm = hla.NormParams(cols)

@@ -156,6 +156,52 @@ def test_strides_and_offsets():
         lc.close(y, x.double(), torch.zeros(133, 128, dtype=torch.float64))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate_dtype", [F32, BF16])
+@pytest.mark.parametrize("c,gate_dim,lens", [(128, 1, [100, 33]), (70, 1, [100, 33]), (128, 64, [100, 33]), (256, 128, [100, 33]),
+                                             (64, 1, [2000]), (128, 64, [3000, 1]), (128, 128, [2500])])
+def test_slices_of_a_projection(dtype, gate_dtype, c, gate_dim, lens):
+    # gates and inputs as slices that start on and off their boundaries: forward pass, gradient, and the step from states
+    prm = hla.RecurrenceParams(c, gate_dim, dtype, gate_dtype)
+    v, n, cu = inputs(prm, lens), sum(lens), lc.cu(lens)
+    dev = {k: t.cuda() for k, t in v.items()}
+    states = hla.alloc_recurrence_states(prm, n)
+    ref = lc.recurrence(v["g"].double(), v["x"].double(), lens, gate_dim, v["h0"].double(), v["dout"].double(),
+                        v["dh_last"].double())
+    one = lc.recurrence(v["g"].double(), v["x"].double(), [1] * n, gate_dim, lc.randn(9, n, c, dtype=torch.float32).double())
+    for glo, xlo in ((0, 0), (4, 4), (1, 0), (0, 1), (3, 2)):
+        wide_g = torch.full((n, c // gate_dim + 8), float("nan"), dtype=TYPE[gate_dtype], device="cuda")
+        wide_x = torch.full((n, c + 8), float("nan"), dtype=TYPE[dtype], device="cuda")
+        g, x = wide_g[:, glo:glo + c // gate_dim], wide_x[:, xlo:xlo + c]
+        g.copy_(dev["g"])
+        x.copy_(dev["x"])
+        out, last = hla.recurrence(prm, g, x, cu, h0=dev["h0"], states=states)
+        lc.close(out, *ref["out"])
+        lc.close(last, *ref["h_last"])
+        grads = hla.recurrence_backward(prm, g, x, states, dev["dout"], cu, h0=dev["h0"], dh_last=dev["dh_last"])
+        for name, t in grads.items():
+            assert t.is_contiguous()
+            lc.close(t, *ref[name])
+        h = lc.randn(9, n, c, dtype=torch.float32).cuda()
+        lc.close(hla.recurrence_step(prm, g, x, h), *one["out"])
+        lc.close(h, *one["h_last"])
+
+
+def test_many_short_sequences():
+    # more sequences than a block has threads, most of one row, some of none
+    prm = hla.RecurrenceParams(64, dtype=F32)
+    lens = [1, 0, 2, 1] * 3000
+    v = inputs(prm, lens)
+    ref = lc.recurrence(v["g"].double(), v["x"].double(), lens, 1, v["h0"].double(), v["dout"].double(), v["dh_last"].double())
+    dev, ws = {k: t.cuda() for k, t in v.items()}, hla.alloc_recurrence_workspace(prm, sum(lens))
+    states, cu = hla.alloc_recurrence_states(prm, sum(lens)), lc.cu(lens)
+    out, last = hla.recurrence(prm, dev["g"], dev["x"], cu, h0=dev["h0"], states=states, ws=ws)
+    grads = hla.recurrence_backward(prm, dev["g"], dev["x"], states, dev["dout"], cu, h0=dev["h0"], dh_last=dev["dh_last"], ws=ws)
+    for t, name in ((out, "out"), (last, "h_last"), (grads["g"], "g"), (grads["x"], "x"), (grads["h0"], "h0")):
+        lc.close(t, *ref[name])
+    assert hla.check_workspace_error(ws) == 0
+
+
 def test_infinities_nan_and_closed_gates():
     # a sequence's infinities and NaN stay in it and in their channels; a gate of -infinity starts anew; a gate of 0 keeps all
     prm = hla.RecurrenceParams(64, dtype=F32)
