@@ -67,15 +67,18 @@ recurrence_kernel(const RecDims R, const G* __restrict__ g, const T* __restrict_
             for (int p = 0; p < NP; ++p) B[p] = through(e.at(i, p), e.keep(p), B[p], two(xs[i], p));
         }
     }
-    float2 A[NP], total[NP];
+    float2 A[NP];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) sums[warp][p][threadIdx.x & 31] = total[p] = e.total(p);
-    const bool root = factors<NP>(total, A);
+    for (int p = 0; p < NP; ++p) {
+        const float2 total = e.total(p);
+        sums[warp][p][threadIdx.x & 31] = total;
+        A[p] = roots_of(total);
+    }
     runs.put(warp, A, B, rows.first != 0);
-    const bool roots = __syncthreads_or(root);
+    __syncthreads();
     float2 h[NP];
-    tile_carry<NP>(S, runs, sums, roots, k, n_time, n_slabs, slab, h, err);
-    runs.pass(0, warp, roots, h);
+    tile_carry<NP>(S, runs, sums, k, n_time, n_slabs, slab, h, err);
+    runs.pass(0, warp, h);
     if (states && t0 % kStateRows == 0 && t0 < R.total) at.store(states + t0 / kStateRows * R.channels, h);
     T* o = out + t0 * R.channels;
     const uint32_t so = (uint32_t)R.channels;

@@ -73,10 +73,10 @@ __device__ __forceinline__ float2 through(float2 v, float2 w, float2 h, float2 x
 // exp(g) h
 __device__ __forceinline__ float2 times(float2 v, float2 w, float2 h) { return ffma2(w, h, mul2(v, h)); }
 
-// The factor exp(s) of a run or tile whose gates add up to s: itself up to exp(+-80), else minus its square root, which is a
-// normal number as far as a state that it is applied to can stay one (at most exp(88): a normal state that grows by more than
-// exp(176) passes fp32's range).  So that 0 stays 0 and what shrinks or grows by more than fp32 holds comes out as row by row.
-// The paths for roots cost the others 2 to 3 % (registers): 131071 rows of 1024 bf16 channels 250 us, 244 without them.
+// The factor exp(s) of a tile whose gates add up to s: itself up to exp(+-80), else minus its square root, which is applied
+// twice and is a normal number as far as a state can stay one under it (at most exp(88): a normal state that grows by more
+// than exp(176) passes fp32's range).  So that 0 stays 0, and what shrinks or grows by more than fp32 holds comes out as row
+// by row.  (This and the runs' roots cost 2 %: 131071 rows of 1024 bf16 channels 250 us, 245 with products of exp(s).)
 constexpr float kFactor = 80.f;
 __device__ __forceinline__ float factor(float s) {
     const bool in = fabsf(s) <= kFactor;
@@ -84,18 +84,21 @@ __device__ __forceinline__ float factor(float s) {
     return in || e == 0.f ? e : -e;
 }
 __device__ __forceinline__ bool is_root(float2 a) { return a.x < 0.f || a.y < 0.f; }
-// Factors of a warp's sums; whether some lane's is a root (or 0, or NaN).
-template <int NP> __device__ __forceinline__ bool factors(const float2 (&s)[NP], float2 (&a)[NP]) {
+// The root of a run's factor, which is applied twice whatever its size.
+__device__ __forceinline__ float2 roots_of(float2 s) {
+    return make_float2(expf(fminf(0.5f * s.x, 88.f)), expf(fminf(0.5f * s.y, 88.f)));
+}
+// Factors of a warp's sums.
+template <int NP> __device__ __forceinline__ void factors(const float2 (&s)[NP], float2 (&a)[NP]) {
     bool in = true;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         in = in && fabsf(s[p].x) <= kFactor && fabsf(s[p].y) <= kFactor;
         a[p] = make_float2(expf(s[p].x), expf(s[p].y));
     }
-    if (__all_sync(kFull, in)) return false;
+    if (__all_sync(kFull, in)) return;
 #pragma unroll
     for (int p = 0; p < NP; ++p) a[p] = make_float2(factor(s[p].x), factor(s[p].y));
-    return true;
 }
 // a c + b for a of those factors
 __device__ __forceinline__ float2 apply(float2 a, float2 c, float2 b) {
@@ -315,7 +318,7 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
         for (int p = 0; p < NP; ++p) c[p] = ffma2(pa[w][p][lane], c[p], pb[w][p][lane]);
 }
 
-// The warps' (A, B) of a tile, in the order in which the state passes them.
+// The warps' (A, B) of a tile, A as its root, in the order in which the state passes them.
 template <int NP>
 struct Runs {
     float2 a[kWarps][NP][32], b[kWarps][NP][32];
@@ -329,24 +332,14 @@ struct Runs {
         }
         if (lane == 0) cut[w] = is_cut;
     }
-    // from run w0 to run w1; roots: some A of the tile is one
-    __device__ __forceinline__ void pass(int w0, int w1, bool roots, float2 (&c)[NP]) const {
+    // from run w0 to run w1
+    __device__ __forceinline__ void pass(int w0, int w1, float2 (&c)[NP]) const {
         const int lane = threadIdx.x & 31;
-        if (roots) {
-#pragma unroll 1
-            for (int w = w0; w < w1; ++w)
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    const float2 y = b[w][p][lane];
-                    c[p] = cut[w] ? y : apply(a[w][p][lane], c[p], y);
-                }
-            return;
-        }
         for (int w = w0; w < w1; ++w) {
             const bool is = cut[w];
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                const float2 y = b[w][p][lane], z = ffma2(a[w][p][lane], c[p], y);
+                const float2 y = b[w][p][lane], e = a[w][p][lane], z = ffma2(e, mul2(e, c[p]), y);
                 c[p] = is ? y : z;
             }
         }
@@ -357,7 +350,7 @@ template <int NP> using Sums = float2[kWarps][NP][32];
 
 // Publishes tile k's map (or state, where a run of it is cut), takes the state in front of it, publishes the one behind.
 template <int NP>
-__device__ __forceinline__ void tile_carry(const Carry& S, const Runs<NP>& runs, const Sums<NP>& sums, bool roots, int k,
+__device__ __forceinline__ void tile_carry(const Carry& S, const Runs<NP>& runs, const Sums<NP>& sums, int k,
                                            int n_time, int n_slabs, int slab, float2 (&c)[NP], int32_t* err) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -372,7 +365,7 @@ __device__ __forceinline__ void tile_carry(const Carry& S, const Runs<NP>& runs,
         for (int p = 0; p < NP; ++p) {
             total[p] = B[p] = splat(0.f);
         }
-        runs.pass(0, kWarps, roots, B);
+        runs.pass(0, kWarps, B);
         for (int w = 0; w < kWarps; ++w) {
             cut |= runs.cut[w] != 0;
 #pragma unroll

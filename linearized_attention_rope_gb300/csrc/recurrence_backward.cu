@@ -116,14 +116,17 @@ recurrence_backward_kernel(const RecDims R, const G* __restrict__ g, const T* __
             for (int p = 0; p < NP; ++p) M[p] = times(e.at(i, p), e.keep(p), add2(two(ds[i], p), M[p]));
         }
     }
-    float2 A[NP], total[NP];
+    float2 A[NP];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) sums[kWarps - 1 - warp][p][threadIdx.x & 31] = total[p] = e.total(p);
-    const bool root = factors<NP>(total, A);
+    for (int p = 0; p < NP; ++p) {
+        const float2 total = e.total(p);
+        sums[kWarps - 1 - warp][p][threadIdx.x & 31] = total;
+        A[p] = roots_of(total);
+    }
     ahead.put(warp, A, B, rows.first != 0);
     back.put(kWarps - 1 - warp, A, M, rows.last != 0);
-    const bool roots = __syncthreads_or(root);
-    ahead.pass(warp / kPer * kPer, warp, roots, h);
+    __syncthreads();
+    ahead.pass(warp / kPer * kPer, warp, h);
     float2 u[ROWS][NP];  // exp(g_t) h_{t-1}
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -136,8 +139,8 @@ recurrence_backward_kernel(const RecDims R, const G* __restrict__ g, const T* __
         }
     }
     float2 m[NP];
-    tile_carry<NP>(S, back, sums, roots, k, n_time, n_slabs, slab, m, err);
-    back.pass(0, kWarps - 1 - warp, roots, m);
+    tile_carry<NP>(S, back, sums, k, n_time, n_slabs, slab, m, err);
+    back.pass(0, kWarps - 1 - warp, m);
     T* px = dx + t0 * R.channels;
     G* pg = dg + t0 * R.channels;
     if (!edge) {
