@@ -17,8 +17,12 @@
 // Measured: 32767 rows of 5120 bf16 with the residual 213 us, 94 % of the copy
 // rate (a block a row: 259); 4097 rows of 4096 fp32 42 us, 96 %; gradients: 524352
 // heads of 128 bf16 72 us (83 %), 4097 rows of 4096 fp32 with the stream's 48 us
-// (84 %), 32767 rows of 5120 bf16 302 us (66 %: two pieces a thread, whose sums of
+// (84 %), 32767 rows of 5120 bf16 296 us (68 %: two pieces a thread, whose sums of
 // dw and factors take the registers).
+// Spilled at the 64 registers that blocks of up to 1024 threads leave (bytes stored
+// and loaded a thread): gradients of bf16 rows in two pieces 72 and 144, in four 104
+// and 104; norms of bf16 rows in four 56 to 84 and 116 to 280; sixteen single
+// values a thread 44 to 60 and 76 to 100, their gradient 660 and 764.
 #include <algorithm>
 
 #include "layer.cuh"
@@ -483,7 +487,7 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
     constexpr bool kHold = P * V <= 8, kRow = SMALL;  // the factors, the row stay in registers between the passes
     constexpr int H = V / 2;
     constexpr int K = kHold ? P : 1;
-    float2 f[K][H], x[H], dy[H], acc[P][H];
+    float2 f[K][H], x[H], dy[H], fdy[H], acc[P][H];
     const float one = weight ? N.offset : 1.f;
     auto factors = [&](int h, int e) {
         const Pc w = weight && e < N.cols ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
@@ -523,7 +527,8 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
                     v0 = ffma2(x[j], x[j], v0);
-                    v1 = ffma2(mul2(f[h][j], dy[j]), x[j], v1);
+                    fdy[j] = mul2(f[h][j], dy[j]);
+                    v1 = ffma2(fdy[j], x[j], v1);
                 }
             }
             float v[2] = {v0.x + v0.y, v1.x + v1.y};
@@ -545,7 +550,7 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
                 Pc o;
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
-                    const float2 u = mul2(x[j], r2), t = ffma2(u, c2, mul2(f[h][j], dy[j]));
+                    const float2 u = mul2(x[j], r2), t = ffma2(u, c2, kRow ? fdy[j] : mul2(f[h][j], dy[j]));
                     const float2 y = dsum ? ffma2(t, r2, g[j]) : mul2(t, r2);
                     acc[p][j] = ffma2(dy[j], u, acc[p][j]);
                     o.x[2 * j] = from_f32<T>(y.x);
