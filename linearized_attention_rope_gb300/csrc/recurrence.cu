@@ -1,8 +1,9 @@
 // Gated linear recurrence, forward, and its step.
 //
-// Measured: 131071 rows of 1024 bf16 channels and gates 247 us (3.3 TB/s, 2.1 instructions a cycle; a third of the time is the
-// tiles' waiting for one another: 32767 rows take 72 us, 53 without looking at other tiles); 16309 rows of 4096, gates in
-// fp32, 126 us (4.2 TB/s); the step of 64 x 4096 states 3 us.
+// Measured: 131071 rows of 1024 bf16 channels and gates 245 us (3.3 TB/s, 2.1 instructions a cycle; a third of the time is the
+// tiles' waiting for one another: 32767 rows took 72 us, 53 without looking at other tiles); 16309 rows of 4096, gates in
+// fp32, 123 us (4.3 TB/s); the step of 64 x 4096 states 3 us.  At the 80 registers that three blocks an SM leave, these two
+// spill 24 and 28 bytes a thread, the others 8 to 32.
 #include "recurrence.cuh"
 
 namespace hla {
@@ -68,13 +69,16 @@ recurrence_kernel(const RecDims R, const G* __restrict__ g, const T* __restrict_
         }
     }
     float2 A[NP];
+    bool far = false;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const float2 total = e.total(p);
         sums[warp][p][threadIdx.x & 31] = total;
-        A[p] = roots_of(total);
+        A[p] = roots(total);
+        far = far || !within(total, kFar);
     }
-    runs.put(warp, A, B, rows.first != 0);
+    far = __any_sync(kFull, far);
+    runs.put(warp, A, B, rows.first != 0, far);
     __syncthreads();
     float2 h[NP];
     tile_carry<NP>(S, runs, sums, k, n_time, n_slabs, slab, h, err);

@@ -12,6 +12,10 @@
 // taken from the tiles before it, and each warp then walks its rows with the
 // state in front of them.
 //
+// A run's A is kept as its root and applied twice, a tile's too where A does not
+// fit fp32 (which costs calls of few channels 8 %: 131072 rows of one channel 55
+// us, 51 with gates that sum up to less than 80 over a tile).
+//
 // The state in front of a tile: every tile publishes (A, B) and, once it knows
 // it, the state behind it.  A tile looks at the eight tiles before it, then at
 // up to 32 (four channels a lane: 16); the nearest with a state is carried
@@ -73,49 +77,32 @@ __device__ __forceinline__ float2 through(float2 v, float2 w, float2 h, float2 x
 // exp(g) h
 __device__ __forceinline__ float2 times(float2 v, float2 w, float2 h) { return ffma2(w, h, mul2(v, h)); }
 
-// The factor exp(s) of a tile whose gates add up to s: itself up to exp(+-80), else minus its square root, which is applied
-// twice and is a normal number as far as a state can stay one under it (at most exp(88): a normal state that grows by more
-// than exp(176) passes fp32's range).  So that 0 stays 0, and what shrinks or grows by more than fp32 holds comes out as row
-// by row.  (This and the runs' roots cost 2 %: 131071 rows of 1024 bf16 channels 250 us, 245 with products of exp(s).)
-constexpr float kFactor = 80.f;
-__device__ __forceinline__ float factor(float s) {
-    const bool in = fabsf(s) <= kFactor;
-    const float e = expf(in ? s : 0.5f * s > 88.f ? 88.f : 0.5f * s);
-    return in || e == 0.f ? e : -e;
-}
-__device__ __forceinline__ bool is_root(float2 a) { return a.x < 0.f || a.y < 0.f; }
-// The root of a run's factor, which is applied twice whatever its size.
-__device__ __forceinline__ float2 roots_of(float2 s) {
+// The factor exp(s) of a run whose gates add up to s, as its root, which is applied twice and is a normal number as far as a
+// state can stay one under it (at most exp(88): a normal state that grows by more than exp(176) passes fp32's range).  So
+// that 0 stays 0, and what shrinks or grows by more than fp32 holds comes out as row by row.  The root of a tile's factor is the
+// product of its runs', as long as that cannot leave fp32's range (sums up to kFar each: exp(80) in all), else that of the sum
+// of their sums; a tile hands on its square where that is within exp(+-80).
+constexpr float kFar = 20.f;
+__device__ __forceinline__ float2 roots(float2 s) {
     return make_float2(expf(fminf(0.5f * s.x, 88.f)), expf(fminf(0.5f * s.y, 88.f)));
 }
-// Factors of a warp's sums.
-template <int NP> __device__ __forceinline__ void factors(const float2 (&s)[NP], float2 (&a)[NP]) {
-    bool in = true;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        in = in && fabsf(s[p].x) <= kFactor && fabsf(s[p].y) <= kFactor;
-        a[p] = make_float2(expf(s[p].x), expf(s[p].y));
-    }
-    if (__all_sync(kFull, in)) return;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) a[p] = make_float2(factor(s[p].x), factor(s[p].y));
+__device__ __forceinline__ bool within(float2 s, float most) { return fabsf(s.x) <= most && fabsf(s.y) <= most; }
+__device__ __forceinline__ bool squares(float2 root) {
+    const float hi = 2.3538527e17f, lo = 4.2483543e-18f;  // exp(+-40)
+    return root.x >= lo && root.x <= hi && root.y >= lo && root.y <= hi;
 }
-// a c + b for a of those factors
-__device__ __forceinline__ float2 apply(float2 a, float2 c, float2 b) {
-    const float2 f = make_float2(a.x < 0.f ? -a.x : 1.f, a.y < 0.f ? -a.y : 1.f);
-    return ffma2(make_float2(fabsf(a.x), fabsf(a.y)), mul2(f, c), b);
-}
+__device__ __forceinline__ float2 twice(float2 root, float2 c, float2 b) { return ffma2(root, mul2(root, c), b); }
 
-// Two values, each in a word with its own flag (0 where it has not been written).
-__device__ __forceinline__ void put_words(uint64_t* p, float2 v) {
-    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"((uint64_t)1 << 32 | __float_as_uint(v.x)),
-                 "l"((uint64_t)1 << 32 | __float_as_uint(v.y)) : "memory");
+// Two values, each in a word with its own flags (0 where it has not been written; 1, and 2 for a root).
+__device__ __forceinline__ void put_words(uint64_t* p, float2 v, uint32_t flags = 1) {
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"((uint64_t)flags << 32 | __float_as_uint(v.x)),
+                 "l"((uint64_t)flags << 32 | __float_as_uint(v.y)) : "memory");
 }
-__device__ __forceinline__ bool get_words(const uint64_t* p, float2* v) {
+__device__ __forceinline__ uint32_t get_words(const uint64_t* p, float2* v) {
     uint64_t x, y;
     asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "l"(p) : "memory");
     *v = make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)y));
-    return (x & y) >> 32;
+    return (uint32_t)((x & y) >> 32);
 }
 
 // Carries between tiles: per tile and channel the state behind it, and its (A, B).
@@ -233,10 +220,10 @@ template <int NP>
 __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, int slab, float2 (&c)[NP], int32_t* err) {
     constexpr int kDeep = 4 / NP, kLook = kDeep * kWarps;  // a warp looks at the tile 1 + warp before this one, 9 + warp ...
     __shared__ float2 pa[kLook][NP][32], pb[kLook][NP][32];
-    __shared__ int status[kLook];  // 0 nothing yet, 1 (A, B), 2 the state, 3 given up; 5 (A, B) with a root
+    __shared__ int status[kLook];  // 0 nothing yet, 1 (A, B), 2 the state, 3 given up; 5 (A, B), A as its root
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int polls = 0, m, deep = 1;
-    bool roots;
+    bool some;  // A as its root
     for (int i = threadIdx.x; i < kLook; i += kThreads) status[i] = 0;
     __syncthreads();
     for (;;) {
@@ -253,27 +240,26 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
                 const int64_t at = (((int64_t)pred * n_slabs + slab) * 32 + lane) * 2 * NP;
                 do {
                     float2 s[NP], a[NP], b[NP];
-                    bool is = true, has = true, root = false;
+                    uint32_t is = 3, has = 3;
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
                         is &= get_words(S.state + at + 2 * p, &s[p]);
                         if (!have) {
                             has &= get_words(S.map + 2 * at + 4 * p, &a[p]);
                             has &= get_words(S.map + 2 * at + 4 * p + 2, &b[p]);
-                            root |= is_root(a[p]);
                         }
                     }
-                    if (__all_sync(kFull, is)) {
+                    if (__all_sync(kFull, is != 0)) {
 #pragma unroll
                         for (int p = 0; p < NP; ++p) pb[i][p][lane] = s[p];
                         have = 2;
-                    } else if (!have && __all_sync(kFull, has)) {
+                    } else if (!have && __all_sync(kFull, has != 0)) {
 #pragma unroll
                         for (int p = 0; p < NP; ++p) {
                             pa[i][p][lane] = a[p];
                             pb[i][p][lane] = b[p];
                         }
-                        have = __any_sync(kFull, root) ? 5 : 1;
+                        have = has & 2 ? 5 : 1;  // (the same in all lanes)
                     }
                     if ((have & 3) < 2 && ++polls > kPolls) have = 3;
                 } while (!have);
@@ -284,7 +270,7 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
         __syncthreads();
         const int got = status[lane % kLook];
         const unsigned ready = __ballot_sync(kFull, got == 2);
-        roots = __any_sync(kFull, got == 5);
+        some = __any_sync(kFull, got == 5);
         if (__any_sync(kFull, got == 3)) {
             m = -1;
             break;
@@ -305,11 +291,16 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
     }
 #pragma unroll
     for (int p = 0; p < NP; ++p) c[p] = pb[m][p][lane];
-    if (roots) {
-#pragma unroll 1
-        for (int w = m - 1; w >= 0; --w)
+    if (some) {
+#pragma unroll 4
+        for (int w = m - 1; w >= 0; --w) {
+            const bool root = status[w] == 5;
 #pragma unroll
-            for (int p = 0; p < NP; ++p) c[p] = apply(pa[w][p][lane], c[p], pb[w][p][lane]);
+            for (int p = 0; p < NP; ++p) {
+                const float2 a = pa[w][p][lane], f = root ? a : splat(1.f);
+                c[p] = ffma2(a, mul2(f, c[p]), pb[w][p][lane]);
+            }
+        }
         return;
     }
 #pragma unroll 4
@@ -322,30 +313,30 @@ __device__ __forceinline__ void look_back(const Carry& S, int k, int n_slabs, in
 template <int NP>
 struct Runs {
     float2 a[kWarps][NP][32], b[kWarps][NP][32];
-    int cut[kWarps];  // the state does not pass this run
-    __device__ __forceinline__ void put(int w, const float2 (&A)[NP], const float2 (&B)[NP], bool is_cut) {
+    int kind[kWarps];  // 1: the state does not pass this run; 2: some sum of gates is past kFar
+    __device__ __forceinline__ void put(int w, const float2 (&A)[NP], const float2 (&B)[NP], bool cut, bool far) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             a[w][p][lane] = A[p];
             b[w][p][lane] = B[p];
         }
-        if (lane == 0) cut[w] = is_cut;
+        if (lane == 0) kind[w] = (cut ? 1 : 0) | (far ? 2 : 0);
     }
     // from run w0 to run w1
     __device__ __forceinline__ void pass(int w0, int w1, float2 (&c)[NP]) const {
         const int lane = threadIdx.x & 31;
         for (int w = w0; w < w1; ++w) {
-            const bool is = cut[w];
+            const bool is = kind[w] & 1;
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                const float2 y = b[w][p][lane], e = a[w][p][lane], z = ffma2(e, mul2(e, c[p]), y);
+                const float2 y = b[w][p][lane], z = twice(a[w][p][lane], c[p], y);
                 c[p] = is ? y : z;
             }
         }
     }
 };
-// The sums of the runs' gates, of which a tile's A is formed.
+// The sums of the runs' gates.
 template <int NP> using Sums = float2[kWarps][NP][32];
 
 // Publishes tile k's map (or state, where a run of it is cut), takes the state in front of it, publishes the one behind.
@@ -357,35 +348,49 @@ __device__ __forceinline__ void tile_carry(const Carry& S, const Runs<NP>& runs,
     for (int p = 0; p < NP; ++p) c[p] = splat(0.f);
     if (n_time == 1) return;
     float2 A[NP], B[NP];
-    bool cut = false;
+    int kinds = 0;
+    bool root = false;
     const int64_t at = (((int64_t)k * n_slabs + slab) * 32 + lane) * 2 * NP;
     if (threadIdx.x < 32 && k + 1 < n_time) {
-        float2 total[NP];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            total[p] = B[p] = splat(0.f);
+            A[p] = splat(1.f);
+            B[p] = splat(0.f);
         }
         runs.pass(0, kWarps, B);
         for (int w = 0; w < kWarps; ++w) {
-            cut |= runs.cut[w] != 0;
+            kinds |= runs.kind[w];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) total[p] = add2(total[p], sums[w][p][lane]);
+            for (int p = 0; p < NP; ++p) A[p] = mul2(A[p], runs.a[w][p][lane]);
         }
-        factors<NP>(total, A);
+        if (kinds == 2)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                float2 total = splat(0.f);
+                for (int w = 0; w < kWarps; ++w) total = add2(total, sums[w][p][lane]);
+                A[p] = roots(total);
+            }
+        bool fine = true;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) fine = fine && squares(A[p]);
+        root = !__all_sync(kFull, fine);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            if (!root) A[p] = mul2(A[p], A[p]);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            if (cut) {
+            if (kinds & 1) {
                 put_words(S.state + at + 2 * p, B[p]);
             } else {
-                put_words(S.map + 2 * at + 4 * p, A[p]);
-                put_words(S.map + 2 * at + 4 * p + 2, B[p]);
+                put_words(S.map + 2 * at + 4 * p, A[p], root ? 3 : 1);
+                put_words(S.map + 2 * at + 4 * p + 2, B[p], root ? 3 : 1);
             }
         }
     }
     look_back<NP>(S, k, n_slabs, slab, c, err);
-    if (threadIdx.x < 32 && k + 1 < n_time && !cut)
+    if (threadIdx.x < 32 && k + 1 < n_time && !(kinds & 1))
 #pragma unroll
-        for (int p = 0; p < NP; ++p) put_words(S.state + at + 2 * p, apply(A[p], c[p], B[p]));
+        for (int p = 0; p < NP; ++p) put_words(S.state + at + 2 * p, root ? twice(A[p], c[p], B[p]) : ffma2(A[p], c[p], B[p]));
 }
 
 // A warp's gates as (v, w): v per row and pair of channels, or (SHARED) row i's in lane i; w per pair.

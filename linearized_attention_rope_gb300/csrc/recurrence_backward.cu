@@ -1,8 +1,9 @@
 // Gradient of the gated linear recurrence.
 //
-// Measured: 16309 rows of 4096 bf16 channels, a gate per channel, 191 us (4.7 TB/s); 16384 rows of 2048, a gate per 64, 76 us
+// Measured: 16309 rows of 4096 bf16 channels, a gate per channel, 192 us (4.7 TB/s); 16384 rows of 2048, a gate per 64, 76 us
 // (2.7 TB/s; 83 with two blocks an SM, 87 with runs of 8 rows): a row's gate goes from its lane to all four times, and the
-// gate's gradient is summed over the warp.
+// gate's gradient is summed over the warp; and at the 80 registers of three blocks an SM 108 to 164 bytes a thread are
+// spilled (a gate per 128: 224 to 360), which costs less than the third block gives.
 #include "recurrence.cuh"
 
 namespace hla {
@@ -117,14 +118,17 @@ recurrence_backward_kernel(const RecDims R, const G* __restrict__ g, const T* __
         }
     }
     float2 A[NP];
+    bool far = false;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const float2 total = e.total(p);
         sums[kWarps - 1 - warp][p][threadIdx.x & 31] = total;
-        A[p] = roots_of(total);
+        A[p] = roots(total);
+        far = far || !within(total, kFar);
     }
-    ahead.put(warp, A, B, rows.first != 0);
-    back.put(kWarps - 1 - warp, A, M, rows.last != 0);
+    far = __any_sync(kFull, far);
+    ahead.put(warp, A, B, rows.first != 0, far);
+    back.put(kWarps - 1 - warp, A, M, rows.last != 0, far);
     __syncthreads();
     ahead.pass(warp / kPer * kPer, warp, h);
     float2 u[ROWS][NP];  // exp(g_t) h_{t-1}
