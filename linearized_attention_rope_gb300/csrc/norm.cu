@@ -487,7 +487,7 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
     constexpr bool kHold = P * V <= 8, kRow = SMALL;  // the factors, the row stay in registers between the passes
     constexpr int H = V / 2;
     constexpr int K = kHold ? P : 1;
-    float2 f[K][H], x[H], dy[H], fdy[H], acc[P][H];
+    float2 f[K][H], x[H], dy[H], acc[P][H];
     const float one = weight ? N.offset : 1.f;
     auto factors = [&](int h, int e) {
         const Pc w = weight && e < N.cols ? *reinterpret_cast<const Pc*>(weight + e) : Pc{};
@@ -527,8 +527,7 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
                     v0 = ffma2(x[j], x[j], v0);
-                    fdy[j] = mul2(f[h][j], dy[j]);
-                    v1 = ffma2(fdy[j], x[j], v1);
+                    v1 = ffma2(mul2(f[h][j], dy[j]), x[j], v1);
                 }
             }
             float v[2] = {v0.x + v0.y, v1.x + v1.y};
@@ -550,7 +549,7 @@ norm_backward_ring_kernel(const NormDims N, const T* s, const T* __restrict__ we
                 Pc o;
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
-                    const float2 u = mul2(x[j], r2), t = ffma2(u, c2, kRow ? fdy[j] : mul2(f[h][j], dy[j]));
+                    const float2 u = mul2(x[j], r2), t = ffma2(u, c2, mul2(f[h][j], dy[j]));
                     const float2 y = dsum ? ffma2(t, r2, g[j]) : mul2(t, r2);
                     acc[p][j] = ffma2(dy[j], u, acc[p][j]);
                     o.x[2 * j] = from_f32<T>(y.x);

@@ -234,13 +234,15 @@ def test_norm_gradient_matches_64_bit(dtype, cols, heads, n, dsum, weight, offse
 @pytest.mark.parametrize("cols,heads,n", [(128, 1, 40), (100, 1, 9), (1000, 1, 33), (1024, 1, 300), (5120, 1, 200), (16384, 1, 3),
                                           (33001, 1, 2)])
 @pytest.mark.parametrize("dsum", [False, True])
-def test_gradient_of_tiny_rows_without_eps(dtype, cols, heads, n, dsum):
-    # rows of 2e-18 (their squares are normal numbers) and gradients of 1e6 that lie along them: mean(w dy x) / rms^3 passes
-    # fp32's range, the gradient does not
+@pytest.mark.parametrize("size,grad", [(2e-18, 1e6), (1e16, 1e-9)])
+def test_gradient_of_tiny_and_huge_rows_without_eps(dtype, cols, heads, n, dsum, size, grad):
+    # rows of 2e-18 and 1e16 (their squares are normal numbers) and gradients that lie along them: mean(w dy x) / rms^3 leaves
+    # fp32's range, the gradient does not.  Every third row is an ordinary one
     prm = hla.NormParams(cols, dtype=dtype, eps=0.0)
-    unit = lc.randn(1, n, cols)
-    x, dout = (2e-18 * unit).to(TYPE[dtype]), (1e6 * (unit + lc.randn(2, n, cols))).to(TYPE[dtype])
-    w, ds = (1 + 0.3 * lc.randn(3, cols)).to(TYPE[dtype]), (1e23 * lc.randn(4, n, cols)).to(TYPE[dtype])
+    unit, mixed = lc.randn(1, n, cols), (torch.arange(n) % 3 == 2)[:, None]
+    size, grad = (torch.where(mixed, 1.0, torch.tensor(y, dtype=torch.float64)) for y in (size, grad))
+    x, dout = (size * unit).to(TYPE[dtype]), (grad * (unit + lc.randn(2, n, cols))).to(TYPE[dtype])
+    w, ds = (1 + 0.3 * lc.randn(3, cols)).to(TYPE[dtype]), (grad / size * lc.randn(4, n, cols)).to(TYPE[dtype])
     dx, dw = hla.rms_norm_backward(prm, x.cuda(), dout.cuda(), weight=w.cuda(), dsum=ds.cuda() if dsum else None)
     ref = lc.norm_grad(x.double(), w.double(), dout.double(), ds.double() if dsum else None, 0.0, 0.0)
     lc.close(dx, ref[0], ref[1])
