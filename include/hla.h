@@ -621,7 +621,8 @@ HLA_API int hla_rms_norm(const hla_norm_params* params, const void* x, const voi
                          int64_t tokens, void* out, uint8_t* exp, void* sum, void* stream);
 
 /* Workspace bytes of hla_rms_norm_backward with a weight (no error word; they
- * depend on n_cols alone). */
+ * depend on n_cols alone).  Two calls that may run at the same time need one
+ * each. */
 HLA_API int hla_rms_norm_backward_workspace_bytes(const hla_norm_params* params, size_t* bytes);
 
 /* Gradients of sum(dout . out) (+ sum(dsum . sum), dsum may be NULL) with respect
@@ -711,8 +712,10 @@ typedef struct hla_linear4_params {
     int64_t x_stride;
 } hla_linear4_params;
 
-/* Workspace bytes of hla_linear4 (no error word; may be 0, and grows with
- * tokens).  Two calls that may run at the same time need one each. */
+/* Workspace bytes of hla_linear4 (no error word; grows with tokens): rows that are
+ * not bf16 on 16-byte boundaries, a multiple of 16 bytes apart, are laid out
+ * there.  (It is asked for whatever the number of tokens; up to 16 of them are not
+ * laid out.)  Two calls that may run at the same time need one each. */
 HLA_API int hla_linear4_workspace_bytes(const hla_linear4_params* params, int64_t tokens, size_t* bytes);
 
 /* out [tokens, n_out] = x W^T, from fp32 sums.  A group's products with q - 8 (and

@@ -143,7 +143,7 @@ int linear4_parts(Rows4 kind);
 template <typename T>
 cudaError_t launch_linear4(const Linear4Dims& L, Rows4 kind, const void* x, const uint8_t* x_exp, const uint8_t* w,
                            const T* scales, const T* offsets, T* out, __nv_bfloat16* parts, cudaStream_t st);
-// More than eight rows: `parts` bf16 parts [parts][rows][n_in] (or one, sx apart) on 16-byte boundaries.
+// More than kFewRows rows: `parts` bf16 parts [parts][rows][n_in] (or one, sx apart) on 16-byte boundaries.
 template <typename T>
 cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat16* x, const uint8_t* w, const T* scales,
                               const T* offsets, T* out, cudaStream_t st);

@@ -344,7 +344,8 @@ cudaError_t launch_linear4_tc(const Linear4Dims& L, int parts, const __nv_bfloat
         !tma::make_map_2d(&map_x, x, 2, (uint64_t)L.n_in, (uint64_t)L.rows * parts, (uint64_t)L.sx * 2, 64, (uint32_t)n))
         return cudaErrorInvalidValue;
     // Two blocks an SM, one where offsets' sums or three parts of x take the room (24 rows through 4096 x 14336 with offsets: 25 us
-    // in single blocks, 32 in clusters of two; 61 through 5120 x 10240 without: 39, 35 and, in clusters of four, 33).
+    // in single blocks, 32 in clusters of two; 61 through 5120 x 10240 without: 39, 35 and, in clusters of four, 33: the rule
+    // takes two there, as it counts a block's start and end as six steps, and loses those 2 us).
     const int resident = offsets || parts == 3 ? 152 : 304;
     const int c = linear4_split((int64_t)((L.n_out + kTile - 1) / kTile) * ((L.rows + n - 1) / n), (L.n_in + 127) / 128, resident, 6);
     auto go = [&](auto nn, auto np, auto offs) {
